@@ -289,6 +289,124 @@ gdn_status gdn_decode_step_static(const gdn_config *cfg, const gdn_weights *w, c
                                   const int32_t *slot_ids, int B, uint16_t *out, uint16_t *conv_state,
                                   void *ssm_state, int num_slots, int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The paged KV cache in 4 bits, and the softmax attention that reads it: the
+ * attention layers that stand between the GDN layers of a hybrid model. (The
+ * pages this library follows have no such layer; the operators and their
+ * interface are this library's own.)
+ *
+ * A page holds page_tokens tokens of every KV head of one layer; `pages` is
+ * [num_pages][n_kv_heads][page_tokens / 16][18 * head_dim] bytes. A group --
+ * 16 consecutive tokens of one head -- is, with d = head_dim:
+ *   [0, 8d)     K codes: token t's d / 2 bytes at t * d / 2
+ *   [8d, 16d)   V codes: token t's d / 2 bytes form row rho(t), whose bits are
+ *               t3 t0 t2 t1 (rho = t & 8 | (t & 1) << 2 | (t >> 1) & 3); for
+ *               d = 128 the two 32-byte halves of rows 2, 3, 6, 7, 10, 11, 14
+ *               and 15 change places
+ *   [16d, 17d)  K scales: token t, block b at t * d / 16 + b
+ *   [17d, 18d)  V scales: token t, block b at
+ *               16 b + 4 ((t >> 1) & 3) + ((t & 1) | (t >> 3) << 1)
+ * Codes are E2M1 (element 2i in the low nibble of byte i), one E4M3 scale per
+ * 16 elements; a K value is e2m1 * e4m3 * k_scale, a V value * v_scale. V's
+ * order puts the tokens that one lane of a warp MMA holds side by side, free
+ * of shared-memory bank conflicts.
+ *
+ * A sequence is a row of block_table: its token p lies in page
+ * block_table[b][p / page_tokens], at p % page_tokens. Pages may be shared by
+ * several sequences. kv_len[b] counts the sequence's tokens, the new ones of
+ * this call among them, so the new rows i = 0 .. n - 1 of sequence b are its
+ * tokens kv_len[b] - n + i. kv_len[b] = 0 marks a padding row.
+ *
+ * Device-detected errors go to *dev_status (device int32, may be NULL; sticky):
+ * GDN_E_RANGE for a kv_len below 0 or above max_pages * page_tokens, a page id
+ * outside [0, num_pages) under a token that is read or written, or a q_start
+ * that does not ascend; what such a sequence gets is unspecified, and nothing
+ * outside the buffers is touched. */
+typedef struct {
+  uint8_t *pages;     /* device, 16-byte aligned */
+  int num_pages;
+  int page_tokens;    /* 16, 32, 64, 128 or 256 */
+  int n_kv_heads;
+  int head_dim;       /* 64 or 128 */
+  float k_scale, v_scale;  /* FP32 tensor scales of K and of V, > 0 */
+} kv4_cache;
+
+typedef struct {
+  const int32_t *kv_len;       /* device [B] */
+  const int32_t *block_table;  /* device [B][max_pages]; entries past a sequence's last page are not read */
+  const int32_t *q_start;      /* device [B + 1]: sequence b's new rows are [q_start[b], q_start[b + 1]) of the T rows;
+                                  rows from q_start[B] on are padding, left alone. NULL: T / B rows each */
+  int B, max_pages, T;
+} kv4_batch;
+
+/* Quantise the batch's new K and V rows (BF16, [T][n_kv_heads][head_dim]; a
+ * token's heads contiguous, tokens k_stride / v_stride elements apart, a
+ * multiple of 8) into their sequences' pages, each 16-block as nvfp4_quantize
+ * does with the cache's tensor scales. A block with NaN or infinity becomes
+ * zeros and sets GDN_E_NONFINITE. Two sequences of a batch that write the same
+ * page race. Errors: GDN_E_NULL, GDN_E_SHAPE (sizes, strides; T not a multiple
+ * of B without q_start), GDN_E_ALIGN, GDN_E_NONFINITE / GDN_E_BAD_SCALE (tensor
+ * scales), GDN_E_OVERFLOW, GDN_E_CUDA. */
+gdn_status kv4_append(const kv4_cache *c, const kv4_batch *b, const uint16_t *k, int64_t k_stride,
+                      const uint16_t *v, int64_t v_stride, int32_t *dev_status, void *stream);
+
+/* The values the pages hold for the batch's new rows, rounded to BF16, into
+ * contiguous k and v [T][n_kv_heads][head_dim]. Errors: as kv4_append. */
+gdn_status kv4_read(const kv4_cache *c, const kv4_batch *b, uint16_t *k, uint16_t *v, int32_t *dev_status,
+                    void *stream);
+
+/* Attention of r = T / B new tokens per sequence (r = 1: a decode step; more:
+ * the check of r candidates) over the cache, which holds them already:
+ *   z_ij = sm_scale * q_i . k_j for j <= kv_len - r + i;  out_i = sum_j softmax(z_i)_j v_j
+ *   lse_i = log sum_j exp(z_ij)
+ * q: BF16, row t's n_q_heads heads contiguous, rows q_stride elements apart (a
+ * multiple of 8); query head h reads KV head h / (n_q_heads / n_kv_heads).
+ * out: BF16 [T][n_q_heads][head_dim]; lse: FP32 [T][n_q_heads], may be NULL. A
+ * row that sees no token gets zeros and lse = -infinity. b->q_start must be
+ * NULL. workspace: kv4_decode_workspace bytes of device memory that no other
+ * call in flight uses; its contents before the call do not matter. Scores,
+ * sums and the output accumulate in FP32; the softmax weights enter the second
+ * product rounded to FP16, all other operands exactly. The order of every sum
+ * depends on the lengths of the whole batch, not on anything else. Errors: as
+ * kv4_append; GDN_E_SHAPE for n_q_heads not a multiple of n_kv_heads or more
+ * than 64 query heads per KV head, or a workspace that is too small. */
+gdn_status kv4_decode(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int n_q_heads,
+                      float sm_scale, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+                      int32_t *dev_status, void *stream);
+size_t kv4_decode_workspace(const kv4_cache *c, const kv4_batch *b, int n_q_heads);
+
+/* The same attention for prompt chunks of any length per sequence (ragged rows
+ * by q_start). total_kv: an upper bound of the sum of the kv_len of all
+ * sequences (it sizes the workspace, which holds the cached tokens in FP16 while the call runs); a sum above
+ * it sets GDN_E_RANGE. Errors: as kv4_decode. */
+gdn_status kv4_prefill(const kv4_cache *c, const kv4_batch *b, int64_t total_kv, const uint16_t *q, int64_t q_stride,
+                       int n_q_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,
+                       size_t workspace_bytes, int32_t *dev_status, void *stream);
+size_t kv4_prefill_workspace(const kv4_cache *c, const kv4_batch *b, int64_t total_kv, int n_q_heads);
+
+/* Copy pages src[i] -> dst[i] (device int32 [n]) in each of n_layers caches
+ * that lie layer_stride bytes apart from `pages`. page_bytes: a multiple of 16.
+ * No dst may repeat or be among the src. An id outside [0, num_pages) sets
+ * GDN_E_RANGE and that copy is left out. Errors: GDN_E_NULL, GDN_E_SHAPE,
+ * GDN_E_ALIGN, GDN_E_OVERFLOW, GDN_E_CUDA. */
+gdn_status kv4_copy_pages(uint8_t *pages, int n_layers, int64_t layer_stride, int num_pages, int64_t page_bytes,
+                          const int32_t *src, const int32_t *dst, int n, int32_t *dev_status, void *stream);
+
+/* Compact a cache: with L the number of distinct pages that block_table
+ * [rows][cols] names (entries below 0 name none), the live pages below L stay
+ * and the k-th live page from L on moves to the k-th free page below L, in all
+ * layers. tables_out [rows][cols] is block_table with the new ids (-1 where it
+ * named none; it must not overlap block_table), page_map [num_pages] the new
+ * id of every page (-1: free), n_live [1] is L: afterwards the pages from L on
+ * are free. The moved pages' old places keep their bytes, so a call with the
+ * same block_table gives the same result again. num_pages <= 2^20. An id >=
+ * num_pages sets GDN_E_RANGE and counts as -1. workspace:
+ * kv4_compact_workspace bytes. Errors: as kv4_copy_pages. */
+gdn_status kv4_compact(uint8_t *pages, int n_layers, int64_t layer_stride, int num_pages, int64_t page_bytes,
+                       const int32_t *block_table, int rows, int cols, int32_t *tables_out, int32_t *page_map,
+                       int32_t *n_live, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+size_t kv4_compact_workspace(int num_pages);
+
 /* Process-wide tuning knobs (they change speed, never results beyond FP32
  * summation order). knob 0: projection kernel of decode and prefill:
  * 0 = automatic (more than 4 activation rows and a reduction length that is a

@@ -37,6 +37,18 @@ class GdnWeights(ctypes.Structure):
                 ("A_log", _vp), ("dt_bias", _vp), ("norm_w", _vp)]
 
 
+class Kv4CacheStruct(ctypes.Structure):
+    _fields_ = [("pages", _vp), ("num_pages", _i), ("page_tokens", _i), ("n_kv_heads", _i), ("head_dim", _i),
+                ("k_scale", _f), ("v_scale", _f)]
+
+
+class Kv4BatchStruct(ctypes.Structure):
+    _fields_ = [("kv_len", _vp), ("block_table", _vp), ("q_start", _vp), ("B", _i), ("max_pages", _i), ("T", _i)]
+
+
+_kvc, _kvb = ctypes.POINTER(Kv4CacheStruct), ctypes.POINTER(Kv4BatchStruct)
+_l, _sz = ctypes.c_int64, ctypes.c_size_t
+
 SIGNATURES = {
     "gdn_status_string": (ctypes.c_char_p, [_i]),
     "gdn_create": (_i, [ctypes.POINTER(GdnConfig), ctypes.POINTER(GdnWeights), _vp, ctypes.POINTER(_vp)]),
@@ -56,6 +68,15 @@ SIGNATURES = {
     "gdn_set_tuning": (_i, [_i, _i]),
     "gdn_decode_step_static": (_i, [ctypes.POINTER(GdnConfig), ctypes.POINTER(GdnWeights), _vp, _vp, _i, _vp, _vp,
                                     _vp, _i, _vp, _vp]),
+    "kv4_append": (_i, [_kvc, _kvb, _vp, _l, _vp, _l, _vp, _vp]),
+    "kv4_read": (_i, [_kvc, _kvb, _vp, _vp, _vp, _vp]),
+    "kv4_decode": (_i, [_kvc, _kvb, _vp, _l, _i, _f, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "kv4_decode_workspace": (_sz, [_kvc, _kvb, _i]),
+    "kv4_prefill": (_i, [_kvc, _kvb, _l, _vp, _l, _i, _f, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "kv4_prefill_workspace": (_sz, [_kvc, _kvb, _l, _i]),
+    "kv4_copy_pages": (_i, [_vp, _i, _l, _i, _l, _vp, _vp, _i, _vp, _vp]),
+    "kv4_compact": (_i, [_vp, _i, _l, _i, _l, _vp, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "kv4_compact_workspace": (_sz, [_i]),
 }
 
 _lib = None
@@ -99,3 +120,4 @@ def _stream(stream=None) -> int:
 
 
 from .api import *  # noqa: E402,F401,F403
+from .kv4 import *  # noqa: E402,F401,F403

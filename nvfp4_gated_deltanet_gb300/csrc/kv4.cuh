@@ -1,0 +1,114 @@
+// The paged 4-bit KV cache: its layout and the kernels' arguments.
+#pragma once
+#include "common.cuh"
+
+namespace gdn {
+
+constexpr int kKv4Group = 16;  // tokens of one head that lie together
+
+// Where a group (16 tokens of one head, 18 d bytes) keeps token t. V's row
+// order and swapped halves let lane (g, tq) of a warp MMA read 8 (d = 64: 4)
+// code bytes of each of its four tokens 2tq, 2tq + 1, 2tq + 8, 2tq + 9 with the
+// 32 lanes on 32 different banks, and their scales of one block as one word.
+GDN_DEV int kv4_v_row(int t) { return (t & 8) | ((t & 1) << 2) | ((t >> 1) & 3); }
+template <int D>
+GDN_DEV int kv4_k_code(int t, int i) { return t * (D / 2) + i; }  // i: byte of the row
+template <int D>
+GDN_DEV int kv4_v_code(int t, int i) {
+  const int r = kv4_v_row(t);
+  return 8 * D + r * (D / 2) + (D == 128 ? i ^ (((r >> 1) & 1) << 5) : i);
+}
+template <int D>
+GDN_DEV int kv4_k_scale(int t, int b) { return 16 * D + t * (D / 16) + b; }
+template <int D>
+GDN_DEV int kv4_v_scale(int t, int b) { return 17 * D + b * 16 + ((t >> 1) & 3) * 4 + ((t & 1) | ((t >> 3) << 1)); }
+
+struct Kv4Args {
+  uint8_t *pages;
+  int num_pages, page_tokens, Hkv, D;
+  float ks, vs;
+  const int32_t *kv_len, *table, *q_start;  // q_start null: T / B rows each
+  int B, cols, T;
+  int32_t *status;
+};
+
+// A sequence's new rows [q0, q1) and its token count, checked: a bad entry
+// flags GDN_E_RANGE and reads as an empty sequence.
+struct Kv4Seq {
+  int q0, q1, len;
+};
+GDN_DEV Kv4Seq kv4_seq(const Kv4Args &a, int b) {
+  Kv4Seq s;
+  if (a.q_start) {
+    s.q0 = a.q_start[b];
+    s.q1 = a.q_start[b + 1];
+  } else {
+    const int r = a.T / a.B;
+    s.q0 = b * r;
+    s.q1 = s.q0 + r;
+  }
+  s.len = a.kv_len[b];
+  const bool bad_q = s.q0 < 0 || s.q1 < s.q0 || s.q1 > a.T;
+  const bool bad_len = s.len < 0 || s.len > (long long)a.cols * a.page_tokens;
+  if (bad_q || bad_len) flag_status(a.status, GDN_E_RANGE);
+  if (bad_q) s.q0 = s.q1 = 0;
+  if (bad_len) s.len = 0;
+  return s;
+}
+// The sequence whose rows hold row n, or -1 (a padding row).
+GDN_DEV int kv4_seq_of(const Kv4Args &a, int n) {
+  if (!a.q_start) return n / (a.T / a.B);
+  int lo = 0, hi = a.B;  // the first b with q_start[b + 1] > n
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.q_start[mid + 1] > n) hi = mid; else lo = mid + 1;
+  }
+  return lo < a.B ? lo : -1;
+}
+// The group that holds token `pos` of sequence b (head 0), or null for a bad page id.
+template <int D>
+GDN_DEV uint8_t *kv4_group(const Kv4Args &a, int b, int pos) {
+  const int page = a.table[(size_t)b * a.cols + pos / a.page_tokens];
+  if (page < 0 || page >= a.num_pages) {
+    flag_status(a.status, GDN_E_RANGE);
+    return nullptr;
+  }
+  return a.pages + ((size_t)page * a.Hkv * (a.page_tokens / 16) + (pos % a.page_tokens) / 16) * (18 * D);
+}
+// Bytes from one head's group to the next head's.
+template <int D>
+GDN_DEV size_t kv4_head_bytes(const Kv4Args &a) { return (size_t)(a.page_tokens / 16) * (18 * D); }
+
+cudaError_t launch_kv4_append(const Kv4Args &a, const uint16_t *k, long long k_stride, const uint16_t *v,
+                              long long v_stride, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4Args &a, uint16_t *k, uint16_t *v, cudaStream_t stream);
+
+struct Kv4AttnArgs {
+  Kv4Args c;
+  const uint16_t *q;
+  long long q_stride;
+  int Hq;
+  float sm_scale;
+  uint16_t *out;
+  float *lse;  // or null
+};
+cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t stream);
+
+struct Kv4PageArgs {
+  uint8_t *pages;
+  int layers, num_pages;
+  long long layer_stride, page_bytes;
+  const int32_t *src, *dst;
+  int n;
+  // compaction
+  const int32_t *table;
+  int rows, cols;
+  int32_t *tables_out, *page_map, *n_live;
+  void *workspace;
+  int32_t *status;
+};
+cudaError_t launch_kv4_copy_pages(const Kv4PageArgs &a, cudaStream_t stream);
+cudaError_t launch_kv4_compact(const Kv4PageArgs &a, cudaStream_t stream);
+size_t kv4_compact_bytes(int num_pages);
+
+}  // namespace gdn

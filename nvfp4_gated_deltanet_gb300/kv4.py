@@ -1,0 +1,400 @@
+"""The paged KV cache in 4 bits: its calls, and the book of who holds which page.
+
+The functions marshal the kv4_* entry points of ``include/gdn.h`` (layout,
+errors and numerics are described there). ``pages`` is a uint8 CUDA tensor
+[num_pages][Hkv][page_tokens / 16][18 * d], or [layers][num_pages]... for the
+calls that take all layers at once; its shape gives page_tokens, Hkv and d.
+
+    pages = kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim)
+    kv4_append(k, v, pages, table, kv_len, k_scale, v_scale)
+    out = kv4_decode(q, pages, table, kv_len, k_scale, v_scale)
+
+``KV4Book`` decides on the host which page goes where (allocation, forks that
+share pages, copy on write, compaction); ``KV4Cache`` joins a book with the
+pages of all layers.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import Kv4BatchStruct, Kv4CacheStruct, _check, _ptr, _stream, lib
+
+__all__ = ["kv4_new_pages", "kv4_append", "kv4_read", "kv4_decode", "kv4_prefill", "kv4_copy_pages", "kv4_compact",
+           "KV4Book", "KV4Batch", "KV4Cache"]
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim, n_layers=None, device="cuda"):
+    """Zeroed pages [num_pages][Hkv][page_tokens / 16][18 d], with a leading [n_layers] when given."""
+    shape = (num_pages, n_kv_heads, page_tokens // 16, 18 * head_dim)
+    return torch.zeros(shape if n_layers is None else (n_layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _i32(t, name, dims):
+    if t.dtype != torch.int32 or t.dim() != dims or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of {dims} dimension(s)")
+    return t
+
+
+def _cache(pages, k_scale, v_scale):
+    if pages.dtype != torch.uint8 or pages.dim() != 4 or not pages.is_cuda or not pages.is_contiguous():
+        raise ValueError("pages: expected a contiguous uint8 CUDA tensor [num_pages][Hkv][page_tokens / 16][18 d]")
+    n, h, g, cell = pages.shape
+    if cell % 18:
+        raise ValueError("pages: the last dimension is 18 * head_dim bytes")
+    return Kv4CacheStruct(pages.data_ptr(), n, 16 * g, h, cell // 18, k_scale, v_scale)
+
+
+def _batch(table, kv_len, q_start, rows):
+    _i32(table, "block_table", 2)
+    _i32(kv_len, "kv_len", 1)
+    B = table.shape[0]
+    if kv_len.shape[0] != B or (q_start is not None and _i32(q_start, "q_start", 1).shape[0] != B + 1):
+        raise ValueError("block_table, kv_len and q_start disagree on the number of sequences")
+    return Kv4BatchStruct(kv_len.data_ptr(), table.data_ptr(), _ptr(q_start), B, table.shape[1], rows)
+
+
+def _rows(t, name, heads, d):
+    """BF16 rows [T][heads][d] whose heads lie together; returns the row stride in elements."""
+    if t.dtype not in _BF16 or not t.is_cuda or t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
+        raise ValueError(f"{name}: expected BF16 CUDA rows [T][{heads or 'heads'}][{d}]")
+    if t.shape[0] == 0:
+        return t.shape[1] * d
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a row's heads must lie together in memory")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+
+
+def _out(t, name, shape, dtypes, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtypes[0], device=device)
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtypes[0]} CUDA tensor of shape {tuple(shape)}")
+    return t
+
+
+def _workspace(n, given, device, stream):
+    """Device scratch of n bytes for work on `stream`."""
+    if given is not None:
+        if not given.is_cuda or not given.is_contiguous():
+            raise ValueError("workspace: expected a contiguous CUDA tensor")
+        return given, given.numel() * given.element_size()
+    w = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        w.record_stream(stream)  # freed here, used there
+    return w, n
+
+
+def kv4_append(k, v, pages, block_table, kv_len, k_scale, v_scale, q_start=None, dev_status=None, stream=None):
+    """Quantise the new rows k and v [T][Hkv][d] (BF16) into their sequences' pages (kv_len counts them already)."""
+    c = _cache(pages, k_scale, v_scale)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v have different numbers of rows")
+    ks, vs = _rows(k, "k", c.n_kv_heads, c.head_dim), _rows(v, "v", c.n_kv_heads, c.head_dim)
+    b = _batch(block_table, kv_len, q_start, k.shape[0])
+    _check(lib().kv4_append(ctypes.byref(c), ctypes.byref(b), _ptr(k), ks, _ptr(v), vs, _ptr(dev_status),
+                            _stream(stream)), "kv4_append")
+
+
+def kv4_read(pages, block_table, kv_len, k_scale, v_scale, rows, q_start=None, k=None, v=None, dev_status=None,
+             stream=None):
+    """(k, v) [rows][Hkv][d] BF16: the values that the pages hold for the batch's new rows."""
+    c = _cache(pages, k_scale, v_scale)
+    b = _batch(block_table, kv_len, q_start, rows)
+    shape = (rows, c.n_kv_heads, c.head_dim)
+    k, v = _out(k, "k", shape, _BF16, pages.device), _out(v, "v", shape, _BF16, pages.device)
+    _check(lib().kv4_read(ctypes.byref(c), ctypes.byref(b), _ptr(k), _ptr(v), _ptr(dev_status), _stream(stream)),
+           "kv4_read")
+    return k, v
+
+
+def kv4_decode(q, pages, block_table, kv_len, k_scale, v_scale, sm_scale=None, out=None, lse=None, return_lse=False,
+               workspace=None, dev_status=None, stream=None):
+    """Attention of the batch's newest tokens: q [B][Hq][d] (one token per
+    sequence) or [B][r][Hq][d] (r candidates) -> out of q's shape, BF16; with
+    return_lse also the rows' log-sum-exp, FP32. sm_scale: d^-1/2 by default."""
+    c = _cache(pages, k_scale, v_scale)
+    if q.dim() not in (3, 4):
+        raise ValueError("q: expected [B][Hq][d] or [B][r][Hq][d]")
+    rows = q
+    if q.dim() == 4:
+        if q.shape[1] != 1 and q.shape[0] > 1 and q.stride(0) != q.shape[1] * q.stride(1):
+            raise ValueError("q: the rows of all sequences must be evenly spaced")
+        rows = q.flatten(0, 1) if q.shape[1] != 1 else q[:, 0]
+    qs = _rows(rows, "q", None, c.head_dim)
+    T, Hq = rows.shape[0], rows.shape[1]
+    b = _batch(block_table, kv_len, None, T)
+    if q.shape[0] != b.B:
+        raise ValueError("q and block_table disagree on the number of sequences")
+    out = _out(out, "out", q.shape, (torch.bfloat16, *_BF16[1:]), q.device)
+    if return_lse or lse is not None:
+        lse = _out(lse, "lse", q.shape[:-1], (torch.float32,), q.device)
+    L = lib()
+    ws, n = _workspace(L.kv4_decode_workspace(ctypes.byref(c), ctypes.byref(b), Hq), workspace, q.device, stream)
+    _check(L.kv4_decode(ctypes.byref(c), ctypes.byref(b), _ptr(rows), qs, Hq,
+                        c.head_dim ** -0.5 if sm_scale is None else sm_scale, _ptr(out), _ptr(lse), _ptr(ws), n,
+                        _ptr(dev_status), _stream(stream)), "kv4_decode")
+    return (out, lse) if return_lse else out
+
+
+def kv4_prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_kv=None, sm_scale=None, out=None,
+                lse=None, return_lse=False, workspace=None, dev_status=None, stream=None):
+    """Causal attention of ragged prompt chunks: q [T][Hq][d], sequence b's rows
+    [q_start[b], q_start[b + 1]) being its newest tokens. total_kv: an upper
+    bound of kv_len's sum (default: what the tables can hold)."""
+    c = _cache(pages, k_scale, v_scale)
+    qs = _rows(q, "q", None, c.head_dim)
+    T, Hq = q.shape[0], q.shape[1]
+    b = _batch(block_table, kv_len, q_start, T)
+    if total_kv is None:
+        total_kv = b.B * b.max_pages * c.page_tokens
+    out = _out(out, "out", q.shape, (torch.bfloat16, *_BF16[1:]), q.device)
+    if return_lse or lse is not None:
+        lse = _out(lse, "lse", q.shape[:-1], (torch.float32,), q.device)
+    L = lib()
+    ws, n = _workspace(L.kv4_prefill_workspace(ctypes.byref(c), ctypes.byref(b), total_kv, Hq), workspace, q.device,
+                       stream)
+    _check(L.kv4_prefill(ctypes.byref(c), ctypes.byref(b), total_kv, _ptr(q), qs, Hq,
+                         c.head_dim ** -0.5 if sm_scale is None else sm_scale, _ptr(out), _ptr(lse), _ptr(ws), n,
+                         _ptr(dev_status), _stream(stream)), "kv4_prefill")
+    return (out, lse) if return_lse else out
+
+
+def _layers(pages):
+    """(layers, bytes from one layer to the next, pages, bytes of a page) of [L][num_pages]... or [num_pages]..."""
+    if pages.dtype != torch.uint8 or pages.dim() not in (4, 5) or not pages.is_cuda:
+        raise ValueError("pages: expected a uint8 CUDA tensor [num_pages][Hkv][groups][18 d] or [layers][num_pages]...")
+    one = pages if pages.dim() == 4 else pages[0]
+    if not one.is_contiguous():
+        raise ValueError("pages: a layer's pages must be contiguous")
+    size = one[0].numel()
+    return (1, 0, one.shape[0], size) if pages.dim() == 4 else (pages.shape[0], pages.stride(0), one.shape[0], size)
+
+
+def kv4_copy_pages(pages, src, dst, dev_status=None, stream=None):
+    """Copy pages src[i] -> dst[i] (int32 CUDA tensors) in every layer."""
+    layers, stride, n, size = _layers(pages)
+    _i32(src, "src", 1)
+    _i32(dst, "dst", 1)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst have different lengths")
+    _check(lib().kv4_copy_pages(_ptr(pages), layers, stride, n, size, _ptr(src), _ptr(dst), src.shape[0],
+                                _ptr(dev_status), _stream(stream)), "kv4_copy_pages")
+
+
+def kv4_compact(pages, block_table, tables_out=None, page_map=None, n_live=None, workspace=None, dev_status=None,
+                stream=None):
+    """Move the live pages (those that block_table names) to the front in every
+    layer. Returns (the tables with the new ids, every page's new id or -1, the
+    number of live pages [1]), all int32."""
+    layers, stride, n, size = _layers(pages)
+    _i32(block_table, "block_table", 2)
+    i32 = (torch.int32,)
+    tables_out = _out(tables_out, "tables_out", block_table.shape, i32, pages.device)
+    page_map = _out(page_map, "page_map", (n,), i32, pages.device)
+    n_live = _out(n_live, "n_live", (1,), i32, pages.device)
+    L = lib()
+    ws, nb = _workspace(L.kv4_compact_workspace(n), workspace, pages.device, stream)
+    _check(L.kv4_compact(_ptr(pages), layers, stride, n, size, _ptr(block_table), *block_table.shape,
+                         _ptr(tables_out), _ptr(page_map), _ptr(n_live), _ptr(ws), nb, _ptr(dev_status),
+                         _stream(stream)), "kv4_compact")
+    return tables_out, page_map, n_live
+
+
+class KV4Book:
+    """Which sequence holds which pages (host only). Pages are counted by their
+    holders; a fork shares them all, and a sequence that grows into a page that
+    it shares gets a copy of its own first."""
+
+    def __init__(self, num_pages: int, page_tokens: int):
+        self.num_pages, self.page_tokens = num_pages, page_tokens
+        self.holders = [0] * num_pages
+        self._free = list(range(num_pages - 1, -1, -1))  # the lowest id is handed out first
+        self.seqs = {}                                   # id -> [pages, tokens]
+        self._next = 0
+
+    @property
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    def length(self, seq: int) -> int:
+        return self.seqs[seq][1]
+
+    def pages(self, seq: int) -> list:
+        return list(self.seqs[seq][0])
+
+    def new(self) -> int:
+        self._next += 1
+        self.seqs[self._next - 1] = [[], 0]
+        return self._next - 1
+
+    def extend(self, seqs, tokens) -> list:
+        """Room for tokens[i] more tokens of sequence seqs[i]; returns the
+        (src, dst) page copies to make before they are written. Changes nothing
+        when the pages run out."""
+        if len(tokens) != len(seqs) or len(set(seqs)) != len(seqs) or any(n < 0 for n in tokens):
+            raise ValueError("one number of tokens, zero or more, for each of distinct sequences")
+        left, plan, want = {}, [], 0  # left: holders of a shared last page that have not yet left it
+        for s, add in zip(seqs, tokens):
+            pages, n = self.seqs[s]
+            need = -(-(n + add) // self.page_tokens) - len(pages)
+            shared = False
+            if add > 0 and n % self.page_tokens != 0:
+                last = pages[-1]
+                shared = left.setdefault(last, self.holders[last]) > 1
+                left[last] -= shared
+            plan.append((s, add, need, shared))
+            want += need + shared
+        if want > len(self._free):
+            raise MemoryError(f"{want} pages wanted, {len(self._free)} free")
+        copies = []
+        for s, add, need, shared in plan:
+            pages = self.seqs[s][0]
+            if shared:
+                mine = self._take()
+                copies.append((pages[-1], mine))
+                self.holders[pages[-1]] -= 1
+                pages[-1] = mine
+            pages += [self._take() for _ in range(need)]
+            self.seqs[s][1] += add
+        return copies
+
+    def fork(self, seq: int) -> int:
+        pages, n = self.seqs[seq]
+        for p in pages:
+            self.holders[p] += 1
+        child = self.new()
+        self.seqs[child] = [list(pages), n]
+        return child
+
+    def truncate(self, seq: int, tokens: int):
+        """Drop the tokens from `tokens` on (rejected candidates) and the pages that only they needed."""
+        pages, n = self.seqs[seq]
+        if not 0 <= tokens <= n:
+            raise ValueError("a sequence is cut to at most its length")
+        keep = -(-tokens // self.page_tokens)
+        for p in pages[keep:]:
+            self._drop(p)
+        self.seqs[seq] = [pages[:keep], tokens]
+
+    def free(self, seq: int):
+        for p in self.seqs.pop(seq)[0]:
+            self._drop(p)
+
+    def compact(self) -> list:
+        """kv4_compact's plan: every page's new id (-1: free), applied to the book."""
+        live = [p for p in range(self.num_pages) if self.holders[p]]
+        L = len(live)
+        holes = iter([p for p in range(L) if not self.holders[p]])
+        to = [-1] * self.num_pages
+        for p in live:
+            to[p] = p if p < L else next(holes)
+        held = [0] * self.num_pages
+        for p in live:
+            held[to[p]] = self.holders[p]
+        self.holders = held
+        self._free = list(range(self.num_pages - 1, L - 1, -1))
+        for s in self.seqs.values():
+            s[0] = [to[p] for p in s[0]]
+        return to
+
+    def _take(self) -> int:
+        p = self._free.pop()
+        self.holders[p] = 1
+        return p
+
+    def _drop(self, p: int):
+        self.holders[p] -= 1
+        if self.holders[p] == 0:
+            self._free.append(p)
+
+
+class KV4Batch:
+    """A batch's device tables: block_table [B][cols], kv_len [B], q_start
+    [B + 1] (int32), and on the host its rows T and its cached tokens total_kv."""
+
+    def __init__(self, block_table, kv_len, q_start, T, total_kv):
+        self.block_table, self.kv_len, self.q_start, self.T, self.total_kv = block_table, kv_len, q_start, T, total_kv
+
+
+class KV4Cache:
+    """The pages of n_layers attention layers, their tensor scales and the book
+    of their sequences. A step: batch = cache.grow(seqs, new_tokens), then per
+    layer append, and decode or prefill."""
+
+    def __init__(self, num_pages, page_tokens, n_kv_heads, head_dim, k_scale, v_scale, n_layers=1, device="cuda"):
+        self.book = KV4Book(num_pages, page_tokens)
+        self.layers = kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim, n_layers, device)
+        self.scales = [(float(k_scale), float(v_scale))] * n_layers
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device = self.layers.device
+
+    def new(self) -> int:
+        return self.book.new()
+
+    def free(self, seq: int):
+        self.book.free(seq)
+
+    def fork(self, seq: int) -> int:
+        """A new sequence with the same tokens; no page is copied until one of the two grows."""
+        return self.book.fork(seq)
+
+    def truncate(self, seq: int, tokens: int):
+        self.book.truncate(seq, tokens)
+
+    def _dev(self, rows):
+        return torch.tensor(rows, dtype=torch.int32).pin_memory().to(self.device, non_blocking=True)
+
+    def grow(self, seqs, tokens, stream=None) -> KV4Batch:
+        """Room for tokens[i] (or `tokens` each) new tokens of every sequence,
+        the copies of shared pages made, and the batch of the new rows."""
+        tokens = [tokens] * len(seqs) if isinstance(tokens, int) else list(tokens)
+        pairs = self.book.extend(seqs, tokens)
+        if pairs:
+            src, dst = self._dev([p[0] for p in pairs]), self._dev([p[1] for p in pairs])
+            kv4_copy_pages(self.layers, src, dst, dev_status=self.status, stream=stream)
+        return self.batch(seqs, tokens)
+
+    def batch(self, seqs, tokens) -> KV4Batch:
+        """The tables of the sequences as they are, their newest tokens[i] as the rows."""
+        pages = [self.book.pages(s) for s in seqs]
+        cols = max([1] + [len(p) for p in pages])
+        lens = [self.book.length(s) for s in seqs]
+        at = [0]
+        for n in tokens:
+            at.append(at[-1] + n)
+        return KV4Batch(self._dev([p + [-1] * (cols - len(p)) for p in pages]), self._dev(lens), self._dev(at), at[-1],
+                        sum(lens))
+
+    def append(self, layer, k, v, batch, stream=None):
+        kv4_append(k, v, self.layers[layer], batch.block_table, batch.kv_len, *self.scales[layer],
+                   q_start=batch.q_start, dev_status=self.status, stream=stream)
+
+    def decode(self, layer, q, batch, **kw):
+        """q [B][Hq][d] or [B][r][Hq][d]: as many rows per sequence as the batch has."""
+        return kv4_decode(q, self.layers[layer], batch.block_table, batch.kv_len, *self.scales[layer],
+                          dev_status=self.status, **kw)
+
+    def prefill(self, layer, q, batch, **kw):
+        return kv4_prefill(q, self.layers[layer], batch.block_table, batch.kv_len, batch.q_start, *self.scales[layer],
+                           total_kv=batch.total_kv, dev_status=self.status, **kw)
+
+    def compact(self, stream=None) -> int:
+        """Move the live pages to the front of every layer; returns their number. Earlier batches are void."""
+        seqs = list(self.book.seqs)
+        pages = [self.book.pages(s) for s in seqs]
+        cols = max([1] + [len(p) for p in pages])
+        table = self._dev([p + [-1] * (cols - len(p)) for p in pages] or [[-1]])
+        kv4_compact(self.layers, table, dev_status=self.status, stream=stream)
+        self.book.compact()
+        return self.book.num_pages - self.book.free_pages
+
+    def check(self) -> int:
+        """Synchronise, return the sticky device status and clear it."""
+        st = int(self.status.item())
+        self.status.zero_()
+        return st

@@ -1,0 +1,95 @@
+"""The 4-bit KV cache and its attention in float64, from the layout and the
+formulas alone (numpy, one head and one token at a time)."""
+import math
+
+import numpy as np
+
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6], np.float64)
+
+
+def e4m3(byte):
+    e, m = byte >> 3 & 15, byte & 7
+    if e == 15 and m == 7:
+        return math.nan
+    v = (1 + m / 8) * 2.0 ** (e - 7) if e else m / 8 * 2.0 ** -6
+    return -v if byte & 128 else v
+
+
+E4M3 = np.array([e4m3(b) for b in range(256)])
+
+
+def v_row(t):
+    return (t & 8) | ((t & 1) << 2) | ((t >> 1) & 3)
+
+
+def places(t, d):
+    """Byte offsets within a group of token t: K codes, V codes, K scales, V scales."""
+    i = np.arange(d // 2)
+    r = v_row(t)
+    swap = (r >> 1 & 1) << 5 if d == 128 else 0
+    b = np.arange(d // 16)
+    return (t * (d // 2) + i, 8 * d + r * (d // 2) + (i ^ swap), 16 * d + t * (d // 16) + b,
+            17 * d + 16 * b + 4 * (t >> 1 & 3) + ((t & 1) | (t >> 3) << 1))
+
+
+def decode_row(codes, scales):
+    nib = np.stack([codes & 15, codes >> 4], 1).reshape(-1)
+    val = E2M1[nib & 7] * np.where(nib & 8, -1.0, 1.0)
+    return val * np.repeat(E4M3[scales], 16)
+
+
+def cached(pages, table_row, n, d, ks, vs):
+    """float64 K, V [Hkv][n][d] of a sequence's first n tokens (pages: numpy uint8)."""
+    H, groups = pages.shape[1], pages.shape[2]
+    K, V = np.empty((H, n, d)), np.empty((H, n, d))
+    for p in range(n):
+        page, off = table_row[p // (16 * groups)], p % (16 * groups)
+        kc, vc, ksc, vsc = places(off % 16, d)
+        for h in range(H):
+            cell = pages[page, h, off // 16]
+            K[h, p] = decode_row(cell[kc], cell[ksc]) * float(np.float32(ks))
+            V[h, p] = decode_row(cell[vc], cell[vsc]) * float(np.float32(vs))
+    return K, V
+
+
+def attention(q, K, V, sm):
+    """q [n][Hq][d] float64 (the sequence's newest tokens) against K, V [Hkv][m][d].
+    Returns out, lse, and the two sums the error bounds are made of: the largest
+    sum_i |q_i k_i| sm over the keys a row sees, and sum_j p_j |v_j|."""
+    n, Hq, d = q.shape
+    H, m, _ = K.shape
+    out, lse = np.zeros((n, Hq, d)), np.full((n, Hq), -math.inf)
+    big, mass = np.zeros((n, Hq)), np.zeros((n, Hq, d))
+    for i in range(n):
+        see = m - n + i + 1
+        if see <= 0:
+            continue
+        for h in range(Hq):
+            k, v = K[h // (Hq // H), :see], V[h // (Hq // H), :see]
+            z = k @ q[i, h] * sm
+            top = z.max()
+            p = np.exp(z - top)
+            lse[i, h] = top + math.log(p.sum())
+            p /= p.sum()
+            out[i, h] = p @ v
+            mass[i, h] = p @ np.abs(v)
+            big[i, h] = (np.abs(k) @ np.abs(q[i, h])).max() * sm
+    return out, lse, big, mass
+
+
+def bounds(ref, d):
+    """Elementwise error bounds of the BF16 output and the FP32 lse.
+
+    A score is a sum of d exact products in FP32 (each of its at most d + 4
+    roundings at most 2^-24 of sum |q_i k_i|) times the scales (2 roundings),
+    and 2^x and the lse's logarithm are good to a few 2^-22. The weight of a
+    key is then off by at most ez relatively, is rounded to FP16 (2^-11; the
+    sum of the weights is taken before it), and P V and the sum are FP32 sums
+    of n positive-weighted terms in blocks (2^-16 covers n / 16 + 64 steps of
+    the lengths tested). The output is rounded to BF16 (2^-8, at most 2^-134
+    near zero)."""
+    out, lse, big, mass = ref
+    ez = (d + 8) * 2.0 ** -24 * big + 2.0 ** -20
+    rel = 2 * ez[..., None] + 2.0 ** -11 + 2.0 ** -15
+    near = np.abs(out) + rel * mass
+    return 2.0 ** -8 * near + rel * mass + 1e-38, ez + 2.0 ** -16 + 2.0 ** -23 * np.abs(np.where(np.isfinite(lse), lse, 0))
