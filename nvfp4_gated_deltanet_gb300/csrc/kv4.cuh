@@ -93,6 +93,8 @@ struct Kv4AttnArgs {
   float *lse;  // or null
 };
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream);
+size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms);  // its workspace
 
 struct Kv4PageArgs {
   uint8_t *pages;

@@ -8,8 +8,21 @@ using namespace gdn;
 
 namespace {
 
+constexpr int kMaxSms = 160;  // what the workspaces are sized for, so that their size needs no device
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 gdn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_E_CUDA; }
+
+// SMs of the current device (0: the query failed).
+int num_sms() {
+  static int known[64] = {};
+  int dev = -1, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < 64 && known[dev]) return known[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev] = n;
+  return n;
+}
 
 // The cache and the batch; rows = T * heads of the largest tensor.
 gdn_status check(const kv4_cache *c, const kv4_batch *b, Kv4Args &a, int32_t *status) {
@@ -93,7 +106,14 @@ gdn_status kv4_read(const kv4_cache *c, const kv4_batch *b, uint16_t *k, uint16_
   return cuda_status(launch_kv4_read(a, k, v, static_cast<cudaStream_t>(stream)));
 }
 
-size_t kv4_decode_workspace(const kv4_cache *, const kv4_batch *, int) { return 0; }
+// 0 for arguments that kv4_decode refuses.
+size_t kv4_decode_workspace(const kv4_cache *c, const kv4_batch *b, int n_q_heads) {
+  Kv4AttnArgs a{};
+  if (check(c, b, a.c, nullptr) != GDN_OK || b->T == 0 || b->q_start || n_q_heads < 1 || n_q_heads % c->n_kv_heads)
+    return 0;
+  a.Hq = n_q_heads;
+  return kv4_decode_bytes(a, kMaxSms);
+}
 
 gdn_status kv4_decode(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int n_q_heads,
                       float sm_scale, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
@@ -103,7 +123,13 @@ gdn_status kv4_decode(const kv4_cache *c, const kv4_batch *b, const uint16_t *q,
   if (st != GDN_OK) return st;
   if (b->q_start) return GDN_E_SHAPE;
   if (b->T == 0) return GDN_OK;
-  return cuda_status(launch_kv4_attention(a, static_cast<cudaStream_t>(stream)));
+  const size_t need = kv4_decode_bytes(a, kMaxSms);
+  if (need && !workspace) return GDN_E_NULL;
+  if (workspace_bytes < need) return GDN_E_SHAPE;
+  if (!aligned16(workspace)) return GDN_E_ALIGN;
+  const int sms = num_sms();
+  if (sms < 1) return GDN_E_CUDA;
+  return cuda_status(launch_kv4_decode(a, workspace, sms < kMaxSms ? sms : kMaxSms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kv4_prefill_workspace(const kv4_cache *, const kv4_batch *, int64_t, int) { return 0; }

@@ -54,12 +54,13 @@ def cached(pages, table_row, n, d, ks, vs):
 
 def attention(q, K, V, sm):
     """q [n][Hq][d] float64 (the sequence's newest tokens) against K, V [Hkv][m][d].
-    Returns out, lse, and the two sums the error bounds are made of: the largest
-    sum_i |q_i k_i| sm over the keys a row sees, and sum_j p_j |v_j|."""
+    Returns out, lse, and the sums the error bounds are made of: the largest
+    sum_i |q_i k_i| sm over the keys a row sees, sum_j p_j |v_j|, and
+    p_max sum_j |v_j|."""
     n, Hq, d = q.shape
     H, m, _ = K.shape
     out, lse = np.zeros((n, Hq, d)), np.full((n, Hq), -math.inf)
-    big, mass = np.zeros((n, Hq)), np.zeros((n, Hq, d))
+    big, mass, flat = np.zeros((n, Hq)), np.zeros((n, Hq, d)), np.zeros((n, Hq, d))
     for i in range(n):
         see = m - n + i + 1
         if see <= 0:
@@ -73,8 +74,9 @@ def attention(q, K, V, sm):
             p /= p.sum()
             out[i, h] = p @ v
             mass[i, h] = p @ np.abs(v)
+            flat[i, h] = p.max() * np.abs(v).sum(0)
             big[i, h] = (np.abs(k) @ np.abs(q[i, h])).max() * sm
-    return out, lse, big, mass
+    return out, lse, big, mass, flat
 
 
 def bounds(ref, d):
@@ -86,10 +88,12 @@ def bounds(ref, d):
     key is then off by at most ez relatively, is rounded to FP16 (2^-11; the
     sum of the weights is taken before it), and P V and the sum are FP32 sums
     of n positive-weighted terms in blocks (2^-16 covers n / 16 + 64 steps of
-    the lengths tested). The output is rounded to BF16 (2^-8, at most 2^-134
-    near zero)."""
-    out, lse, big, mass = ref
+    the lengths tested). FP16 is fixed point at its lower end, with steps of
+    2^-24: the weights are scaled by at least 2^6 over the largest, so one that
+    is far below it is off by up to 2^-31 of the largest instead. The output is
+    rounded to BF16 (2^-8, at most 2^-134 near zero)."""
+    out, lse, big, mass, flat = ref
     ez = (d + 8) * 2.0 ** -24 * big + 2.0 ** -20
     rel = 2 * ez[..., None] + 2.0 ** -11 + 2.0 ** -15
-    near = np.abs(out) + rel * mass
-    return 2.0 ** -8 * near + rel * mass + 1e-38, ez + 2.0 ** -16 + 2.0 ** -23 * np.abs(np.where(np.isfinite(lse), lse, 0))
+    err = rel * mass + 2.0 ** -31 * flat
+    return 2.0 ** -8 * (np.abs(out) + err) + err + 1e-38, ez + 2.0 ** -16 + 2.0 ** -23 * np.abs(np.where(np.isfinite(lse), lse, 0))

@@ -57,7 +57,7 @@ def queries(T, hq, d, seed, scale=1.5):
 
 
 def want(pages, tab, lens, counts, q, d):
-    """The reference's (out, lse, big, mass) of every row."""
+    """The reference's outputs and error sums of every row."""
     p, t, q = pages.cpu().numpy(), tab.cpu().numpy(), f64(q)
     parts, at = [], 0
     for b, (n, m) in enumerate(zip(counts, lens)):
