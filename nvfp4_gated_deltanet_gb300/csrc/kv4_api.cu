@@ -132,7 +132,12 @@ gdn_status kv4_decode(const kv4_cache *c, const kv4_batch *b, const uint16_t *q,
   return cuda_status(launch_kv4_decode(a, workspace, sms < kMaxSms ? sms : kMaxSms, static_cast<cudaStream_t>(stream)));
 }
 
-size_t kv4_prefill_workspace(const kv4_cache *, const kv4_batch *, int64_t, int) { return 0; }
+// 0 for arguments that kv4_prefill refuses.
+size_t kv4_prefill_workspace(const kv4_cache *c, const kv4_batch *b, int64_t total_kv, int) {
+  Kv4AttnArgs a{};
+  if (check(c, b, a.c, nullptr) != GDN_OK || b->T == 0 || total_kv < 0 || total_kv > 0x7fffffffLL) return 0;
+  return kv4_prefill_bytes(a, total_kv);
+}
 
 gdn_status kv4_prefill(const kv4_cache *c, const kv4_batch *b, int64_t total_kv, const uint16_t *q, int64_t q_stride,
                        int n_q_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,
@@ -142,7 +147,12 @@ gdn_status kv4_prefill(const kv4_cache *c, const kv4_batch *b, int64_t total_kv,
   if (st != GDN_OK) return st;
   if (total_kv < 0) return GDN_E_SHAPE;
   if (b->T == 0) return GDN_OK;
-  return cuda_status(launch_kv4_attention(a, static_cast<cudaStream_t>(stream)));
+  const size_t need = total_kv > 0x7fffffffLL ? 0 : kv4_prefill_bytes(a, total_kv);
+  if (need == 0) return GDN_E_OVERFLOW;
+  if (!workspace) return GDN_E_NULL;
+  if (workspace_bytes < need) return GDN_E_SHAPE;
+  if (!aligned16(workspace)) return GDN_E_ALIGN;
+  return cuda_status(launch_kv4_prefill(a, total_kv, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status kv4_copy_pages(uint8_t *pages, int n_layers, int64_t layer_stride, int num_pages, int64_t page_bytes,

@@ -69,23 +69,6 @@ struct ScanLayout {
   static_assert(6 * R <= 256, "three accumulators of 2R columns");
 };
 
-// byte offset of FP16 element (row, col) in a [rows][64 FP16] tile, 128-byte swizzle
-GDN_DEV uint32_t sw_off16(int row, int col) {
-  return (uint32_t)(row * 128 + ((((col >> 3) ^ (row & 7)) << 4) | ((col & 7) << 1)));
-}
-// Instruction descriptor of kind::f16 with FP16 A and B, FP32 accumulator,
-// both K-major, M = 128, N = n.
-GDN_DEV uint32_t idesc_f16(int n) {
-  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-GDN_DEV void mma_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // D (+)= A B'^T over K = 64 (four K = 16 steps) with A = hi + lo in a ring
 // slot (hi tile at `slot`, lo tile kLoOff further) and B' = [B_hi; B_lo]
 // (N = 2R; b(j): the descriptor of K step j): columns 0..R-1 of D collect
@@ -126,28 +109,6 @@ GDN_DEV void prefetch_l2(const void *p, uint32_t bytes) {
 
 // 1 / s for a power of two s = 2^k, |k| <= 126: the exponent negated (exact)
 GDN_DEV float inv_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
-
-// Bounded wait that also gives up when another role has given up.
-GDN_DEV bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag, int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!mbar_try_wait_sleep(bar, parity, 2000u)) {
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *abort_flag = 1u;
-      flag_status(status, GDN_E_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-// The same, decided by lane 0 for the whole warp (collective TMEM accesses
-// that follow run with all 32 lanes or none).
-GDN_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag, int32_t *status) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait_or_abort(bar, parity, abort_flag, status) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
 
 // The largest of v over the eight epilogue warps: lane 0 of each warp posts
 // its warp's largest value in red[warp] and arrives on `bar` (count 8), waits
