@@ -79,6 +79,39 @@ GDN_DEV uint8_t *kv4_group(const Kv4Args &a, int b, int pos) {
 template <int D>
 GDN_DEV size_t kv4_head_bytes(const Kv4Args &a) { return (size_t)(a.page_tokens / 16) * (18 * D); }
 
+// ---------------------------------------------------------------- arithmetic of the attention kernels
+GDN_DEV uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+// Eight E2M1 codes times a pair of scales
+GDN_DEV void decode8(uint32_t w, __half2 s, uint32_t (&o)[4]) {
+  __half2 h[4];
+  e2m1x8_to_h2x4(w, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = h2u(__hmul2(h[i], s));
+}
+
+// 2^x, to two units in the last place; 2^-inf = 0
+GDN_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (x.lo, x.hi) * s + o
+GDN_DEV float2 fma2(float2 x, float2 s, float2 o) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<unsigned long long *>(&r))
+      : "l"(*reinterpret_cast<unsigned long long *>(&x)), "l"(*reinterpret_cast<unsigned long long *>(&s)),
+        "l"(*reinterpret_cast<unsigned long long *>(&o)));
+  return r;
+}
+GDN_DEV float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long *>(&r))
+      : "l"(*reinterpret_cast<unsigned long long *>(&x)), "l"(*reinterpret_cast<unsigned long long *>(&y)));
+  return r;
+}
+
 cudaError_t launch_kv4_append(const Kv4Args &a, const uint16_t *k, long long k_stride, const uint16_t *v,
                               long long v_stride, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4Args &a, uint16_t *k, uint16_t *v, cudaStream_t stream);

@@ -22,49 +22,76 @@
 // that are loaded), for at most 64 columns.
 //
 // Rounding: q enters in FP16 scaled by a power of two per row (exact but for
-// elements 2^-27 below the row's largest); the weights 2^(z - m + 14) are
-// rounded to FP16 (2^-11 relative, down to 2^-28 of the largest weight); the
-// scores, the sums and the output are FP32.
+// elements 2^-27 below the row's largest); the weights 2^(z - m + 7) are rounded
+// to FP16 (2^-11 relative down to 2^-21 of the largest weight, in steps of 2^-31
+// of it below); the scores, the sums and the output are FP32.
 //
-// Work: a tile is 64 tokens (32 with more than 16 query rows) of one item = a
-// (sequence, KV head, group of query rows). All items' tiles, in order, are
-// cut into equal runs, one per CTA -- ragged lengths cost no idle SM -- and a
-// run's tiles go round its 8 warps, each with its own ring of stages that it
-// fills by bulk copies. At the end of an item (or run) the warps' (m, l, O)
-// meet in shared memory; an item that lies in one run is finished there, the
-// pieces of others go to the workspace and kv4_join_kernel adds them in order.
+// Work: a tile is 32 tokens (64 for d = 64) of one item = a (sequence, KV head,
+// group of query rows). All items' tiles, in order, are cut into runs of equal
+// cost, one per team of warps -- ragged lengths leave no SM idle. The team's
+// warps take the run's tiles in turn, each with two slots of its own that it
+// refills by bulk copies as soon as it has read them, and its own (m, l, O),
+// which meet in shared memory at the end of an item or of the run. An item that
+// lies in one run is finished there; the pieces of others go to the workspace
+// and kv4_join_kernel adds them in order.
+// A team is a whole CTA where there are fewer items than SMs (long contexts:
+// few pieces to join), else four warps: the other teams of the CTA work while
+// one's parts meet, and fewer warps wait for the slowest.
 #include "kv4.cuh"
+#include "tc.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr float kShift = 14.0f;  // weights are 2^(z - m + 14): at most 2^14 in FP16, normal down to 2^-28 of that
+// A column's weights are 2^(z - m + 7); m only moves (and O is rescaled) when a
+// score passes it by 7, so that a tile whose scores do not costs no exchange
+// between lanes and no rescaling. Weights stay below 2^14 in FP16.
+constexpr float kShift = 7.0f, kSlack = 7.0f;
 
-template <int D, int NQ>
+// Warps by the registers they need: 128, 168 or 255 each. NQ: 8-row column
+// blocks of an item.
+// TEAM: warps of a team, 0 for the whole CTA.
+template <int D, int NQ, int TEAM>
 struct DecodeShape {
-  static constexpr int kGroups = NQ == 4 ? 2 : 4;           // 16-token groups of a tile
+  static constexpr int kWarps = D == 128 ? (NQ == 1 ? 16 : NQ == 2 ? 12 : 8) : (NQ <= 2 ? 16 : 12);
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kTeam = TEAM ? TEAM : kWarps, kTeams = kWarps / kTeam;
+  static_assert(kWarps % kTeam == 0, "teams fill the CTA");
+  static constexpr int kGroups = D == 64 && NQ <= 2 ? 4 : 2;  // 16-token groups of a tile
   static constexpr int kTile = kGroups * 16;
-  static constexpr int kStage = kGroups * 18 * D;
-  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kSlot = kGroups * 18 * D;
   static constexpr int kRows = 8 * NQ;
-  static constexpr int kLd = D + 4;                         // row of the meeting buffer, floats
-  static constexpr bool kQShared = D == 128 && NQ == 4;     // 64 registers of q would not fit beside 128 of O
-  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kLd = D + 4;                           // row of the meeting buffer, floats
+  static constexpr bool kQShared = D == 128 && NQ == 4;       // 64 registers of q would not fit beside 128 of O
   static constexpr int kMeet = kWarps * kRows * kLd * 4;
-  static constexpr int kStats = 2 * 2 * kWarps * kRows * 4;  // m and l, two segments
+  static constexpr int kStats = 2 * 2 * kWarps * kRows * 4;   // m and l, two segments
+  static constexpr int kQRaw = kTeams * kRows * D * 2;        // a segment's query rows
   static constexpr int kQ = kQShared ? (D / 16) * NQ * 32 * 8 : 0;
-  static constexpr int kBytes = kRing + kMeet + kStats + kQ + kWarps * kStages * 8;
+  static_assert(!kQShared || kTeams == 1, "one converted copy of q");
+  static constexpr int kFixed = kMeet + kStats + kQRaw + kQ + 1024;
+  static constexpr int kSlots = 2 * kWarps;
+  static constexpr int kRing = kSlots * kSlot;
+  static constexpr int kBytes = kRing + kFixed;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
 struct DecodeArgs {
   Kv4AttnArgs a;
   int r, G, RG;      // new tokens per sequence, query heads per KV head, row groups per (sequence, KV head)
-  int whole;         // every item fits one CTA's warps: runs hold whole items, nothing to join
+  int extra;         // cost of an item beside its tiles, in tiles; kWhole: runs hold whole items, nothing to join
   float *part;       // [2 CTAs][rows][D] and, after them, their (m, l) [2 CTAs][rows][2]
 };
+// An item's query rows, its meeting and its output take a team about as long as
+// this many tiles of its run: a whole CTA, four warps.
+constexpr int kExtraCta = 24, kExtraTeam = 6;
+constexpr int kWhole = 1 << 20;
+constexpr int kManyItems = 152;  // from here on (a GB300's SMs) teams of four warps
+
+// a / b, mostly in 32 bits
+GDN_DEV long long quot(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 
 // Sequence b's tokens, checked (kv4_seq without rows), and its tiles: an empty
 // sequence has one tile with no tokens, so that its rows are written.
@@ -80,48 +107,96 @@ GDN_DEV int warp_isum(int v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// All sequences' tiles (of one KV head and row group).
-template <int TILE>
-GDN_DEV long long total_tiles(const Kv4Args &c, int lane) {
-  long long n = 0;
-  for (int b0 = 0; b0 < c.B; b0 += 32) n += warp_isum(b0 + lane < c.B ? tiles_of<TILE>(seq_len(c, b0 + lane)) : 0);
-  return n;
+// Runs that share `tiles` tiles: each warp gets at least one (`warps` per run).
+GDN_DEV int runs(long long tiles, int warps, int most) {
+  return tiles < (long long)warps * most ? (int)(((int)tiles + warps - 1) / warps) : most;
 }
-// The sequence that holds unit u of all units (each sequence has HR times its
-// tiles of them), and the units before it.
+
+// A place in the sequence of all tiles: an item and a tile of it.
+struct Cursor {
+  int b, hr, tile, nt, len;
+};
 template <int TILE>
-GDN_DEV int find_seq(const Kv4Args &c, long long u, int HR, int lane, long long &before) {
-  long long base = 0;
+GDN_DEV void seek(const Kv4Args &c, Cursor &k, int b) {
+  k.b = b;
+  k.len = seq_len(c, b);
+  k.nt = tiles_of<TILE>(k.len);
+}
+template <int TILE>
+GDN_DEV void next_item(const Kv4Args &c, Cursor &k, int HR) {
+  k.tile = 0;
+  if (++k.hr == HR) {
+    k.hr = 0;
+    seek<TILE>(c, k, k.b + 1);
+  }
+}
+// The tiles of sequences b0 + lane (0 past the end), for one KV head and row group.
+template <int TILE>
+GDN_DEV int lane_tiles(const Kv4Args &c, int b0, int lane) {
+  return b0 + lane < c.B ? tiles_of<TILE>(seq_len(c, b0 + lane)) : 0;
+}
+// The tile at cost u (each item costs its tiles and `extra`, which comes
+// first), and how many tiles lie before it. All lanes of a warp. n0:
+// lane_tiles of the first 32 sequences.
+template <int TILE>
+GDN_DEV long long find_tile(const Kv4Args &c, long long u, int HR, int extra, int lane, int n0, Cursor &k) {
+  long long cost = 0, tiles = 0;  // of the sequences before, per (KV head, row group)
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const int n = b0 + lane < c.B ? tiles_of<TILE>(seq_len(c, b0 + lane)) : 0;
+    const int n = b0 ? lane_tiles<TILE>(c, b0, lane) : n0;
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, (base + incl) * HR > u);
+    const int seqs = min(lane + 1, c.B - b0);
+    const unsigned past = __ballot_sync(0xffffffffu, b0 + lane < c.B && (cost + incl + (long long)seqs * extra) * HR > u);
     if (past) {
       const int l = __ffs(past) - 1;
-      before = (base + __shfl_sync(0xffffffffu, incl - n, l)) * HR;
-      return b0 + l;
+      const int before = __shfl_sync(0xffffffffu, incl - n, l);
+      seek<TILE>(c, k, b0 + l);
+      const long long off = u - (cost + before + (long long)l * extra) * HR;
+      k.hr = (int)quot(off, k.nt + extra);
+      k.tile = max((int)(off - (long long)k.hr * (k.nt + extra)) - extra, 0);
+      return (tiles + before) * HR + (long long)k.hr * k.nt + k.tile;
     }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    const int all = __shfl_sync(0xffffffffu, incl, 31);
+    cost += all + (long long)min(32, c.B - b0) * extra;
+    tiles += all;
   }
-  before = 0;
-  return -1;
+  return tiles * HR;  // past the end
 }
-// CTAs that share the tiles: each gets at least one per warp.
-GDN_DEV int runs(long long units, int ctas) {
-  const long long most = (units + kWarps - 1) / kWarps;
-  return (int)(most < ctas ? most : ctas);
+// Run `run` of at most `most`: its first tile and how many tiles it has.
+template <int TILE>
+GDN_DEV int find_run(const DecodeArgs &p, int warps, int HR, int lane, int run, int most, Cursor &k) {
+  const Kv4Args &c = p.a.c;
+  k = Cursor{0, 0, 0, 0, 0};
+  if (p.extra == kWhole) {  // runs of whole items, as many in each
+    const int items = c.B * HR;
+    const int i0 = (int)quot((long long)items * run, most), i1 = (int)quot((long long)items * (run + 1), most);
+    int n = 0;
+    for (int i = i0; i < i1; ++i) n += tiles_of<TILE>(seq_len(c, i / HR));
+    if (n) {
+      seek<TILE>(c, k, i0 / HR);
+      k.hr = i0 % HR;
+    }
+    return n;
+  }
+  const int n0 = lane_tiles<TILE>(c, 0, lane);
+  long long tiles = warp_isum(n0);
+  for (int b0 = 32; b0 < c.B; b0 += 32) tiles += warp_isum(lane_tiles<TILE>(c, b0, lane));
+  const long long units = (tiles + (long long)c.B * p.extra) * HR;
+  const int N = runs(tiles * HR, warps, most);
+  if (run >= N) return 0;
+  // cut k lies at floor(units k / N)
+  const long long q = quot(units, N);
+  const int rest = (int)(units - q * N);
+  Cursor end;
+  const long long t1 = run + 1 == N ? tiles * HR
+                                    : find_tile<TILE>(c, q * (run + 1) + rest * (run + 1) / N, HR, p.extra, lane, n0, end);
+  return (int)(t1 - find_tile<TILE>(c, q * run + rest * run / N, HR, p.extra, lane, n0, k));
 }
 
-GDN_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 GDN_DEV uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -135,7 +210,6 @@ GDN_DEV void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-GDN_DEV uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 GDN_DEV __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 // Two E4M3 bytes -> two FP16 (exact)
 GDN_DEV uint32_t e4m3x2_to_h2(uint32_t two) {
@@ -143,139 +217,115 @@ GDN_DEV uint32_t e4m3x2_to_h2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
   return h;
 }
-// Eight E2M1 codes times a pair of scales
-GDN_DEV void decode8(uint32_t w, __half2 s, uint32_t (&o)[4]) {
-  __half2 h[4];
-  e2m1x8_to_h2x4(w, h);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = h2u(__hmul2(h[i], s));
-}
 
-// Where a warp stands in the run: an item and a tile of it.
-struct Cursor {
-  int b, hr, tile, nt, len;
-};
-template <int TILE>
-GDN_DEV void seek(const Kv4Args &c, Cursor &k, int b) {
-  k.b = b;
-  k.len = seq_len(c, b);
-  k.nt = tiles_of<TILE>(k.len);
-}
-template <int TILE>
-GDN_DEV void advance(const Kv4Args &c, Cursor &k, int step, int HR) {
-  while (step >= k.nt - k.tile) {
-    step -= k.nt - k.tile;
-    k.tile = 0;
-    if (++k.hr == HR) {
-      k.hr = 0;
-      seek<TILE>(c, k, k.b + 1);
-    }
-  }
-  k.tile += step;
-}
-
-// This CTA's run: its first tile and how many tiles it has.
-template <int TILE>
-GDN_DEV long long find_run(const DecodeArgs &p, int HR, int lane, Cursor &k) {
-  const Kv4Args &c = p.a.c;
-  k.tile = k.hr = k.b = k.nt = k.len = 0;
-  if (p.whole) {
-    const long long items = (long long)c.B * HR;
-    const long long i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
-    long long n = 0;
-    for (long long i = i0; i < i1; ++i) n += tiles_of<TILE>(seq_len(c, (int)(i / HR)));
-    seek<TILE>(c, k, (int)(i0 / HR));
-    k.hr = (int)(i0 % HR);
-    return n;
-  }
-  const long long units = total_tiles<TILE>(c, lane) * HR;
-  const int N = runs(units, gridDim.x);
-  if ((int)blockIdx.x >= N) return 0;
-  const long long u0 = units * blockIdx.x / N, u1 = units * (blockIdx.x + 1) / N;
-  long long before;
-  const int b = find_seq<TILE>(c, u0, HR, lane, before);
-  seek<TILE>(c, k, b);
-  k.hr = (int)((u0 - before) / k.nt);
-  k.tile = (int)((u0 - before) % k.nt);
-  return u1 - u0;
-}
-
-template <int D, int NQ>
-__global__ void __launch_bounds__(kWarps * 32, 1) kv4_decode_kernel(DecodeArgs p) {
-  using S = DecodeShape<D, NQ>;
-  constexpr int TILE = S::kTile, GR = S::kGroups, KS = D / 16;  // KS: k steps of S, and MMAs of 16 channels of O
+template <int D, int NQ, int TEAM>
+__global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_decode_kernel(DecodeArgs p) {
+  using S = DecodeShape<D, NQ, TEAM>;
+  constexpr int TILE = S::kTile, GR = S::kGroups, W = S::kTeam;
+  constexpr int KS = D / 16;  // k steps of S, and MMAs of 16 channels of O
   extern __shared__ __align__(128) unsigned char sm[];
-  float *meet = reinterpret_cast<float *>(sm + S::kRing);
-  float *stats = reinterpret_cast<float *>(sm + S::kRing + S::kMeet);
-  uint2 *qsm = reinterpret_cast<uint2 *>(sm + S::kRing + S::kMeet + S::kStats);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::kRing + S::kMeet + S::kStats + S::kQ);
   const Kv4Args &c = p.a.c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  unsigned char *ring = sm + warp * S::kStages * S::kStage;
-  uint64_t *full = bars + warp * S::kStages;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int team = threadIdx.x / (32 * W), tid = threadIdx.x - team * (32 * W), warp = tid >> 5;  // within the team
+  const int run = blockIdx.x * S::kTeams + team;
+  float *meet = reinterpret_cast<float *>(sm + S::kRing) + team * (W * S::kRows * S::kLd);
+  float *stats = reinterpret_cast<float *>(sm + S::kRing + S::kMeet) + team * (4 * W * S::kRows);
+  unsigned char *qraw = sm + S::kRing + S::kMeet + S::kStats + team * (S::kRows * D * 2);
+  unsigned char *tail_sm = sm + S::kRing + S::kMeet + S::kStats + S::kQRaw;
+  uint2 *qsm = reinterpret_cast<uint2 *>(tail_sm);
+  uint64_t *full = reinterpret_cast<uint64_t *>(tail_sm + S::kQ), *q_full = full + S::kSlots + team;
+  volatile uint32_t *abort_flag = reinterpret_cast<uint32_t *>(full + S::kSlots + S::kTeams);
   const int HR = c.Hkv * p.RG, R = p.r * p.G;
+  auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * W) : "memory"); };
   pdl_launch_dependents();  // kv4_join_kernel finds its places meanwhile
-  if (lane == 0) {
-    for (int s = 0; s < S::kStages; ++s) mbar_init(full + s, 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kSlots + S::kTeams; ++s) mbar_init(full + s, 1);
+    *abort_flag = 0u;
     fence_barrier_init();
   }
-  __syncwarp();
+  __syncthreads();
+  Cursor cur;
+  const int n_tiles = find_run<TILE>(p, W, HR, lane, run, gridDim.x * S::kTeams, cur);
   if (blockIdx.x == 0)
-    for (int b = tid; b < c.B; b += kWarps * 32)
+    for (int b = threadIdx.x; b < c.B; b += S::kThreads)
       if (c.kv_len[b] != seq_len(c, b)) flag_status(c.status, GDN_E_RANGE);
 
-  Cursor cur;
-  const long long n_units = find_run<TILE>(p, HR, lane, cur);
-
-  // ------------------------------------------------ this warp's loads: tiles warp, warp + 8, ... of the run
-  Cursor load = cur;
-  long long load_at = warp;
-  if (load_at < n_units) advance<TILE>(c, load, warp, HR);
-  auto issue = [&](int s) {  // the warp's next tile into stage s
-    const int pos = load.tile * TILE + lane * 16;
-    const uint8_t *src = nullptr;
-    if (lane < GR && pos < load.len) {
-      const int page = c.table[(size_t)load.b * c.cols + pos / c.page_tokens];
-      if (page >= 0 && page < c.num_pages)
-        src = c.pages + (((size_t)page * c.Hkv + load.hr / p.RG) * (c.page_tokens / 16) + (pos % c.page_tokens) / 16) * (18 * D);
-      else
-        flag_status(c.status, GDN_E_RANGE);
+  int at = 0, next = warp;  // the segment's first tile (cur), and this warp's next one, within the run
+  // ------------------------------------------------ loads
+  // This warp's tiles warp, warp + W, ... go into its two slots in turn. Where
+  // the groups of the next TB of them lie is worked out at once, one group per
+  // lane (a tile at a time cost 100 instructions a tile, of 820).
+  constexpr int TB = 32 / GR;
+  uint64_t *my_full = full + 2 * (team * W + warp);
+  unsigned char *my_slots = sm + 2 * (team * W + warp) * S::kSlot;
+  int ld = warp, ld_i = TB;       // the next tile to load, and its place in the batch
+  const uint8_t *ld_src = nullptr;
+  auto load = [&](int s) {
+    if (ld_i == TB) {
+      ld_i = 0;
+      ld_src = nullptr;
+      const int off = ld + W * (lane / GR);
+      if (off < n_tiles) {
+        Cursor k = cur;
+        for (int step = off - at;;) {
+          if (step < k.nt - k.tile) {
+            k.tile += step;
+            break;
+          }
+          step -= k.nt - k.tile;
+          next_item<TILE>(c, k, HR);
+        }
+        const int pos = k.tile * TILE + (lane % GR) * 16;
+        if (pos < k.len) {
+          ld_src = kv4_group<D>(c, k.b, pos);
+          if (ld_src) ld_src += (k.hr / p.RG) * kv4_head_bytes<D>(c);
+        }
+      }
     }
-    const unsigned good = __ballot_sync(0xffffffffu, src != nullptr);
-    if (lane == 0) mbar_arrive_expect_tx(full + s, __popc(good) * 18 * D);
+    const uint8_t *src = reinterpret_cast<const uint8_t *>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(ld_src), ld_i * GR + lane % GR));
+    const unsigned goods = __ballot_sync(0xffffffffu, lane < GR && src != nullptr);
+    if (lane == 0) mbar_arrive_expect_tx(my_full + s, __popc(goods) * 18 * D);
     __syncwarp();
-    if (src) bulk_g2s(ring + s * S::kStage + lane * 18 * D, src, 18 * D, full + s);
-    load_at += kWarps;
-    if (load_at < n_units) advance<TILE>(c, load, kWarps, HR);
+    if (goods >> lane & 1) bulk_g2s(my_slots + s * S::kSlot + lane * 18 * D, src, 18 * D, my_full + s);
+    ++ld_i;
+    ld += W;
   };
-  for (int s = 0; s < S::kStages; ++s)
-    if (load_at < n_units) issue(s);
+  // The team's warp 0 loads the query rows of a segment, one per lane.
+  auto load_q = [&](const Cursor &k) {
+    const int row0 = (k.hr % p.RG) * S::kRows, rows = min(S::kRows, R - row0), ri = row0 + lane;
+    if (lane == 0) mbar_arrive_expect_tx(q_full, rows * D * 2);
+    __syncwarp();
+    if (lane < rows)
+      bulk_g2s(qraw + lane * (D * 2),
+               p.a.q + ((long long)k.b * p.r + ri / p.G) * p.a.q_stride + (long long)(k.hr / p.RG * p.G + ri % p.G) * D,
+               D * 2, q_full);
+  };
+  if (warp == 0 && n_tiles > 0) load_q(cur);
+  for (int i = 0; i < 2; ++i)
+    if (ld < n_tiles) load(i);
 
-  int stage = 0, flip = 0;
-  uint32_t parity = 0;
+  int slot = 0, flip = 0;
+  uint32_t turn = 0;  // parity of the slots' round
   bool alive = true;
-  long long at = 0;  // the segment's first tile within the run
-  bool first_segment = true;
-  while (at < n_units) {
-    const int seg = (int)min((long long)(cur.nt - cur.tile), n_units - at);
+  for (int sg = 0; at < n_tiles; ++sg) {
+    const int seg = min(cur.nt - cur.tile, n_tiles - at);
     const int h = cur.hr / p.RG, row0 = (cur.hr % p.RG) * S::kRows;
     const int rows = min(S::kRows, R - row0);
-    const int first = (int)((warp - at % kWarps + kWarps) % kWarps);  // this warp's first tile of the segment
+    const bool mine = next < at + seg;
     // ------------------------------------------------ q: B operand, lane (g, t) = row g, channels t D/4 ...
     uint2 qf[S::kQShared ? 1 : NQ][S::kQShared ? 1 : KS];
     float cs[NQ][2];   // sm k_scale log2 e / the row's scale, of columns 2t and 2t + 1
     int last[NQ][2];   // the last token that the row sees
     float O[KS][NQ][4], m[NQ][2], l[NQ][2];
+    if (alive && !__all_sync(0xffffffffu, wait_or_abort(q_full, (uint32_t)sg & 1u, abort_flag, c.status))) alive = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const int row = n * 8 + g;
       uint4 w[D / 32];
-      const int ri = row0 + row;
-      const bool in = row < rows;
-      const uint16_t *qp = p.a.q + ((long long)cur.b * p.r + ri / p.G) * p.a.q_stride +
-                           (long long)(h * p.G + ri % p.G) * D + t * (D / 4);
+      const uint4 *qp = reinterpret_cast<const uint4 *>(qraw + row * (D * 2) + t * (D / 2));
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) w[i] = in ? reinterpret_cast<const uint4 *>(qp)[i] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < D / 32; ++i) w[i] = row < rows ? qp[i] : make_uint4(0, 0, 0, 0);
       uint32_t mx = 0;  // the largest magnitude, as BF16 bits (a NaN counts as the largest: its row is NaN anyway)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -320,17 +370,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_decode_kernel(DecodeArgs p
 #pragma unroll
         for (int j = 0; j < 4; ++j) O[i][n][j] = 0.0f;
     }
-    if constexpr (S::kQShared) __syncthreads();
+    if constexpr (S::kQShared) team_sync();
 
     // ------------------------------------------------ the warp's tiles of this segment
-    for (int ti = first; ti < seg && alive; ti += kWarps) {
-      if (!__all_sync(0xffffffffu, mbar_wait(full + stage, parity))) {
-        flag_status(c.status, GDN_E_TIMEOUT);
-        alive = false;
-        break;
-      }
-      const unsigned char *buf = ring + stage * S::kStage;
-      const int pos0 = (cur.tile + ti) * TILE;
+    for (; next < at + seg; next += W) {
+      if (alive && !__all_sync(0xffffffffu, wait_or_abort(my_full + slot, turn, abort_flag, c.status))) alive = false;
+      if (!alive) continue;
+      const unsigned char *buf = my_slots + slot * S::kSlot;
+      const int pos0 = (cur.tile + next - at) * TILE;
       float s[GR][NQ][4];
 #pragma unroll
       for (int q = 0; q < GR; ++q) {
@@ -383,50 +430,60 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_decode_kernel(DecodeArgs p
             for (int j = 0; j < 4; ++j)
               if (pos0 + q * 16 + g + (j >> 1) * 8 > last[n][j & 1]) s[q][n][j] = -INFINITY;
       }
-      // ---- running maximum, weights, and P^T as the B operand
-      uint32_t pb[GR][NQ][2];
-      bool moved = false;
-      float f[NQ][2];
+      // ---- the maximum (moved only where a score passes it by kSlack)
+      float x[NQ][2];
+      bool up = false;
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
+      for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
-          float x = -INFINITY;
+          x[n][e2] = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < GR; ++q) x = fmaxf(x, fmaxf(s[q][n][e2], s[q][n][2 + e2]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float mn = fmaxf(m[n][e2], x * cs[n][e2]);
-          const float safe = mn == -INFINITY ? 0.0f : mn;
-          f[n][e2] = ex2(m[n][e2] - safe);
-          moved |= mn != m[n][e2];
-          m[n][e2] = mn;
-          const float off = kShift - safe;
-          float sum = 0.0f;
-#pragma unroll
-          for (int q = 0; q < GR; ++q)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float &v = s[q][n][2 * j + e2];
-              v = ex2(fmaf(v, cs[n][e2], off));
-              sum += v;
-            }
-          l[n][e2] = fmaf(l[n][e2], f[n][e2], sum);
+          for (int q = 0; q < GR; ++q) x[n][e2] = fmaxf(x[n][e2], fmaxf(s[q][n][e2], s[q][n][2 + e2]));
+          x[n][e2] *= cs[n][e2];
+          up |= x[n][e2] > m[n][e2] + kSlack;
         }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          float f[2];
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {
+            float top = x[n][e2];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const bool move = top > m[n][e2] + kSlack;  // decided column by column: no row's result depends on another's
+            f[e2] = move ? ex2(m[n][e2] - top) : 1.0f;
+            if (move) m[n][e2] = top;
+            l[n][e2] *= f[e2];
+          }
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O[i][n][j] *= f[j & 1];
+        }
+      }
+      // ---- weights, and P^T as the B operand
+      uint32_t pb[GR][NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const float2 c2 = make_float2(cs[n][0], cs[n][1]);
+        const float2 o2 = make_float2(kShift - (m[n][0] == -INFINITY ? 0.0f : m[n][0]),
+                                      kShift - (m[n][1] == -INFINITY ? 0.0f : m[n][1]));
+        float2 sum = make_float2(l[n][0], l[n][1]);
 #pragma unroll
         for (int q = 0; q < GR; ++q)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            pb[q][n][j] = transpose8x8(h2u(__floats2half2_rn(s[q][n][2 * j], s[q][n][2 * j + 1])));
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) O[i][n][j] *= f[n][j & 1];
+          for (int j = 0; j < 2; ++j) {
+            float2 z = fma2(make_float2(s[q][n][2 * j], s[q][n][2 * j + 1]), c2, o2);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            sum = add2(sum, z);
+            pb[q][n][j] = transpose8x8(h2u(__floats2half2_rn(z.x, z.y)));
+          }
+        l[n][0] = sum.x;
+        l[n][1] = sum.y;
       }
       // ---- O^T += V^T P^T
       const bool tail = pos0 + TILE > cur.len;  // places past the end hold anything: their scales count as 0
@@ -468,17 +525,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_decode_kernel(DecodeArgs p
               mma_acc(O[w * 4 + i][n], lo0[i], hi0[i], lo1[i], hi1[i], pb[q][n][0], pb[q][n][1]);
         }
       }
-      __syncwarp();  // every lane has read the stage
-      if (load_at < n_units) issue(stage);
-      if (++stage == S::kStages) {
-        stage = 0;
-        parity ^= 1u;
-      }
+      __syncwarp();  // every lane has read the slot
+      if (ld < n_tiles) load(slot);
+      slot ^= 1;
+      turn ^= slot == 0;
     }
     // ------------------------------------------------ the segment's end: the warps' parts meet
     const bool done = seg == cur.nt;  // the item lies in this run
-    const size_t slot = 2 * (size_t)blockIdx.x + (first_segment ? 0 : 1);
-    float *mw = stats + flip * 2 * kWarps * S::kRows, *lw = mw + kWarps * S::kRows;
+    const size_t piece = 2 * (size_t)run + (sg == 0 ? 0 : 1);
+    float *mw = stats + flip * 2 * W * S::kRows, *lw = mw + W * S::kRows;
     flip ^= 1;
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -490,12 +545,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_decode_kernel(DecodeArgs p
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         if (g == 0) {
           mw[warp * S::kRows + n * 8 + 2 * t + e2] = m[n][e2];
-          lw[warp * S::kRows + n * 8 + 2 * t + e2] = x;
+          lw[warp * S::kRows + n * 8 + 2 * t + e2] = mine ? x : -1.0f;  // -1: a warp that had no tile
         }
       }
-    __syncthreads();
-    const int live = min(seg, kWarps);  // warps that had a tile: (at + i) % 8, i < live
-    const bool mine = first < seg;
+    team_sync();
+    if (warp == 0 && at + seg < n_tiles) {  // every warp has read this segment's query rows: the next one's
+      Cursor k = cur;
+      next_item<TILE>(c, k, HR);
+      load_q(k);
+    }
     if (mine) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -504,7 +562,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_decode_kernel(DecodeArgs p
         for (int e2 = 0; e2 < 2; ++e2) {
           float top = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mw[w * S::kRows + n * 8 + 2 * t + e2]);
+          for (int w = 0; w < W; ++w) top = fmaxf(top, mw[w * S::kRows + n * 8 + 2 * t + e2]);
           fw[e2] = ex2(m[n][e2] - (top == -INFINITY ? 0.0f : top));
         }
 #pragma unroll
@@ -518,21 +576,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_decode_kernel(DecodeArgs p
         }
       }
     }
-    __syncthreads();
-    const int w0 = (int)(at % kWarps);
-    for (int i = tid; i < S::kRows * (D / 4); i += kWarps * 32) {
+    team_sync();
+    for (int i = tid; i < rows * (D / 4); i += 32 * W) {
       const int row = i / (D / 4), d4 = i % (D / 4) * 4;
-      if (row >= rows) break;
       float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mw[w * S::kRows + row]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, mw[w * S::kRows + row]);
       const float safe = top == -INFINITY ? 0.0f : top;
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int j = 0; j < live; ++j) {
-        const int w = (w0 + j) & (kWarps - 1);
-        sum += lw[w * S::kRows + row] * ex2(mw[w * S::kRows + row] - safe);
-        const float4 x = *reinterpret_cast<const float4 *>(meet + (size_t)(w * S::kRows + row) * S::kLd + d4);
-        o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float lx = lw[w * S::kRows + row];
+        if (lx == -1.0f) continue;
+        sum += lx * ex2(mw[w * S::kRows + row] - safe);
+        const float4 y = *reinterpret_cast<const float4 *>(meet + (size_t)(w * S::kRows + row) * S::kLd + d4);
+        o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
       }
       if (done) {
         const int ri = row0 + row;
@@ -543,59 +601,78 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv4_decode_kernel(DecodeArgs p
                        f32_to_bf16_bits(o.z * inv) | (uint32_t)f32_to_bf16_bits(o.w * inv) << 16);
         if (p.a.lse && d4 == 0) p.a.lse[out] = (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
       } else {
-        *reinterpret_cast<float4 *>(p.part + (slot * S::kRows + row) * D + d4) = o;
+        *reinterpret_cast<float4 *>(p.part + (piece * S::kRows + row) * D + d4) = o;
         if (d4 == 0)
-          *reinterpret_cast<float2 *>(p.part + 2 * (size_t)gridDim.x * S::kRows * D + (slot * S::kRows + row) * 2) =
+          *reinterpret_cast<float2 *>(p.part + 2 * (size_t)gridDim.x * S::kTeams * S::kRows * D + (piece * S::kRows + row) * 2) =
               make_float2(top, sum);
       }
     }
     at += seg;
-    first_segment = false;
-    if (at < n_units) advance<TILE>(c, cur, seg, HR);
+    if (at < n_tiles) next_item<TILE>(c, cur, HR);
   }
-  if (!alive)  // a wait ran out: give the copies still in flight one more bounded wait each
-    for (int s = 0; s < S::kStages; ++s) mbar_wait(full + s, s >= stage ? parity : parity ^ 1u);
+  if (!alive) {  // a wait gave up: the copies in flight land (or a bounded wait for each ends) first
+    mbar_wait(my_full + slot, turn);
+    mbar_wait(my_full + (slot ^ 1), slot == 0 ? turn : turn ^ 1u);
+  }
 }
 
 // The items that lie in several runs: one CTA per query row, its warps taking
-// every fourth piece.
-template <int D, int NQ>
-__global__ void __launch_bounds__(128) kv4_join_kernel(DecodeArgs p, int ctas) {
-  using S = DecodeShape<D, NQ>;
+// every eighth piece. most: runs at most, as in the decode kernel.
+template <int D, int NQ, int TEAM>
+__global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
+  using S = DecodeShape<D, NQ, TEAM>;
   constexpr int E = D / 32;
-  __shared__ float sh[4][D + 2];
+  __shared__ float sh[8][D + 2];
   const Kv4Args &c = p.a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HR = c.Hkv * p.RG, R = p.r * p.G;
   const int row_id = blockIdx.x % R, bh = blockIdx.x / R, b = bh / c.Hkv, h = bh % c.Hkv;
   const int hr = h * p.RG + row_id / S::kRows, row = row_id % S::kRows;
-  long long units = 0, before = 0;
+  long long tiles = 0, before = 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const int n = b0 + lane < c.B ? tiles_of<S::kTile>(seq_len(c, b0 + lane)) : 0;
-    units += warp_isum(n);
+    const int n = lane_tiles<S::kTile>(c, b0, lane);
+    tiles += warp_isum(n);
     before += warp_isum(b0 + lane < b ? n : 0);
   }
-  units *= HR;
-  const int nt = tiles_of<S::kTile>(seq_len(c, b));
-  const long long a0 = before * HR + (long long)hr * nt;  // the item's tiles are [a0, a0 + nt)
-  const int N = runs(units, ctas);
-  const int c0 = (int)(((a0 + 1) * N - 1) / units), c1 = (int)(((a0 + nt) * N - 1) / units);
+  const int nt = tiles_of<S::kTile>(seq_len(c, b)), N = runs(tiles * HR, S::kTeam, most);
+  const long long units = (tiles + (long long)c.B * p.extra) * HR;
+  const long long a0 = (before + (long long)b * p.extra) * HR + (long long)hr * (nt + p.extra);
+  // the runs that hold the item's first and last tile (its tile t lies at cost a0 + extra + t)
+  const int c0 = (int)quot((a0 + p.extra + 1) * N - 1, units), c1 = (int)quot((a0 + p.extra + nt) * N - 1, units);
   pdl_wait();  // on every path: this grid must not end before the one it follows
   if (c0 == c1) return;
   float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  const float *ml = p.part + 2 * (size_t)ctas * S::kRows * D;
-  for (int k = c0 + warp; k <= c1; k += 4) {
-    const size_t slot = 2 * (size_t)k + (units * k / N >= a0 ? 0 : 1);  // the run's first segment, or its last
-    const float2 x = *reinterpret_cast<const float2 *>(ml + (slot * S::kRows + row) * 2);
-    const float *op = p.part + (slot * S::kRows + row) * D + lane * E;
-    const float mn = fmaxf(m, x.x), safe = mn == -INFINITY ? 0.0f : mn;
-    const float f = ex2(m - safe), fx = ex2(x.x - safe);
-    l = l * f + x.y * fx;
+  const float *ml = p.part + 2 * (size_t)most * S::kRows * D;
+  // run c0 may hold earlier items before this one: then it is not its first segment; the others start inside it
+  const bool c0_first = quot(units * c0, N) >= a0;
+  for (int k0 = c0 + warp; k0 <= c1; k0 += 8 * 4) {
+    float2 x[4];
+    float y[4][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + op[e] * fx;
-    m = mn;
+    for (int j = 0; j < 4; ++j) {  // four pieces in flight
+      const int k = k0 + 8 * j;
+      const size_t piece = 2 * (size_t)k + (k > c0 || c0_first ? 0 : 1);
+      x[j] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[j][e] = 0.0f;
+      if (k <= c1) {
+        x[j] = *reinterpret_cast<const float2 *>(ml + (piece * S::kRows + row) * 2);
+        const float *op = p.part + (piece * S::kRows + row) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[j][e] = op[e];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float mn = fmaxf(m, x[j].x), safe = mn == -INFINITY ? 0.0f : mn;
+      const float f = ex2(m - safe), fx = ex2(x[j].x - safe);
+      l = l * f + x[j].y * fx;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * f + y[j][e] * fx;
+      m = mn;
+    }
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = o[e];
@@ -605,11 +682,13 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(DecodeArgs p, int ctas) {
   }
   __syncthreads();
   if (threadIdx.x < D) {
-    float top = fmaxf(fmaxf(sh[0][D], sh[1][D]), fmaxf(sh[2][D], sh[3][D]));
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, sh[w][D]);
     const float safe = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 8; ++w) {
       const float f = ex2(sh[w][D] - safe);
       sum += sh[w][D + 1] * f;
       v += sh[w][threadIdx.x] * f;
@@ -620,46 +699,70 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(DecodeArgs p, int ctas) {
   }
 }
 
-template <int D, int NQ>
-cudaError_t launch_decode_t(DecodeArgs p, int ctas, int num_sms, cudaStream_t stream) {
-  using S = DecodeShape<D, NQ>;
-  cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+template <int D, int NQ, int TEAM>
+cudaError_t launch_decode_t(const DecodeArgs &p, int ctas, cudaStream_t stream) {
+  using S = DecodeShape<D, NQ, TEAM>;
+  cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, NQ, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
-  kv4_decode_kernel<D, NQ><<<ctas, kWarps * 32, S::kBytes, stream>>>(p);
-  if (p.whole) return cudaGetLastError();
+  kv4_decode_kernel<D, NQ, TEAM><<<ctas, S::kThreads, S::kBytes, stream>>>(p);
+  if (p.extra == kWhole) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.a.c.B * p.a.Hq * p.r), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NQ>, p, ctas);
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NQ, TEAM>, p, ctas * S::kTeams);
 }
 
 // Query rows per (sequence, KV head) -> 8-row column blocks of one item.
 int blocks_of(int R) { return R <= 8 ? 1 : R <= 16 ? 2 : 4; }
 
+// What a kernel's shape says to the host.
+struct ShapeInfo {
+  int team, teams, tile;
+};
+template <int D, int NQ>
+ShapeInfo shape_info(bool small) {
+  if constexpr (!DecodeShape<D, NQ, 0>::kQShared)
+    if (small) return {DecodeShape<D, NQ, 4>::kTeam, DecodeShape<D, NQ, 4>::kTeams, DecodeShape<D, NQ, 4>::kTile};
+  return {DecodeShape<D, NQ, 0>::kTeam, DecodeShape<D, NQ, 0>::kTeams, DecodeShape<D, NQ, 0>::kTile};
+}
+
 struct DecodePlan {
-  int NQ, RG, ctas, whole;
+  int NQ, RG, ctas, extra;
+  bool small;    // teams of four warps
   size_t bytes;
 };
-// Everything the host knows: an upper bound of the lengths.
+// Everything the host knows: an upper bound of the lengths. Where it says that
+// no item has more tiles than a team has warps, items stay whole.
 DecodePlan decode_plan(const Kv4AttnArgs &a, int num_sms) {
   DecodePlan d{};
   const int R = a.c.T / a.c.B * (a.Hq / a.c.Hkv);
   d.NQ = blocks_of(R);
   d.RG = (R + 8 * d.NQ - 1) / (8 * d.NQ);
-  const int tile = d.NQ == 4 ? 32 : 64;
   const long long items = (long long)a.c.B * a.c.Hkv * d.RG;
-  const long long most = ((long long)a.c.cols * a.c.page_tokens + tile - 1) / tile;  // tiles of an item
-  d.whole = most <= kWarps;
-  const long long units = d.whole ? items : (items * most + kWarps - 1) / kWarps;
-  d.ctas = (int)(units < num_sms ? units : num_sms);
-  d.bytes = d.whole ? 0 : 2 * (size_t)d.ctas * 8 * d.NQ * (a.c.D + 2) * sizeof(float);
+  d.small = items >= kManyItems && !(a.c.D == 128 && d.NQ == 4);
+  const ShapeInfo s = a.c.D == 128 ? (d.NQ == 1 ? shape_info<128, 1>(d.small) : d.NQ == 2 ? shape_info<128, 2>(d.small)
+                                                                                          : shape_info<128, 4>(d.small))
+                                   : (d.NQ == 1 ? shape_info<64, 1>(d.small) : d.NQ == 2 ? shape_info<64, 2>(d.small)
+                                                                                         : shape_info<64, 4>(d.small));
+  const long long most = ((long long)a.c.cols * a.c.page_tokens + s.tile - 1) / s.tile;  // tiles of an item
+  d.extra = most <= s.team ? kWhole : d.small ? kExtraTeam : kExtraCta;
+  const long long n = d.extra == kWhole ? items : (items * most + s.team - 1) / s.team;  // runs that could have work
+  d.ctas = (int)(n < (long long)num_sms * s.teams ? (n + s.teams - 1) / s.teams : num_sms);
+  d.bytes = d.extra == kWhole ? 0 : 2 * (size_t)d.ctas * s.teams * 8 * d.NQ * (a.c.D + 2) * sizeof(float);
   return d;
+}
+
+template <int D, int NQ>
+cudaError_t launch_decode(const DecodeArgs &p, const DecodePlan &d, cudaStream_t stream) {
+  if constexpr (!DecodeShape<D, NQ, 0>::kQShared)
+    if (d.small) return launch_decode_t<D, NQ, 4>(p, d.ctas, stream);
+  return launch_decode_t<D, NQ, 0>(p, d.ctas, stream);
 }
 
 }  // namespace
@@ -668,14 +771,12 @@ size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms) { return a.c.T ? deco
 
 cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
   const DecodePlan d = decode_plan(a, num_sms);
-  DecodeArgs p{a, a.c.T / a.c.B, a.Hq / a.c.Hkv, d.RG, d.whole, static_cast<float *>(workspace)};
+  const DecodeArgs p{a, a.c.T / a.c.B, a.Hq / a.c.Hkv, d.RG, d.extra, static_cast<float *>(workspace)};
   if (a.c.D == 128)
-    return d.NQ == 1 ? launch_decode_t<128, 1>(p, d.ctas, num_sms, stream)
-         : d.NQ == 2 ? launch_decode_t<128, 2>(p, d.ctas, num_sms, stream)
-                     : launch_decode_t<128, 4>(p, d.ctas, num_sms, stream);
-  return d.NQ == 1 ? launch_decode_t<64, 1>(p, d.ctas, num_sms, stream)
-       : d.NQ == 2 ? launch_decode_t<64, 2>(p, d.ctas, num_sms, stream)
-                   : launch_decode_t<64, 4>(p, d.ctas, num_sms, stream);
+    return d.NQ == 1 ? launch_decode<128, 1>(p, d, stream) : d.NQ == 2 ? launch_decode<128, 2>(p, d, stream)
+                                                                       : launch_decode<128, 4>(p, d, stream);
+  return d.NQ == 1 ? launch_decode<64, 1>(p, d, stream) : d.NQ == 2 ? launch_decode<64, 2>(p, d, stream)
+                                                                    : launch_decode<64, 4>(p, d, stream);
 }
 
 }  // namespace gdn

@@ -79,15 +79,6 @@ GDN_DEV int find_item(int B, int x, int lane, F count, int &before, int &total) 
   return b;
 }
 
-GDN_DEV uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-// Eight E2M1 codes times a pair of scales
-GDN_DEV void decode8(uint32_t w, __half2 s, uint32_t (&o)[4]) {
-  __half2 h[4];
-  e2m1x8_to_h2x4(w, h);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = h2u(__hmul2(h[i], s));
-}
-
 // One CTA per tile of 128 tokens and KV head. Tokens past the end become 0.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_expand_kernel(PrefillKv4 p) {
@@ -161,28 +152,6 @@ struct PrefillShape {
   static_assert(kO + 2 * D <= 512, "tensor memory");
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
-
-GDN_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// (x.lo, x.hi) * s + o
-GDN_DEV float2 fma2(float2 x, float2 s, float2 o) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(*reinterpret_cast<unsigned long long *>(&r))
-      : "l"(*reinterpret_cast<unsigned long long *>(&x)), "l"(*reinterpret_cast<unsigned long long *>(&s)),
-        "l"(*reinterpret_cast<unsigned long long *>(&o)));
-  return r;
-}
-GDN_DEV float2 add2(float2 x, float2 y) {
-  float2 r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(*reinterpret_cast<unsigned long long *>(&r))
-      : "l"(*reinterpret_cast<unsigned long long *>(&x)), "l"(*reinterpret_cast<unsigned long long *>(&y)));
-  return r;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) {
