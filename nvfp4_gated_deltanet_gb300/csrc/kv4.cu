@@ -229,7 +229,8 @@ size_t kv4_compact_bytes(int num_pages) { return sizeof(int32_t) * (4 + 2 * (siz
 cudaError_t launch_kv4_compact(const Kv4PageArgs &a, cudaStream_t stream) {
   const CompactWs w = compact_ws(a.workspace, a.num_pages);
   const size_t smem = (size_t)(a.num_pages + 31) / 32 * 4;
-  cudaError_t e = cudaFuncSetAttribute(compact_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+  static bool allowed[64];
+  cudaError_t e = kv4_allow_smem(compact_plan_kernel, 128 * 1024, allowed);
   if (e != cudaSuccess) return e;
   compact_plan_kernel<<<1, 1024, smem, stream>>>(a, w);
   Kv4PageArgs c = a;

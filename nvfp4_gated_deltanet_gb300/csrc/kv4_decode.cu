@@ -702,7 +702,8 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
 template <int D, int NQ, int TEAM>
 cudaError_t launch_decode_t(const DecodeArgs &p, int ctas, cudaStream_t stream) {
   using S = DecodeShape<D, NQ, TEAM>;
-  cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, NQ, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  static bool allowed[64];
+  cudaError_t e = kv4_allow_smem(kv4_decode_kernel<D, NQ, TEAM>, S::kBytes, allowed);
   if (e != cudaSuccess) return e;
   kv4_decode_kernel<D, NQ, TEAM><<<ctas, S::kThreads, S::kBytes, stream>>>(p);
   if (p.extra == kWhole) return cudaGetLastError();

@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
 template <int D>
 cudaError_t launch_prefill_t(const PrefillKv4 &p, cudaStream_t stream) {
   using S = PrefillShape<D>;
-  cudaError_t e = cudaFuncSetAttribute(kv4_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  static bool allowed[64];
+  cudaError_t e = kv4_allow_smem(kv4_prefill_kernel<D>, S::kBytes, allowed);
   if (e != cudaSuccess) return e;
   const Kv4Args &c = p.a.c;
   kv4_expand_kernel<D><<<(unsigned)p.cap * c.Hkv, 256, 0, stream>>>(p);

@@ -15,17 +15,28 @@ pages of all layers.
 """
 from __future__ import annotations
 
-import ctypes
-import math
+import importlib
 
 import torch
 
-from . import Kv4BatchStruct, Kv4CacheStruct, _check, _ptr, _stream, lib
+from . import lib
 
 __all__ = ["kv4_new_pages", "kv4_append", "kv4_read", "kv4_decode", "kv4_prefill", "kv4_copy_pages", "kv4_compact",
            "KV4Book", "KV4Batch", "KV4Cache"]
 
-_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_module = None
+
+
+def _native():
+    """The native binding; raises if it or the library was not built."""
+    global _module
+    if _module is None:
+        lib()
+        try:
+            _module = importlib.import_module("._kv4", __package__)
+        except ImportError as e:
+            raise RuntimeError(f"the _kv4 binding is missing ({e}): build it with {__package__}.build.build()") from e
+    return _module
 
 
 def kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim, n_layers=None, device="cuda"):
@@ -34,82 +45,16 @@ def kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim, n_layers=None, d
     return torch.zeros(shape if n_layers is None else (n_layers, *shape), dtype=torch.uint8, device=device)
 
 
-def _i32(t, name, dims):
-    if t.dtype != torch.int32 or t.dim() != dims or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of {dims} dimension(s)")
-    return t
-
-
-def _cache(pages, k_scale, v_scale):
-    if pages.dtype != torch.uint8 or pages.dim() != 4 or not pages.is_cuda or not pages.is_contiguous():
-        raise ValueError("pages: expected a contiguous uint8 CUDA tensor [num_pages][Hkv][page_tokens / 16][18 d]")
-    n, h, g, cell = pages.shape
-    if cell % 18:
-        raise ValueError("pages: the last dimension is 18 * head_dim bytes")
-    return Kv4CacheStruct(pages.data_ptr(), n, 16 * g, h, cell // 18, k_scale, v_scale)
-
-
-def _batch(table, kv_len, q_start, rows):
-    _i32(table, "block_table", 2)
-    _i32(kv_len, "kv_len", 1)
-    B = table.shape[0]
-    if kv_len.shape[0] != B or (q_start is not None and _i32(q_start, "q_start", 1).shape[0] != B + 1):
-        raise ValueError("block_table, kv_len and q_start disagree on the number of sequences")
-    return Kv4BatchStruct(kv_len.data_ptr(), table.data_ptr(), _ptr(q_start), B, table.shape[1], rows)
-
-
-def _rows(t, name, heads, d):
-    """BF16 rows [T][heads][d] whose heads lie together; returns the row stride in elements."""
-    if t.dtype not in _BF16 or not t.is_cuda or t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
-        raise ValueError(f"{name}: expected BF16 CUDA rows [T][{heads or 'heads'}][{d}]")
-    if t.shape[0] == 0:
-        return t.shape[1] * d
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: a row's heads must lie together in memory")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
-
-
-def _out(t, name, shape, dtypes, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtypes[0], device=device)
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtypes[0]} CUDA tensor of shape {tuple(shape)}")
-    return t
-
-
-def _workspace(n, given, device, stream):
-    """Device scratch of n bytes for work on `stream`."""
-    if given is not None:
-        if not given.is_cuda or not given.is_contiguous():
-            raise ValueError("workspace: expected a contiguous CUDA tensor")
-        return given, given.numel() * given.element_size()
-    w = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
-    if stream is not None:
-        w.record_stream(stream)  # freed here, used there
-    return w, n
-
-
 def kv4_append(k, v, pages, block_table, kv_len, k_scale, v_scale, q_start=None, dev_status=None, stream=None):
-    """Quantise the new rows k and v [T][Hkv][d] (BF16) into their sequences' pages (kv_len counts them already)."""
-    c = _cache(pages, k_scale, v_scale)
-    if k.shape[0] != v.shape[0]:
-        raise ValueError("k and v have different numbers of rows")
-    ks, vs = _rows(k, "k", c.n_kv_heads, c.head_dim), _rows(v, "v", c.n_kv_heads, c.head_dim)
-    b = _batch(block_table, kv_len, q_start, k.shape[0])
-    _check(lib().kv4_append(ctypes.byref(c), ctypes.byref(b), _ptr(k), ks, _ptr(v), vs, _ptr(dev_status),
-                            _stream(stream)), "kv4_append")
+    """Quantise the new rows k and v [T][Hkv][d] (BF16, a row's heads together,
+    rows evenly spaced) into their sequences' pages; kv_len counts them already."""
+    _native().append(k, v, pages, block_table, kv_len, k_scale, v_scale, q_start, dev_status, stream)
 
 
 def kv4_read(pages, block_table, kv_len, k_scale, v_scale, rows, q_start=None, k=None, v=None, dev_status=None,
              stream=None):
     """(k, v) [rows][Hkv][d] BF16: the values that the pages hold for the batch's new rows."""
-    c = _cache(pages, k_scale, v_scale)
-    b = _batch(block_table, kv_len, q_start, rows)
-    shape = (rows, c.n_kv_heads, c.head_dim)
-    k, v = _out(k, "k", shape, _BF16, pages.device), _out(v, "v", shape, _BF16, pages.device)
-    _check(lib().kv4_read(ctypes.byref(c), ctypes.byref(b), _ptr(k), _ptr(v), _ptr(dev_status), _stream(stream)),
-           "kv4_read")
-    return k, v
+    return _native().read(pages, block_table, kv_len, k_scale, v_scale, rows, q_start, k, v, dev_status, stream)
 
 
 def kv4_decode(q, pages, block_table, kv_len, k_scale, v_scale, sm_scale=None, out=None, lse=None, return_lse=False,
@@ -117,28 +62,9 @@ def kv4_decode(q, pages, block_table, kv_len, k_scale, v_scale, sm_scale=None, o
     """Attention of the batch's newest tokens: q [B][Hq][d] (one token per
     sequence) or [B][r][Hq][d] (r candidates) -> out of q's shape, BF16; with
     return_lse also the rows' log-sum-exp, FP32. sm_scale: d^-1/2 by default."""
-    c = _cache(pages, k_scale, v_scale)
-    if q.dim() not in (3, 4):
-        raise ValueError("q: expected [B][Hq][d] or [B][r][Hq][d]")
-    rows = q
-    if q.dim() == 4:
-        if q.shape[1] != 1 and q.shape[0] > 1 and q.stride(0) != q.shape[1] * q.stride(1):
-            raise ValueError("q: the rows of all sequences must be evenly spaced")
-        rows = q.flatten(0, 1) if q.shape[1] != 1 else q[:, 0]
-    qs = _rows(rows, "q", None, c.head_dim)
-    T, Hq = rows.shape[0], rows.shape[1]
-    b = _batch(block_table, kv_len, None, T)
-    if q.shape[0] != b.B:
-        raise ValueError("q and block_table disagree on the number of sequences")
-    out = _out(out, "out", q.shape, (torch.bfloat16, *_BF16[1:]), q.device)
-    if return_lse or lse is not None:
-        lse = _out(lse, "lse", q.shape[:-1], (torch.float32,), q.device)
-    L = lib()
-    ws, n = _workspace(L.kv4_decode_workspace(ctypes.byref(c), ctypes.byref(b), Hq), workspace, q.device, stream)
-    _check(L.kv4_decode(ctypes.byref(c), ctypes.byref(b), _ptr(rows), qs, Hq,
-                        c.head_dim ** -0.5 if sm_scale is None else sm_scale, _ptr(out), _ptr(lse), _ptr(ws), n,
-                        _ptr(dev_status), _stream(stream)), "kv4_decode")
-    return (out, lse) if return_lse else out
+    return _native().decode(q, pages, block_table, kv_len, k_scale, v_scale,
+                            q.shape[-1] ** -0.5 if sm_scale is None else sm_scale, out, lse, return_lse, workspace,
+                            dev_status, stream)
 
 
 def kv4_prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_kv=None, sm_scale=None, out=None,
@@ -146,44 +72,14 @@ def kv4_prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_
     """Causal attention of ragged prompt chunks: q [T][Hq][d], sequence b's rows
     [q_start[b], q_start[b + 1]) being its newest tokens. total_kv: an upper
     bound of kv_len's sum (default: what the tables can hold)."""
-    c = _cache(pages, k_scale, v_scale)
-    qs = _rows(q, "q", None, c.head_dim)
-    T, Hq = q.shape[0], q.shape[1]
-    b = _batch(block_table, kv_len, q_start, T)
-    if total_kv is None:
-        total_kv = b.B * b.max_pages * c.page_tokens
-    out = _out(out, "out", q.shape, (torch.bfloat16, *_BF16[1:]), q.device)
-    if return_lse or lse is not None:
-        lse = _out(lse, "lse", q.shape[:-1], (torch.float32,), q.device)
-    L = lib()
-    ws, n = _workspace(L.kv4_prefill_workspace(ctypes.byref(c), ctypes.byref(b), total_kv, Hq), workspace, q.device,
-                       stream)
-    _check(L.kv4_prefill(ctypes.byref(c), ctypes.byref(b), total_kv, _ptr(q), qs, Hq,
-                         c.head_dim ** -0.5 if sm_scale is None else sm_scale, _ptr(out), _ptr(lse), _ptr(ws), n,
-                         _ptr(dev_status), _stream(stream)), "kv4_prefill")
-    return (out, lse) if return_lse else out
-
-
-def _layers(pages):
-    """(layers, bytes from one layer to the next, pages, bytes of a page) of [L][num_pages]... or [num_pages]..."""
-    if pages.dtype != torch.uint8 or pages.dim() not in (4, 5) or not pages.is_cuda:
-        raise ValueError("pages: expected a uint8 CUDA tensor [num_pages][Hkv][groups][18 d] or [layers][num_pages]...")
-    one = pages if pages.dim() == 4 else pages[0]
-    if not one.is_contiguous():
-        raise ValueError("pages: a layer's pages must be contiguous")
-    size = one[0].numel()
-    return (1, 0, one.shape[0], size) if pages.dim() == 4 else (pages.shape[0], pages.stride(0), one.shape[0], size)
+    return _native().prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_kv,
+                             q.shape[-1] ** -0.5 if sm_scale is None else sm_scale, out, lse, return_lse, workspace,
+                             dev_status, stream)
 
 
 def kv4_copy_pages(pages, src, dst, dev_status=None, stream=None):
     """Copy pages src[i] -> dst[i] (int32 CUDA tensors) in every layer."""
-    layers, stride, n, size = _layers(pages)
-    _i32(src, "src", 1)
-    _i32(dst, "dst", 1)
-    if src.shape != dst.shape:
-        raise ValueError("src and dst have different lengths")
-    _check(lib().kv4_copy_pages(_ptr(pages), layers, stride, n, size, _ptr(src), _ptr(dst), src.shape[0],
-                                _ptr(dev_status), _stream(stream)), "kv4_copy_pages")
+    _native().copy_pages(pages, src, dst, dev_status, stream)
 
 
 def kv4_compact(pages, block_table, tables_out=None, page_map=None, n_live=None, workspace=None, dev_status=None,
@@ -191,18 +87,7 @@ def kv4_compact(pages, block_table, tables_out=None, page_map=None, n_live=None,
     """Move the live pages (those that block_table names) to the front in every
     layer. Returns (the tables with the new ids, every page's new id or -1, the
     number of live pages [1]), all int32."""
-    layers, stride, n, size = _layers(pages)
-    _i32(block_table, "block_table", 2)
-    i32 = (torch.int32,)
-    tables_out = _out(tables_out, "tables_out", block_table.shape, i32, pages.device)
-    page_map = _out(page_map, "page_map", (n,), i32, pages.device)
-    n_live = _out(n_live, "n_live", (1,), i32, pages.device)
-    L = lib()
-    ws, nb = _workspace(L.kv4_compact_workspace(n), workspace, pages.device, stream)
-    _check(L.kv4_compact(_ptr(pages), layers, stride, n, size, _ptr(block_table), *block_table.shape,
-                         _ptr(tables_out), _ptr(page_map), _ptr(n_live), _ptr(ws), nb, _ptr(dev_status),
-                         _stream(stream)), "kv4_compact")
-    return tables_out, page_map, n_live
+    return _native().compact(pages, block_table, tables_out, page_map, n_live, workspace, dev_status, stream)
 
 
 class KV4Book:
