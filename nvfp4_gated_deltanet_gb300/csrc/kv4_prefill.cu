@@ -19,7 +19,7 @@
 // tensor cores run the other's products:
 //   warps 0..3, 4..7  softmax of row tile 0 / 1, one row per thread: S from
 //                     tensor memory, weights back into tensor memory as FP16
-//                     in S's place (the A operand of O += P V)
+//                     in the place of S's second half (the A operand of O += P V)
 //   warp 8            TMEM allocation; one thread issues the MMAs
 //   warp 9            one thread streams K and V tiles by bulk copies
 // A row's weights are 2^(z - m + 6) with a maximum m that is only moved (and O
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
   uint8_t *qs = sm, *kbuf = sm + 2 * S::kTileBytes, *vbuf = kbuf + NS * S::kTileBytes;
   uint64_t *k_full = reinterpret_cast<uint64_t *>(vbuf + NS * S::kTileBytes);
   uint64_t *v_full = k_full + NS, *k_free = v_full + NS, *v_free = k_free + NS;
-  uint64_t *q_ready = v_free + NS, *s_full = q_ready + 2, *p_ready = s_full + 2, *o_done = p_ready + 2;
+  uint64_t *q_ready = v_free + NS, *s_full = q_ready + 2, *p_ready = s_full + 2, *o_done = p_ready + 4;
   uint64_t *fin = o_done + 2;
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(fin + 1);
   volatile uint32_t *abort_flag = tmem_holder + 1;
@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_ready + i, 128);
       mbar_init(s_full + i, 1);
-      mbar_init(p_ready + i, 128);
+      mbar_init(p_ready + 2 * i, 128);
+      mbar_init(p_ready + 2 * i + 1, 128);
       mbar_init(o_done + i, 1);
     }
     mbar_init(fin, 1);
@@ -271,25 +272,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < nkv[i]; ++j) {
-      if (!warp_wait(s_full + i, (uint32_t)(j & 1), abort_flag, c.status)) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, wait_or_abort(s_full + i, (uint32_t)(j & 1), abort_flag, c.status))) { ok = false; break; }
       tc_fence_after();
-      uint32_t raw[kKv];
+      const bool mask = j * kKv + kKv - 1 > sure;
+      // Half of the scores at a time (64 registers): the second half's weights
+      // take the place of its own scores, columns 96..127, and go to the MMAs
+      // while the first half is read again and its weights, columns 64..95, are made.
+      float s[64];
+      auto fetch = [&](int half) {
+        uint32_t raw[64];
+        tmem_ld32(tS + 64 * half, raw);
+        tmem_ld32(tS + 64 * half + 32, raw + 32);
+        tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, raw + 32 * q);
-      tmem_ld_wait();
-      float s[kKv];
+        for (int q = 0; q < 64; ++q) s[q] = __uint_as_float(raw[q]);
+        if (mask) {
 #pragma unroll
-      for (int q = 0; q < kKv; ++q) s[q] = __uint_as_float(raw[q]);
-      if (j * kKv + kKv - 1 > sure) {
+          for (int q = 0; q < 64; ++q)
+            if (j * kKv + 64 * half + q > last) s[q] = -INFINITY;
+        }
+      };
+      float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto largest = [&]() {
 #pragma unroll
-        for (int q = 0; q < kKv; ++q)
-          if (j * kKv + q > last) s[q] = -INFINITY;
-      }
-      float x4[4] = {s[0], s[1], s[2], s[3]};
+        for (int q = 0; q < 64; q += 4)
 #pragma unroll
-      for (int q = 4; q < kKv; q += 4)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
+          for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
+      };
+      fetch(0);
+      largest();
+      fetch(1);
+      largest();
       const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * cs;
       const bool up = top > m + kSlack;  // decided row by row: a row's result depends on no other row
       if (j == 0) {
@@ -311,25 +324,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
       }
       const float off = kShift - (m == -INFINITY ? 0.0f : m);
       const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
-      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
+      auto weigh = [&](int half) {
         uint32_t w[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          float2 z = fma2(make_float2(s[64 * q + 2 * e], s[64 * q + 2 * e + 1]), cs2, off2);
+          float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), cs2, off2);
           z.x = ex2(z.x);
           z.y = ex2(z.y);
           sum[e & 1] = add2(sum[e & 1], z);
           w[e] = h2u(__floats2half2_rn(z.x, z.y));
         }
-        tmem_st32(tS + 32 * q, w);
-      }
+        tmem_st32(tS + 64 + 32 * half, w);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_ready + 2 * i + half);
+      };
+      weigh(1);
+      fetch(0);
+      weigh(0);
       sum[0] = add2(sum[0], sum[1]);
-      l += sum[0].x + sum[0].y;
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(p_ready + i);
+      l = sum[0].x + sum[0].y;
     }
     // ------------------------------------------------ the rows' results
     const bool any = nkv[i] > 0 && ok && warp_wait(o_done + i, 0, abort_flag, c.status);
@@ -382,12 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
         ok = wait(v_full + j % NS, j / NS) && (j + 1 >= nmax || wait(k_full + (j + 1) % NS, (j + 1) / NS));
         for (int i = 0; i < 2 && ok; ++i) {
           if (j >= nkv[i]) continue;
-          if (!(ok = wait(p_ready + i, j))) break;
-          tc_fence_after();
+          for (int half = 1; half >= 0 && ok; --half) {  // O_i += P_i V_j, tokens 64..127 first
+            if (!(ok = wait(p_ready + 2 * i + half, j))) break;
+            tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < kKv / 16; ++k)  // O_i += P_i V_j
-            mma_f16_ts(tmem + S::kO + i * D, tmem + i * kKv + 8 * k,
-                       desc_sw128(va + (j % NS) * S::kTileBytes + (k / 4) * (D * 128)) + 2 * (k & 3), idO, j > 0 || k > 0);
+            for (int k = 0; k < 4; ++k)
+              mma_f16_ts(tmem + S::kO + i * D, tmem + i * kKv + 64 + 32 * half + 8 * k,
+                         desc_sw128(va + (j % NS) * S::kTileBytes + half * (D * 128)) + 2 * k, idO, j > 0 || half == 0 || k > 0);
+          }
+          if (!ok) break;
           if (j + 1 < nkv[i]) scores(i, j + 1);
           else tc_commit(o_done + i);
         }
