@@ -375,18 +375,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
       p.a.lse[(long long)(seq.q0 + tok) * p.a.Hq + hq] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
   } else if (warp == 8) {
     // ------------------------------------------------ MMAs
-    if (lane == 0 && nmax > 0) {
-      const uint32_t idS = idesc_f16(kKv), idO = idesc_f16(D);
-      const uint32_t qa = smem_u32(qs), ka = smem_u32(kbuf), va = smem_u32(vbuf);
+    if (nmax > 0 && elect_one()) {
+      constexpr uint32_t idS = idesc_f16(kKv), idO = idesc_f16(D);
+      constexpr uint64_t kStep = S::kTileBytes / 16;  // from one stage or tile to the next, in a descriptor
+      const uint64_t qd = desc_sw128(smem_u32(qs)), kd = desc_sw128(smem_u32(kbuf)), vd = desc_sw128(smem_u32(vbuf));
       auto wait = [&](uint64_t *bar, int use) { return wait_or_abort(bar, (uint32_t)(use & 1), abort_flag, c.status); };
       auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
+        const uint64_t q = qd + i * kStep, kk = kd + (uint64_t)(j % NS) * kStep;
+        const uint32_t d = tmem + i * kKv;
+        mma_f16_ss_c<false>(d, q, kk, idS);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_f16_ss(tmem + i * kKv, desc_sw128(qa + i * S::kTileBytes + (k / 4) * (kM * 128)) + 2 * (k & 3),
-                     desc_sw128(ka + (j % NS) * S::kTileBytes + (k / 4) * (kKv * 128)) + 2 * (k & 3), idS, k > 0);
+        for (int k = 1; k < D / 16; ++k)
+          mma_f16_ss_c<true>(d, q + (k / 4) * (kM * 128 / 16) + 2 * (k & 3), kk + (k / 4) * (kKv * 128 / 16) + 2 * (k & 3), idS);
         tc_commit(s_full + i);
       };
       bool ok = wait(q_ready, 0) && wait(q_ready + 1, 0) && wait(k_full, 0);
+      auto values = [&](int i, int j) {  // O_i += P_i V_j
+        const uint64_t v = vd + (uint64_t)(j % NS) * kStep;
+        const uint32_t d = tmem + S::kO + i * D, a = tmem + i * kKv + 64;
+        if (!(ok = wait(p_ready + 2 * i + 1, j))) return;  // tokens 64..127 first
+        tc_fence_after();
+        if (j == 0) mma_f16_ts_c<false>(d, a + 32, v + D * 128 / 16, idO);
+        else mma_f16_ts_c<true>(d, a + 32, v + D * 128 / 16, idO);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) mma_f16_ts_c<true>(d, a + 32 + 8 * k, v + D * 128 / 16 + 2 * k, idO);
+        if (!(ok = wait(p_ready + 2 * i, j))) return;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_f16_ts_c<true>(d, a + 8 * k, v + 2 * k, idO);
+      };
       if (ok) {
         tc_fence_after();
         for (int i = 0; i < 2; ++i)
@@ -395,16 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
       }
       for (int j = 0; j < nmax && ok; ++j) {
         ok = wait(v_full + j % NS, j / NS) && (j + 1 >= nmax || wait(k_full + (j + 1) % NS, (j + 1) / NS));
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (j >= nkv[i]) continue;
-          for (int half = 1; half >= 0 && ok; --half) {  // O_i += P_i V_j, tokens 64..127 first
-            if (!(ok = wait(p_ready + 2 * i + half, j))) break;
-            tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16_ts(tmem + S::kO + i * D, tmem + i * kKv + 64 + 32 * half + 8 * k,
-                         desc_sw128(va + (j % NS) * S::kTileBytes + half * (D * 128)) + 2 * k, idO, j > 0 || half == 0 || k > 0);
-          }
+        for (int i = 0; i < 2; ++i) {
+          if (!ok || j >= nkv[i]) continue;
+          values(i, j);
           if (!ok) break;
           if (j + 1 < nkv[i]) scores(i, j + 1);
           else tc_commit(o_done + i);

@@ -129,7 +129,7 @@ GDN_DEV uint32_t sw_off16(int row, int col) {
 }
 // Instruction descriptor of kind::f16 with FP16 A and B, FP32 accumulator,
 // both K-major, M = 128, N = n.
-GDN_DEV uint32_t idesc_f16(int n) {
+__host__ __device__ constexpr uint32_t idesc_f16(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 GDN_DEV void mma_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -140,14 +140,34 @@ GDN_DEV void mma_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t ide
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// D (+)= A B^T with A (FP16 pairs, 8 columns per K = 16 step) in tensor memory.
-GDN_DEV void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The same with the accumulate flag fixed at compile time, and with A (FP16
+// pairs, 8 columns per K = 16 step) in tensor memory. With descriptors that are
+// a base plus a constant these issue at the MMA's own rate (M = N = 128, K = 16:
+// 64 cycles on GB300); computing descriptors and flags between the MMAs costs
+// 105 to 140 cycles each, whatever N.
+template <bool ACC>
+GDN_DEV void mma_f16_ss_c(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+template <bool ACC>
+GDN_DEV void mma_f16_ts_c(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
+}
+// One lane of the (converged) warp.
+GDN_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 GDN_DEV void tmem_ld32(uint32_t taddr, uint32_t *r) {
   asm volatile(
