@@ -66,6 +66,19 @@ bool make_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t row_bytes
   return r == CUDA_SUCCESS;
 }
 
+bool make_heads_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t heads, uint64_t d, uint64_t row_stride,
+                    uint32_t box_rows, uint32_t box_heads) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {d, heads, rows};
+  cuuint64_t strides[2] = {d * 2, row_stride * 2};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 constexpr int kThreads = 192;

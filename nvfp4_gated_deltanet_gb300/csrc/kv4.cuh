@@ -139,7 +139,8 @@ struct Kv4AttnArgs {
 };
 cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream);
 size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms);  // its workspace
-cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, long long total_kv, void *workspace, cudaStream_t stream);
+cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, long long total_kv, void *workspace, int num_sms,
+                               cudaStream_t stream);
 size_t kv4_prefill_bytes(const Kv4AttnArgs &a, long long total_kv);  // its workspace; 0: too large
 
 struct Kv4PageArgs {

@@ -152,7 +152,9 @@ gdn_status kv4_prefill(const kv4_cache *c, const kv4_batch *b, int64_t total_kv,
   if (!workspace) return GDN_E_NULL;
   if (workspace_bytes < need) return GDN_E_SHAPE;
   if (!aligned16(workspace)) return GDN_E_ALIGN;
-  return cuda_status(launch_kv4_prefill(a, total_kv, workspace, static_cast<cudaStream_t>(stream)));
+  const int sms = num_sms();
+  if (sms < 1) return GDN_E_CUDA;
+  return cuda_status(launch_kv4_prefill(a, total_kv, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status kv4_copy_pages(uint8_t *pages, int n_layers, int64_t layer_stride, int num_pages, int64_t page_bytes,

@@ -6,27 +6,31 @@
 // chunk of a few tokens. Two kernels:
 //
 // kv4_expand_kernel decodes every sequence's cache once into tiles of 128
-// tokens in FP16 (exact: E2M1 x E4M3 has five significant bits), K as the
-// B operand of S = Q K^T and V transposed as the B operand of O += P V, both
-// already in the 128-byte swizzle that the MMA reads: each tile is one bulk
-// copy, no tensor map. Decoding inside the attention kernel would repeat it for
+// tokens, exactly (E2M1 x E4M3 has five significant bits): K in BF16 as the
+// B operand of S = Q K^T, whose A operand is q as it came, and V transposed in
+// FP16 as the B operand of O += P V, both already in the 128-byte swizzle that
+// the MMA reads: each tile is one bulk copy. Decoding inside the attention kernel would repeat it for
 // every 256 query rows (at 4096 tokens 64 times per KV head) on issue slots
 // that the softmax needs.
 //
-// kv4_prefill_kernel: one CTA per 256 query rows of one KV head -- two tiles of
+// kv4_prefill_kernel: an item is 256 query rows of one KV head -- two tiles of
 // 128 rows, a row being a (token, query head of the group), so the whole group
 // shares the tiles of K and V. While one tile's scores are in its softmax, the
-// tensor cores run the other's products:
+// tensor cores run the other's products. A CTA per SM takes items, the longest
+// first, until none is left; the next one's query rows and first products come
+// while the last one's results are written:
 //   warps 0..3, 4..7  softmax of row tile 0 / 1, one row per thread: S from
 //                     tensor memory, weights back into tensor memory as FP16
-//                     in the place of S's second half (the A operand of O += P V)
+//                     in the place of S's second half (the A operand of O += P V);
+//                     the item's results
 //   warp 8            TMEM allocation; one thread issues the MMAs
-//   warp 9            one thread streams K and V tiles by bulk copies
+//   warp 9            one thread streams K and V tiles by bulk copies and an
+//                     item's query rows by TMA (a box of tokens x the group's heads)
+//   warp 10           finds the next item
 // A row's weights are 2^(z - m + 6) with a maximum m that is only moved (and O
 // rescaled in tensor memory) when the row's true maximum passes it by 8: they
 // stay below 2^14, and normal FP16 numbers down to 2^-20 of the largest.
-// Rounding as in decode: q in FP16 by a power of two per row (exact but for
-// elements 2^-27 below the row's largest), the weights in FP16, all else FP32.
+// Rounding: q, K and V enter exactly, the weights in FP16, all else is FP32.
 // Every wait is bounded; one that gives up sets GDN_E_TIMEOUT and an abort flag
 // that ends every role's loop.
 #include "kv4.cuh"
@@ -38,7 +42,7 @@ namespace {
 
 constexpr int kKv = 128;          // tokens of a K / V tile
 constexpr int kM = 128;           // rows of a query tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr float kShift = 6.0f;    // weights are 2^(z - m + 6)
 constexpr float kSlack = 8.0f;    // how far a row's maximum may pass m before m moves
 constexpr float kLog2e = 1.4426950408889634f;
@@ -47,7 +51,8 @@ struct PrefillKv4 {
   Kv4AttnArgs a;
   int G, tpt;                     // query heads per KV head; tokens of a query tile: 128 / G
   int cap;                        // K / V tiles (of all KV heads) that the workspace holds
-  uint16_t *tiles;                // [cap][Hkv][K: d / 64 x 128 rows x 64, V^T: 2 x d rows x 64] FP16, swizzled
+  int *next;                      // items handed out beside each CTA's first one; zeroed by the expansion
+  uint16_t *tiles;                // [cap][Hkv][K: d / 64 x 128 rows x 64, BF16; V^T: 2 x d rows x 64, FP16], swizzled
 };
 
 GDN_DEV int seq_len(const Kv4Args &c, int b) {
@@ -89,7 +94,10 @@ __global__ void __launch_bounds__(256) kv4_expand_kernel(PrefillKv4 p) {
   int before = 0, total = 0;
   const int b = find_item(c.B, x, lane, [&](int i) { return (seq_len(c, i) + kKv - 1) / kKv; }, before, total);
   if (blockIdx.x == 0) {
-    if (tid == 0 && total > p.cap) flag_status(c.status, GDN_E_RANGE);
+    if (tid == 0) {
+      if (total > p.cap) flag_status(c.status, GDN_E_RANGE);
+      *p.next = 0;
+    }
     for (int i = tid; i < c.B; i += 256) kv4_seq(c, i);  // flags bad entries
   }
   if (b < 0) return;
@@ -108,8 +116,18 @@ __global__ void __launch_bounds__(256) kv4_expand_kernel(PrefillKv4 p) {
     const uint8_t *g = groups[row / 16];
     uint32_t o[4] = {0, 0, 0, 0};
     if (g && pos0 + row < len) {
-      const __half2 s = __float2half2_rn(e4m3_to_f32(g[kv4_k_scale<D>(row & 15, w / 2)]));
-      decode8(*reinterpret_cast<const uint32_t *>(g + kv4_k_code<D>(row & 15, w * 4)), s, o);
+      // an FP16 code moved down 3 bits is the BF16 value 2^-112 times as large; the scale (at most 448) makes that good
+      const float s = e4m3_to_f32(g[kv4_k_scale<D>(row & 15, w / 2)]) * 5.192296858534828e33f;  // 2^112
+      const __nv_bfloat162 s2 = __float2bfloat162_rn(s);
+      __half2 e[4];
+      e2m1x8_to_h2x4(*reinterpret_cast<const uint32_t *>(g + kv4_k_code<D>(row & 15, w * 4)), e);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t x = h2u(e[q]);
+        uint32_t y = ((x >> 3) & 0x0FFF0FFFu) | (x & 0x80008000u);
+        const __nv_bfloat162 z = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&y), s2);
+        o[q] = *reinterpret_cast<const uint32_t *>(&z);
+      }
     }
     *reinterpret_cast<uint4 *>(tile + (w / 8) * (kKv * 128) + sw_off16(row, (w & 7) * 8)) = make_uint4(o[0], o[1], o[2], o[3]);
   }
@@ -146,62 +164,102 @@ template <int D>
 struct PrefillShape {
   static constexpr int kStages = D == 128 ? 2 : 4;   // of K and of V each
   static constexpr int kTileBytes = kKv * D * 2;     // a K tile, a V tile, and 128 query rows
-  static constexpr int kBars = 256;
-  static constexpr int kBytes = 1024 + (2 + 2 * kStages) * kTileBytes + kBars;
+  static constexpr int kOut = 8 * 4096;              // per softmax warp: 32 rows x 128 bytes of results on their way
+  static constexpr int kBars = 512;
+  static constexpr int kBytes = (2 + 2 * kStages) * kTileBytes + kOut + kBars;
   static constexpr int kO = 2 * kKv;                 // TMEM columns: S0, S1, then O0, O1
   static_assert(kO + 2 * D <= 512, "tensor memory");
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
+// 256 query rows of one KV head: sequence rows q0 + t0 .., and the K / V tiles
+// that each row tile sees.
+struct Item {
+  int h, q0, n, t0, len, nkv[2], tile0;  // h < 0: no more items
+};
+
+// The x-th item by falling cost (K / V tiles) of all sequences, without its
+// head; false past the end. All lanes of a warp.
+GDN_DEV bool find_work(const PrefillKv4 &p, int x, int lane, Item &w) {
+  const Kv4Args &c = p.a.c;
+  const int step = 2 * p.tpt;
+  Kv4Seq s0 = {0, 0, 0};  // of sequence `lane`
+  if (lane < c.B) s0 = kv4_seq(c, lane);
+  auto seq_of = [&](int b) { return b < 32 ? s0 : kv4_seq(c, b); };  // b % 32 == lane
+  auto count = [&](const Kv4Seq &s, int cost) {  // the sequence's items of at least this cost
+    const int n = s.q1 - s.q0, items = (n + step - 1) / step;
+    if (cost == 0) return items;
+    const long long at = (long long)(cost - 1) * kKv - (s.len - n);  // an item's last token, at least
+    return at <= 0 ? items : at >= n ? 0 : items - (int)at / step;
+  };
+  auto all = [&](int cost) {
+    int v = 0;
+    for (int b = lane; b < c.B; b += 32) v += count(seq_of(b), cost);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  if (x >= all(0)) return false;
+  int lo = 0, hi = (int)(((long long)c.cols * c.page_tokens + kKv - 1) / kKv) + 1;  // all(lo) > x >= all(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (all(mid) > x) lo = mid; else hi = mid;
+  }
+  int r = x - all(lo + 1);  // among the items of cost lo, by sequence
+  int tiles = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 32) {
+    const bool in = b0 + lane < c.B;
+    const Kv4Seq s = in ? seq_of(b0 + lane) : Kv4Seq{0, 0, 0};
+    const int above = count(s, lo + 1), e = count(s, lo) - above, kt = (s.len + kKv - 1) / kKv;
+    int incl = e, kincl = kt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, kincl, o);
+      if (lane >= o) {
+        incl += y;
+        kincl += z;
+      }
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, incl > r);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const int n = s.q1 - s.q0, items = (n + step - 1) / step;
+      w.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+      w.n = __shfl_sync(0xffffffffu, n, l);
+      w.len = __shfl_sync(0xffffffffu, s.len, l);
+      w.t0 = __shfl_sync(0xffffffffu, items - 1 - above - (r - (incl - e)), l) * step;
+      w.tile0 = tiles + __shfl_sync(0xffffffffu, kincl - kt, l);
+      break;
+    }
+    r -= __shfl_sync(0xffffffffu, incl, 31);
+    tiles += __shfl_sync(0xffffffffu, kincl, 31);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t1 = min(w.n, w.t0 + (i + 1) * p.tpt) - 1;  // the row tile's last token
+    const int last = w.len - w.n + t1;
+    w.nkv[i] = t1 >= w.t0 + i * p.tpt && last >= 0 ? last / kKv + 1 : 0;
+    if (w.tile0 + w.nkv[i] > p.cap) w.nkv[i] = 0;         // the workspace was too small (flagged by the expansion)
+  }
+  return true;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) {
+__global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, PrefillKv4 p) {
   using S = PrefillShape<D>;
   constexpr int NS = S::kStages;
-  extern __shared__ uint8_t smraw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
-  uint8_t *qs = sm, *kbuf = sm + 2 * S::kTileBytes, *vbuf = kbuf + NS * S::kTileBytes;
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(vbuf + NS * S::kTileBytes);
+  extern __shared__ __align__(1024) uint8_t sm[];  // the swizzled tiles start on 1024 bytes
+  uint8_t *qs = sm, *kbuf = sm + 2 * S::kTileBytes, *vbuf = kbuf + NS * S::kTileBytes, *obuf = vbuf + NS * S::kTileBytes;
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(obuf + S::kOut);
   uint64_t *v_full = k_full + NS, *k_free = v_full + NS, *v_free = k_free + NS;
-  uint64_t *q_ready = v_free + NS, *s_full = q_ready + 2, *p_ready = s_full + 2, *o_done = p_ready + 4;
-  uint64_t *fin = o_done + 2;
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(fin + 1);
+  uint64_t *s_full = v_free + NS, *p_ready = s_full + 2, *o_done = p_ready + 4;
+  uint64_t *q_full = o_done + 2, *q_free = q_full + 1;
+  uint64_t *item_full = q_free + 1, *item_free = item_full + 2, *fin = item_free + 2;
+  Item *items = reinterpret_cast<Item *>(fin + 1);  // [2]
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(items + 2);
   volatile uint32_t *abort_flag = tmem_holder + 1;
   const Kv4Args &c = p.a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  // ------------------------------------------------ which rows: the last, longest ones first
-  const int h = blockIdx.x % c.Hkv, x = blockIdx.x / c.Hkv;
-  int before = 0, total = 0, unused = 0;
-  auto qtiles = [&](int b) {
-    const Kv4Seq s = kv4_seq(c, b);
-    return (s.q1 - s.q0 + 2 * p.tpt - 1) / (2 * p.tpt);
-  };
-  find_item(c.B, 0x7fffffff, lane, qtiles, before, total);
-  if (x >= total) {
-    pdl_wait();  // on every path: this grid must not end before the one it follows
-    return;
-  }
-  const int item = total - 1 - x;
-  const int b = find_item(c.B, item, lane, qtiles, before, unused);
-  const Kv4Seq seq = kv4_seq(c, b);
-  const int n = seq.q1 - seq.q0, t0 = (item - before) * 2 * p.tpt;  // this CTA's first new token
-  int tile0 = 0;  // the sequence's first K / V tile
-  for (int b0 = 0; b0 < b; b0 += 32) {
-    int v = b0 + lane < b ? (seq_len(c, b0 + lane) + kKv - 1) / kKv : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    tile0 += v;
-  }
-  // K / V tiles that each row tile sees (none where the workspace was too small: flagged by the expansion)
-  int nkv[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t1 = min(n, t0 + (i + 1) * p.tpt) - 1;   // the row tile's last token
-    const int last = seq.len - n + t1;
-    nkv[i] = t1 >= t0 + i * p.tpt && last >= 0 ? last / kKv + 1 : 0;
-    if (tile0 + nkv[i] > p.cap) nkv[i] = 0;
-  }
-  const int nmax = max(nkv[0], nkv[1]);
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -211,12 +269,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
       mbar_init(v_free + s, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_ready + i, 128);
       mbar_init(s_full + i, 1);
       mbar_init(p_ready + 2 * i, 128);
       mbar_init(p_ready + 2 * i + 1, 128);
       mbar_init(o_done + i, 1);
+      mbar_init(item_full + i, 1);
+      mbar_init(item_free + i, 10);  // every warp but the one that fills it
     }
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
     mbar_init(fin, 1);
     *abort_flag = 0u;
     fence_barrier_init();
@@ -229,228 +290,286 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  auto wait = [&](uint64_t *bar, uint32_t use) { return wait_or_abort(bar, use & 1u, abort_flag, c.status); };
+  auto warp_wait_all = [&](uint64_t *bar, uint32_t use) { return __all_sync(0xffffffffu, wait(bar, use)) != 0; };
+  // Item `it` of this CTA; false when there is none (or a wait gave up). A whole warp.
+  auto take = [&](int it, Item &w) {
+    if (!warp_wait_all(item_full + (it & 1), it >> 1)) return false;
+    w = items[it & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_free + (it & 1));
+    return w.h >= 0;
+  };
 
   if (warp < 8) {
     // ------------------------------------------------ softmax: thread = row r of row tile i
     const int i = warp >> 2, r = tid & 127;
-    const int tok = t0 + i * p.tpt + r / p.G;
-    const bool in = r < p.tpt * p.G && tok < n;
-    const int hq = h * p.G + r % p.G;
-    float cs;
-    {
-      uint4 w[D / 8];
-      const uint16_t *qp = p.a.q + (long long)(seq.q0 + tok) * p.a.q_stride + (long long)hq * D;
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) w[j] = in ? reinterpret_cast<const uint4 *>(qp)[j] : make_uint4(0, 0, 0, 0);
-      uint32_t mx = 0;  // the largest magnitude, as BF16 bits
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        const uint32_t y[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx = max(mx, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
-      }
-      const int k = min(140 - (int)(mx >> 7), 60);  // 2^k takes the largest to [2^13, 2^14)
-      const float sc = __uint_as_float((uint32_t)(k + 127) << 23);
-      cs = p.a.sm_scale * c.ks * kLog2e * __uint_as_float((uint32_t)(127 - k) << 23);
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        const uint32_t y[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-        uint32_t z[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          z[e] = h2u(__floats2half2_rn(__uint_as_float(y[e] << 16) * sc, __uint_as_float(y[e] & 0xFFFF0000u) * sc));
-        *reinterpret_cast<uint4 *>(qs + i * S::kTileBytes + (j / 8) * (kM * 128) + sw_off16(r, (j & 7) * 8)) =
-            make_uint4(z[0], z[1], z[2], z[3]);
-      }
-      fence_async_shared();
-      mbar_arrive(q_ready + i);
-    }
-    const int last = in ? seq.len - n + tok : -1;               // the last token this row sees
-    const int sure = seq.len - n + t0 + i * p.tpt;              // every row of the tile sees up to here
     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = base + i * kKv, tO = base + S::kO + i * D;
-    float m = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int j = 0; j < nkv[i]; ++j) {
-      if (!__all_sync(0xffffffffu, wait_or_abort(s_full + i, (uint32_t)(j & 1), abort_flag, c.status))) { ok = false; break; }
-      tc_fence_after();
-      const bool mask = j * kKv + kKv - 1 > sure;
-      // Half of the scores at a time (64 registers): the second half's weights
-      // take the place of its own scores, columns 96..127, and go to the MMAs
-      // while the first half is read again and its weights, columns 64..95, are made.
-      float s[64];
-      auto fetch = [&](int half) {
-        uint32_t raw[64];
-        tmem_ld32(tS + 64 * half, raw);
-        tmem_ld32(tS + 64 * half + 32, raw + 32);
-        tmem_ld_wait();
-#pragma unroll
-        for (int q = 0; q < 64; ++q) s[q] = __uint_as_float(raw[q]);
-        if (mask) {
-#pragma unroll
-          for (int q = 0; q < 64; ++q)
-            if (j * kKv + 64 * half + q > last) s[q] = -INFINITY;
-        }
-      };
-      float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto largest = [&]() {
-#pragma unroll
-        for (int q = 0; q < 64; q += 4)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
-      };
-      fetch(0);
-      largest();
-      fetch(1);
-      largest();
-      const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * cs;
-      const bool up = top > m + kSlack;  // decided row by row: a row's result depends on no other row
-      if (j == 0) {
-        m = top;
-      } else if (__any_sync(0xffffffffu, up)) {
-        // S of this tile is complete, so the O += P V issued before it is too
-        const float f = up ? ex2(m - top) : 1.0f;
-        if (up) m = top;
-        l *= f;
-#pragma unroll
-        for (int q = 0; q < D; q += 32) {
-          uint32_t o[32];
-          tmem_ld32(tO + q, o);
+    const float cs = p.a.sm_scale * c.ks * kLog2e;
+    uint32_t uses = 0, dones = 0;  // of this row tile's scores, and items that had any
+    for (int it = 0; warp_wait_all(item_full + (it & 1), it >> 1); ++it) {
+      const Item &w = items[it & 1];  // read where it is needed, and given back at the end: registers are short
+      if (w.h < 0) break;
+      const int off_t = i * p.tpt + r / p.G;                      // the row's token, from the item's first
+      const int sure = w.len - w.n + w.t0 + i * p.tpt;            // every row of the tile sees up to here
+      const int last = r < p.tpt * p.G && w.t0 + off_t < w.n ? w.len - w.n + w.t0 + off_t : -1;  // the last token this row sees
+      const int nkv = w.nkv[i];
+      float m = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < nkv; ++j, ++uses) {
+        if (!warp_wait_all(s_full + i, uses)) { ok = false; break; }
+        tc_fence_after();
+        const bool mask = j * kKv + kKv - 1 > sure;
+        // Half of the scores at a time (64 registers): the second half's weights
+        // take the place of its own scores, columns 96..127, and go to the MMAs
+        // while the first half is read again and its weights, columns 64..95, are made.
+        float s[64];
+        auto fetch = [&](int half) {
+          uint32_t raw[64];
+          tmem_ld32(tS + 64 * half, raw);
+          tmem_ld32(tS + 64 * half + 32, raw + 32);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st32(tO + q, o);
+          for (int q = 0; q < 64; ++q) s[q] = __uint_as_float(raw[q]);
+          if (mask) {
+#pragma unroll
+            for (int q = 0; q < 64; ++q)
+              if (j * kKv + 64 * half + q > last) s[q] = -INFINITY;
+          }
+        };
+        float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto largest = [&]() {
+#pragma unroll
+          for (int q = 0; q < 64; q += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
+        };
+        fetch(0);
+        largest();
+        fetch(1);
+        largest();
+        const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * cs;
+        const bool up = top > m + kSlack;  // decided row by row: a row's result depends on no other row
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, up)) {
+          // S of this tile is complete, so the O += P V issued before it is too
+          const float f = up ? ex2(m - top) : 1.0f;
+          if (up) m = top;
+          l *= f;
+#pragma unroll
+          for (int q = 0; q < D; q += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + q, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(tO + q, o);
+          }
         }
-      }
-      const float off = kShift - (m == -INFINITY ? 0.0f : m);
-      const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
-      float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
-      auto weigh = [&](int half) {
-        uint32_t w[32];
+        const float off = kShift - (m == -INFINITY ? 0.0f : m);
+        const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
+        float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
+        auto weigh = [&](int half) {
+          uint32_t x[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), cs2, off2);
-          z.x = ex2(z.x);
-          z.y = ex2(z.y);
-          sum[e & 1] = add2(sum[e & 1], z);
-          w[e] = h2u(__floats2half2_rn(z.x, z.y));
+          for (int e = 0; e < 32; ++e) {
+            float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), cs2, off2);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            sum[e & 1] = add2(sum[e & 1], z);
+            x[e] = h2u(__floats2half2_rn(z.x, z.y));
+          }
+          tmem_st32(tS + 64 + 32 * half, x);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_ready + 2 * i + half);
+        };
+        weigh(1);
+        fetch(0);
+        weigh(0);
+        sum[0] = add2(sum[0], sum[1]);
+        l = sum[0].x + sum[0].y;
+      }
+      // ---------------------------------------------- the rows' results, 64 channels at a time: each lane's row
+      // into the warp's staging rows, from there whole 128-byte lines to memory (16 bytes of 32 rows at a time
+      // straight from the lanes took 5000 cycles an item)
+      if (!ok || (nkv > 0 && !warp_wait_all(o_done + i, dones++))) break;
+      tc_fence_after();
+      const float inv = l == 0.0f ? 0.0f : c.vs / l;
+      uint8_t *st = obuf + warp * 4096;
+#pragma unroll
+      for (int q0 = 0; q0 < D; q0 += 64) {
+#pragma unroll
+        for (int q = 0; q < 64; q += 32) {
+          uint32_t o[32];
+          if (nkv > 0) {
+            tmem_ld32(tO + q0 + q, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          uint32_t x[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x[e] = f32_to_bf16_bits(__uint_as_float(o[2 * e]) * inv) |
+                   (uint32_t)f32_to_bf16_bits(__uint_as_float(o[2 * e + 1]) * inv) << 16;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4 *>(st + lane * 128 + (((q / 8 + e) ^ (lane & 7)) << 4)) =
+                make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
-        tmem_st32(tS + 64 + 32 * half, w);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(p_ready + 2 * i + half);
-      };
-      weigh(1);
-      fetch(0);
-      weigh(0);
-      sum[0] = add2(sum[0], sum[1]);
-      l = sum[0].x + sum[0].y;
-    }
-    // ------------------------------------------------ the rows' results
-    const bool any = nkv[i] > 0 && ok && warp_wait(o_done + i, 0, abort_flag, c.status);
-    tc_fence_after();
-    const float inv = l == 0.0f ? 0.0f : c.vs / l;
-    uint16_t *op = p.a.out + ((long long)(seq.q0 + tok) * p.a.Hq + hq) * D;
+        __syncwarp();
 #pragma unroll
-    for (int q = 0; q < D; q += 32) {
-      uint32_t o[32];
-      if (any) {
-        tmem_ld32(tO + q, o);
-        tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0u;
+        for (int k = 0; k < 8; ++k) {
+          const int row = k * 4 + (lane >> 3), rr = (warp & 3) * 32 + row, tk = w.t0 + i * p.tpt + rr / p.G;
+          if (rr < p.tpt * p.G && tk < w.n)
+            reinterpret_cast<uint4 *>(p.a.out + ((long long)(w.q0 + tk) * p.a.Hq + w.h * p.G + rr % p.G) * D + q0)[lane & 7] =
+                *reinterpret_cast<const uint4 *>(st + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+        }
+        __syncwarp();
       }
-      uint32_t w[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        w[e] = f32_to_bf16_bits(__uint_as_float(o[2 * e]) * inv) | (uint32_t)f32_to_bf16_bits(__uint_as_float(o[2 * e + 1]) * inv) << 16;
-      if (in) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          reinterpret_cast<uint4 *>(op + q)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-      }
+      tc_fence_before();  // O has been read: the next item's products follow this row tile's next weights
+      const int tok = w.t0 + off_t;
+      if (p.a.lse && r < p.tpt * p.G && tok < w.n)
+        p.a.lse[(long long)(w.q0 + tok) * p.a.Hq + w.h * p.G + r % p.G] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_free + (it & 1));
     }
-    if (in && p.a.lse)
-      p.a.lse[(long long)(seq.q0 + tok) * p.a.Hq + hq] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
   } else if (warp == 8) {
     // ------------------------------------------------ MMAs
-    if (nmax > 0 && elect_one()) {
-      constexpr uint32_t idS = idesc_f16(kKv), idO = idesc_f16(D);
-      constexpr uint64_t kStep = S::kTileBytes / 16;  // from one stage or tile to the next, in a descriptor
-      const uint64_t qd = desc_sw128(smem_u32(qs)), kd = desc_sw128(smem_u32(kbuf)), vd = desc_sw128(smem_u32(vbuf));
-      auto wait = [&](uint64_t *bar, int use) { return wait_or_abort(bar, (uint32_t)(use & 1), abort_flag, c.status); };
-      auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
-        const uint64_t q = qd + i * kStep, kk = kd + (uint64_t)(j % NS) * kStep;
-        const uint32_t d = tmem + i * kKv;
-        mma_f16_ss_c<false>(d, q, kk, idS);
+    constexpr uint32_t idS = idesc_bf16(kKv), idO = idesc_f16(D);
+    constexpr uint64_t kStep = S::kTileBytes / 16;  // from one stage or tile to the next, in a descriptor
+    const uint64_t qd = desc_sw128(smem_u32(qs)), kd = desc_sw128(smem_u32(kbuf)), vd = desc_sw128(smem_u32(vbuf));
+    const bool me = elect_one();
+    uint32_t kv = 0, uses[2] = {0, 0};  // K / V tiles taken, and each row tile's
+    Item w;
+    bool ok = true;
+    for (int it = 0; ok && take(it, w); ++it) {
+      const int nmax = max(w.nkv[0], w.nkv[1]);
+      if (me) {
+        auto scores = [&](int i, uint32_t use) {  // S_i = Q_i K^T
+          const uint64_t q = qd + i * kStep, kk = kd + (uint64_t)(use % NS) * kStep;
+          const uint32_t d = tmem + i * kKv;
+          mma_f16_ss_c<false>(d, q, kk, idS);
 #pragma unroll
-        for (int k = 1; k < D / 16; ++k)
-          mma_f16_ss_c<true>(d, q + (k / 4) * (kM * 128 / 16) + 2 * (k & 3), kk + (k / 4) * (kKv * 128 / 16) + 2 * (k & 3), idS);
-        tc_commit(s_full + i);
-      };
-      bool ok = wait(q_ready, 0) && wait(q_ready + 1, 0) && wait(k_full, 0);
-      auto values = [&](int i, int j) {  // O_i += P_i V_j
-        const uint64_t v = vd + (uint64_t)(j % NS) * kStep;
-        const uint32_t d = tmem + S::kO + i * D, a = tmem + i * kKv + 64;
-        if (!(ok = wait(p_ready + 2 * i + 1, j))) return;  // tokens 64..127 first
-        tc_fence_after();
-        if (j == 0) mma_f16_ts_c<false>(d, a + 32, v + D * 128 / 16, idO);
-        else mma_f16_ts_c<true>(d, a + 32, v + D * 128 / 16, idO);
+          for (int k = 1; k < D / 16; ++k)
+            mma_f16_ss_c<true>(d, q + (k / 4) * (kM * 128 / 16) + 2 * (k & 3), kk + (k / 4) * (kKv * 128 / 16) + 2 * (k & 3), idS);
+          tc_commit(s_full + i);
+        };
+        auto values = [&](int i, uint32_t use, bool first) {  // O_i += P_i V
+          const uint64_t v = vd + (uint64_t)(use % NS) * kStep;
+          const uint32_t d = tmem + S::kO + i * D, a = tmem + i * kKv + 64;
+          if (!(ok = wait(p_ready + 2 * i + 1, uses[i]))) return;  // tokens 64..127 first
+          tc_fence_after();
+          if (first) mma_f16_ts_c<false>(d, a + 32, v + D * 128 / 16, idO);
+          else mma_f16_ts_c<true>(d, a + 32, v + D * 128 / 16, idO);
 #pragma unroll
-        for (int k = 1; k < 4; ++k) mma_f16_ts_c<true>(d, a + 32 + 8 * k, v + D * 128 / 16 + 2 * k, idO);
-        if (!(ok = wait(p_ready + 2 * i, j))) return;
-        tc_fence_after();
+          for (int k = 1; k < 4; ++k) mma_f16_ts_c<true>(d, a + 32 + 8 * k, v + D * 128 / 16 + 2 * k, idO);
+          if (!(ok = wait(p_ready + 2 * i, uses[i]))) return;
+          tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f16_ts_c<true>(d, a + 8 * k, v + 2 * k, idO);
-      };
-      if (ok) {
-        tc_fence_after();
-        for (int i = 0; i < 2; ++i)
-          if (nkv[i] > 0) scores(i, 0);
-        tc_commit(k_free);
-      }
-      for (int j = 0; j < nmax && ok; ++j) {
-        ok = wait(v_full + j % NS, j / NS) && (j + 1 >= nmax || wait(k_full + (j + 1) % NS, (j + 1) / NS));
+          for (int k = 0; k < 4; ++k) mma_f16_ts_c<true>(d, a + 8 * k, v + 2 * k, idO);
+          ++uses[i];
+        };
+        ok = wait(q_full, it);
+        if (ok && nmax > 0 && (ok = wait(k_full + kv % NS, kv / NS))) {
+          tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok || j >= nkv[i]) continue;
-          values(i, j);
-          if (!ok) break;
-          if (j + 1 < nkv[i]) scores(i, j + 1);
-          else tc_commit(o_done + i);
+          for (int i = 0; i < 2; ++i)
+            if (w.nkv[i] > 0) scores(i, kv);
+          tc_commit(k_free + kv % NS);
         }
-        if (!ok) break;
-        tc_commit(v_free + j % NS);
-        if (j + 1 < nmax) tc_commit(k_free + (j + 1) % NS);
+        if (ok && nmax <= 1) tc_commit(q_free);
+        for (int j = 0; j < nmax && ok; ++j) {
+          const uint32_t u = kv + j;
+          ok = wait(v_full + u % NS, u / NS) && (j + 1 >= nmax || wait(k_full + (u + 1) % NS, (u + 1) / NS));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || j >= w.nkv[i]) continue;
+            values(i, u, j == 0);
+            if (!ok) break;
+            if (j + 1 < w.nkv[i]) scores(i, u + 1);
+            else tc_commit(o_done + i);
+          }
+          if (!ok) break;
+          tc_commit(v_free + u % NS);
+          if (j + 1 < nmax) tc_commit(k_free + (u + 1) % NS);
+          if (j + 2 == nmax) tc_commit(q_free);  // the item's last scores are issued
+        }
       }
-      // every MMA issued has completed before the CTA may leave
+      ok = __any_sync(0xffffffffu, me && ok);
+      kv += nmax;
+    }
+    // every MMA issued has completed before the CTA may leave
+    if (me) {
       tc_commit(fin);
       mbar_wait(fin, 0u);
     }
-  } else if (lane == 0) {
-    // ------------------------------------------------ K and V tiles
-    pdl_wait();  // the expansion has finished
-    const uint8_t *src = reinterpret_cast<const uint8_t *>(p.tiles) + ((size_t)tile0 * c.Hkv + h) * (2 * S::kTileBytes);
-    const size_t step = (size_t)c.Hkv * 2 * S::kTileBytes;
-    int j = 0;
-    for (; j < nmax; ++j) {
-      const int s = j % NS, u = j / NS;
-      if (u > 0 && !wait_or_abort(k_free + s, (uint32_t)((u - 1) & 1), abort_flag, c.status)) break;
-      mbar_arrive_expect_tx(k_full + s, S::kTileBytes);
-      bulk_g2s(kbuf + s * S::kTileBytes, src + j * step, S::kTileBytes, k_full + s);
-      if (u > 0 && !wait_or_abort(v_free + s, (uint32_t)((u - 1) & 1), abort_flag, c.status)) break;
-      mbar_arrive_expect_tx(v_full + s, S::kTileBytes);
-      bulk_g2s(vbuf + s * S::kTileBytes, src + j * step + S::kTileBytes, S::kTileBytes, v_full + s);
-    }
-    if (*abort_flag)  // the copies in flight land (or a bounded wait for each ends) before the CTA leaves
-      for (int s = 0; s < NS; ++s) {
-        const int uses = (j + NS - 1 - s) / NS;
-        if (uses > 0) {
-          mbar_wait(k_full + s, (uint32_t)((uses - 1) & 1));
-          mbar_wait(v_full + s, (uint32_t)((uses - 1) & 1));
+  } else if (warp == 9) {
+    // ------------------------------------------------ query rows, K and V tiles
+    const int q_bytes = p.tpt * p.G * D * 2;  // of a row tile
+    uint32_t u = 0, taken = 0;  // K / V tiles, items
+    Item w;
+    bool ok = true;
+    for (int it = 0; ok && take(it, w); ++it) {
+      const int nmax = max(w.nkv[0], w.nkv[1]);
+      if (lane == 0 && it > 0) ok = wait(q_free, it - 1);
+      if (lane == 0 && ok) {
+        mbar_arrive_expect_tx(q_full, 2 * q_bytes);
+        ++taken;
+#pragma unroll
+        for (int x = 0; x < 2 * (D / 64); ++x)
+          tma_load_3d(qs + (x / (D / 64)) * S::kTileBytes + (x % (D / 64)) * (kM * 128), &tmQ, x % (D / 64) * 64, w.h * p.G,
+                      w.q0 + w.t0 + x / (D / 64) * p.tpt, q_full);
+        if (it == 0) pdl_wait();  // the expansion has finished
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(p.tiles) + ((size_t)w.tile0 * c.Hkv + w.h) * (2 * S::kTileBytes);
+        const size_t step = (size_t)c.Hkv * 2 * S::kTileBytes;
+        for (int j = 0; j < nmax; ++j, ++u) {
+          const int s = u % NS;
+          if (u >= NS && !(ok = wait(k_free + s, u / NS - 1))) break;
+          mbar_arrive_expect_tx(k_full + s, S::kTileBytes);
+          bulk_g2s(kbuf + s * S::kTileBytes, src + j * step, S::kTileBytes, k_full + s);
+          if (u >= NS && !(ok = wait(v_free + s, u / NS - 1))) {
+            mbar_wait(k_full + s, (u / NS) & 1u);
+            break;
+          }
+          mbar_arrive_expect_tx(v_full + s, S::kTileBytes);
+          bulk_g2s(vbuf + s * S::kTileBytes, src + j * step + S::kTileBytes, S::kTileBytes, v_full + s);
         }
       }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    }
+    if (lane == 0 && u == 0) pdl_wait();
+    if (lane == 0 && *abort_flag) {  // the copies in flight land (or a bounded wait for each ends) before the CTA leaves
+      if (taken > 0) mbar_wait(q_full, (taken - 1) & 1u);
+      for (uint32_t x = u < NS ? 0 : u - NS; x < u; ++x) {
+        mbar_wait(k_full + x % NS, (x / NS) & 1u);
+        mbar_wait(v_full + x % NS, (x / NS) & 1u);
+      }
+    }
+  } else {
+    // ------------------------------------------------ the next item
+    for (int it = 0;; ++it) {
+      if (it == 1) pdl_wait();  // the counter is zeroed by the expansion
+      int x = blockIdx.x;
+      if (it > 0) {
+        if (lane == 0) x = (int)gridDim.x + atomicAdd(p.next, 1);
+        x = __shfl_sync(0xffffffffu, x, 0);
+      }
+      Item w{-1, 0, 0, 0, 0, {0, 0}, 0};
+      if (find_work(p, x / c.Hkv, lane, w)) w.h = x % c.Hkv;
+      if (it >= 2 && !warp_wait_all(item_free + (it & 1), (it >> 1) - 1)) break;
+      if (lane == 0) {
+        items[it & 1] = w;
+        mbar_arrive(item_full + (it & 1));
+      }
+      __syncwarp();
+      if (w.h < 0) break;
+    }
+    pdl_wait();  // on every path: this grid must not end before the one it follows
   }
   tc_fence_before();
   __syncthreads();
@@ -461,15 +580,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(PrefillKv4 p) 
 }
 
 template <int D>
-cudaError_t launch_prefill_t(const PrefillKv4 &p, cudaStream_t stream) {
+cudaError_t launch_prefill_t(const PrefillKv4 &p, int num_sms, cudaStream_t stream) {
   using S = PrefillShape<D>;
+  CUtensorMap tmQ;
+  if (!make_heads_map(&tmQ, p.a.q, p.a.c.T, p.a.Hq, D, p.a.q_stride, p.tpt, p.G)) return cudaErrorInvalidValue;
   static bool allowed[64];
   cudaError_t e = kv4_allow_smem(kv4_prefill_kernel<D>, S::kBytes, allowed);
   if (e != cudaSuccess) return e;
   const Kv4Args &c = p.a.c;
   kv4_expand_kernel<D><<<(unsigned)p.cap * c.Hkv, 256, 0, stream>>>(p);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(c.T / (2 * p.tpt) + c.B) * c.Hkv, 1, 1);
+  const long long items = (long long)(c.T / (2 * p.tpt) + c.B) * c.Hkv;  // at most
+  cfg.gridDim = dim3((unsigned)(items < num_sms ? items : num_sms), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = S::kBytes;
   cfg.stream = stream;
@@ -478,7 +600,7 @@ cudaError_t launch_prefill_t(const PrefillKv4 &p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_prefill_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, kv4_prefill_kernel<D>, tmQ, p);
 }
 
 // K / V tiles: every sequence's last one may be partly filled.
@@ -489,13 +611,15 @@ long long tile_cap(const Kv4AttnArgs &a, long long total_kv) { return total_kv /
 // 0 where the tiles would pass what a grid can index.
 size_t kv4_prefill_bytes(const Kv4AttnArgs &a, long long total_kv) {
   const long long n = tile_cap(a, total_kv) * a.c.Hkv;
-  return n > 0x7fffffffLL ? 0 : (size_t)n * 4 * kKv * a.c.D;
+  return n > 0x7fffffffLL ? 0 : (size_t)n * 4 * kKv * a.c.D + 16;
 }
 
-cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, long long total_kv, void *workspace, cudaStream_t stream) {
-  const int G = a.Hq / a.c.Hkv;
-  const PrefillKv4 p{a, G, kM / G, (int)tile_cap(a, total_kv), static_cast<uint16_t *>(workspace)};
-  return a.c.D == 128 ? launch_prefill_t<128>(p, stream) : launch_prefill_t<64>(p, stream);
+cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, long long total_kv, void *workspace, int num_sms, cudaStream_t stream) {
+  const int G = a.Hq / a.c.Hkv, cap = (int)tile_cap(a, total_kv);
+  const size_t tiles = (size_t)cap * a.c.Hkv * 4 * kKv * a.c.D;
+  const PrefillKv4 p{a, G, kM / G, cap, reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + tiles),
+                     static_cast<uint16_t *>(workspace)};
+  return a.c.D == 128 ? launch_prefill_t<128>(p, num_sms, stream) : launch_prefill_t<64>(p, num_sms, stream);
 }
 
 }  // namespace gdn

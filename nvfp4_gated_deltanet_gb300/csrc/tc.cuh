@@ -64,6 +64,14 @@ GDN_DEV void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64
       : "memory");
 }
 
+GDN_DEV void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // ---------------------------------------------------------------- split TF32 on tcgen05
 // TF32 rounding of x (nearest, ties away from zero) on the bit pattern: add
 // half a unit of the 13 dropped bits to the magnitude, then clear them -- two
@@ -140,6 +148,8 @@ GDN_DEV void mma_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t ide
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same for BF16 A and B.
+__host__ __device__ constexpr uint32_t idesc_bf16(int n) { return idesc_f16(n) | (1u << 7) | (1u << 10); }
 // The same with the accumulate flag fixed at compile time, and with A (FP16
 // pairs, 8 columns per K = 16 step) in tensor memory. With descriptors that are
 // a base plus a constant these issue at the MMA's own rate (M = N = 128, K = 16:
@@ -207,4 +217,8 @@ GDN_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_
 // [box_rows][box_bytes], optionally with the 128-byte swizzle (host side).
 bool make_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
               uint32_t box_bytes, bool swizzle128);
+// 3-D BF16 tensor [rows][heads][d], rows row_stride elements apart, box
+// [box_rows][box_heads][64] with the 128-byte swizzle (host side).
+bool make_heads_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t heads, uint64_t d, uint64_t row_stride,
+                    uint32_t box_rows, uint32_t box_heads);
 }  // namespace gdn
