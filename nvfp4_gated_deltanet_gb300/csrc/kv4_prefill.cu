@@ -27,6 +27,13 @@
 //   warp 9            one thread streams K and V tiles by bulk copies and an
 //                     item's query rows by TMA (a box of tokens x the group's heads)
 //   warp 10           finds the next item
+// The softmax warps take over the others' registers (232 and 40 of 168 each), so
+// that a thread holds its row's 128 scores: with 168 they had to be read from
+// tensor memory twice, half at a time (two 4096-token chunks 284 against 272 us).
+// Measured: two chunks of 4096 and 789 tokens, 32 query heads on 8 of d = 128,
+// over 8100 and 2221 cached: 272 us, 1581 TFLOP/s, 0.83 of a large BF16 product.
+// What is left: a row tile's chain of softmax (1500 cycles), O += P V and S = Q K^T
+// (1024) takes longer than the tensor cores' 2048 for both tiles.
 // A row's weights are 2^(z - m + 6) with a maximum m that is only moved (and O
 // rescaled in tensor memory) when the row's true maximum passes it by 8: they
 // stay below 2^14, and normal FP16 numbers down to 2^-20 of the largest.
@@ -42,7 +49,7 @@ namespace {
 
 constexpr int kKv = 128;          // tokens of a K / V tile
 constexpr int kM = 128;           // rows of a query tile
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr float kShift = 6.0f;    // weights are 2^(z - m + 6)
 constexpr float kSlack = 8.0f;    // how far a row's maximum may pass m before m moves
 constexpr float kLog2e = 1.4426950408889634f;
@@ -301,7 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     return w.h >= 0;
   };
 
+  // registers: 384 threads x 168 at launch = 256 x 232 + 128 x 40
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ------------------------------------------------ softmax: thread = row r of row tile i
     const int i = warp >> 2, r = tid & 127;
     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -321,34 +330,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         if (!warp_wait_all(s_full + i, uses)) { ok = false; break; }
         tc_fence_after();
         const bool mask = j * kKv + kKv - 1 > sure;
-        // Half of the scores at a time (64 registers): the second half's weights
-        // take the place of its own scores, columns 96..127, and go to the MMAs
-        // while the first half is read again and its weights, columns 64..95, are made.
-        float s[64];
-        auto fetch = [&](int half) {
-          uint32_t raw[64];
-          tmem_ld32(tS + 64 * half, raw);
-          tmem_ld32(tS + 64 * half + 32, raw + 32);
+        // The second half's weights go to the MMAs (columns 96..127) while the first half's, columns 64..95, are made.
+        float s[128];
+        {
+          uint32_t raw[128];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, raw + 32 * q);
           tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 64; ++q) s[q] = __uint_as_float(raw[q]);
+          for (int q = 0; q < 128; ++q) s[q] = __uint_as_float(raw[q]);
           if (mask) {
 #pragma unroll
-            for (int q = 0; q < 64; ++q)
-              if (j * kKv + 64 * half + q > last) s[q] = -INFINITY;
+            for (int q = 0; q < 128; ++q)
+              if (j * kKv + q > last) s[q] = -INFINITY;
           }
-        };
-        float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto largest = [&]() {
+        }
+        float x4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int q = 0; q < 64; q += 4)
+        for (int q = 4; q < 128; q += 4)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
-        };
-        fetch(0);
-        largest();
-        fetch(1);
-        largest();
+          for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
         const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * cs;
         const bool up = top > m + kSlack;  // decided row by row: a row's result depends on no other row
         if (j == 0) {
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
           uint32_t x[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), cs2, off2);
+            float2 z = fma2(make_float2(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), cs2, off2);
             z.x = ex2(z.x);
             z.y = ex2(z.y);
             sum[e & 1] = add2(sum[e & 1], z);
@@ -387,7 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
           mbar_arrive(p_ready + 2 * i + half);
         };
         weigh(1);
-        fetch(0);
         weigh(0);
         sum[0] = add2(sum[0], sum[1]);
         l = sum[0].x + sum[0].y;
@@ -438,138 +438,141 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(item_free + (it & 1));
     }
-  } else if (warp == 8) {
-    // ------------------------------------------------ MMAs
-    constexpr uint32_t idS = idesc_bf16(kKv), idO = idesc_f16(D);
-    constexpr uint64_t kStep = S::kTileBytes / 16;  // from one stage or tile to the next, in a descriptor
-    const uint64_t qd = desc_sw128(smem_u32(qs)), kd = desc_sw128(smem_u32(kbuf)), vd = desc_sw128(smem_u32(vbuf));
-    const bool me = elect_one();
-    uint32_t kv = 0, uses[2] = {0, 0};  // K / V tiles taken, and each row tile's
-    Item w;
-    bool ok = true;
-    for (int it = 0; ok && take(it, w); ++it) {
-      const int nmax = max(w.nkv[0], w.nkv[1]);
-      if (me) {
-        auto scores = [&](int i, uint32_t use) {  // S_i = Q_i K^T
-          const uint64_t q = qd + i * kStep, kk = kd + (uint64_t)(use % NS) * kStep;
-          const uint32_t d = tmem + i * kKv;
-          mma_f16_ss_c<false>(d, q, kk, idS);
-#pragma unroll
-          for (int k = 1; k < D / 16; ++k)
-            mma_f16_ss_c<true>(d, q + (k / 4) * (kM * 128 / 16) + 2 * (k & 3), kk + (k / 4) * (kKv * 128 / 16) + 2 * (k & 3), idS);
-          tc_commit(s_full + i);
-        };
-        auto values = [&](int i, uint32_t use, bool first) {  // O_i += P_i V
-          const uint64_t v = vd + (uint64_t)(use % NS) * kStep;
-          const uint32_t d = tmem + S::kO + i * D, a = tmem + i * kKv + 64;
-          if (!(ok = wait(p_ready + 2 * i + 1, uses[i]))) return;  // tokens 64..127 first
-          tc_fence_after();
-          if (first) mma_f16_ts_c<false>(d, a + 32, v + D * 128 / 16, idO);
-          else mma_f16_ts_c<true>(d, a + 32, v + D * 128 / 16, idO);
-#pragma unroll
-          for (int k = 1; k < 4; ++k) mma_f16_ts_c<true>(d, a + 32 + 8 * k, v + D * 128 / 16 + 2 * k, idO);
-          if (!(ok = wait(p_ready + 2 * i, uses[i]))) return;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16_ts_c<true>(d, a + 8 * k, v + 2 * k, idO);
-          ++uses[i];
-        };
-        ok = wait(q_full, it);
-        if (ok && nmax > 0 && (ok = wait(k_full + kv % NS, kv / NS))) {
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (w.nkv[i] > 0) scores(i, kv);
-          tc_commit(k_free + kv % NS);
-        }
-        if (ok && nmax <= 1) tc_commit(q_free);
-        for (int j = 0; j < nmax && ok; ++j) {
-          const uint32_t u = kv + j;
-          ok = wait(v_full + u % NS, u / NS) && (j + 1 >= nmax || wait(k_full + (u + 1) % NS, (u + 1) / NS));
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!ok || j >= w.nkv[i]) continue;
-            values(i, u, j == 0);
-            if (!ok) break;
-            if (j + 1 < w.nkv[i]) scores(i, u + 1);
-            else tc_commit(o_done + i);
-          }
-          if (!ok) break;
-          tc_commit(v_free + u % NS);
-          if (j + 1 < nmax) tc_commit(k_free + (u + 1) % NS);
-          if (j + 2 == nmax) tc_commit(q_free);  // the item's last scores are issued
-        }
-      }
-      ok = __any_sync(0xffffffffu, me && ok);
-      kv += nmax;
-    }
-    // every MMA issued has completed before the CTA may leave
-    if (me) {
-      tc_commit(fin);
-      mbar_wait(fin, 0u);
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------ query rows, K and V tiles
-    const int q_bytes = p.tpt * p.G * D * 2;  // of a row tile
-    uint32_t u = 0, taken = 0;  // K / V tiles, items
-    Item w;
-    bool ok = true;
-    for (int it = 0; ok && take(it, w); ++it) {
-      const int nmax = max(w.nkv[0], w.nkv[1]);
-      if (lane == 0 && it > 0) ok = wait(q_free, it - 1);
-      if (lane == 0 && ok) {
-        mbar_arrive_expect_tx(q_full, 2 * q_bytes);
-        ++taken;
-#pragma unroll
-        for (int x = 0; x < 2 * (D / 64); ++x)
-          tma_load_3d(qs + (x / (D / 64)) * S::kTileBytes + (x % (D / 64)) * (kM * 128), &tmQ, x % (D / 64) * 64, w.h * p.G,
-                      w.q0 + w.t0 + x / (D / 64) * p.tpt, q_full);
-        if (it == 0) pdl_wait();  // the expansion has finished
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(p.tiles) + ((size_t)w.tile0 * c.Hkv + w.h) * (2 * S::kTileBytes);
-        const size_t step = (size_t)c.Hkv * 2 * S::kTileBytes;
-        for (int j = 0; j < nmax; ++j, ++u) {
-          const int s = u % NS;
-          if (u >= NS && !(ok = wait(k_free + s, u / NS - 1))) break;
-          mbar_arrive_expect_tx(k_full + s, S::kTileBytes);
-          bulk_g2s(kbuf + s * S::kTileBytes, src + j * step, S::kTileBytes, k_full + s);
-          if (u >= NS && !(ok = wait(v_free + s, u / NS - 1))) {
-            mbar_wait(k_full + s, (u / NS) & 1u);
-            break;
-          }
-          mbar_arrive_expect_tx(v_full + s, S::kTileBytes);
-          bulk_g2s(vbuf + s * S::kTileBytes, src + j * step + S::kTileBytes, S::kTileBytes, v_full + s);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-    }
-    if (lane == 0 && u == 0) pdl_wait();
-    if (lane == 0 && *abort_flag) {  // the copies in flight land (or a bounded wait for each ends) before the CTA leaves
-      if (taken > 0) mbar_wait(q_full, (taken - 1) & 1u);
-      for (uint32_t x = u < NS ? 0 : u - NS; x < u; ++x) {
-        mbar_wait(k_full + x % NS, (x / NS) & 1u);
-        mbar_wait(v_full + x % NS, (x / NS) & 1u);
-      }
-    }
   } else {
-    // ------------------------------------------------ the next item
-    for (int it = 0;; ++it) {
-      if (it == 1) pdl_wait();  // the counter is zeroed by the expansion
-      int x = blockIdx.x;
-      if (it > 0) {
-        if (lane == 0) x = (int)gridDim.x + atomicAdd(p.next, 1);
-        x = __shfl_sync(0xffffffffu, x, 0);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 8) {
+      // ------------------------------------------------ MMAs
+      constexpr uint32_t idS = idesc_bf16(kKv), idO = idesc_f16(D);
+      constexpr uint64_t kStep = S::kTileBytes / 16;  // from one stage or tile to the next, in a descriptor
+      const uint64_t qd = desc_sw128(smem_u32(qs)), kd = desc_sw128(smem_u32(kbuf)), vd = desc_sw128(smem_u32(vbuf));
+      const bool me = elect_one();
+      uint32_t kv = 0, uses[2] = {0, 0};  // K / V tiles taken, and each row tile's
+      Item w;
+      bool ok = true;
+      for (int it = 0; ok && take(it, w); ++it) {
+        const int nmax = max(w.nkv[0], w.nkv[1]);
+        if (me) {
+          auto scores = [&](int i, uint32_t use) {  // S_i = Q_i K^T
+            const uint64_t q = qd + i * kStep, kk = kd + (uint64_t)(use % NS) * kStep;
+            const uint32_t d = tmem + i * kKv;
+            mma_f16_ss_c<false>(d, q, kk, idS);
+  #pragma unroll
+            for (int k = 1; k < D / 16; ++k)
+              mma_f16_ss_c<true>(d, q + (k / 4) * (kM * 128 / 16) + 2 * (k & 3), kk + (k / 4) * (kKv * 128 / 16) + 2 * (k & 3), idS);
+            tc_commit(s_full + i);
+          };
+          auto values = [&](int i, uint32_t use, bool first) {  // O_i += P_i V
+            const uint64_t v = vd + (uint64_t)(use % NS) * kStep;
+            const uint32_t d = tmem + S::kO + i * D, a = tmem + i * kKv + 64;
+            if (!(ok = wait(p_ready + 2 * i + 1, uses[i]))) return;  // tokens 64..127 first
+            tc_fence_after();
+            if (first) mma_f16_ts_c<false>(d, a + 32, v + D * 128 / 16, idO);
+            else mma_f16_ts_c<true>(d, a + 32, v + D * 128 / 16, idO);
+  #pragma unroll
+            for (int k = 1; k < 4; ++k) mma_f16_ts_c<true>(d, a + 32 + 8 * k, v + D * 128 / 16 + 2 * k, idO);
+            if (!(ok = wait(p_ready + 2 * i, uses[i]))) return;
+            tc_fence_after();
+  #pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ts_c<true>(d, a + 8 * k, v + 2 * k, idO);
+            ++uses[i];
+          };
+          ok = wait(q_full, it);
+          if (ok && nmax > 0 && (ok = wait(k_full + kv % NS, kv / NS))) {
+            tc_fence_after();
+  #pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (w.nkv[i] > 0) scores(i, kv);
+            tc_commit(k_free + kv % NS);
+          }
+          if (ok && nmax <= 1) tc_commit(q_free);
+          for (int j = 0; j < nmax && ok; ++j) {
+            const uint32_t u = kv + j;
+            ok = wait(v_full + u % NS, u / NS) && (j + 1 >= nmax || wait(k_full + (u + 1) % NS, (u + 1) / NS));
+  #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!ok || j >= w.nkv[i]) continue;
+              values(i, u, j == 0);
+              if (!ok) break;
+              if (j + 1 < w.nkv[i]) scores(i, u + 1);
+              else tc_commit(o_done + i);
+            }
+            if (!ok) break;
+            tc_commit(v_free + u % NS);
+            if (j + 1 < nmax) tc_commit(k_free + (u + 1) % NS);
+            if (j + 2 == nmax) tc_commit(q_free);  // the item's last scores are issued
+          }
+        }
+        ok = __any_sync(0xffffffffu, me && ok);
+        kv += nmax;
       }
-      Item w{-1, 0, 0, 0, 0, {0, 0}, 0};
-      if (find_work(p, x / c.Hkv, lane, w)) w.h = x % c.Hkv;
-      if (it >= 2 && !warp_wait_all(item_free + (it & 1), (it >> 1) - 1)) break;
-      if (lane == 0) {
-        items[it & 1] = w;
-        mbar_arrive(item_full + (it & 1));
+      // every MMA issued has completed before the CTA may leave
+      if (me) {
+        tc_commit(fin);
+        mbar_wait(fin, 0u);
       }
-      __syncwarp();
-      if (w.h < 0) break;
+    } else if (warp == 9) {
+      // ------------------------------------------------ query rows, K and V tiles
+      const int q_bytes = p.tpt * p.G * D * 2;  // of a row tile
+      uint32_t u = 0, taken = 0;  // K / V tiles, items
+      Item w;
+      bool ok = true;
+      for (int it = 0; ok && take(it, w); ++it) {
+        const int nmax = max(w.nkv[0], w.nkv[1]);
+        if (lane == 0 && it > 0) ok = wait(q_free, it - 1);
+        if (lane == 0 && ok) {
+          mbar_arrive_expect_tx(q_full, 2 * q_bytes);
+          ++taken;
+  #pragma unroll
+          for (int x = 0; x < 2 * (D / 64); ++x)
+            tma_load_3d(qs + (x / (D / 64)) * S::kTileBytes + (x % (D / 64)) * (kM * 128), &tmQ, x % (D / 64) * 64, w.h * p.G,
+                        w.q0 + w.t0 + x / (D / 64) * p.tpt, q_full);
+          if (it == 0) pdl_wait();  // the expansion has finished
+          const uint8_t *src = reinterpret_cast<const uint8_t *>(p.tiles) + ((size_t)w.tile0 * c.Hkv + w.h) * (2 * S::kTileBytes);
+          const size_t step = (size_t)c.Hkv * 2 * S::kTileBytes;
+          for (int j = 0; j < nmax; ++j, ++u) {
+            const int s = u % NS;
+            if (u >= NS && !(ok = wait(k_free + s, u / NS - 1))) break;
+            mbar_arrive_expect_tx(k_full + s, S::kTileBytes);
+            bulk_g2s(kbuf + s * S::kTileBytes, src + j * step, S::kTileBytes, k_full + s);
+            if (u >= NS && !(ok = wait(v_free + s, u / NS - 1))) {
+              mbar_wait(k_full + s, (u / NS) & 1u);
+              break;
+            }
+            mbar_arrive_expect_tx(v_full + s, S::kTileBytes);
+            bulk_g2s(vbuf + s * S::kTileBytes, src + j * step + S::kTileBytes, S::kTileBytes, v_full + s);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      }
+      if (lane == 0 && u == 0) pdl_wait();
+      if (lane == 0 && *abort_flag) {  // the copies in flight land (or a bounded wait for each ends) before the CTA leaves
+        if (taken > 0) mbar_wait(q_full, (taken - 1) & 1u);
+        for (uint32_t x = u < NS ? 0 : u - NS; x < u; ++x) {
+          mbar_wait(k_full + x % NS, (x / NS) & 1u);
+          mbar_wait(v_full + x % NS, (x / NS) & 1u);
+        }
+      }
+    } else if (warp == 10) {
+      // ------------------------------------------------ the next item
+      for (int it = 0;; ++it) {
+        if (it == 1) pdl_wait();  // the counter is zeroed by the expansion
+        int x = blockIdx.x;
+        if (it > 0) {
+          if (lane == 0) x = (int)gridDim.x + atomicAdd(p.next, 1);
+          x = __shfl_sync(0xffffffffu, x, 0);
+        }
+        Item w{-1, 0, 0, 0, 0, {0, 0}, 0};
+        if (find_work(p, x / c.Hkv, lane, w)) w.h = x % c.Hkv;
+        if (it >= 2 && !warp_wait_all(item_free + (it & 1), (it >> 1) - 1)) break;
+        if (lane == 0) {
+          items[it & 1] = w;
+          mbar_arrive(item_full + (it & 1));
+        }
+        __syncwarp();
+        if (w.h < 0) break;
+      }
+      pdl_wait();  // on every path: this grid must not end before the one it follows
     }
-    pdl_wait();  // on every path: this grid must not end before the one it follows
   }
   tc_fence_before();
   __syncthreads();
