@@ -166,6 +166,26 @@ GDN_DEV long long find_tile(const Kv4Args &c, long long u, int HR, int extra, in
   }
   return tiles * HR;  // past the end
 }
+// The runs: N of them, cut k at cost floor(units k / N).
+struct Cuts {
+  int N, rest, n0;
+  long long tiles, q;
+  GDN_DEV long long at(int k) const { return q * k + rest * k / N; }
+};
+template <int TILE>
+GDN_DEV Cuts find_cuts(const DecodeArgs &p, int warps, int HR, int lane, int most) {
+  const Kv4Args &c = p.a.c;
+  Cuts k;
+  k.n0 = lane_tiles<TILE>(c, 0, lane);
+  long long tiles = warp_isum(k.n0);
+  for (int b0 = 32; b0 < c.B; b0 += 32) tiles += warp_isum(lane_tiles<TILE>(c, b0, lane));
+  const long long units = (tiles + (long long)c.B * p.extra) * HR;
+  k.tiles = tiles * HR;
+  k.N = runs(k.tiles, warps, most);
+  k.q = quot(units, k.N);
+  k.rest = (int)(units - k.q * k.N);
+  return k;
+}
 // Run `run` of at most `most`: its first tile and how many tiles it has.
 template <int TILE>
 GDN_DEV int find_run(const DecodeArgs &p, int warps, int HR, int lane, int run, int most, Cursor &k) {
@@ -182,19 +202,11 @@ GDN_DEV int find_run(const DecodeArgs &p, int warps, int HR, int lane, int run, 
     }
     return n;
   }
-  const int n0 = lane_tiles<TILE>(c, 0, lane);
-  long long tiles = warp_isum(n0);
-  for (int b0 = 32; b0 < c.B; b0 += 32) tiles += warp_isum(lane_tiles<TILE>(c, b0, lane));
-  const long long units = (tiles + (long long)c.B * p.extra) * HR;
-  const int N = runs(tiles * HR, warps, most);
-  if (run >= N) return 0;
-  // cut k lies at floor(units k / N)
-  const long long q = quot(units, N);
-  const int rest = (int)(units - q * N);
+  const Cuts x = find_cuts<TILE>(p, warps, HR, lane, most);
+  if (run >= x.N) return 0;
   Cursor end;
-  const long long t1 = run + 1 == N ? tiles * HR
-                                    : find_tile<TILE>(c, q * (run + 1) + rest * (run + 1) / N, HR, p.extra, lane, n0, end);
-  return (int)(t1 - find_tile<TILE>(c, q * run + rest * run / N, HR, p.extra, lane, n0, k));
+  const long long t1 = run + 1 == x.N ? x.tiles : find_tile<TILE>(c, x.at(run + 1), HR, p.extra, lane, x.n0, end);
+  return (int)(t1 - find_tile<TILE>(c, x.at(run), HR, p.extra, lane, x.n0, k));
 }
 
 GDN_DEV uint32_t transpose8x8(uint32_t x) {
@@ -245,7 +257,32 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   }
   __syncthreads();
   Cursor cur;
-  const int n_tiles = find_run<TILE>(p, W, HR, lane, run, gridDim.x * S::kTeams, cur);
+  int n_tiles;
+  {  // the team's first warp finds its run for all (16 warps at once took 2 us of the issue slots)
+    struct Found {
+      Cursor k;
+      int n;
+    };
+    volatile Found *found = reinterpret_cast<volatile Found *>(meet);
+    if (warp == 0) {
+      n_tiles = find_run<TILE>(p, W, HR, lane, run, gridDim.x * S::kTeams, cur);
+      if (lane == 0) {
+        found->k.b = cur.b;
+        found->k.hr = cur.hr;
+        found->k.tile = cur.tile;
+        found->k.nt = cur.nt;
+        found->k.len = cur.len;
+        found->n = n_tiles;
+      }
+    }
+    team_sync();
+    cur.b = found->k.b;
+    cur.hr = found->k.hr;
+    cur.tile = found->k.tile;
+    cur.nt = found->k.nt;
+    cur.len = found->k.len;
+    n_tiles = found->n;
+  }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < c.B; b += S::kThreads)
       if (c.kv_len[b] != seq_len(c, b)) flag_status(c.status, GDN_E_RANGE);
@@ -616,8 +653,11 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   }
 }
 
-// The items that lie in several runs: one CTA per query row, its warps taking
-// every eighth piece. most: runs at most, as in the decode kernel.
+// The items that lie in several runs: their pieces are joined in order, by the
+// CTA of the first cut inside an item, or with whole-CTA teams (fewer items than
+// cuts, more pieces) by a CTA per item and row.
+// Few pieces: a warp per row. More: the CTA's warps take every eighth piece of a
+// row. most: runs at most, as in the decode kernel.
 template <int D, int NQ, int TEAM>
 __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
   using S = DecodeShape<D, NQ, TEAM>;
@@ -626,76 +666,116 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
   const Kv4Args &c = p.a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HR = c.Hkv * p.RG, R = p.r * p.G;
-  const int row_id = blockIdx.x % R, bh = blockIdx.x / R, b = bh / c.Hkv, h = bh % c.Hkv;
-  const int hr = h * p.RG + row_id / S::kRows, row = row_id % S::kRows;
-  long long tiles = 0, before = 0;
-  for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const int n = lane_tiles<S::kTile>(c, b0, lane);
-    tiles += warp_isum(n);
-    before += warp_isum(b0 + lane < b ? n : 0);
+  const Cuts x = find_cuts<S::kTile>(p, S::kTeam, HR, lane, most);
+  Cursor k{0, 0, 0, 0, 0};
+  int cut;           // the first cut inside the item
+  bool mine;
+  long long a0 = 0;  // the item's cost begins here; its tile t lies at a0 + extra + t
+  if (TEAM) {        // more items than cuts: a CTA per cut
+    cut = blockIdx.x + 1;
+    mine = cut < x.N;
+    if (mine) {
+      find_tile<S::kTile>(c, x.at(cut), HR, p.extra, lane, x.n0, k);
+      a0 = x.at(cut) - k.tile - p.extra;
+      mine = k.tile > 0 && x.at(cut - 1) <= a0 + p.extra;
+    }
+  } else {           // a CTA per item (and row)
+    seek<S::kTile>(c, k, blockIdx.x / HR);
+    k.hr = blockIdx.x % HR;
+    long long before = 0;
+    for (int b0 = 0; b0 < k.b; b0 += 32)
+      before += warp_isum(b0 + lane < k.b ? (b0 ? lane_tiles<S::kTile>(c, b0, lane) : x.n0) : 0);
+    a0 = (before + (long long)k.b * p.extra) * HR + (long long)k.hr * (k.nt + p.extra);
+    cut = (int)quot((a0 + p.extra + 1) * x.N - 1, x.q * x.N + x.rest) + 1;
+    mine = cut < x.N && x.at(cut) < a0 + p.extra + k.nt;
   }
-  const int nt = tiles_of<S::kTile>(seq_len(c, b)), N = runs(tiles * HR, S::kTeam, most);
-  const long long units = (tiles + (long long)c.B * p.extra) * HR;
-  const long long a0 = (before + (long long)b * p.extra) * HR + (long long)hr * (nt + p.extra);
-  // the runs that hold the item's first and last tile (its tile t lies at cost a0 + extra + t)
-  const int c0 = (int)quot((a0 + p.extra + 1) * N - 1, units), c1 = (int)quot((a0 + p.extra + nt) * N - 1, units);
   pdl_wait();  // on every path: this grid must not end before the one it follows
-  if (c0 == c1) return;
-  float m = -INFINITY, l = 0.0f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  if (!mine) return;
+  // pieces: runs cut - 1 (where the item may be its first segment, or its last) to the one of its last tile
+  const int np = (int)quot((a0 + p.extra + k.nt) * x.N - 1, x.q * x.N + x.rest) - cut + 2;
+  const bool first = x.at(cut - 1) >= a0;
+  const int h = k.hr / p.RG, row0 = (k.hr % p.RG) * S::kRows, rows = min(S::kRows, R - row0);
   const float *ml = p.part + 2 * (size_t)most * S::kRows * D;
-  // run c0 may hold earlier items before this one: then it is not its first segment; the others start inside it
-  const bool c0_first = quot(units * c0, N) >= a0;
-  for (int k0 = c0 + warp; k0 <= c1; k0 += 8 * 4) {
-    float2 x[4];
-    float y[4][E];
+  auto piece = [&](int j, int row) { return (2 * (size_t)(cut - 1 + j) + (j > 0 || first ? 0 : 1)) * S::kRows + row; };
+  float m, l, o[E];
+  auto begin = [&]() {
+    m = -INFINITY;
+    l = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // four pieces in flight
-      const int k = k0 + 8 * j;
-      const size_t piece = 2 * (size_t)k + (k > c0 || c0_first ? 0 : 1);
-      x[j] = make_float2(-INFINITY, 0.0f);
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  };
+  auto add = [&](int row, int j0, int step) {  // pieces j0, j0 + step, ...: four in flight
+    for (; j0 < np; j0 += 4 * step) {
+      float2 v[4];
+      float y[4][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[j][e] = 0.0f;
-      if (k <= c1) {
-        x[j] = *reinterpret_cast<const float2 *>(ml + (piece * S::kRows + row) * 2);
-        const float *op = p.part + (piece * S::kRows + row) * D + lane * E;
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + u * step;
+        v[u] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[j][e] = op[e];
+        for (int e = 0; e < E; ++e) y[u][e] = 0.0f;
+        if (j < np) {
+          v[u] = *reinterpret_cast<const float2 *>(ml + piece(j, row) * 2);
+          const float *op = p.part + piece(j, row) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[u][e] = op[e];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float mn = fmaxf(m, v[u].x), safe = mn == -INFINITY ? 0.0f : mn;
+        const float f = ex2(m - safe), fx = ex2(v[u].x - safe);
+        l = l * f + v[u].y * fx;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = o[e] * f + y[u][e] * fx;
+        m = mn;
       }
     }
+  };
+  auto out_row = [&](int row) {
+    const int ri = row0 + row;
+    return ((long long)k.b * p.r + ri / p.G) * p.a.Hq + h * p.G + ri % p.G;
+  };
+  if (np <= 8) {
+    for (int row = blockIdx.y + gridDim.y * warp; row < rows; row += gridDim.y * 8) {
+      begin();
+      add(row, 0, 1);
+      const float inv = l == 0.0f ? 0.0f : c.vs / l;
+      uint16_t *dst = p.a.out + out_row(row) * D + lane * E;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float mn = fmaxf(m, x[j].x), safe = mn == -INFINITY ? 0.0f : mn;
-      const float f = ex2(m - safe), fx = ex2(x[j].x - safe);
-      l = l * f + x[j].y * fx;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + y[j][e] * fx;
-      m = mn;
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t *>(dst + e) =
+            f32_to_bf16_bits(o[e] * inv) | (uint32_t)f32_to_bf16_bits(o[e + 1] * inv) << 16;
+      if (p.a.lse && lane == 0) p.a.lse[out_row(row)] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
     }
+    return;
   }
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    begin();
+    add(row, warp, 8);
 #pragma unroll
-  for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    sh[warp][D] = m;
-    sh[warp][D + 1] = l;
-  }
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, sh[w][D]);
-    const float safe = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float f = ex2(sh[w][D] - safe);
-      sum += sh[w][D + 1] * f;
-      v += sh[w][threadIdx.x] * f;
+    for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = o[e];
+    if (lane == 0) {
+      sh[warp][D] = m;
+      sh[warp][D + 1] = l;
     }
-    const long long out = ((long long)b * p.r + row_id / p.G) * p.a.Hq + h * p.G + row_id % p.G;
-    p.a.out[out * D + threadIdx.x] = f32_to_bf16_bits(sum == 0.0f ? 0.0f : v * (c.vs / sum));
-    if (p.a.lse && threadIdx.x == 0) p.a.lse[out] = (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) top = fmaxf(top, sh[w][D]);
+      const float safe = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f, v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float f = ex2(sh[w][D] - safe);
+        sum += sh[w][D + 1] * f;
+        v += sh[w][threadIdx.x] * f;
+      }
+      p.a.out[out_row(row) * D + threadIdx.x] = f32_to_bf16_bits(sum == 0.0f ? 0.0f : v * (c.vs / sum));
+      if (p.a.lse && threadIdx.x == 0) p.a.lse[out_row(row)] = (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
@@ -708,7 +788,10 @@ cudaError_t launch_decode_t(const DecodeArgs &p, int ctas, cudaStream_t stream) 
   kv4_decode_kernel<D, NQ, TEAM><<<ctas, S::kThreads, S::kBytes, stream>>>(p);
   if (p.extra == kWhole) return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.a.c.B * p.a.Hq * p.r), 1, 1);
+  const int most = ctas * S::kTeams;  // runs, and cuts but one
+  if (most < 2) return cudaGetLastError();
+  cfg.gridDim = TEAM ? dim3((unsigned)most - 1, 1, 1)
+                     : dim3((unsigned)(p.a.c.B * p.a.c.Hkv * p.RG), S::kRows < p.r * p.G ? S::kRows : p.r * p.G, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -716,7 +799,7 @@ cudaError_t launch_decode_t(const DecodeArgs &p, int ctas, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NQ, TEAM>, p, ctas * S::kTeams);
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NQ, TEAM>, p, most);
 }
 
 // Query rows per (sequence, KV head) -> 8-row column blocks of one item.
