@@ -6,155 +6,225 @@ namespace gdn {
 
 namespace {
 
-// New rows into their pages, or back. One CTA per 16-token group that the new
-// rows touch and a few heads: its threads take one 16-element block of one token
-// each (append: 32 bytes in, 8 code bytes out). The group's scales are gathered in
-// shared memory and leave as 16-byte words where all of its tokens are new: a V
-// scale is a byte 16 bytes from its neighbours in the token, and single bytes of
-// 16 tokens cost more memory transactions than all the codes.
-// Bound by the bytes: 4 d per token-head and K or V read or written in BF16, 9/16 d in 4 bits.
-constexpr int kHeads = 8;  // of a CTA, at most
+// New rows into their pages, or back: one CTA per 16-token group that the new
+// rows touch and up to four heads (fewer where that leaves SMs idle). Bound by
+// the bytes: per token, head and K or V, 2 d in BF16 and 9/16 d in 4 bits.
+constexpr int kHeads = 4;
 
 struct RowsArgs {
   Kv4Args a;
   uint16_t *k, *v;
   long long k_stride, v_stride;
   int heads;  // of a CTA
+  int items;  // append: (group, chunk of heads) pairs at most
 };
+// A group's new tokens [t0, t1) of sequence b (-1: none); token t is row n0 + t.
+struct Group {
+  int b, pos0, t0, t1;
+  long long n0;
+};
+// The x-th group that new rows touch. One warp.
+GDN_DEV Group find_group(const Kv4Args &a, int x, int lane) {
+  Group r{-1, 0, 0, 0, 0};
+  int base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    Kv4Seq s{0, 0, 0};
+    int n = 0, lo = 0;
+    if (b0 + lane < a.B) {
+      s = kv4_seq(a, b0 + lane);
+      lo = max(0, s.len - (s.q1 - s.q0));  // the first new token
+      n = s.q1 > s.q0 && s.len > lo ? ((s.len - 1) >> 4) - (lo >> 4) + 1 : 0;
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, base + incl > x);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const int pos0 = ((lo >> 4) + x - (base + incl - n)) * 16;
+      r.b = b0 + l;
+      r.pos0 = __shfl_sync(0xffffffffu, pos0, l);
+      r.t0 = __shfl_sync(0xffffffffu, max(0, lo - pos0), l);
+      r.t1 = __shfl_sync(0xffffffffu, min(16, s.len - pos0), l);
+      r.n0 = __shfl_sync(0xffffffffu, s.q1 - s.len + pos0, l);
+      return r;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
 
-template <int D, bool READ>
-__global__ void __launch_bounds__(256) kv4_rows_kernel(RowsArgs p) {
+// Append. A CTA goes through its groups with two buffers: while it quantises one
+// group, a thread per 16-element block, the next one's rows come to shared memory
+// (a token's heads lie together: one bulk copy per token, 32 KB a buffer, three
+// CTAs an SM). Its warps find eight groups at once, one each: finding them one by
+// one, a chain of three loads, took longer than the group itself. The scales are gathered in
+// shared memory and leave as 16-byte words where all of the group's tokens are
+// new: a V scale is a byte 16 bytes from its token's next one, and single bytes
+// cost more memory transactions than all the codes.
+template <int D>
+struct AppendSmem {
+  uint16_t rows[2][2][16][kHeads * D];  // [buffer][K, V][token]
+  uint8_t scales[kHeads * 2 * D];
+  Group found[8];
+  uint8_t *place[8];
+  uint64_t landed[2];
+};
+template <int D>
+__global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
   constexpr int NB = D / 16, ITEMS = 2 * 16 * NB;  // of a head: K and V blocks of 16 tokens
-  constexpr int U = 2;
-  __shared__ int sb, sgroup;
-  __shared__ __align__(16) uint8_t scales[kHeads * 2 * D];
+  extern __shared__ __align__(128) unsigned char raw[];
+  AppendSmem<D> &sm = *reinterpret_cast<AppendSmem<D> *>(raw);
   const Kv4Args &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < 32) {  // the sequence and its group: the blockIdx.x-th that new rows touch
-    int base = 0, found = -1, group = 0;
-    for (int b0 = 0; b0 < a.B && found < 0; b0 += 32) {
-      int n = 0, g0 = 0;
-      if (b0 + lane < a.B) {
-        const Kv4Seq s = kv4_seq(a, b0 + lane);
-        const int lo = max(0, s.len - (s.q1 - s.q0));
-        g0 = lo >> 4;
-        n = s.q1 > s.q0 && s.len > lo ? ((s.len - 1) >> 4) - g0 + 1 : 0;
-      }
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, base + incl > (int)blockIdx.x);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        found = b0 + l;
-        group = __shfl_sync(0xffffffffu, g0 - (base + incl - n), l) + (int)blockIdx.x;
-      }
-      base += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) {
-      sb = found;
-      sgroup = group;
-    }
+  const int chunks = (a.Hkv + p.heads - 1) / p.heads;  // an item: a group, and a chunk of its heads
+  if (tid == 0) {
+    mbar_init(&sm.landed[0], 1);
+    mbar_init(&sm.landed[1], 1);
+    fence_barrier_init();
   }
-  __syncthreads();
-  const int b = sb;
-  if (b < 0) return;
-  const Kv4Seq s = kv4_seq(a, b);
-  const int first = s.len - (s.q1 - s.q0), pos0 = sgroup * 16;  // the first new token; the group's
-  const int t0 = max(0, max(first, 0) - pos0), t1 = min(16, s.len - pos0);  // the group's new tokens
-  uint8_t *g = kv4_group<D>(a, b, pos0);
-  if (!g) return;
-  const int h0 = blockIdx.y * p.heads, hn = min(p.heads, a.Hkv - h0);
+  auto fetch = [&](int item, int k, int buf) {  // warp 0: the rows of found[k]
+    const Group r = sm.found[k];
+    if (r.b < 0) return;
+    const int h0 = item % chunks * p.heads, hn = min(p.heads, a.Hkv - h0);
+    if (lane == 0) mbar_arrive_expect_tx(&sm.landed[buf], 2 * (r.t1 - r.t0) * hn * D * 2);
+    __syncwarp();
+    const int t = lane & 15;
+    if (t >= r.t0 && t < r.t1)
+      bulk_g2s(sm.rows[buf][lane >> 4][t],
+               (lane < 16 ? p.k + (r.n0 + t) * p.k_stride : p.v + (r.n0 + t) * p.v_stride) + h0 * D, hn * D * 2,
+               &sm.landed[buf]);
+  };
   const size_t head = kv4_head_bytes<D>(a);
   const float invk = inv6ts_of(a.ks), invv = inv6ts_of(a.vs);
-  for (int i0 = tid; i0 < hn * ITEMS; i0 += 256 * U) {
-    uint4 x[U][2];
-    uint2 code[U];
-    uint8_t sc[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + 256 * u, blk = i % NB, t = i / NB % 16, is_v = i / (16 * NB) & 1, h = i / ITEMS;
-      if (i >= hn * ITEMS || t < t0 || t >= t1) continue;
-      if (READ) {
-        const uint8_t *q = g + (h0 + h) * head;
-        code[u] = *reinterpret_cast<const uint2 *>(q + (is_v ? kv4_v_code<D>(t, blk * 8) : kv4_k_code<D>(t, blk * 8)));
-        sc[u] = q[is_v ? kv4_v_scale<D>(t, blk) : kv4_k_scale<D>(t, blk)];
-      } else {
-        const long long n = s.q0 + (pos0 + t - first);
-        const uint4 *row = reinterpret_cast<const uint4 *>((is_v ? p.v + n * p.v_stride : p.k + n * p.k_stride) +
-                                                           (h0 + h) * D + blk * 16);
-        x[u][0] = row[0];
-        x[u][1] = row[1];
+  uint32_t turns = 0;  // bit `buf`: parity of the buffer's next use
+  for (int item = blockIdx.x, n = 0;; item += gridDim.x, ++n) {
+    const int k = n & 7, buf = n & 1;
+    __syncthreads();  // the other buffer, the scales and the last found group have been read
+    if (k == 0) {
+      const long long mine = item + (long long)(tid >> 5) * gridDim.x;
+      const Group r = mine < p.items ? find_group(a, (int)(mine / chunks), lane) : Group{-1, 0, 0, 0, 0};
+      if (lane == 0) {
+        sm.found[tid >> 5] = r;
+        sm.place[tid >> 5] = r.b >= 0 ? kv4_group<D>(a, r.b, r.pos0) : nullptr;
       }
+      __syncthreads();
+      if (tid < 32) fetch(item, 0, buf);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + 256 * u, blk = i % NB, t = i / NB % 16, is_v = i / (16 * NB) & 1, h = i / ITEMS;
-      if (i >= hn * ITEMS || t < t0 || t >= t1) continue;
-      const float ts = is_v ? a.vs : a.ks;
-      if (READ) {
-        __half2 e[8];
-        e2m1x8_to_h2x4(code[u].x, *reinterpret_cast<__half2(*)[4]>(&e[0]));
-        e2m1x8_to_h2x4(code[u].y, *reinterpret_cast<__half2(*)[4]>(&e[4]));
-        const float f = e4m3_to_f32(sc[u]);
-        uint32_t o[8];
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          const float2 y = __half22float2(e[m]);  // e2m1 x e4m3 is exact; one FP32 rounding by ts, one to BF16
-          o[m] = f32_to_bf16_bits(y.x * f * ts) | (uint32_t)f32_to_bf16_bits(y.y * f * ts) << 16;
-        }
-        const long long n = s.q0 + (pos0 + t - first);
-        uint4 *row = reinterpret_cast<uint4 *>((is_v ? p.v + n * p.v_stride : p.k + n * p.k_stride) + (h0 + h) * D + blk * 16);
-        row[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        row[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      } else {
-        float y[16];
-        const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          y[2 * m] = __uint_as_float(w[m] << 16);
-          y[2 * m + 1] = __uint_as_float(w[m] & 0xFFFF0000u);
-        }
+    const Group r = sm.found[k];
+    if (r.b < 0) break;  // items are in order: none follows
+    if (tid < 32 && k < 7) fetch(item + gridDim.x, k + 1, buf ^ 1);
+    const bool ok = mbar_wait(&sm.landed[buf], turns >> buf & 1u);
+    turns ^= 1u << buf;
+    if (!ok) flag_status(a.status, GDN_E_TIMEOUT);
+    const int h0 = item % chunks * p.heads, hn = min(p.heads, a.Hkv - h0);
+    uint8_t *g = sm.place[k];  // null: a bad page, flagged
+    if (g && ok) {
+      g += h0 * head;
+      for (int i = tid; i < hn * ITEMS; i += 256) {
+        const int blk = i % NB, t = i / NB % 16, is_v = i / (16 * NB) & 1, h = i / ITEMS;
+        if (t < r.t0 || t >= r.t1) continue;
+        float x[16];
+        load_bf16x16(&sm.rows[buf][is_v][t][h * D + blk * 16], x);
         uint32_t lo, hi, scale;
-        if (!quant_block16(y, ts, is_v ? invv : invk, lo, hi, scale)) flag_status(a.status, GDN_E_NONFINITE);
-        *reinterpret_cast<uint2 *>(g + (h0 + h) * head + (is_v ? kv4_v_code<D>(t, blk * 8) : kv4_k_code<D>(t, blk * 8))) =
+        if (!quant_block16(x, is_v ? a.vs : a.ks, is_v ? invv : invk, lo, hi, scale)) flag_status(a.status, GDN_E_NONFINITE);
+        *reinterpret_cast<uint2 *>(g + h * head + (is_v ? kv4_v_code<D>(t, blk * 8) : kv4_k_code<D>(t, blk * 8))) =
             make_uint2(lo, hi);
-        scales[h * 2 * D + (is_v ? kv4_v_scale<D>(t, blk) : kv4_k_scale<D>(t, blk)) - 16 * D] = (uint8_t)scale;
+        sm.scales[h * 2 * D + (is_v ? kv4_v_scale<D>(t, blk) : kv4_k_scale<D>(t, blk)) - 16 * D] = (uint8_t)scale;
       }
     }
-  }
-  if (READ) return;
-  __syncthreads();
-  if (t0 == 0 && t1 == 16) {
-    for (int i = tid; i < hn * (2 * D / 16); i += 256) {
-      const int h = i / (2 * D / 16), w = i % (2 * D / 16);
-      reinterpret_cast<uint4 *>(g + (h0 + h) * head + 16 * D)[w] = reinterpret_cast<const uint4 *>(scales + h * 2 * D)[w];
-    }
-  } else {  // the other tokens' scales stay
-    for (int i = tid; i < hn * ITEMS; i += 256) {
-      const int blk = i % NB, t = i / NB % 16, is_v = i / (16 * NB) & 1, h = i / ITEMS;
-      if (t < t0 || t >= t1) continue;
-      const int at = is_v ? kv4_v_scale<D>(t, blk) : kv4_k_scale<D>(t, blk);
-      (g + (h0 + h) * head)[at] = scales[h * 2 * D + at - 16 * D];
+    __syncthreads();
+    if (g && ok) {
+      if (r.t0 == 0 && r.t1 == 16) {
+        for (int i = tid; i < hn * (2 * D / 16); i += 256) {
+          const int h = i / (2 * D / 16), w = i % (2 * D / 16);
+          reinterpret_cast<uint4 *>(g + h * head + 16 * D)[w] = reinterpret_cast<const uint4 *>(sm.scales + h * 2 * D)[w];
+        }
+      } else {  // the other tokens' scales stay
+        for (int i = tid; i < hn * ITEMS; i += 256) {
+          const int blk = i % NB, t = i / NB % 16, is_v = i / (16 * NB) & 1, h = i / ITEMS;
+          if (t < r.t0 || t >= r.t1) continue;
+          const int at = is_v ? kv4_v_scale<D>(t, blk) : kv4_k_scale<D>(t, blk);
+          (g + h * head)[at] = sm.scales[h * 2 * D + at - 16 * D];
+        }
+      }
     }
   }
 }
 
-template <bool READ>
-cudaError_t launch_rows(const Kv4Args &a, uint16_t *k, long long ks, uint16_t *v, long long vs, cudaStream_t stream) {
-  if (a.T == 0 || a.B == 0) return cudaSuccess;
-  // groups that n new rows touch: at most n, and (n + 30) / 16
-  const long long groups = min((long long)a.T, (long long)a.T / 16 + 2LL * a.B);
-  RowsArgs p{a, k, v, ks, vs, min(a.Hkv, kHeads)};
-  while (p.heads > 1 && groups * ((a.Hkv + p.heads - 1) / p.heads) < 2 * 152) p.heads = (p.heads + 1) / 2;  // fill the SMs
-  const dim3 grid((unsigned)groups, (unsigned)((a.Hkv + p.heads - 1) / p.heads));
-  if (a.D == 128)
-    kv4_rows_kernel<128, READ><<<grid, 256, 0, stream>>>(p);
-  else
-    kv4_rows_kernel<64, READ><<<grid, 256, 0, stream>>>(p);
+// Read back: a thread takes half a block (4 code bytes in, 16 bytes out), so that a
+// warp's stores are whole lines (with a block a thread 30 us instead of 25).
+template <int D>
+__global__ void __launch_bounds__(256) kv4_read_kernel(RowsArgs p) {
+  constexpr int NH = D / 8, ITEMS = 2 * 16 * NH;  // half blocks of a row; of a head's K and V of 16 tokens
+  constexpr int U = 4;                            // loads in flight
+  __shared__ Group found;
+  __shared__ uint8_t *place;
+  const Kv4Args &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {
+    const Group r = find_group(a, blockIdx.x, lane);
+    if (lane == 0) {
+      found = r;
+      place = r.b >= 0 ? kv4_group<D>(a, r.b, r.pos0) : nullptr;
+    }
+  }
+  __syncthreads();
+  const Group r = found;
+  if (r.b < 0 || !place) return;
+  const int h0 = blockIdx.y * p.heads, hn = min(p.heads, a.Hkv - h0);
+  const size_t head = kv4_head_bytes<D>(a);
+  const uint8_t *g = place + h0 * head;
+  for (int i0 = tid; i0 < hn * ITEMS; i0 += 256 * U) {
+    uint32_t code[U];
+    uint8_t sc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 256 * u, e = i % NH, t = i / NH % 16, is_v = i / (16 * NH) & 1, h = i / ITEMS;
+      if (i >= hn * ITEMS) continue;
+      const uint8_t *q = g + h * head;  // the group's other tokens lie in the page too: they are read and dropped
+      code[u] = *reinterpret_cast<const uint32_t *>(q + (is_v ? kv4_v_code<D>(t, e * 4) : kv4_k_code<D>(t, e * 4)));
+      sc[u] = q[is_v ? kv4_v_scale<D>(t, e / 2) : kv4_k_scale<D>(t, e / 2)];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 256 * u, e = i % NH, t = i / NH % 16, is_v = i / (16 * NH) & 1, h = i / ITEMS;
+      if (i >= hn * ITEMS || t < r.t0 || t >= r.t1) continue;
+      __half2 v[4];
+      e2m1x8_to_h2x4(code[u], v);
+      const float f = e4m3_to_f32(sc[u]), ts = is_v ? a.vs : a.ks;
+      uint32_t o[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 y = __half22float2(v[m]);  // e2m1 x e4m3 is exact; one FP32 rounding by ts, one to BF16
+        o[m] = f32_to_bf16_bits(y.x * f * ts) | (uint32_t)f32_to_bf16_bits(y.y * f * ts) << 16;
+      }
+      uint16_t *row = is_v ? p.v + (r.n0 + t) * p.v_stride : p.k + (r.n0 + t) * p.k_stride;
+      reinterpret_cast<uint4 *>(row + (h0 + h) * D)[e] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+// The arguments, and the groups that the new rows touch at most: n rows of a
+// sequence touch at most n, and (n + 30) / 16.
+RowsArgs rows_args(const Kv4Args &a, uint16_t *k, long long ks, uint16_t *v, long long vs, long long &groups, int &chunks) {
+  groups = min((long long)a.T, (long long)a.T / 16 + 2LL * a.B);
+  RowsArgs p{a, k, v, ks, vs, min(a.Hkv, kHeads), 0};
+  auto parts = [&]() { return (a.Hkv + p.heads - 1) / p.heads; };
+  while (p.heads > 1 && groups * parts() < 2 * 152) p.heads = (p.heads + 1) / 2;  // fill the SMs
+  chunks = parts();
+  return p;
+}
+
+template <int D>
+cudaError_t launch_append(const RowsArgs &p, cudaStream_t stream) {
+  static bool allowed[64];
+  cudaError_t e = kv4_allow_smem(kv4_append_kernel<D>, sizeof(AppendSmem<D>), allowed);
+  if (e != cudaSuccess) return e;
+  kv4_append_kernel<D><<<min(p.items, 3 * 152), 256, sizeof(AppendSmem<D>), stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -291,11 +361,24 @@ __global__ void __launch_bounds__(1024) compact_plan_kernel(Kv4PageArgs a, Compa
 
 cudaError_t launch_kv4_append(const Kv4Args &a, const uint16_t *k, long long k_stride, const uint16_t *v,
                               long long v_stride, cudaStream_t stream) {
-  return launch_rows<false>(a, const_cast<uint16_t *>(k), k_stride, const_cast<uint16_t *>(v), v_stride, stream);
+  if (a.T == 0 || a.B == 0) return cudaSuccess;
+  long long groups;
+  int chunks;
+  RowsArgs p = rows_args(a, const_cast<uint16_t *>(k), k_stride, const_cast<uint16_t *>(v), v_stride, groups, chunks);
+  if (groups * chunks > 0x7fffffffLL - 3 * 152) return cudaErrorInvalidValue;
+  p.items = (int)(groups * chunks);
+  return a.D == 128 ? launch_append<128>(p, stream) : launch_append<64>(p, stream);
 }
 cudaError_t launch_kv4_read(const Kv4Args &a, uint16_t *k, uint16_t *v, cudaStream_t stream) {
+  if (a.T == 0 || a.B == 0) return cudaSuccess;
   const long long stride = (long long)a.Hkv * a.D;
-  return launch_rows<true>(a, k, stride, v, stride, stream);
+  long long groups;
+  int chunks;
+  const RowsArgs p = rows_args(a, k, stride, v, stride, groups, chunks);
+  const dim3 grid((unsigned)groups, (unsigned)chunks);
+  if (a.D == 128) kv4_read_kernel<128><<<grid, 256, 0, stream>>>(p);
+  else kv4_read_kernel<64><<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_copy_pages(const Kv4PageArgs &a, cudaStream_t stream) {
