@@ -52,6 +52,52 @@ def cached(pages, table_row, n, d, ks, vs):
     return K, V
 
 
+def places_all(d):
+    """places() of the 16 tokens as index arrays [16][d / 2] and [16][d / 16]."""
+    return [np.stack(x) for x in zip(*(places(t, d) for t in range(16)))]
+
+
+def cached_torch(pages, table_row, n, d, ks, vs):
+    """cached() by tensor indexing (torch, any device): float64 K, V [Hkv][n][d]."""
+    import torch
+    dev = pages.device
+    cells = pages[table_row.long()]                                 # [pages][Hkv][groups][18 d]
+    cells = cells.permute(1, 0, 2, 3).reshape(pages.shape[1], -1, 18 * d)
+    val = torch.tensor(np.concatenate([E2M1, -E2M1]), device=dev)
+    scl = torch.tensor(E4M3, device=dev)
+    kc, vc, ksc, vsc = (torch.from_numpy(x).to(dev) for x in places_all(d))
+    out = []
+    for c, s, ts in ((kc, ksc, ks), (vc, vsc, vs)):
+        code = cells[..., c].long()
+        x = torch.stack([val[code & 15], val[code >> 4]], -1).reshape(*code.shape[:-1], d)
+        x = x * scl[cells[..., s].long()].repeat_interleave(16, -1) * float(np.float32(ts))
+        out.append(x.reshape(pages.shape[1], -1, d)[:, :n])
+    return out
+
+
+def attention_torch(q, K, V, sm):
+    """attention() by tensor products (float64 torch): the same five results as numpy arrays."""
+    import torch
+    n, Hq, d = q.shape
+    H, m, _ = K.shape
+    G = Hq // H
+    x = q.reshape(n, H, G, d).permute(1, 0, 2, 3).reshape(H, n * G, d)
+    see = torch.arange(m, device=q.device)[None] <= (m - n + torch.arange(n, device=q.device)).repeat_interleave(G)[:, None]
+    z = torch.where(see, x @ K.transpose(1, 2) * sm, -math.inf)
+    top = z.amax(-1, keepdim=True) if m else torch.full((H, n * G, 1), -math.inf, dtype=z.dtype, device=z.device)
+    safe = torch.where(torch.isinf(top), torch.zeros_like(top), top)
+    p = torch.exp(z - safe)
+    total = p.sum(-1, keepdim=True)
+    lse = (safe + torch.log(total))[..., 0]
+    p = p / torch.where(total > 0, total, torch.ones_like(total))
+    big = torch.where(see, x.abs() @ K.abs().transpose(1, 2) * sm, 0.0).amax(-1) if m else torch.zeros_like(lse)
+    seen_v = torch.cumsum(V.abs(), 1) if m else V
+    last = (m - n + torch.arange(n, device=q.device)).repeat_interleave(G).clamp(min=0)
+    flat = (p.amax(-1, keepdim=True) * seen_v[:, last] if m else torch.zeros_like(x))
+    back = lambda t: t.reshape(H, n, G, *t.shape[2:]).transpose(0, 1).reshape(n, Hq, *t.shape[2:]).cpu().numpy()
+    return back(p @ V), back(lse), back(big), back(p @ V.abs()), back(flat)
+
+
 def attention(q, K, V, sm):
     """q [n][Hq][d] float64 (the sequence's newest tokens) against K, V [Hkv][m][d].
     Returns out, lse, and the sums the error bounds are made of: the largest

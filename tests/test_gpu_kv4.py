@@ -433,3 +433,150 @@ def test_cache_in_use(g):
     step([b, f], [2, 2], True)
     step([f], [25], False)
     assert c.check() == 0
+
+
+def want_fast(pages, tab, lens, counts, q, d):
+    parts, at = [], 0
+    for b, (n, m) in enumerate(zip(counts, lens)):
+        need = -(-m // (16 * pages.shape[2]))
+        K, V = ref.cached_torch(pages, tab[b, :need], m, d, KS, VS)
+        parts.append(ref.attention_torch(q[at:at + n].double(), K, V, float(np.float32(d ** -0.5))))
+        at += n
+    return [np.concatenate(x) for x in zip(*parts)]
+
+
+# sequences, tokens at most, r, hq, hkv, d, page: runs that cut items, in both team sizes and all column blocks
+SPLIT = [(40, 1500, 1, 8, 8, 128, 64), (160, 700, 1, 4, 1, 128, 16), (30, 1200, 2, 48, 8, 128, 32), (6, 3000, 5, 16, 2, 128, 64),
+         (50, 900, 1, 16, 4, 64, 16), (45, 800, 3, 32, 8, 64, 64), (40, 600, 8, 24, 4, 64, 128), (3, 9000, 1, 4, 2, 64, 256),
+         (2, 20000, 1, 16, 1, 128, 128), (1, 30000, 8, 64, 1, 128, 64), (1, 12000, 2, 64, 2, 64, 32), (200, 130, 1, 8, 2, 128, 16)]
+
+
+@pytest.mark.parametrize("B,most,r,hq,hkv,d,page", SPLIT)
+def test_decode_split_over_runs(g, B, most, r, hq, hkv, d, page):
+    rng = np.random.RandomState(B + r)
+    lens = [most] + [int(x) for x in np.exp(rng.uniform(0, np.log(most), B - 1))]
+    if B > 4:
+        lens[2] = 0
+    pages, tab, n, *_ = setup(g, lens, page, hkv, d, seed=B)
+    q = queries(B * r, hq, d, B).reshape(B, r, hq, d)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = g.kv4_decode(q, pages, tab, n, KS, VS, return_lse=True, dev_status=st)
+    close(out, lse, want_fast(pages, tab, lens, [r] * B, q.flatten(0, 1), d), d)
+    again = g.kv4_decode(q, pages, tab, n, KS, VS, return_lse=True, dev_status=st)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and st.item() == 0
+
+
+# (new, cached) of the longest, sequences, hq, hkv, d, page: more items than CTAs, rows of several sequences, long caches
+MANY = [(1200, 1200, 4, 32, 8, 128, 64), (300, 5000, 3, 16, 4, 64, 32), (64, 900, 40, 8, 8, 128, 16), (700, 701, 7, 12, 2, 64, 128),
+        (1, 3000, 50, 40, 8, 128, 64), (500, 2500, 2, 56, 8, 128, 256)]
+
+
+@pytest.mark.parametrize("new,total,B,hq,hkv,d,page", MANY)
+def test_prefill_many_items(g, new, total, B, hq, hkv, d, page):
+    rng = np.random.RandomState(new)
+    counts = [new] + [int(x) for x in rng.randint(0, new + 1, B - 1)]
+    lens = [total] + [c + int(rng.randint(0, total - new + 1)) for c in counts[1:]]
+    pages, tab, n, *_ = setup(g, lens, page, hkv, d, seed=B)
+    T = sum(counts)
+    q = queries(T + 3, hq, d, T)                     # three padding rows, left alone
+    start = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((T + 3, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T + 3, hq), 7.0, device="cuda")
+    g.kv4_prefill(q, pages, tab, n, start, KS, VS, total_kv=sum(lens), out=out, lse=lse, dev_status=st)
+    close(out[:T], lse[:T], want_fast(pages, tab, lens, counts, q, d), d)
+    assert (out[T:] == 7).all() and (lse[T:] == 7).all()
+    again = g.kv4_prefill(q[:T].contiguous(), pages, tab, n, start, KS, VS, return_lse=True, dev_status=st)
+    assert torch.equal(out[:T], again[0]) and torch.equal(lse[:T], again[1]) and st.item() == 0
+
+
+def test_a_rows_result_depends_on_no_other_row(g):
+    """The same queries beside others give the same bits (the maxima and the rescaling are decided row by row)."""
+    d, hq, hkv, page = 128, 8, 2, 16
+    lens = [600, 600]
+    pages, tab, n, *_ = setup(g, lens, page, hkv, d)
+    start = torch.tensor([0, 70, 140], dtype=torch.int32, device="cuda")
+    q = queries(140, hq, d, 1)
+    other = q.clone()
+    other[:, ::2] *= 40
+    a, b = (g.kv4_prefill(x, pages, tab, n, start, KS, VS) for x in (q, other))
+    assert torch.equal(a[:, 1::2], b[:, 1::2]) and not torch.equal(a, b)
+    a, b = (g.kv4_decode(x[[69, 139]], pages, tab, n, KS, VS) for x in (q, other))
+    assert torch.equal(a[:, 1::2], b[:, 1::2]) and not torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(g):
+    """A cache of 4.7 GB: its last pages lie past 2^32 bytes."""
+    d, hkv, hq, page, num = 128, 8, 16, 256, 16000
+    pages = g.kv4_new_pages(num, page, hkv, d)
+    assert pages.numel() > 2 ** 32
+    T = 300
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(T, hkv, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    tab = torch.tensor([[num - 1, num - 3]], dtype=torch.int32, device="cuda")
+    n = torch.tensor([T], dtype=torch.int32, device="cuda")
+    g.kv4_append(k, v, pages, tab, n, KS, VS)
+    small = g.kv4_new_pages(2, page, hkv, d)
+    stab = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    g.kv4_append(k, v, small, stab, n, KS, VS)
+    assert torch.equal(pages[[num - 1, num - 3]], small)
+    for x, y in zip(g.kv4_read(pages, tab, n, KS, VS, T), g.kv4_read(small, stab, n, KS, VS, T)):
+        assert torch.equal(x, y)
+    q = queries(5, hq, d, 3)
+    start = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    assert torch.equal(g.kv4_decode(q[None], pages, tab, n, KS, VS), g.kv4_decode(q[None], small, stab, n, KS, VS))
+    assert torch.equal(g.kv4_prefill(q, pages, tab, n, start, KS, VS), g.kv4_prefill(q, small, stab, n, start, KS, VS))
+    g.kv4_copy_pages(pages, torch.tensor([num - 1], dtype=torch.int32, device="cuda"),
+                     torch.tensor([num - 2], dtype=torch.int32, device="cuda"))
+    assert torch.equal(pages[num - 2], small[0])
+    t2, m, live = g.kv4_compact(pages, tab)
+    # in ascending order: num - 3 to page 0, num - 1 to page 1
+    assert t2.tolist() == [[1, 0]] and live.item() == 2 and torch.equal(pages[[1, 0]], small)
+
+
+def test_prefill_workspace_too_small_is_flagged(g):
+    """total_kv below the real sum: GDN_E_RANGE, nothing out of bounds, the sequences that fit are right."""
+    d, hq, hkv, page = 64, 4, 2, 16
+    pages, tab, n, *_ = setup(g, [200, 900], page, hkv, d)
+    q = queries(2, hq, d, 1)
+    start = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = g.kv4_prefill(q, pages, tab, n, start, KS, VS)
+    out = g.kv4_prefill(q, pages, tab, n, start, KS, VS, total_kv=200, dev_status=st)
+    assert st.item() == 6 and torch.equal(out[0], good[0])
+
+
+def test_python_refusals_on_the_gpu(g):
+    d, hq, hkv, page = 64, 4, 2, 16
+    pages, tab, n, k, v, start = setup(g, [20, 20], page, hkv, d)
+    q = queries(2, hq, d, 0)
+    one = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    bad = [(ValueError, lambda: g.kv4_decode(q.float(), pages, tab, n, KS, VS)),
+           (ValueError, lambda: g.kv4_decode(q[..., ::2], pages, tab, n, KS, VS)),
+           (ValueError, lambda: g.kv4_decode(q.transpose(0, 1), pages, tab, n, KS, VS)),
+           (ValueError, lambda: g.kv4_decode(q[:1], pages, tab, n, KS, VS)),
+           (ValueError, lambda: g.kv4_decode(q, pages, tab.long(), n, KS, VS)),
+           (ValueError, lambda: g.kv4_decode(q, pages, tab, n[:1], KS, VS)),
+           (ValueError, lambda: g.kv4_decode(q, pages.transpose(0, 1), tab, n, KS, VS)),
+           (ValueError, lambda: g.kv4_decode(q, pages, tab, n, KS, VS, out=torch.empty(2, hq, d, device="cuda"))),
+           (ValueError, lambda: g.kv4_decode(q, pages, tab, n, KS, VS, lse=torch.empty(2, hq + 1, device="cuda"))),
+           (g.GdnError, lambda: g.kv4_decode(q[:, :3], pages, tab, n, KS, VS)),
+           (g.GdnError, lambda: g.kv4_decode(q, pages, tab, n, 0.0, VS)),
+           (g.GdnError, lambda: g.kv4_decode(q, pages, tab, n, KS, VS, sm_scale=-1.0)),
+           (ValueError, lambda: g.kv4_prefill(q, pages, tab, n, one[:2], KS, VS)),
+           (g.GdnError, lambda: g.kv4_prefill(q, pages, tab, n, one, KS, VS, total_kv=-1)),
+           (g.GdnError, lambda: g.kv4_prefill(q, pages, tab, n, one, KS, VS, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))),
+           (ValueError, lambda: g.kv4_append(k, v[1:], pages, tab, n, KS, VS, q_start=start)),
+           (ValueError, lambda: g.kv4_append(k.float(), v, pages, tab, n, KS, VS, q_start=start)),
+           (ValueError, lambda: g.kv4_copy_pages(pages, one, one[:2])),
+           (ValueError, lambda: g.kv4_copy_pages(pages[:, :1], one, one)),
+           (ValueError, lambda: g.kv4_compact(pages, tab, page_map=one)),
+           (TypeError, lambda: g.kv4_decode(q, pages, tab, n, "x", VS))]
+    for kind, f in bad:
+        with pytest.raises(kind):
+            f()
+    odd = torch.zeros(2 * hq * d + 8, dtype=torch.bfloat16, device="cuda")[1:1 + 2 * hq * d].reshape(2, hq, d)
+    with pytest.raises(g.GdnError, match="GDN_E_ALIGN"):
+        g.kv4_decode(odd, pages, tab, n, KS, VS)
+    with pytest.raises(g.GdnError, match="GDN_E_SHAPE"):    # rows 4 elements off a multiple of 8 apart
+        g.kv4_decode(torch.zeros(2, hq * d + 4, dtype=torch.bfloat16, device="cuda")[:, :hq * d].view(2, hq, d), pages, tab, n, KS, VS)

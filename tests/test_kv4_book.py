@@ -209,3 +209,30 @@ def test_python_refusals(g):
         g.kv4_copy_pages(pages, n, n)
     with pytest.raises(ValueError, match="CUDA"):
         g.kv4_compact(pages, t)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_reference_forms_agree(d):
+    """The tensor forms of the float64 reference equal the ones written token by token."""
+    import numpy as np
+    import torch
+    import kv4_ref as ref
+    rng = np.random.RandomState(d)
+    pages = rng.randint(0, 256, (5, 2, 2, 18 * d)).astype(np.uint8)
+    pages[..., 16 * d:] %= 120                       # finite positive scales
+    row = np.array([3, 0, 4, 1], np.int32)
+    for n, new in ((0, 2), (1, 3), (77, 5), (128, 1)):
+        K, V = ref.cached(pages, row, n, d, 0.017, 0.013)
+        Kt, Vt = ref.cached_torch(torch.from_numpy(pages), torch.from_numpy(row), n, d, 0.017, 0.013)
+        assert np.array_equal(K, Kt.numpy()) and np.array_equal(V, Vt.numpy())
+        q = rng.randn(new, 6, d) * 0.05
+        for a, b in zip(ref.attention(q, K, V, 0.1), ref.attention_torch(torch.from_numpy(q), Kt, Vt, 0.1)):
+            np.testing.assert_allclose(a, b, rtol=1e-12, atol=1e-12)
+
+
+def test_every_layout_place_is_used_once():
+    import numpy as np
+    import kv4_ref as ref
+    for d in (64, 128):
+        at = np.concatenate([np.concatenate(ref.places(t, d)) for t in range(16)])
+        assert np.array_equal(np.sort(at), np.arange(18 * d))
