@@ -68,7 +68,7 @@ def _link_binding(obj: str):
         tlib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
         tmp = BINDING + ".tmp"
         _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libgdn.so", "-Wl,-rpath,$ORIGIN", "-L", tlib,
-              "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "linking _kv4.so")
+              "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "linking _kv4.so")
         os.replace(tmp, BINDING)
 
 

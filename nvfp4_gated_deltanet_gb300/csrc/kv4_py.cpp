@@ -5,11 +5,12 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <exception>
 #include <string>
 
@@ -88,6 +89,7 @@ kv4_cache cache(PyObject *o, PyObject *ks, PyObject *vs) {
   return {p.data_ptr<uint8_t>(), as_int(p.size(0), "pages"), as_int(16 * p.size(2), "pages"), as_int(p.size(1), "pages"),
           as_int(p.size(3) / 18, "pages"), (float)number(ks), (float)number(vs)};
 }
+float scale_of(PyObject *o, const kv4_cache &c) { return given(o) ? (float)number(o) : 1.0f / std::sqrt((float)c.head_dim); }
 kv4_batch batch(PyObject *table, PyObject *kv_len, PyObject *q_start, int64_t rows) {
   kv4_batch b{};
   b.block_table = i32(table, "block_table", 2);
@@ -110,9 +112,13 @@ int64_t rows_stride(const at::Tensor &t, const char *name, int heads, int d) {
     throw Bad(std::string(name) + ": a row's heads must lie together in memory");
   return t.size(0) > 1 ? t.stride(0) : t.size(1) * d;
 }
+// A new tensor, without the dispatcher's microsecond
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
 // The given output, checked, or a new one of the type
 at::Tensor output(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) {
-  if (!given(o)) return at::empty(shape, like.options().dtype(type));
+  if (!given(o)) return fresh(shape, type, like);
   const at::Tensor &t = tensor(o, name);
   const bool typed = type == at::kBFloat16 ? is_bf16(t) : t.scalar_type() == type;
   if (!typed || t.sizes() != shape || !t.is_cuda() || !t.is_contiguous())
@@ -129,9 +135,9 @@ at::Tensor workspace(PyObject *o, size_t n, const at::Tensor &like, PyObject *st
   }
   bytes = n;
   if (n == 0) return at::Tensor();
-  if (!given(stream)) return at::empty({(int64_t)n}, like.options().dtype(at::kByte));
+  if (!given(stream)) return fresh({(int64_t)n}, at::kByte, like);
   c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(s, like.device().index()));
-  return at::empty({(int64_t)n}, like.options().dtype(at::kByte));
+  return fresh({(int64_t)n}, at::kByte, like);
 }
 void *ptr(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 const uint16_t *u16(const at::Tensor &t) { return static_cast<const uint16_t *>(t.const_data_ptr()); }
@@ -187,7 +193,7 @@ PyObject *decode(PyObject *const *a) {
   const cudaStream_t s = stream_of(a[12]);
   size_t n;
   const at::Tensor ws = workspace(a[10], kv4_decode_workspace(&c, &b, as_int(Hq, "q")), q, a[12], s, n);
-  check(kv4_decode(&c, &b, u16(q), row, as_int(Hq, "q"), (float)number(a[6]), u16_out(out), static_cast<float *>(ptr(lse)),
+  check(kv4_decode(&c, &b, u16(q), row, as_int(Hq, "q"), scale_of(a[6], c), u16_out(out), static_cast<float *>(ptr(lse)),
                    ptr(ws), n, status_word(a[11]), s),
         "kv4_decode");
   return want ? pair(out, lse) : THPVariable_Wrap(out);
@@ -206,7 +212,7 @@ PyObject *prefill(PyObject *const *a) {
   const cudaStream_t s = stream_of(a[14]);
   size_t n;
   const at::Tensor ws = workspace(a[12], kv4_prefill_workspace(&c, &b, total, Hq), q, a[14], s, n);
-  check(kv4_prefill(&c, &b, total, u16(q), qs, Hq, (float)number(a[8]), u16_out(out), static_cast<float *>(ptr(lse)), ptr(ws),
+  check(kv4_prefill(&c, &b, total, u16(q), qs, Hq, scale_of(a[8], c), u16_out(out), static_cast<float *>(ptr(lse)), ptr(ws),
                     n, status_word(a[13]), s),
         "kv4_prefill");
   return want ? pair(out, lse) : THPVariable_Wrap(out);

@@ -62,8 +62,7 @@ def kv4_decode(q, pages, block_table, kv_len, k_scale, v_scale, sm_scale=None, o
     """Attention of the batch's newest tokens: q [B][Hq][d] (one token per
     sequence) or [B][r][Hq][d] (r candidates) -> out of q's shape, BF16; with
     return_lse also the rows' log-sum-exp, FP32. sm_scale: d^-1/2 by default."""
-    return _native().decode(q, pages, block_table, kv_len, k_scale, v_scale,
-                            q.shape[-1] ** -0.5 if sm_scale is None else sm_scale, out, lse, return_lse, workspace,
+    return _native().decode(q, pages, block_table, kv_len, k_scale, v_scale, sm_scale, out, lse, return_lse, workspace,
                             dev_status, stream)
 
 
@@ -72,9 +71,8 @@ def kv4_prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_
     """Causal attention of ragged prompt chunks: q [T][Hq][d], sequence b's rows
     [q_start[b], q_start[b + 1]) being its newest tokens. total_kv: an upper
     bound of kv_len's sum (default: what the tables can hold)."""
-    return _native().prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_kv,
-                             q.shape[-1] ** -0.5 if sm_scale is None else sm_scale, out, lse, return_lse, workspace,
-                             dev_status, stream)
+    return _native().prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_kv, sm_scale, out, lse,
+                             return_lse, workspace, dev_status, stream)
 
 
 def kv4_copy_pages(pages, src, dst, dev_status=None, stream=None):
