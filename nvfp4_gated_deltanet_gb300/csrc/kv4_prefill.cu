@@ -207,10 +207,21 @@ GDN_DEV bool find_work(const PrefillKv4 &p, int x, int lane, Item &w) {
     return v;
   };
   if (x >= all(0)) return false;
-  int lo = 0, hi = (int)(((long long)c.cols * c.page_tokens + kKv - 1) / kKv) + 1;  // all(lo) > x >= all(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (all(mid) > x) lo = mid; else hi = mid;
+  int hi = 0;
+  for (int b = lane; b < c.B; b += 32) hi = max(hi, (seq_of(b).len + kKv - 1) / kKv);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  int lo = 0;
+  if (c.B == 1) {  // costs rise from item to item by what they do: the item's place gives its cost
+    const int n = __shfl_sync(0xffffffffu, s0.q1 - s0.q0, 0), len = __shfl_sync(0xffffffffu, s0.len, 0);
+    const int last = len - n + min(n, ((n + step - 1) / step - x) * step) - 1;  // of the x-th item from the end
+    lo = last >= 0 ? last / kKv + 1 : 0;
+  } else {
+    ++hi;  // all(lo) > x >= all(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (all(mid) > x) lo = mid; else hi = mid;
+    }
   }
   int r = x - all(lo + 1);  // among the items of cost lo, by sequence
   int tiles = 0;
