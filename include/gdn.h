@@ -366,8 +366,10 @@ gdn_status kv4_read(const kv4_cache *c, const kv4_batch *b, uint16_t *k, uint16_
  * NULL. workspace: kv4_decode_workspace bytes of device memory that no other
  * call in flight uses; its contents before the call do not matter. Scores,
  * sums and the output accumulate in FP32; the softmax weights enter the second
- * product rounded to FP16, all other operands exactly. The order of every sum
- * depends on the lengths of the whole batch, not on anything else. Errors: as
+ * product rounded to FP16, q in FP16 scaled by a power of two per row (exact but
+ * for elements 2^-27 below the row's largest), K and V exactly. The order of
+ * every sum depends on the lengths of the whole batch and on the tables' width,
+ * not on anything else. Errors: as
  * kv4_append; GDN_E_SHAPE for n_q_heads not a multiple of n_kv_heads or more
  * than 64 query heads per KV head, or a workspace that is too small. */
 gdn_status kv4_decode(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int n_q_heads,
@@ -377,8 +379,12 @@ size_t kv4_decode_workspace(const kv4_cache *c, const kv4_batch *b, int n_q_head
 
 /* The same attention for prompt chunks of any length per sequence (ragged rows
  * by q_start). total_kv: an upper bound of the sum of the kv_len of all
- * sequences (it sizes the workspace, which holds the cached tokens in FP16 while the call runs); a sum above
- * it sets GDN_E_RANGE. Errors: as kv4_decode. */
+ * sequences; it sizes the workspace, which holds the cached tokens expanded to
+ * 16 bits while the call runs. A sum far enough above it (whole tiles of 128
+ * tokens per sequence count) sets GDN_E_RANGE, and sequences that do not fit get
+ * zeros. q and K enter exactly (BF16), the softmax weights in FP16; a row's
+ * result depends on its own sequence alone. Errors: as kv4_decode;
+ * GDN_E_OVERFLOW for a workspace beyond 2^31 tiles. */
 gdn_status kv4_prefill(const kv4_cache *c, const kv4_batch *b, int64_t total_kv, const uint16_t *q, int64_t q_stride,
                        int n_q_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,
                        size_t workspace_bytes, int32_t *dev_status, void *stream);

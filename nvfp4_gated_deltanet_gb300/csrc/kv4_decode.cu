@@ -37,6 +37,13 @@
 // A team is a whole CTA where there are fewer items than SMs (long contexts:
 // few pieces to join), else four warps: the other teams of the CTA work while
 // one's parts meet, and fewer warps wait for the slowest.
+//
+// Measured (32 query heads, d = 128): 64 sequences of up to 8190 tokens, 8 KV
+// heads, 291 MB: 59 us, 4.9 TB/s (0.73 of the copy bandwidth); one of 200001, 4 KV
+// heads, 115 MB: 29.6 us. Of these 4 us are the launch and finding the runs, 3 the
+// join; the loads alone take 54 and 24, the arithmetic alone 55 and 26. A tile
+// costs about 570 issue slots a warp: 128 conversions, 96 shifts that bring bytes
+// to them, 128 scale products, 32 MMAs.
 #include "kv4.cuh"
 #include "tc.cuh"
 
@@ -82,11 +89,23 @@ struct DecodeArgs {
   int extra;         // cost of an item beside its tiles, in tiles; kWhole: runs hold whole items, nothing to join
   float *part;       // [2 CTAs][rows][D] and, after them, their (m, l) [2 CTAs][rows][2]
 };
+// What the plan goes by, all measured on GB300 (d = 128, us):
 // An item's query rows, its meeting and its output take a team about as long as
-// this many tiles of its run: a whole CTA, four warps.
+// this many tiles of its run. A whole CTA: 12 / 24 / 40 gave 28.9 / 26.2 / 26.2 at
+// 16 sequences of up to 8000 tokens (8 KV heads); four warps: 3 / 6 / 10 gave
+// 67.7 / 64.4 / 64.7 at 64 of up to 8190.
 constexpr int kExtraCta = 24, kExtraTeam = 6;
-constexpr int kWhole = 1 << 20;
-constexpr int kManyItems = 152;  // from here on (a GB300's SMs) teams of four warps
+// From as many items as a GB300 has SMs, teams of four warps instead of whole
+// CTAs: 59 against 72 with 512 items (64 sequences, above), 24 against 41 with 768
+// (96 of up to 600); with 128 items 27.4 against 26.2, with 4 of 200001 tokens 56
+// against 30.
+constexpr int kManyItems = 152;
+// Items stay whole while a team goes through the longest in this many rounds: 64
+// items of 1000 tokens (2 rounds of a CTA) 9.8 against 11.9 cut and joined, 4 of
+// 3000 (6 rounds) 16.7 against 11.9; 768 of up to 600 (5 rounds of a team) 23.0
+// against 24.3.
+constexpr int kRoundsCta = 3, kRoundsTeam = 6;
+constexpr int kWhole = 1 << 20;  // the `extra` of whole items
 
 // a / b, mostly in 32 bits
 GDN_DEV long long quot(long long a, long long b) {
@@ -821,8 +840,8 @@ struct DecodePlan {
   bool small;    // teams of four warps
   size_t bytes;
 };
-// Everything the host knows: an upper bound of the lengths. Where it says that
-// no item has more tiles than a team has warps, items stay whole.
+// Everything the host knows: an upper bound of the lengths. Where it says that an
+// item takes a team few rounds of tiles, items stay whole: no piece to join.
 DecodePlan decode_plan(const Kv4AttnArgs &a, int num_sms) {
   DecodePlan d{};
   const int R = a.c.T / a.c.B * (a.Hq / a.c.Hkv);
@@ -835,7 +854,7 @@ DecodePlan decode_plan(const Kv4AttnArgs &a, int num_sms) {
                                    : (d.NQ == 1 ? shape_info<64, 1>(d.small) : d.NQ == 2 ? shape_info<64, 2>(d.small)
                                                                                          : shape_info<64, 4>(d.small));
   const long long most = ((long long)a.c.cols * a.c.page_tokens + s.tile - 1) / s.tile;  // tiles of an item
-  d.extra = most <= s.team ? kWhole : d.small ? kExtraTeam : kExtraCta;
+  d.extra = most <= (long long)s.team * (d.small ? kRoundsTeam : kRoundsCta) ? kWhole : d.small ? kExtraTeam : kExtraCta;
   const long long n = d.extra == kWhole ? items : (items * most + s.team - 1) / s.team;  // runs that could have work
   d.ctas = (int)(n < (long long)num_sms * s.teams ? (n + s.teams - 1) / s.teams : num_sms);
   d.bytes = d.extra == kWhole ? 0 : 2 * (size_t)d.ctas * s.teams * 8 * d.NQ * (a.c.D + 2) * sizeof(float);
