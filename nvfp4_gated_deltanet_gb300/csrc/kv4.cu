@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(RowsArgs p) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const float2 y = __half22float2(v[m]);  // e2m1 x e4m3 is exact; one FP32 rounding by ts, one to BF16
-        o[m] = f32_to_bf16_bits(y.x * f * ts) | (uint32_t)f32_to_bf16_bits(y.y * f * ts) << 16;
+        o[m] = bf16x2(y.x * f * ts, y.y * f * ts);
       }
       uint16_t *row = is_v ? p.v + (r.n0 + t) * p.v_stride : p.k + (r.n0 + t) * p.k_stride;
       reinterpret_cast<uint4 *>(row + (h0 + h) * D)[e] = make_uint4(o[0], o[1], o[2], o[3]);

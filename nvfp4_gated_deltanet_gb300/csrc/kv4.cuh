@@ -89,6 +89,11 @@ GDN_DEV void decode8(uint32_t w, __half2 s, uint32_t (&o)[4]) {
   for (int i = 0; i < 4; ++i) o[i] = h2u(__hmul2(h[i], s));
 }
 
+// Two floats rounded to BF16, the first in the low half
+GDN_DEV uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
 // 2^x, to two units in the last place; 2^-inf = 0
 GDN_DEV float ex2(float x) {
   float y;

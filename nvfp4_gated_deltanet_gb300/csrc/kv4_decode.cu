@@ -653,8 +653,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
         const long long out = ((long long)cur.b * p.r + ri / p.G) * p.a.Hq + h * p.G + ri % p.G;
         const float inv = sum == 0.0f ? 0.0f : c.vs / sum;
         *reinterpret_cast<uint2 *>(p.a.out + out * D + d4) =
-            make_uint2(f32_to_bf16_bits(o.x * inv) | (uint32_t)f32_to_bf16_bits(o.y * inv) << 16,
-                       f32_to_bf16_bits(o.z * inv) | (uint32_t)f32_to_bf16_bits(o.w * inv) << 16);
+            make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
         if (p.a.lse && d4 == 0) p.a.lse[out] = (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
       } else {
         *reinterpret_cast<float4 *>(p.part + (piece * S::kRows + row) * D + d4) = o;
@@ -763,8 +762,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
       uint16_t *dst = p.a.out + out_row(row) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t *>(dst + e) =
-            f32_to_bf16_bits(o[e] * inv) | (uint32_t)f32_to_bf16_bits(o[e + 1] * inv) << 16;
+        *reinterpret_cast<uint32_t *>(dst + e) = bf16x2(o[e] * inv, o[e + 1] * inv);
       if (p.a.lse && lane == 0) p.a.lse[out_row(row)] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
     }
     return;

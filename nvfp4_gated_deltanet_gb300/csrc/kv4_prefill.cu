@@ -57,6 +57,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct PrefillKv4 {
   Kv4AttnArgs a;
   int G, tpt;                     // query heads per KV head; tokens of a query tile: 128 / G
+  uint32_t inv_g;                 // ceil(2^16 / G): r / G = r inv_g >> 16 for r < 128
   int cap;                        // K / V tiles (of all KV heads) that the workspace holds
   int *next;                      // items handed out beside each CTA's first one; zeroed by the expansion
   uint16_t *tiles;                // [cap][Hkv][K: d / 64 x 128 rows x 64, BF16; V^T: 2 x d rows x 64, FP16], swizzled
@@ -186,49 +187,59 @@ struct Item {
 };
 
 // The x-th item by falling cost (K / V tiles) of all sequences, without its
-// head; false past the end. All lanes of a warp.
-GDN_DEV bool find_work(const PrefillKv4 &p, int x, int lane, Item &w) {
+// head; false past the end. All lanes of a warp. items: of all sequences, for a
+// head.
+GDN_DEV bool find_work(const PrefillKv4 &p, int x, int lane, Item &w, int &items) {
   const Kv4Args &c = p.a.c;
   const int step = 2 * p.tpt;
+  auto own_of = [&](const Kv4Seq &s) { return (int)((unsigned)(s.q1 - s.q0 + step - 1) / (unsigned)step); };
   Kv4Seq s0 = {0, 0, 0};  // of sequence `lane`
   if (lane < c.B) s0 = kv4_seq(c, lane);
+  const int own0 = own_of(s0);
   auto seq_of = [&](int b) { return b < 32 ? s0 : kv4_seq(c, b); };  // b % 32 == lane
-  auto count = [&](const Kv4Seq &s, int cost) {  // the sequence's items of at least this cost
-    const int n = s.q1 - s.q0, items = (n + step - 1) / step;
-    if (cost == 0) return items;
+  auto count = [&](const Kv4Seq &s, int own, int cost) {  // the sequence's items of at least this cost
+    const int n = s.q1 - s.q0;
+    if (cost == 0) return own;
     const long long at = (long long)(cost - 1) * kKv - (s.len - n);  // an item's last token, at least
-    return at <= 0 ? items : at >= n ? 0 : items - (int)at / step;
+    return at <= 0 ? own : at >= n ? 0 : own - (int)((unsigned)at / (unsigned)step);
   };
-  auto all = [&](int cost) {
-    int v = 0;
-    for (int b = lane; b < c.B; b += 32) v += count(seq_of(b), cost);
+  auto sum = [&](int v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   };
-  if (x >= all(0)) return false;
-  int hi = 0;
-  for (int b = lane; b < c.B; b += 32) hi = max(hi, (seq_of(b).len + kKv - 1) / kKv);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  auto all = [&](int cost) {
+    int v = lane < c.B ? count(s0, own0, cost) : 0;
+    for (int b = lane + 32; b < c.B; b += 32) {
+      const Kv4Seq s = kv4_seq(c, b);
+      v += count(s, own_of(s), cost);
+    }
+    return sum(v);
+  };
+  items = all(0);
+  if (x >= items) return false;
+  // Where every item has a CTA of its own the order does not matter: then, and
+  // for one sequence, whose costs rise from item to item, no search (it takes 2 us
+  // of one warp, before the first product).
+  const bool any_order = c.B == 1 || (long long)items * c.Hkv <= gridDim.x;
   int lo = 0;
-  if (c.B == 1) {  // costs rise from item to item by what they do: the item's place gives its cost
-    const int n = __shfl_sync(0xffffffffu, s0.q1 - s0.q0, 0), len = __shfl_sync(0xffffffffu, s0.len, 0);
-    const int last = len - n + min(n, ((n + step - 1) / step - x) * step) - 1;  // of the x-th item from the end
-    lo = last >= 0 ? last / kKv + 1 : 0;
-  } else {
+  if (!any_order) {
+    int hi = 0;
+    for (int b = lane; b < c.B; b += 32) hi = max(hi, (seq_of(b).len + kKv - 1) / kKv);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     ++hi;  // all(lo) > x >= all(hi)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (all(mid) > x) lo = mid; else hi = mid;
     }
   }
-  int r = x - all(lo + 1);  // among the items of cost lo, by sequence
+  int r = any_order ? x : x - all(lo + 1);  // among the items of cost lo (or all), by sequence
   int tiles = 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const bool in = b0 + lane < c.B;
-    const Kv4Seq s = in ? seq_of(b0 + lane) : Kv4Seq{0, 0, 0};
-    const int above = count(s, lo + 1), e = count(s, lo) - above, kt = (s.len + kKv - 1) / kKv;
+    const Kv4Seq s = b0 + lane < c.B ? seq_of(b0 + lane) : Kv4Seq{0, 0, 0};
+    const int own = b0 ? own_of(s) : own0;
+    const int above = any_order ? 0 : count(s, own, lo + 1), e = count(s, own, lo) - above, kt = (s.len + kKv - 1) / kKv;
     int incl = e, kincl = kt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -241,11 +252,10 @@ GDN_DEV bool find_work(const PrefillKv4 &p, int x, int lane, Item &w) {
     const unsigned past = __ballot_sync(0xffffffffu, incl > r);
     if (past) {
       const int l = __ffs(past) - 1;
-      const int n = s.q1 - s.q0, items = (n + step - 1) / step;
       w.q0 = __shfl_sync(0xffffffffu, s.q0, l);
-      w.n = __shfl_sync(0xffffffffu, n, l);
+      w.n = __shfl_sync(0xffffffffu, s.q1 - s.q0, l);
       w.len = __shfl_sync(0xffffffffu, s.len, l);
-      w.t0 = __shfl_sync(0xffffffffu, items - 1 - above - (r - (incl - e)), l) * step;
+      w.t0 = __shfl_sync(0xffffffffu, own - 1 - above - (r - (incl - e)), l) * step;
       w.tile0 = tiles + __shfl_sync(0xffffffffu, kincl - kt, l);
       break;
     }
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     for (int it = 0; warp_wait_all(item_full + (it & 1), it >> 1); ++it) {
       const Item &w = items[it & 1];  // read where it is needed, and given back at the end: registers are short
       if (w.h < 0) break;
-      const int off_t = i * p.tpt + r / p.G;                      // the row's token, from the item's first
+      const int off_t = i * p.tpt + (int)(r * p.inv_g >> 16);                      // the row's token, from the item's first
       const int sure = w.len - w.n + w.t0 + i * p.tpt;            // every row of the tile sees up to here
       const int last = r < p.tpt * p.G && w.t0 + off_t < w.n ? w.len - w.n + w.t0 + off_t : -1;  // the last token this row sees
       const int nkv = w.nkv[i];
@@ -425,8 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
           uint32_t x[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            x[e] = f32_to_bf16_bits(__uint_as_float(o[2 * e]) * inv) |
-                   (uint32_t)f32_to_bf16_bits(__uint_as_float(o[2 * e + 1]) * inv) << 16;
+            x[e] = bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             *reinterpret_cast<uint4 *>(st + lane * 128 + (((q / 8 + e) ^ (lane & 7)) << 4)) =
@@ -435,9 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int row = k * 4 + (lane >> 3), rr = (warp & 3) * 32 + row, tk = w.t0 + i * p.tpt + rr / p.G;
+          const int row = k * 4 + (lane >> 3), rr = (warp & 3) * 32 + row;
+          const int tr = (int)(rr * p.inv_g >> 16), tk = w.t0 + i * p.tpt + tr;
           if (rr < p.tpt * p.G && tk < w.n)
-            reinterpret_cast<uint4 *>(p.a.out + ((long long)(w.q0 + tk) * p.a.Hq + w.h * p.G + rr % p.G) * D + q0)[lane & 7] =
+            reinterpret_cast<uint4 *>(p.a.out + ((long long)(w.q0 + tk) * p.a.Hq + w.h * p.G + rr - tr * p.G) * D +
+                                      q0)[lane & 7] =
                 *reinterpret_cast<const uint4 *>(st + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
         }
         __syncwarp();
@@ -445,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       tc_fence_before();  // O has been read: the next item's products follow this row tile's next weights
       const int tok = w.t0 + off_t;
       if (p.a.lse && r < p.tpt * p.G && tok < w.n)
-        p.a.lse[(long long)(w.q0 + tok) * p.a.Hq + w.h * p.G + r % p.G] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+        p.a.lse[(long long)(w.q0 + tok) * p.a.Hq + w.h * p.G + r - (off_t - i * p.tpt) * p.G] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
       __syncwarp();
       if (lane == 0) mbar_arrive(item_free + (it & 1));
     }
@@ -565,15 +576,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       }
     } else if (warp == 10) {
       // ------------------------------------------------ the next item
+      int all_items = 0;
       for (int it = 0;; ++it) {
-        if (it == 1) pdl_wait();  // the counter is zeroed by the expansion
-        int x = blockIdx.x;
-        if (it > 0) {
-          if (lane == 0) x = (int)gridDim.x + atomicAdd(p.next, 1);
-          x = __shfl_sync(0xffffffffu, x, 0);
-        }
         Item w{-1, 0, 0, 0, 0, {0, 0}, 0};
-        if (find_work(p, x / c.Hkv, lane, w)) w.h = x % c.Hkv;
+        if (it == 0 || (long long)all_items * c.Hkv > gridDim.x) {  // else every item has its CTA
+          if (it == 1) pdl_wait();  // the counter is zeroed by the expansion
+          int x = blockIdx.x;
+          if (it > 0) {
+            if (lane == 0) x = (int)gridDim.x + atomicAdd(p.next, 1);
+            x = __shfl_sync(0xffffffffu, x, 0);
+          }
+          if (find_work(p, x / c.Hkv, lane, w, all_items)) w.h = x % c.Hkv;
+        }
         if (it >= 2 && !warp_wait_all(item_free + (it & 1), (it >> 1) - 1)) break;
         if (lane == 0) {
           items[it & 1] = w;
@@ -631,7 +645,7 @@ size_t kv4_prefill_bytes(const Kv4AttnArgs &a, long long total_kv) {
 cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, long long total_kv, void *workspace, int num_sms, cudaStream_t stream) {
   const int G = a.Hq / a.c.Hkv, cap = (int)tile_cap(a, total_kv);
   const size_t tiles = (size_t)cap * a.c.Hkv * 4 * kKv * a.c.D;
-  const PrefillKv4 p{a, G, kM / G, cap, reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + tiles),
+  const PrefillKv4 p{a, G, kM / G, (65536u + G - 1) / G, cap, reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + tiles),
                      static_cast<uint16_t *>(workspace)};
   return a.c.D == 128 ? launch_prefill_t<128>(p, num_sms, stream) : launch_prefill_t<64>(p, num_sms, stream);
 }
