@@ -57,6 +57,57 @@ GDN_DEV Group find_group(const Kv4Args &a, int x, int lane) {
   return r;
 }
 
+GDN_DEV uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Four pairs of floats -> eight E2M1 codes, the first in the lowest nibble
+GDN_DEV uint32_t e2m1x8_from_f32(const float2 (&v)[4]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+  return r;
+}
+GDN_DEV float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long *>(&r))
+      : "l"(*reinterpret_cast<unsigned long long *>(&x)), "l"(*reinterpret_cast<unsigned long long *>(&y)));
+  return r;
+}
+// quant_block16 of 16 BF16 values, the same steps two at a time (264 instructions a
+// block with it): the largest magnitude as an integer maximum of the bits, NaN and
+// infinity above all others.
+GDN_DEV bool quant_bf16x16(const uint4 (&x)[2], float ts, float inv6ts, uint32_t (&codes)[2], uint32_t &scale) {
+  const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+  uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_u16x2(m, w[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  codes[0] = codes[1] = scale = 0u;
+  if (m >= 0x7F80u) return false;
+  scale = e4m3_from_f32(__fmul_rn(__uint_as_float(m << 16), inv6ts));
+  const float sv = e4m3_to_f32(scale);
+  if (sv == 0.0f) return true;
+  const float r = __frcp_rn(__fmul_rn(sv, ts));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = mul2(make_float2(__uint_as_float(w[4 * k + i] << 16), __uint_as_float(w[4 * k + i] & 0xFFFF0000u)), make_float2(r, r));
+    codes[k] = e2m1x8_from_f32(v);
+  }
+  return true;
+}
+
 // Append. A CTA goes through its groups with two buffers: while it quantises one
 // group, a thread per 16-element block, the next one's rows come to shared memory
 // (a token's heads lie together: one bulk copy per token, 32 KB a buffer, three
@@ -127,12 +178,12 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
       for (int i = tid; i < hn * ITEMS; i += 256) {
         const int blk = i % NB, t = i / NB % 16, is_v = i / (16 * NB) & 1, h = i / ITEMS;
         if (t < r.t0 || t >= r.t1) continue;
-        float x[16];
-        load_bf16x16(&sm.rows[buf][is_v][t][h * D + blk * 16], x);
-        uint32_t lo, hi, scale;
-        if (!quant_block16(x, is_v ? a.vs : a.ks, is_v ? invv : invk, lo, hi, scale)) flag_status(a.status, GDN_E_NONFINITE);
+        const uint4 *row = reinterpret_cast<const uint4 *>(&sm.rows[buf][is_v][t][h * D + blk * 16]);
+        const uint4 x[2] = {row[0], row[1]};
+        uint32_t codes[2], scale;
+        if (!quant_bf16x16(x, is_v ? a.vs : a.ks, is_v ? invv : invk, codes, scale)) flag_status(a.status, GDN_E_NONFINITE);
         *reinterpret_cast<uint2 *>(g + h * head + (is_v ? kv4_v_code<D>(t, blk * 8) : kv4_k_code<D>(t, blk * 8))) =
-            make_uint2(lo, hi);
+            make_uint2(codes[0], codes[1]);
         sm.scales[h * 2 * D + (is_v ? kv4_v_scale<D>(t, blk) : kv4_k_scale<D>(t, blk)) - 16 * D] = (uint8_t)scale;
       }
     }
@@ -199,8 +250,9 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(RowsArgs p) {
       uint32_t o[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float2 y = __half22float2(v[m]);  // e2m1 x e4m3 is exact; one FP32 rounding by ts, one to BF16
-        o[m] = bf16x2(y.x * f * ts, y.y * f * ts);
+        // e2m1 x e4m3 is exact; one FP32 rounding by ts, one to BF16
+        const float2 y = mul2(mul2(__half22float2(v[m]), make_float2(f, f)), make_float2(ts, ts));
+        o[m] = bf16x2(y.x, y.y);
       }
       uint16_t *row = is_v ? p.v + (r.n0 + t) * p.v_stride : p.k + (r.n0 + t) * p.k_stride;
       reinterpret_cast<uint4 *>(row + (h0 + h) * D)[e] = make_uint4(o[0], o[1], o[2], o[3]);
