@@ -6,6 +6,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -116,9 +117,17 @@ int64_t rows_stride(const at::Tensor &t, const char *name, int heads, int d) {
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) {
   return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
-// The given output, checked, or a new one of the type
-at::Tensor output(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) {
-  if (!given(o)) return fresh(shape, type, like);
+// The given output, checked, or a new one of the type; where `stream` is another
+// than the current one, its memory is not handed out again before that is done.
+at::Tensor output(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like,
+                  PyObject *stream) {
+  if (!given(o)) {
+    at::Tensor t = fresh(shape, type, like);
+    if (given(stream) && t.numel() > 0)
+      c10::cuda::CUDACachingAllocator::recordStream(
+          t.storage().data_ptr(), c10::cuda::getStreamFromExternal(stream_of(stream), like.device().index()));
+    return t;
+  }
   const at::Tensor &t = tensor(o, name);
   const bool typed = type == at::kBFloat16 ? is_bf16(t) : t.scalar_type() == type;
   if (!typed || t.sizes() != shape || !t.is_cuda() || !t.is_contiguous())
@@ -168,7 +177,8 @@ PyObject *read(PyObject *const *a) {
   const kv4_batch b = batch(a[1], a[2], a[6], rows);
   const int64_t shape[3] = {rows, c.n_kv_heads, c.head_dim};
   const at::Tensor &p = THPVariable_Unpack(a[0]);
-  const at::Tensor k = output(a[7], "k", shape, at::kBFloat16, p), v = output(a[8], "v", shape, at::kBFloat16, p);
+  const at::Tensor k = output(a[7], "k", shape, at::kBFloat16, p, a[10]),
+                   v = output(a[8], "v", shape, at::kBFloat16, p, a[10]);
   check(kv4_read(&c, &b, u16_out(k), u16_out(v), status_word(a[9]), stream_of(a[10])), "kv4_read");
   return pair(k, v);
 }
@@ -188,8 +198,9 @@ PyObject *decode(PyObject *const *a) {
   const kv4_batch b = batch(a[2], a[3], Py_None, B * r);
   if (b.B != B) throw Bad("q and block_table disagree on the number of sequences");
   const bool want = PyObject_IsTrue(a[9]) == 1;
-  const at::Tensor out = output(a[7], "out", q.sizes(), at::kBFloat16, q);
-  const at::Tensor lse = want || given(a[8]) ? output(a[8], "lse", q.sizes().slice(0, q.dim() - 1), at::kFloat, q) : at::Tensor();
+  const at::Tensor out = output(a[7], "out", q.sizes(), at::kBFloat16, q, a[12]);
+  const at::Tensor lse = want || given(a[8]) ? output(a[8], "lse", q.sizes().slice(0, q.dim() - 1), at::kFloat, q, a[12])
+                                              : at::Tensor();
   const cudaStream_t s = stream_of(a[12]);
   size_t n;
   const at::Tensor ws = workspace(a[10], kv4_decode_workspace(&c, &b, as_int(Hq, "q")), q, a[12], s, n);
@@ -207,8 +218,9 @@ PyObject *prefill(PyObject *const *a) {
   const kv4_batch b = batch(a[2], a[3], a[4], q.size(0));
   const int64_t total = given(a[7]) ? whole(a[7]) : (int64_t)b.B * b.max_pages * c.page_tokens;
   const bool want = PyObject_IsTrue(a[11]) == 1;
-  const at::Tensor out = output(a[9], "out", q.sizes(), at::kBFloat16, q);
-  const at::Tensor lse = want || given(a[10]) ? output(a[10], "lse", q.sizes().slice(0, 2), at::kFloat, q) : at::Tensor();
+  const at::Tensor out = output(a[9], "out", q.sizes(), at::kBFloat16, q, a[14]);
+  const at::Tensor lse = want || given(a[10]) ? output(a[10], "lse", q.sizes().slice(0, 2), at::kFloat, q, a[14])
+                                               : at::Tensor();
   const cudaStream_t s = stream_of(a[14]);
   size_t n;
   const at::Tensor ws = workspace(a[12], kv4_prefill_workspace(&c, &b, total, Hq), q, a[14], s, n);
@@ -251,8 +263,9 @@ PyObject *compact(PyObject *const *a) {
   const int32_t *table = i32(a[1], "block_table", 2);
   const at::Tensor &t = THPVariable_Unpack(a[1]), &p = THPVariable_Unpack(a[0]);
   const int64_t num[1] = {l.num}, one[1] = {1};
-  const at::Tensor out = output(a[2], "tables_out", t.sizes(), at::kInt, p), map = output(a[3], "page_map", num, at::kInt, p),
-                   live = output(a[4], "n_live", one, at::kInt, p);
+  const at::Tensor out = output(a[2], "tables_out", t.sizes(), at::kInt, p, a[7]),
+                   map = output(a[3], "page_map", num, at::kInt, p, a[7]),
+                   live = output(a[4], "n_live", one, at::kInt, p, a[7]);
   const cudaStream_t s = stream_of(a[7]);
   size_t n;
   const at::Tensor ws = workspace(a[5], kv4_compact_workspace(l.num), p, a[7], s, n);

@@ -15,6 +15,7 @@ pages of all layers.
 """
 from __future__ import annotations
 
+import contextlib
 import importlib
 
 import torch
@@ -232,15 +233,22 @@ class KV4Cache:
     def _dev(self, rows):
         return torch.tensor(rows, dtype=torch.int32).pin_memory().to(self.device, non_blocking=True)
 
+    @staticmethod
+    def _on(stream):
+        """Tables are uploaded, used and freed in the order of one stream."""
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
     def grow(self, seqs, tokens, stream=None) -> KV4Batch:
         """Room for tokens[i] (or `tokens` each) new tokens of every sequence,
-        the copies of shared pages made, and the batch of the new rows."""
+        the copies of shared pages made, and the batch of the new rows; all on
+        `stream` (default: the current one), where the batch is to be used."""
         tokens = [tokens] * len(seqs) if isinstance(tokens, int) else list(tokens)
         pairs = self.book.extend(seqs, tokens)
-        if pairs:
-            src, dst = self._dev([p[0] for p in pairs]), self._dev([p[1] for p in pairs])
-            kv4_copy_pages(self.layers, src, dst, dev_status=self.status, stream=stream)
-        return self.batch(seqs, tokens)
+        with self._on(stream):
+            if pairs:
+                src, dst = self._dev([p[0] for p in pairs]), self._dev([p[1] for p in pairs])
+                kv4_copy_pages(self.layers, src, dst, dev_status=self.status)
+            return self.batch(seqs, tokens)
 
     def batch(self, seqs, tokens) -> KV4Batch:
         """The tables of the sequences as they are, their newest tokens[i] as the rows."""
@@ -271,8 +279,9 @@ class KV4Cache:
         seqs = list(self.book.seqs)
         pages = [self.book.pages(s) for s in seqs]
         cols = max([1] + [len(p) for p in pages])
-        table = self._dev([p + [-1] * (cols - len(p)) for p in pages] or [[-1]])
-        kv4_compact(self.layers, table, dev_status=self.status, stream=stream)
+        with self._on(stream):
+            table = self._dev([p + [-1] * (cols - len(p)) for p in pages] or [[-1]])
+            kv4_compact(self.layers, table, dev_status=self.status)
         self.book.compact()
         return self.book.num_pages - self.book.free_pages
 

@@ -580,3 +580,42 @@ def test_python_refusals_on_the_gpu(g):
         g.kv4_decode(odd, pages, tab, n, KS, VS)
     with pytest.raises(g.GdnError, match="GDN_E_SHAPE"):    # rows 4 elements off a multiple of 8 apart
         g.kv4_decode(torch.zeros(2, hq * d + 4, dtype=torch.bfloat16, device="cuda")[:, :hq * d].view(2, hq, d), pages, tab, n, KS, VS)
+
+
+def test_a_side_stream_throughout(g):
+    """A cache used on a side stream only, its outputs dropped and reallocated
+    on the current one meanwhile: the results are those of the current stream."""
+    hq, hkv, d = 8, 2, 128
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    rows = [torch.randn(300, hq + 2 * hkv, d, generator=gen, device="cuda").bfloat16() for _ in range(3)]
+    want = []
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        c = g.KV4Cache(64, 16, hkv, d, KS, VS)
+        a, b = c.new(), c.new()
+        torch.cuda.synchronize()
+        outs = []
+        for k, x in enumerate(rows):
+            if k == 1:
+                f = c.fork(a)
+            seqs = [a, b] if k == 0 else [a, f, b]
+            counts = [200, 100] if k == 0 else [100, 100, 100]
+            batch = c.grow(seqs, counts, stream=stream)
+            c.append(0, x[:, hq:hq + hkv], x[:, hq + hkv:], batch, stream=stream)
+            out = c.prefill(0, x[:, :hq], batch, stream=stream)
+            if stream is not None:
+                side.synchronize()
+            outs.append(out.clone())
+            for _ in range(4):
+                c.prefill(0, x[:, :hq], batch, stream=stream)            # dropped at once
+                torch.full((300, hq, d), 3.0, dtype=torch.bfloat16, device="cuda")
+            if k == 1:
+                c.free(b)
+                b = c.new()
+                c.compact(stream=stream)
+        torch.cuda.synchronize()
+        assert c.check() == 0
+        if stream is None:
+            want = outs
+        else:
+            assert all(torch.equal(x, y) for x, y in zip(outs, want))
