@@ -112,10 +112,13 @@ GDN_DEV bool quant_bf16x16(const uint4 (&x)[2], float ts, float inv6ts, uint32_t
 // group, a thread per 16-element block, the next one's rows come to shared memory
 // (a token's heads lie together: one bulk copy per token, 32 KB a buffer, three
 // CTAs an SM). Its warps find eight groups at once, one each: finding them one by
-// one, a chain of three loads, took longer than the group itself. The scales are gathered in
-// shared memory and leave as 16-byte words where all of the group's tokens are
-// new: a V scale is a byte 16 bytes from its token's next one, and single bytes
-// cost more memory transactions than all the codes.
+// one, a chain of three loads, took longer than the group itself. The scales are
+// gathered in shared memory and leave as 16-byte words where all of the group's
+// tokens are new: a V scale is a byte 16 bytes from its token's next one, and
+// single bytes cost more memory transactions than all the codes.
+// Bound by issue slots (a block's 16 values: a maximum, a division, 16 products,
+// 8 conversions) beside the bytes: 16384 rows of 8 heads, d = 128, 67 MB read as
+// rows: 25.7 us.
 template <int D>
 struct AppendSmem {
   uint16_t rows[2][2][16][kHeads * D];  // [buffer][K, V][token]
@@ -207,7 +210,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
 }
 
 // Read back: a thread takes half a block (4 code bytes in, 16 bytes out), so that a
-// warp's stores are whole lines (with a block a thread 30 us instead of 25).
+// warp's stores are whole lines. 16384 rows of 8 heads, d = 128, 26 MB read and
+// 67 written: 22 us (a block a thread, whose stores are half lines, took 5 more).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(RowsArgs p) {
   constexpr int NH = D / 8, ITEMS = 2 * 16 * NH;  // half blocks of a row; of a head's K and V of 16 tokens
@@ -283,6 +287,8 @@ cudaError_t launch_append(const RowsArgs &p, cudaStream_t stream) {
 // ---------------------------------------------------------------- pages
 constexpr int kCopyChunk = 16384;  // bytes of one page and layer that one CTA moves: 4 x 16 bytes a thread
 
+// Bound by the bytes: 700 pages, 413 MB read and written, 62 us cold, 0.98 of the
+// copy bandwidth.
 // n_dev (compaction): the number of copies comes from the plan, and the tables
 // are rewritten by its map beside the copies.
 __global__ void __launch_bounds__(256) copy_pages_kernel(Kv4PageArgs a, const int32_t *n_dev) {
@@ -339,7 +345,8 @@ CompactWs compact_ws(void *p, int num_pages) {
 // One CTA: a bitmap of the live pages in shared memory, its prefix counts, and
 // from them every page's new id, a thread per page. With before(p) the live pages
 // below p: a hole p < L is the (p - before(p))-th, a live p >= L the
-// (before(p) - before(L))-th to move.
+// (before(p) - before(L))-th to move. A chain of one CTA's barriers and of the
+// tables' loads: 5 to 8 us whatever the size.
 __global__ void __launch_bounds__(1024) compact_plan_kernel(Kv4PageArgs a, CompactWs w) {
   extern __shared__ uint32_t bits[];
   __shared__ int sums[32], prefix[1024], live_total;

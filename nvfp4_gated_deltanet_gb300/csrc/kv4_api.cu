@@ -202,9 +202,9 @@ gdn_status kv4_compact(uint8_t *pages, int n_layers, int64_t layer_stride, int n
   if (!page_map || !n_live || !workspace || ((long long)rows * cols > 0 && (!block_table || !tables_out)))
     return GDN_E_NULL;
   if (workspace_bytes < kv4_compact_bytes(num_pages)) return GDN_E_SHAPE;
-  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(tables_out) |
-       reinterpret_cast<uintptr_t>(page_map) | reinterpret_cast<uintptr_t>(n_live) |
-       (reinterpret_cast<uintptr_t>(workspace) & 12u)) & 3u || !aligned16(workspace))
+  const uintptr_t words = reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(tables_out) |
+                          reinterpret_cast<uintptr_t>(page_map) | reinterpret_cast<uintptr_t>(n_live);
+  if ((words & 3u) || !aligned16(workspace))
     return GDN_E_ALIGN;
   return cuda_status(launch_kv4_compact(a, static_cast<cudaStream_t>(stream)));
 }
