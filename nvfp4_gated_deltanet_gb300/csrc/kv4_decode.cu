@@ -86,6 +86,7 @@ struct DecodeShape {
 struct DecodeArgs {
   Kv4AttnArgs a;
   int r, G, RG;      // new tokens per sequence, query heads per KV head, row groups per (sequence, KV head)
+  uint32_t inv_g;    // ceil(2^16 / G): x / G = x inv_g >> 16 for x < 128 (G <= 64)
   int extra;         // cost of an item beside its tiles, in tiles; kWhole: runs hold whole items, nothing to join
   float *part;       // [2 CTAs][rows][D] and, after them, their (m, l) [2 CTAs][rows][2]
 };
@@ -108,8 +109,9 @@ constexpr int kRoundsCta = 3, kRoundsTeam = 6;
 constexpr int kWhole = 1 << 20;  // the `extra` of whole items
 
 // a / b, mostly in 32 bits
+__device__ __noinline__ long long quot64(long long a, long long b) { return a / b; }
 GDN_DEV long long quot(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : quot64(a, b);
 }
 
 // Sequence b's tokens, checked (kv4_seq without rows), and its tiles: an empty
@@ -205,27 +207,42 @@ GDN_DEV Cuts find_cuts(const DecodeArgs &p, int warps, int HR, int lane, int mos
   k.rest = (int)(units - k.q * k.N);
   return k;
 }
-// Run `run` of at most `most`: its first tile and how many tiles it has.
+// Cut `cut` of at most `most` runs: the tile there, and how many lie before it.
+// With whole items, runs have as many each, and a run's tiles are counted from
+// its own beginning: `from` is the run's first cut.
 template <int TILE>
-GDN_DEV int find_run(const DecodeArgs &p, int warps, int HR, int lane, int run, int most, Cursor &k) {
+GDN_DEV long long find_cut(const DecodeArgs &p, int warps, int HR, int lane, int from, int cut, int most, Cursor &k) {
   const Kv4Args &c = p.a.c;
   k = Cursor{0, 0, 0, 0, 0};
-  if (p.extra == kWhole) {  // runs of whole items, as many in each
+  if (p.extra == kWhole) {
     const int items = c.B * HR;
-    const int i0 = (int)quot((long long)items * run, most), i1 = (int)quot((long long)items * (run + 1), most);
+    const int i0 = (int)quot((long long)items * from, most), i1 = (int)quot((long long)items * cut, most);
     int n = 0;
     for (int i = i0; i < i1; ++i) n += tiles_of<TILE>(seq_len(c, i / HR));
-    if (n) {
-      seek<TILE>(c, k, i0 / HR);
-      k.hr = i0 % HR;
+    if (i1 < items) {
+      seek<TILE>(c, k, i1 / HR);
+      k.hr = i1 % HR;
     }
     return n;
   }
   const Cuts x = find_cuts<TILE>(p, warps, HR, lane, most);
-  if (run >= x.N) return 0;
-  Cursor end;
-  const long long t1 = run + 1 == x.N ? x.tiles : find_tile<TILE>(c, x.at(run + 1), HR, p.extra, lane, x.n0, end);
-  return (int)(t1 - find_tile<TILE>(c, x.at(run), HR, p.extra, lane, x.n0, k));
+  return cut >= x.N ? x.tiles : find_tile<TILE>(c, x.at(cut), HR, p.extra, lane, x.n0, k);
+}
+
+// A group of an item's query rows, ROWS at most: row x is a (token, query head).
+struct RowGroup {
+  int h, rows;       // the KV head, the rows
+  int tok, off, G;   // the first row's token, and its place among that token's heads
+  uint32_t inv_g;
+  GDN_DEV int over(int x) const { return (int)((uint32_t)(off + x) * inv_g >> 16); }
+  GDN_DEV int token(int x) const { return tok + over(x); }
+  GDN_DEV int head(int x) const { return off + x - over(x) * G; }
+};
+template <int ROWS>
+GDN_DEV RowGroup row_group(const DecodeArgs &p, int hr) {
+  const int h = p.RG == 1 ? hr : hr / p.RG, row0 = (hr - h * p.RG) * ROWS;
+  const int tok = row0 ? row0 / p.G : 0;
+  return {h, min(ROWS, p.r * p.G - row0), tok, row0 - tok * p.G, p.G, p.inv_g};
 }
 
 GDN_DEV uint32_t transpose8x8(uint32_t x) {
@@ -266,7 +283,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   uint2 *qsm = reinterpret_cast<uint2 *>(tail_sm);
   uint64_t *full = reinterpret_cast<uint64_t *>(tail_sm + S::kQ), *q_full = full + S::kSlots + team;
   volatile uint32_t *abort_flag = reinterpret_cast<uint32_t *>(full + S::kSlots + S::kTeams);
-  const int HR = c.Hkv * p.RG, R = p.r * p.G;
+  const int HR = c.Hkv * p.RG;
   auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * W) : "memory"); };
   pdl_launch_dependents();  // kv4_join_kernel finds its places meanwhile
   if (threadIdx.x == 0) {
@@ -277,30 +294,30 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   __syncthreads();
   Cursor cur;
   int n_tiles;
-  {  // the team's first warp finds its run for all (16 warps at once took 2 us of the issue slots)
+  {  // the team's first two warps find its run's ends for all (16 warps at once took 2 us of the issue slots)
     struct Found {
       Cursor k;
-      int n;
+      long long at;
     };
     volatile Found *found = reinterpret_cast<volatile Found *>(meet);
-    if (warp == 0) {
-      n_tiles = find_run<TILE>(p, W, HR, lane, run, gridDim.x * S::kTeams, cur);
+    if (warp < 2) {
+      const long long n = find_cut<TILE>(p, W, HR, lane, run, run + warp, gridDim.x * S::kTeams, cur);
       if (lane == 0) {
-        found->k.b = cur.b;
-        found->k.hr = cur.hr;
-        found->k.tile = cur.tile;
-        found->k.nt = cur.nt;
-        found->k.len = cur.len;
-        found->n = n_tiles;
+        found[warp].k.b = cur.b;
+        found[warp].k.hr = cur.hr;
+        found[warp].k.tile = cur.tile;
+        found[warp].k.nt = cur.nt;
+        found[warp].k.len = cur.len;
+        found[warp].at = n;
       }
     }
     team_sync();
-    cur.b = found->k.b;
-    cur.hr = found->k.hr;
-    cur.tile = found->k.tile;
-    cur.nt = found->k.nt;
-    cur.len = found->k.len;
-    n_tiles = found->n;
+    cur.b = found[0].k.b;
+    cur.hr = found[0].k.hr;
+    cur.tile = found[0].k.tile;
+    cur.nt = found[0].k.nt;
+    cur.len = found[0].k.len;
+    n_tiles = (int)(found[1].at - found[0].at);
   }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < c.B; b += S::kThreads)
@@ -334,7 +351,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
         const int pos = k.tile * TILE + (lane % GR) * 16;
         if (pos < k.len) {
           ld_src = kv4_group<D>(c, k.b, pos);
-          if (ld_src) ld_src += (k.hr / p.RG) * kv4_head_bytes<D>(c);
+          if (ld_src) ld_src += (p.RG == 1 ? k.hr : k.hr / p.RG) * kv4_head_bytes<D>(c);
         }
       }
     }
@@ -349,15 +366,17 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   };
   // The team's warp 0 loads the query rows of a segment, one per lane.
   auto load_q = [&](const Cursor &k) {
-    const int row0 = (k.hr % p.RG) * S::kRows, rows = min(S::kRows, R - row0), ri = row0 + lane;
+    const RowGroup rg = row_group<S::kRows>(p, k.hr);
+    const int rows = rg.rows;
     if (lane == 0) mbar_arrive_expect_tx(q_full, rows * D * 2);
     __syncwarp();
     if (lane < rows)
       bulk_g2s(qraw + lane * (D * 2),
-               p.a.q + ((long long)k.b * p.r + ri / p.G) * p.a.q_stride + (long long)(k.hr / p.RG * p.G + ri % p.G) * D,
+               p.a.q + ((long long)k.b * p.r + rg.token(lane)) * p.a.q_stride + (long long)(rg.h * p.G + rg.head(lane)) * D,
                D * 2, q_full);
   };
   if (warp == 0 && n_tiles > 0) load_q(cur);
+#pragma unroll 1
   for (int i = 0; i < 2; ++i)
     if (ld < n_tiles) load(i);
 
@@ -366,14 +385,13 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   bool alive = true;
   for (int sg = 0; at < n_tiles; ++sg) {
     const int seg = min(cur.nt - cur.tile, n_tiles - at);
-    const int h = cur.hr / p.RG, row0 = (cur.hr % p.RG) * S::kRows;
-    const int rows = min(S::kRows, R - row0);
     const bool mine = next < at + seg;
     // ------------------------------------------------ q: B operand, lane (g, t) = row g, channels t D/4 ...
     uint2 qf[S::kQShared ? 1 : NQ][S::kQShared ? 1 : KS];
     float cs[NQ][2];   // sm k_scale log2 e / the row's scale, of columns 2t and 2t + 1
     int last[NQ][2];   // the last token that the row sees
     float O[KS][NQ][4], m[NQ][2], l[NQ][2];
+    const RowGroup qg = row_group<S::kRows>(p, cur.hr);
     if (alive && !__all_sync(0xffffffffu, wait_or_abort(q_full, (uint32_t)sg & 1u, abort_flag, c.status))) alive = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -381,7 +399,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
       uint4 w[D / 32];
       const uint4 *qp = reinterpret_cast<const uint4 *>(qraw + row * (D * 2) + t * (D / 2));
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) w[i] = row < rows ? qp[i] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < D / 32; ++i) w[i] = row < qg.rows ? qp[i] : make_uint4(0, 0, 0, 0);
       uint32_t mx = 0;  // the largest magnitude, as BF16 bits (a NaN counts as the largest: its row is NaN anyway)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -416,8 +434,8 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
         cs[n][e2] = __shfl_sync(0xffffffffu, inv, (2 * t + e2) * 4);
-        const int rr = row0 + n * 8 + 2 * t + e2;
-        last[n][e2] = n * 8 + 2 * t + e2 < rows ? cur.len - p.r + rr / p.G : -1;
+        const int rr = n * 8 + 2 * t + e2;
+        last[n][e2] = rr < qg.rows ? cur.len - p.r + qg.token(rr) : -1;
         m[n][e2] = -INFINITY;
         l[n][e2] = 0.0f;
       }
@@ -633,7 +651,8 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
       }
     }
     team_sync();
-    for (int i = tid; i < rows * (D / 4); i += 32 * W) {
+    const RowGroup rg = row_group<S::kRows>(p, cur.hr);
+    for (int i = tid; i < rg.rows * (D / 4); i += 32 * W) {
       const int row = i / (D / 4), d4 = i % (D / 4) * 4;
       float top = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -649,8 +668,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
         o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
       }
       if (done) {
-        const int ri = row0 + row;
-        const long long out = ((long long)cur.b * p.r + ri / p.G) * p.a.Hq + h * p.G + ri % p.G;
+        const long long out = ((long long)cur.b * p.r + rg.token(row)) * p.a.Hq + rg.h * p.G + rg.head(row);
         const float inv = sum == 0.0f ? 0.0f : c.vs / sum;
         *reinterpret_cast<uint2 *>(p.a.out + out * D + d4) =
             make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
@@ -675,7 +693,8 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
 // CTA of the first cut inside an item, or with whole-CTA teams (fewer items than
 // cuts, more pieces) by a CTA per item and row.
 // Few pieces: a warp per row. More: the CTA's warps take every eighth piece of a
-// row. most: runs at most, as in the decode kernel.
+// row. most: runs at most, as in the decode kernel. 3 to 3.5 us of latency behind
+// the decode kernel (the first loads of a piece depend on the plan's search).
 template <int D, int NQ, int TEAM>
 __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
   using S = DecodeShape<D, NQ, TEAM>;
@@ -683,7 +702,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
   __shared__ float sh[8][D + 2];
   const Kv4Args &c = p.a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int HR = c.Hkv * p.RG, R = p.r * p.G;
+  const int HR = c.Hkv * p.RG;
   const Cuts x = find_cuts<S::kTile>(p, S::kTeam, HR, lane, most);
   Cursor k{0, 0, 0, 0, 0};
   int cut;           // the first cut inside the item
@@ -707,12 +726,13 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
     cut = (int)quot((a0 + p.extra + 1) * x.N - 1, x.q * x.N + x.rest) + 1;
     mine = cut < x.N && x.at(cut) < a0 + p.extra + k.nt;
   }
-  pdl_wait();  // on every path: this grid must not end before the one it follows
-  if (!mine) return;
   // pieces: runs cut - 1 (where the item may be its first segment, or its last) to the one of its last tile
   const int np = (int)quot((a0 + p.extra + k.nt) * x.N - 1, x.q * x.N + x.rest) - cut + 2;
   const bool first = x.at(cut - 1) >= a0;
-  const int h = k.hr / p.RG, row0 = (k.hr % p.RG) * S::kRows, rows = min(S::kRows, R - row0);
+  const RowGroup rg = row_group<S::kRows>(p, k.hr);
+  const int rows = rg.rows;
+  pdl_wait();  // on every path: this grid must not end before the one it follows
+  if (!mine) return;
   const float *ml = p.part + 2 * (size_t)most * S::kRows * D;
   auto piece = [&](int j, int row) { return (2 * (size_t)(cut - 1 + j) + (j > 0 || first ? 0 : 1)) * S::kRows + row; };
   float m, l, o[E];
@@ -751,8 +771,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
     }
   };
   auto out_row = [&](int row) {
-    const int ri = row0 + row;
-    return ((long long)k.b * p.r + ri / p.G) * p.a.Hq + h * p.G + ri % p.G;
+    return ((long long)k.b * p.r + rg.token(row)) * p.a.Hq + rg.h * p.G + rg.head(row);
   };
   if (np <= 8) {
     for (int row = blockIdx.y + gridDim.y * warp; row < rows; row += gridDim.y * 8) {
@@ -872,7 +891,8 @@ size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms) { return a.c.T ? deco
 
 cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
   const DecodePlan d = decode_plan(a, num_sms);
-  const DecodeArgs p{a, a.c.T / a.c.B, a.Hq / a.c.Hkv, d.RG, d.extra, static_cast<float *>(workspace)};
+  const int G = a.Hq / a.c.Hkv;
+  const DecodeArgs p{a, a.c.T / a.c.B, G, d.RG, (uint32_t)((65536 + G - 1) / G), d.extra, static_cast<float *>(workspace)};
   if (a.c.D == 128)
     return d.NQ == 1 ? launch_decode<128, 1>(p, d, stream) : d.NQ == 2 ? launch_decode<128, 2>(p, d, stream)
                                                                        : launch_decode<128, 4>(p, d, stream);
