@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
     mbar_init(&sm.landed[1], 1);
     fence_barrier_init();
   }
+  kv4_begin();
   auto fetch = [&](int item, int k, int buf) {  // warp 0: the rows of found[k]
     const Group r = sm.found[k];
     if (r.b < 0) return;
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(RowsArgs p) {
   __shared__ uint8_t *place;
   const Kv4Args &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31;
+  kv4_begin();
   if (tid < 32) {
     const Group r = find_group(a, blockIdx.x, lane);
     if (lane == 0) {
@@ -280,8 +282,7 @@ cudaError_t launch_append(const RowsArgs &p, cudaStream_t stream) {
   static bool allowed[64];
   cudaError_t e = kv4_allow_smem(kv4_append_kernel<D>, sizeof(AppendSmem<D>), allowed);
   if (e != cudaSuccess) return e;
-  kv4_append_kernel<D><<<min(p.items, 3 * 152), 256, sizeof(AppendSmem<D>), stream>>>(p);
-  return cudaGetLastError();
+  return kv4_launch(kv4_append_kernel<D>, min(p.items, 3 * 152), 256, sizeof(AppendSmem<D>), stream, p);
 }
 
 // ---------------------------------------------------------------- pages
@@ -293,8 +294,8 @@ constexpr int kCopyChunk = 16384;  // bytes of one page and layer that one CTA m
 // are rewritten by its map beside the copies.
 __global__ void __launch_bounds__(256) copy_pages_kernel(Kv4PageArgs a, const int32_t *n_dev) {
   int n = a.n;
+  kv4_begin();
   if (n_dev) {
-    pdl_wait();  // the plan is made
     n = *n_dev;
     const long long entries = (long long)a.rows * a.cols;
     for (long long i = blockIdx.x * 256LL + threadIdx.x; i < entries; i += gridDim.x * 256LL) {
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(1024) compact_plan_kernel(Kv4PageArgs a, Compa
   extern __shared__ uint32_t bits[];
   __shared__ int sums[32], prefix[1024], live_total;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_launch_dependents();
+  kv4_begin();
   const int words = (a.num_pages + 31) / 32;
   for (int i = tid; i < words; i += 1024) bits[i] = 0;
   __syncthreads();
@@ -435,16 +436,13 @@ cudaError_t launch_kv4_read(const Kv4Args &a, uint16_t *k, uint16_t *v, cudaStre
   int chunks;
   const RowsArgs p = rows_args(a, k, stride, v, stride, groups, chunks);
   const dim3 grid((unsigned)groups, (unsigned)chunks);
-  if (a.D == 128) kv4_read_kernel<128><<<grid, 256, 0, stream>>>(p);
-  else kv4_read_kernel<64><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return kv4_launch(a.D == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, grid, 256, 0, stream, p);
 }
 
 cudaError_t launch_kv4_copy_pages(const Kv4PageArgs &a, cudaStream_t stream) {
   const long long total = (long long)a.n * a.layers * ((a.page_bytes + kCopyChunk - 1) / kCopyChunk);
   if (total == 0) return cudaSuccess;
-  copy_pages_kernel<<<(unsigned)min(total, 152LL * 8), 256, 0, stream>>>(a, nullptr);
-  return cudaGetLastError();
+  return kv4_launch(copy_pages_kernel, (unsigned)min(total, 152LL * 8), 256, 0, stream, a, nullptr);
 }
 
 size_t kv4_compact_bytes(int num_pages) { return sizeof(int32_t) * (4 + 2 * (size_t)((num_pages + 3) / 4 * 4)); }
@@ -455,22 +453,12 @@ cudaError_t launch_kv4_compact(const Kv4PageArgs &a, cudaStream_t stream) {
   static bool allowed[64];
   cudaError_t e = kv4_allow_smem(compact_plan_kernel, 128 * 1024, allowed);
   if (e != cudaSuccess) return e;
-  compact_plan_kernel<<<1, 1024, smem, stream>>>(a, w);
-  e = cudaGetLastError();
+  e = kv4_launch(compact_plan_kernel, 1, 1024, smem, stream, a, w);
   if (e != cudaSuccess) return e;
   Kv4PageArgs c = a;
   c.src = w.src;
   c.dst = w.dst;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(152 * 8, 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, copy_pages_kernel, c, (const int32_t *)w.n_moves);
+  return kv4_launch(copy_pages_kernel, 152 * 8, 256, 0, stream, c, w.n_moves);
 }
 
 }  // namespace gdn

@@ -285,12 +285,12 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   volatile uint32_t *abort_flag = reinterpret_cast<uint32_t *>(full + S::kSlots + S::kTeams);
   const int HR = c.Hkv * p.RG;
   auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * W) : "memory"); };
-  pdl_launch_dependents();  // kv4_join_kernel finds its places meanwhile
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kSlots + S::kTeams; ++s) mbar_init(full + s, 1);
     *abort_flag = 0u;
     fence_barrier_init();
   }
+  kv4_begin();  // kv4_join_kernel finds its places meanwhile
   __syncthreads();
   Cursor cur;
   int n_tiles;
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
   const bool first = x.at(cut - 1) >= a0;
   const RowGroup rg = row_group<S::kRows>(p, k.hr);
   const int rows = rg.rows;
-  pdl_wait();  // on every path: this grid must not end before the one it follows
+  kv4_begin();  // on every path: this grid must not end before the one it follows
   if (!mine) return;
   const float *ml = p.part + 2 * (size_t)most * S::kRows * D;
   auto piece = [&](int j, int row) { return (2 * (size_t)(cut - 1 + j) + (j > 0 || first ? 0 : 1)) * S::kRows + row; };
@@ -821,21 +821,12 @@ cudaError_t launch_decode_t(const DecodeArgs &p, int ctas, cudaStream_t stream) 
   static bool allowed[64];
   cudaError_t e = kv4_allow_smem(kv4_decode_kernel<D, NQ, TEAM>, S::kBytes, allowed);
   if (e != cudaSuccess) return e;
-  kv4_decode_kernel<D, NQ, TEAM><<<ctas, S::kThreads, S::kBytes, stream>>>(p);
-  if (p.extra == kWhole) return cudaGetLastError();
-  cudaLaunchConfig_t cfg = {};
+  e = kv4_launch(kv4_decode_kernel<D, NQ, TEAM>, ctas, S::kThreads, S::kBytes, stream, p);
   const int most = ctas * S::kTeams;  // runs, and cuts but one
-  if (most < 2) return cudaGetLastError();
-  cfg.gridDim = TEAM ? dim3((unsigned)most - 1, 1, 1)
-                     : dim3((unsigned)(p.a.c.B * p.a.c.Hkv * p.RG), S::kRows < p.r * p.G ? S::kRows : p.r * p.G, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NQ, TEAM>, p, most);
+  if (e != cudaSuccess || p.extra == kWhole || most < 2) return e;
+  const dim3 grid = TEAM ? dim3((unsigned)most - 1, 1, 1)
+                         : dim3((unsigned)(p.a.c.B * p.a.c.Hkv * p.RG), S::kRows < p.r * p.G ? S::kRows : p.r * p.G, 1);
+  return kv4_launch(kv4_join_kernel<D, NQ, TEAM>, grid, 256, 0, stream, p, most);
 }
 
 // Query rows per (sequence, KV head) -> 8-row column blocks of one item.

@@ -97,7 +97,7 @@ GDN_DEV int find_item(int B, int x, int lane, F count, int &before, int &total) 
 template <int D>
 __global__ void __launch_bounds__(256) kv4_expand_kernel(PrefillKv4 p) {
   const Kv4Args &c = p.a.c;
-  pdl_launch_dependents();
+  kv4_begin();
   const int tid = threadIdx.x, lane = tid & 31;
   const int x = blockIdx.x / c.Hkv, h = blockIdx.x % c.Hkv;
   int before = 0, total = 0;
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         __syncwarp();
         if (w.h < 0) break;
       }
-      pdl_wait();  // on every path: this grid must not end before the one it follows
+      kv4_begin();  // on every path: this grid must not end before the one it follows
     }
   }
   tc_fence_before();
@@ -617,19 +617,10 @@ cudaError_t launch_prefill_t(const PrefillKv4 &p, int num_sms, cudaStream_t stre
   cudaError_t e = kv4_allow_smem(kv4_prefill_kernel<D>, S::kBytes, allowed);
   if (e != cudaSuccess) return e;
   const Kv4Args &c = p.a.c;
-  kv4_expand_kernel<D><<<(unsigned)p.cap * c.Hkv, 256, 0, stream>>>(p);
-  cudaLaunchConfig_t cfg = {};
+  e = kv4_launch(kv4_expand_kernel<D>, (unsigned)p.cap * c.Hkv, 256, 0, stream, p);
+  if (e != cudaSuccess) return e;
   const long long items = (long long)(c.T / (2 * p.tpt) + c.B) * c.Hkv;  // at most
-  cfg.gridDim = dim3((unsigned)(items < num_sms ? items : num_sms), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = S::kBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_prefill_kernel<D>, tmQ, p);
+  return kv4_launch(kv4_prefill_kernel<D>, (unsigned)(items < num_sms ? items : num_sms), kThreads, S::kBytes, stream, tmQ, p);
 }
 
 // K / V tiles: every sequence's last one may be partly filled.

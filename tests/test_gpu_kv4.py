@@ -619,3 +619,64 @@ def test_a_side_stream_throughout(g):
             want = outs
         else:
             assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_order_among_streams_and_other_kernels(g, graph):
+    """Inputs written on another stream (an event between) and by copies, fills
+    and kernels of other libraries just before a call, and overwritten just after
+    it: every call sees what came before it in its stream."""
+    hkv, d, T = 4, 128, 512
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    src = torch.randn(2, T, hkv, d, generator=gen, device="cuda").bfloat16()
+    q = torch.randn(1, 1, 8, d, generator=gen, device="cuda").bfloat16()
+    table = torch.randperm(T // 16, generator=gen, device="cuda").int().view(1, -1)
+    full = torch.tensor([T], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    big = torch.randn(4096, 4096, generator=gen, device="cuda").bfloat16()
+
+    def fresh():
+        return g.kv4_new_pages(T // 16, 16, hkv, d)
+
+    want_pages = fresh()
+    g.kv4_append(src[0], src[1], want_pages, table, full, KS, VS, q_start=start)
+    want = [*g.kv4_read(want_pages, table, full, KS, VS, T, q_start=start), g.kv4_decode(q, want_pages, table, full, KS, VS)]
+    pages, rows, lens, tab = fresh(), torch.zeros_like(src), torch.zeros_like(full), torch.zeros_like(table)
+    spare = fresh()
+    got = [torch.zeros_like(x) for x in want]
+    side = torch.cuda.Stream()
+
+    def go():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                big @ big
+            rows.copy_(src)
+        lens.copy_(full)
+        tab.copy_(table)
+        g.kv4_append(src[1], src[0], spare, tab, lens, KS, VS, q_start=start)
+        here.wait_stream(side)
+        g.kv4_append(rows[0], rows[1], pages, tab, lens, KS, VS, q_start=start)
+        rows.zero_()
+        g.kv4_read(pages, tab, lens, KS, VS, T, q_start=start, k=got[0], v=got[1])
+        g.kv4_decode(q, pages, tab, lens, KS, VS, out=got[2])
+        lens.zero_()
+        tab.zero_()
+        pages.zero_()
+
+    if graph:
+        run = torch.cuda.Stream()
+        run.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(run):
+            go()
+        torch.cuda.current_stream().wait_stream(run)
+        cuda_graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cuda_graph):
+            go()
+    for _ in range(10):
+        for x in got:
+            x.zero_()
+        cuda_graph.replay() if graph else go()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
