@@ -88,7 +88,8 @@ struct DecodeArgs {
   int r, G, RG;      // new tokens per sequence, query heads per KV head, row groups per (sequence, KV head)
   uint32_t inv_g;    // ceil(2^16 / G): x / G = x inv_g >> 16 for x < 128 (G <= 64)
   int extra;         // cost of an item beside its tiles, in tiles; kWhole: runs hold whole items, nothing to join
-  float *part;       // [2 CTAs][rows][D] and, after them, their (m, l) [2 CTAs][rows][2]
+  int items;         // (sequence, KV head, row group)
+  float *part;       // pieces [2 runs][rows][D], their (m, l) [2 runs][rows][2], the items' ends [items][2]
 };
 // What the plan goes by, all measured on GB300 (d = 128, us):
 // An item's query rows, its meeting and its output take a team about as long as
@@ -229,7 +230,7 @@ GDN_DEV long long find_cut(const DecodeArgs &p, int warps, int HR, int lane, int
   return cut >= x.N ? x.tiles : find_tile<TILE>(c, x.at(cut), HR, p.extra, lane, x.n0, k);
 }
 
-// A group of an item's query rows, ROWS at most: row x is a (token, query head).
+// A group of an item's query rows, `most` at most: row x is a (token, query head).
 struct RowGroup {
   int h, rows;       // the KV head, the rows
   int tok, off, G;   // the first row's token, and its place among that token's heads
@@ -238,11 +239,10 @@ struct RowGroup {
   GDN_DEV int token(int x) const { return tok + over(x); }
   GDN_DEV int head(int x) const { return off + x - over(x) * G; }
 };
-template <int ROWS>
-GDN_DEV RowGroup row_group(const DecodeArgs &p, int hr) {
-  const int h = p.RG == 1 ? hr : hr / p.RG, row0 = (hr - h * p.RG) * ROWS;
+GDN_DEV RowGroup row_group(const DecodeArgs &p, int hr, int most) {
+  const int h = p.RG == 1 ? hr : hr / p.RG, row0 = (hr - h * p.RG) * most;
   const int tok = row0 ? row0 / p.G : 0;
-  return {h, min(ROWS, p.r * p.G - row0), tok, row0 - tok * p.G, p.G, p.inv_g};
+  return {h, min(most, p.r * p.G - row0), tok, row0 - tok * p.G, p.G, p.inv_g};
 }
 
 GDN_DEV uint32_t transpose8x8(uint32_t x) {
@@ -264,6 +264,11 @@ GDN_DEV uint32_t e4m3x2_to_h2(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
   return h;
+}
+
+template <int D>
+GDN_DEV int32_t *join_ends(const DecodeArgs &p, int runs, int rows) {
+  return reinterpret_cast<int32_t *>(p.part + 2 * (size_t)runs * rows * (D + 2));
 }
 
 template <int D, int NQ, int TEAM>
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   };
   // The team's warp 0 loads the query rows of a segment, one per lane.
   auto load_q = [&](const Cursor &k) {
-    const RowGroup rg = row_group<S::kRows>(p, k.hr);
+    const RowGroup rg = row_group(p, k.hr, S::kRows);
     const int rows = rg.rows;
     if (lane == 0) mbar_arrive_expect_tx(q_full, rows * D * 2);
     __syncwarp();
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     float cs[NQ][2];   // sm k_scale log2 e / the row's scale, of columns 2t and 2t + 1
     int last[NQ][2];   // the last token that the row sees
     float O[KS][NQ][4], m[NQ][2], l[NQ][2];
-    const RowGroup qg = row_group<S::kRows>(p, cur.hr);
+    const RowGroup qg = row_group(p, cur.hr, S::kRows);
     if (alive && !__all_sync(0xffffffffu, wait_or_abort(q_full, (uint32_t)sg & 1u, abort_flag, c.status))) alive = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
       }
     }
     team_sync();
-    const RowGroup rg = row_group<S::kRows>(p, cur.hr);
+    const RowGroup rg = row_group(p, cur.hr, S::kRows);
     for (int i = tid; i < rg.rows * (D / 4); i += 32 * W) {
       const int row = i / (D / 4), d4 = i % (D / 4) * 4;
       float top = -INFINITY, sum = 0.0f;
@@ -680,6 +685,12 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
               make_float2(top, sum);
       }
     }
+    // for the join: an item's first piece (-1: it is done) and the run of its last one
+    if (tid == 0 && p.extra != kWhole) {
+      int32_t *ends = join_ends<D>(p, gridDim.x * S::kTeams, S::kRows) + 2 * ((long long)cur.b * HR + cur.hr);
+      if (cur.tile == 0) ends[0] = done ? -1 : (int)piece;
+      if (cur.tile + seg == cur.nt) ends[1] = run;
+    }
     at += seg;
     if (at < n_tiles) next_item<TILE>(c, cur, HR);
   }
@@ -689,129 +700,135 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   }
 }
 
-// The items that lie in several runs: their pieces are joined in order, by the
-// CTA of the first cut inside an item, or with whole-CTA teams (fewer items than
-// cuts, more pieces) by a CTA per item and row.
-// Few pieces: a warp per row. More: the CTA's warps take every eighth piece of a
-// row. most: runs at most, as in the decode kernel. 3 to 3.5 us of latency behind
-// the decode kernel (the first loads of a piece depend on the plan's search).
-template <int D, int NQ, int TEAM>
-__global__ void __launch_bounds__(256) kv4_join_kernel(DecodeArgs p, int most) {
-  using S = DecodeShape<D, NQ, TEAM>;
+// Join R rows, from `row`, of pieces j0, j0 + step, ... < np: U at a time are in flight.
+template <int D, int U, int R, typename Piece>
+GDN_DEV void join_pieces(const float *part, const float *ml, Piece piece, int row, int rows, int j0, int step, int np,
+                         float (&m)[R], float (&l)[R], float (&o)[R][D / 32]) {
   constexpr int E = D / 32;
-  __shared__ float sh[8][D + 2];
-  const Kv4Args &c = p.a.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int HR = c.Hkv * p.RG;
-  const Cuts x = find_cuts<S::kTile>(p, S::kTeam, HR, lane, most);
-  Cursor k{0, 0, 0, 0, 0};
-  int cut;           // the first cut inside the item
-  bool mine;
-  long long a0 = 0;  // the item's cost begins here; its tile t lies at a0 + extra + t
-  if (TEAM) {        // more items than cuts: a CTA per cut
-    cut = blockIdx.x + 1;
-    mine = cut < x.N;
-    if (mine) {
-      find_tile<S::kTile>(c, x.at(cut), HR, p.extra, lane, x.n0, k);
-      a0 = x.at(cut) - k.tile - p.extra;
-      mine = k.tile > 0 && x.at(cut - 1) <= a0 + p.extra;
-    }
-  } else {           // a CTA per item (and row)
-    seek<S::kTile>(c, k, blockIdx.x / HR);
-    k.hr = blockIdx.x % HR;
-    long long before = 0;
-    for (int b0 = 0; b0 < k.b; b0 += 32)
-      before += warp_isum(b0 + lane < k.b ? (b0 ? lane_tiles<S::kTile>(c, b0, lane) : x.n0) : 0);
-    a0 = (before + (long long)k.b * p.extra) * HR + (long long)k.hr * (k.nt + p.extra);
-    cut = (int)quot((a0 + p.extra + 1) * x.N - 1, x.q * x.N + x.rest) + 1;
-    mine = cut < x.N && x.at(cut) < a0 + p.extra + k.nt;
-  }
-  // pieces: runs cut - 1 (where the item may be its first segment, or its last) to the one of its last tile
-  const int np = (int)quot((a0 + p.extra + k.nt) * x.N - 1, x.q * x.N + x.rest) - cut + 2;
-  const bool first = x.at(cut - 1) >= a0;
-  const RowGroup rg = row_group<S::kRows>(p, k.hr);
-  const int rows = rg.rows;
-  kv4_begin();  // on every path: this grid must not end before the one it follows
-  if (!mine) return;
-  const float *ml = p.part + 2 * (size_t)most * S::kRows * D;
-  auto piece = [&](int j, int row) { return (2 * (size_t)(cut - 1 + j) + (j > 0 || first ? 0 : 1)) * S::kRows + row; };
-  float m, l, o[E];
-  auto begin = [&]() {
-    m = -INFINITY;
-    l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  struct alignas(4 * E) Lane {
+    float v[E];
   };
-  auto add = [&](int row, int j0, int step) {  // pieces j0, j0 + step, ...: four in flight
-    for (; j0 < np; j0 += 4 * step) {
-      float2 v[4];
-      float y[4][E];
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = j0 + u * step;
-        v[u] = make_float2(-INFINITY, 0.0f);
+  for (int i = 0; i < R; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[u][e] = 0.0f;
-        if (j < np) {
-          v[u] = *reinterpret_cast<const float2 *>(ml + piece(j, row) * 2);
-          const float *op = p.part + piece(j, row) * D + lane * E;
+    for (int e = 0; e < E; ++e) o[i][e] = 0.0f;
+  }
+  for (; j0 < np; j0 += U * step) {
+    float2 v[U][R];
+    float y[U][R][E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) y[u][e] = op[e];
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        v[u][i] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[u][i][e] = 0.0f;
+        if (j0 + u * step < np && row + i < rows) {
+          const size_t at = piece(j0 + u * step) + row + i;
+          v[u][i] = *reinterpret_cast<const float2 *>(ml + at * 2);
+          const Lane x = reinterpret_cast<const Lane *>(part + at * D)[lane];
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[u][i][e] = x.v[e];
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float mn = fmaxf(m, v[u].x), safe = mn == -INFINITY ? 0.0f : mn;
-        const float f = ex2(m - safe), fx = ex2(v[u].x - safe);
-        l = l * f + v[u].y * fx;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + y[u][e] * fx;
-        m = mn;
+      for (int i = 0; i < R; ++i) {
+        const float mn = fmaxf(m[i], v[u][i].x), safe = mn == -INFINITY ? 0.0f : mn;
+        const float f = ex2(m[i] - safe), fx = ex2(v[u][i].x - safe);
+        l[i] = l[i] * f + v[u][i].y * fx;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[i][e] = o[i][e] * f + y[u][i][e] * fx;
+        m[i] = mn;
       }
-    }
-  };
-  auto out_row = [&](int row) {
-    return ((long long)k.b * p.r + rg.token(row)) * p.a.Hq + rg.h * p.G + rg.head(row);
-  };
-  if (np <= 8) {
-    for (int row = blockIdx.y + gridDim.y * warp; row < rows; row += gridDim.y * 8) {
-      begin();
-      add(row, 0, 1);
-      const float inv = l == 0.0f ? 0.0f : c.vs / l;
-      uint16_t *dst = p.a.out + out_row(row) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t *>(dst + e) = bf16x2(o[e] * inv, o[e + 1] * inv);
-      if (p.a.lse && lane == 0) p.a.lse[out_row(row)] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
-    }
-    return;
   }
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-    begin();
-    add(row, warp, 8);
+}
+
+// The items that lie in several runs: their pieces, which the decode kernel wrote
+// down, are joined in order. Up to eight pieces: a warp per row. More: a warp for
+// every eighth of them -- of one row, with a CTA per row (SPLIT, after whole-CTA
+// teams: few items of many pieces; eight rows a CTA took 26 us instead of 22 at 16
+// sequences of which one has 131072 tokens), else of four rows at a time.
+// Bound by latency: two loads, one after the other, and the launch.
+// runs, most: as the decode kernel's runs and rows of an item.
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(256, 3) kv4_join_kernel(DecodeArgs p, int runs, int most) {
+  constexpr int E = D / 32, R = SPLIT ? 1 : 8, H = SPLIT ? 1 : 4;  // rows of the CTA, and at a time
+  struct alignas(4 * E) Lane {
+    float v[E];
+  };
+  __shared__ float sh[8][R][D + 4];
+  const Kv4Args &c = p.a.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, HR = c.Hkv * p.RG, row0 = blockIdx.y * R;
+  const float *ml = p.part + 2 * (size_t)runs * most * D;
+  const int2 *ends = reinterpret_cast<const int2 *>(join_ends<D>(p, runs, most));
+  int b = blockIdx.x / HR;
+  RowGroup rg = row_group(p, blockIdx.x - b * HR, most);
+  kv4_begin();  // on every path: this grid must not end before the one it follows
+  for (long long item = blockIdx.x;;) {
+    const int2 e = ends[item];  // the first piece, or -1; then one in each run up to e.y
+    const int first = e.x / 2, np = e.y - first + 1;
+    auto piece = [&](int j) { return (size_t)(j > 0 ? 2 * (first + j) : e.x) * most; };
+    auto put = [&](int row, int ch, float m, float l, auto &v) {  // channels ch ... of a row
+      const long long out = ((long long)b * p.r + rg.token(row)) * p.a.Hq + rg.h * p.G + rg.head(row);
+      const float inv = l == 0.0f ? 0.0f : c.vs / l;
 #pragma unroll
-    for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = o[e];
-    if (lane == 0) {
-      sh[warp][D] = m;
-      sh[warp][D + 1] = l;
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) top = fmaxf(top, sh[w][D]);
-      const float safe = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f, v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const float f = ex2(sh[w][D] - safe);
-        sum += sh[w][D + 1] * f;
-        v += sh[w][threadIdx.x] * f;
+      for (int x = 0; x < (int)(sizeof(v) / sizeof(float)); x += 2)
+        *reinterpret_cast<uint32_t *>(p.a.out + out * D + ch + x) = bf16x2(v[x] * inv, v[x + 1] * inv);
+      if (p.a.lse && ch == 0) p.a.lse[out] = (m + (log2f(l) - kShift)) * 0.6931471805599453f;
+    };
+    if (e.x >= 0 && np <= 8) {
+      const int row = row0 + warp;
+      if (row0 % 8 == 0 && row < rg.rows) {
+        float m[1], l[1], o[1][E];
+        join_pieces<D, 8>(p.part, ml, piece, row, rg.rows, 0, 1, np, m, l, o);
+        put(row, lane * E, m[0], l[0], o[0]);
       }
-      p.a.out[out_row(row) * D + threadIdx.x] = f32_to_bf16_bits(sum == 0.0f ? 0.0f : v * (c.vs / sum));
-      if (p.a.lse && threadIdx.x == 0) p.a.lse[out_row(row)] = (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
+    } else if (e.x >= 0 && row0 < rg.rows) {
+#pragma unroll 1
+      for (int i0 = 0; i0 < R; i0 += H) {
+        float m[H], l[H], o[H][E];
+        join_pieces<D, 8 / H>(p.part, ml, piece, row0 + i0, rg.rows, warp, 8, np, m, l, o);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          Lane x;
+#pragma unroll
+          for (int k = 0; k < E; ++k) x.v[k] = o[i][k];
+          reinterpret_cast<Lane *>(sh[warp][i0 + i])[lane] = x;
+          if (lane == 0) {
+            sh[warp][i0 + i][D] = m[i];
+            sh[warp][i0 + i][D + 1] = l[i];
+          }
+        }
+      }
+      __syncthreads();
+      for (int x = threadIdx.x; x < R * (D / 2); x += 256) {
+        const int i = x / (D / 2), ch = x % (D / 2) * 2;
+        if (row0 + i >= rg.rows) break;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, sh[w][i][D]);
+        const float safe = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f, v[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float f = ex2(sh[w][i][D] - safe);
+          sum += sh[w][i][D + 1] * f;
+          v[0] += sh[w][i][ch] * f;
+          v[1] += sh[w][i][ch + 1] * f;
+        }
+        put(row0 + i, ch, top, sum, v);
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    item += gridDim.x;
+    if (item >= p.items) return;
+    b = (int)item / HR;
+    rg = row_group(p, (int)item - b * HR, most);
   }
 }
 
@@ -824,9 +841,9 @@ cudaError_t launch_decode_t(const DecodeArgs &p, int ctas, cudaStream_t stream) 
   e = kv4_launch(kv4_decode_kernel<D, NQ, TEAM>, ctas, S::kThreads, S::kBytes, stream, p);
   const int most = ctas * S::kTeams;  // runs, and cuts but one
   if (e != cudaSuccess || p.extra == kWhole || most < 2) return e;
-  const dim3 grid = TEAM ? dim3((unsigned)most - 1, 1, 1)
-                         : dim3((unsigned)(p.a.c.B * p.a.c.Hkv * p.RG), S::kRows < p.r * p.G ? S::kRows : p.r * p.G, 1);
-  return kv4_launch(kv4_join_kernel<D, NQ, TEAM>, grid, 256, 0, stream, p, most);
+  const int rows = std::min(int(S::kRows), p.r * p.G);
+  const dim3 grid(TEAM ? std::min(p.items, 8 * 152) : p.items, TEAM ? (rows + 7) / 8 : rows);
+  return kv4_launch(kv4_join_kernel<D, TEAM == 0>, grid, 256, 0, stream, p, most, int(S::kRows));
 }
 
 // Query rows per (sequence, KV head) -> 8-row column blocks of one item.
@@ -865,7 +882,7 @@ DecodePlan decode_plan(const Kv4AttnArgs &a, int num_sms) {
   d.extra = most <= (long long)s.team * (d.small ? kRoundsTeam : kRoundsCta) ? kWhole : d.small ? kExtraTeam : kExtraCta;
   const long long n = d.extra == kWhole ? items : (items * most + s.team - 1) / s.team;  // runs that could have work
   d.ctas = (int)(n < (long long)num_sms * s.teams ? (n + s.teams - 1) / s.teams : num_sms);
-  d.bytes = d.extra == kWhole ? 0 : 2 * (size_t)d.ctas * s.teams * 8 * d.NQ * (a.c.D + 2) * sizeof(float);
+  d.bytes = d.extra == kWhole ? 0 : 2 * (size_t)d.ctas * s.teams * 8 * d.NQ * (a.c.D + 2) * sizeof(float) + 8 * (size_t)items;
   return d;
 }
 
@@ -883,7 +900,8 @@ size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms) { return a.c.T ? deco
 cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
   const DecodePlan d = decode_plan(a, num_sms);
   const int G = a.Hq / a.c.Hkv;
-  const DecodeArgs p{a, a.c.T / a.c.B, G, d.RG, (uint32_t)((65536 + G - 1) / G), d.extra, static_cast<float *>(workspace)};
+  const DecodeArgs p{a, a.c.T / a.c.B, G, d.RG, (uint32_t)((65536 + G - 1) / G), d.extra, (int)(a.c.B * a.c.Hkv * d.RG),
+                     static_cast<float *>(workspace)};
   if (a.c.D == 128)
     return d.NQ == 1 ? launch_decode<128, 1>(p, d, stream) : d.NQ == 2 ? launch_decode<128, 2>(p, d, stream)
                                                                        : launch_decode<128, 4>(p, d, stream);
