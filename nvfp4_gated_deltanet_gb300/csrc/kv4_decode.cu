@@ -39,11 +39,12 @@
 // one's parts meet, and fewer warps wait for the slowest.
 //
 // Measured (32 query heads, d = 128): 64 sequences of up to 8190 tokens, 8 KV
-// heads, 291 MB: 59 us, 4.9 TB/s (0.73 of the copy bandwidth); one of 200001, 4 KV
-// heads, 115 MB: 29.6 us. Of these 4 us are the launch and finding the runs, 3 the
-// join; the loads alone take 54 and 24, the arithmetic alone 55 and 26. A tile
-// costs about 570 issue slots a warp: 128 conversions, 96 shifts that bring bytes
-// to them, 128 scale products, 32 MMAs.
+// heads, 291 MB: 57 us, 5.1 TB/s (0.75 of the copy bandwidth); one of 200001, 4 KV
+// heads, 115 MB: 28 us. Before the first tile pass 10000 cycles, 5 us (the lengths,
+// the run's ends, the page table, the query rows, the first tiles, one after the
+// other); the join adds 3. When both took 59 and 29.6, the loads alone took 54 and
+// 24, the arithmetic alone 55 and 26. A tile costs about 570 issue slots a warp: 128
+// conversions, 96 shifts that bring bytes to them, 128 scale products, 32 MMAs.
 #include "kv4.cuh"
 #include "tc.cuh"
 
@@ -93,20 +94,21 @@ struct DecodeArgs {
 };
 // What the plan goes by, all measured on GB300 (d = 128, us):
 // An item's query rows, its meeting and its output take a team about as long as
-// this many tiles of its run. A whole CTA: 12 / 24 / 40 gave 28.9 / 26.2 / 26.2 at
-// 16 sequences of up to 8000 tokens (8 KV heads); four warps: 3 / 6 / 10 gave
-// 67.7 / 64.4 / 64.7 at 64 of up to 8190.
-constexpr int kExtraCta = 24, kExtraTeam = 6;
+// this many tiles of its run. A whole CTA: 16 / 24 / 32 gave 25.7 / 24.3 / 24.0 at
+// 16 sequences of up to 8000 tokens (8 KV heads), 21.4 / 20.8 / 20.3 at 8 of up to
+// 30000 (4, d = 64, 16 rows); four warps: 3 / 6 / 10 gave 67.7 / 64.4 / 64.7 at 64
+// of up to 8190.
+constexpr int kExtraCta = 32, kExtraTeam = 6;
 // From as many items as a GB300 has SMs, teams of four warps instead of whole
-// CTAs: 59 against 72 with 512 items (64 sequences, above), 24 against 41 with 768
-// (96 of up to 600); with 128 items 27.4 against 26.2, with 4 of 200001 tokens 56
-// against 30.
+// CTAs: 59 against 72 with 512 items (64 sequences, above), 26.7 against 29.2 with
+// 192 (24 of up to 6000); with 128 items 25.3 against 24.2, with 4 of 200001 tokens
+// 56 against 30.
 constexpr int kManyItems = 152;
-// Items stay whole while a team goes through the longest in this many rounds: 64
-// items of 1000 tokens (2 rounds of a CTA) 9.8 against 11.9 cut and joined, 4 of
-// 3000 (6 rounds) 16.7 against 11.9; 768 of up to 600 (5 rounds of a team) 23.0
-// against 24.3.
-constexpr int kRoundsCta = 3, kRoundsTeam = 6;
+// Items stay whole while a team goes through the longest in this many rounds. Whole
+// against cut and joined: 64 items of 1000 tokens (2 rounds of a CTA) 8.8 and 10.7,
+// 4 of 3000 (6 rounds) 16.7 and 11.9; 1600 of up to 250 (2 rounds of a team) 21.4
+// and 29.4, of up to 400 (4) 27.5 and 29.6, 768 of up to 600 (5) 21.7 and 21.1.
+constexpr int kRoundsCta = 3, kRoundsTeam = 4;
 constexpr int kWhole = 1 << 20;  // the `extra` of whole items
 
 // a / b, mostly in 32 bits
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     *abort_flag = 0u;
     fence_barrier_init();
   }
-  kv4_begin();  // kv4_join_kernel finds its places meanwhile
+  kv4_begin();
   __syncthreads();
   Cursor cur;
   int n_tiles;
