@@ -680,3 +680,22 @@ def test_order_among_streams_and_other_kernels(g, graph):
         cuda_graph.replay() if graph else go()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+# one long sequence among short ones: an item of many runs' pieces beside whole ones, more items than the join has
+# CTAs, one item over all runs, 8-, 16- and 32-row items in both team sizes
+SKEW = [(160, 12000, 5, 1, 8, 8, 64, 16), (20, 30000, 40, 1, 32, 8, 128, 64), (3, 40000, 7, 4, 16, 2, 64, 32),
+        (1, 60000, 0, 1, 8, 1, 128, 128), (40, 20000, 3, 4, 32, 4, 64, 16), (2, 20000, 1000, 7, 24, 2, 128, 16)]
+
+
+@pytest.mark.parametrize("B,long,short,r,hq,hkv,d,page", SKEW)
+def test_decode_one_long_among_short(g, B, long, short, r, hq, hkv, d, page):
+    lens = [short + b % 3 for b in range(B)]
+    lens[B // 3] = long
+    pages, tab, n, *_ = setup(g, lens, page, hkv, d, seed=B)
+    q = queries(B * r, hq, d, B + 1).reshape(B, r, hq, d)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = g.kv4_decode(q, pages, tab, n, KS, VS, return_lse=True, dev_status=st)
+    close(out, lse, want_fast(pages, tab, lens, [r] * B, q.flatten(0, 1), d), d)
+    again = g.kv4_decode(q, pages, tab, n, KS, VS, return_lse=True, dev_status=st)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and st.item() == 0
