@@ -117,15 +117,18 @@ int64_t rows_stride(const at::Tensor &t, const char *name, int heads, int d) {
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) {
   return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
-// The given output, checked, or a new one of the type; where `stream` is another
-// than the current one, its memory is not handed out again before that is done.
+// The given output, checked, or a new one of the type. For work on `stream` it is
+// allocated as that stream's: a block that the current stream has freed may still
+// be in use there, and nothing orders the two. The caller goes on with it on the
+// current stream, so it is recorded there.
 at::Tensor output(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like,
                   PyObject *stream) {
   if (!given(o)) {
+    if (!given(stream)) return fresh(shape, type, like);
+    const c10::cuda::CUDAStream here = c10::cuda::getCurrentCUDAStream(like.device().index());
+    c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(stream_of(stream), like.device().index()));
     at::Tensor t = fresh(shape, type, like);
-    if (given(stream) && t.numel() > 0)
-      c10::cuda::CUDACachingAllocator::recordStream(
-          t.storage().data_ptr(), c10::cuda::getStreamFromExternal(stream_of(stream), like.device().index()));
+    if (t.numel() > 0) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), here);
     return t;
   }
   const at::Tensor &t = tensor(o, name);
