@@ -13,6 +13,7 @@
 
 #include <cmath>
 #include <exception>
+#include <initializer_list>
 #include <string>
 
 #include "gdn.h"
@@ -72,6 +73,38 @@ int32_t *status_word(PyObject *o) {
   if (t.numel() < 1) throw Bad("dev_status: expected one element");
   return t.data_ptr<int32_t>();
 }
+// A call runs on the device of its first tensor (its pages): every other tensor
+// and the stream must be of that device too. With it the current one, the stream
+// used by default, the launches and what is kept per device are that device's.
+struct Named {
+  const char *name;
+  PyObject *o;
+};
+c10::Device device_of(std::initializer_list<Named> tensors, PyObject *stream) {
+  const Named &first = *tensors.begin();
+  const c10::Device dev = tensor(first.o, first.name).device();
+  if (!dev.is_cuda()) throw Bad(std::string(first.name) + ": expected a CUDA tensor");
+  for (const Named &t : tensors) {
+    if (!given(t.o)) continue;
+    const c10::Device d = tensor(t.o, t.name).device();
+    if (d != dev)
+      throw Bad(std::string(t.name) + ": is on " + d.str() + ", but " + first.name + " is on the CUDA device " + dev.str());
+  }
+  if (given(stream)) {
+    PyObject *v = PyObject_GetAttrString(stream, "device_index");  // torch's streams have one
+    if (!v) {
+      PyErr_Clear();
+      return dev;
+    }
+    const long long i = PyLong_AsLongLong(v);
+    Py_DECREF(v);
+    if (PyErr_Occurred()) throw Raised();
+    if (i != dev.index())
+      throw Bad("stream: is of CUDA device " + std::to_string(i) + ", but " + first.name + " is on " + dev.str());
+  }
+  return dev;
+}
+// The stream on the current device
 cudaStream_t stream_of(PyObject *o) {
   if (!given(o)) return c10::cuda::getCurrentCUDAStream().stream();
   PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
@@ -164,6 +197,8 @@ PyObject *pair(const at::Tensor &a, const at::Tensor &b) {
 
 // k v pages table kv_len k_scale v_scale q_start dev_status stream
 PyObject *append(PyObject *const *a) {
+  const c10::cuda::CUDAGuard on(device_of({{"pages", a[2]}, {"k", a[0]}, {"v", a[1]}, {"block_table", a[3]},
+                                           {"kv_len", a[4]}, {"q_start", a[7]}, {"dev_status", a[8]}}, a[9]));
   const kv4_cache c = cache(a[2], a[5], a[6]);
   const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
   const int64_t ks = rows_stride(k, "k", c.n_kv_heads, c.head_dim), vs = rows_stride(v, "v", c.n_kv_heads, c.head_dim);
@@ -174,6 +209,8 @@ PyObject *append(PyObject *const *a) {
 }
 // pages table kv_len k_scale v_scale rows q_start k v dev_status stream
 PyObject *read(PyObject *const *a) {
+  const c10::cuda::CUDAGuard on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"kv_len", a[2]}, {"q_start", a[6]},
+                                           {"k", a[7]}, {"v", a[8]}, {"dev_status", a[9]}}, a[10]));
   const kv4_cache c = cache(a[0], a[3], a[4]);
   const int64_t rows = whole(a[5]);
   if (rows < 0) throw Bad("rows: expected a number of rows");
@@ -187,6 +224,9 @@ PyObject *read(PyObject *const *a) {
 }
 // q pages table kv_len k_scale v_scale sm_scale out lse return_lse workspace dev_status stream
 PyObject *decode(PyObject *const *a) {
+  const c10::cuda::CUDAGuard on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
+                                           {"out", a[7]}, {"lse", a[8]}, {"workspace", a[10]},
+                                           {"dev_status", a[11]}}, a[12]));
   const kv4_cache c = cache(a[1], a[4], a[5]);
   const at::Tensor &q = tensor(a[0], "q");
   if (q.dim() != 3 && q.dim() != 4) throw Bad("q: expected [B][Hq][d] or [B][r][Hq][d]");
@@ -214,6 +254,9 @@ PyObject *decode(PyObject *const *a) {
 }
 // q pages table kv_len q_start k_scale v_scale total_kv sm_scale out lse return_lse workspace dev_status stream
 PyObject *prefill(PyObject *const *a) {
+  const c10::cuda::CUDAGuard on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
+                                           {"q_start", a[4]}, {"out", a[9]}, {"lse", a[10]}, {"workspace", a[12]},
+                                           {"dev_status", a[13]}}, a[14]));
   const kv4_cache c = cache(a[1], a[5], a[6]);
   const at::Tensor &q = tensor(a[0], "q");
   const int64_t qs = rows_stride(q, "q", -1, c.head_dim);
@@ -252,6 +295,7 @@ Layers layers_of(PyObject *o) {
 }
 // pages src dst dev_status stream
 PyObject *copy_pages(PyObject *const *a) {
+  const c10::cuda::CUDAGuard on(device_of({{"pages", a[0]}, {"src", a[1]}, {"dst", a[2]}, {"dev_status", a[3]}}, a[4]));
   const Layers l = layers_of(a[0]);
   const int32_t *src = i32(a[1], "src", 1), *dst = i32(a[2], "dst", 1);
   const int64_t n = THPVariable_Unpack(a[1]).size(0);
@@ -262,6 +306,9 @@ PyObject *copy_pages(PyObject *const *a) {
 }
 // pages table tables_out page_map n_live workspace dev_status stream
 PyObject *compact(PyObject *const *a) {
+  const c10::cuda::CUDAGuard on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"tables_out", a[2]},
+                                           {"page_map", a[3]}, {"n_live", a[4]}, {"workspace", a[5]},
+                                           {"dev_status", a[6]}}, a[7]));
   const Layers l = layers_of(a[0]);
   const int32_t *table = i32(a[1], "block_table", 2);
   const at::Tensor &t = THPVariable_Unpack(a[1]), &p = THPVariable_Unpack(a[0]);

@@ -3,7 +3,9 @@
 The functions marshal the kv4_* entry points of ``include/gdn.h`` (layout,
 errors and numerics are described there). ``pages`` is a uint8 CUDA tensor
 [num_pages][Hkv][page_tokens / 16][18 * d], or [layers][num_pages]... for the
-calls that take all layers at once; its shape gives page_tokens, Hkv and d.
+calls that take all layers at once; its shape gives page_tokens, Hkv and d. A
+call runs on the pages' device, where its other tensors must be, and on that
+device's current stream unless one is given.
 
     pages = kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim)
     kv4_append(k, v, pages, table, kv_len, k_scale, v_scale)

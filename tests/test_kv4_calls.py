@@ -1,0 +1,57 @@
+"""What the 4-bit KV cache's Python calls refuse before they touch a device
+(no GPU: tensors without data that name a CUDA device stand in for real ones)."""
+from types import SimpleNamespace
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def g():
+    from nvfp4_gated_deltanet_gb300 import build
+    build.build()
+    import nvfp4_gated_deltanet_gb300 as pkg
+    return pkg
+
+
+def on(device, *shape, dtype=torch.int32):
+    """A tensor of `device` without data: reading its address raises RuntimeError, no call gets past that."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def calls(g):
+    """Every call: its function, and its tensors by argument name."""
+    bf, fl, u8 = torch.bfloat16, torch.float32, torch.uint8
+    pages, table, lens = ((4, 2, 1, 18 * 128), u8), ((2, 2), torch.int32), ((2,), torch.int32)
+    starts, status = ((3,), torch.int32), ((1,), torch.int32)
+    kv, q, lse = ((2, 2, 128), bf), ((2, 4, 128), bf), ((2, 4), fl)
+    common = dict(pages=pages, block_table=table, kv_len=lens, dev_status=status)
+    scales = dict(k_scale=1.0, v_scale=1.0)
+    return [
+        (g.kv4_append, dict(common, k=kv, v=kv, q_start=starts), scales),
+        (g.kv4_read, dict(common, q_start=starts, k=kv, v=kv), dict(scales, rows=2)),
+        (g.kv4_decode, dict(common, q=q, out=q, lse=lse, workspace=((4096,), u8)), scales),
+        (g.kv4_prefill, dict(common, q=q, q_start=starts, out=q, lse=lse, workspace=((4096,), u8)), scales),
+        (g.kv4_copy_pages, dict(pages=pages, src=lens, dst=lens, dev_status=status), {}),
+        (g.kv4_compact, dict(pages=pages, block_table=table, tables_out=table, page_map=((4,), torch.int32),
+                             n_live=((1,), torch.int32), workspace=((4096,), u8), dev_status=status), {})]
+
+
+@pytest.mark.parametrize("i", range(6))
+def test_tensors_of_several_devices_are_refused(g, i):
+    f, tensors, rest = calls(g)[i]
+    for odd in tensors:
+        args = {k: on("cuda:1" if k == odd else "cuda:0", *shape, dtype=dt) for k, (shape, dt) in tensors.items()}
+        with pytest.raises(ValueError, match="cuda:1"):
+            f(**args, **rest)
+    args = {k: on("cuda:1", *shape, dtype=dt) for k, (shape, dt) in tensors.items()}
+    with pytest.raises(ValueError, match="stream"):
+        f(**args, **rest, stream=SimpleNamespace(cuda_stream=0, device_index=0))
+    for odd in tensors:                              # a host tensor among them
+        args = {k: torch.zeros(*shape, dtype=dt) if k == odd else on("cuda:0", *shape, dtype=dt)
+                for k, (shape, dt) in tensors.items()}
+        with pytest.raises(ValueError, match="cpu|CUDA"):
+            f(**args, **rest)
