@@ -287,8 +287,16 @@ class KV4Cache:
         self.book.compact()
         return self.book.num_pages - self.book.free_pages
 
-    def check(self) -> int:
-        """Synchronise, return the sticky device status and clear it."""
-        st = int(self.status.item())
-        self.status.zero_()
+    def check(self, stream=None) -> int:
+        """Wait for `stream` (default: for every stream of the device), return
+        the sticky status of what ran there and clear it; what is launched
+        after that sets it anew."""
+        wait = stream.synchronize if stream is not None else lambda: torch.cuda.synchronize(self.device)
+        wait()
+        with self._on(stream):
+            st = int(self.status.item())
+            if st:
+                self.status.zero_()
+        if st:
+            wait()
         return st

@@ -121,3 +121,26 @@ def test_outputs_for_a_stream_within_a_capture(g):
         first = got.clone()
         assert torch.equal(first, go()[0])
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_check_sees_what_other_streams_have_yet_to_flag(g, own):
+    """An append on a side stream, behind milliseconds of other work there, names a
+    page that does not exist: check() (of all streams, or of that one) tells."""
+    c = g.KV4Cache(8, 16, 2, 64, KS, VS)
+    big = torch.randn(8192, 8192, device="cuda").bfloat16()
+    k = torch.randn(3, 2, 64, device="cuda").bfloat16()
+    seq = c.new()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    batch = c.grow([seq], 3, stream=side)
+    with torch.cuda.stream(side):
+        batch.block_table.fill_(99)
+        for _ in range(50):
+            big @ big
+    c.append(0, k, k, batch, stream=side)
+    assert c.check(side if own else None) == 6
+    assert c.check() == 0
+    batch = c.grow([seq], 3, stream=side)
+    c.append(0, k, k, batch, stream=side)
+    assert c.check(side) == 0

@@ -55,3 +55,18 @@ def test_tensors_of_several_devices_are_refused(g, i):
                 for k, (shape, dt) in tensors.items()}
         with pytest.raises(ValueError, match="cpu|CUDA"):
             f(**args, **rest)
+
+
+def test_check_waits_for_the_device_before_it_reads(g, monkeypatch):
+    """A status that a call on some stream has yet to set is not missed."""
+    c = g.KV4Cache(4, 16, 2, 64, 1.0, 1.0, device="cpu")
+    late, waits = [6], []
+
+    def wait(device=None):
+        waits.append(device)
+        if late:
+            c.status.fill_(late.pop())
+
+    monkeypatch.setattr(torch.cuda, "synchronize", wait)
+    assert c.check() == 6 and waits[0] == c.device
+    assert c.check() == 0 and c.status.item() == 0
