@@ -201,10 +201,13 @@ class KV4Book:
 
 class KV4Batch:
     """A batch's device tables: block_table [B][cols], kv_len [B], q_start
-    [B + 1] (int32), and on the host its rows T and its cached tokens total_kv."""
+    [B + 1] (int32), and on the host its rows T, its cached tokens total_kv and
+    the rows of each sequence, None where they differ (by default T / B)."""
 
-    def __init__(self, block_table, kv_len, q_start, T, total_kv):
+    def __init__(self, block_table, kv_len, q_start, T, total_kv, rows="even"):
         self.block_table, self.kv_len, self.q_start, self.T, self.total_kv = block_table, kv_len, q_start, T, total_kv
+        B = kv_len.shape[0]
+        self.rows = rows if rows != "even" else T // B if B and T % B == 0 else None
 
 
 class KV4Cache:
@@ -260,15 +263,22 @@ class KV4Cache:
         at = [0]
         for n in tokens:
             at.append(at[-1] + n)
+        rows = tokens[0] if len(set(tokens)) == 1 else None
         return KV4Batch(self._dev([p + [-1] * (cols - len(p)) for p in pages]), self._dev(lens), self._dev(at), at[-1],
-                        sum(lens))
+                        sum(lens), rows)
 
     def append(self, layer, k, v, batch, stream=None):
         kv4_append(k, v, self.layers[layer], batch.block_table, batch.kv_len, *self.scales[layer],
                    q_start=batch.q_start, dev_status=self.status, stream=stream)
 
     def decode(self, layer, q, batch, **kw):
-        """q [B][Hq][d] or [B][r][Hq][d]: as many rows per sequence as the batch has."""
+        """q [B][Hq][d] or [B][r][Hq][d]: as many rows per sequence as the batch
+        has (a row's place in its sequence, and so what it sees, follows from that)."""
+        if q.dim() in (3, 4):
+            B, r = q.shape[0], q.shape[1] if q.dim() == 4 else 1
+            if B != batch.kv_len.shape[0] or r != batch.rows:
+                has = "different numbers of rows" if batch.rows is None else f"{batch.rows} rows each"
+                raise ValueError(f"q: {B} sequences of {r} rows, but the batch has {batch.kv_len.shape[0]} with {has}")
         return kv4_decode(q, self.layers[layer], batch.block_table, batch.kv_len, *self.scales[layer],
                           dev_status=self.status, **kw)
 

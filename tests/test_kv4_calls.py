@@ -70,3 +70,28 @@ def test_check_waits_for_the_device_before_it_reads(g, monkeypatch):
     monkeypatch.setattr(torch.cuda, "synchronize", wait)
     assert c.check() == 6 and waits[0] == c.device
     assert c.check() == 0 and c.status.item() == 0
+
+
+def test_decode_refuses_other_rows_than_the_batch_has(g, monkeypatch):
+    """Candidates of another number than the batch was grown by would be masked at the wrong tokens."""
+    c = g.KV4Cache(16, 16, 2, 64, 1.0, 1.0, device="cpu")
+    monkeypatch.setattr(c, "_dev", lambda rows: torch.tensor(rows, dtype=torch.int32))
+    a, b = c.new(), c.new()
+
+    def q(*shape):
+        return torch.zeros(*shape, 4, 64, dtype=torch.bfloat16)
+
+    def grow(tokens):
+        c.book.extend([a, b], tokens)
+        return c.batch([a, b], tokens)
+
+    for batch, fit, bad in ((grow([3, 3]), [q(2, 3)], [q(2), q(2, 1), q(2, 4), q(1, 6), q(3, 2)]),
+                            (grow([1, 1]), [q(2), q(2, 1)], [q(2, 2), q(1), q(1, 2)]),
+                            (grow([3, 1]), [], [q(2), q(2, 2), q(4), q(1, 4)]),
+                            (g.KV4Batch(torch.zeros(2, 1), torch.zeros(2), torch.zeros(3), 4, 4), [q(2, 2)], [q(2), q(4)])):
+        for x in bad:
+            with pytest.raises(ValueError, match="rows"):
+                c.decode(0, x, batch)
+        for x in fit:                                # goes on to the checks of the call itself
+            with pytest.raises(ValueError, match="CUDA"):
+                c.decode(0, x, batch)
