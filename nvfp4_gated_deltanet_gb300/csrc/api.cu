@@ -65,7 +65,7 @@ struct Tuning {
   int scan_tc = 0;         // prefill chunk scan: 0 auto (tcgen05 for d = 128), 1 FP32 CUDA cores, 2 warp MMA, 3 tcgen05
   int persist_gemm = 0;    // tensor-core projections as one persistent CTA per SM: 0 auto, 1 off, 2 streaming
                            // form whenever allowed, 3 weight-stationary form whenever allowed
-  long long barrier_wait = 0;  // grid-barrier wait budget in SM cycles (0 = kWaitCycles)
+  long long barrier_wait = 0;  // wait budget in SM cycles (0 = kWaitCycles)
   int proj_mix = 0;        // decode of up to 8 rows with the in-projection inside the mixing kernel: 0 auto (off),
                            // 1 off, 2 on
   int tile_in = 0;         // warp-MMA tile of the in- / out-projection (GemvArgs::mma_tile): 0 auto
@@ -415,12 +415,14 @@ FusedArgs fused_args(gdn_ctx *ctx, const uint16_t *x, const int32_t *slot_ids, i
   f.y_codes = ctx->y_codes;
   f.y_scales = ctx->y_scales;
   f.bar = ctx->grid_bar;
-  f.wait_cycles = g_tune.barrier_wait > 0 ? g_tune.barrier_wait : kWaitCycles;
+  f.wait_cycles = wait_budget();
   f.status = ctx->status;
   return f;
 }
 
 }  // namespace
+
+long long gdn::wait_budget() { return g_tune.barrier_wait > 0 ? g_tune.barrier_wait : kWaitCycles; }
 
 extern "C" {
 

@@ -287,6 +287,18 @@ GDN_DEV bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// The same without the wait that try_wait may make.
+GDN_DEV bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Every wait is bounded: ~2^31 SM cycles (about one second at 2 GHz), then the
 // caller records GDN_E_TIMEOUT and gives up instead of hanging the GPU.
 constexpr long long kWaitCycles = 1LL << 31;
@@ -332,6 +344,8 @@ GDN_DEV float softplusf_(float x) { return x > 20.0f ? x : log1pf(expf(x)); }
 
 // ---------------------------------------------------------------- launchers (internal)
 namespace gdn {
+// The budget of a wait that tuning knob 12 sets, in SM cycles (kWaitCycles by default).
+long long wait_budget();
 struct LaunchCtx {
   cudaStream_t stream;
   int num_sms;

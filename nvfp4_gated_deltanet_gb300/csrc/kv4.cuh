@@ -30,6 +30,7 @@ struct Kv4Args {
   const int32_t *kv_len, *table, *q_start;  // q_start null: T / B rows each
   int B, cols, T;
   int32_t *status;
+  long long wait;  // budget of a wait on copies, SM cycles
 };
 
 // A sequence's new rows [q0, q1) and its token count, checked: a bad entry

@@ -399,7 +399,10 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     int last[NQ][2];   // the last token that the row sees
     float O[KS][NQ][4], m[NQ][2], l[NQ][2];
     const RowGroup qg = row_group(p, cur.hr, S::kRows);
-    if (alive && !__all_sync(0xffffffffu, wait_or_abort(q_full, (uint32_t)sg & 1u, abort_flag, c.status))) alive = false;
+    if (alive && !__all_sync(0xffffffffu, wait_or_abort(q_full, (uint32_t)sg & 1u, abort_flag, c.status, c.wait))) {
+      alive = false;
+      if (warp == 0) mbar_wait(q_full, (uint32_t)sg & 1u);  // its copies: no more follow once it has given up
+    }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const int row = n * 8 + g;
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
 
     // ------------------------------------------------ the warp's tiles of this segment
     for (; next < at + seg; next += W) {
-      if (alive && !__all_sync(0xffffffffu, wait_or_abort(my_full + slot, turn, abort_flag, c.status))) alive = false;
+      if (alive && !__all_sync(0xffffffffu, wait_or_abort(my_full + slot, turn, abort_flag, c.status, c.wait))) alive = false;
       if (!alive) continue;
       const unsigned char *buf = my_slots + slot * S::kSlot;
       const int pos0 = (cur.tile + next - at) * TILE;
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
         }
       }
     team_sync();
-    if (warp == 0 && at + seg < n_tiles) {  // every warp has read this segment's query rows: the next one's
+    if (warp == 0 && alive && at + seg < n_tiles) {  // every warp has read this segment's query rows: the next one's
       Cursor k = cur;
       next_item<TILE>(c, k, HR);
       load_q(k);
@@ -696,9 +699,12 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     at += seg;
     if (at < n_tiles) next_item<TILE>(c, cur, HR);
   }
-  if (!alive) {  // a wait gave up: the copies in flight land (or a bounded wait for each ends) first
-    mbar_wait(my_full + slot, turn);
-    mbar_wait(my_full + (slot ^ 1), slot == 0 ? turn : turn ^ 1u);
+  // A wait gave up: this warp's copies in flight land (or a bounded wait for each ends) before it leaves. It has
+  // loaded (ld - warp) / W tiles and taken slot + 2 turn, modulo 4: two, one or none of them are on their way.
+  if (!alive) {
+    const int held = ((ld - warp) / W - (slot + 2 * (int)turn)) & 3;
+    if (held > 0) mbar_wait(my_full + slot, turn);
+    if (held > 1) mbar_wait(my_full + (slot ^ 1), slot == 0 ? turn : turn ^ 1u);
   }
 }
 

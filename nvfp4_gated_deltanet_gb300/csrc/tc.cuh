@@ -191,18 +191,20 @@ GDN_DEV void tmem_ld32(uint32_t taddr, uint32_t *r) {
       : "memory");
 }
 // ---------------------------------------------------------------- waits of a kernel with roles
-// Bounded wait that also gives up when another role has given up.
-GDN_DEV bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag, int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait that also gives up when another role has given up. A short budget
+// (SM cycles) gives up on whatever is not there at once.
+GDN_DEV bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_flag, int32_t *status,
+                           long long budget = kWaitCycles) {
+  if (mbar_test_wait(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait_sleep(bar, parity, 2000u)) {
+  do {
     if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > budget) {
       *abort_flag = 1u;
       flag_status(status, GDN_E_TIMEOUT);
       return false;
     }
-  }
+  } while (!mbar_try_wait_sleep(bar, parity, 2000u));
   return true;
 }
 // The same, decided by lane 0 for the whole warp (collective TMEM accesses
