@@ -464,9 +464,9 @@ size_t kv4_compact_workspace(int num_pages);
  * tiles per SM, else one tile per CTA; 1 = one tile per CTA; 2 = streaming
  * whenever the form allows; 3 = weight-stationary whenever the form allows
  * (else as 2). knob 12: the budget, in SM cycles, of each grid-barrier wait of
- * the persistent single-kernel step (knob 3) and of each wait of kv4_decode:
- * 0 = the default, 2^31 (about
- * one second); any positive value sets it. A wait that runs out records
+ * the persistent single-kernel step (knob 3) and of each wait of kv4_append
+ * and kv4_decode: 0 = the default, 2^31 (about one second); any positive value
+ * sets it. A wait that runs out records
  * GDN_E_TIMEOUT in the status word and the kernel finishes without it (that
  * step's results are then meaningless); the next call starts clean (the
  * barrier words are cleared before every launch). A short budget exists to test

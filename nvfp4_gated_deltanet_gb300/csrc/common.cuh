@@ -323,6 +323,15 @@ GDN_DEV bool mbar_wait(uint64_t *bar, uint32_t parity) {
     if (clock64() - t0 > kWaitCycles) return false;
   return true;
 }
+// The same with a budget of its own (SM cycles): a short one gives up on what is not there at once.
+GDN_DEV bool mbar_wait_within(uint64_t *bar, uint32_t parity, long long budget) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  do {
+    if (clock64() - t0 > budget) return false;
+  } while (!mbar_try_wait_sleep(bar, parity, 20000u));
+  return true;
+}
 // Bulk (non-tensor) copy global -> shared, completion counted on `bar`.
 // dst, src 16-byte aligned, bytes a multiple of 16.
 GDN_DEV void bulk_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {

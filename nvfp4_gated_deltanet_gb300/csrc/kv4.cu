@@ -126,6 +126,7 @@ struct AppendSmem {
   Group found[8];
   uint8_t *place[8];
   uint64_t landed[2];
+  int gave_up;
 };
 template <int D>
 __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
   if (tid == 0) {
     mbar_init(&sm.landed[0], 1);
     mbar_init(&sm.landed[1], 1);
+    sm.gave_up = 0;
     fence_barrier_init();
   }
   kv4_begin();
@@ -172,9 +174,11 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
     const Group r = sm.found[k];
     if (r.b < 0) break;  // items are in order: none follows
     if (tid < 32 && k < 7) fetch(item + gridDim.x, k + 1, buf ^ 1);
-    const bool ok = mbar_wait(&sm.landed[buf], turns >> buf & 1u);
-    turns ^= 1u << buf;
-    if (!ok) flag_status(a.status, GDN_E_TIMEOUT);
+    const bool ok = mbar_wait_within(&sm.landed[buf], turns >> buf & 1u, a.wait);
+    if (!ok) {
+      flag_status(a.status, GDN_E_TIMEOUT);
+      sm.gave_up = 1;
+    }
     const int h0 = item % chunks * p.heads, hn = min(p.heads, a.Hkv - h0);
     uint8_t *g = sm.place[k];  // null: a bad page, flagged
     if (g && ok) {
@@ -192,7 +196,13 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
       }
     }
     __syncthreads();
-    if (g && ok) {
+    if (sm.gave_up) {  // a thread's wait gave up: the copies in flight land (or a bounded wait for each ends), and the CTA ends
+      mbar_wait(&sm.landed[buf], turns >> buf & 1u);
+      if (k < 7 && sm.found[k + 1].b >= 0) mbar_wait(&sm.landed[buf ^ 1], turns >> (buf ^ 1) & 1u);
+      break;
+    }
+    turns ^= 1u << buf;
+    if (g) {
       if (r.t0 == 0 && r.t1 == 16) {
         for (int i = tid; i < hn * (2 * D / 16); i += 256) {
           const int h = i / (2 * D / 16), w = i % (2 * D / 16);

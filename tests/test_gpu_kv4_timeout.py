@@ -53,3 +53,22 @@ def test_decode(g, short, B, n, r, hq, hkv, d, page):
         st.zero_()
         got = g.kv4_decode(q, pages, tab, lens, KS, VS, return_lse=True, dev_status=st)
         assert st.item() == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("lens,hkv,d", [([20000, 12001, 9, 33], 8, 128), ([700] * 40, 3, 64), ([1, 5], 1, 128)])
+def test_append(g, short, lens, hkv, d):
+    page = 32
+    pages, tab, n, k, v, start = cached(g, lens, page, hkv, d, spare=4)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    unused = sorted(set(range(pages.shape[0])) - set(tab[tab >= 0].tolist()))
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(4):
+        again = torch.full_like(pages, 0x7F)
+        flush.fill_(1)
+        short(True)
+        g.kv4_append(k, v, again, tab, n, KS, VS, q_start=start, dev_status=st)
+        assert st.item() == GDN_E_TIMEOUT and (again[unused] == 0x7F).all()
+        short(False)
+        st.zero_()
+        g.kv4_append(k, v, again, tab, n, KS, VS, q_start=start, dev_status=st)
+        assert st.item() == 0 and torch.equal(again, pages)
