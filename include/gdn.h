@@ -464,8 +464,8 @@ size_t kv4_compact_workspace(int num_pages);
  * tiles per SM, else one tile per CTA; 1 = one tile per CTA; 2 = streaming
  * whenever the form allows; 3 = weight-stationary whenever the form allows
  * (else as 2). knob 12: the budget, in SM cycles, of each grid-barrier wait of
- * the persistent single-kernel step (knob 3) and of each wait of kv4_append
- * and kv4_decode: 0 = the default, 2^31 (about one second); any positive value
+ * the persistent single-kernel step (knob 3) and of each wait of kv4_append,
+ * kv4_decode and kv4_prefill: 0 = the default, 2^31 (about one second); any positive value
  * sets it. A wait that runs out records
  * GDN_E_TIMEOUT in the status word and the kernel finishes without it (that
  * step's results are then meaningless); the next call starts clean (the

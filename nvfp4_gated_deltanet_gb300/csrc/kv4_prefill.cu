@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  auto wait = [&](uint64_t *bar, uint32_t use) { return wait_or_abort(bar, use & 1u, abort_flag, c.status); };
+  auto wait = [&](uint64_t *bar, uint32_t use) { return wait_or_abort(bar, use & 1u, abort_flag, c.status, c.wait); };
   auto warp_wait_all = [&](uint64_t *bar, uint32_t use) { return __all_sync(0xffffffffu, wait(bar, use)) != 0; };
   // Item `it` of this CTA; false when there is none (or a wait gave up). A whole warp.
   auto take = [&](int it, Item &w) {
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     } else if (warp == 9) {
       // ------------------------------------------------ query rows, K and V tiles
       const int q_bytes = p.tpt * p.G * D * 2;  // of a row tile
-      uint32_t u = 0, taken = 0;  // K / V tiles, items
+      uint32_t u = 0, ku = 0, taken = 0;  // V tiles, K tiles and items whose copies were issued
       Item w;
       bool ok = true;
       for (int it = 0; ok && take(it, w); ++it) {
@@ -557,10 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
             if (u >= NS && !(ok = wait(k_free + s, u / NS - 1))) break;
             mbar_arrive_expect_tx(k_full + s, S::kTileBytes);
             bulk_g2s(kbuf + s * S::kTileBytes, src + j * step, S::kTileBytes, k_full + s);
-            if (u >= NS && !(ok = wait(v_free + s, u / NS - 1))) {
-              mbar_wait(k_full + s, (u / NS) & 1u);
-              break;
-            }
+            ku = u + 1;
+            if (u >= NS && !(ok = wait(v_free + s, u / NS - 1))) break;
             mbar_arrive_expect_tx(v_full + s, S::kTileBytes);
             bulk_g2s(vbuf + s * S::kTileBytes, src + j * step + S::kTileBytes, S::kTileBytes, v_full + s);
           }
@@ -568,12 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       }
       if (lane == 0 && u == 0) pdl_wait();
-      if (lane == 0 && *abort_flag) {  // the copies in flight land (or a bounded wait for each ends) before the CTA leaves
+      if (lane == 0) {  // the last copies land (or a bounded wait for each ends) before the CTA leaves, whoever gives up when
         if (taken > 0) mbar_wait(q_full, (taken - 1) & 1u);
-        for (uint32_t x = u < NS ? 0 : u - NS; x < u; ++x) {
-          mbar_wait(k_full + x % NS, (x / NS) & 1u);
-          mbar_wait(v_full + x % NS, (x / NS) & 1u);
-        }
+        for (uint32_t x = ku < NS ? 0 : ku - NS; x < ku; ++x) mbar_wait(k_full + x % NS, (x / NS) & 1u);
+        for (uint32_t x = u < NS ? 0 : u - NS; x < u; ++x) mbar_wait(v_full + x % NS, (x / NS) & 1u);
       }
     } else if (warp == 10) {
       // ------------------------------------------------ the next item

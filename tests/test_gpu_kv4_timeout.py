@@ -72,3 +72,40 @@ def test_append(g, short, lens, hkv, d):
         st.zero_()
         g.kv4_append(k, v, again, tab, n, KS, VS, q_start=start, dev_status=st)
         assert st.item() == 0 and torch.equal(again, pages)
+
+
+@pytest.mark.parametrize("counts,lens,hq,hkv,d,page", [([2000, 900, 33], [6000, 900, 5000], 16, 4, 128, 64), ([700], [700], 8, 2, 64, 16),
+                                                       ([3000, 3000], [9000, 3001], 32, 8, 64, 64), ([70] * 9, [3000] * 9, 8, 1, 128, 32)])
+def test_prefill(g, short, counts, lens, hq, hkv, d, page):
+    """With one cycle every role gives up at its first wait; with more of them in the middle of an item, or not at all."""
+    pages, tab, n, *_ = cached(g, lens, page, hkv, d, seed=len(lens))
+    T = sum(counts)
+    q = queries(T, hq, d, T)
+    start = torch.tensor([sum(counts[:i]) for i in range(len(counts) + 1)], dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(total_kv=sum(lens), return_lse=True, dev_status=st)
+    want = g.kv4_prefill(q, pages, tab, n, start, KS, VS, **kw)
+    assert st.item() == 0
+    for budget in (1, 1, 300, 1000, 2000, 4000, 8000, 16000):
+        short(budget)
+        g.kv4_prefill(q, pages, tab, n, start, KS, VS, **kw)
+        assert st.item() == GDN_E_TIMEOUT or (budget > 1 and st.item() == 0)
+        short(0)
+        st.zero_()
+        got = g.kv4_prefill(q, pages, tab, n, start, KS, VS, **kw)
+        assert st.item() == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("B,n,r,hq,hkv,d,page", DECODE)
+def test_decode_gives_up_midway(g, short, B, n, r, hq, hkv, d, page):
+    pages, tab, lens, *_ = cached(g, [n - 7 * (b % 5) for b in range(B)], page, hkv, d, seed=B)
+    q = queries(B * r, hq, d, r).reshape(B, r, hq, d)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = g.kv4_decode(q, pages, tab, lens, KS, VS, dev_status=st)
+    for budget in (200, 600, 1500, 3000, 6000):
+        short(budget)
+        g.kv4_decode(q, pages, tab, lens, KS, VS, dev_status=st)
+        assert st.item() in (0, GDN_E_TIMEOUT)
+        short(0)
+        st.zero_()
+        assert torch.equal(g.kv4_decode(q, pages, tab, lens, KS, VS, dev_status=st), want) and st.item() == 0
