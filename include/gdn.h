@@ -351,7 +351,9 @@ gdn_status kv4_append(const kv4_cache *c, const kv4_batch *b, const uint16_t *k,
                       const uint16_t *v, int64_t v_stride, int32_t *dev_status, void *stream);
 
 /* The values the pages hold for the batch's new rows, rounded to BF16, into
- * contiguous k and v [T][n_kv_heads][head_dim]. Errors: as kv4_append. */
+ * contiguous k and v [T][n_kv_heads][head_dim]. A row that holds no token (a
+ * sequence's rows beyond kv_len, counted from its newest) gets zeros. Errors:
+ * as kv4_append. */
 gdn_status kv4_read(const kv4_cache *c, const kv4_batch *b, uint16_t *k, uint16_t *v, int32_t *dev_status,
                     void *stream);
 

@@ -19,11 +19,13 @@ struct RowsArgs {
   int items;  // append: (group, chunk of heads) pairs at most
 };
 // A group's new tokens [t0, t1) of sequence b (-1: none); token t is row n0 + t.
+// pos0 < 0: no tokens, rows of a batch that counts more new rows than the sequence has tokens.
 struct Group {
   int b, pos0, t0, t1;
   long long n0;
 };
-// The x-th group that new rows touch. One warp.
+// The x-th group that new rows touch, with ALL those before a sequence's start too. One warp.
+template <bool ALL>
 GDN_DEV Group find_group(const Kv4Args &a, int x, int lane) {
   Group r{-1, 0, 0, 0, 0};
   int base = 0;
@@ -32,7 +34,8 @@ GDN_DEV Group find_group(const Kv4Args &a, int x, int lane) {
     int n = 0, lo = 0;
     if (b0 + lane < a.B) {
       s = kv4_seq(a, b0 + lane);
-      lo = max(0, s.len - (s.q1 - s.q0));  // the first new token
+      lo = s.len - (s.q1 - s.q0);  // the first new token
+      if (!ALL) lo = max(0, lo);
       n = s.q1 > s.q0 && s.len > lo ? ((s.len - 1) >> 4) - (lo >> 4) + 1 : 0;
     }
     int incl = n;
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
     __syncthreads();  // the other buffer, the scales and the last found group have been read
     if (k == 0) {
       const long long mine = item + (long long)(tid >> 5) * gridDim.x;
-      const Group r = mine < p.items ? find_group(a, (int)(mine / chunks), lane) : Group{-1, 0, 0, 0, 0};
+      const Group r = mine < p.items ? find_group<false>(a, (int)(mine / chunks), lane) : Group{-1, 0, 0, 0, 0};
       if (lane == 0) {
         sm.found[tid >> 5] = r;
         sm.place[tid >> 5] = r.b >= 0 ? kv4_group<D>(a, r.b, r.pos0) : nullptr;
@@ -233,16 +236,25 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(RowsArgs p) {
   const int tid = threadIdx.x, lane = tid & 31;
   kv4_begin();
   if (tid < 32) {
-    const Group r = find_group(a, blockIdx.x, lane);
+    const Group r = find_group<true>(a, blockIdx.x, lane);
     if (lane == 0) {
       found = r;
-      place = r.b >= 0 ? kv4_group<D>(a, r.b, r.pos0) : nullptr;
+      place = r.b >= 0 && r.pos0 >= 0 ? kv4_group<D>(a, r.b, r.pos0) : nullptr;
     }
   }
   __syncthreads();
   const Group r = found;
-  if (r.b < 0 || !place) return;
+  if (r.b < 0) return;
   const int h0 = blockIdx.y * p.heads, hn = min(p.heads, a.Hkv - h0);
+  if (!place) {  // rows before the sequence's start (or of a bad page): zeros
+    const int words = hn * D / 8;
+    for (int i = tid; i < 2 * (r.t1 - r.t0) * words; i += 256) {
+      const int w = i % words, t = r.t0 + i / words % (r.t1 - r.t0);
+      uint16_t *row = i < (r.t1 - r.t0) * words ? p.k + (r.n0 + t) * p.k_stride : p.v + (r.n0 + t) * p.v_stride;
+      reinterpret_cast<uint4 *>(row + h0 * D)[w] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
   const size_t head = kv4_head_bytes<D>(a);
   const uint8_t *g = place + h0 * head;
   for (int i0 = tid; i0 < hn * ITEMS; i0 += 256 * U) {

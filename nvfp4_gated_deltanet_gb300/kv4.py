@@ -56,7 +56,8 @@ def kv4_append(k, v, pages, block_table, kv_len, k_scale, v_scale, q_start=None,
 
 def kv4_read(pages, block_table, kv_len, k_scale, v_scale, rows, q_start=None, k=None, v=None, dev_status=None,
              stream=None):
-    """(k, v) [rows][Hkv][d] BF16: the values that the pages hold for the batch's new rows."""
+    """(k, v) [rows][Hkv][d] BF16: the values that the pages hold for the
+    batch's new rows, zeros in rows that hold no token."""
     return _native().read(pages, block_table, kv_len, k_scale, v_scale, rows, q_start, k, v, dev_status, stream)
 
 
