@@ -80,6 +80,12 @@ struct Named {
   const char *name;
   PyObject *o;
 };
+struct OnDevice {
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit OnDevice(c10::Device d) {
+    if (c10::cuda::current_device() != d.index()) guard.set_device(d);
+  }
+};
 c10::Device device_of(std::initializer_list<Named> tensors, PyObject *stream) {
   const Named &first = *tensors.begin();
   const c10::Device dev = tensor(first.o, first.name).device();
@@ -197,7 +203,7 @@ PyObject *pair(const at::Tensor &a, const at::Tensor &b) {
 
 // k v pages table kv_len k_scale v_scale q_start dev_status stream
 PyObject *append(PyObject *const *a) {
-  const c10::cuda::CUDAGuard on(device_of({{"pages", a[2]}, {"k", a[0]}, {"v", a[1]}, {"block_table", a[3]},
+  const OnDevice on(device_of({{"pages", a[2]}, {"k", a[0]}, {"v", a[1]}, {"block_table", a[3]},
                                            {"kv_len", a[4]}, {"q_start", a[7]}, {"dev_status", a[8]}}, a[9]));
   const kv4_cache c = cache(a[2], a[5], a[6]);
   const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
@@ -209,7 +215,7 @@ PyObject *append(PyObject *const *a) {
 }
 // pages table kv_len k_scale v_scale rows q_start k v dev_status stream
 PyObject *read(PyObject *const *a) {
-  const c10::cuda::CUDAGuard on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"kv_len", a[2]}, {"q_start", a[6]},
+  const OnDevice on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"kv_len", a[2]}, {"q_start", a[6]},
                                            {"k", a[7]}, {"v", a[8]}, {"dev_status", a[9]}}, a[10]));
   const kv4_cache c = cache(a[0], a[3], a[4]);
   const int64_t rows = whole(a[5]);
@@ -224,7 +230,7 @@ PyObject *read(PyObject *const *a) {
 }
 // q pages table kv_len k_scale v_scale sm_scale out lse return_lse workspace dev_status stream
 PyObject *decode(PyObject *const *a) {
-  const c10::cuda::CUDAGuard on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
+  const OnDevice on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
                                            {"out", a[7]}, {"lse", a[8]}, {"workspace", a[10]},
                                            {"dev_status", a[11]}}, a[12]));
   const kv4_cache c = cache(a[1], a[4], a[5]);
@@ -254,7 +260,7 @@ PyObject *decode(PyObject *const *a) {
 }
 // q pages table kv_len q_start k_scale v_scale total_kv sm_scale out lse return_lse workspace dev_status stream
 PyObject *prefill(PyObject *const *a) {
-  const c10::cuda::CUDAGuard on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
+  const OnDevice on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
                                            {"q_start", a[4]}, {"out", a[9]}, {"lse", a[10]}, {"workspace", a[12]},
                                            {"dev_status", a[13]}}, a[14]));
   const kv4_cache c = cache(a[1], a[5], a[6]);
@@ -295,7 +301,7 @@ Layers layers_of(PyObject *o) {
 }
 // pages src dst dev_status stream
 PyObject *copy_pages(PyObject *const *a) {
-  const c10::cuda::CUDAGuard on(device_of({{"pages", a[0]}, {"src", a[1]}, {"dst", a[2]}, {"dev_status", a[3]}}, a[4]));
+  const OnDevice on(device_of({{"pages", a[0]}, {"src", a[1]}, {"dst", a[2]}, {"dev_status", a[3]}}, a[4]));
   const Layers l = layers_of(a[0]);
   const int32_t *src = i32(a[1], "src", 1), *dst = i32(a[2], "dst", 1);
   const int64_t n = THPVariable_Unpack(a[1]).size(0);
@@ -306,7 +312,7 @@ PyObject *copy_pages(PyObject *const *a) {
 }
 // pages table tables_out page_map n_live workspace dev_status stream
 PyObject *compact(PyObject *const *a) {
-  const c10::cuda::CUDAGuard on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"tables_out", a[2]},
+  const OnDevice on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"tables_out", a[2]},
                                            {"page_map", a[3]}, {"n_live", a[4]}, {"workspace", a[5]},
                                            {"dev_status", a[6]}}, a[7]));
   const Layers l = layers_of(a[0]);
