@@ -337,6 +337,8 @@ typedef struct {
   const int32_t *q_start;      /* device [B + 1]: sequence b's new rows are [q_start[b], q_start[b + 1]) of the T rows;
                                   rows from q_start[B] on are padding, left alone. NULL: T / B rows each */
   int B, max_pages, T;
+  int zero_padding;            /* kv4_read, kv4_prefill: bit 0: padding rows of the first output (k; out) get zeros,
+                                  bit 1: of the second (v zeros; lse -infinity). 0: they are left alone */
 } kv4_batch;
 
 /* Quantise the batch's new K and V rows (BF16, [T][n_kv_heads][head_dim]; a

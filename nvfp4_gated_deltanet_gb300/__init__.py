@@ -43,7 +43,8 @@ class Kv4CacheStruct(ctypes.Structure):
 
 
 class Kv4BatchStruct(ctypes.Structure):
-    _fields_ = [("kv_len", _vp), ("block_table", _vp), ("q_start", _vp), ("B", _i), ("max_pages", _i), ("T", _i)]
+    _fields_ = [("kv_len", _vp), ("block_table", _vp), ("q_start", _vp), ("B", _i), ("max_pages", _i), ("T", _i),
+                ("zero_padding", _i)]
 
 
 _kvc, _kvb = ctypes.POINTER(Kv4CacheStruct), ctypes.POINTER(Kv4BatchStruct)

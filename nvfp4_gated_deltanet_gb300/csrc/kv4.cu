@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(RowsArgs p) {
   const Kv4Args &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31;
   kv4_begin();
+  const int padding = kv4_padding(a);
   if (tid < 32) {
     const Group r = find_group<true>(a, blockIdx.x, lane);
     if (lane == 0) {
@@ -244,8 +245,12 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(RowsArgs p) {
   }
   __syncthreads();
   const Group r = found;
-  if (r.b < 0) return;
   const int h0 = blockIdx.y * p.heads, hn = min(p.heads, a.Hkv - h0);
+  for (long long row = (long long)padding + blockIdx.x; row < a.T; row += gridDim.x)
+    for (int i = tid; i < 2 * hn * (D / 8); i += 256)
+      if (a.zero_padding >> (i & 1) & 1)
+        reinterpret_cast<uint4 *>((i & 1 ? p.v + row * p.v_stride : p.k + row * p.k_stride) + h0 * D)[i / 2] = make_uint4(0, 0, 0, 0);
+  if (r.b < 0) return;
   if (!place) {  // rows before the sequence's start (or of a bad page): zeros
     const int words = hn * D / 8;
     for (int i = tid; i < 2 * (r.t1 - r.t0) * words; i += 256) {

@@ -31,7 +31,10 @@ struct Kv4Args {
   int B, cols, T;
   int32_t *status;
   long long wait;  // budget of a wait on copies, SM cycles
+  int zero_padding;  // kv4_batch::zero_padding; 0 without q_start
 };
+// The first padding row that is to be written: T where none is.
+GDN_DEV int kv4_padding(const Kv4Args &a) { return a.zero_padding ? max(0, a.q_start[a.B]) : a.T; }
 
 // A sequence's new rows [q0, q1) and its token count, checked: a bad entry
 // flags GDN_E_RANGE and reads as an empty sequence.

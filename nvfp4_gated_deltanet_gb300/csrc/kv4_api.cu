@@ -45,7 +45,8 @@ gdn_status check(const kv4_cache *c, const kv4_batch *b, Kv4Args &a, int32_t *st
     if ((long long)b->max_pages * p > 0x7fffffffLL) return GDN_E_OVERFLOW;
   }
   a = Kv4Args{c->pages, c->num_pages, p, c->n_kv_heads, c->head_dim, c->k_scale, c->v_scale, b->kv_len,
-              b->block_table, b->q_start, b->B, b->max_pages, b->T, status, wait_budget()};
+              b->block_table, b->q_start, b->B, b->max_pages, b->T, status, wait_budget(),
+              b->q_start ? b->zero_padding & 3 : 0};
   return GDN_OK;
 }
 

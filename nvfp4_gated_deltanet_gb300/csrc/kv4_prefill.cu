@@ -28,6 +28,7 @@
 //   warp 9            one thread streams K and V tiles by bulk copies and an
 //                     item's query rows by TMA (a box of tokens x the group's heads)
 //   warp 10           finds the next item
+//   warp 11           the padding rows, where they are asked for
 // The softmax warps take over the others' registers (232 and 40 of 168 each), so
 // that a thread holds its row's 128 scores: with 168 they had to be read from
 // tensor memory twice, half at a time (two 4096-token chunks 284 against 272 us).
@@ -594,6 +595,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         if (w.h < 0) break;
       }
       kv4_begin();  // on every path: this grid must not end before the one it follows
+    } else {
+      // ------------------------------------------------ padding rows (in the expansion they cost each of its CTAs a load)
+      for (long long row = (long long)kv4_padding(c) + blockIdx.x; row < c.T; row += gridDim.x) {
+        if (c.zero_padding & 1)
+          for (int i = lane; i < p.a.Hq * (D / 8); i += 32)
+            reinterpret_cast<uint4 *>(p.a.out + row * p.a.Hq * D)[i] = make_uint4(0, 0, 0, 0);
+        if ((c.zero_padding & 2) && p.a.lse)
+          for (int i = lane; i < p.a.Hq; i += 32) p.a.lse[row * p.a.Hq + i] = -INFINITY;
+      }
     }
   }
   tc_fence_before();

@@ -220,7 +220,8 @@ PyObject *read(PyObject *const *a) {
   const kv4_cache c = cache(a[0], a[3], a[4]);
   const int64_t rows = whole(a[5]);
   if (rows < 0) throw Bad("rows: expected a number of rows");
-  const kv4_batch b = batch(a[1], a[2], a[6], rows);
+  kv4_batch b = batch(a[1], a[2], a[6], rows);
+  b.zero_padding = !given(a[7]) | !given(a[8]) << 1;  // rows that nobody writes are zeros in outputs made here
   const int64_t shape[3] = {rows, c.n_kv_heads, c.head_dim};
   const at::Tensor &p = THPVariable_Unpack(a[0]);
   const at::Tensor k = output(a[7], "k", shape, at::kBFloat16, p, a[10]),
@@ -267,7 +268,8 @@ PyObject *prefill(PyObject *const *a) {
   const at::Tensor &q = tensor(a[0], "q");
   const int64_t qs = rows_stride(q, "q", -1, c.head_dim);
   const int Hq = as_int(q.size(1), "q");
-  const kv4_batch b = batch(a[2], a[3], a[4], q.size(0));
+  kv4_batch b = batch(a[2], a[3], a[4], q.size(0));
+  b.zero_padding = !given(a[9]) | !given(a[10]) << 1;
   const int64_t total = given(a[7]) ? whole(a[7]) : (int64_t)b.B * b.max_pages * c.page_tokens;
   const bool want = PyObject_IsTrue(a[11]) == 1;
   const at::Tensor out = output(a[9], "out", q.sizes(), at::kBFloat16, q, a[14]);

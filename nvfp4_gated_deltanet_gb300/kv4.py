@@ -57,7 +57,8 @@ def kv4_append(k, v, pages, block_table, kv_len, k_scale, v_scale, q_start=None,
 def kv4_read(pages, block_table, kv_len, k_scale, v_scale, rows, q_start=None, k=None, v=None, dev_status=None,
              stream=None):
     """(k, v) [rows][Hkv][d] BF16: the values that the pages hold for the
-    batch's new rows, zeros in rows that hold no token."""
+    batch's new rows, zeros in rows that hold no token. Padding rows (from
+    q_start[B] on) of a given k or v are left alone."""
     return _native().read(pages, block_table, kv_len, k_scale, v_scale, rows, q_start, k, v, dev_status, stream)
 
 
@@ -74,7 +75,9 @@ def kv4_prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_
                 lse=None, return_lse=False, workspace=None, dev_status=None, stream=None):
     """Causal attention of ragged prompt chunks: q [T][Hq][d], sequence b's rows
     [q_start[b], q_start[b + 1]) being its newest tokens. total_kv: an upper
-    bound of kv_len's sum (default: what the tables can hold)."""
+    bound of kv_len's sum (default: what the tables can hold). Padding rows
+    (from q_start[B] on) get zeros and lse = -infinity; in a given out or lse
+    they are left alone."""
     return _native().prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_kv, sm_scale, out, lse,
                              return_lse, workspace, dev_status, stream)
 

@@ -38,3 +38,42 @@ def test_read_writes_zeros_where_a_row_has_no_token(g, counts, lens, d, hkv):
         for x, y in zip(g.kv4_read(pages, tab, n, KS, VS, T, dev_status=st), (k, v)):
             assert torch.equal(x, y)
     assert st.item() == 0
+
+
+def dirty(like):
+    """Leave NaN in the memory that the next tensors of these sizes are made of."""
+    held = [torch.full_like(x, float("nan")) for x in like for _ in range(3)]
+    del held
+
+
+@pytest.mark.parametrize("d,hkv,hq,pad", [(64, 2, 6, 1), (128, 8, 16, 37), (128, 1, 64, 700)])
+def test_padding_rows(g, d, hkv, hq, pad):
+    """Rows from q_start[B] on: zeros (lse -infinity) in outputs that a call makes, left alone in given ones."""
+    counts, lens = [3, 40, 1], [20, 40, 0]
+    pages, tab, n, *_ = cached(g, lens, 16, hkv, d)
+    T = sum(counts)
+    start = torch.tensor([0, 3, 43, 44], dtype=torch.int32, device="cuda")
+    q = queries(T + pad, hq, d, 1)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def read(**kw):
+        return g.kv4_read(pages, tab, n, KS, VS, T + pad, q_start=start, dev_status=st, **kw)
+
+    def prefill(**kw):
+        return g.kv4_prefill(q, pages, tab, n, start, KS, VS, return_lse=True, dev_status=st, **kw)
+
+    for call, names, rest in ((read, ("k", "v"), (0.0, 0.0)), (prefill, ("out", "lse"), (0.0, -float("inf")))):
+        want = [x.clone() for x in call()]
+        for x, z in zip(want, rest):
+            assert not x[:T].isnan().any() and (x[T:] == z).all()
+        for _ in range(3):
+            dirty(want)
+            got = call()
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+            del got
+        for mine in (names, names[:1], names[1:]):   # both given, one of the two
+            given = {m: torch.full_like(want[names.index(m)], 7.0) for m in mine}
+            dirty(want)
+            for m, x, y, z in zip(names, call(**given), want, rest):
+                assert torch.equal(x[:T], y[:T]) and (x[T:] == (7.0 if m in mine else z)).all()
+    assert st.item() == 0
