@@ -50,11 +50,13 @@ gdn_status check(const kv4_cache *c, const kv4_batch *b, Kv4Args &a, int32_t *st
   return GDN_OK;
 }
 
+bool heads_fit(const kv4_cache *c, int Hq) { return Hq > 0 && Hq % c->n_kv_heads == 0 && Hq / c->n_kv_heads <= 64; }
+
 gdn_status check_attn(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int Hq, float sm,
                       uint16_t *out, float *lse, int32_t *status, Kv4AttnArgs &a) {
   gdn_status st = check(c, b, a.c, status);
   if (st != GDN_OK) return st;
-  if (Hq < 1 || Hq % c->n_kv_heads || Hq / c->n_kv_heads > 64) return GDN_E_SHAPE;
+  if (!heads_fit(c, Hq)) return GDN_E_SHAPE;
   if (!std::isfinite(sm)) return GDN_E_NONFINITE;
   if (!(sm > 0.0f)) return GDN_E_BAD_SCALE;
   if (b->T > 0) {
@@ -110,8 +112,7 @@ gdn_status kv4_read(const kv4_cache *c, const kv4_batch *b, uint16_t *k, uint16_
 // 0 for arguments that kv4_decode refuses.
 size_t kv4_decode_workspace(const kv4_cache *c, const kv4_batch *b, int n_q_heads) {
   Kv4AttnArgs a{};
-  if (check(c, b, a.c, nullptr) != GDN_OK || b->T == 0 || b->q_start || n_q_heads < 1 || n_q_heads % c->n_kv_heads)
-    return 0;
+  if (check(c, b, a.c, nullptr) != GDN_OK || b->T == 0 || b->q_start || !heads_fit(c, n_q_heads)) return 0;
   a.Hq = n_q_heads;
   return kv4_decode_bytes(a, kMaxSms);
 }
@@ -134,9 +135,10 @@ gdn_status kv4_decode(const kv4_cache *c, const kv4_batch *b, const uint16_t *q,
 }
 
 // 0 for arguments that kv4_prefill refuses.
-size_t kv4_prefill_workspace(const kv4_cache *c, const kv4_batch *b, int64_t total_kv, int) {
+size_t kv4_prefill_workspace(const kv4_cache *c, const kv4_batch *b, int64_t total_kv, int n_q_heads) {
   Kv4AttnArgs a{};
-  if (check(c, b, a.c, nullptr) != GDN_OK || b->T == 0 || total_kv < 0 || total_kv > 0x7fffffffLL) return 0;
+  if (check(c, b, a.c, nullptr) != GDN_OK || b->T == 0 || !heads_fit(c, n_q_heads)) return 0;
+  if (total_kv < 0 || total_kv > 0x7fffffffLL) return 0;
   return kv4_prefill_bytes(a, total_kv);
 }
 
