@@ -77,3 +77,45 @@ def test_padding_rows(g, d, hkv, hq, pad):
             for m, x, y, z in zip(names, call(**given), want, rest):
                 assert torch.equal(x[:T], y[:T]) and (x[T:] == (7.0 if m in mine else z)).all()
     assert st.item() == 0
+
+
+@pytest.mark.parametrize("rows", [[0, 4], [2, 1], [-1, 3], [0, -1], [4, 4], [0, 2 ** 31 - 1], [-2 ** 31, 0]])
+def test_bad_row_starts_are_flagged_and_write_nothing(g, rows):
+    """Row starts that do not ascend or leave the batch's three rows: GDN_E_RANGE from every call that takes them."""
+    hkv, hq, d = 2, 8, 128
+    x = torch.randn(3, hkv, d, device="cuda").bfloat16()
+    q = queries(3, hq, d, 0)
+    tab = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    n = torch.tensor([3], dtype=torch.int32, device="cuda")
+    start = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    pages, st = g.kv4_new_pages(2, 16, hkv, d), torch.zeros(1, dtype=torch.int32, device="cuda")
+    g.kv4_append(x, x, pages, tab, n, KS, VS, q_start=start, dev_status=st)
+    assert st.item() == 6 and not pages.any()
+    st.zero_()
+    g.kv4_read(pages, tab, n, KS, VS, 3, q_start=start, dev_status=st)
+    assert st.item() == 6
+    st.zero_()
+    g.kv4_prefill(q, pages, tab, n, start, KS, VS, dev_status=st)
+    assert st.item() == 6 and not pages.any()
+
+
+# whole-CTA teams and teams of four, cut items of 8, 16 and 32 rows
+@pytest.mark.parametrize("B,n,r,hq,hkv,d", [(2, 9000, 1, 8, 2, 128), (90, 900, 1, 16, 2, 128), (5, 6000, 4, 16, 4, 64),
+                                            (3, 5000, 8, 8, 2, 128)])
+def test_decode_in_a_workspace_of_exactly_its_size(g, B, n, r, hq, hkv, d):
+    """A caller's workspace, full of NaN, with bytes after it that stay: the result of the call's own."""
+    import ctypes
+    pages, tab, lens, *_ = cached(g, [n - 9 * b for b in range(B)], 64, hkv, d)
+    q = queries(B * r, hq, d, r).reshape(B, r, hq, d)
+    c = g.Kv4CacheStruct(pages.data_ptr(), pages.shape[0], 64, hkv, d, KS, VS)
+    b = g.Kv4BatchStruct(lens.data_ptr(), tab.data_ptr(), None, B, tab.shape[1], B * r)
+    need = g.lib().kv4_decode_workspace(ctypes.byref(c), ctypes.byref(b), hq)
+    assert need > 0
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = g.kv4_decode(q, pages, tab, lens, KS, VS, return_lse=True)
+    room = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        got = g.kv4_decode(q, pages, tab, lens, KS, VS, return_lse=True, workspace=room[:need], dev_status=st)
+        assert all(torch.equal(x, y) for x, y in zip(got, want)) and (room[need:] == 0xFF).all() and st.item() == 0
+    with pytest.raises(g.GdnError, match="GDN_E_SHAPE"):
+        g.kv4_decode(q, pages, tab, lens, KS, VS, workspace=room[:need - 1])
