@@ -50,6 +50,11 @@ int64_t whole(PyObject *o) {
   if (v == -1 && PyErr_Occurred()) throw Raised();
   return v;
 }
+bool truth(PyObject *o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised();
+  return v != 0;
+}
 bool given(PyObject *o) { return o != Py_None; }
 
 bool is_bf16(const at::Tensor &t) {
@@ -231,6 +236,7 @@ PyObject *read(PyObject *const *a) {
 }
 // q pages table kv_len k_scale v_scale sm_scale out lse return_lse workspace dev_status stream
 PyObject *decode(PyObject *const *a) {
+  const bool want = truth(a[9]);
   const OnDevice on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
                                            {"out", a[7]}, {"lse", a[8]}, {"workspace", a[10]},
                                            {"dev_status", a[11]}}, a[12]));
@@ -247,7 +253,6 @@ PyObject *decode(PyObject *const *a) {
   if (r > 1 && B > 1 && q.stride(0) != r * row) throw Bad("q: the rows of all sequences must be evenly spaced");
   const kv4_batch b = batch(a[2], a[3], Py_None, B * r);
   if (b.B != B) throw Bad("q and block_table disagree on the number of sequences");
-  const bool want = PyObject_IsTrue(a[9]) == 1;
   const at::Tensor out = output(a[7], "out", q.sizes(), at::kBFloat16, q, a[12]);
   const at::Tensor lse = want || given(a[8]) ? output(a[8], "lse", q.sizes().slice(0, q.dim() - 1), at::kFloat, q, a[12])
                                               : at::Tensor();
@@ -261,6 +266,7 @@ PyObject *decode(PyObject *const *a) {
 }
 // q pages table kv_len q_start k_scale v_scale total_kv sm_scale out lse return_lse workspace dev_status stream
 PyObject *prefill(PyObject *const *a) {
+  const bool want = truth(a[11]);
   const OnDevice on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
                                            {"q_start", a[4]}, {"out", a[9]}, {"lse", a[10]}, {"workspace", a[12]},
                                            {"dev_status", a[13]}}, a[14]));
@@ -271,7 +277,6 @@ PyObject *prefill(PyObject *const *a) {
   kv4_batch b = batch(a[2], a[3], a[4], q.size(0));
   b.zero_padding = !given(a[9]) | !given(a[10]) << 1;
   const int64_t total = given(a[7]) ? whole(a[7]) : (int64_t)b.B * b.max_pages * c.page_tokens;
-  const bool want = PyObject_IsTrue(a[11]) == 1;
   const at::Tensor out = output(a[9], "out", q.sizes(), at::kBFloat16, q, a[14]);
   const at::Tensor lse = want || given(a[10]) ? output(a[10], "lse", q.sizes().slice(0, 2), at::kFloat, q, a[14])
                                                : at::Tensor();

@@ -95,3 +95,14 @@ def test_decode_refuses_other_rows_than_the_batch_has(g, monkeypatch):
         for x in fit:                                # goes on to the checks of the call itself
             with pytest.raises(ValueError, match="CUDA"):
                 c.decode(0, x, batch)
+
+
+def test_a_return_lse_without_a_truth_value_raises_its_error(g):
+    """Not a result with an error set, which Python reports as a SystemError of the next call."""
+    pages, table, n = torch.zeros(4, 2, 1, 18 * 64, dtype=torch.uint8), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2).int()
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    for both in (torch.ones(2), torch.zeros(3)):
+        with pytest.raises(RuntimeError, match="Boolean value"):
+            g.kv4_decode(q, pages, table, n, 1.0, 1.0, return_lse=both)
+        with pytest.raises(RuntimeError, match="Boolean value"):
+            g.kv4_prefill(q, pages, table, n, None, 1.0, 1.0, return_lse=both)
