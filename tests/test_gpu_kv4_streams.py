@@ -144,3 +144,85 @@ def test_check_sees_what_other_streams_have_yet_to_flag(g, own):
     batch = c.grow([seq], 3, stream=side)
     c.append(0, k, k, batch, stream=side)
     assert c.check(side) == 0
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_order_of_prefill_copies_and_compaction(g, graph):
+    """Queries, lengths, row starts, tables, page ids and pages written just
+    before a call (on another stream, by copies and fills, by the calls
+    themselves) and overwritten just after it: prefill, page copies and
+    compaction see what came before them in their stream, and only that."""
+    hkv, hq, d, T, new = 4, 16, 128, 1500, 700
+    num = 2 * (T // 16 + 1)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    src = torch.randn(2, T, hkv, d, generator=gen, device="cuda").bfloat16()
+    queries = torch.randn(new, hq, d, generator=gen, device="cuda").bfloat16()
+    table = torch.randperm(num, generator=gen, device="cuda")[:T // 16 + 1].int().view(1, -1)
+    full = torch.tensor([T], dtype=torch.int32, device="cuda")
+    rows, all_rows = (torch.tensor([0, m], dtype=torch.int32, device="cuda") for m in (new, T))
+    free = torch.tensor([p for p in range(num) if p not in set(table[0].tolist())][:20], dtype=torch.int32, device="cuda")
+    some = table[0, :20].contiguous()
+    big = torch.randn(4096, 4096, generator=gen, device="cuda").bfloat16()
+    start = g.kv4_new_pages(num, 16, hkv, d)
+    g.kv4_append(src[0], src[1], start, table, full, KS, VS, q_start=all_rows)
+
+    q, lens, at, tab = torch.zeros_like(queries), torch.zeros_like(full), torch.zeros_like(rows), torch.zeros_like(table)
+    ids, to, pages = torch.zeros_like(some), torch.zeros_like(free), torch.zeros_like(start)
+    out, lse = torch.zeros_like(queries), torch.zeros(new, hq, device="cuda")
+    last, last_lse = torch.zeros_like(out), torch.zeros_like(lse)
+    tables, where, live = torch.zeros_like(table), torch.zeros(num, dtype=torch.int32, device="cuda"), torch.zeros_like(full)
+    got = [out, lse, last, last_lse, tables, where, live]
+    moved = torch.zeros_like(start)
+    side = torch.cuda.Stream()
+
+    def go(sync=lambda: None):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                big @ big
+            q.copy_(queries)
+            pages.copy_(start)
+        for x, y in ((lens, full), (at, rows), (tab, table), (ids, some), (to, free)):
+            x.copy_(y)
+        here.wait_stream(side)
+        sync()
+        g.kv4_prefill(q, pages, tab, lens, at, KS, VS, total_kv=T, out=out, lse=lse)
+        sync()
+        q.zero_()
+        at.zero_()
+        g.kv4_copy_pages(pages, ids, to)
+        sync()
+        ids.fill_(3)
+        tab[0, :20].copy_(to)                        # the copies in place of the pages they were made of
+        to.fill_(5)
+        g.kv4_compact(pages, tab, tables_out=tables, page_map=where, n_live=live)
+        sync()
+        tab.zero_()
+        q.copy_(queries)
+        at.copy_(rows)
+        g.kv4_prefill(q, pages, tables, lens, at, KS, VS, total_kv=T, out=last, lse=last_lse)
+        sync()
+        moved.copy_(pages)
+        for x in (q, lens, at, pages):
+            x.zero_()
+
+    go(torch.cuda.synchronize)                       # each call alone on the device
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (*got, moved)]
+    assert torch.equal(out, last) and torch.equal(lse, last_lse) and live.item() == T // 16 + 1
+    if graph:
+        run = torch.cuda.Stream()
+        run.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(run):
+            go()
+        torch.cuda.current_stream().wait_stream(run)
+        cuda_graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cuda_graph):
+            go()
+    for _ in range(10):
+        for x in (*got, moved):
+            x.zero_()
+        cuda_graph.replay() if graph else go()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((*got, moved), want))
