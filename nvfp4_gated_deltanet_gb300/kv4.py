@@ -44,6 +44,8 @@ def _native():
 
 def kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim, n_layers=None, device="cuda"):
     """Zeroed pages [num_pages][Hkv][page_tokens / 16][18 d], with a leading [n_layers] when given."""
+    if page_tokens < 16 or page_tokens % 16:         # the pages would hold fewer tokens than the caller counts
+        raise ValueError(f"page_tokens: expected a multiple of 16, not {page_tokens}")
     shape = (num_pages, n_kv_heads, page_tokens // 16, 18 * head_dim)
     return torch.zeros(shape if n_layers is None else (n_layers, *shape), dtype=torch.uint8, device=device)
 

@@ -106,3 +106,12 @@ def test_a_return_lse_without_a_truth_value_raises_its_error(g):
             g.kv4_decode(q, pages, table, n, 1.0, 1.0, return_lse=both)
         with pytest.raises(RuntimeError, match="Boolean value"):
             g.kv4_prefill(q, pages, table, n, None, 1.0, 1.0, return_lse=both)
+
+
+@pytest.mark.parametrize("page", [0, 8, 17, 24, 40, 100, 250, -16])
+def test_pages_that_are_no_whole_groups_are_refused(g, page):
+    """24 tokens a page would be 16 on the device, and the book's pages others than the kernels'."""
+    with pytest.raises(ValueError, match="page_tokens"):
+        g.kv4_new_pages(4, page, 2, 64, device="cpu")
+    with pytest.raises(ValueError, match="page_tokens"):
+        g.KV4Cache(4, page, 2, 64, 1.0, 1.0, device="cpu")
