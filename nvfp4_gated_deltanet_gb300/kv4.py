@@ -155,6 +155,20 @@ class KV4Book:
             self.seqs[s][1] += add
         return copies
 
+    def retract(self, seqs, tokens, copies):
+        """Take back the extend that was the book's last change; its copies need not have been made."""
+        source = {dst: src for src, dst in copies}
+        for s, add in zip(reversed(seqs), reversed(tokens)):
+            entry = self.seqs[s]
+            pages, n = entry[0], entry[1] - add
+            while len(pages) > -(-n // self.page_tokens):
+                self._drop(pages.pop())
+            if pages and pages[-1] in source:
+                mine, pages[-1] = pages[-1], source[pages[-1]]
+                self.holders[pages[-1]] += 1
+                self._drop(mine)
+            entry[1] = n
+
     def fork(self, seq: int) -> int:
         pages, n = self.seqs[seq]
         for p in pages:
@@ -252,14 +266,20 @@ class KV4Cache:
     def grow(self, seqs, tokens, stream=None) -> KV4Batch:
         """Room for tokens[i] (or `tokens` each) new tokens of every sequence,
         the copies of shared pages made, and the batch of the new rows; all on
-        `stream` (default: the current one), where the batch is to be used."""
+        `stream` (default: the current one), where the batch is to be used.
+        Where one of these fails, the book is as before."""
+        seqs = list(seqs)
         tokens = [tokens] * len(seqs) if isinstance(tokens, int) else list(tokens)
         pairs = self.book.extend(seqs, tokens)
-        with self._on(stream):
-            if pairs:
-                src, dst = self._dev([p[0] for p in pairs]), self._dev([p[1] for p in pairs])
-                kv4_copy_pages(self.layers, src, dst, dev_status=self.status)
-            return self.batch(seqs, tokens)
+        try:
+            with self._on(stream):
+                if pairs:
+                    src, dst = self._dev([p[0] for p in pairs]), self._dev([p[1] for p in pairs])
+                    kv4_copy_pages(self.layers, src, dst, dev_status=self.status)
+                return self.batch(seqs, tokens)
+        except BaseException:
+            self.book.retract(seqs, tokens, pairs)
+            raise
 
     def batch(self, seqs, tokens) -> KV4Batch:
         """The tables of the sequences as they are, their newest tokens[i] as the rows."""

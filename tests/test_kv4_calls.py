@@ -115,3 +115,59 @@ def test_pages_that_are_no_whole_groups_are_refused(g, page):
         g.kv4_new_pages(4, page, 2, 64, device="cpu")
     with pytest.raises(ValueError, match="page_tokens"):
         g.KV4Cache(4, page, 2, 64, 1.0, 1.0, device="cpu")
+
+
+def state(book):
+    return book.holders[:], book._free[:], {k: (v[0][:], v[1]) for k, v in book.seqs.items()}
+
+
+def test_growth_that_fails_on_the_device_leaves_the_book(g, monkeypatch):
+    """No memory for the tables: the sequences are not longer, and shared pages not given up for copies nobody made."""
+    c = g.KV4Cache(16, 16, 2, 64, 1.0, 1.0, device="cpu")
+    a, b = c.new(), c.new()
+    c.book.extend([a, b], [40, 16])
+    f = c.fork(a)
+    before = state(c.book)
+
+    def full(rows):
+        raise torch.cuda.OutOfMemoryError("no memory")
+
+    monkeypatch.setattr(c, "_dev", full)
+    for seqs, tokens in (([a, f, b], [1, 20, 1]), ([b], 30), ([f], [0]), ([a, b], 3)):
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            c.grow(seqs, tokens)
+        assert state(c.book) == before
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_retract_takes_an_extend_back(g, seed):
+    import random
+    rng = random.Random(seed)
+    b = g.KV4Book(60, 16)
+    for _ in range(400):
+        ids = list(b.seqs)
+        op = rng.choice(["new", "extend", "extend", "extend", "fork", "free", "truncate", "compact"])
+        if op == "new" or not ids:
+            b.new()
+        elif op == "extend":
+            some = rng.sample(ids, rng.randint(1, min(5, len(ids))))
+            tokens = [rng.randint(0, 40) for _ in some]
+            before = state(b)
+            try:
+                copies = b.extend(some, tokens)
+            except MemoryError:
+                b.free(some[0])
+                continue
+            after = state(b)
+            b.retract(some, tokens, copies)
+            assert state(b) == before
+            assert b.extend(some, tokens) == copies and state(b) == after
+        elif op == "fork" and len(ids) < 12:
+            b.fork(rng.choice(ids))
+        elif op == "free":
+            b.free(rng.choice(ids))
+        elif op == "truncate":
+            s = rng.choice(ids)
+            b.truncate(s, rng.randint(0, b.length(s)))
+        elif op == "compact":
+            b.compact()
