@@ -5,7 +5,6 @@ DeltaNet layer (recurrent state in a slot) followed by a softmax attention layer
     prompts        gdn prefill per sequence, kv4 append + prefill for all of them
     decode         gdn decode step, kv4 append + decode, one token per sequence
     fork           the KV pages are shared until one side grows, the slot is copied
-    truncate       rejected candidates leave the cache
     compact        the live pages move to the front of every layer
 
     python examples/hybrid_stack.py

@@ -59,15 +59,10 @@ GDN_DEV Kv4Seq kv4_seq(const Kv4Args &a, int b) {
   if (bad_len) s.len = 0;
   return s;
 }
-// The sequence whose rows hold row n, or -1 (a padding row).
-GDN_DEV int kv4_seq_of(const Kv4Args &a, int n) {
-  if (!a.q_start) return n / (a.T / a.B);
-  int lo = 0, hi = a.B;  // the first b with q_start[b + 1] > n
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.q_start[mid + 1] > n) hi = mid; else lo = mid + 1;
-  }
-  return lo < a.B ? lo : -1;
+// Sequence b's tokens, checked (kv4_seq without rows and without the flag).
+GDN_DEV int kv4_len(const Kv4Args &a, int b) {
+  const int n = a.kv_len[b];
+  return n < 0 || n > (long long)a.cols * a.page_tokens ? 0 : n;
 }
 // The group that holds token `pos` of sequence b (head 0), or null for a bad page id.
 template <int D>

@@ -117,12 +117,7 @@ GDN_DEV long long quot(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : quot64(a, b);
 }
 
-// Sequence b's tokens, checked (kv4_seq without rows), and its tiles: an empty
-// sequence has one tile with no tokens, so that its rows are written.
-GDN_DEV int seq_len(const Kv4Args &c, int b) {
-  const int n = c.kv_len[b];
-  return n < 0 || n > (long long)c.cols * c.page_tokens ? 0 : n;
-}
+// A sequence's tiles: an empty one has one tile with no tokens, so that its rows are written.
 template <int TILE>
 GDN_DEV int tiles_of(int len) { return len > 0 ? (len + TILE - 1) / TILE : 1; }
 
@@ -143,7 +138,7 @@ struct Cursor {
 template <int TILE>
 GDN_DEV void seek(const Kv4Args &c, Cursor &k, int b) {
   k.b = b;
-  k.len = seq_len(c, b);
+  k.len = kv4_len(c, b);
   k.nt = tiles_of<TILE>(k.len);
 }
 template <int TILE>
@@ -157,7 +152,7 @@ GDN_DEV void next_item(const Kv4Args &c, Cursor &k, int HR) {
 // The tiles of sequences b0 + lane (0 past the end), for one KV head and row group.
 template <int TILE>
 GDN_DEV int lane_tiles(const Kv4Args &c, int b0, int lane) {
-  return b0 + lane < c.B ? tiles_of<TILE>(seq_len(c, b0 + lane)) : 0;
+  return b0 + lane < c.B ? tiles_of<TILE>(kv4_len(c, b0 + lane)) : 0;
 }
 // The tile at cost u (each item costs its tiles and `extra`, which comes
 // first), and how many tiles lie before it. All lanes of a warp. n0:
@@ -221,7 +216,7 @@ GDN_DEV long long find_cut(const DecodeArgs &p, int warps, int HR, int lane, int
     const int items = c.B * HR;
     const int i0 = (int)quot((long long)items * from, most), i1 = (int)quot((long long)items * cut, most);
     int n = 0;
-    for (int i = i0; i < i1; ++i) n += tiles_of<TILE>(seq_len(c, i / HR));
+    for (int i = i0; i < i1; ++i) n += tiles_of<TILE>(kv4_len(c, i / HR));
     if (i1 < items) {
       seek<TILE>(c, k, i1 / HR);
       k.hr = i1 % HR;
@@ -328,7 +323,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
   }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < c.B; b += S::kThreads)
-      if (c.kv_len[b] != seq_len(c, b)) flag_status(c.status, GDN_E_RANGE);
+      if (c.kv_len[b] != kv4_len(c, b)) flag_status(c.status, GDN_E_RANGE);
 
   int at = 0, next = warp;  // the segment's first tile (cur), and this warp's next one, within the run
   // ------------------------------------------------ loads

@@ -65,10 +65,6 @@ struct PrefillKv4 {
   uint16_t *tiles;                // [cap][Hkv][K: d / 64 x 128 rows x 64, BF16; V^T: 2 x d rows x 64, FP16], swizzled
 };
 
-GDN_DEV int seq_len(const Kv4Args &c, int b) {
-  const int n = c.kv_len[b];
-  return n < 0 || n > (long long)c.cols * c.page_tokens ? 0 : n;
-}
 // The sequence that holds item x when sequence b has count(b) of them, and the
 // items before it; -1 past the end. All lanes of a warp.
 template <typename F>
@@ -102,7 +98,7 @@ __global__ void __launch_bounds__(256) kv4_expand_kernel(PrefillKv4 p) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int x = blockIdx.x / c.Hkv, h = blockIdx.x % c.Hkv;
   int before = 0, total = 0;
-  const int b = find_item(c.B, x, lane, [&](int i) { return (seq_len(c, i) + kKv - 1) / kKv; }, before, total);
+  const int b = find_item(c.B, x, lane, [&](int i) { return (kv4_len(c, i) + kKv - 1) / kKv; }, before, total);
   if (blockIdx.x == 0) {
     if (tid == 0) {
       if (total > p.cap) flag_status(c.status, GDN_E_RANGE);
@@ -111,7 +107,7 @@ __global__ void __launch_bounds__(256) kv4_expand_kernel(PrefillKv4 p) {
     for (int i = tid; i < c.B; i += 256) kv4_seq(c, i);  // flags bad entries
   }
   if (b < 0) return;
-  const int pos0 = (x - before) * kKv, len = seq_len(c, b);
+  const int pos0 = (x - before) * kKv, len = kv4_len(c, b);
   __shared__ const uint8_t *groups[kKv / 16];
   if (tid < kKv / 16) {
     const uint8_t *g = pos0 + tid * 16 < len ? kv4_group<D>(c, b, pos0 + tid * 16) : nullptr;

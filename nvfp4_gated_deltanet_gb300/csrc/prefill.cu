@@ -421,20 +421,6 @@ constexpr int kPrepSub = 128 * 128;           // one [128 rows][64 FP16] sub-til
 constexpr int kPrepTile = 2 * kPrepSub;       // a 128 x 128 FP16 operand
 constexpr int kPrepSmem = 1024 + 3 * kPrepTile + 4 * kC * 4 + 64;
 
-GDN_DEV void mma_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// byte offset of FP16 element (row, col) in a [rows][64 FP16] tile, 128-byte swizzle
-GDN_DEV uint32_t sw16(int row, int col) {
-  return (uint32_t)(row * 128 + ((((col >> 3) ^ (row & 7)) << 4) | ((col & 7) << 1)));
-}
-
 __global__ void __launch_bounds__(256, 2)
     chunk_prep_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          PrefillArgs a) {
@@ -604,10 +590,10 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
       for (int k = 0; k < 32; k += 2) {
         const int j = j0 + k;
-        const uint16_t h0 = *reinterpret_cast<const uint16_t *>(bp + sw16(j, d & 63));
-        const uint16_t h1 = *reinterpret_cast<const uint16_t *>(bp + sw16(j + 1, d & 63));
-        const uint16_t l0 = *reinterpret_cast<const uint16_t *>(bp + sw16(64 + j, d & 63));
-        const uint16_t l1 = *reinterpret_cast<const uint16_t *>(bp + sw16(65 + j, d & 63));
+        const uint16_t h0 = *reinterpret_cast<const uint16_t *>(bp + sw_off16(j, d & 63));
+        const uint16_t h1 = *reinterpret_cast<const uint16_t *>(bp + sw_off16(j + 1, d & 63));
+        const uint16_t l0 = *reinterpret_cast<const uint16_t *>(bp + sw_off16(64 + j, d & 63));
+        const uint16_t l1 = *reinterpret_cast<const uint16_t *>(bp + sw_off16(65 + j, d & 63));
         x[k] = (__half2float(__ushort_as_half(h0)) + __half2float(__ushort_as_half(l0))) * 0x1p-14f;
         x[k + 1] = (__half2float(__ushort_as_half(h1)) + __half2float(__ushort_as_half(l1))) * 0x1p-14f;
         hw[k / 2] = (uint32_t)h0 | ((uint32_t)h1 << 16);
