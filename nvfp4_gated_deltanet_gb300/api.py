@@ -26,14 +26,30 @@ def _dev(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
+def _new(stream, *shape, dtype, device):
+    """An output of a call on `stream` (default: the current one), allocated as
+    that stream's: a block that the current stream has freed may still be in
+    use there, and nothing orders the two. The caller goes on with it on the
+    current stream, so it is recorded there."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):    # anything with a cuda_stream
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(*shape, dtype=dtype, device=device)
+    if t.numel():
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def nvfp4_quantize(x: torch.Tensor, tensor_scale: float, codes=None, scales=None, dev_status=None, stream=None):
     """x [rows][cols] BF16 (or its bits) or FP32 -> (codes uint8 [rows][cols/2], scales uint8 [rows][cols/16])."""
     _dev(x)
     rows, cols = x.shape
     if codes is None:
-        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
+        codes = _new(stream, rows, cols // 2, dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty(rows, cols // 16, dtype=torch.uint8, device=x.device)
+        scales = _new(stream, rows, cols // 16, dtype=torch.uint8, device=x.device)
     st = lib().nvfp4_quantize(_ptr(x), int(x.dtype == torch.float32), rows, cols, float(tensor_scale),
                               _ptr(codes), _ptr(scales), _ptr(dev_status), _stream(stream))
     _check(st, "nvfp4_quantize")
@@ -48,7 +64,7 @@ def nvfp4_gemm(a_codes, a_scales, a_ts, b_codes, b_scales, b_ts, out_dtype=torch
     """C[M][N] = A_hat[M][K] B_hat[N][K]^T (FP32 accumulation) as BF16 or FP32."""
     M, N, K = a_codes.shape[0], b_codes.shape[0], a_codes.shape[1] * 2
     if c is None:
-        c = torch.empty(M, N, dtype=out_dtype, device=a_codes.device)
+        c = _new(stream, M, N, dtype=out_dtype, device=a_codes.device)
     A, B = _nv(a_codes, a_scales, a_ts), _nv(b_codes, b_scales, b_ts)
     st = lib().nvfp4_gemm(ctypes.byref(A), M, ctypes.byref(B), N, K, _ptr(c), int(c.dtype != torch.float32),
                           _stream(stream))
@@ -68,7 +84,7 @@ def kda_step(q, k, v, g, beta, state, o=None, stream=None):
     if not bf16 and state.dtype != torch.float32:
         raise ValueError("state must be float32 or BF16 bits")
     if o is None:
-        o = torch.empty(M, H, d, dtype=torch.float32, device=q.device)
+        o = _new(stream, M, H, d, dtype=torch.float32, device=q.device)
     st = lib().kda_step(_ptr(_dev(q)), _ptr(_dev(k)), _ptr(_dev(v)), _ptr(_dev(g)), _ptr(_dev(beta)),
                         _ptr(_dev(state)), int(bf16), M, H, d, _ptr(_dev(o)), _stream(stream))
     _check(st, "kda_step")
@@ -125,7 +141,7 @@ class GatedDeltaNetLayer:
     def decode_step(self, x, slot_ids, conv_state, ssm_state, out=None, stream=None):
         B = x.shape[0]
         if out is None:
-            out = torch.empty(B, self.H, dtype=torch.int16, device=x.device)
+            out = _new(stream, B, self.H, dtype=torch.int16, device=x.device)
         st = lib().gdn_decode_step(self._ctx, _ptr(_dev(x)), _ptr(_dev(slot_ids)), B, _ptr(out),
                                    _ptr(_dev(conv_state)), _ptr(self._state(ssm_state)), conv_state.shape[0],
                                    _stream(stream))
@@ -135,7 +151,7 @@ class GatedDeltaNetLayer:
     def mix_step(self, qkvz, ba, slot_ids, conv_state, ssm_state, y=None, stream=None):
         B = qkvz.shape[0]
         if y is None:
-            y = torch.empty(B, self.Hv * self.D, dtype=torch.float32, device=qkvz.device)
+            y = _new(stream, B, self.Hv * self.D, dtype=torch.float32, device=qkvz.device)
         st = lib().gdn_mix_step(self._ctx, _ptr(_dev(qkvz)), _ptr(_dev(ba)), _ptr(_dev(slot_ids)), B, _ptr(y),
                                 _ptr(_dev(conv_state)), _ptr(self._state(ssm_state)), conv_state.shape[0], _stream(stream))
         _check(st, "gdn_mix_step")
@@ -146,7 +162,7 @@ class GatedDeltaNetLayer:
         B = x.shape[0]
         nin = 2 * self.Hk * self.D + 2 * self.Hv * self.D + 2 * self.Hv
         if out is None:
-            out = torch.empty(B, nin, dtype=torch.int16, device=x.device)
+            out = _new(stream, B, nin, dtype=torch.int16, device=x.device)
         st = lib().gdn_in_proj(self._ctx, _ptr(_dev(x)), _ptr(slot_ids), B, _ptr(_dev(out)), _stream(stream))
         _check(st, "gdn_in_proj")
         return out
@@ -157,9 +173,9 @@ class GatedDeltaNetLayer:
         B = x.shape[0]
         vd = self.Hv * self.D
         if y_codes is None:
-            y_codes = torch.empty(B, vd // 2, dtype=torch.uint8, device=x.device)
+            y_codes = _new(stream, B, vd // 2, dtype=torch.uint8, device=x.device)
         if y_scales is None:
-            y_scales = torch.empty(B, vd // 16, dtype=torch.uint8, device=x.device)
+            y_scales = _new(stream, B, vd // 16, dtype=torch.uint8, device=x.device)
         st = lib().gdn_in_mix(self._ctx, _ptr(_dev(x)), _ptr(_dev(slot_ids)), B, _ptr(_dev(y_codes)),
                               _ptr(_dev(y_scales)), _ptr(_dev(conv_state)), _ptr(self._state(ssm_state)),
                               conv_state.shape[0], _stream(stream))
@@ -170,7 +186,7 @@ class GatedDeltaNetLayer:
         """The out-projection of B <= 8 NVFP4 rows -> out [B][H] BF16 bits."""
         B = y_codes.shape[0]
         if out is None:
-            out = torch.empty(B, self.H, dtype=torch.int16, device=y_codes.device)
+            out = _new(stream, B, self.H, dtype=torch.int16, device=y_codes.device)
         st = lib().gdn_out_proj(self._ctx, _ptr(_dev(y_codes)), _ptr(_dev(y_scales)), B, _ptr(_dev(out)),
                                 _stream(stream))
         _check(st, "gdn_out_proj")
@@ -189,7 +205,7 @@ class GatedDeltaNetLayer:
         after every token; the slots' states are not modified."""
         B, r = x.shape[0], x.shape[1]
         if out is None:
-            out = torch.empty(B, r, self.H, dtype=torch.int16, device=x.device)
+            out = _new(stream, B, r, self.H, dtype=torch.int16, device=x.device)
         st = lib().gdn_verify(self._ctx, _ptr(_dev(x)), _ptr(_dev(slot_ids)), B, r, _ptr(out),
                               _ptr(_dev(conv_state)), _ptr(self._state(ssm_state)), conv_state.shape[0],
                               _ptr(_dev(snap_conv)), _ptr(self._state(snap_ssm)), _stream(stream))
@@ -207,7 +223,7 @@ class GatedDeltaNetLayer:
     def prefill(self, x, slot, init_zero, conv_state, ssm_state, out=None, stream=None):
         T = x.shape[0]
         if out is None:
-            out = torch.empty(T, self.H, dtype=torch.int16, device=x.device)
+            out = _new(stream, T, self.H, dtype=torch.int16, device=x.device)
         st = lib().gdn_prefill(self._ctx, _ptr(_dev(x)), T, int(slot), int(bool(init_zero)), _ptr(out),
                                _ptr(_dev(conv_state)), _ptr(self._state(ssm_state)), conv_state.shape[0], _stream(stream))
         _check(st, "gdn_prefill")
