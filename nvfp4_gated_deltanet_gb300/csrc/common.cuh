@@ -325,7 +325,7 @@ GDN_DEV bool mbar_wait(uint64_t *bar, uint32_t parity) {
 }
 // The same with a budget of its own (SM cycles): a short one gives up on what is not there at once.
 GDN_DEV bool mbar_wait_within(uint64_t *bar, uint32_t parity, long long budget) {
-  if (mbar_test_wait(bar, parity)) return true;
+  if (budget < kWaitCycles ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   do {
     if (clock64() - t0 > budget) return false;
