@@ -146,11 +146,13 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
     fence_barrier_init();
   }
   kv4_begin();
+  uint32_t armed = 0, turns = 0;  // bit `buf`: parity of the buffer's next fetch (thread 0), of its next wait
   auto fetch = [&](int item, int k, int buf) {  // warp 0: the rows of found[k]
     const Group r = sm.found[k];
     if (r.b < 0) return;
     const int h0 = item % chunks * p.heads, hn = min(p.heads, a.Hkv - h0);
     if (lane == 0) mbar_arrive_expect_tx(&sm.landed[buf], 2 * (r.t1 - r.t0) * hn * D * 2);
+    armed ^= 1u << buf;
     __syncwarp();
     const int t = lane & 15;
     if (t >= r.t0 && t < r.t1)
@@ -160,7 +162,6 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
   };
   const size_t head = kv4_head_bytes<D>(a);
   const float invk = inv6ts_of(a.ks), invv = inv6ts_of(a.vs);
-  uint32_t turns = 0;  // bit `buf`: parity of the buffer's next use
   for (int item = blockIdx.x, n = 0;; item += gridDim.x, ++n) {
     const int k = n & 7, buf = n & 1;
     __syncthreads();  // the other buffer, the scales and the last found group have been read
@@ -178,14 +179,15 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
     if (r.b < 0) break;  // items are in order: none follows
     if (tid < 32 && k < 7) fetch(item + gridDim.x, k + 1, buf ^ 1);
     const bool ok = mbar_wait_within(&sm.landed[buf], turns >> buf & 1u, a.wait);
+    turns ^= 1u << buf;
     if (!ok) {
       flag_status(a.status, GDN_E_TIMEOUT);
       sm.gave_up = 1;
     }
     const int h0 = item % chunks * p.heads, hn = min(p.heads, a.Hkv - h0);
     uint8_t *g = sm.place[k];  // null: a bad page, flagged
+    if (g) g += h0 * head;
     if (g && ok) {
-      g += h0 * head;
       for (int i = tid; i < hn * ITEMS; i += 256) {
         const int blk = i % NB, t = i / NB % 16, is_v = i / (16 * NB) & 1, h = i / ITEMS;
         if (t < r.t0 || t >= r.t1) continue;
@@ -199,13 +201,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
       }
     }
     __syncthreads();
-    if (sm.gave_up) {  // a thread's wait gave up: the copies in flight land (or a bounded wait for each ends), and the CTA ends
-      mbar_wait(&sm.landed[buf], turns >> buf & 1u);
-      if (k < 7 && sm.found[k + 1].b >= 0) mbar_wait(&sm.landed[buf ^ 1], turns >> (buf ^ 1) & 1u);
-      break;
-    }
-    turns ^= 1u << buf;
-    if (g) {
+    const bool stop = sm.gave_up;  // set between the loop's first barrier and this one only: the same for all
+    if (g) {  // (what a group gets whose rows a thread gave up waiting for is unspecified)
       if (r.t0 == 0 && r.t1 == 16) {
         for (int i = tid; i < hn * (2 * D / 16); i += 256) {
           const int h = i / (2 * D / 16), w = i % (2 * D / 16);
@@ -220,6 +217,11 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(RowsArgs p) {
         }
       }
     }
+    if (stop) break;
+  }
+  if (tid == 0 && sm.gave_up) {  // the copies in flight land (or a bounded wait for each ends) before the CTA leaves
+    mbar_wait(&sm.landed[0], (armed & 1u) ^ 1u);
+    mbar_wait(&sm.landed[1], (armed >> 1 & 1u) ^ 1u);
   }
 }
 
