@@ -119,9 +119,10 @@ GDN_DEV bool quant_bf16x16(const uint4 (&x)[2], float ts, float inv6ts, uint32_t
 // gathered in shared memory and leave as 16-byte words where all of the group's
 // tokens are new: a V scale is a byte 16 bytes from its token's next one, and
 // single bytes cost more memory transactions than all the codes.
-// Bound by issue slots (a block's 16 values: a maximum, a division, 16 products,
-// 8 conversions) beside the bytes: 16384 rows of 8 heads, d = 128, 67 MB read as
-// rows: 25.7 us.
+// Bound by neither the bytes nor the issue slots (a block's 16 values: a maximum, a
+// division, 16 products, 8 conversions; 51% of them used) but by the two barriers of
+// a group, the largest stall: 22638 rows of 8 heads, d = 128, 93 MB read and 26
+// written: 22.9 us in a graph, where the bytes take 17.5.
 template <int D>
 struct AppendSmem {
   uint16_t rows[2][2][16][kHeads * D];  // [buffer][K, V][token]
@@ -243,8 +244,8 @@ __device__ __noinline__ void read_zeros(const RowsArgs &p, Group r, bool empty, 
 }
 
 // Read back: a thread takes half a block (4 code bytes in, 16 bytes out), so that a
-// warp's stores are whole lines. 16384 rows of 8 heads, d = 128, 26 MB read and
-// 67 written: 22 us (a block a thread, whose stores are half lines, took 5 more).
+// warp's stores are whole lines. 22638 rows of 8 heads, d = 128, 26 MB read and
+// 93 written: 21.9 us (a block a thread, whose stores are half lines, took 5 more).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ RowsArgs p) {
   constexpr int NH = D / 8, ITEMS = 2 * 16 * NH;  // half blocks of a row; of a head's K and V of 16 tokens

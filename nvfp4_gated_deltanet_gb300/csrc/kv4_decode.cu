@@ -39,7 +39,7 @@
 // one's parts meet, and fewer warps wait for the slowest.
 //
 // Measured (32 query heads, d = 128): 64 sequences of up to 8190 tokens, 8 KV
-// heads, 291 MB: 57 us, 5.1 TB/s (0.75 of the copy bandwidth); one of 200001, 4 KV
+// heads, 291 MB: 56 us, 5.2 TB/s (0.76 of the copy bandwidth); one of 200001, 4 KV
 // heads, 115 MB: 28 us. Before the first tile pass 10000 cycles, 5 us (the lengths,
 // the run's ends, the page table, the query rows, the first tiles, one after the
 // other); the join adds 3. When both took 59 and 29.6, the loads alone took 54 and

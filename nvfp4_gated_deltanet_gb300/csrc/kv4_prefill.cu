@@ -6,7 +6,8 @@
 // chunk of a few tokens. Two kernels:
 //
 // kv4_expand_kernel decodes every sequence's cache once into tiles of 128
-// tokens, exactly (E2M1 x E4M3 has five significant bits): K in BF16 as the
+// tokens, exactly (E2M1 x E4M3 has at most six significant bits, 3 x 15 = 45, and is
+// 0 or between 2^-10 and 2688 in magnitude): K in BF16 as the
 // B operand of S = Q K^T, whose A operand is q as it came, and V transposed in
 // FP16 as the B operand of O += P V, both already in the 128-byte swizzle that
 // the MMA reads: each tile is one bulk copy. Decoding inside the attention kernel
@@ -31,9 +32,10 @@
 //   warp 11           the padding rows, where they are asked for
 // The softmax warps take over the others' registers (232 and 40 of 168 each), so
 // that a thread holds its row's 128 scores: with 168 they had to be read from
-// tensor memory twice, half at a time (two 4096-token chunks 284 against 272 us).
+// tensor memory twice, half at a time (284 against 272 us for the chunks below).
 // Measured: two chunks of 4096 and 789 tokens, 32 query heads on 8 of d = 128,
-// over 8100 and 2221 cached: 267 us, 1609 TFLOP/s, 0.85 of a large BF16 product.
+// over 8100 and 2221 cached: 268 us in a graph, 1.60 PFLOP/s, 0.84 of a large BF16
+// product; call after call 280 us, 1.54.
 // What is left: a row tile's chain of softmax (1500 cycles), O += P V and S = Q K^T
 // (1024) takes longer than the tensor cores' 2048 for both tiles.
 // A row's weights are 2^(z - m + 6) with a maximum m that is only moved (and O

@@ -5,7 +5,9 @@ errors and numerics are described there). ``pages`` is a uint8 CUDA tensor
 [num_pages][Hkv][page_tokens / 16][18 * d], or [layers][num_pages]... for the
 calls that take all layers at once; its shape gives page_tokens, Hkv and d. A
 call runs on the pages' device, where its other tensors must be, and on that
-device's current stream unless one is given.
+device's current stream unless one is given. Outputs it makes on a given stream
+are that stream's memory, kept until the current stream is done with them too;
+its inputs are the caller's to keep until the given stream has read them.
 
     pages = kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim)
     kv4_append(k, v, pages, table, kv_len, k_scale, v_scale)
