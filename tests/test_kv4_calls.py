@@ -42,6 +42,8 @@ def calls(g):
 
 @pytest.mark.parametrize("i", range(6))
 def test_tensors_of_several_devices_are_refused(g, i):
+    if torch.cuda.device_count() == 1:
+        pytest.skip("where there is one GPU, not even a stand-in can name a second")
     f, tensors, rest = calls(g)[i]
     for odd in tensors:
         args = {k: on("cuda:1" if k == odd else "cuda:0", *shape, dtype=dt) for k, (shape, dt) in tensors.items()}
