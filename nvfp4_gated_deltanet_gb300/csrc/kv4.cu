@@ -256,7 +256,10 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ R
   const Kv4Args &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31;
   kv4_begin();
-  if (tid == 32) padding = kv4_padding(a);
+  if (tid >> 5 == 1) {
+    const int first = kv4_padding(a, lane);
+    if (lane == 0) padding = first;
+  }
   if (tid < 32) {
     const Group r = find_group<true>(a, blockIdx.x, lane);
     if (lane == 0) {

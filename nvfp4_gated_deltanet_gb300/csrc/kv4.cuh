@@ -33,8 +33,19 @@ struct Kv4Args {
   long long wait;  // budget of a wait on copies, SM cycles
   int zero_padding;  // kv4_batch::zero_padding; 0 without q_start
 };
-// The first padding row that is to be written: T where none is.
-GDN_DEV int kv4_padding(const Kv4Args &a) { return a.zero_padding ? max(0, a.q_start[a.B]) : a.T; }
+// The first padding row that is to be written (T where none is): past every row
+// start, so that a bad one takes no rows from the other sequences. A whole warp.
+GDN_DEV int kv4_padding(const Kv4Args &a, int lane) {
+  if (!a.zero_padding) return a.T;
+  int last = 0;
+  for (int i = lane; i <= a.B; i += 32) {
+    const int q = a.q_start[i];
+    if (q <= a.T) last = max(last, q);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+  return last;
+}
 
 // A sequence's new rows [q0, q1) and its token count, checked: a bad entry
 // flags GDN_E_RANGE and reads as an empty sequence.

@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       kv4_begin();  // on every path: this grid must not end before the one it follows
     } else {
       // ------------------------------------------------ padding rows (in the expansion they cost each of its CTAs a load)
-      for (long long row = (long long)kv4_padding(c) + blockIdx.x; row < c.T; row += gridDim.x) {
+      for (long long row = (long long)kv4_padding(c, lane) + blockIdx.x; row < c.T; row += gridDim.x) {
         if (c.zero_padding & 1)
           for (int i = lane; i < p.a.Hq * (D / 8); i += 32)
             reinterpret_cast<uint4 *>(p.a.out + row * p.a.Hq * D)[i] = make_uint4(0, 0, 0, 0);

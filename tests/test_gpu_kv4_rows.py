@@ -119,3 +119,24 @@ def test_decode_in_a_workspace_of_exactly_its_size(g, B, n, r, hq, hkv, d):
         assert all(torch.equal(x, y) for x, y in zip(got, want)) and (room[need:] == 0xFF).all() and st.item() == 0
     with pytest.raises(g.GdnError, match="GDN_E_SHAPE"):
         g.kv4_decode(q, pages, tab, lens, KS, VS, workspace=room[:need - 1])
+
+
+@pytest.mark.parametrize("bad", [[0, 5, -1], [0, 5, 3], [0, 5, 99], [0, 5, 0], [0, 5, -2 ** 31]])
+def test_a_bad_row_start_takes_no_rows_from_other_sequences(g, bad):
+    """The first sequence's rows are as with good row starts, in outputs that the calls make."""
+    hkv, hq, d, T = 2, 8, 128, 40
+    pages, tab, n, *_ = cached(g, [30, 20], 16, hkv, d)
+    q = queries(T, hq, d, 3)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def both(start):
+        start = torch.tensor(start, dtype=torch.int32, device="cuda")
+        return (*g.kv4_read(pages, tab, n, KS, VS, T, q_start=start, dev_status=st),
+                *g.kv4_prefill(q, pages, tab, n, start, KS, VS, return_lse=True, dev_status=st))
+
+    want = both([0, 5, 9])
+    assert st.item() == 0
+    for _ in range(20):
+        got = both(bad)
+        assert all(torch.equal(x[:5], y[:5]) for x, y in zip(got, want))
+    assert st.item() == 6
