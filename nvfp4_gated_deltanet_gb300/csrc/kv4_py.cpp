@@ -85,12 +85,6 @@ struct Named {
   const char *name;
   PyObject *o;
 };
-struct OnDevice {
-  c10::cuda::OptionalCUDAGuard guard;
-  explicit OnDevice(c10::Device d) {
-    if (c10::cuda::current_device() != d.index()) guard.set_device(d);
-  }
-};
 c10::Device device_of(std::initializer_list<Named> tensors, PyObject *stream) {
   const Named &first = *tensors.begin();
   const c10::Device dev = tensor(first.o, first.name).device();
@@ -115,6 +109,12 @@ c10::Device device_of(std::initializer_list<Named> tensors, PyObject *stream) {
   }
   return dev;
 }
+struct OnDevice {
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit OnDevice(c10::Device d) {
+    if (c10::cuda::current_device() != d.index()) guard.set_device(d);
+  }
+};
 // The stream on the current device
 cudaStream_t stream_of(PyObject *o) {
   if (!given(o)) return c10::cuda::getCurrentCUDAStream().stream();
@@ -209,7 +209,7 @@ PyObject *pair(const at::Tensor &a, const at::Tensor &b) {
 // k v pages table kv_len k_scale v_scale q_start dev_status stream
 PyObject *append(PyObject *const *a) {
   const OnDevice on(device_of({{"pages", a[2]}, {"k", a[0]}, {"v", a[1]}, {"block_table", a[3]},
-                                           {"kv_len", a[4]}, {"q_start", a[7]}, {"dev_status", a[8]}}, a[9]));
+                               {"kv_len", a[4]}, {"q_start", a[7]}, {"dev_status", a[8]}}, a[9]));
   const kv4_cache c = cache(a[2], a[5], a[6]);
   const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
   const int64_t ks = rows_stride(k, "k", c.n_kv_heads, c.head_dim), vs = rows_stride(v, "v", c.n_kv_heads, c.head_dim);
@@ -221,7 +221,7 @@ PyObject *append(PyObject *const *a) {
 // pages table kv_len k_scale v_scale rows q_start k v dev_status stream
 PyObject *read(PyObject *const *a) {
   const OnDevice on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"kv_len", a[2]}, {"q_start", a[6]},
-                                           {"k", a[7]}, {"v", a[8]}, {"dev_status", a[9]}}, a[10]));
+                               {"k", a[7]}, {"v", a[8]}, {"dev_status", a[9]}}, a[10]));
   const kv4_cache c = cache(a[0], a[3], a[4]);
   const int64_t rows = whole(a[5]);
   if (rows < 0) throw Bad("rows: expected a number of rows");
@@ -238,8 +238,8 @@ PyObject *read(PyObject *const *a) {
 PyObject *decode(PyObject *const *a) {
   const bool want = truth(a[9]);
   const OnDevice on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
-                                           {"out", a[7]}, {"lse", a[8]}, {"workspace", a[10]},
-                                           {"dev_status", a[11]}}, a[12]));
+                               {"out", a[7]}, {"lse", a[8]}, {"workspace", a[10]},
+                               {"dev_status", a[11]}}, a[12]));
   const kv4_cache c = cache(a[1], a[4], a[5]);
   const at::Tensor &q = tensor(a[0], "q");
   if (q.dim() != 3 && q.dim() != 4) throw Bad("q: expected [B][Hq][d] or [B][r][Hq][d]");
@@ -268,8 +268,8 @@ PyObject *decode(PyObject *const *a) {
 PyObject *prefill(PyObject *const *a) {
   const bool want = truth(a[11]);
   const OnDevice on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
-                                           {"q_start", a[4]}, {"out", a[9]}, {"lse", a[10]}, {"workspace", a[12]},
-                                           {"dev_status", a[13]}}, a[14]));
+                               {"q_start", a[4]}, {"out", a[9]}, {"lse", a[10]}, {"workspace", a[12]},
+                               {"dev_status", a[13]}}, a[14]));
   const kv4_cache c = cache(a[1], a[5], a[6]);
   const at::Tensor &q = tensor(a[0], "q");
   const int64_t qs = rows_stride(q, "q", -1, c.head_dim);
@@ -320,8 +320,8 @@ PyObject *copy_pages(PyObject *const *a) {
 // pages table tables_out page_map n_live workspace dev_status stream
 PyObject *compact(PyObject *const *a) {
   const OnDevice on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"tables_out", a[2]},
-                                           {"page_map", a[3]}, {"n_live", a[4]}, {"workspace", a[5]},
-                                           {"dev_status", a[6]}}, a[7]));
+                               {"page_map", a[3]}, {"n_live", a[4]}, {"workspace", a[5]},
+                               {"dev_status", a[6]}}, a[7]));
   const Layers l = layers_of(a[0]);
   const int32_t *table = i32(a[1], "block_table", 2);
   const at::Tensor &t = THPVariable_Unpack(a[1]), &p = THPVariable_Unpack(a[0]);
