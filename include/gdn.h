@@ -394,6 +394,83 @@ gdn_status kv4_prefill(const kv4_cache *c, const kv4_batch *b, int64_t total_kv,
                        size_t workspace_bytes, int32_t *dev_status, void *stream);
 size_t kv4_prefill_workspace(const kv4_cache *c, const kv4_batch *b, int64_t total_kv, int n_q_heads);
 
+/* Groups of sequences that share a prefix: sequences [group_start[g],
+ * group_start[g + 1]) of the batch hold the same first shared_len[g] tokens
+ * (prompts before their samples, forks), which are read through the pages of
+ * the group's first sequence with tokens. Sequences in no group share nothing. */
+typedef struct {
+  const int32_t *group_start;  /* device [groups + 1] */
+  const int32_t *shared_len;   /* device [groups] */
+  int groups;                  /* 0: none */
+  int max_shared;              /* an upper bound: more of shared_len is not shared */
+} kv4_shared;
+
+/* kv4_decode with the tokens that a group shares read once for all of its rows.
+ * The result is kv4_decode's, but for the order of the sums: a group shares, of
+ * its shared_len, whole pages that every row of every member with tokens sees;
+ * what is left of it each sequence reads for itself. Sums, maxima and the parts
+ * that are joined are FP32; roundings as kv4_decode's. group_start that does not
+ * ascend within [0, B], or a shared_len below 0, sets GDN_E_RANGE and shares
+ * nothing (there). workspace: kv4_decode_shared_workspace bytes.
+ * Errors: as kv4_decode; GDN_E_SHAPE for groups or max_shared below 0. */
+gdn_status kv4_decode_shared(const kv4_cache *c, const kv4_batch *b, const kv4_shared *s, const uint16_t *q,
+                             int64_t q_stride, int n_q_heads, float sm_scale, uint16_t *out, float *lse,
+                             void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+size_t kv4_decode_shared_workspace(const kv4_cache *c, const kv4_batch *b, const kv4_shared *s, int n_q_heads);
+
+/* Scores: the attention weights that each cached token got, summed over calls:
+ * FP32 rows [n_slots][n_kv_heads][tokens], sequence b's in slot slots[b]. */
+typedef struct {
+  const float *in;         /* device */
+  float *out;              /* device: `in` itself, or memory of the same size that does not overlap it */
+  const int32_t *slots;    /* device [B], -1: the sequence is left out; NULL: slot b */
+  int n_slots;
+  int tokens;              /* that a row holds */
+} kv4_scores;
+
+/* Add what the batch's rows gave to each cached token:
+ *   out_j = (j < scored ? in_j : 0) + sum_i exp(sm_scale * q_i . k_j - lse_i)
+ * for the tokens j < kv_len of every sequence and KV head, i running over the
+ * sequence's rows (as in kv4_prefill with q_start, kv4_decode without) that see
+ * token j and the query heads that read the KV head. lse: FP32 [T][n_q_heads],
+ * contiguous, as the attention call returned it; a row whose lse is -infinity
+ * adds nothing. scored (device [B], may be NULL: all): how many of a sequence's
+ * tokens have a score; the others' begin at 0, whatever `in` holds there. Rows
+ * of slots that the batch does not name, and a row's places from kv_len on, are
+ * left alone. A sequence whose slot is out of range or named twice, or whose
+ * tokens a row does not hold, sets GDN_E_RANGE and is left out. q enters in FP16
+ * scaled by a power of two per row, as in kv4_decode, K exactly; products,
+ * exponentials and sums are FP32, in an order that depends on the sizes and the
+ * table's width alone. workspace: kv4_score_workspace bytes (0: may be NULL).
+ * Errors: as kv4_append; GDN_E_SHAPE for heads as kv4_decode, for `out` that
+ * overlaps `in` in part, for a workspace that is too small. v_scale is not used. */
+gdn_status kv4_score(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int n_q_heads,
+                     float sm_scale, const float *lse, const kv4_scores *s, const int32_t *scored, void *workspace,
+                     size_t workspace_bytes, int32_t *dev_status, void *stream);
+size_t kv4_score_workspace(const kv4_cache *c, const kv4_batch *b, int n_q_heads);
+
+/* Evict by score: of the n = kv_len tokens of every sequence and KV head keep
+ * k = min(keep, n): the newest min(recent, k), and of the others the k -
+ * min(recent, k) of the highest scores (of equal ones the older; NaN counts as
+ * the lowest). They move, in order, to the pages that new_table names -- place i
+ * gets token kept[i] -- and their scores with them: out_i = in_kept[i], zeros
+ * from k to n. All n_layers layers (pages layer_stride bytes apart, scores
+ * score_stride floats apart) choose for themselves. The rest of the last group
+ * of 16 places gets zeros; the old pages are left as they are.
+ *   keep: device [B]; new_table: device [B][new_pages], none of whose pages may
+ *   be among the batch's own; kept: device [n_layers][B][n_kv_heads][max_keep],
+ *   -1 past a sequence's k; new_len: device [B], k.
+ * A sequence with a bad kv_len, keep (below 0, or a k beyond max_keep or the
+ * new pages) or slot (out of range, named twice) sets GDN_E_RANGE and is left
+ * out, as is one whose slot is -1: it keeps its pages and scores, kept and
+ * new_len are -1. A bad page id sets GDN_E_RANGE: what its tokens become is
+ * unspecified. Of b only kv_len, block_table, B and max_pages are used.
+ * Errors: GDN_E_NULL, GDN_E_SHAPE (sizes below 0, strides, `out` that overlaps
+ * `in` in part), GDN_E_ALIGN, GDN_E_OVERFLOW, GDN_E_CUDA. */
+gdn_status kv4_evict(const kv4_cache *c, int n_layers, int64_t layer_stride, const kv4_batch *b, const int32_t *keep,
+                     int recent, const kv4_scores *s, int64_t score_stride, const int32_t *new_table, int new_pages,
+                     int32_t *kept, int max_keep, int32_t *new_len, int32_t *dev_status, void *stream);
+
 /* Copy pages src[i] -> dst[i] (device int32 [n]) in each of n_layers caches
  * that lie layer_stride bytes apart from `pages`. page_bytes: a multiple of 16.
  * No dst may repeat or be among the src. An id outside [0, num_pages) sets

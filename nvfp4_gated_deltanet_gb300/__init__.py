@@ -47,7 +47,16 @@ class Kv4BatchStruct(ctypes.Structure):
                 ("zero_padding", _i)]
 
 
+class Kv4SharedStruct(ctypes.Structure):
+    _fields_ = [("group_start", _vp), ("shared_len", _vp), ("groups", _i), ("max_shared", _i)]
+
+
+class Kv4ScoresStruct(ctypes.Structure):
+    _fields_ = [("in_", _vp), ("out", _vp), ("slots", _vp), ("n_slots", _i), ("tokens", _i)]
+
+
 _kvc, _kvb = ctypes.POINTER(Kv4CacheStruct), ctypes.POINTER(Kv4BatchStruct)
+_kvg, _kvs = ctypes.POINTER(Kv4SharedStruct), ctypes.POINTER(Kv4ScoresStruct)
 _l, _sz = ctypes.c_int64, ctypes.c_size_t
 
 SIGNATURES = {
@@ -75,6 +84,11 @@ SIGNATURES = {
     "kv4_decode_workspace": (_sz, [_kvc, _kvb, _i]),
     "kv4_prefill": (_i, [_kvc, _kvb, _l, _vp, _l, _i, _f, _vp, _vp, _vp, _sz, _vp, _vp]),
     "kv4_prefill_workspace": (_sz, [_kvc, _kvb, _l, _i]),
+    "kv4_decode_shared": (_i, [_kvc, _kvb, _kvg, _vp, _l, _i, _f, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "kv4_decode_shared_workspace": (_sz, [_kvc, _kvb, _kvg, _i]),
+    "kv4_score": (_i, [_kvc, _kvb, _vp, _l, _i, _f, _vp, _kvs, _vp, _vp, _sz, _vp, _vp]),
+    "kv4_score_workspace": (_sz, [_kvc, _kvb, _i]),
+    "kv4_evict": (_i, [_kvc, _i, _l, _kvb, _vp, _i, _kvs, _l, _vp, _i, _vp, _i, _vp, _vp, _vp]),
     "kv4_copy_pages": (_i, [_vp, _i, _l, _i, _l, _vp, _vp, _i, _vp, _vp]),
     "kv4_compact": (_i, [_vp, _i, _l, _i, _l, _vp, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "kv4_compact_workspace": (_sz, [_i]),

@@ -177,11 +177,59 @@ struct Kv4AttnArgs {
   uint16_t *out;
   float *lse;  // or null
 };
-cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream);
+// raw, raw_ml: where FP32 sums before the division go instead of out and lse: sum_j 2^(z_j - m) v_j / v_scale
+// [T][Hq][D] and (m, sum_j 2^(z_j - m)) [T][Hq][2], z in bits.
+cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream,
+                              float *raw = nullptr, float *raw_ml = nullptr);
 size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms);  // its workspace
 cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, long long total_kv, void *workspace, int num_sms,
                                cudaStream_t stream);
 size_t kv4_prefill_bytes(const Kv4AttnArgs &a, long long total_kv);  // its workspace; 0: too large
+
+// Rows of accumulated attention weights, kv4_scores (include/gdn.h).
+struct Kv4ScoreRows {
+  const float *in;
+  float *out;
+  const int32_t *slots;  // or null: sequence b's row is b
+  int n_slots, tokens;
+};
+
+struct Kv4ScoreArgs {
+  Kv4Args c;
+  Kv4ScoreRows s;
+  const uint16_t *q;
+  long long q_stride;
+  int Hq;
+  float sm_scale;
+  const float *lse;
+  const int32_t *scored;  // or null
+};
+cudaError_t launch_kv4_score(const Kv4ScoreArgs &a, void *workspace, int num_sms, cudaStream_t stream);
+size_t kv4_score_bytes(const Kv4ScoreArgs &a, int num_sms);  // its workspace
+
+struct Kv4EvictArgs {
+  Kv4Args c;                // pages: of the first layer
+  Kv4ScoreRows s;           // of the first layer
+  int layers;
+  long long layer_stride;   // bytes
+  long long score_layer;    // elements
+  const int32_t *keep;
+  int recent;
+  const int32_t *new_table;
+  int new_cols;
+  int32_t *kept, *new_len;
+  int max_keep;
+};
+cudaError_t launch_kv4_evict(const Kv4EvictArgs &a, cudaStream_t stream);
+
+struct Kv4SharedArgs {
+  Kv4AttnArgs a;
+  const int32_t *group_start, *shared_len;
+  int groups;
+  int max_shared;  // tokens
+};
+cudaError_t launch_kv4_decode_shared(const Kv4SharedArgs &a, void *workspace, int num_sms, cudaStream_t stream);
+size_t kv4_decode_shared_bytes(const Kv4SharedArgs &a, int num_sms);  // its workspace
 
 struct Kv4PageArgs {
   uint8_t *pages;

@@ -1,6 +1,7 @@
 // The C ABI of the 4-bit KV cache (include/gdn.h): argument checks, then one
 // launcher per call.
 #include <cmath>
+#include <initializer_list>
 
 #include "kv4.cuh"
 
@@ -83,6 +84,54 @@ gdn_status check_pages(const Kv4PageArgs &a) {
   return GDN_OK;
 }
 
+bool words(std::initializer_list<const void *> ps) {
+  uintptr_t all = 0;
+  for (const void *p : ps) all |= reinterpret_cast<uintptr_t>(p);
+  return (all & 3u) == 0;
+}
+
+// The sequences of a batch whose rows do not matter (or may be none).
+gdn_status check_seqs(const kv4_cache *c, const kv4_batch *b, Kv4Args &a, int32_t *status) {
+  if (!b) return GDN_E_NULL;
+  kv4_batch one = *b;
+  one.T = b->B > 0 ? b->B : 0;
+  one.q_start = nullptr;
+  return check(c, &one, a, status);
+}
+
+// The score rows of n_layers layers, `stride` floats apart.
+gdn_status check_scores(const kv4_cache *c, const kv4_scores *s, int n_layers, int64_t stride, Kv4ScoreRows &r) {
+  if (!s) return GDN_E_NULL;
+  if (s->n_slots < 0 || s->tokens < 0) return GDN_E_SHAPE;
+  const long long row = (long long)c->n_kv_heads * s->tokens;  // below 2^42
+  if (s->n_slots > 0 && row > (1LL << 44) / s->n_slots) return GDN_E_OVERFLOW;
+  const long long layer = row * s->n_slots;
+  if (n_layers > 1 && stride < layer) return GDN_E_SHAPE;
+  if (layer > 0) {
+    if (!s->in || !s->out) return GDN_E_NULL;
+    if (!words({s->in, s->out, s->slots})) return GDN_E_ALIGN;
+    if (n_layers > 1 && stride > (1LL << 58) / n_layers) return GDN_E_OVERFLOW;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(s->in), y = reinterpret_cast<uintptr_t>(s->out);
+    const uintptr_t size = 4 * (uintptr_t)((n_layers - 1) * stride + layer);
+    if (x != y && (x < y ? y - x : x - y) < size) return GDN_E_SHAPE;
+  }
+  r = Kv4ScoreRows{s->in, s->out, s->slots, s->n_slots, s->tokens};
+  return GDN_OK;
+}
+
+gdn_status check_shared(const kv4_shared *s, Kv4SharedArgs &a) {
+  if (!s) return GDN_E_NULL;
+  if (s->groups < 0 || s->max_shared < 0) return GDN_E_SHAPE;
+  if (s->groups > 0 && (!s->group_start || !s->shared_len)) return GDN_E_NULL;
+  if (s->groups > 0 && !words({s->group_start, s->shared_len})) return GDN_E_ALIGN;
+  if ((long long)a.a.c.B + s->groups > 0x7fffffffLL) return GDN_E_OVERFLOW;
+  a.group_start = s->group_start;
+  a.shared_len = s->shared_len;
+  a.groups = s->groups;
+  a.max_shared = s->max_shared;
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -158,6 +207,108 @@ gdn_status kv4_prefill(const kv4_cache *c, const kv4_batch *b, int64_t total_kv,
   const int sms = num_sms();
   if (sms < 1) return GDN_E_CUDA;
   return cuda_status(launch_kv4_prefill(a, total_kv, workspace, sms, static_cast<cudaStream_t>(stream)));
+}
+
+// 0 for arguments that kv4_decode_shared refuses.
+size_t kv4_decode_shared_workspace(const kv4_cache *c, const kv4_batch *b, const kv4_shared *s, int n_q_heads) {
+  Kv4SharedArgs a{};
+  if (check(c, b, a.a.c, nullptr) != GDN_OK || b->T == 0 || b->q_start || !heads_fit(c, n_q_heads)) return 0;
+  if (check_shared(s, a) != GDN_OK) return 0;
+  a.a.Hq = n_q_heads;
+  return kv4_decode_shared_bytes(a, kMaxSms);
+}
+
+gdn_status kv4_decode_shared(const kv4_cache *c, const kv4_batch *b, const kv4_shared *s, const uint16_t *q,
+                             int64_t q_stride, int n_q_heads, float sm_scale, uint16_t *out, float *lse,
+                             void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
+  Kv4SharedArgs a{};
+  gdn_status st = check_attn(c, b, q, q_stride, n_q_heads, sm_scale, out, lse, dev_status, a.a);
+  if (st != GDN_OK) return st;
+  if (b->q_start) return GDN_E_SHAPE;
+  st = check_shared(s, a);
+  if (st != GDN_OK || b->T == 0) return st;
+  const size_t need = kv4_decode_shared_bytes(a, kMaxSms);
+  if (!workspace) return GDN_E_NULL;
+  if (workspace_bytes < need) return GDN_E_SHAPE;
+  if (!aligned16(workspace)) return GDN_E_ALIGN;
+  const int sms = num_sms();
+  if (sms < 1) return GDN_E_CUDA;
+  return cuda_status(
+      launch_kv4_decode_shared(a, workspace, sms < kMaxSms ? sms : kMaxSms, static_cast<cudaStream_t>(stream)));
+}
+
+// 0 where none is needed, and for arguments that kv4_score refuses.
+size_t kv4_score_workspace(const kv4_cache *c, const kv4_batch *b, int n_q_heads) {
+  Kv4ScoreArgs a{};
+  if (check(c, b, a.c, nullptr) != GDN_OK || b->T == 0 || !heads_fit(c, n_q_heads)) return 0;
+  a.Hq = n_q_heads;
+  return kv4_score_bytes(a, kMaxSms);
+}
+
+gdn_status kv4_score(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int n_q_heads,
+                     float sm_scale, const float *lse, const kv4_scores *s, const int32_t *scored, void *workspace,
+                     size_t workspace_bytes, int32_t *dev_status, void *stream) {
+  Kv4ScoreArgs a{};
+  gdn_status st = check_seqs(c, b, a.c, dev_status);
+  if (st == GDN_OK) st = check(c, b, a.c, dev_status);
+  if (st != GDN_OK) return st;
+  if (!heads_fit(c, n_q_heads)) return GDN_E_SHAPE;
+  if (!std::isfinite(sm_scale)) return GDN_E_NONFINITE;
+  if (!(sm_scale > 0.0f)) return GDN_E_BAD_SCALE;
+  st = check_scores(c, s, 1, 0, a.s);
+  if (st != GDN_OK) return st;
+  if (b->T > 0) {
+    if (!q || !lse) return GDN_E_NULL;
+    if (!aligned16(q) || !words({lse})) return GDN_E_ALIGN;
+    if (q_stride % 8 || q_stride < (int64_t)n_q_heads * c->head_dim) return GDN_E_SHAPE;
+    if ((long long)b->T * n_q_heads > 0x7fffffffLL) return GDN_E_OVERFLOW;
+  }
+  if (!words({scored})) return GDN_E_ALIGN;
+  if (b->B == 0 || b->max_pages == 0 || s->n_slots == 0) return GDN_OK;
+  // a CTA per so many tokens of a sequence and head
+  if (((long long)b->max_pages * c->page_tokens / 128 + 1) * b->B > 0x7fffffffLL / c->n_kv_heads) return GDN_E_OVERFLOW;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.Hq = n_q_heads;
+  a.sm_scale = sm_scale;
+  a.lse = lse;
+  a.scored = scored;
+  const size_t need = b->T > 0 ? kv4_score_bytes(a, kMaxSms) : 0;
+  if (need && !workspace) return GDN_E_NULL;
+  if (workspace_bytes < need) return GDN_E_SHAPE;
+  if (!aligned16(workspace)) return GDN_E_ALIGN;
+  const int sms = num_sms();
+  if (sms < 1) return GDN_E_CUDA;
+  return cuda_status(launch_kv4_score(a, workspace, sms < kMaxSms ? sms : kMaxSms, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status kv4_evict(const kv4_cache *c, int n_layers, int64_t layer_stride, const kv4_batch *b, const int32_t *keep,
+                     int recent, const kv4_scores *s, int64_t score_stride, const int32_t *new_table, int new_pages,
+                     int32_t *kept, int max_keep, int32_t *new_len, int32_t *dev_status, void *stream) {
+  Kv4EvictArgs a{};
+  gdn_status st = check_seqs(c, b, a.c, dev_status);
+  if (st != GDN_OK) return st;
+  if (n_layers < 1 || recent < 0 || new_pages < 0 || max_keep < 0) return GDN_E_SHAPE;
+  const int64_t page_bytes = (int64_t)c->n_kv_heads * (c->page_tokens / 16) * 18 * c->head_dim;
+  if (page_bytes > (1LL << 40) / c->num_pages) return GDN_E_OVERFLOW;
+  if (n_layers > 1 && (layer_stride % 16 || layer_stride < c->num_pages * page_bytes)) return GDN_E_SHAPE;
+  st = check_scores(c, s, n_layers, score_stride, a.s);
+  if (st != GDN_OK || b->B == 0) return st;
+  if (!keep || !new_len || (max_keep > 0 && !kept) || (new_pages > 0 && !new_table)) return GDN_E_NULL;
+  if (!words({keep, new_len, kept, new_table})) return GDN_E_ALIGN;
+  const long long rows = (long long)b->B * c->n_kv_heads;
+  if (rows > 0x7fffffffLL / n_layers || rows * n_layers > 0x7fffffffLL / (max_keep / 128 + 1)) return GDN_E_OVERFLOW;
+  a.layers = n_layers;
+  a.layer_stride = layer_stride;
+  a.score_layer = score_stride;
+  a.keep = keep;
+  a.recent = recent;
+  a.new_table = new_table;
+  a.new_cols = new_pages;
+  a.kept = kept;
+  a.new_len = new_len;
+  a.max_keep = max_keep;
+  return cuda_status(launch_kv4_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status kv4_copy_pages(uint8_t *pages, int n_layers, int64_t layer_stride, int num_pages, int64_t page_bytes,

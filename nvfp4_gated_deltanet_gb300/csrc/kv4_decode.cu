@@ -91,6 +91,7 @@ struct DecodeArgs {
   int extra;         // cost of an item beside its tiles, in tiles; kWhole: runs hold whole items, nothing to join
   int items;         // (sequence, KV head, row group)
   float *part;       // pieces [2 runs][rows][D], their (m, l) [2 runs][rows][2], the items' ends [items][2]
+  float *raw, *raw_ml;  // not null: instead of out and lse, O [T][Hq][D] and its (m, l) [T][Hq][2], FP32
 };
 // What the plan goes by, all measured on GB300 (d = 128, us):
 // An item's query rows, its meeting and its output take a team about as long as
@@ -674,6 +675,11 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
       }
       if (done) {
         const long long out = ((long long)cur.b * p.r + rg.token(row)) * p.a.Hq + rg.h * p.G + rg.head(row);
+        if (p.raw) {
+          *reinterpret_cast<float4 *>(p.raw + out * D + d4) = o;
+          if (d4 == 0) *reinterpret_cast<float2 *>(p.raw_ml + out * 2) = make_float2(top - kShift, sum);
+          continue;
+        }
         const float inv = sum == 0.0f ? 0.0f : c.vs / sum;
         *reinterpret_cast<uint2 *>(p.a.out + out * D + d4) =
             make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
@@ -778,6 +784,13 @@ __global__ void __launch_bounds__(256, 3) kv4_join_kernel(DecodeArgs p, int runs
     auto piece = [&](int j) { return (size_t)(j > 0 ? 2 * (first + j) : e.x) * most; };
     auto put = [&](int row, int ch, float m, float l, auto &v) {  // channels ch ... of a row
       const long long out = ((long long)b * p.r + rg.token(row)) * p.a.Hq + rg.h * p.G + rg.head(row);
+      if (p.raw) {
+#pragma unroll
+        for (int x = 0; x < (int)(sizeof(v) / sizeof(float)); x += 2)
+          *reinterpret_cast<float2 *>(p.raw + out * D + ch + x) = make_float2(v[x], v[x + 1]);
+        if (ch == 0) *reinterpret_cast<float2 *>(p.raw_ml + out * 2) = make_float2(m - kShift, l);
+        return;
+      }
       const float inv = l == 0.0f ? 0.0f : c.vs / l;
 #pragma unroll
       for (int x = 0; x < (int)(sizeof(v) / sizeof(float)); x += 2)
@@ -900,11 +913,12 @@ cudaError_t launch_decode(const DecodeArgs &p, const DecodePlan &d, cudaStream_t
 
 size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms) { return a.c.T ? decode_plan(a, num_sms).bytes : 0; }
 
-cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream) {
+cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream, float *raw,
+                              float *raw_ml) {
   const DecodePlan d = decode_plan(a, num_sms);
   const int G = a.Hq / a.c.Hkv;
   const DecodeArgs p{a, a.c.T / a.c.B, G, d.RG, (uint32_t)((65536 + G - 1) / G), d.extra, (int)(a.c.B * a.c.Hkv * d.RG),
-                     static_cast<float *>(workspace)};
+                     static_cast<float *>(workspace), raw, raw_ml};
   if (a.c.D == 128)
     return d.NQ == 1 ? launch_decode<128, 1>(p, d, stream) : d.NQ == 2 ? launch_decode<128, 2>(p, d, stream)
                                                                        : launch_decode<128, 4>(p, d, stream);

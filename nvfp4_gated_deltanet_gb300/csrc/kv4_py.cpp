@@ -234,6 +234,22 @@ PyObject *read(PyObject *const *a) {
   check(kv4_read(&c, &b, u16_out(k), u16_out(v), status_word(a[9]), stream_of(a[10])), "kv4_read");
   return pair(k, v);
 }
+// Query rows [B][Hq][d] or [B][r][Hq][d] whose heads lie together, evenly spaced
+struct SeqRows {
+  int64_t B, r, Hq, stride;
+};
+SeqRows seq_rows(const at::Tensor &q, int d) {
+  if (q.dim() != 3 && q.dim() != 4) throw Bad("q: expected [B][Hq][d] or [B][r][Hq][d]");
+  const bool four = q.dim() == 4;
+  const int64_t B = q.size(0), r = four ? q.size(1) : 1, Hq = q.size(four ? 2 : 1);
+  if (!is_bf16(q) || !q.is_cuda() || q.size(-1) != d)
+    throw Bad("q: expected BF16 CUDA rows [B][heads][" + std::to_string(d) + "]");
+  if (q.numel() > 0 && (q.stride(-1) != 1 || (Hq > 1 && q.stride(-2) != d)))
+    throw Bad("q: a row's heads must lie together in memory");
+  const int64_t row = r > 1 ? q.stride(1) : B > 1 ? q.stride(0) : Hq * d;
+  if (r > 1 && B > 1 && q.stride(0) != r * row) throw Bad("q: the rows of all sequences must be evenly spaced");
+  return {B, r, Hq, row};
+}
 // q pages table kv_len k_scale v_scale sm_scale out lse return_lse workspace dev_status stream
 PyObject *decode(PyObject *const *a) {
   const bool want = truth(a[9]);
@@ -242,15 +258,7 @@ PyObject *decode(PyObject *const *a) {
                                {"dev_status", a[11]}}, a[12]));
   const kv4_cache c = cache(a[1], a[4], a[5]);
   const at::Tensor &q = tensor(a[0], "q");
-  if (q.dim() != 3 && q.dim() != 4) throw Bad("q: expected [B][Hq][d] or [B][r][Hq][d]");
-  const bool four = q.dim() == 4;
-  const int64_t B = q.size(0), r = four ? q.size(1) : 1, Hq = q.size(four ? 2 : 1);
-  if (!is_bf16(q) || !q.is_cuda() || q.size(-1) != c.head_dim)
-    throw Bad("q: expected BF16 CUDA rows [B][heads][" + std::to_string(c.head_dim) + "]");
-  if (q.numel() > 0 && (q.stride(-1) != 1 || (Hq > 1 && q.stride(-2) != c.head_dim)))
-    throw Bad("q: a row's heads must lie together in memory");
-  const int64_t row = r > 1 ? q.stride(1) : B > 1 ? q.stride(0) : Hq * c.head_dim;
-  if (r > 1 && B > 1 && q.stride(0) != r * row) throw Bad("q: the rows of all sequences must be evenly spaced");
+  const auto [B, r, Hq, row] = seq_rows(q, c.head_dim);
   const kv4_batch b = batch(a[2], a[3], Py_None, B * r);
   if (b.B != B) throw Bad("q and block_table disagree on the number of sequences");
   const at::Tensor out = output(a[7], "out", q.sizes(), at::kBFloat16, q, a[12]);
@@ -287,6 +295,101 @@ PyObject *prefill(PyObject *const *a) {
                     n, status_word(a[13]), s),
         "kv4_prefill");
   return want ? pair(out, lse) : THPVariable_Wrap(out);
+}
+
+// q pages table kv_len group_start shared_len k_scale v_scale max_shared sm_scale out lse return_lse workspace dev_status stream
+PyObject *decode_shared(PyObject *const *a) {
+  const bool want = truth(a[12]);
+  const OnDevice on(device_of({{"pages", a[1]}, {"q", a[0]}, {"block_table", a[2]}, {"kv_len", a[3]},
+                               {"group_start", a[4]}, {"shared_len", a[5]}, {"out", a[10]}, {"lse", a[11]},
+                               {"workspace", a[13]}, {"dev_status", a[14]}}, a[15]));
+  const kv4_cache c = cache(a[1], a[6], a[7]);
+  const at::Tensor &q = tensor(a[0], "q");
+  const SeqRows n = seq_rows(q, c.head_dim);
+  const kv4_batch b = batch(a[2], a[3], Py_None, n.B * n.r);
+  if (b.B != n.B) throw Bad("q and block_table disagree on the number of sequences");
+  kv4_shared g{};
+  g.group_start = i32(a[4], "group_start", 1);
+  g.shared_len = i32(a[5], "shared_len", 1);
+  const int64_t groups = THPVariable_Unpack(a[5]).size(0);
+  if (THPVariable_Unpack(a[4]).size(0) != groups + 1) throw Bad("group_start: expected one entry more than shared_len has");
+  g.groups = as_int(groups, "shared_len");
+  const int64_t room = (int64_t)b.max_pages * c.page_tokens, most = given(a[8]) ? whole(a[8]) : room;
+  if (most < 0) throw Bad("max_shared: expected a number of tokens");
+  g.max_shared = as_int(most, "max_shared");
+  const at::Tensor out = output(a[10], "out", q.sizes(), at::kBFloat16, q, a[15]);
+  const at::Tensor lse = want || given(a[11]) ? output(a[11], "lse", q.sizes().slice(0, q.dim() - 1), at::kFloat, q, a[15])
+                                               : at::Tensor();
+  const cudaStream_t s = stream_of(a[15]);
+  size_t bytes;
+  const at::Tensor ws = workspace(a[13], kv4_decode_shared_workspace(&c, &b, &g, as_int(n.Hq, "q")), q, a[15], s, bytes);
+  check(kv4_decode_shared(&c, &b, &g, u16(q), n.stride, as_int(n.Hq, "q"), scale_of(a[9], c), u16_out(out),
+                          static_cast<float *>(ptr(lse)), ptr(ws), bytes, status_word(a[14]), s),
+        "kv4_decode_shared");
+  return want ? pair(out, lse) : THPVariable_Wrap(out);
+}
+// Rows of scores FP32 [slots][Hkv][tokens], or [layers]... of them where `layers` is not 0
+const at::Tensor &score_rows(PyObject *o, const char *name, int layers, int heads) {
+  const at::Tensor &t = tensor(o, name);
+  const int k = layers ? 1 : 0;
+  if (t.scalar_type() != at::kFloat || t.dim() != 3 + k || !t.is_cuda() || !t.is_contiguous() || t.size(1 + k) != heads ||
+      (layers && t.size(0) != layers))
+    throw Bad(std::string(name) + ": expected a contiguous FP32 CUDA tensor " + (layers ? "[layers]" : "") + "[slots][" +
+              std::to_string(heads) + "][tokens]");
+  return t;
+}
+kv4_scores scores_of(PyObject *in, PyObject *out, const char *out_name, PyObject *slots, int B, int layers, int heads) {
+  const at::Tensor &x = score_rows(in, "scores", layers, heads);
+  const at::Tensor &y = given(out) ? score_rows(out, out_name, layers, heads) : x;
+  if (y.sizes() != x.sizes()) throw Bad(std::string(out_name) + ": expected the shape of scores");
+  kv4_scores s{};
+  s.in = x.const_data_ptr<float>();
+  s.out = y.data_ptr<float>();
+  const int k = layers ? 1 : 0;
+  s.n_slots = as_int(x.size(k), "scores");
+  s.tokens = as_int(x.size(k + 2), "scores");
+  if (given(slots)) {
+    s.slots = i32(slots, "slots", 1);
+    if (THPVariable_Unpack(slots).size(0) != B) throw Bad("slots and block_table disagree on the number of sequences");
+  }
+  return s;
+}
+const int32_t *per_seq(PyObject *o, const char *name, int B) {
+  const int32_t *p = i32(o, name, 1);
+  if (THPVariable_Unpack(o).size(0) != B)
+    throw Bad(std::string(name) + " and block_table disagree on the number of sequences");
+  return p;
+}
+// q lse pages table kv_len scores k_scale q_start slots scored out sm_scale workspace dev_status stream
+PyObject *score(PyObject *const *a) {
+  const OnDevice on(device_of({{"pages", a[2]}, {"q", a[0]}, {"lse", a[1]}, {"block_table", a[3]}, {"kv_len", a[4]},
+                               {"scores", a[5]}, {"q_start", a[7]}, {"slots", a[8]}, {"scored", a[9]}, {"out", a[10]},
+                               {"workspace", a[12]}, {"dev_status", a[13]}}, a[14]));
+  kv4_cache c = cache(a[2], a[6], a[6]);
+  c.v_scale = 1.0f;
+  const at::Tensor &q = tensor(a[0], "q"), &lse = tensor(a[1], "lse");
+  SeqRows n{};
+  if (given(a[7])) {
+    n.stride = rows_stride(q, "q", -1, c.head_dim);
+    n.r = q.size(0);
+    n.Hq = q.size(1);
+    n.B = 1;
+  } else {
+    n = seq_rows(q, c.head_dim);
+  }
+  const kv4_batch b = batch(a[3], a[4], a[7], n.B * n.r);
+  if (!given(a[7]) && b.B != n.B) throw Bad("q and block_table disagree on the number of sequences");
+  if (lse.scalar_type() != at::kFloat || !lse.is_contiguous() || lse.sizes() != q.sizes().slice(0, q.dim() - 1))
+    throw Bad("lse: expected contiguous FP32, one for each row and head of q");
+  const kv4_scores s = scores_of(a[5], a[10], "out", a[8], b.B, 0, c.n_kv_heads);
+  const int32_t *scored = given(a[9]) ? per_seq(a[9], "scored", b.B) : nullptr;
+  const cudaStream_t st = stream_of(a[14]);
+  size_t bytes;
+  const at::Tensor ws = workspace(a[12], kv4_score_workspace(&c, &b, as_int(n.Hq, "q")), q, a[14], st, bytes);
+  check(kv4_score(&c, &b, u16(q), n.stride, as_int(n.Hq, "q"), scale_of(a[11], c), lse.const_data_ptr<float>(), &s, scored,
+                  ptr(ws), bytes, status_word(a[13]), st),
+        "kv4_score");
+  Py_RETURN_NONE;
 }
 
 struct Layers {
@@ -344,6 +447,37 @@ PyObject *compact(PyObject *const *a) {
   return r;
 }
 
+// pages table kv_len keep recent scores new_table max_keep slots kept new_len scores_out dev_status stream
+PyObject *evict(PyObject *const *a) {
+  const OnDevice on(device_of({{"pages", a[0]}, {"block_table", a[1]}, {"kv_len", a[2]}, {"keep", a[3]}, {"scores", a[5]},
+                               {"new_table", a[6]}, {"slots", a[8]}, {"kept", a[9]}, {"new_len", a[10]},
+                               {"scores_out", a[11]}, {"dev_status", a[12]}}, a[13]));
+  const Layers l = layers_of(a[0]);
+  const at::Tensor &p = THPVariable_Unpack(a[0]);
+  const int k = (int)p.dim() - 4;
+  if (p.size(k + 3) % 18) throw Bad("pages: the last dimension is 18 * head_dim bytes");
+  const kv4_cache c{l.p, l.num, as_int(16 * p.size(k + 2), "pages"), as_int(p.size(k + 1), "pages"),
+                    as_int(p.size(k + 3) / 18, "pages"), 1.0f, 1.0f};
+  const kv4_batch b = batch(a[1], a[2], Py_None, 0);
+  const int32_t *keep = per_seq(a[3], "keep", b.B);
+  const int64_t recent = whole(a[4]);
+  if (recent < 0) throw Bad("recent: expected a number of tokens");
+  const kv4_scores s = scores_of(a[5], a[11], "scores_out", a[8], b.B, k ? l.layers : 0, c.n_kv_heads);
+  const int32_t *table = i32(a[6], "new_table", 2);
+  const at::Tensor &nt = THPVariable_Unpack(a[6]);
+  if (nt.size(0) != b.B) throw Bad("new_table and block_table disagree on the number of sequences");
+  const int64_t room = nt.size(1) * c.page_tokens, most = given(a[7]) ? whole(a[7]) : room;
+  if (most < 0) throw Bad("max_keep: expected a number of tokens");
+  const int64_t shape[4] = {l.layers, b.B, c.n_kv_heads, as_int(most, "max_keep")}, one[1] = {b.B};
+  const at::Tensor kept = output(a[9], "kept", at::IntArrayRef(shape + 1 - k, 3 + k), at::kInt, p, a[13]),
+                   len = output(a[10], "new_len", one, at::kInt, p, a[13]);
+  check(kv4_evict(&c, l.layers, l.stride, &b, keep, as_int(recent, "recent"), &s,
+                  (int64_t)s.n_slots * c.n_kv_heads * s.tokens, table, as_int(nt.size(1), "new_table"),
+                  kept.data_ptr<int32_t>(), (int)most, len.data_ptr<int32_t>(), status_word(a[12]), stream_of(a[13])),
+        "kv4_evict");
+  return pair(kept, len);
+}
+
 // No C++ exception crosses into Python.
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -373,7 +507,8 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
 #define KV4_METHOD(f, n) \
   {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {KV4_METHOD(append, 10), KV4_METHOD(read, 11), KV4_METHOD(decode, 13), KV4_METHOD(prefill, 15),
-                         KV4_METHOD(copy_pages, 5), KV4_METHOD(compact, 8), {nullptr, nullptr, 0, nullptr}};
+                         KV4_METHOD(copy_pages, 5), KV4_METHOD(compact, 8), KV4_METHOD(decode_shared, 16), KV4_METHOD(score, 15),
+                         KV4_METHOD(evict, 14), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv4", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -26,8 +26,8 @@ import torch
 
 from . import lib
 
-__all__ = ["kv4_new_pages", "kv4_append", "kv4_read", "kv4_decode", "kv4_prefill", "kv4_copy_pages", "kv4_compact",
-           "KV4Book", "KV4Batch", "KV4Cache"]
+__all__ = ["kv4_new_pages", "kv4_append", "kv4_read", "kv4_decode", "kv4_decode_shared", "kv4_prefill", "kv4_score",
+           "kv4_evict", "kv4_copy_pages", "kv4_compact", "KV4Book", "KV4Batch", "KV4Cache"]
 
 _module = None
 
@@ -75,6 +75,16 @@ def kv4_decode(q, pages, block_table, kv_len, k_scale, v_scale, sm_scale=None, o
                             dev_status, stream)
 
 
+def kv4_decode_shared(q, pages, block_table, kv_len, group_start, shared_len, k_scale, v_scale, max_shared=None,
+                      sm_scale=None, out=None, lse=None, return_lse=False, workspace=None, dev_status=None, stream=None):
+    """kv4_decode of sequences that share a prefix: sequences [group_start[g],
+    group_start[g + 1]) hold the same first shared_len[g] tokens, of which whole
+    pages are read once for all of them. max_shared: an upper bound of shared_len
+    (default: what the tables can hold)."""
+    return _native().decode_shared(q, pages, block_table, kv_len, group_start, shared_len, k_scale, v_scale, max_shared,
+                                   sm_scale, out, lse, return_lse, workspace, dev_status, stream)
+
+
 def kv4_prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_kv=None, sm_scale=None, out=None,
                 lse=None, return_lse=False, workspace=None, dev_status=None, stream=None):
     """Causal attention of ragged prompt chunks: q [T][Hq][d], sequence b's rows
@@ -84,6 +94,32 @@ def kv4_prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_
     they are left alone."""
     return _native().prefill(q, pages, block_table, kv_len, q_start, k_scale, v_scale, total_kv, sm_scale, out, lse,
                              return_lse, workspace, dev_status, stream)
+
+
+def kv4_score(q, lse, pages, block_table, kv_len, scores, k_scale, q_start=None, slots=None, scored=None, out=None,
+              sm_scale=None, workspace=None, dev_status=None, stream=None):
+    """Add the attention weights exp(sm_scale q k - lse) that the rows q gave to
+    each cached token, summed over rows and query heads, to the sequences' rows of
+    scores FP32 [slots][Hkv][tokens] (sequence b's: slots[b], or b). q and lse as
+    kv4_decode takes and returns them, or ragged with q_start as kv4_prefill;
+    scored [B]: how many tokens of each sequence have a score, the others' begin
+    at 0 (default: all have). out: where the sums go (default: scores itself)."""
+    _native().score(q, lse, pages, block_table, kv_len, scores, k_scale, q_start, slots, scored, out, sm_scale, workspace,
+                    dev_status, stream)
+
+
+def kv4_evict(pages, block_table, kv_len, keep, recent, scores, new_table, max_keep=None, slots=None, kept=None,
+              new_len=None, scores_out=None, dev_status=None, stream=None):
+    """Keep min(keep[b], kv_len[b]) tokens of each sequence and KV head: the newest
+    `recent` and, of the others, those of the highest scores (of equal ones the
+    older). They move in order to the pages of new_table, their scores with them
+    (to scores_out: default scores itself). Returns (kept [B][Hkv][max_keep], the
+    places they had, -1 past the last; new_len [B]), int32; with pages and scores
+    of all layers, [layers][num_pages]... and [layers][slots]..., kept has a
+    leading [layers]. max_keep: an upper bound of keep (default: what the new
+    pages can hold)."""
+    return _native().evict(pages, block_table, kv_len, keep, recent, scores, new_table, max_keep, slots, kept, new_len,
+                           scores_out, dev_status, stream)
 
 
 def kv4_copy_pages(pages, src, dst, dev_status=None, stream=None):
@@ -193,6 +229,59 @@ class KV4Book:
         for p in self.seqs.pop(seq)[0]:
             self._drop(p)
 
+    def exchange(self, seqs, tokens) -> list:
+        """Give distinct sequences seqs[i] new pages for tokens[i] tokens; returns
+        what they held, for release or restore. Changes nothing when the pages run out."""
+        want = sum(-(-n // self.page_tokens) for n in tokens)
+        if want > len(self._free):
+            raise MemoryError(f"{want} pages wanted, {len(self._free)} free")
+        old = [self.seqs[s] for s in seqs]
+        for s, n in zip(seqs, tokens):
+            self.seqs[s] = [[self._take() for _ in range(-(-n // self.page_tokens))], n]
+        return old
+
+    def release(self, old):
+        """Drop the pages that sequences held before an exchange."""
+        for pages, _ in old:
+            for p in pages:
+                self._drop(p)
+
+    def restore(self, seqs, old):
+        """Take back the exchange that was the book's last change."""
+        for s, entry in zip(reversed(seqs), reversed(old)):
+            for p in reversed(self.seqs[s][0]):
+                self._drop(p)
+            self.seqs[s] = entry
+
+    def groups(self, seqs):
+        """Neighbours among seqs that share leading pages, as kv4_decode_shared takes
+        them: where each group begins (and len(seqs)), and its shared tokens. A
+        sequence joins the group before it where that saves more page reads."""
+        def common(a, b):  # sequences that share a page share all before it
+            lo, hi = 0, min(len(a), len(b))
+            while lo < hi:
+                mid = (lo + hi) // 2
+                if a[mid] == b[mid]:
+                    lo = mid + 1
+                else:
+                    hi = mid
+            return lo
+
+        start, shared = [], []
+        pages, n = [self.seqs[s][0] for s in seqs], len(seqs)
+        for i in range(n):
+            if start:
+                members = i - start[-1]
+                both = common(pages[i - 1], pages[i])
+                if members > 1:
+                    both = min(both, shared[-1])
+                if members * both > (members - 1) * shared[-1]:
+                    shared[-1] = both
+                    continue
+            start.append(i)
+            shared.append(0)
+        return start + [n], [p * self.page_tokens for p in shared]
+
     def compact(self) -> list:
         """kv4_compact's plan: every page's new id (-1: free), applied to the book."""
         live = [p for p in range(self.num_pages) if self.holders[p]]
@@ -224,38 +313,77 @@ class KV4Book:
 class KV4Batch:
     """A batch's device tables: block_table [B][cols], kv_len [B], q_start
     [B + 1] (int32), and on the host its rows T, its cached tokens total_kv and
-    the rows of each sequence, None where they differ (by default T / B)."""
+    the rows of each sequence, None where they differ (by default T / B). With
+    shared prefixes: group_start, shared_len and on the host max_shared; of a cache
+    with scores: slots and scored, and on the host the sequences and their lengths."""
 
     def __init__(self, block_table, kv_len, q_start, T, total_kv, rows="even"):
         self.block_table, self.kv_len, self.q_start, self.T, self.total_kv = block_table, kv_len, q_start, T, total_kv
         B = kv_len.shape[0]
         self.rows = rows if rows != "even" else T // B if B and T % B == 0 else None
+        self.group_start = self.shared_len = self.max_shared = None
+        self.slots = self.scored = self.seqs = self.lens = None
 
 
 class KV4Cache:
     """The pages of n_layers attention layers, their tensor scales and the book
     of their sequences. A step: batch = cache.grow(seqs, new_tokens), then per
-    layer append, and decode or prefill."""
+    layer append, and decode or prefill.
 
-    def __init__(self, num_pages, page_tokens, n_kv_heads, head_dim, k_scale, v_scale, n_layers=1, device="cuda"):
+    With score_slots and score_tokens the cache also keeps what attention weight
+    each token got, for up to score_slots sequences of up to score_tokens tokens
+    (4 bytes per token, KV head and layer): per layer score after decode or
+    prefill -- in every layer that is to be evicted from, for the same batches --
+    and evict from time to time."""
+
+    def __init__(self, num_pages, page_tokens, n_kv_heads, head_dim, k_scale, v_scale, n_layers=1, device="cuda",
+                 score_slots=0, score_tokens=0):
         self.book = KV4Book(num_pages, page_tokens)
         self.layers = kv4_new_pages(num_pages, page_tokens, n_kv_heads, head_dim, n_layers, device)
         self.scales = [(float(k_scale), float(v_scale))] * n_layers
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self.device = self.layers.device
+        self.scores = None
+        if score_slots:
+            self.scores = torch.zeros(n_layers, score_slots, n_kv_heads, score_tokens, device=device)
+        self._free_slots, self._slot, self._scored = list(range(score_slots - 1, -1, -1)), {}, {}
+
+    def _needs_scores(self):
+        if self.scores is None:
+            raise ValueError("the cache was made without score_slots")
+
+    def _slot_for(self, make, scored):
+        """The sequence that `make` adds to the book, with a slot where the cache has scores."""
+        if self.scores is None:
+            return make()
+        if not self._free_slots:
+            raise MemoryError("no score slot is free")
+        seq = make()
+        self._slot[seq], self._scored[seq] = self._free_slots.pop(), scored
+        return seq
 
     def new(self) -> int:
-        return self.book.new()
+        return self._slot_for(self.book.new, 0)
 
     def free(self, seq: int):
         self.book.free(seq)
+        if self.scores is not None:
+            self._free_slots.append(self._slot.pop(seq))
+            del self._scored[seq]
 
-    def fork(self, seq: int) -> int:
-        """A new sequence with the same tokens; no page is copied until one of the two grows."""
-        return self.book.fork(seq)
+    def fork(self, seq: int, stream=None) -> int:
+        """A new sequence with the same tokens; no page is copied until one of the
+        two grows (its scores are, on `stream`)."""
+        child = self._slot_for(lambda: self.book.fork(seq), self._scored.get(seq, 0))
+        if self.scores is not None:
+            with self._on(stream):
+                self.scores[:, self._slot[child]].copy_(self.scores[:, self._slot[seq]])
+        return child
 
     def truncate(self, seq: int, tokens: int):
         self.book.truncate(seq, tokens)
+        if self.scores is not None:
+            self._scored[seq] = min(self._scored[seq], tokens)
 
     def _dev(self, rows):
         return torch.tensor(rows, dtype=torch.int32).pin_memory().to(self.device, non_blocking=True)
@@ -265,11 +393,13 @@ class KV4Cache:
         """Tables are uploaded, used and freed in the order of one stream."""
         return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
-    def grow(self, seqs, tokens, stream=None) -> KV4Batch:
+    def grow(self, seqs, tokens, stream=None, share=False) -> KV4Batch:
         """Room for tokens[i] (or `tokens` each) new tokens of every sequence,
         the copies of shared pages made, and the batch of the new rows; all on
         `stream` (default: the current one), where the batch is to be used.
-        Where one of these fails, the book is as before."""
+        share: with the tables that decode_shared needs; sequences that share
+        pages have to be neighbours in seqs. Where one of these fails, the book
+        is as before."""
         seqs = list(seqs)
         tokens = [tokens] * len(seqs) if isinstance(tokens, int) else list(tokens)
         pairs = self.book.extend(seqs, tokens)
@@ -278,13 +408,15 @@ class KV4Cache:
                 if pairs:
                     src, dst = self._dev([p[0] for p in pairs]), self._dev([p[1] for p in pairs])
                     kv4_copy_pages(self.layers, src, dst, dev_status=self.status)
-                return self.batch(seqs, tokens)
+                return self.batch(seqs, tokens, share)
         except BaseException:
             self.book.retract(seqs, tokens, pairs)
             raise
 
-    def batch(self, seqs, tokens) -> KV4Batch:
+    def batch(self, seqs, tokens, share=False) -> KV4Batch:
         """The tables of the sequences as they are, their newest tokens[i] as the rows."""
+        if self.scores is not None and max([0] + [self.book.length(s) for s in seqs]) > self.scores.shape[3]:
+            raise MemoryError(f"a row of scores holds {self.scores.shape[3]} tokens")
         pages = [self.book.pages(s) for s in seqs]
         cols = max([1] + [len(p) for p in pages])
         lens = [self.book.length(s) for s in seqs]
@@ -292,27 +424,108 @@ class KV4Cache:
         for n in tokens:
             at.append(at[-1] + n)
         rows = tokens[0] if len(set(tokens)) == 1 else None
-        return KV4Batch(self._dev([p + [-1] * (cols - len(p)) for p in pages]), self._dev(lens), self._dev(at), at[-1],
-                        sum(lens), rows)
+        batch = KV4Batch(self._dev([p + [-1] * (cols - len(p)) for p in pages]), self._dev(lens), self._dev(at), at[-1],
+                         sum(lens), rows)
+        if share:
+            start, shared = self.book.groups(seqs)
+            batch.group_start, batch.shared_len, batch.max_shared = self._dev(start), self._dev(shared), max([0] + shared)
+        if self.scores is not None:
+            batch.slots, batch.scored = self._dev([self._slot[s] for s in seqs]), self._dev([self._scored[s] for s in seqs])
+            batch.seqs, batch.lens = list(seqs), lens
+        return batch
 
     def append(self, layer, k, v, batch, stream=None):
         kv4_append(k, v, self.layers[layer], batch.block_table, batch.kv_len, *self.scales[layer],
                    q_start=batch.q_start, dev_status=self.status, stream=stream)
 
-    def decode(self, layer, q, batch, **kw):
-        """q [B][Hq][d] or [B][r][Hq][d]: as many rows per sequence as the batch
-        has (a row's place in its sequence, and so what it sees, follows from that)."""
+    @staticmethod
+    def _same_rows(q, batch):
         if q.dim() in (3, 4):
             B, r = q.shape[0], q.shape[1] if q.dim() == 4 else 1
             if B != batch.kv_len.shape[0] or r != batch.rows:
                 has = "different numbers of rows" if batch.rows is None else f"{batch.rows} rows each"
                 raise ValueError(f"q: {B} sequences of {r} rows, but the batch has {batch.kv_len.shape[0]} with {has}")
+
+    def decode(self, layer, q, batch, **kw):
+        """q [B][Hq][d] or [B][r][Hq][d]: as many rows per sequence as the batch
+        has (a row's place in its sequence, and so what it sees, follows from that)."""
+        self._same_rows(q, batch)
         return kv4_decode(q, self.layers[layer], batch.block_table, batch.kv_len, *self.scales[layer],
                           dev_status=self.status, **kw)
+
+    def decode_shared(self, layer, q, batch, **kw):
+        """decode, the pages that neighbours of the batch share read once (a batch of grow(..., share=True))."""
+        self._same_rows(q, batch)
+        if batch.group_start is None:
+            raise ValueError("the batch was made without share=True")
+        return kv4_decode_shared(q, self.layers[layer], batch.block_table, batch.kv_len, batch.group_start,
+                                 batch.shared_len, *self.scales[layer], max_shared=batch.max_shared,
+                                 dev_status=self.status, **kw)
 
     def prefill(self, layer, q, batch, **kw):
         return kv4_prefill(q, self.layers[layer], batch.block_table, batch.kv_len, batch.q_start, *self.scales[layer],
                            total_kv=batch.total_kv, dev_status=self.status, **kw)
+
+    def score(self, layer, q, lse, batch, q_start=None, **kw):
+        """Add the weights of the batch's rows to its sequences' scores, by the
+        queries and the log-sum-exp of decode, decode_shared or prefill. q_start
+        [B + 1]: q holds only these of the newest rows (a prompt's window)."""
+        self._needs_scores()
+        if q.dim() == 4:
+            self._same_rows(q, batch)
+        elif q_start is None:
+            q_start = batch.q_start
+            if q.dim() == 3 and q.shape[0] != batch.T:
+                raise ValueError(f"q: {q.shape[0]} rows, but the batch has {batch.T}")
+        kv4_score(q, lse, self.layers[layer], batch.block_table, batch.kv_len, self.scores[layer], self.scales[layer][0],
+                  q_start=q_start, slots=batch.slots, scored=batch.scored, dev_status=self.status, **kw)
+        for s, n in zip(batch.seqs, batch.lens):
+            self._scored[s] = n
+
+    def evict(self, seqs, keep, recent=0, stream=None):
+        """Cut each of the sequences that is longer to keep[i] (or `keep`) tokens per
+        layer and KV head: the newest `recent`, and of the others those that got the
+        most attention weight. Returns the sequences that were cut and the places
+        their kept tokens had, int32 [layers][cut][Hkv][most], -1 past the last. From
+        then on a cached token's place is not its position in the text, and differs
+        between heads. The cut sequences get new pages, the old ones are free after
+        the call (MemoryError when there are not enough; the book is then as before):
+        evict a few sequences at a time where pages are short. Earlier batches are void."""
+        self._needs_scores()
+        seqs = list(seqs)
+        keep = [keep] * len(seqs) if isinstance(keep, int) else list(keep)
+        if len(keep) != len(seqs) or len(set(seqs)) != len(seqs) or recent < 0 or any(k < 0 for k in keep):
+            raise ValueError("one number of tokens, zero or more, for each of distinct sequences")
+        cut = [(s, k) for s, k in zip(seqs, keep) if self.book.length(s) > k]
+        news = [self.book.length(s) - self._scored[s] for s, _ in cut]  # the newest tokens, which have no score yet
+        for (s, k), n in zip(cut, news):
+            if n > min(recent, k):
+                raise ValueError(f"sequence {s}: {n} tokens have no score")
+        seqs, keep = [s for s, _ in cut], [k for _, k in cut]
+        most = max([0] + keep)
+        if not seqs:
+            heads = self.layers.shape[2]
+            return [], torch.empty(len(self.layers), 0, heads, 0, dtype=torch.int32, device=self.device)
+
+        def table():
+            pages = [self.book.pages(s) for s in seqs]
+            cols = max([1] + [len(p) for p in pages])
+            return self._dev([p + [-1] * (cols - len(p)) for p in pages])
+
+        with self._on(stream):
+            before, lens = table(), self._dev([self.book.length(s) for s in seqs])
+            slots, keeps = self._dev([self._slot[s] for s in seqs]), self._dev(keep)
+            old = self.book.exchange(seqs, keep)
+            try:
+                kept, _ = kv4_evict(self.layers, before, lens, keeps, recent, self.scores, table(), max_keep=most,
+                                    slots=slots, dev_status=self.status)
+            except BaseException:
+                self.book.restore(seqs, old)
+                raise
+        self.book.release(old)
+        for s, k, n in zip(seqs, keep, news):
+            self._scored[s] = k - n
+        return seqs, kept
 
     def compact(self, stream=None) -> int:
         """Move the live pages to the front of every layer; returns their number. Earlier batches are void."""
