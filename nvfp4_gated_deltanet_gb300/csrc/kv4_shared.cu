@@ -1,9 +1,17 @@
 // Decode attention for sequences that share a prefix (include/gdn.h): a group's
 // shared tokens are read once for all rows of the group, what follows them by
-// kv4_decode's kernels, and the two joined row by row:
+// kv4_decode's kernels, and the parts joined row by row:
 //
-//   out = (2^(m0 - m) O0 + 2^(m1 - m) O1) / (2^(m0 - m) l0 + 2^(m1 - m) l1),  m = max(m0, m1)
+//   out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p,  m = max_p m_p
+//
+// What bounds it: with the G r rows of many sequences on one cached token the
+// prefix is a matrix product, 4 d operations per (row, token) on the tensor cores
+// (from about 80 rows per KV head they take longer than the token's bytes), and
+// beside them one 2^x per (row, token) and the decoding of the token's 2 d values.
+#include <algorithm>
+
 #include "kv4.cuh"
+#include "tc.cuh"
 
 namespace gdn {
 
@@ -19,7 +27,9 @@ struct SharedWs {
   int32_t *seq_group;  // [B]: its group, -1: none
   int32_t *len, *lead; // [groups]: shared tokens (0: none), the sequence through whose pages they are read
   float *own, *own_ml;   // [T][Hq][D], [T][Hq][2]: kv4_decode's sums and their (maximum, weight)
-  float *pre, *pre_ml;   // [Hkv][D][rows], [Hkv][rows][2]: the shared tokens'
+  int32_t *ends;         // [Hkv][slots][2]: an item's first piece, or -1: it is whole; the run of its last piece
+  float *pre, *pre_ml;   // whole items: [Hkv][D][rows], [Hkv][rows][2]
+  float *part, *part_ml; // pieces [2 runs][D][ld], [2 runs][ld][2]
   void *decode;
 };
 
@@ -27,20 +37,37 @@ struct SharedKv4 {
   Kv4SharedArgs s;
   SharedWs w;
   int r, G, rows;  // new tokens per sequence, query heads per KV head, T G
+  int runs;        // CTAs of the prefix kernel
+  int slots, ld;   // items of a KV head, at most; rows of a piece
 };
+
+constexpr int kItemRows = 256;  // query rows of an item: two tiles of 128
+
+// Items of all KV heads together have at most this many tiles of 128 tokens.
+long long prefix_tiles(const Kv4SharedArgs &s, int slots) {
+  return (long long)s.a.c.Hkv * slots * ((std::min((long long)s.max_shared, (long long)s.a.c.cols * s.a.c.page_tokens) + 127) / 128);
+}
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-// Lays the workspace out from `base` (which may be null) and returns its size.
-size_t lay_out(const Kv4SharedArgs &s, uint8_t *base, int num_sms, SharedWs &w) {
+// The sizes of a call, its workspace laid out from `base` (which may be null), and how large that is.
+size_t lay_out(const Kv4SharedArgs &s, uint8_t *base, int num_sms, SharedKv4 &p) {
   const Kv4Args &c = s.a.c;
+  SharedWs &w = p.w;
+  p.s = s;
+  p.r = c.T / c.B;
+  p.G = s.a.Hq / c.Hkv;
+  p.rows = c.T * p.G;
+  p.slots = p.rows / kItemRows + s.groups + 1;  // item_slot
+  p.ld = std::min(kItemRows, (p.rows + 31) / 32 * 32);
+  p.runs = s.groups ? (int)std::min((long long)num_sms, prefix_tiles(s, p.slots)) : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t *p = base + at;
     at += up16(bytes);
     return p;
   };
-  const size_t rows = (size_t)c.T * (s.a.Hq / c.Hkv), all = (size_t)c.T * s.a.Hq;
+  const size_t rows = p.rows, all = (size_t)c.T * s.a.Hq;
   w.own_len = reinterpret_cast<int32_t *>(take(4 * (size_t)c.B));
   w.own_table = reinterpret_cast<int32_t *>(take(4 * (size_t)c.B * c.cols));
   w.seq_group = reinterpret_cast<int32_t *>(take(4 * (size_t)c.B));
@@ -48,8 +75,11 @@ size_t lay_out(const Kv4SharedArgs &s, uint8_t *base, int num_sms, SharedWs &w) 
   w.lead = reinterpret_cast<int32_t *>(take(4 * (size_t)s.groups));
   w.own = reinterpret_cast<float *>(take(4 * all * c.D));
   w.own_ml = reinterpret_cast<float *>(take(8 * all));
+  w.ends = reinterpret_cast<int32_t *>(take(8 * (size_t)c.Hkv * p.slots));
   w.pre = reinterpret_cast<float *>(take(4 * rows * c.Hkv * c.D));
   w.pre_ml = reinterpret_cast<float *>(take(8 * rows * c.Hkv));
+  w.part = reinterpret_cast<float *>(take(8 * (size_t)p.runs * p.ld * c.D));
+  w.part_ml = reinterpret_cast<float *>(take(16 * (size_t)p.runs * p.ld));
   w.decode = take(kv4_decode_bytes(s.a, num_sms));
   return at;
 }
@@ -125,121 +155,618 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
     p.w.own_table[(size_t)b * c.cols + i] = from + i < c.cols ? c.table[(size_t)b * c.cols + from + i] : -1;
 }
 
-// A warp per row and KV head.
+// ---------------------------------------------------------------- the shared tokens
+// kv4_prefix_kernel: an item is 256 query rows of a group and KV head -- two tiles
+// of 128, a row being (sequence, token, query head) -- against the group's shared
+// tokens. All items' tiles of 128 tokens, in order, are cut into runs of equal
+// cost, one per CTA (one per SM); a run's part of an item that it does not hold
+// whole goes to the workspace as a piece. Within a CTA:
+//   warps 0..3, 4..7  one row per thread: its query in FP16 (scaled by a power of
+//                     two) to shared memory, then softmax of row tile 0 / 1, the
+//                     weights back into tensor memory; the row's sums
+//   warps 8..11       decode a tile from its 4-bit bytes into the MMAs' operands
+//   warp 12           TMEM allocation; one thread issues the MMAs
+//   warp 13           streams the cached bytes by bulk copies
+// A thread holds its row's 128 scores: the softmax warps take over registers
+// (184, 96 and 48 of 128 each). K and V are exact in FP16 (six significant bits).
+// The weights are 2^(z - m + 6), with a maximum m that is only moved (and O
+// rescaled in tensor memory) when the row's true maximum passes it by 8.
+// Every wait is bounded; one that gives up sets GDN_E_TIMEOUT and an abort flag
+// that ends every role's loop.
+constexpr int kKv = 128;
+constexpr int kPrefixThreads = 512;
+constexpr float kShift = 6.0f, kSlack = 8.0f;
+// What an item costs beside its tiles, in tiles: its queries, its sums and their joining.
+constexpr int kItemCost = 2;
+
 template <int D>
-__global__ void __launch_bounds__(256) kv4_prefix_kernel(SharedKv4 p) {
-  kv4_begin();
-  const Kv4Args &c = p.s.a.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
-  const int row = blockIdx.x * 8 + warp;
-  __shared__ float qs[8][D];
-  if (row >= p.rows) return;
-  const int tok = row / p.G, b = tok / p.r, g = p.w.seq_group[b];
-  if (g < 0) return;
-  const int S = p.w.len[g], lead = p.w.lead[g];
-  const uint16_t *q = p.s.a.q + (long long)tok * p.s.a.q_stride + (long long)(h * p.G + row - tok * p.G) * D;
-  for (int i = lane; i < D; i += 32) qs[warp][i] = bf16_bits_to_f32(q[i]);
-  __syncwarp();
-  const float cs = p.s.a.sm_scale * c.ks * kLog2e;
-  float m = -INFINITY, l = 0.0f, o[D / 32] = {};
-  for (int pos0 = 0; pos0 < S; pos0 += 32) {
-    const int pos = pos0 + lane;
-    const uint8_t *grp = pos < S ? kv4_group<D>(c, lead, pos) : nullptr;
-    if (grp) grp += h * kv4_head_bytes<D>(c);
-    float z = 0.0f;
-    for (int i = 0; i < D / 2 && grp; ++i) {
-      const float2 k = __half22float2(e2m1x2_to_h2(grp[kv4_k_code<D>(pos & 15, i)]));
-      const float s = e4m3_to_f32(grp[kv4_k_scale<D>(pos & 15, i / 8)]);
-      z = fmaf(qs[warp][2 * i], k.x * s, z);
-      z = fmaf(qs[warp][2 * i + 1], k.y * s, z);
+struct PrefixShape {
+  static constexpr int kStages = D == 128 ? 2 : 4;      // of K and of V each
+  static constexpr int kTileBytes = kKv * D * 2;        // a K tile, a V tile, and 128 query rows
+  // 64 tokens' bytes as they come: a group's second half begins 64 bytes late and groups lie 4 words apart modulo
+  // 32, so that the eight octets of tokens whose words a warp reads together lie on different banks
+  static constexpr int kFirst = 12 * D, kGap = 64, kGroup = 18 * D + 144;
+  static constexpr int kRaw = 4 * kGroup, kRaws = D == 128 ? 3 : 8;
+  static constexpr int kBars = 512;
+  static constexpr int kBytes = (2 + 2 * kStages) * kTileBytes + kRaws * kRaw + kBars;
+  static constexpr int kO = 2 * kKv;                    // TMEM columns: S0, S1, then O0, O1
+  static_assert((kGroup / 4) % 32 == 4 && kGroup % 16 == 0, "banks");
+  static_assert(kBytes <= 227 * 1024, "one CTA per SM");
+};
+
+// A place in the sequence of all tiles: an item, and a tile of it.
+struct Place {
+  int g, h, pair, tile;
+  int nt, S, lead, row0, rows, pairs;  // the group's tiles and tokens, through whom; its first row, rows, items per KV head
+  GDN_DEV void group(const SharedKv4 &p, int at) {
+    g = at;
+    S = p.w.len[g];
+    lead = p.w.lead[g];
+    nt = (S + kKv - 1) / kKv;
+    const int first = p.s.group_start[g];
+    row0 = first * p.r * p.G;
+    rows = (p.s.group_start[g + 1] - first) * p.r * p.G;
+    pairs = (rows + kItemRows - 1) / kItemRows;
+  }
+  GDN_DEV int item_row0() const { return row0 + pair * kItemRows; }
+  GDN_DEV int item_rows() const { return min(kItemRows, rows - pair * kItemRows); }
+  // Unique among the items of a KV head: each group takes at most rows / 256 + 1 places
+  GDN_DEV int slot() const { return row0 / kItemRows + g + pair; }
+  // The next item; only called while there is one.
+  GDN_DEV void next(const SharedKv4 &p) {
+    tile = 0;
+    if (++pair < pairs) return;
+    pair = 0;
+    if (++h < p.s.a.c.Hkv) return;
+    h = 0;
+    int at = g + 1;
+    while (p.w.len[at] == 0) ++at;
+    group(p, at);
+  }
+};
+// The tile at cost u (an item's own cost comes before its tiles), and how many tiles
+// lie before it; past the end only the number. total: all items' cost. A whole warp.
+GDN_DEV long long find_place(const SharedKv4 &p, long long u, int lane, Place &k, long long &total) {
+  long long cost = 0, tiles = 0, at = -1;
+  for (int g0 = 0; g0 < p.s.groups; g0 += 32) {
+    long long items = 0;
+    int nt = 0;
+    if (g0 + lane < p.s.groups && p.w.len[g0 + lane] > 0) {
+      Place x;
+      x.group(p, g0 + lane);
+      nt = x.nt;
+      items = (long long)x.pairs * p.s.a.c.Hkv;
     }
-    z = pos < S ? z * cs : -INFINITY;
-    float top = z;
+    const long long own = nt ? items * (nt + kItemCost) : 0;
+    long long incl = own, tincl = items * nt;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    top = fmaxf(top, m);
-    const float f = ex2(m - top), w = ex2(z - top);
-    m = top;
-    l = l * f + w;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] *= f;
-    for (int j = 0; j < 32 && pos0 + j < S; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
-      const uint8_t *gj = reinterpret_cast<const uint8_t *>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(grp), j));
-      const int t = (pos0 + j) & 15;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int ch = i * 32 + lane;
-        if (!gj) continue;
-        const float2 v = __half22float2(e2m1x2_to_h2(gj[kv4_v_code<D>(t, ch / 2)]));
-        o[i] = fmaf(wj, (ch & 1 ? v.y : v.x) * e4m3_to_f32(gj[kv4_v_scale<D>(t, ch / 16)]), o[i]);
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, tincl, o);
+      if (lane >= o) {
+        incl += y;
+        tincl += z;
       }
     }
+    const unsigned past = __ballot_sync(0xffffffffu, cost + incl > u);
+    if (at < 0 && past) {
+      const int l = __ffs(past) - 1;
+      k.group(p, g0 + l);
+      const long long off = u - cost - __shfl_sync(0xffffffffu, incl - own, l), item = off / (k.nt + kItemCost);
+      k.tile = max((int)(off - item * (k.nt + kItemCost)) - kItemCost, 0);
+      k.h = (int)(item / k.pairs);
+      k.pair = (int)(item - (long long)k.h * k.pairs);
+      at = tiles + __shfl_sync(0xffffffffu, tincl - items * nt, l) + item * k.nt + k.tile;
+    }
+    cost += __shfl_sync(0xffffffffu, incl, 31);
+    tiles += __shfl_sync(0xffffffffu, tincl, 31);
   }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) p.w.pre[((size_t)h * D + i * 32 + lane) * p.rows + row] = o[i];
-  if (lane == 0) reinterpret_cast<float2 *>(p.w.pre_ml)[(size_t)h * p.rows + row] = make_float2(m, l);
+  total = cost;
+  return at < 0 ? tiles : at;
 }
 
-// A warp per row: the two parts joined.
+template <int D>
+__global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4 p) {
+  using S = PrefixShape<D>;
+  constexpr int NS = S::kStages, NR = S::kRaws;
+  extern __shared__ __align__(1024) uint8_t sm[];  // the swizzled tiles start on 1024 bytes
+  uint8_t *qs = sm, *kbuf = sm + 2 * S::kTileBytes, *vbuf = kbuf + NS * S::kTileBytes, *raw = vbuf + NS * S::kTileBytes;
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(raw + NR * S::kRaw);
+  uint64_t *v_full = k_full + NS, *k_free = v_full + NS, *v_free = k_free + NS;
+  uint64_t *s_full = v_free + NS, *p_ready = s_full + 2, *o_done = p_ready + 4;
+  uint64_t *q_full = o_done + 2, *raw_full = q_full + 2, *raw_free = raw_full + NR, *fin = raw_free + NR;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(fin + 1);
+  volatile uint32_t *abort_flag = tmem_holder + 1;
+  Place *first = reinterpret_cast<Place *>(tmem_holder + 2);
+  long long *ends = reinterpret_cast<long long *>(raw + NR * S::kRaw + S::kBars - 16);
+  const Kv4Args &c = p.s.a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(k_full + s, 128);
+      mbar_init(v_full + s, 128);
+      mbar_init(k_free + s, 1);
+      mbar_init(v_free + s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + 2 * i, 128);
+      mbar_init(p_ready + 2 * i + 1, 128);
+      mbar_init(o_done + i, 1);
+      mbar_init(q_full + i, 128);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(raw_full + s, 1);
+      mbar_init(raw_free + s, 4);
+    }
+    mbar_init(fin, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  kv4_begin();
+  if (warp < 2) {  // the run's two ends
+    Place k{};
+    long long total = 0;
+    const long long tiles = find_place(p, 0x7fffffffffffffffLL, lane, k, total);
+    // no more runs than tiles: then the pieces of an item lie in neighbouring ones
+    const long long n = max(1LL, min((long long)gridDim.x, tiles)), x = min(n, (long long)blockIdx.x + warp);
+    const long long at = find_place(p, total / n * x + total % n * x / n, lane, k, total);
+    if (lane == 0) {
+      if (warp == 0) *first = k;
+      ends[warp] = at;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int n_tiles = (int)(ends[1] - ends[0]);
+  auto wait = [&](uint64_t *bar, uint32_t use) { return wait_or_abort(bar, use & 1u, abort_flag, c.status, c.wait); };
+  auto warp_wait_all = [&](uint64_t *bar, uint32_t use) { return __all_sync(0xffffffffu, wait(bar, use)) != 0; };
+  // For each of the run's segments (a part of one item): f(its number, place, tiles), until it returns false.
+  auto segments = [&](auto f) {
+    if (n_tiles == 0) return;
+    Place k = *first;
+    for (int at = 0, sg = 0;; ++sg) {
+      const int n = min(k.nt - k.tile, n_tiles - at);
+      if (!f(sg, k, n)) return;
+      at += n;
+      if (at == n_tiles) return;
+      k.next(p);
+    }
+  };
+
+  // registers: 512 threads x 128 at launch = 256 x 184 + 128 x 96 + 128 x 48
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    // ------------------------------------------------ softmax: thread = row r of row tile i
+    const int i = warp >> 2, r = tid & 127;
+    const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = base + i * kKv, tO = base + S::kO + i * D;
+    uint32_t uses = 0, dones = 0;  // of this row tile's scores, and items that had any
+    segments([&](int sg, const Place &w, int nkv) {
+      const int rows = w.item_rows(), row = w.item_row0() + i * 128 + r;  // the row's number among the KV head's
+      const bool have = i * 128 + r < rows;
+      if (i * 128 >= rows) return true;  // no rows in this tile
+      // ---- the row's query: FP16, scaled so that its largest lies in [2^13, 2^14)
+      float cs = p.s.a.sm_scale * c.ks * kLog2e;
+      {
+        uint4 x[D / 8];
+        const int tok = row / p.G;
+        const uint16_t *src = p.s.a.q + (long long)tok * p.s.a.q_stride + (long long)(w.h * p.G + row - tok * p.G) * D;
+        uint32_t mx = 0;
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q) {
+          x[q] = have ? reinterpret_cast<const uint4 *>(src)[q] : make_uint4(0, 0, 0, 0);
+          const uint32_t y[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
+        }
+        const int e = min(140 - (int)(mx >> 7), 60);
+        const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
+        cs *= __uint_as_float((uint32_t)(127 - e) << 23);
+        uint8_t *dst = qs + i * S::kTileBytes;
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q) {
+          const uint32_t y[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o[k] = h2u(__floats2half2_rn(__uint_as_float(y[k] << 16) * sc, __uint_as_float(y[k] & 0xFFFF0000u) * sc));
+          *reinterpret_cast<uint4 *>(dst + (q / 8) * (128 * 128) + sw_off16(r, (q & 7) * 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_async_shared();
+        mbar_arrive(q_full + i);
+      }
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < nkv; ++j, ++uses) {
+        if (!warp_wait_all(s_full + i, uses)) return false;
+        tc_fence_after();
+        const int valid = w.S - (w.tile + j) * kKv;  // tokens of this tile
+        float s[128];
+        {
+          uint32_t x[128];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, x + 32 * q);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 128; ++q) s[q] = __uint_as_float(x[q]);
+          if (valid < kKv) {
+#pragma unroll
+            for (int q = 0; q < 128; ++q)
+              if (q >= valid) s[q] = -INFINITY;
+          }
+        }
+        float x4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int q = 4; q < 128; q += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
+        const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * cs;
+        const bool up = top > m + kSlack;  // decided row by row: a row's result depends on no other row
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, up)) {
+          // S of this tile is complete, so the O += P V issued before it is too
+          const float f = up ? ex2(m - top) : 1.0f;
+          if (up) m = top;
+          l *= f;
+#pragma unroll
+          for (int q = 0; q < D; q += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + q, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(tO + q, o);
+          }
+        }
+        const float off = kShift - (m == -INFINITY ? 0.0f : m);
+        const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
+        float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
+        auto weigh = [&](int half) {
+          uint32_t x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float2 z = fma2(make_float2(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), cs2, off2);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            sum[e & 1] = add2(sum[e & 1], z);
+            x[e] = h2u(__floats2half2_rn(z.x, z.y));
+          }
+          tmem_st32(tS + 64 + 32 * half, x);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_ready + 2 * i + half);
+        };
+        weigh(1);
+        weigh(0);
+        sum[0] = add2(sum[0], sum[1]);
+        l = sum[0].x + sum[0].y;
+      }
+      // ---- the row's sums, channel by channel: 32 rows are a line
+      const bool whole = nkv == w.nt;
+      const int piece = 2 * (int)blockIdx.x + (sg == 0 ? 0 : 1);
+      {
+        if (!warp_wait_all(o_done + i, dones++)) return false;
+        tc_fence_after();
+        float *dst = whole ? p.w.pre + (size_t)w.h * D * p.rows + row : p.w.part + (size_t)piece * D * p.ld + i * 128 + r;
+        const size_t step = whole ? p.rows : p.ld;
+#pragma unroll
+        for (int q = 0; q < D; q += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + q, o);
+          tmem_ld_wait();
+          if (have) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) dst[(q + e) * step] = __uint_as_float(o[e]);
+          }
+        }
+        tc_fence_before();  // O has been read: the next item's products follow this row tile's next weights
+        if (have) {
+          const float2 ml = make_float2(m - kShift, l);
+          if (whole) reinterpret_cast<float2 *>(p.w.pre_ml)[(size_t)w.h * p.rows + row] = ml;
+          else reinterpret_cast<float2 *>(p.w.part_ml)[(size_t)piece * p.ld + i * 128 + r] = ml;
+        }
+      }
+      if (tid == 0) {
+        int32_t *e = p.w.ends + 2 * ((size_t)w.h * p.slots + w.slot());
+        if (w.tile == 0) e[0] = whole ? -1 : piece;
+        if (w.tile + nkv == w.nt) e[1] = blockIdx.x;
+      }
+      return true;
+    });
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    // ------------------------------------------------ 4-bit bytes into the operands
+    const int t0 = tid - 256;
+    uint32_t u = 0;  // tiles
+    segments([&](int, const Place &w, int n) {
+      for (int j = 0; j < n; ++j, ++u) {
+        const uint32_t s = u % NS;
+        const int valid = w.S - (w.tile + j) * kKv;
+        uint8_t *kt = kbuf + s * S::kTileBytes, *vt = vbuf + s * S::kTileBytes;
+        if (u >= NS && !warp_wait_all(k_free + s, u / NS - 1)) return false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t x = 2 * u + half;
+          if (!warp_wait_all(raw_full + x % NR, x / NR)) return false;
+          const uint8_t *rb = raw + x % NR * S::kRaw;
+#pragma unroll
+          for (int i = t0; i < 64 * (D / 8); i += 128) {  // K: eight channels of one token
+            const int row = i / (D / 8), ww = i % (D / 8);
+            const uint8_t *g = rb + row / 16 * S::kGroup;
+            const __half2 sc = __float2half2_rn(e4m3_to_f32(g[S::kGap + kv4_k_scale<D>(row & 15, ww / 2)]));
+            uint32_t o[4];
+            decode8(*reinterpret_cast<const uint32_t *>(g + kv4_k_code<D>(row & 15, ww * 4)), sc, o);
+            *reinterpret_cast<uint4 *>(kt + (ww / 8) * (kKv * 128) + sw_off16(half * 64 + row, (ww & 7) * 8)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        fence_async_shared();
+        mbar_arrive(k_full + s);
+        if (u >= NS && !warp_wait_all(v_free + s, u / NS - 1)) return false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t x = 2 * u + half;
+          const uint8_t *rb = raw + x % NR * S::kRaw;
+          if (t0 < D) {  // V^T: eight tokens of eight channels; eight neighbouring lanes write a whole 128-byte row
+            const int oct = t0 & 7, ww = t0 >> 3, hi = oct & 1;
+            const uint8_t *g = rb + (oct >> 1) * S::kGroup;
+            const uint8_t *codes = g + hi * S::kGap;  // tokens 8 .. 15 lie in the second half
+            uint4 sw = *reinterpret_cast<const uint4 *>(g + S::kGap + 17 * D + (ww / 2) * 16);
+            if (half * 64 + oct * 8 >= valid) sw = make_uint4(0, 0, 0, 0);  // no tokens there: anything
+            const uint32_t sc[4] = {sw.x, sw.y, sw.z, sw.w};
+            uint32_t o[4][2][4];  // [pair of tokens][even / odd channels][channel pair]
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t a = *reinterpret_cast<const uint32_t *>(codes + kv4_v_code<D>(hi * 8 + 2 * q, ww * 4));
+              const uint32_t b = *reinterpret_cast<const uint32_t *>(codes + kv4_v_code<D>(hi * 8 + 2 * q + 1, ww * 4));
+              uint32_t h;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(hi ? sc[q] >> 16 : sc[q] & 0xFFFFu)));
+              const __half2 f = *reinterpret_cast<__half2 *>(&h);
+              decode8((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), f, o[q][0]);
+              decode8(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), f, o[q][1]);
+            }
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+              *reinterpret_cast<uint4 *>(vt + half * (D * 128) + sw_off16(ww * 8 + ch, oct * 8)) =
+                  make_uint4(o[0][ch & 1][ch >> 1], o[1][ch & 1][ch >> 1], o[2][ch & 1][ch >> 1], o[3][ch & 1][ch >> 1]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(raw_free + x % NR);
+        }
+        fence_async_shared();
+        mbar_arrive(v_full + s);
+      }
+      return true;
+    });
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 12) {
+      // ------------------------------------------------ MMAs
+      constexpr uint32_t idS = idesc_f16(kKv), idO = idesc_f16(D);
+      constexpr uint64_t kStep = S::kTileBytes / 16;  // from one stage or tile to the next, in a descriptor
+      const uint64_t qd = desc_sw128(smem_u32(qs)), kd = desc_sw128(smem_u32(kbuf)), vd = desc_sw128(smem_u32(vbuf));
+      const bool me = elect_one();
+      uint32_t kv = 0, uses[2] = {0, 0}, items[2] = {0, 0};  // K / V tiles taken, each row tile's, and its items
+      segments([&](int, const Place &w, int n) {
+        bool ok = true;
+        if (me) {
+          const int two = w.item_rows() > 128 ? 2 : 1;
+          auto scores = [&](int i, uint32_t use) {  // S_i = Q_i K^T
+            const uint64_t q = qd + i * kStep, kk = kd + (uint64_t)(use % NS) * kStep;
+            const uint32_t d = tmem + i * kKv;
+            mma_f16_ss_c<false>(d, q, kk, idS);
+#pragma unroll
+            for (int k = 1; k < D / 16; ++k)
+              mma_f16_ss_c<true>(d, q + (k / 4) * (128 * 128 / 16) + 2 * (k & 3), kk + (k / 4) * (kKv * 128 / 16) + 2 * (k & 3), idS);
+            tc_commit(s_full + i);
+          };
+          auto values = [&](int i, uint32_t use, bool zero) {  // O_i += P_i V
+            const uint64_t v = vd + (uint64_t)(use % NS) * kStep;
+            const uint32_t d = tmem + S::kO + i * D, a = tmem + i * kKv + 64;
+            if (!(ok = wait(p_ready + 2 * i + 1, uses[i]))) return;  // tokens 64..127 first
+            tc_fence_after();
+            if (zero) mma_f16_ts_c<false>(d, a + 32, v + D * 128 / 16, idO);
+            else mma_f16_ts_c<true>(d, a + 32, v + D * 128 / 16, idO);
+#pragma unroll
+            for (int k = 1; k < 4; ++k) mma_f16_ts_c<true>(d, a + 32 + 8 * k, v + D * 128 / 16 + 2 * k, idO);
+            if (!(ok = wait(p_ready + 2 * i, uses[i]))) return;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ts_c<true>(d, a + 8 * k, v + 2 * k, idO);
+            ++uses[i];
+          };
+          ok = wait(q_full, items[0]++) && (two == 1 || wait(q_full + 1, items[1]++)) && wait(k_full + kv % NS, kv / NS);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (i < two) scores(i, kv);
+            tc_commit(k_free + kv % NS);
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            const uint32_t u = kv + j;
+            ok = wait(v_full + u % NS, u / NS) && (j + 1 >= n || wait(k_full + (u + 1) % NS, (u + 1) / NS));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!ok || i >= two) continue;
+              values(i, u, j == 0);
+              if (!ok) break;
+              if (j + 1 < n) scores(i, u + 1);
+              else tc_commit(o_done + i);
+            }
+            if (!ok) break;
+            tc_commit(v_free + u % NS);
+            if (j + 1 < n) tc_commit(k_free + (u + 1) % NS);
+          }
+        }
+        kv += n;
+        return __any_sync(0xffffffffu, me && ok) != 0;
+      });
+      // every MMA issued has completed before the CTA may leave
+      if (me) {
+        tc_commit(fin);
+        mbar_wait(fin, 0u);
+      }
+    } else if (warp == 13) {
+      // ------------------------------------------------ the cached bytes, 64 tokens at a time: a lane per group
+      uint32_t x = 0;
+      segments([&](int, const Place &w, int n) {
+        for (int j = 0; j < 2 * n; ++j, ++x) {
+          const uint32_t s = x % NR;
+          const int pos = (w.tile * 2 + j) * 64 + lane * 16;
+          const uint8_t *src = nullptr;
+          if (lane < 4 && pos < w.S) {
+            const uint8_t *g = kv4_group<D>(c, w.lead, pos);  // a bad page id (flagged) reads page 0
+            src = (g ? g : c.pages) + w.h * kv4_head_bytes<D>(c);
+          }
+          const unsigned there = __ballot_sync(0xffffffffu, src != nullptr);
+          if (x >= NR && !warp_wait_all(raw_free + s, x / NR - 1)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(raw_full + s, __popc(there) * 18 * D);
+          __syncwarp();
+          if (src) {
+            uint8_t *dst = raw + s * S::kRaw + lane * S::kGroup;
+            bulk_g2s(dst, src, S::kFirst, raw_full + s);
+            bulk_g2s(dst + S::kFirst + S::kGap, src + S::kFirst, 18 * D - S::kFirst, raw_full + s);
+          }
+        }
+        return true;
+      });
+      // the last copies land (or a bounded wait for each ends) before the CTA leaves, whoever gives up when
+      if (lane == 0)
+        for (uint32_t y = x < NR ? 0 : x - NR; y < x; ++y) mbar_wait(raw_full + y % NR, (y / NR) & 1u);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- the parts joined
+// A CTA per 32 rows of a KV head and 32 channels: the prefix's pieces, lane = row,
+// then with the row's own part. Bound by latency: an item's ends, the pieces'
+// (m, l), then their sums.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(SharedKv4 p) {
+  __shared__ float tile[32][33], f_own[32];
   kv4_begin();
   const Kv4Args &c = p.s.a.c;
-  const int lane = threadIdx.x & 31, h = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
-  const int tok = row / p.G, b = tok / p.r;
-  const long long out = (long long)tok * p.s.a.Hq + h * p.G + row - tok * p.G;
-  const bool two = p.w.seq_group[b] >= 0;
-  const float2 x = reinterpret_cast<const float2 *>(p.w.own_ml)[out];
-  const float2 y = two ? reinterpret_cast<const float2 *>(p.w.pre_ml)[(size_t)h * p.rows + row] : make_float2(-INFINITY, 0.0f);
-  const float m = fmaxf(x.x, y.x), safe = m == -INFINITY ? 0.0f : m;
-  const float fx = ex2(x.x - safe), fy = ex2(y.x - safe), l = x.y * fx + y.y * fy;
-  const float inv = l == 0.0f ? 0.0f : c.vs / l;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const int ch = i * 64 + 2 * lane;
-    const float2 o = *reinterpret_cast<const float2 *>(p.w.own + out * D + ch);
-    float2 v = make_float2(0.0f, 0.0f);
-    if (two) {
-      const float *pre = p.w.pre + ((size_t)h * D + ch) * p.rows + row;
-      v = make_float2(pre[0], pre[p.rows]);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, ch0 = blockIdx.z * 32;
+  const int row = blockIdx.x * 32 + lane;
+  {
+    const bool have = row < p.rows;
+    const int tok = have ? row / p.G : 0, b = tok / p.r, g = have && p.runs ? p.w.seq_group[b] : -1;
+    const long long out = (long long)tok * p.s.a.Hq + h * p.G + row - tok * p.G;
+    // the pieces: the first, then one in each run
+    const float *src = nullptr;   // the first piece's channel 0
+    const float2 *ml = nullptr;
+    int np = 0;
+    size_t step = 0, ch_step = p.rows;
+    int second = 0;
+    if (g >= 0) {
+      const int row0 = p.s.group_start[g] * p.r * p.G, pair = (row - row0) / kItemRows;
+      const int2 e = reinterpret_cast<const int2 *>(p.w.ends)[(size_t)h * p.slots + row0 / kItemRows + g + pair];
+      const int in = row - row0 - pair * kItemRows;
+      if (e.x < 0) {
+        np = 1;
+        src = p.w.pre + (size_t)h * D * p.rows + row;
+        ml = reinterpret_cast<const float2 *>(p.w.pre_ml) + (size_t)h * p.rows + row;
+      } else {
+        np = e.y - e.x / 2 + 1;
+        src = p.w.part + (size_t)e.x * D * p.ld + in;
+        ml = reinterpret_cast<const float2 *>(p.w.part_ml) + (size_t)e.x * p.ld + in;
+        ch_step = p.ld;
+        second = 2 - (e.x & 1);  // from the first piece to the second, in pieces
+        step = 2;
+      }
     }
-    *reinterpret_cast<uint32_t *>(p.s.a.out + out * D + ch) = bf16x2((o.x * fx + v.x * fy) * inv, (o.y * fx + v.y * fy) * inv);
+    auto at = [&](int j) { return j == 0 ? (size_t)0 : second + (size_t)(j - 1) * step; };
+    const float2 own = have ? reinterpret_cast<const float2 *>(p.w.own_ml)[out] : make_float2(-INFINITY, 0.0f);
+    float m = own.x;
+    for (int j = 0; j < np; j += 4) {
+      float x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = j + u < np ? ml[at(j + u) * p.ld].x : -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) m = fmaxf(m, x[u]);
+    }
+    const float safe = m == -INFINITY ? 0.0f : m, fo = ex2(own.x - safe);
+    float l = own.y * fo, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < np; j += 4) {
+      float2 x[4];
+      float v[4][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        x[u] = j + u < np ? ml[at(j + u) * p.ld] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[u][k] = j + u < np ? src[(at(j + u) * D + ch0 + warp * 4 + k) * ch_step] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = ex2(x[u].x - safe);
+        l = fmaf(x[u].y, f, l);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = fmaf(v[u][k], f, acc[k]);
+      }
+    }
+    const float inv = l == 0.0f ? 0.0f : c.vs / l;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tile[lane][warp * 4 + k] = acc[k] * inv;
+    if (warp == 0) {
+      f_own[lane] = fo * inv;
+      if (p.s.a.lse && ch0 == 0 && have) p.s.a.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+    }
   }
-  if (p.s.a.lse && lane == 0) p.s.a.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+  __syncthreads();
+  const int r = threadIdx.x / 8, ch = threadIdx.x % 8 * 4, mine = blockIdx.x * 32 + r;
+  if (mine >= p.rows) return;
+  const int tok = mine / p.G;
+  const long long out = ((long long)tok * p.s.a.Hq + h * p.G + mine - tok * p.G) * D + ch0 + ch;
+  const float4 o = *reinterpret_cast<const float4 *>(p.w.own + out);
+  const float f = f_own[r];
+  *reinterpret_cast<uint2 *>(p.s.a.out + out) = make_uint2(bf16x2(fmaf(o.x, f, tile[r][ch]), fmaf(o.y, f, tile[r][ch + 1])),
+                                                           bf16x2(fmaf(o.z, f, tile[r][ch + 2]), fmaf(o.w, f, tile[r][ch + 3])));
 }
 
 template <int D>
 cudaError_t launch_t(const SharedKv4 &p, int num_sms, cudaStream_t stream) {
+  using S = PrefixShape<D>;
   const Kv4Args &c = p.s.a.c;
   cudaError_t e = kv4_launch(kv4_shared_plan_kernel, c.B + p.s.groups, kPlanThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
-  const dim3 grid((p.rows + 7) / 8, c.Hkv);
-  e = kv4_launch(kv4_prefix_kernel<D>, grid, 256, 0, stream, p);
-  if (e != cudaSuccess) return e;
+  if (p.runs > 0) {
+    static bool allowed[64];
+    e = kv4_allow_smem(kv4_prefix_kernel<D>, S::kBytes, allowed);
+    if (e == cudaSuccess) e = kv4_launch(kv4_prefix_kernel<D>, p.runs, kPrefixThreads, S::kBytes, stream, p);
+    if (e != cudaSuccess) return e;
+  }
   Kv4AttnArgs own = p.s.a;
   own.c.kv_len = p.w.own_len;
   own.c.table = p.w.own_table;
   e = launch_kv4_decode(own, p.w.decode, num_sms, stream, p.w.own, p.w.own_ml);
   if (e != cudaSuccess) return e;
-  return kv4_launch(kv4_merge_kernel<D>, grid, 256, 0, stream, p);
+  return kv4_launch(kv4_merge_kernel<D>, dim3((p.rows + 31) / 32, c.Hkv, D / 32), 256, 0, stream, p);
 }
 
 }  // namespace
 
 size_t kv4_decode_shared_bytes(const Kv4SharedArgs &s, int num_sms) {
-  SharedWs w;
-  return s.a.c.T ? lay_out(s, nullptr, num_sms, w) : 0;
+  SharedKv4 p{};
+  return s.a.c.T ? lay_out(s, nullptr, num_sms, p) : 0;
 }
 
 cudaError_t launch_kv4_decode_shared(const Kv4SharedArgs &s, void *workspace, int num_sms, cudaStream_t stream) {
-  const int G = s.a.Hq / s.a.c.Hkv;
-  SharedKv4 p{s, {}, s.a.c.T / s.a.c.B, G, s.a.c.T * G};
-  lay_out(s, static_cast<uint8_t *>(workspace), num_sms, p.w);
+  SharedKv4 p{};
+  lay_out(s, static_cast<uint8_t *>(workspace), num_sms, p);
   return s.a.c.D == 128 ? launch_t<128>(p, num_sms, stream) : launch_t<64>(p, num_sms, stream);
 }
 
