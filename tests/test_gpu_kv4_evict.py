@@ -105,6 +105,10 @@ def bits(t):
     (1, 128, 128, 1, [9001], [4097], 1024),
     (8, 64, 16, 1, [77] * 9, [7] * 9, 2),
     (1, 64, 64, 1, [70000], [300], 10),                         # far more tokens than a CTA has threads
+    (1, 64, 256, 1, [400000], [1000], 100),                     # more than a cluster's shared memory holds
+    (2, 64, 64, 1, [30000, 17], [20011, 9], 5),
+    (1, 64, 64, 1, [12000], [7], 0),
+    (2, 64, 64, 40, [9000], [3], 1),                            # a CTA a row
 ])
 @pytest.mark.parametrize("kind", ["weights", "ties"])
 def test_evict(g, hkv, d, page, layers, lens, keeps, recent, kind):
@@ -132,7 +136,7 @@ def test_evict(g, hkv, d, page, layers, lens, keeps, recent, kind):
 
 
 @pytest.mark.parametrize("kind", ["signs", "equal"])
-@pytest.mark.parametrize("n", [5, 33, 1024, 1025, 5000])
+@pytest.mark.parametrize("n", [5, 33, 1024, 1025, 5000, 20001])
 def test_order_of_scores(g, kind, n):
     """Ties to the older, the zeros equal, NaN below all; the scores keep their bits."""
     hkv, d, page = 2, 64, 64
