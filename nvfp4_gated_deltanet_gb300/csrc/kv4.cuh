@@ -127,14 +127,15 @@ GDN_DEV float2 add2(float2 x, float2 y) {
   return r;
 }
 
-// Let a kernel (one flag array each) have `bytes` of dynamic shared memory, once per device.
+// Let a kernel (one flag array each) have `bytes` of dynamic shared memory (and clusters of 16), once per device.
 template <typename K>
-cudaError_t kv4_allow_smem(K kernel, int bytes, bool (&done)[64]) {
+cudaError_t kv4_allow_smem(K kernel, int bytes, bool (&done)[64], bool clusters = false) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && done[dev]) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) done[dev] = true;
   return e;
 }

@@ -64,17 +64,19 @@ GDN_DEV unsigned block_before(unsigned v, unsigned *sums, unsigned &total) {
 }
 
 // ---------------------------------------------------------------- the choice
-// A cluster of CTAs per (layer, sequence, KV head); a CTA holds the scores of its
-// slice of the row in shared memory, so that the row is read once (and may be
-// overwritten once all have read). The lowest order that is kept is found 11 bits
-// at a time: each CTA counts its own, all read all counts. Then the kept tokens'
-// places follow from prefix counts, in order.
-// Bound by latency: three counting passes, a barrier of the cluster in each, and
-// the row's one read.
-constexpr int kBins = 2048;
-constexpr int kMaxSlice = 48 * 1024;  // tokens whose scores fit beside the counts
-constexpr int kSplit = 8192;          // where SMs are idle, a CTA's slice is halved down to this
-constexpr int kShort = 4096;          // rows up to this take CTAs of 256 threads
+// A CTA, or a cluster of them, per (layer, sequence, KV head); a CTA holds its
+// slice of the row in shared memory and the tokens' orders in registers, so that
+// the row is read once (and may be overwritten once all have read). The lowest
+// order that is kept is found in passes that split its range into bins, first from
+// the least order to the greatest. (Bins of the leading bits put the scores' few
+// exponents into few bins, whose counters the lanes of a warp then wait for.) A
+// cluster adds its CTAs' counts up a share of the bins each: remote loads take a
+// warp about 34 cycles each, and every CTA reading all counts took 35000 cycles a
+// pass. Then the kept tokens' places follow from prefix counts, in order: a warp
+// has neighbouring tokens, counts them, and after one barrier writes them.
+// Bound by latency: the passes' barriers, and the row's one read.
+constexpr int kMaxHeld = 48 * 1024;   // tokens that shared memory holds beside the counts
+constexpr int kSplit = 4096;          // where SMs are idle, a CTA's slice is halved down to this
 
 GDN_DEV uint32_t cluster_rank() {
   uint32_t r;
@@ -92,19 +94,36 @@ GDN_DEV unsigned cluster_load(const unsigned *p, uint32_t rank) {
   return v;
 }
 
-// HELD: the row is in shared memory; without, it is read again in each pass (one CTA, any length).
-template <int THREADS, int CS, bool HELD>
+// E: a thread's tokens, whose orders are in registers; 0: any number, worked out
+// in each pass. HELD: the slice is in shared memory; without, it is read again
+// each time (one CTA, which overwrites only what it has read).
+template <int THREADS, int CS, int E, bool HELD>
 __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
-  static_assert(HELD || CS == 1, "a CTA overwrites only what it has read");
-  constexpr int PER = kBins / THREADS;
+  static_assert(HELD || (CS == 1 && E == 0), "a CTA overwrites only what it has read");
+  constexpr int BITS = CS > 1 ? 8 : 11, BINS = 1 << BITS, PER = BINS > THREADS ? BINS / THREADS : 1, WARPS = THREADS / 32;
+  constexpr int SHARE = CS > 1 ? BINS / CS : 1;  // bins whose counts a CTA of the cluster adds up
   extern __shared__ __align__(16) float held[];  // the slice's scores
-  __shared__ unsigned hist[2][kBins], sums[33], mine[2];
-  __shared__ unsigned found[2];
+  __shared__ unsigned hist[2][BINS], gathered[2][SHARE], sums[33], range[2][32], ext[2], mine[2], found[2];
   kv4_begin();
   const Kv4Args &c = p.c;
-  const int tid = threadIdx.x, rank = CS > 1 ? (int)cluster_rank() : 0, row_id = blockIdx.x / CS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CS > 1 ? (int)cluster_rank() : 0, row_id = blockIdx.x / CS;
   const int h = row_id % c.Hkv, b = row_id / c.Hkv % c.B, l = row_id / c.Hkv / c.B;
   Evictee e = evictee(p, b);
+  const size_t row = (size_t)l * p.score_layer + ((size_t)max(e.slot, 0) * c.Hkv + h) * p.s.tokens;
+  const float *in = p.s.in + row;
+  float *out = p.s.out + row;
+  if (e.slot < 0) e.n = e.k = 0;
+  const int n = e.n, k = e.k, r = min(p.recent, k), m = n - r;  // m tokens compete for k - r places
+  const int slice = (n + CS - 1) / CS, i0 = min(n, rank * slice), len = min(n - i0, slice);  // this CTA's tokens
+  const int rivals = max(0, min(len, m - i0));                                               // of them, those that compete
+  // a warp has `part` neighbours, of which this lane takes every 32nd
+  const int part = (len + THREADS - 1) / THREADS * 32, w0 = min(len, warp * part), w1 = min(len, w0 + part);
+  float f[E > 0 ? E : 1];
+  if constexpr (E > 0) {
+#pragma unroll
+    for (int x = 0; x < E; ++x) f[x] = w0 + x * 32 + lane < w1 ? in[i0 + w0 + x * 32 + lane] : 0.0f;
+  }
   if (p.s.slots && e.slot >= 0) {  // a slot that another sequence has too: both are left out
     int twice = 0;
     for (int i = tid; i < c.B; i += THREADS) twice |= i != b && p.s.slots[i] == e.slot;
@@ -114,134 +133,200 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
     }
   }
   int32_t *kept = p.kept + (size_t)row_id * p.max_keep;
-  if (h == 0 && l == 0 && tid == 0 && rank == 0) p.new_len[b] = e.slot < 0 ? -1 : e.k;
+  if (h == 0 && l == 0 && tid == 0 && rank == 0) p.new_len[b] = e.slot < 0 ? -1 : k;
   if (e.slot < 0) {  // all CTAs of the cluster alike
     for (int i = rank * THREADS + tid; i < p.max_keep; i += CS * THREADS) kept[i] = -1;
     return;
   }
-  const size_t row = (size_t)l * p.score_layer + ((size_t)e.slot * c.Hkv + h) * p.s.tokens;
-  const float *in = p.s.in + row;
-  float *out = p.s.out + row;
-  const int n = e.n, k = e.k, r = min(p.recent, k), m = n - r;  // m tokens compete for k - r places
-  const int slice = (n + CS - 1) / CS, i0 = min(n, rank * slice), len = min(n - i0, slice);  // this CTA's tokens
-  auto score = [&](int i) { return HELD ? held[i] : in[i]; };
-  for (int x = tid; x < kBins; x += THREADS) hist[0][x] = 0;
-  __syncthreads();
-  // ---- read: orders kept, the first count beside it (tokens that compete: i0 + i < m)
-#pragma unroll 4
-  for (int i = tid; i < len; i += THREADS) {
-    const float f = in[i0 + i];
-    if (HELD) held[i] = f;
-    if (i0 + i < m) atomicAdd(&hist[0][order_of(f) >> 21], 1u);
-  }
-  // ---- the lowest order that is kept
-  uint32_t low = 0;
-  unsigned need = k - r;  // places left for tokens whose higher bits are low's
-  const bool some = need > 0;
+  for (int x = tid; x < BINS; x += THREADS) hist[0][x] = 0;
+  auto score = [&](int i) { return HELD ? held[i] : in[i0 + i]; };
+  // ---- read: the least and the greatest order of the tokens that compete
+  uint32_t lo = ~0u, hi = 0u, o[E > 0 ? E : 1];
+  if constexpr (E > 0) {
 #pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    unsigned *cnt = hist[pass & 1];
-    if (pass > 0) {
-      if (some)
-#pragma unroll 4
-        for (int i = tid; i < len; i += THREADS) {
-          const uint32_t o = order_of(score(i));
-          if (i0 + i < m && (o >> (shift + bits)) == (low >> (shift + bits)))
-            atomicAdd(&cnt[o >> shift & ((1 << bits) - 1)], 1u);
-        }
-    }
-    // the other counts are cleared for the next pass (everybody has read them: a barrier of the last pass)
-    if (pass < 2)
-      for (int x = tid; x < kBins; x += THREADS) hist[(pass & 1) ^ 1][x] = 0;
-    if (CS > 1) cluster_sync();
-    else __syncthreads();
-    // bins from the top: this thread's PER of them, summed over the cluster
-    unsigned v[PER], sum = 0, total;
-#pragma unroll
-    for (int x = 0; x < PER; ++x) {
-      const int bin = kBins - 1 - (tid * PER + x);
-      v[x] = 0;
-      if (CS > 1) {
-#pragma unroll
-        for (int y = 0; y < CS; ++y) v[x] += cluster_load(&cnt[bin], y);
-      } else {
-        v[x] = cnt[bin];
+    for (int x = 0; x < E; ++x) {
+      const int i = w0 + x * 32 + lane;
+      if (i < w1) held[i] = f[x];
+      o[x] = order_of(f[x]);
+      if (i < w1 && i < rivals) {
+        lo = min(lo, o[x]);
+        hi = max(hi, o[x]);
       }
-      sum += v[x];
+    }
+  } else {
+    for (int i = tid; i < len; i += THREADS) {
+      const float f = in[i0 + i];
+      if (HELD) held[i] = f;
+      if (i < rivals) {
+        lo = min(lo, order_of(f));
+        hi = max(hi, order_of(f));
+      }
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    range[0][warp] = lo;
+    range[1][warp] = hi;
+  }
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, lane < WARPS ? range[0][lane] : ~0u);
+  hi = __reduce_max_sync(0xffffffffu, lane < WARPS ? range[1][lane] : 0u);
+  if (CS > 1) {
+    if (tid == 0) {
+      ext[0] = lo;
+      ext[1] = hi;
+    }
+    cluster_sync();  // (also: everybody has read the row)
+    lo = __reduce_min_sync(0xffffffffu, cluster_load(&ext[0], lane % CS));
+    hi = __reduce_max_sync(0xffffffffu, cluster_load(&ext[1], lane % CS));
+  }
+  // ---- the lowest order that is kept: of the tokens in [low, low + 2^width) the need-th from the top
+  uint32_t low = lo;
+  unsigned need = k - r;
+  const bool some = need > 0;
+  int width = 32, shift = hi > lo ? max(0, 32 - __clz(hi - lo) - BITS) : 0;
+  for (int pass = 0; some; ++pass) {
+    unsigned *cnt = hist[pass & 1];
+    unsigned first = 0;  // tokens in the lowest bin: many scores are equal where attention never looked
+    auto count = [&](uint32_t x) {
+      const uint32_t t = x - low;
+      if (x >= low && (width >= 32 || (t >> width) == 0)) {
+        if ((t >> shift) == 0) ++first;
+        else atomicAdd(&cnt[t >> shift], 1u);
+      }
+    };
+    if constexpr (E > 0) {
+#pragma unroll
+      for (int x = 0; x < E; ++x)
+        if (w0 + x * 32 + lane < min(w1, rivals)) count(o[x]);
+    } else {
+      for (int i = tid; i < rivals; i += THREADS) count(order_of(score(i)));
+    }
+    first = __reduce_add_sync(0xffffffffu, first);
+    if (lane == 0 && first) atomicAdd(&cnt[0], first);
+    // the other counts are cleared for the next pass (everybody has read them: the last pass's barriers)
+    for (int x = tid; x < BINS; x += THREADS) hist[(pass & 1) ^ 1][x] = 0;
+    unsigned v[PER], sum = 0, total;
+    if constexpr (CS > 1) {
+      cluster_sync();
+      if (tid < BINS) {  // thread: bin rank SHARE + tid / CS of CTA tid % CS
+        unsigned x = cluster_load(&cnt[rank * SHARE + tid / CS], tid % CS);
+#pragma unroll
+        for (int d = 1; d < CS; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        if (tid % CS == 0) gathered[pass & 1][tid / CS] = x;
+      }
+      cluster_sync();
+      const int bin = BINS - 1 - tid;  // from the top
+      v[0] = tid < BINS ? cluster_load(&gathered[pass & 1][bin % SHARE], bin / SHARE) : 0u;
+      sum = v[0];
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < PER; ++x) sum += v[x] = cnt[BINS - 1 - (tid * PER + x)];
     }
     // bin x holds the place `need` when the bins above it hold fewer than `need` and with it at least as many
     unsigned before = block_before<THREADS>(sum, sums, total);
 #pragma unroll
     for (int x = 0; x < PER; ++x) {
       if (before < need && before + v[x] >= need) {
-        found[0] = kBins - 1 - (tid * PER + x);
+        found[0] = BINS - 1 - (tid * PER + x);
         found[1] = before;
       }
       before += v[x];
     }
     __syncthreads();
-    if (some) {
-      low |= found[0] << shift;
-      need -= found[1];
-    }
-    if (CS > 1) cluster_sync();  // everybody has read these counts
-    else __syncthreads();
-  }
-  // ---- this slice's tokens above low and at it, and those of the slices before
-  unsigned above = 0, at = 0;
-  if (CS > 1) {
-    unsigned a = 0, s = 0;
-    for (int i = tid; i < len; i += THREADS) {
-      const uint32_t o = order_of(score(i));
-      a += i0 + i < m && o > low;
-      s += i0 + i < m && o == low;
-    }
-    unsigned ta, ts;
-    block_before<THREADS>(a, sums, ta);
-    block_before<THREADS>(s, sums, ts);
-    if (tid == 0) {
-      mine[0] = ta;
-      mine[1] = ts;
-    }
-    cluster_sync();
-    for (int y = 0; y < rank; ++y) {
-      above += cluster_load(&mine[0], y);
-      at += cluster_load(&mine[1], y);
-    }
+    low += found[0] << shift;
+    need -= found[1];
+    if (shift == 0) break;
+    width = shift;
+    shift = max(0, shift - BITS);
+    __syncthreads();  // everybody has read `found`, and (one CTA) the counts
   }
   // ---- in order: the tokens above low, the first `need` of those at it, the newest
-  for (int j0 = 0; j0 < len; j0 += 4 * THREADS) {
-    const int j = j0 + 4 * tid;
-    float f[4];
-    unsigned over = 0, same = 0;
+  auto kinds = [&](int j, uint32_t x, unsigned &over, unsigned &same) {  // of the 32 tokens from j, this lane's order being x
+    const bool in_m = some && j + lane < min(w1, rivals);
+    over = __ballot_sync(0xffffffffu, in_m && x > low);
+    same = __ballot_sync(0xffffffffu, in_m && x == low);
+  };
+  unsigned above = 0, at = 0;
+  if constexpr (E > 0) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      f[x] = j + x < len ? score(j + x) : 0.0f;
-      const uint32_t o = order_of(f[x]);
-      const bool in_m = some && j + x < len && i0 + j + x < m;
-      over |= (unsigned)(in_m && o > low) << x;
-      same |= (unsigned)(in_m && o == low) << x;
+    for (int x = 0; x < E; ++x) {
+      unsigned over, same;
+      kinds(w0 + x * 32, o[x], over, same);
+      above += __popc(over);
+      at += __popc(same);
     }
-    unsigned total;
-    const unsigned before = block_before<THREADS>((unsigned)__popc(over) | (unsigned)__popc(same) << 16, sums, total);
-    unsigned a = above + (before & 0xffffu), t = at + (before >> 16);
+  } else if (HELD) {
+    for (int j = w0; j < w1; j += 32) {
+      unsigned over, same;
+      kinds(j, j + lane < w1 ? order_of(held[j + lane]) : 0u, over, same);
+      above += __popc(over);
+      at += __popc(same);
+    }
+  }
+  unsigned a_all, t_all;
+  const unsigned a0 = block_before<THREADS>(lane == 0 ? above : 0u, sums, a_all);
+  const unsigned t0 = block_before<THREADS>(lane == 0 ? at : 0u, sums, t_all);
+  above = __shfl_sync(0xffffffffu, a0, 0);
+  at = __shfl_sync(0xffffffffu, t0, 0);
+  if (CS > 1) {
+    if (tid == 0) {
+      mine[0] = a_all;
+      mine[1] = t_all;
+    }
+    cluster_sync();
+    above += __reduce_add_sync(0xffffffffu, lane < rank ? cluster_load(&mine[0], lane) : 0u);
+    at += __reduce_add_sync(0xffffffffu, lane < rank ? cluster_load(&mine[1], lane) : 0u);
+  }
+  auto write = [&](int j, uint32_t x) {
+    unsigned over, same;
+    kinds(j, x, over, same);
+    const unsigned before = (1u << lane) - 1u, a = above + __popc(over & before), t = at + __popc(same & before);
+    const int i = i0 + j + lane;
+    int to = -1;
+    if ((over >> lane & 1) || ((same >> lane & 1) && t < need)) to = (int)(a + min(t, need));
+    else if (j + lane < w1 && i >= m) to = k - r + (i - m);
+    if (to >= 0) {
+      kept[to] = i;
+      out[to] = held[j + lane];
+    }
+    above += __popc(over);
+    at += __popc(same);
+  };
+  if constexpr (E > 0) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int i = i0 + j + x;
-      const bool is_over = over >> x & 1, is_same = same >> x & 1;
+    for (int x = 0; x < E; ++x)
+      if (w0 + x * 32 < w1) write(w0 + x * 32, o[x]);
+  } else if (HELD) {
+    for (int j = w0; j < w1; j += 32) write(j, j + lane < w1 ? order_of(held[j + lane]) : 0u);
+  } else {  // in steps of the block, each read by all before any of it is written
+    above = at = 0;
+    for (int j0 = 0; j0 < len; j0 += THREADS) {
+      const int j = j0 + warp * 32;
+      const float f = j + lane < len ? in[j + lane] : 0.0f;
+      const uint32_t x = order_of(f);
+      const bool in_m = some && j + lane < rivals;
+      const unsigned over = __ballot_sync(0xffffffffu, in_m && x > low), same = __ballot_sync(0xffffffffu, in_m && x == low);
+      unsigned all;
+      const unsigned b4 = block_before<THREADS>(lane == 0 ? (unsigned)__popc(over) | (unsigned)__popc(same) << 16 : 0u, sums, all);
+      const unsigned first = __shfl_sync(0xffffffffu, b4, 0), keep_a = above, keep_t = at;
+      above += first & 0xffffu;
+      at += first >> 16;
+      const int i = j + lane;
+      const unsigned before = (1u << lane) - 1u, a = above + __popc(over & before), t = at + __popc(same & before);
       int to = -1;
-      if (is_over || (is_same && t < need)) to = (int)(a + min(t, need));
-      else if (j + x < len && i >= m) to = k - r + (i - m);
-      a += is_over;
-      t += is_same;
+      if ((over >> lane & 1) || ((same >> lane & 1) && t < need)) to = (int)(a + min(t, need));
+      else if (i < len && i >= m) to = k - r + (i - m);
       if (to >= 0) {
         kept[to] = i;
-        out[to] = f[x];
+        out[to] = f;
       }
+      above = keep_a + (all & 0xffffu);
+      at = keep_t + (all >> 16);
     }
-    above += total & 0xffffu;
-    at += total >> 16;
+    __syncthreads();
   }
   for (int i = k + rank * THREADS + tid; i < n; i += CS * THREADS) out[i] = 0.0f;
   for (int i = k + rank * THREADS + tid; i < p.max_keep; i += CS * THREADS) kept[i] = -1;
@@ -315,14 +400,14 @@ __global__ void __launch_bounds__(256) kv4_move_kernel(Kv4EvictArgs p) {
   else *reinterpret_cast<uint16_t *>(dst + kv4_k_scale<D>(t, b0)) = (uint16_t)word;
 }
 
-template <int THREADS, int CS, bool HELD>
+template <int THREADS, int CS, int E, bool HELD = true>
 cudaError_t launch_select(const Kv4EvictArgs &p, int slice, cudaStream_t stream) {
-  const size_t smem = HELD ? 4 * (size_t)slice : 0;
   static bool allowed[64];
-  cudaError_t e = kv4_allow_smem(kv4_select_kernel<THREADS, CS, HELD>, HELD ? 4 * kMaxSlice : 0, allowed);
+  const auto kernel = kv4_select_kernel<THREADS, CS, E, HELD>;
+  cudaError_t e = kv4_allow_smem(kernel, HELD ? 4 * (E ? THREADS * E : kMaxHeld) : 0, allowed, CS > 8);
   if (e != cudaSuccess) return e;
-  return kv4_launch_cluster(kv4_select_kernel<THREADS, CS, HELD>, (unsigned)(p.layers * p.c.B * p.c.Hkv) * CS, CS, THREADS,
-                            smem, stream, p);
+  return kv4_launch_cluster(kernel, (unsigned)(p.layers * p.c.B * p.c.Hkv) * CS, CS, THREADS, HELD ? 4 * (size_t)slice : 0,
+                            stream, p);
 }
 
 }  // namespace
@@ -331,16 +416,22 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs &p, cudaStream_t stream) {
   const Kv4Args &c = p.c;
   const long long rows = (long long)p.layers * c.B * c.Hkv;
   const int most = (int)std::min((long long)p.s.tokens, (long long)c.cols * c.page_tokens);  // tokens of a row
+  // CTAs of a row: as many as registers need, and while SMs are idle and the slices long
   int cs = 1;
-  while (cs < 8 && ((most + cs - 1) / cs > kMaxSlice || (most / cs > kSplit && rows * cs < 152))) cs *= 2;
+  while (cs < 16 && ((most + cs - 1) / cs > 16384 || (most / cs > kSplit && rows * cs < 152))) cs *= 2;
   const int slice = (most + cs - 1) / cs;
   cudaError_t e;
-  if (slice > kMaxSlice) e = launch_select<1024, 1, false>(p, 0, stream);
-  else if (cs == 8) e = launch_select<1024, 8, true>(p, slice, stream);
-  else if (cs == 4) e = launch_select<1024, 4, true>(p, slice, stream);
-  else if (cs == 2) e = launch_select<1024, 2, true>(p, slice, stream);
-  else if (most > kShort) e = launch_select<1024, 1, true>(p, slice, stream);
-  else e = launch_select<256, 1, true>(p, slice, stream);
+  if (slice > kMaxHeld) e = launch_select<1024, 1, 0, false>(p, 0, stream);
+  else if (slice > 16384) e = launch_select<1024, 16, 0>(p, slice, stream);
+  else if (cs == 16) e = launch_select<1024, 16, 16>(p, slice, stream);
+  else if (cs == 8) e = launch_select<1024, 8, 16>(p, slice, stream);
+  else if (cs == 4) e = launch_select<1024, 4, 16>(p, slice, stream);
+  else if (cs == 2) e = launch_select<1024, 2, 16>(p, slice, stream);
+  else if (slice > 8192) e = launch_select<1024, 1, 16>(p, slice, stream);
+  else if (slice > 4096) e = launch_select<512, 1, 16>(p, slice, stream);
+  else if (slice > 2048) e = launch_select<256, 1, 16>(p, slice, stream);
+  else if (slice > 1024) e = launch_select<256, 1, 8>(p, slice, stream);
+  else e = launch_select<256, 1, 4>(p, slice, stream);
   if (e != cudaSuccess || p.max_keep == 0) return e;
   const unsigned grid = (unsigned)((p.max_keep + 127) / 128) * c.B * c.Hkv * p.layers;
   return kv4_launch(c.D == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>, grid, 256, 0, stream, p);

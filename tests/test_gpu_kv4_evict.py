@@ -105,7 +105,9 @@ def bits(t):
     (1, 128, 128, 1, [9001], [4097], 1024),
     (8, 64, 16, 1, [77] * 9, [7] * 9, 2),
     (1, 64, 64, 1, [70000], [300], 10),                         # far more tokens than a CTA has threads
-    (1, 64, 256, 1, [400000], [1000], 100),                     # more than a cluster's shared memory holds
+    (1, 64, 256, 1, [800000], [1000], 100),                     # more than a cluster's shared memory holds
+    (1, 64, 256, 1, [700000, 200], [1000, 100], 100),           # the most that it holds, nearly
+    (2, 64, 64, 5, [40000], [100], 7),                          # clusters of 4
     (2, 64, 64, 1, [30000, 17], [20011, 9], 5),
     (1, 64, 64, 1, [12000], [7], 0),
     (2, 64, 64, 40, [9000], [3], 1),                            # a CTA a row
