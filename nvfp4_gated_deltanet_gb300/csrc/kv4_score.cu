@@ -300,142 +300,462 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
   }
 }
 
-// 32 tokens of one head as the A operand of S^T = K Q^T, m16n8k16: lane (g, t)
-// holds tokens g and g + 8 of two groups, 16 (d = 64: 8) consecutive code bytes of
-// each -- the k order is free. Exact in FP16.
-template <int D>
-struct KeyRows {
-  uint32_t a[2][D / 32][2][4];  // [group][word][token g, g + 8][channel pairs]
-  GDN_DEV void load(const uint8_t *const (&grp)[2], int lane) {
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int tok = g + 8 * x;
-        uint32_t w[D / 32];
-        float s[D / 64 + 1];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          w[i] = grp[q] ? reinterpret_cast<const uint32_t *>(grp[q] + kv4_k_code<D>(tok, 0))[t * (D / 32) + i] : 0u;
-#pragma unroll
-        for (int i = 0; i < (D == 128 ? 2 : 1); ++i)
-          s[i] = grp[q] ? e4m3_to_f32(grp[q][kv4_k_scale<D>(tok, t * (D == 128 ? 2 : 1) + i)]) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) decode8(w[i], __float2half2_rn(s[i / 2]), a[q][i][x]);
-      }
-  }
+// ---------------------------------------------------------------- many rows: tiles of 128 tokens by 128 rows
+// S^T = K Q^T on tcgen05, a token per lane of tensor memory and a row per column: a
+// thread adds its token's weights over the columns, and nothing crosses lanes. An
+// item is 128 tokens of a sequence and KV head against the tiles of rows (tokens x
+// the KV head's query heads) that see any of them. All items' tiles, in order, are
+// cut into runs of equal cost, one per CTA (one per SM); what a run has of an item
+// that it does not hold whole goes to the workspace and kv4_score_join_kernel adds
+// the pieces in order. Within a CTA:
+//   warps 0..3, 4..7  weights of every other tile: a thread per token
+//   warps 8..11       decode an item's K into the A operand, BF16, exactly
+//   warp 12           TMEM allocation; one thread issues the MMAs
+//   warp 13           streams row tiles by TMA, as they came (BF16, the B operand)
+//   warp 14           the rows' lse in bits, and the last token that each sees
+// What bounds it: one 2^x per (row, token). Every wait is bounded; one that gives up
+// sets GDN_E_TIMEOUT and an abort flag that ends every role's loop.
+constexpr int kTok = 128, kRow = 128;
+constexpr int kTileThreads = 512;
+constexpr int kAccs = 4;          // tiles of sums in tensor memory, 128 columns each
+constexpr int kTileItem = 1;      // what an item costs beside its tiles, in tiles
+
+struct ScoreInfo {  // of a run: what it leaves to be joined
+  int head;         // its first part continues an item: 0 no, 1 and does not end it, 2 and ends it
+  int tail;         // its last part begins an item that it does not end
+  int b, h, kt;     // that item
+};
+struct TileKv4 {
+  Kv4ScoreArgs a;
+  int G, tpt;       // query heads per KV head; tokens of a row tile: 128 / G
+  uint32_t inv_g;   // ceil(2^16 / G): x / G = x inv_g >> 16 for x < 128
+  float c2, skew;
+  float *pieces;    // [runs][head, tail][128]
+  ScoreInfo *info;  // [runs]
 };
 
-constexpr int kRowChunk = 64;   // query rows in shared memory at once
-constexpr int kTokChunk = 256;  // tokens of a CTA
-
-template <int D>
-__global__ void __launch_bounds__(256) kv4_score_kernel(Kv4ScoreArgs p, int chunks, float c2, float skew) {
-  constexpr int KS = D / 16;
-  __shared__ uint2 qsm[kRowChunk / 8][KS][32];
-  __shared__ float row_c[kRowChunk], row_hi[kRowChunk], row_w[kRowChunk];
-  __shared__ int row_last[kRowChunk];
-  kv4_begin();
-  const Kv4Args &c = p.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int chunk = blockIdx.x % chunks, h = blockIdx.x / chunks % c.Hkv, b = blockIdx.x / chunks / c.Hkv;
-  const Kv4Seq s = kv4_seq(c, b);
-  if (chunk * kTokChunk >= s.len) return;
-  const int slot = score_slot(p, b, s.len);
-  if (slot < 0 || slot_twice(p, b, slot, lane)) return;
-  const int G = p.Hq / c.Hkv, n = s.q1 - s.q0, R = n * G;
-  const int pos0 = chunk * kTokChunk + warp * 32;
-  const uint8_t *grp[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    grp[q] = pos0 + q * 16 < s.len ? kv4_group<D>(c, b, pos0 + q * 16) : nullptr;
-    if (grp[q]) grp[q] += h * kv4_head_bytes<D>(c);
+// A sequence's rows and tokens. Its item kt: tokens [128 kt, ...), row tiles [first(kt), tiles).
+struct ScoreSeq {
+  int q0, n, len, tiles, items, tpt;
+  GDN_DEV ScoreSeq(const TileKv4 &p, int b) : tpt(p.tpt) {
+    const Kv4Seq s = kv4_seq(p.a.c, b);
+    q0 = s.q0;
+    n = s.q1 - s.q0;
+    len = s.len;
+    tiles = (int)((unsigned)(n + tpt - 1) / (unsigned)tpt);
+    items = (len + kTok - 1) / kTok;
   }
-  KeyRows<D> k;
-  k.load(grp, lane);
-  float acc[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // tokens g, g + 8 of both groups, this lane's columns
-  for (int row0 = 0; row0 < R; row0 += kRowChunk) {
-    __syncthreads();
-    {  // q: B operand, lane (g, t) = row g of the warp's eight, channels t D/4 ...; scaled to FP16 by a power of two
-      const int row = row0 + warp * 8 + g, tok = row / G;
-      uint4 w[D / 32];
-      const uint16_t *src = p.q + (long long)(s.q0 + tok) * p.q_stride + (long long)(h * G + row - tok * G) * D + t * (D / 4);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) w[i] = row < R ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
-      uint32_t mx = 0;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx = max(mx, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
-      }
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = min(140 - (int)(mx >> 7), 60);
-      const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          y[j] = h2u(__floats2half2_rn(__uint_as_float(x[j] << 16) * sc, __uint_as_float(x[j] & 0xFFFF0000u) * sc));
-        qsm[warp][2 * i][lane] = make_uint2(y[0], y[1]);
-        qsm[warp][2 * i + 1][lane] = make_uint2(y[2], y[3]);
-      }
-      if (t == 0) {
-        const int x = warp * 8 + g;
-        const float lse = row < R ? p.lse[(long long)(s.q0 + tok) * p.Hq + h * G + row - tok * G] : -INFINITY;
-        const RowWeight rw = row_weight(lse, skew);
-        row_c[x] = c2 * __uint_as_float((uint32_t)(127 - e) << 23);
-        row_hi[x] = rw.hi;
-        row_w[x] = rw.w;
-        row_last[x] = lse == -INFINITY ? -1 : s.len - n + tok;
-      }
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int nb = 0; nb < kRowChunk / 8 && row0 + nb * 8 < R; ++nb) {
-      float d[2][4] = {};
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const uint2 qv = qsm[nb][i][lane];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          mma_acc(d[q], k.a[q][i / 2][0][2 * (i & 1)], k.a[q][i / 2][1][2 * (i & 1)], k.a[q][i / 2][0][2 * (i & 1) + 1],
-                  k.a[q][i / 2][1][2 * (i & 1) + 1], qv.x, qv.y);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int x = nb * 8 + 2 * t + e;
-        const float rc = row_c[x], hi = row_hi[x], w = row_w[x];
-        const int last = row_last[x];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            if (pos0 + q * 16 + g + 8 * y <= last) acc[q][y] = fmaf(ex2(fmaf(d[q][2 * y + e], rc, -hi)), w, acc[q][y]);
-      }
-    }
+  GDN_DEV int first(int kt) const {
+    const int row = max(0, kt * kTok - (len - n));  // the first row (token) that sees any of them
+    return (int)((unsigned)row / (unsigned)tpt);
   }
-  const int scored = p.scored ? p.scored[b] : s.len;
-  const size_t row = ((size_t)slot * c.Hkv + h) * p.s.tokens;
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      float v = acc[q][y];
-      v += __shfl_xor_sync(0xffffffffu, v, 1);
-      v += __shfl_xor_sync(0xffffffffu, v, 2);
-      const int pos = pos0 + q * 16 + g + 8 * y;
-      if (t == 0 && pos < s.len) p.s.out[row + pos] = v + (pos < scored ? p.s.in[row + pos] : 0.0f);
+  // The cost of items before kt for a KV head, in tiles x tpt, the tiles before the first one taken as a fraction.
+  GDN_DEV long long cost(int kt) const {
+    const long long o = len - n, k = kt, f = o >= 0 ? o / kTok + 1 : 0;
+    return k * (kTileItem + tiles) * tpt - (k > f ? 64 * (k * (k - 1) - f * (f - 1)) - o * (k - f) : 0);
+  }
+};
+struct ScorePlace {
+  int b, h, kt, r;  // an item, and a tile of it from its first one
+  GDN_DEV bool same_item(const ScorePlace &o) const { return b == o.b && h == o.h && kt == o.kt; }
+};
+// The place at cost u; b = B past the end. total: all items' cost. A whole warp.
+GDN_DEV ScorePlace find_score(const TileKv4 &p, long long u, int lane, long long &total) {
+  const Kv4Args &c = p.a.c;
+  ScorePlace k{c.B, 0, 0, 0};
+  total = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 32) {
+    long long own = 0;
+    if (b0 + lane < c.B) {
+      const ScoreSeq s(p, b0 + lane);
+      own = s.cost(s.items) * c.Hkv;
     }
+    long long incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, total + incl > u);
+    if (k.b == c.B && past) {
+      const int l = __ffs(past) - 1;
+      k.b = b0 + l;
+      long long off = u - total - __shfl_sync(0xffffffffu, incl - own, l);
+      const ScoreSeq s(p, k.b);
+      const long long head = s.cost(s.items);
+      k.h = (int)(off / head);
+      off -= k.h * head;
+      int lo = 0, hi = s.items;  // cost(lo) <= off < cost(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.cost(mid) <= off) lo = mid; else hi = mid;
+      }
+      k.kt = lo;
+      k.r = min(s.tiles - s.first(lo), max(0, (int)((off - s.cost(lo)) / p.tpt) - kTileItem));
+    }
+    total += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return k;
 }
 
-}  // namespace
+// Whether `p` holds for any of the first 256 threads, which all meet here.
+GDN_DEV bool any_of_256(bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)p)
+      : "memory");
+  return any != 0;
+}
 
-size_t kv4_score_bytes(const Kv4ScoreArgs &, int) { return 0; }
+template <int D>
+struct TileShape {
+  static constexpr int kBytesTile = 128 * D * 2;        // 128 tokens of K, and 128 rows
+  static constexpr int kQs = D == 128 ? 4 : 8;          // row tiles on their way
+  static constexpr int kConst = kAccs * kRow * 8;       // (-lse in bits, last token) of a tile's rows
+  static constexpr int kBytes = (2 + kQs) * kBytesTile + kConst + 2 * kTok * 4 + 512;
+  static_assert(kBytes <= 227 * 1024, "one CTA per SM");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const __grid_constant__ CUtensorMap tmQ, TileKv4 p) {
+  using S = TileShape<D>;
+  constexpr int NQ = S::kQs;
+  extern __shared__ __align__(1024) uint8_t sm[];  // the swizzled tiles start on 1024 bytes
+  uint8_t *kbuf = sm, *qbuf = sm + 2 * S::kBytesTile;
+  float *row_hi = reinterpret_cast<float *>(qbuf + NQ * S::kBytesTile);  // [kAccs][128]
+  int *row_last = reinterpret_cast<int *>(row_hi + kAccs * kRow);        // [kAccs][128]
+  float *other = reinterpret_cast<float *>(row_last + kAccs * kRow);     // [2][128]: the second four warps' sums
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(other + 2 * kTok), *k_free = k_full + 2;
+  uint64_t *q_full = k_free + 2, *q_free = q_full + NQ;
+  uint64_t *acc_full = q_free + NQ, *acc_free = acc_full + kAccs, *row_full = acc_free + kAccs, *fin = row_full + kAccs;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(fin + 1);
+  volatile uint32_t *abort_flag = tmem_holder + 1;
+  ScorePlace *ends = reinterpret_cast<ScorePlace *>(tmem_holder + 2);  // [2]
+  const Kv4Args &c = p.a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 128);
+      mbar_init(k_free + i, 1);
+    }
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_free + i, 1);
+    }
+    for (int i = 0; i < kAccs; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_free + i, 128);
+      mbar_init(row_full + i, 32);
+    }
+    mbar_init(fin, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (p.tpt * p.G < kRow) {  // rows that no copy fills: zeros, so that what comes of them is a number
+    for (int i = tid; i < NQ * S::kBytesTile / 16; i += kTileThreads) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
+    fence_async_shared();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  kv4_begin();
+  if (warp < 2) {  // the run's two ends
+    long long total = 0;
+    find_score(p, 0x7fffffffffffffffLL, lane, total);
+    const long long x = blockIdx.x + warp, n = gridDim.x;
+    const ScorePlace k = find_score(p, total / n * x + total % n * x / n, lane, total);
+    if (lane == 0) ends[warp] = k;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const ScorePlace from = ends[0], to = ends[1];
+  auto wait = [&](uint64_t *bar, uint32_t use) { return wait_or_abort(bar, use & 1u, abort_flag, c.status, c.wait); };
+  auto warp_wait_all = [&](uint64_t *bar, uint32_t use) { return __all_sync(0xffffffffu, wait(bar, use)) != 0; };
+  // For each item of the run with what the run has of it: f(place, sequence, the first row tile, one past the last,
+  // whether that is all), until it returns false.
+  auto items = [&](auto f) {
+    ScorePlace k = from;
+    while (k.b < c.B) {
+      const ScoreSeq s(p, k.b);
+      for (; k.h < c.Hkv; ++k.h, k.kt = 0)
+        for (; k.kt < s.items; ++k.kt) {
+          const bool last = k.same_item(to);
+          if (last && to.r == 0) return;
+          const int t0 = s.first(k.kt), all = s.tiles - t0;
+          const int r0 = k.same_item(from) ? from.r : 0, r1 = last ? to.r : all;
+          if (r0 == 0 || r0 < r1) {
+            if (!f(k, s, t0 + r0, t0 + r1, r0 == 0 && r1 == all)) return;
+          }
+          if (last) return;
+        }
+      k.h = 0;
+      ++k.b;
+    }
+  };
+  if (tid == 0) {
+    ScoreInfo x{0, 0, to.b, to.h, to.kt};
+    const bool one = from.same_item(to);
+    if (from.b < c.B && from.r > 0) {
+      const ScoreSeq s(p, from.b);
+      const int all = s.tiles - s.first(from.kt), r1 = one ? to.r : all;
+      if (from.r < r1) x.head = r1 == all ? 2 : 1;
+    }
+    if (to.b < c.B && to.r > 0 && !(one && from.r > 0)) {
+      const ScoreSeq s(p, to.b);
+      if (to.r < s.tiles - s.first(to.kt)) x.tail = 1;
+    }
+    p.info[blockIdx.x] = x;
+  }
+
+  if (warp < 8) {
+    // ------------------------------------------------ weights: thread = token r; tiles u with u % 2 == i
+    const int i = warp >> 2, r = tid & 127;
+    const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t u = 0, it = 0;
+    int at_b = -1, slot = -1, scored = 0;
+    items([&](const ScorePlace &w, const ScoreSeq &s, int t0, int t1, bool whole) {
+      if (w.b != at_b) {
+        at_b = w.b;
+        slot = score_slot(p.a, w.b, s.len);
+        if (slot >= 0 && slot_twice(p.a, w.b, slot, lane)) slot = -1;
+        scored = p.a.scored ? p.a.scored[w.b] : s.len;
+      }
+      const int pos = w.kt * kTok + r;
+      const size_t at = ((size_t)max(slot, 0) * c.Hkv + w.h) * p.a.s.tokens + pos;
+      float old = 0.0f;
+      if (whole && i == 0 && slot >= 0 && pos < min(scored, s.len)) old = p.a.s.in[at];
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      bool ok = true;
+      for (int t = t0; t < t1; ++t, ++u) {
+        if ((int)(u & 1u) != i) continue;
+        const uint32_t a = u % kAccs;
+        ok = warp_wait_all(row_full + a, u / kAccs) && warp_wait_all(acc_full + a, u / kAccs);
+        if (!ok) break;
+        tc_fence_after();
+        // whole tiles: every row sees every token; their rows that are none have hi = infinity
+        const bool mask = (w.kt + 1) * kTok - 1 > s.len - s.n + t * p.tpt || (t + 1) * p.tpt > s.n;
+        const float2 c2 = make_float2(p.c2, p.c2);
+        const float4 *hi = reinterpret_cast<const float4 *>(row_hi + a * kRow);
+        const int4 *last = reinterpret_cast<const int4 *>(row_last + a * kRow);
+        uint32_t x[2][32];
+        tmem_ld32(base + a * kRow, x[0]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          tmem_ld_wait();
+          if (q < 3) tmem_ld32(base + a * kRow + 32 * (q + 1), x[(q + 1) & 1]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 h = hi[q * 8 + e];
+            float2 z0 = fma2(make_float2(__uint_as_float(x[q & 1][4 * e]), __uint_as_float(x[q & 1][4 * e + 1])), c2, make_float2(h.x, h.y));
+            float2 z1 = fma2(make_float2(__uint_as_float(x[q & 1][4 * e + 2]), __uint_as_float(x[q & 1][4 * e + 3])), c2, make_float2(h.z, h.w));
+            z0.x = ex2(z0.x), z0.y = ex2(z0.y), z1.x = ex2(z1.x), z1.y = ex2(z1.y);
+            if (mask) {
+              const int4 l = last[q * 8 + e];
+              z0.x = pos <= l.x ? z0.x : 0.0f;
+              z0.y = pos <= l.y ? z0.y : 0.0f;
+              z1.x = pos <= l.z ? z1.x : 0.0f;
+              z1.y = pos <= l.w ? z1.y : 0.0f;
+            }
+            sum[0] = add2(sum[0], z0);
+            sum[1] = add2(sum[1], z1);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(acc_free + a);
+      }
+      // ---- both halves' sums
+      const float2 v2 = add2(sum[0], sum[1]);
+      float v = v2.x + v2.y;
+      float *mine = other + (it & 1) * kTok;
+      ++it;
+      if (i == 1) mine[r] = v;
+      if (any_of_256(!ok)) return false;  // both halves give up together
+      if (i == 0) {
+        v += mine[r];
+        if (!whole) p.pieces[((size_t)blockIdx.x * 2 + (w.same_item(from) && from.r > 0 ? 0 : 1)) * kTok + r] = v;
+        else if (slot >= 0 && pos < s.len) p.a.s.out[at] = old + v;
+      }
+      return true;
+    });
+  } else if (warp < 12) {
+    // ------------------------------------------------ K: a thread takes 4 times 32 (d = 64: 16) channels of a token
+    const int t0 = tid - 256;
+    constexpr int W = D / 32;  // words of a piece: four pieces a token
+    uint32_t it = 0;
+    items([&](const ScorePlace &w, const ScoreSeq &s, int, int, bool) {
+      const uint32_t st = it & 1;
+      uint8_t *kt = kbuf + st * S::kBytesTile;
+      uint32_t code[4][W], sc[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = (x * 128 + t0) >> 2, part = t0 & 3, pos = w.kt * kTok + row;
+        const uint8_t *g = pos < s.len ? kv4_group<D>(c, w.b, pos) : nullptr;
+        if (g) g += w.h * kv4_head_bytes<D>(c);
+        if constexpr (D == 128) {
+          const uint4 v = g ? *reinterpret_cast<const uint4 *>(g + kv4_k_code<D>(row & 15, part * 16)) : make_uint4(0, 0, 0, 0);
+          code[x][0] = v.x, code[x][1] = v.y, code[x][2 % W] = v.z, code[x][3 % W] = v.w;
+          sc[x] = g ? *reinterpret_cast<const uint16_t *>(g + kv4_k_scale<D>(row & 15, 2 * part)) : 0u;
+        } else {
+          const uint2 v = g ? *reinterpret_cast<const uint2 *>(g + kv4_k_code<D>(row & 15, part * 8)) : make_uint2(0, 0);
+          code[x][0] = v.x, code[x][1] = v.y;
+          sc[x] = g ? g[kv4_k_scale<D>(row & 15, part)] : 0u;
+        }
+      }
+      if (it >= 2 && !warp_wait_all(k_free + st, it / 2 - 1)) return false;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = (x * 128 + t0) >> 2, part = t0 & 3;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const int ww = part * W + j;  // eight channels
+          // an FP16 code moved down 3 bits is the BF16 value 2^-112 times as large; the scale (at most 448) makes that good
+          const float f = e4m3_to_f32(sc[x] >> (8 * (j / 2))) * 5.192296858534828e33f;  // 2^112
+          const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+          __half2 e[4];
+          e2m1x8_to_h2x4(code[x][j], e);
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t v = h2u(e[q]);
+            uint32_t y = ((v >> 3) & 0x0FFF0FFFu) | (v & 0x80008000u);
+            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&y), f2);
+            o[q] = *reinterpret_cast<const uint32_t *>(&z);
+          }
+          *reinterpret_cast<uint4 *>(kt + (ww / 8) * (kTok * 128) + sw_off16(row, (ww & 7) * 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      fence_async_shared();
+      mbar_arrive(k_full + st);
+      ++it;
+      return true;
+    });
+  } else if (warp == 12) {
+    // ------------------------------------------------ MMAs
+    constexpr uint32_t id = idesc_bf16(kRow);
+    constexpr uint64_t kStep = S::kBytesTile / 16;  // from one stage to the next, in a descriptor
+    const uint64_t kd = desc_sw128(smem_u32(kbuf)), qd = desc_sw128(smem_u32(qbuf));
+    const bool me = elect_one();
+    uint32_t u = 0, it = 0;
+    items([&](const ScorePlace &, const ScoreSeq &, int t0, int t1, bool) {
+      bool ok = true;
+      if (me) {
+        ok = wait(k_full + (it & 1), it / 2);
+        for (int t = t0; t < t1 && ok; ++t) {
+          const uint32_t v = u + (t - t0), a = v % kAccs, q = v % NQ;
+          ok = wait(q_full + q, v / NQ) && (v < kAccs || wait(acc_free + a, v / kAccs - 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kk = kd + (uint64_t)(it & 1) * kStep, qq = qd + (uint64_t)q * kStep;
+          const uint32_t d = tmem + a * kRow;
+          mma_f16_ss_c<false>(d, kk, qq, id);
+#pragma unroll
+          for (int k = 1; k < D / 16; ++k)
+            mma_f16_ss_c<true>(d, kk + (k / 4) * (kTok * 128 / 16) + 2 * (k & 3), qq + (k / 4) * (kRow * 128 / 16) + 2 * (k & 3), id);
+          tc_commit(acc_full + a);
+          tc_commit(q_free + q);
+        }
+        if (ok) tc_commit(k_free + (it & 1));
+      }
+      u += t1 - t0;
+      ++it;
+      return __any_sync(0xffffffffu, me && ok) != 0;
+    });
+    // every MMA issued has completed before the CTA may leave
+    if (me) {
+      tc_commit(fin);
+      mbar_wait(fin, 0u);
+    }
+  } else if (warp == 13) {
+    // ------------------------------------------------ row tiles
+    uint32_t u = 0;
+    items([&](const ScorePlace &w, const ScoreSeq &s, int t0, int t1, bool) {
+      bool ok = true;
+      for (int t = t0; t < t1; ++t, ++u) {
+        const uint32_t q = u % NQ;
+        if (u >= NQ && !(ok = warp_wait_all(q_free + q, u / NQ - 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full + q, p.tpt * p.G * D * 2);
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_3d(qbuf + q * S::kBytesTile + x * (kRow * 128), &tmQ, x * 64, w.h * p.G, s.q0 + t * p.tpt, q_full + q);
+        }
+        __syncwarp();
+      }
+      return ok;
+    });
+    // the last copies land (or a bounded wait for each ends) before the CTA leaves, whoever gives up when
+    if (lane == 0)
+      for (uint32_t x = u < NQ ? 0 : u - NQ; x < u; ++x) mbar_wait(q_full + x % NQ, (x / NQ) & 1u);
+  } else if (warp == 14) {
+    // ------------------------------------------------ what the tiles' rows are weighed by
+    uint32_t u = 0;
+    items([&](const ScorePlace &w, const ScoreSeq &s, int t0, int t1, bool) {
+      for (int t = t0; t < t1; ++t, ++u) {
+        const uint32_t a = u % kAccs;
+        float hi[4];
+        int last[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int x = lane + 32 * j, over = (int)(x * p.inv_g >> 16), tok = t * p.tpt + over;
+          const bool have = x < p.tpt * p.G && tok < s.n;
+          const float lse = have ? p.a.lse[(long long)(s.q0 + tok) * p.a.Hq + w.h * p.G + x - over * p.G] : -INFINITY;
+          const bool seen = lse != -INFINITY;
+          hi[j] = seen ? -fmaf(lse, kLog2e, lse * (1.925963e-8f - p.skew * kLog2e)) : -INFINITY;
+          last[j] = seen ? s.len - s.n + tok : -1;
+        }
+        if (u >= kAccs && !warp_wait_all(acc_free + a, u / kAccs - 1)) return false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          row_hi[a * kRow + lane + 32 * j] = hi[j];
+          row_last[a * kRow + lane + 32 * j] = last[j];
+        }
+        mbar_arrive(row_full + a);
+      }
+      return true;
+    });
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// A CTA per run: the item that it begins and does not end, its pieces in order.
+__global__ void __launch_bounds__(kTok) kv4_score_join_kernel(TileKv4 p, int runs) {
+  kv4_begin();
+  const Kv4Args &c = p.a.c;
+  const ScoreInfo x = p.info[blockIdx.x];
+  if (!x.tail) return;
+  const int r = threadIdx.x, pos = x.kt * kTok + r, len = kv4_len(c, x.b);
+  float v = p.pieces[((size_t)blockIdx.x * 2 + 1) * kTok + r];
+  for (int y = blockIdx.x + 1; y < runs; ++y) {
+    const int head = p.info[y].head;
+    if (head) v += p.pieces[(size_t)y * 2 * kTok + r];
+    if (head == 2) break;
+  }
+  const int slot = score_slot(p.a, x.b, len);
+  if (slot < 0 || slot_twice(p.a, x.b, slot, r & 31) || pos >= len) return;
+  const int scored = p.a.scored ? p.a.scored[x.b] : len;
+  const size_t at = ((size_t)slot * c.Hkv + x.h) * p.a.s.tokens + pos;
+  p.a.s.out[at] = v + (pos < scored ? p.a.s.in[at] : 0.0f);
+}
+
+// Rows of one sequence and KV head that a call may have, at most.
+int most_rows(const Kv4ScoreArgs &p) {
+  const Kv4Args &c = p.c;
+  return (c.q_start ? c.T : c.T / c.B) * (p.Hq / c.Hkv);
+}
 
 template <int D, int NQ>
 cudaError_t launch_rows(const Kv4ScoreArgs &p, float c2, float skew, int num_sms, cudaStream_t stream) {
@@ -446,16 +766,45 @@ cudaError_t launch_rows(const Kv4ScoreArgs &p, float c2, float skew, int num_sms
                     32 * kRowWarps, 0, stream, p, c2, skew);
 }
 
-cudaError_t launch_kv4_score(const Kv4ScoreArgs &p, void *, int num_sms, cudaStream_t stream) {
+// CTAs: no more than there can be tiles.
+int tile_runs(const Kv4ScoreArgs &a, int num_sms) {
+  const Kv4Args &c = a.c;
+  const long long tpt = kRow / (a.Hq / c.Hkv), tiles = (c.q_start ? c.T : c.T / c.B) / tpt + 1;
+  const long long items = (long long)c.B * c.Hkv * (((long long)c.cols * c.page_tokens + kTok - 1) / kTok);
+  return (int)(items >= num_sms ? num_sms : std::min((long long)num_sms, items * tiles));
+}
+
+template <int D>
+cudaError_t launch_tile(const TileKv4 &p, int num_sms, cudaStream_t stream) {
+  using S = TileShape<D>;
+  CUtensorMap tmQ;
+  if (!make_heads_map(&tmQ, p.a.q, p.a.c.T, p.a.Hq, D, p.a.q_stride, p.tpt, p.G)) return cudaErrorInvalidValue;
+  static bool allowed[64];
+  cudaError_t e = kv4_allow_smem(kv4_score_tile_kernel<D>, S::kBytes, allowed);
+  if (e != cudaSuccess) return e;
+  const int runs = tile_runs(p.a, num_sms);
+  e = kv4_launch(kv4_score_tile_kernel<D>, runs, kTileThreads, S::kBytes, stream, tmQ, p);
+  if (e != cudaSuccess || runs == 1) return e;
+  return kv4_launch(kv4_score_join_kernel, runs - 1, kTok, 0, stream, p, runs);
+}
+
+}  // namespace
+
+size_t kv4_score_bytes(const Kv4ScoreArgs &p, int num_sms) {
+  return most_rows(p) <= 16 ? 0 : (size_t)tile_runs(p, num_sms) * (2 * kTok * sizeof(float) + sizeof(ScoreInfo));
+}
+
+cudaError_t launch_kv4_score(const Kv4ScoreArgs &p, void *workspace, int num_sms, cudaStream_t stream) {
   const Kv4Args &c = p.c;
   const double exact = (double)p.sm_scale * c.ks * 1.4426950408889634074;  // a score in bits
   const float c2 = (float)exact, skew = (float)(exact / c2 - 1.0);
-  const int R = c.q_start ? 0 : c.T / c.B * (p.Hq / c.Hkv);  // rows per sequence and KV head, where they are known
-  if (!c.q_start && R <= 8) return c.D == 128 ? launch_rows<128, 1>(p, c2, skew, num_sms, stream) : launch_rows<64, 1>(p, c2, skew, num_sms, stream);
-  if (!c.q_start && R <= 16) return c.D == 128 ? launch_rows<128, 2>(p, c2, skew, num_sms, stream) : launch_rows<64, 2>(p, c2, skew, num_sms, stream);
-  const int chunks = (int)(((long long)c.cols * c.page_tokens + kTokChunk - 1) / kTokChunk);
-  return kv4_launch(c.D == 128 ? kv4_score_kernel<128> : kv4_score_kernel<64>, (unsigned)(chunks * c.Hkv * c.B), 256, 0,
-                    stream, p, chunks, c2, skew);
+  const int R = most_rows(p), G = p.Hq / c.Hkv;
+  if (R <= 8) return c.D == 128 ? launch_rows<128, 1>(p, c2, skew, num_sms, stream) : launch_rows<64, 1>(p, c2, skew, num_sms, stream);
+  if (R <= 16) return c.D == 128 ? launch_rows<128, 2>(p, c2, skew, num_sms, stream) : launch_rows<64, 2>(p, c2, skew, num_sms, stream);
+  float *pieces = static_cast<float *>(workspace);
+  const TileKv4 t{p, G, kRow / G, (65536u + G - 1) / G, c2, skew, pieces,
+                  reinterpret_cast<ScoreInfo *>(pieces + (size_t)tile_runs(p, num_sms) * 2 * kTok)};
+  return c.D == 128 ? launch_tile<128>(t, num_sms, stream) : launch_tile<64>(t, num_sms, stream);
 }
 
 }  // namespace gdn

@@ -474,9 +474,12 @@ class KV4Cache:
         if q.dim() == 4:
             self._same_rows(q, batch)
         elif q_start is None:
-            q_start = batch.q_start
             if q.dim() == 3 and q.shape[0] != batch.T:
                 raise ValueError(f"q: {q.shape[0]} rows, but the batch has {batch.T}")
+            if batch.rows is None:
+                q_start = batch.q_start
+            elif batch.rows != 1:                        # as many rows each: a batch of candidates
+                q, lse = (x.unflatten(0, (-1, batch.rows)) for x in (q, lse))
         kv4_score(q, lse, self.layers[layer], batch.block_table, batch.kv_len, self.scores[layer], self.scales[layer][0],
                   q_start=q_start, slots=batch.slots, scored=batch.scored, dev_status=self.status, **kw)
         for s, n in zip(batch.seqs, batch.lens):

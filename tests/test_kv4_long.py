@@ -118,11 +118,17 @@ def test_cache_scores_and_evicts(g, monkeypatch):
     assert batch.scored.tolist() == [30, 50]
     c.score(0, q, lse, batch)
     name, args, kw = calls[-1]
-    assert kw["q_start"] is batch.q_start and kw["scored"] is batch.scored and args[6] == 1.0
+    assert kw["q_start"] is None and kw["scored"] is batch.scored and args[6] == 1.0
     c.score(1, q[:, None], lse[:, None], batch)
     assert calls[-1][2]["q_start"] is None
     with pytest.raises(ValueError, match="rows"):
         c.score(1, q[:1, None], lse[:1, None], batch)
+    batch = c.batch([a, b], [2, 2])
+    c.score(0, torch.zeros(4, 4, 64, dtype=torch.bfloat16), torch.zeros(4, 4), batch)
+    assert calls[-1][1][0].shape == (2, 2, 4, 64) and calls[-1][1][1].shape == (2, 2, 4)
+    batch = c.batch([a, b], [2, 1])
+    c.score(0, torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 4), batch)
+    assert calls[-1][2]["q_start"] is batch.q_start
     batch = c.grow([a, b], [3, 0])                                    # three that are not scored
     with pytest.raises(ValueError, match="no score"):
         c.evict([a, b], 20, recent=2)
@@ -133,7 +139,7 @@ def test_cache_scores_and_evicts(g, monkeypatch):
     assert args[1].tolist() == [before] and args[2].tolist() == [54] and args[3].tolist() == [20] and args[4] == 4
     assert args[6].tolist() == [c.book.pages(a)] and not set(before) & set(c.book.pages(a))
     assert c.grow([a], 1).scored.tolist() == [17]                     # the three newest have none still
-    assert c.evict([b], 31) [0] == [] and len(calls) == 4 + 1
+    assert c.evict([b], 31)[0] == [] and len(calls) == 6 + 1
     c.truncate(b, 10)
     f = c.fork(b)
     assert c.grow([b, f], 0).scored.tolist() == [10, 10]
