@@ -9,6 +9,7 @@
 // head, read once (V is not), and 8 bytes of scores; for a prompt's rows 2 d
 // operations and one 2^x per (row, token).
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "tc.cuh"
@@ -312,12 +313,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
 //   warps 8..11       decode an item's K into the A operand, BF16, exactly
 //   warp 12           TMEM allocation; one thread issues the MMAs
 //   warp 13           streams row tiles by TMA, as they came (BF16, the B operand)
-//   warp 14           the rows' lse in bits, and the last token that each sees
+//   warps 14, 15      the rows' lse in bits, of every other tile
 // What bounds it: one 2^x per (row, token). Every wait is bounded; one that gives up
 // sets GDN_E_TIMEOUT and an abort flag that ends every role's loop.
 constexpr int kTok = 128, kRow = 128;
 constexpr int kTileThreads = 512;
 constexpr int kAccs = 4;          // tiles of sums in tensor memory, 128 columns each
+constexpr int kLses = 8;          // tiles whose rows' lse is in shared memory
 constexpr int kTileItem = 1;      // what an item costs beside its tiles, in tiles
 
 struct ScoreInfo {  // of a run: what it leaves to be joined
@@ -416,7 +418,7 @@ template <int D>
 struct TileShape {
   static constexpr int kBytesTile = 128 * D * 2;        // 128 tokens of K, and 128 rows
   static constexpr int kQs = D == 128 ? 4 : 8;          // row tiles on their way
-  static constexpr int kConst = kAccs * kRow * 8;       // (-lse in bits, last token) of a tile's rows
+  static constexpr int kConst = kLses * kRow * 4;       // -lse in bits of the tiles' rows
   static constexpr int kBytes = (2 + kQs) * kBytesTile + kConst + 2 * kTok * 4 + 512;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
@@ -427,12 +429,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
   constexpr int NQ = S::kQs;
   extern __shared__ __align__(1024) uint8_t sm[];  // the swizzled tiles start on 1024 bytes
   uint8_t *kbuf = sm, *qbuf = sm + 2 * S::kBytesTile;
-  float *row_hi = reinterpret_cast<float *>(qbuf + NQ * S::kBytesTile);  // [kAccs][128]
-  int *row_last = reinterpret_cast<int *>(row_hi + kAccs * kRow);        // [kAccs][128]
-  float *other = reinterpret_cast<float *>(row_last + kAccs * kRow);     // [2][128]: the second four warps' sums
+  float *row_hi = reinterpret_cast<float *>(qbuf + NQ * S::kBytesTile);  // [kLses][128]
+  float *other = row_hi + kLses * kRow;                                  // [2][128]: the second four warps' sums
   uint64_t *k_full = reinterpret_cast<uint64_t *>(other + 2 * kTok), *k_free = k_full + 2;
   uint64_t *q_full = k_free + 2, *q_free = q_full + NQ;
-  uint64_t *acc_full = q_free + NQ, *acc_free = acc_full + kAccs, *row_full = acc_free + kAccs, *fin = row_full + kAccs;
+  uint64_t *acc_full = q_free + NQ, *acc_free = acc_full + kAccs, *row_full = acc_free + kAccs, *row_free = row_full + kLses,
+           *fin = row_free + kLses;
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(fin + 1);
   volatile uint32_t *abort_flag = tmem_holder + 1;
   ScorePlace *ends = reinterpret_cast<ScorePlace *>(tmem_holder + 2);  // [2]
@@ -451,7 +453,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     for (int i = 0; i < kAccs; ++i) {
       mbar_init(acc_full + i, 1);
       mbar_init(acc_free + i, 128);
+    }
+    for (int i = 0; i < kLses; ++i) {
       mbar_init(row_full + i, 32);
+      mbar_init(row_free + i, 128);
     }
     mbar_init(fin, 1);
     *abort_flag = 0u;
@@ -537,40 +542,52 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
       bool ok = true;
       for (int t = t0; t < t1; ++t, ++u) {
         if ((int)(u & 1u) != i) continue;
-        const uint32_t a = u % kAccs;
-        ok = warp_wait_all(row_full + a, u / kAccs) && warp_wait_all(acc_full + a, u / kAccs);
+        const uint32_t a = u % kAccs, e8 = u % kLses;
+        ok = warp_wait_all(row_full + e8, u / kLses) && warp_wait_all(acc_full + a, u / kAccs);
         if (!ok) break;
         tc_fence_after();
         // whole tiles: every row sees every token; their rows that are none have hi = infinity
         const bool mask = (w.kt + 1) * kTok - 1 > s.len - s.n + t * p.tpt || (t + 1) * p.tpt > s.n;
+        const int own = pos - (s.len - s.n) - t * p.tpt;  // the first of the tile's tokens that sees this one
         const float2 c2 = make_float2(p.c2, p.c2);
-        const float4 *hi = reinterpret_cast<const float4 *>(row_hi + a * kRow);
-        const int4 *last = reinterpret_cast<const int4 *>(row_last + a * kRow);
-        uint32_t x[2][32];
-        tmem_ld32(base + a * kRow, x[0]);
+        const float4 *hi = reinterpret_cast<const float4 *>(row_hi + e8 * kRow);
+        auto weigh = [&](auto masked) {
+          uint32_t x[2][32];
+          tmem_ld32(base + a * kRow, x[0]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_ld_wait();
-          if (q < 3) tmem_ld32(base + a * kRow + 32 * (q + 1), x[(q + 1) & 1]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 h = hi[q * 8 + e];
-            float2 z0 = fma2(make_float2(__uint_as_float(x[q & 1][4 * e]), __uint_as_float(x[q & 1][4 * e + 1])), c2, make_float2(h.x, h.y));
-            float2 z1 = fma2(make_float2(__uint_as_float(x[q & 1][4 * e + 2]), __uint_as_float(x[q & 1][4 * e + 3])), c2, make_float2(h.z, h.w));
-            z0.x = ex2(z0.x), z0.y = ex2(z0.y), z1.x = ex2(z1.x), z1.y = ex2(z1.y);
-            if (mask) {
-              const int4 l = last[q * 8 + e];
-              z0.x = pos <= l.x ? z0.x : 0.0f;
-              z0.y = pos <= l.y ? z0.y : 0.0f;
-              z1.x = pos <= l.z ? z1.x : 0.0f;
-              z1.y = pos <= l.w ? z1.y : 0.0f;
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait();
+            if (q < 3) {
+              tmem_ld32(base + a * kRow + 32 * (q + 1), x[(q + 1) & 1]);
+            } else {
+              tc_fence_before();
+              mbar_arrive(acc_free + a);
             }
-            sum[0] = add2(sum[0], z0);
-            sum[1] = add2(sum[1], z1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 h = hi[q * 8 + e];
+              const uint32_t(&y)[32] = x[q & 1];
+              float2 z0 = fma2(make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), c2, make_float2(h.x, h.y));
+              float2 z1 = fma2(make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])), c2, make_float2(h.z, h.w));
+              z0.x = ex2(z0.x), z0.y = ex2(z0.y), z1.x = ex2(z1.x), z1.y = ex2(z1.y);
+              if constexpr (masked()) {  // rows that do not see the token, and those that are none
+                auto sees = [&](int col) {
+                  const int tok = (int)(col * p.inv_g >> 16);
+                  return tok >= own && t * p.tpt + tok < s.n;
+                };
+                z0.x = sees(q * 32 + 4 * e) ? z0.x : 0.0f;
+                z0.y = sees(q * 32 + 4 * e + 1) ? z0.y : 0.0f;
+                z1.x = sees(q * 32 + 4 * e + 2) ? z1.x : 0.0f;
+                z1.y = sees(q * 32 + 4 * e + 3) ? z1.y : 0.0f;
+              }
+              sum[0] = add2(sum[0], z0);
+              sum[1] = add2(sum[1], z1);
+            }
           }
-        }
-        tc_fence_before();
-        mbar_arrive(acc_free + a);
+        };
+        if (mask) weigh(std::true_type{});
+        else weigh(std::false_type{});
+        mbar_arrive(row_free + e8);
       }
       // ---- both halves' sums
       const float2 v2 = add2(sum[0], sum[1]);
@@ -590,44 +607,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     // ------------------------------------------------ K: a thread takes 4 times 32 (d = 64: 16) channels of a token
     const int t0 = tid - 256;
     constexpr int W = D / 32;  // words of a piece: four pieces a token
+    struct Bytes {
+      uint32_t code[4][W], sc[4];
+    };
     uint32_t it = 0;
-    items([&](const ScorePlace &w, const ScoreSeq &s, int, int, bool) {
+    auto convert = [&](const Bytes &x) {
       const uint32_t st = it & 1;
       uint8_t *kt = kbuf + st * S::kBytesTile;
-      uint32_t code[4][W], sc[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = (x * 128 + t0) >> 2, part = t0 & 3, pos = w.kt * kTok + row;
-        const uint8_t *g = pos < s.len ? kv4_group<D>(c, w.b, pos) : nullptr;
-        if (g) g += w.h * kv4_head_bytes<D>(c);
-        if constexpr (D == 128) {
-          const uint4 v = g ? *reinterpret_cast<const uint4 *>(g + kv4_k_code<D>(row & 15, part * 16)) : make_uint4(0, 0, 0, 0);
-          code[x][0] = v.x, code[x][1] = v.y, code[x][2 % W] = v.z, code[x][3 % W] = v.w;
-          sc[x] = g ? *reinterpret_cast<const uint16_t *>(g + kv4_k_scale<D>(row & 15, 2 * part)) : 0u;
-        } else {
-          const uint2 v = g ? *reinterpret_cast<const uint2 *>(g + kv4_k_code<D>(row & 15, part * 8)) : make_uint2(0, 0);
-          code[x][0] = v.x, code[x][1] = v.y;
-          sc[x] = g ? g[kv4_k_scale<D>(row & 15, part)] : 0u;
-        }
-      }
       if (it >= 2 && !warp_wait_all(k_free + st, it / 2 - 1)) return false;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = (x * 128 + t0) >> 2, part = t0 & 3;
+      for (int y = 0; y < 4; ++y) {
+        const int row = (y * 128 + t0) >> 2, part = t0 & 3;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
           const int ww = part * W + j;  // eight channels
           // an FP16 code moved down 3 bits is the BF16 value 2^-112 times as large; the scale (at most 448) makes that good
-          const float f = e4m3_to_f32(sc[x] >> (8 * (j / 2))) * 5.192296858534828e33f;  // 2^112
+          const float f = e4m3_to_f32(x.sc[y] >> (8 * (j / 2))) * 5.192296858534828e33f;  // 2^112
           const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
           __half2 e[4];
-          e2m1x8_to_h2x4(code[x][j], e);
+          e2m1x8_to_h2x4(x.code[y][j], e);
           uint32_t o[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t v = h2u(e[q]);
-            uint32_t y = ((v >> 3) & 0x0FFF0FFFu) | (v & 0x80008000u);
-            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&y), f2);
+            uint32_t b = ((v >> 3) & 0x0FFF0FFFu) | (v & 0x80008000u);
+            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&b), f2);
             o[q] = *reinterpret_cast<const uint32_t *>(&z);
           }
           *reinterpret_cast<uint4 *>(kt + (ww / 8) * (kTok * 128) + sw_off16(row, (ww & 7) * 8)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -637,7 +641,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
       mbar_arrive(k_full + st);
       ++it;
       return true;
+    };
+    auto load = [&](const ScorePlace &w, const ScoreSeq &s, Bytes &x) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int row = (y * 128 + t0) >> 2, part = t0 & 3, pos = w.kt * kTok + row;
+        const uint8_t *g = pos < s.len ? kv4_group<D>(c, w.b, pos) : nullptr;
+        if (g) g += w.h * kv4_head_bytes<D>(c);
+        if constexpr (D == 128) {
+          const uint4 v = g ? *reinterpret_cast<const uint4 *>(g + kv4_k_code<D>(row & 15, part * 16)) : make_uint4(0, 0, 0, 0);
+          x.code[y][0] = v.x, x.code[y][1] = v.y, x.code[y][2 % W] = v.z, x.code[y][3 % W] = v.w;
+          x.sc[y] = g ? *reinterpret_cast<const uint16_t *>(g + kv4_k_scale<D>(row & 15, 2 * part)) : 0u;
+        } else {
+          const uint2 v = g ? *reinterpret_cast<const uint2 *>(g + kv4_k_code<D>(row & 15, part * 8)) : make_uint2(0, 0);
+          x.code[y][0] = v.x, x.code[y][1] = v.y;
+          x.sc[y] = g ? g[kv4_k_scale<D>(row & 15, part)] : 0u;
+        }
+      }
+    };
+    Bytes even, odd;  // an item's bytes are on their way while the one before is decoded
+    int n = 0;
+    bool ok = true;
+    items([&](const ScorePlace &w, const ScoreSeq &s, int, int, bool) {
+      if (n & 1) {
+        load(w, s, odd);
+        ok = convert(even);
+      } else {
+        load(w, s, even);
+        if (n > 0) ok = convert(odd);
+      }
+      ++n;
+      return ok;
     });
+    if (ok && n > 0) {
+      if (n & 1) convert(even);
+      else convert(odd);
+    }
   } else if (warp == 12) {
     // ------------------------------------------------ MMAs
     constexpr uint32_t id = idesc_bf16(kRow);
@@ -695,31 +734,34 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     // the last copies land (or a bounded wait for each ends) before the CTA leaves, whoever gives up when
     if (lane == 0)
       for (uint32_t x = u < NQ ? 0 : u - NQ; x < u; ++x) mbar_wait(q_full + x % NQ, (x / NQ) & 1u);
-  } else if (warp == 14) {
-    // ------------------------------------------------ what the tiles' rows are weighed by
+  } else {
+    // ------------------------------------------------ what the tiles' rows are weighed by: tiles u with u % 2 == warp % 2
     uint32_t u = 0;
     items([&](const ScorePlace &w, const ScoreSeq &s, int t0, int t1, bool) {
-      for (int t = t0; t < t1; ++t, ++u) {
-        const uint32_t a = u % kAccs;
-        float hi[4];
-        int last[4];
+      auto lses = [&](int t, float (&hi)[4]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int x = lane + 32 * j, over = (int)(x * p.inv_g >> 16), tok = t * p.tpt + over;
           const bool have = x < p.tpt * p.G && tok < s.n;
-          const float lse = have ? p.a.lse[(long long)(s.q0 + tok) * p.a.Hq + w.h * p.G + x - over * p.G] : -INFINITY;
-          const bool seen = lse != -INFINITY;
-          hi[j] = seen ? -fmaf(lse, kLog2e, lse * (1.925963e-8f - p.skew * kLog2e)) : -INFINITY;
-          last[j] = seen ? s.len - s.n + tok : -1;
+          hi[j] = have ? p.a.lse[(long long)(s.q0 + tok) * p.a.Hq + w.h * p.G + x - over * p.G] : -INFINITY;
         }
-        if (u >= kAccs && !warp_wait_all(acc_free + a, u / kAccs - 1)) return false;
+      };
+      float next[4];
+      const int mine = t0 + ((u ^ warp) & 1);
+      if (mine < t1) lses(mine, next);
+      for (int t = mine; t < t1; t += 2) {
+        const uint32_t v = u + (t - t0), e8 = v % kLses;
+        float hi[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          row_hi[a * kRow + lane + 32 * j] = hi[j];
-          row_last[a * kRow + lane + 32 * j] = last[j];
-        }
-        mbar_arrive(row_full + a);
+        for (int j = 0; j < 4; ++j)  // a row that saw nothing, or is none, adds nothing
+          hi[j] = next[j] == -INFINITY ? -INFINITY : -fmaf(next[j], kLog2e, next[j] * (1.925963e-8f - p.skew * kLog2e));
+        if (t + 2 < t1) lses(t + 2, next);
+        if (v >= kLses && !warp_wait_all(row_free + e8, v / kLses - 1)) return false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) row_hi[e8 * kRow + lane + 32 * j] = hi[j];
+        mbar_arrive(row_full + e8);
       }
+      u += t1 - t0;
       return true;
     });
   }
