@@ -309,16 +309,20 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
 // cut into runs of equal cost, one per CTA (one per SM); what a run has of an item
 // that it does not hold whole goes to the workspace and kv4_score_join_kernel adds
 // the pieces in order. Within a CTA:
-//   warps 0..3, 4..7  weights of every other tile: a thread per token
-//   warps 8..11       decode an item's K into the A operand, BF16, exactly
-//   warp 12           TMEM allocation; one thread issues the MMAs
-//   warp 13           streams row tiles by TMA, as they came (BF16, the B operand)
-//   warps 14, 15      the rows' lse in bits, of every other tile
+//   warps 0..11       weights, four warps a tile, a thread per token; the exponentials'
+//                     latency wants three tiles at once (two: 225 us instead of 180 below)
+//   warps 12..15      decode an item's K into the A operand in tensor memory, BF16,
+//                     exactly (from shared memory it would take half of its bandwidth)
+//   warp 16           TMEM allocation; one thread issues the MMAs
+//   warp 17           streams row tiles by TMA, as they came (BF16, the B operand)
+//   warps 18, 19      the rows' lse in bits, of every other tile
 // What bounds it: one 2^x per (row, token). Every wait is bounded; one that gives up
 // sets GDN_E_TIMEOUT and an abort flag that ends every role's loop.
 constexpr int kTok = 128, kRow = 128;
-constexpr int kTileThreads = 512;
-constexpr int kAccs = 4;          // tiles of sums in tensor memory, 128 columns each
+constexpr int kAccs = 3;          // tiles of sums in tensor memory, 128 columns each: one for each four warps
+constexpr int kWeigh = 4 * kAccs; // warps
+constexpr int kTileThreads = 32 * (kWeigh + 8);
+constexpr int kKCol = kAccs * kRow;  // TMEM column of the two items' K
 constexpr int kLses = 8;          // tiles whose rows' lse is in shared memory
 constexpr int kTileItem = 1;      // what an item costs beside its tiles, in tiles
 
@@ -400,26 +404,27 @@ GDN_DEV ScorePlace find_score(const TileKv4 &p, long long u, int lane, long long
   return k;
 }
 
-// Whether `p` holds for any of the first 256 threads, which all meet here.
-GDN_DEV bool any_of_256(bool p) {
+// Whether `p` holds for any of the threads that weigh, which all meet here.
+GDN_DEV bool any_weighing(bool p) {
   uint32_t any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(any)
-      : "r"((uint32_t)p)
+      : "r"((uint32_t)p), "n"(32 * kWeigh)
       : "memory");
   return any != 0;
 }
 
 template <int D>
 struct TileShape {
-  static constexpr int kBytesTile = 128 * D * 2;        // 128 tokens of K, and 128 rows
-  static constexpr int kQs = D == 128 ? 4 : 8;          // row tiles on their way
+  static constexpr int kBytesTile = 128 * D * 2;        // 128 rows
+  static constexpr int kQs = D == 128 ? 6 : 8;          // row tiles on their way
+  static_assert(kKCol + 2 * (D / 2) <= 512, "tensor memory");
   static constexpr int kConst = kLses * kRow * 4;       // -lse in bits of the tiles' rows
-  static constexpr int kBytes = (2 + kQs) * kBytesTile + kConst + 2 * kTok * 4 + 512;
+  static constexpr int kBytes = kQs * kBytesTile + kConst + 2 * (kAccs - 1) * kTok * 4 + 512;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
@@ -428,10 +433,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
   using S = TileShape<D>;
   constexpr int NQ = S::kQs;
   extern __shared__ __align__(1024) uint8_t sm[];  // the swizzled tiles start on 1024 bytes
-  uint8_t *kbuf = sm, *qbuf = sm + 2 * S::kBytesTile;
+  uint8_t *qbuf = sm;
   float *row_hi = reinterpret_cast<float *>(qbuf + NQ * S::kBytesTile);  // [kLses][128]
-  float *other = row_hi + kLses * kRow;                                  // [2][128]: the second four warps' sums
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(other + 2 * kTok), *k_free = k_full + 2;
+  float *other = row_hi + kLses * kRow;                                  // [2][kAccs - 1][128]: the other warps' sums
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(other + 2 * (kAccs - 1) * kTok), *k_free = k_full + 2;
   uint64_t *q_full = k_free + 2, *q_free = q_full + NQ;
   uint64_t *acc_full = q_free + NQ, *acc_free = acc_full + kAccs, *row_full = acc_free + kAccs, *row_free = row_full + kLses,
            *fin = row_free + kLses;
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     for (int i = tid; i < NQ * S::kBytesTile / 16; i += kTileThreads) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
     fence_async_shared();
   }
-  if (warp == 12) {
+  if (warp == kWeigh + 4) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -521,9 +526,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     p.info[blockIdx.x] = x;
   }
 
-  if (warp < 8) {
-    // ------------------------------------------------ weights: thread = token r; tiles u with u % 2 == i
-    const int i = warp >> 2, r = tid & 127;
+  if (warp < kWeigh) {
+    // ------------------------------------------------ weights: thread = token r; tiles u with u % kAccs == i
+    const uint32_t i = warp >> 2, r = tid & 127;
     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t u = 0, it = 0;
     int at_b = -1, slot = -1, scored = 0;
@@ -541,8 +546,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
       bool ok = true;
       for (int t = t0; t < t1; ++t, ++u) {
-        if ((int)(u & 1u) != i) continue;
-        const uint32_t a = u % kAccs, e8 = u % kLses;
+        if (u % kAccs != i) continue;
+        const uint32_t a = i, e8 = u % kLses;
         ok = warp_wait_all(row_full + e8, u / kLses) && warp_wait_all(acc_full + a, u / kAccs);
         if (!ok) break;
         tc_fence_after();
@@ -552,21 +557,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
         const float2 c2 = make_float2(p.c2, p.c2);
         const float4 *hi = reinterpret_cast<const float4 *>(row_hi + e8 * kRow);
         auto weigh = [&](auto masked) {
-          uint32_t x[2][32];
-          tmem_ld32(base + a * kRow, x[0]);
+          uint32_t x[2][16];
+          tmem_ld16(base + a * kRow, x[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 8; ++q) {
             tmem_ld_wait();
-            if (q < 3) {
-              tmem_ld32(base + a * kRow + 32 * (q + 1), x[(q + 1) & 1]);
+            if (q < 7) {
+              tmem_ld16(base + a * kRow + 16 * (q + 1), x[(q + 1) & 1]);
             } else {
               tc_fence_before();
               mbar_arrive(acc_free + a);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 h = hi[q * 8 + e];
-              const uint32_t(&y)[32] = x[q & 1];
+            for (int e = 0; e < 4; ++e) {
+              const float4 h = hi[q * 4 + e];
+              const uint32_t(&y)[16] = x[q & 1];
               float2 z0 = fma2(make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), c2, make_float2(h.x, h.y));
               float2 z1 = fma2(make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])), c2, make_float2(h.z, h.w));
               z0.x = ex2(z0.x), z0.y = ex2(z0.y), z1.x = ex2(z1.x), z1.y = ex2(z1.y);
@@ -575,10 +580,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
                   const int tok = (int)(col * p.inv_g >> 16);
                   return tok >= own && t * p.tpt + tok < s.n;
                 };
-                z0.x = sees(q * 32 + 4 * e) ? z0.x : 0.0f;
-                z0.y = sees(q * 32 + 4 * e + 1) ? z0.y : 0.0f;
-                z1.x = sees(q * 32 + 4 * e + 2) ? z1.x : 0.0f;
-                z1.y = sees(q * 32 + 4 * e + 3) ? z1.y : 0.0f;
+                z0.x = sees(q * 16 + 4 * e) ? z0.x : 0.0f;
+                z0.y = sees(q * 16 + 4 * e + 1) ? z0.y : 0.0f;
+                z1.x = sees(q * 16 + 4 * e + 2) ? z1.x : 0.0f;
+                z1.y = sees(q * 16 + 4 * e + 3) ? z1.y : 0.0f;
               }
               sum[0] = add2(sum[0], z0);
               sum[1] = add2(sum[1], z1);
@@ -589,75 +594,73 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
         else weigh(std::false_type{});
         mbar_arrive(row_free + e8);
       }
-      // ---- both halves' sums
+      // ---- all warps' sums
       const float2 v2 = add2(sum[0], sum[1]);
       float v = v2.x + v2.y;
-      float *mine = other + (it & 1) * kTok;
+      float *theirs = other + (it & 1) * (kAccs - 1) * kTok;
       ++it;
-      if (i == 1) mine[r] = v;
-      if (any_of_256(!ok)) return false;  // both halves give up together
+      if (i > 0) theirs[(i - 1) * kTok + r] = v;
+      if (any_weighing(!ok)) return false;  // all give up together
       if (i == 0) {
-        v += mine[r];
+#pragma unroll
+        for (int x = 0; x < kAccs - 1; ++x) v += theirs[x * kTok + r];
         if (!whole) p.pieces[((size_t)blockIdx.x * 2 + (w.same_item(from) && from.r > 0 ? 0 : 1)) * kTok + r] = v;
         else if (slot >= 0 && pos < s.len) p.a.s.out[at] = old + v;
       }
       return true;
     });
-  } else if (warp < 12) {
-    // ------------------------------------------------ K: a thread takes 4 times 32 (d = 64: 16) channels of a token
-    const int t0 = tid - 256;
-    constexpr int W = D / 32;  // words of a piece: four pieces a token
+  } else if (warp < kWeigh + 4) {
+    // ------------------------------------------------ K: a thread per token, 2 BF16 a column
+    const int r = tid & 127;
+    const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kKCol;
+    constexpr int W = D / 8;  // words of eight codes
     struct Bytes {
-      uint32_t code[4][W], sc[4];
+      uint32_t code[W], sc[D / 64];
     };
     uint32_t it = 0;
+    auto load = [&](const ScorePlace &w, const ScoreSeq &s, Bytes &x) {
+      const int pos = w.kt * kTok + r;
+      const uint8_t *g = pos < s.len ? kv4_group<D>(c, w.b, pos) : nullptr;
+      if (g) g += w.h * kv4_head_bytes<D>(c);
+#pragma unroll
+      for (int y = 0; y < W / 4; ++y) {
+        const uint4 v = g ? reinterpret_cast<const uint4 *>(g + kv4_k_code<D>(r & 15, 0))[y] : make_uint4(0, 0, 0, 0);
+        x.code[4 * y] = v.x, x.code[4 * y + 1] = v.y, x.code[4 * y + 2] = v.z, x.code[4 * y + 3] = v.w;
+      }
+#pragma unroll
+      for (int y = 0; y < D / 64; ++y)
+        x.sc[y] = g ? reinterpret_cast<const uint32_t *>(g + kv4_k_scale<D>(r & 15, 0))[y] : 0u;
+    };
     auto convert = [&](const Bytes &x) {
       const uint32_t st = it & 1;
-      uint8_t *kt = kbuf + st * S::kBytesTile;
       if (it >= 2 && !warp_wait_all(k_free + st, it / 2 - 1)) return false;
+      tc_fence_after();
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int row = (y * 128 + t0) >> 2, part = t0 & 3;
+      for (int y = 0; y < W / 4; ++y) {  // 32 channels, 16 columns
+        uint32_t o[16];
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const int ww = part * W + j;  // eight channels
+        for (int j = 0; j < 4; ++j) {
+          const int b = 2 * y + j / 2;  // the block of 16 channels
           // an FP16 code moved down 3 bits is the BF16 value 2^-112 times as large; the scale (at most 448) makes that good
-          const float f = e4m3_to_f32(x.sc[y] >> (8 * (j / 2))) * 5.192296858534828e33f;  // 2^112
+          const float f = e4m3_to_f32(x.sc[b / 4] >> (8 * (b & 3))) * 5.192296858534828e33f;  // 2^112
           const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
           __half2 e[4];
-          e2m1x8_to_h2x4(x.code[y][j], e);
-          uint32_t o[4];
+          e2m1x8_to_h2x4(x.code[4 * y + j], e);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t v = h2u(e[q]);
-            uint32_t b = ((v >> 3) & 0x0FFF0FFFu) | (v & 0x80008000u);
-            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&b), f2);
-            o[q] = *reinterpret_cast<const uint32_t *>(&z);
+            uint32_t u = ((v >> 3) & 0x0FFF0FFFu) | (v & 0x80008000u);
+            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&u), f2);
+            o[4 * j + q] = *reinterpret_cast<const uint32_t *>(&z);
           }
-          *reinterpret_cast<uint4 *>(kt + (ww / 8) * (kTok * 128) + sw_off16(row, (ww & 7) * 8)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        tmem_st16(base + st * (D / 2) + 16 * y, o);
       }
-      fence_async_shared();
+      tmem_st_wait();
+      tc_fence_before();
       mbar_arrive(k_full + st);
       ++it;
       return true;
-    };
-    auto load = [&](const ScorePlace &w, const ScoreSeq &s, Bytes &x) {
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int row = (y * 128 + t0) >> 2, part = t0 & 3, pos = w.kt * kTok + row;
-        const uint8_t *g = pos < s.len ? kv4_group<D>(c, w.b, pos) : nullptr;
-        if (g) g += w.h * kv4_head_bytes<D>(c);
-        if constexpr (D == 128) {
-          const uint4 v = g ? *reinterpret_cast<const uint4 *>(g + kv4_k_code<D>(row & 15, part * 16)) : make_uint4(0, 0, 0, 0);
-          x.code[y][0] = v.x, x.code[y][1] = v.y, x.code[y][2 % W] = v.z, x.code[y][3 % W] = v.w;
-          x.sc[y] = g ? *reinterpret_cast<const uint16_t *>(g + kv4_k_scale<D>(row & 15, 2 * part)) : 0u;
-        } else {
-          const uint2 v = g ? *reinterpret_cast<const uint2 *>(g + kv4_k_code<D>(row & 15, part * 8)) : make_uint2(0, 0);
-          x.code[y][0] = v.x, x.code[y][1] = v.y;
-          x.sc[y] = g ? g[kv4_k_scale<D>(row & 15, part)] : 0u;
-        }
-      }
     };
     Bytes even, odd;  // an item's bytes are on their way while the one before is decoded
     int n = 0;
@@ -677,11 +680,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
       if (n & 1) convert(even);
       else convert(odd);
     }
-  } else if (warp == 12) {
+  } else if (warp == kWeigh + 4) {
     // ------------------------------------------------ MMAs
     constexpr uint32_t id = idesc_bf16(kRow);
     constexpr uint64_t kStep = S::kBytesTile / 16;  // from one stage to the next, in a descriptor
-    const uint64_t kd = desc_sw128(smem_u32(kbuf)), qd = desc_sw128(smem_u32(qbuf));
+    const uint64_t qd = desc_sw128(smem_u32(qbuf));
     const bool me = elect_one();
     uint32_t u = 0, it = 0;
     items([&](const ScorePlace &, const ScoreSeq &, int t0, int t1, bool) {
@@ -693,12 +696,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
           ok = wait(q_full + q, v / NQ) && (v < kAccs || wait(acc_free + a, v / kAccs - 1));
           if (!ok) break;
           tc_fence_after();
-          const uint64_t kk = kd + (uint64_t)(it & 1) * kStep, qq = qd + (uint64_t)q * kStep;
-          const uint32_t d = tmem + a * kRow;
-          mma_f16_ss_c<false>(d, kk, qq, id);
+          const uint64_t qq = qd + (uint64_t)q * kStep;
+          const uint32_t d = tmem + a * kRow, kk = tmem + kKCol + (it & 1) * (D / 2);
+          mma_f16_ts_c<false>(d, kk, qq, id);
 #pragma unroll
           for (int k = 1; k < D / 16; ++k)
-            mma_f16_ss_c<true>(d, kk + (k / 4) * (kTok * 128 / 16) + 2 * (k & 3), qq + (k / 4) * (kRow * 128 / 16) + 2 * (k & 3), id);
+            mma_f16_ts_c<true>(d, kk + 8 * k, qq + (k / 4) * (kRow * 128 / 16) + 2 * (k & 3), id);
           tc_commit(acc_full + a);
           tc_commit(q_free + q);
         }
@@ -713,7 +716,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
       tc_commit(fin);
       mbar_wait(fin, 0u);
     }
-  } else if (warp == 13) {
+  } else if (warp == kWeigh + 5) {
     // ------------------------------------------------ row tiles
     uint32_t u = 0;
     items([&](const ScorePlace &w, const ScoreSeq &s, int t0, int t1, bool) {
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kWeigh + 4) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
