@@ -325,6 +325,7 @@ constexpr int kTileThreads = 32 * (kWeigh + 8);
 constexpr int kKCol = kAccs * kRow;  // TMEM column of the two items' K
 constexpr int kLses = 8;          // tiles whose rows' lse is in shared memory
 constexpr int kTileItem = 1;      // what an item costs beside its tiles, in tiles
+constexpr int kOpen = 4;          // items whose sums are not all there
 
 struct ScoreInfo {  // of a run: what it leaves to be joined
   int head;         // its first part continues an item: 0 no, 1 and does not end it, 2 and ends it
@@ -404,27 +405,13 @@ GDN_DEV ScorePlace find_score(const TileKv4 &p, long long u, int lane, long long
   return k;
 }
 
-// Whether `p` holds for any of the threads that weigh, which all meet here.
-GDN_DEV bool any_weighing(bool p) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"((uint32_t)p), "n"(32 * kWeigh)
-      : "memory");
-  return any != 0;
-}
-
 template <int D>
 struct TileShape {
   static constexpr int kBytesTile = 128 * D * 2;        // 128 rows
   static constexpr int kQs = D == 128 ? 6 : 8;          // row tiles on their way
   static_assert(kKCol + 2 * (D / 2) <= 512, "tensor memory");
   static constexpr int kConst = kLses * kRow * 4;       // -lse in bits of the tiles' rows
-  static constexpr int kBytes = kQs * kBytesTile + kConst + 2 * (kAccs - 1) * kTok * 4 + 512;
+  static constexpr int kBytes = kQs * kBytesTile + kConst + kOpen * kAccs * kTok * 4 + 512;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
@@ -435,11 +422,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
   extern __shared__ __align__(1024) uint8_t sm[];  // the swizzled tiles start on 1024 bytes
   uint8_t *qbuf = sm;
   float *row_hi = reinterpret_cast<float *>(qbuf + NQ * S::kBytesTile);  // [kLses][128]
-  float *other = row_hi + kLses * kRow;                                  // [2][kAccs - 1][128]: the other warps' sums
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(other + 2 * (kAccs - 1) * kTok), *k_free = k_full + 2;
+  float *parts = row_hi + kLses * kRow;                                  // [kOpen][kAccs][128]: each four warps' sums
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(parts + kOpen * kAccs * kTok), *k_free = k_full + 2;
   uint64_t *q_full = k_free + 2, *q_free = q_full + NQ;
   uint64_t *acc_full = q_free + NQ, *acc_free = acc_full + kAccs, *row_full = acc_free + kAccs, *row_free = row_full + kLses,
-           *fin = row_free + kLses;
+           *item_full = row_free + kLses, *item_free = item_full + kOpen, *fin = item_free + kOpen;
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(fin + 1);
   volatile uint32_t *abort_flag = tmem_holder + 1;
   ScorePlace *ends = reinterpret_cast<ScorePlace *>(tmem_holder + 2);  // [2]
@@ -462,6 +449,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     for (int i = 0; i < kLses; ++i) {
       mbar_init(row_full + i, 32);
       mbar_init(row_free + i, 128);
+    }
+    for (int i = 0; i < kOpen; ++i) {
+      mbar_init(item_full + i, 32 * kWeigh);
+      mbar_init(item_free + i, 128);
     }
     mbar_init(fin, 1);
     *abort_flag = 0u;
@@ -532,6 +523,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t u = 0, it = 0;
     int at_b = -1, slot = -1, scored = 0;
+    // The item before the last, where these four warps add its sums up: by then the others' are there.
+    struct {
+      bool on = false;
+      uint32_t it = 0;
+      float old = 0.0f, *dst = nullptr;  // null: goes nowhere
+    } open;
+    auto close = [&]() {
+      const uint32_t e = open.it % kOpen;
+      if (!warp_wait_all(item_full + e, open.it / kOpen)) return false;
+      float v = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kAccs; ++x) v += parts[(e * kAccs + x) * kTok + r];
+      mbar_arrive(item_free + e);
+      if (open.dst) *open.dst = open.old + v;
+      open.on = false;
+      return true;
+    };
     items([&](const ScorePlace &w, const ScoreSeq &s, int t0, int t1, bool whole) {
       if (w.b != at_b) {
         at_b = w.b;
@@ -540,75 +548,90 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
         scored = p.a.scored ? p.a.scored[w.b] : s.len;
       }
       const int pos = w.kt * kTok + r;
-      const size_t at = ((size_t)max(slot, 0) * c.Hkv + w.h) * p.a.s.tokens + pos;
-      float old = 0.0f;
-      if (whole && i == 0 && slot >= 0 && pos < min(scored, s.len)) old = p.a.s.in[at];
+      const bool mine = it % kAccs == i;  // these four warps close the item
+      float old = 0.0f, *dst = nullptr;
+      if (mine) {
+        const size_t at = ((size_t)max(slot, 0) * c.Hkv + w.h) * p.a.s.tokens + pos;
+        if (!whole) {
+          dst = p.pieces + ((size_t)blockIdx.x * 2 + (w.same_item(from) && from.r > 0 ? 0 : 1)) * kTok + r;
+        } else if (slot >= 0 && pos < s.len) {
+          dst = p.a.s.out + at;
+          if (pos < scored) old = p.a.s.in[at];
+        }
+      }
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      bool ok = true;
       for (int t = t0; t < t1; ++t, ++u) {
         if (u % kAccs != i) continue;
-        const uint32_t a = i, e8 = u % kLses;
-        ok = warp_wait_all(row_full + e8, u / kLses) && warp_wait_all(acc_full + a, u / kAccs);
-        if (!ok) break;
+        const uint32_t e8 = u % kLses;
+        if (!warp_wait_all(row_full + e8, u / kLses) || !warp_wait_all(acc_full + i, u / kAccs)) return false;
         tc_fence_after();
         // whole tiles: every row sees every token; their rows that are none have hi = infinity
         const bool mask = (w.kt + 1) * kTok - 1 > s.len - s.n + t * p.tpt || (t + 1) * p.tpt > s.n;
         const int own = pos - (s.len - s.n) - t * p.tpt;  // the first of the tile's tokens that sees this one
         const float2 c2 = make_float2(p.c2, p.c2);
         const float4 *hi = reinterpret_cast<const float4 *>(row_hi + e8 * kRow);
-        auto weigh = [&](auto masked) {
-          uint32_t x[2][16];
-          tmem_ld16(base + a * kRow, x[0]);
+        const uint32_t acc = base + i * kRow;
+        auto weigh = [&](const uint32_t(&y)[16], int q, auto masked) {  // columns 16 q ..
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 h = hi[q * 4 + e];
+            float2 z0 = fma2(make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), c2, make_float2(h.x, h.y));
+            float2 z1 = fma2(make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])), c2, make_float2(h.z, h.w));
+            z0.x = ex2(z0.x), z0.y = ex2(z0.y), z1.x = ex2(z1.x), z1.y = ex2(z1.y);
+            if constexpr (masked()) {  // rows that do not see the token, and those that are none
+              auto sees = [&](int col) {
+                const int tok = (int)(col * p.inv_g >> 16);
+                return tok >= own && t * p.tpt + tok < s.n;
+              };
+              z0.x = sees(q * 16 + 4 * e) ? z0.x : 0.0f;
+              z0.y = sees(q * 16 + 4 * e + 1) ? z0.y : 0.0f;
+              z1.x = sees(q * 16 + 4 * e + 2) ? z1.x : 0.0f;
+              z1.y = sees(q * 16 + 4 * e + 3) ? z1.y : 0.0f;
+            }
+            sum[0] = add2(sum[0], z0);
+            sum[1] = add2(sum[1], z1);
+          }
+        };
+        uint32_t x[2][16];
+        tmem_ld16(acc, x[0]);
+        if (mask) {
+#pragma unroll 1
+          for (int q = 0; q < 8; q += 2) {
+            tmem_ld_wait();
+            tmem_ld16(acc + 16 * (q + 1), x[1]);
+            weigh(x[0], q, std::true_type{});
+            tmem_ld_wait();
+            if (q < 6) tmem_ld16(acc + 16 * (q + 2), x[0]);
+            weigh(x[1], q + 1, std::true_type{});
+          }
+        } else {
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             tmem_ld_wait();
-            if (q < 7) {
-              tmem_ld16(base + a * kRow + 16 * (q + 1), x[(q + 1) & 1]);
-            } else {
-              tc_fence_before();
-              mbar_arrive(acc_free + a);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 h = hi[q * 4 + e];
-              const uint32_t(&y)[16] = x[q & 1];
-              float2 z0 = fma2(make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), c2, make_float2(h.x, h.y));
-              float2 z1 = fma2(make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])), c2, make_float2(h.z, h.w));
-              z0.x = ex2(z0.x), z0.y = ex2(z0.y), z1.x = ex2(z1.x), z1.y = ex2(z1.y);
-              if constexpr (masked()) {  // rows that do not see the token, and those that are none
-                auto sees = [&](int col) {
-                  const int tok = (int)(col * p.inv_g >> 16);
-                  return tok >= own && t * p.tpt + tok < s.n;
-                };
-                z0.x = sees(q * 16 + 4 * e) ? z0.x : 0.0f;
-                z0.y = sees(q * 16 + 4 * e + 1) ? z0.y : 0.0f;
-                z1.x = sees(q * 16 + 4 * e + 2) ? z1.x : 0.0f;
-                z1.y = sees(q * 16 + 4 * e + 3) ? z1.y : 0.0f;
-              }
-              sum[0] = add2(sum[0], z0);
-              sum[1] = add2(sum[1], z1);
-            }
+            if (q < 7) tmem_ld16(acc + 16 * (q + 1), x[(q + 1) & 1]);
+            weigh(x[q & 1], q, std::false_type{});
           }
-        };
-        if (mask) weigh(std::true_type{});
-        else weigh(std::false_type{});
+        }
+        tc_fence_before();
+        mbar_arrive(acc_free + i);
         mbar_arrive(row_free + e8);
       }
-      // ---- all warps' sums
-      const float2 v2 = add2(sum[0], sum[1]);
-      float v = v2.x + v2.y;
-      float *theirs = other + (it & 1) * (kAccs - 1) * kTok;
-      ++it;
-      if (i > 0) theirs[(i - 1) * kTok + r] = v;
-      if (any_weighing(!ok)) return false;  // all give up together
-      if (i == 0) {
-#pragma unroll
-        for (int x = 0; x < kAccs - 1; ++x) v += theirs[x * kTok + r];
-        if (!whole) p.pieces[((size_t)blockIdx.x * 2 + (w.same_item(from) && from.r > 0 ? 0 : 1)) * kTok + r] = v;
-        else if (slot >= 0 && pos < s.len) p.a.s.out[at] = old + v;
+      const float2 v = add2(sum[0], sum[1]);
+      const uint32_t e = it % kOpen;
+      if (it >= kOpen && !warp_wait_all(item_free + e, it / kOpen - 1)) return false;
+      parts[(e * kAccs + i) * kTok + r] = v.x + v.y;
+      mbar_arrive(item_full + e);
+      if (open.on && !close()) return false;
+      if (mine) {
+        open.on = true;
+        open.it = it;
+        open.old = old;
+        open.dst = dst;
       }
+      ++it;
       return true;
     });
+    if (open.on) close();
   } else if (warp < kWeigh + 4) {
     // ------------------------------------------------ K: a thread per token, 2 BF16 a column
     const int r = tid & 127;
