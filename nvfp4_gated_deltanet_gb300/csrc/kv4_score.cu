@@ -405,13 +405,23 @@ GDN_DEV ScorePlace find_score(const TileKv4 &p, long long u, int lane, long long
   return k;
 }
 
+// Asynchronous copies of B bytes by the thread for itself; the rest of them, from `have` on, becomes zeros.
+template <int B>
+GDN_DEV void async_copy(void *dst, const void *src, int have) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(B), "r"(have) : "memory");
+}
+GDN_DEV void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+GDN_DEV void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 template <int D>
 struct TileShape {
   static constexpr int kBytesTile = 128 * D * 2;        // 128 rows
   static constexpr int kQs = D == 128 ? 6 : 8;          // row tiles on their way
   static_assert(kKCol + 2 * (D / 2) <= 512, "tensor memory");
+  static constexpr int kToken = D / 2 + 16;             // a token's K bytes as they come: an odd number of 16-byte words
   static constexpr int kConst = kLses * kRow * 4;       // -lse in bits of the tiles' rows
-  static constexpr int kBytes = kQs * kBytesTile + kConst + kOpen * kAccs * kTok * 4 + 512;
+  static constexpr int kBytes = kQs * kBytesTile + kConst + kOpen * kAccs * kTok * 4 + 2 * kTok * kToken + 512;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
@@ -423,7 +433,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
   uint8_t *qbuf = sm;
   float *row_hi = reinterpret_cast<float *>(qbuf + NQ * S::kBytesTile);  // [kLses][128]
   float *parts = row_hi + kLses * kRow;                                  // [kOpen][kAccs][128]: each four warps' sums
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(parts + kOpen * kAccs * kTok), *k_free = k_full + 2;
+  uint8_t *kbytes = reinterpret_cast<uint8_t *>(parts + kOpen * kAccs * kTok);  // [2][128][kToken]
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(kbytes + 2 * kTok * S::kToken), *k_free = k_full + 2;
   uint64_t *q_full = k_free + 2, *q_free = q_full + NQ;
   uint64_t *acc_full = q_free + NQ, *acc_free = acc_full + kAccs, *row_full = acc_free + kAccs, *row_free = row_full + kLses,
            *item_full = row_free + kLses, *item_free = item_full + kOpen, *fin = item_free + kOpen;
@@ -637,38 +648,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     const int r = tid & 127;
     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kKCol;
     constexpr int W = D / 8;  // words of eight codes
-    struct Bytes {
-      uint32_t code[W], sc[D / 64];
-    };
+    // A token's bytes go to shared memory two items ahead, by and for its own thread. (Loops are kept short: the roles'
+    // code, all of it in use at once, has to fit the instruction caches.)
+    uint8_t *mine = kbytes + r * S::kToken;
     uint32_t it = 0;
-    auto load = [&](const ScorePlace &w, const ScoreSeq &s, Bytes &x) {
-      const int pos = w.kt * kTok + r;
-      const uint8_t *g = pos < s.len ? kv4_group<D>(c, w.b, pos) : nullptr;
-      if (g) g += w.h * kv4_head_bytes<D>(c);
-#pragma unroll
-      for (int y = 0; y < W / 4; ++y) {
-        const uint4 v = g ? reinterpret_cast<const uint4 *>(g + kv4_k_code<D>(r & 15, 0))[y] : make_uint4(0, 0, 0, 0);
-        x.code[4 * y] = v.x, x.code[4 * y + 1] = v.y, x.code[4 * y + 2] = v.z, x.code[4 * y + 3] = v.w;
-      }
-#pragma unroll
-      for (int y = 0; y < D / 64; ++y)
-        x.sc[y] = g ? reinterpret_cast<const uint32_t *>(g + kv4_k_scale<D>(r & 15, 0))[y] : 0u;
-    };
-    auto convert = [&](const Bytes &x) {
+    auto convert = [&](uint32_t it) {
       const uint32_t st = it & 1;
+      const uint8_t *src = mine + st * (kTok * S::kToken);
       if (it >= 2 && !warp_wait_all(k_free + st, it / 2 - 1)) return false;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int y = 0; y < W / 4; ++y) {  // 32 channels, 16 columns
+        const uint4 v4 = *reinterpret_cast<const uint4 *>(src + 16 * y);
+        const uint32_t code[4] = {v4.x, v4.y, v4.z, v4.w}, sc = *reinterpret_cast<const uint16_t *>(src + D / 2 + 2 * y);
         uint32_t o[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int b = 2 * y + j / 2;  // the block of 16 channels
           // an FP16 code moved down 3 bits is the BF16 value 2^-112 times as large; the scale (at most 448) makes that good
-          const float f = e4m3_to_f32(x.sc[b / 4] >> (8 * (b & 3))) * 5.192296858534828e33f;  // 2^112
+          const float f = e4m3_to_f32(sc >> (8 * (j / 2))) * 5.192296858534828e33f;  // 2^112
           const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
           __half2 e[4];
-          e2m1x8_to_h2x4(x.code[4 * y + j], e);
+          e2m1x8_to_h2x4(code[j], e);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t v = h2u(e[q]);
@@ -682,27 +682,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(k_full + st);
-      ++it;
       return true;
     };
-    Bytes even, odd;  // an item's bytes are on their way while the one before is decoded
-    int n = 0;
     bool ok = true;
     items([&](const ScorePlace &w, const ScoreSeq &s, int, int, bool) {
-      if (n & 1) {
-        load(w, s, odd);
-        ok = convert(even);
-      } else {
-        load(w, s, even);
-        if (n > 0) ok = convert(odd);
+      const int pos = w.kt * kTok + r;
+      const uint8_t *g = pos < s.len ? kv4_group<D>(c, w.b, pos) : nullptr;
+      const int have = g ? 16 : 0;  // none: zeros
+      g = (g ? g + w.h * kv4_head_bytes<D>(c) : c.pages);
+      uint8_t *dst = mine + (it & 1) * (kTok * S::kToken);
+#pragma unroll
+      for (int y = 0; y < W / 4; ++y) async_copy<16>(dst + 16 * y, g + kv4_k_code<D>(r & 15, 0) + 16 * y, have);
+      async_copy<D / 16>(dst + D / 2, g + kv4_k_scale<D>(r & 15, 0), min(have, D / 16));
+      async_commit();
+      if (it > 0) {
+        async_wait<1>();
+        ok = convert(it - 1);
       }
-      ++n;
+      ++it;
       return ok;
     });
-    if (ok && n > 0) {
-      if (n & 1) convert(even);
-      else convert(odd);
-    }
+    async_wait<0>();
+    if (ok && it > 0) convert(it - 1);
   } else if (warp == kWeigh + 4) {
     // ------------------------------------------------ MMAs
     constexpr uint32_t id = idesc_bf16(kRow);
