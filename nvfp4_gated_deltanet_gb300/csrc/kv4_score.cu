@@ -353,8 +353,8 @@ struct ScoreSeq {
     items = (len + kTok - 1) / kTok;
   }
   GDN_DEV int first(int kt) const {
-    const int row = max(0, kt * kTok - (len - n));  // the first row (token) that sees any of them
-    return (int)((unsigned)row / (unsigned)tpt);
+    const int row = kt * kTok - (len - n);  // the first row (token) that sees any of them
+    return row > 0 ? (int)((unsigned)row / (unsigned)tpt) : 0;
   }
   // The cost of items before kt for a KV head, in tiles x tpt, the tiles before the first one taken as a fraction.
   GDN_DEV long long cost(int kt) const {
