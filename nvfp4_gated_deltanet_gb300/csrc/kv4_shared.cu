@@ -164,17 +164,22 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
 //   warps 0..3, 4..7  one row per thread: its query in FP16 (scaled by a power of
 //                     two) to shared memory, then softmax of row tile 0 / 1, the
 //                     weights back into tensor memory; the row's sums
-//   warps 8..11       decode a tile from its 4-bit bytes into the MMAs' operands
-//   warp 12           TMEM allocation; one thread issues the MMAs
-//   warp 13           streams the cached bytes by bulk copies
-// A thread holds its row's 128 scores: the softmax warps take over registers
-// (184, 96 and 48 of 128 each). K and V are exact in FP16 (six significant bits).
+//   warps 8..11       decode a tile's K from its 4-bit bytes into the MMAs' operand
+//   warps 12..15      decode its V
+//   warp 16           TMEM allocation; one thread issues the MMAs
+//   warp 17           streams the cached bytes by bulk copies
+// The softmax warps take over registers (152, 64 and 48 of 96 each), enough for half
+// of a row's 128 scores at a time, which are read from tensor memory twice (with all
+// of them in registers there is room for four decoding warps only, a warp on each
+// scheduler, which then take 5000 cycles a tile: 140 us instead of 95 for 1024 rows
+// of each of 4 KV heads on 65536 tokens). K and V are exact in FP16 (six significant
+// bits).
 // The weights are 2^(z - m + 6), with a maximum m that is only moved (and O
 // rescaled in tensor memory) when the row's true maximum passes it by 8.
 // Every wait is bounded; one that gives up sets GDN_E_TIMEOUT and an abort flag
 // that ends every role's loop.
 constexpr int kKv = 128;
-constexpr int kPrefixThreads = 512;
+constexpr int kPrefixThreads = 640;
 constexpr float kShift = 6.0f, kSlack = 8.0f;
 // What an item costs beside its tiles, in tiles: its queries, its sums and their joining.
 constexpr int kItemCost = 2;
@@ -297,13 +302,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(raw_full + s, 1);
-      mbar_init(raw_free + s, 4);
+      mbar_init(raw_free + s, 8);
     }
     mbar_init(fin, 1);
     *abort_flag = 0u;
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -340,9 +345,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
     }
   };
 
-  // registers: 512 threads x 128 at launch = 256 x 184 + 128 x 96 + 128 x 48
+  // registers: 640 threads x 96 at launch = 256 x 152 + 256 x 64 + 128 x 48
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     // ------------------------------------------------ softmax: thread = row r of row tile i
     const int i = warp >> 2, r = tid & 127;
     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -387,25 +392,28 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
         if (!warp_wait_all(s_full + i, uses)) return false;
         tc_fence_after();
         const int valid = w.S - (w.tile + j) * kKv;  // tokens of this tile
-        float s[128];
-        {
-          uint32_t x[128];
+        auto half_scores = [&](int half, float (&s)[64]) {
+          uint32_t x[64];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, x + 32 * q);
+          for (int q = 0; q < 2; ++q) tmem_ld32(tS + 64 * half + 32 * q, x + 32 * q);
           tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 128; ++q) s[q] = __uint_as_float(x[q]);
+          for (int q = 0; q < 64; ++q) s[q] = __uint_as_float(x[q]);
           if (valid < kKv) {
 #pragma unroll
-            for (int q = 0; q < 128; ++q)
-              if (q >= valid) s[q] = -INFINITY;
+            for (int q = 0; q < 64; ++q)
+              if (64 * half + q >= valid) s[q] = -INFINITY;
           }
+        };
+        float s[64], x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // the second stays in s
+          half_scores(half, s);
+#pragma unroll
+          for (int q = 0; q < 64; q += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
         }
-        float x4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int q = 4; q < 128; q += 4)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
         const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * cs;
         const bool up = top > m + kSlack;  // decided row by row: a row's result depends on no other row
         if (j == 0) {
@@ -428,23 +436,28 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
         const float off = kShift - (m == -INFINITY ? 0.0f : m);
         const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
         float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
-        auto weigh = [&](int half) {
-          uint32_t x[32];
+        auto weigh = [&](const float (&s)[64], uint32_t (&x)[32]) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float2 z = fma2(make_float2(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]), cs2, off2);
+            float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), cs2, off2);
             z.x = ex2(z.x);
             z.y = ex2(z.y);
             sum[e & 1] = add2(sum[e & 1], z);
             x[e] = h2u(__floats2half2_rn(z.x, z.y));
           }
+        };
+        auto put = [&](int half, const uint32_t (&x)[32]) {
           tmem_st32(tS + 64 + 32 * half, x);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(p_ready + 2 * i + half);
         };
-        weigh(1);
-        weigh(0);
+        uint32_t x[32];
+        weigh(s, x);  // tokens 64 ..: weights in columns 96 .., which only they held
+        put(1, x);
+        half_scores(0, s);
+        weigh(s, x);
+        put(0, x);
         sum[0] = add2(sum[0], sum[1]);
         l = sum[0].x + sum[0].y;
       }
@@ -480,41 +493,37 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
       }
       return true;
     });
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    // ------------------------------------------------ 4-bit bytes into the operands
-    const int t0 = tid - 256;
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // ------------------------------------------------ 4-bit bytes into the operands: four warps for K, four for V
+    const bool values = warp >= 12;
+    const int t0 = tid & 127;
+    uint64_t *full = values ? v_full : k_full, *free = values ? v_free : k_free;
     uint32_t u = 0;  // tiles
     segments([&](int, const Place &w, int n) {
       for (int j = 0; j < n; ++j, ++u) {
         const uint32_t s = u % NS;
         const int valid = w.S - (w.tile + j) * kKv;
-        uint8_t *kt = kbuf + s * S::kTileBytes, *vt = vbuf + s * S::kTileBytes;
-        if (u >= NS && !warp_wait_all(k_free + s, u / NS - 1)) return false;
-#pragma unroll
+        if (u >= NS && !warp_wait_all(free + s, u / NS - 1)) return false;
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const uint32_t x = 2 * u + half;
           if (!warp_wait_all(raw_full + x % NR, x / NR)) return false;
           const uint8_t *rb = raw + x % NR * S::kRaw;
+          if (!values) {
+            uint8_t *kt = kbuf + s * S::kTileBytes;
 #pragma unroll
-          for (int i = t0; i < 64 * (D / 8); i += 128) {  // K: eight channels of one token
-            const int row = i / (D / 8), ww = i % (D / 8);
-            const uint8_t *g = rb + row / 16 * S::kGroup;
-            const __half2 sc = __float2half2_rn(e4m3_to_f32(g[S::kGap + kv4_k_scale<D>(row & 15, ww / 2)]));
-            uint32_t o[4];
-            decode8(*reinterpret_cast<const uint32_t *>(g + kv4_k_code<D>(row & 15, ww * 4)), sc, o);
-            *reinterpret_cast<uint4 *>(kt + (ww / 8) * (kKv * 128) + sw_off16(half * 64 + row, (ww & 7) * 8)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        }
-        fence_async_shared();
-        mbar_arrive(k_full + s);
-        if (u >= NS && !warp_wait_all(v_free + s, u / NS - 1)) return false;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t x = 2 * u + half;
-          const uint8_t *rb = raw + x % NR * S::kRaw;
-          if (t0 < D) {  // V^T: eight tokens of eight channels; eight neighbouring lanes write a whole 128-byte row
+            for (int i = t0; i < 64 * (D / 8); i += 128) {  // eight channels of one token
+              const int row = i / (D / 8), ww = i % (D / 8);
+              const uint8_t *g = rb + row / 16 * S::kGroup;
+              const __half2 sc = __float2half2_rn(e4m3_to_f32(g[S::kGap + kv4_k_scale<D>(row & 15, ww / 2)]));
+              uint32_t o[4];
+              decode8(*reinterpret_cast<const uint32_t *>(g + kv4_k_code<D>(row & 15, ww * 4)), sc, o);
+              *reinterpret_cast<uint4 *>(kt + (ww / 8) * (kKv * 128) + sw_off16(half * 64 + row, (ww & 7) * 8)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          } else if (t0 < D) {  // V^T: eight tokens of eight channels; eight neighbouring lanes write a whole 128-byte row
+            uint8_t *vt = vbuf + s * S::kTileBytes;
             const int oct = t0 & 7, ww = t0 >> 3, hi = oct & 1;
             const uint8_t *g = rb + (oct >> 1) * S::kGroup;
             const uint8_t *codes = g + hi * S::kGap;  // tokens 8 .. 15 lie in the second half
@@ -541,13 +550,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
           if (lane == 0) mbar_arrive(raw_free + x % NR);
         }
         fence_async_shared();
-        mbar_arrive(v_full + s);
+        mbar_arrive(full + s);
       }
       return true;
     });
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 12) {
+    if (warp == 16) {
       // ------------------------------------------------ MMAs
       constexpr uint32_t idS = idesc_f16(kKv), idO = idesc_f16(D);
       constexpr uint64_t kStep = S::kTileBytes / 16;  // from one stage or tile to the next, in a descriptor
@@ -614,7 +623,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
         tc_commit(fin);
         mbar_wait(fin, 0u);
       }
-    } else if (warp == 13) {
+    } else if (warp == 17) {
       // ------------------------------------------------ the cached bytes, 64 tokens at a time: a lane per group
       uint32_t x = 0;
       segments([&](int, const Place &w, int n) {
@@ -645,7 +654,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
