@@ -421,7 +421,10 @@ struct TileShape {
   static_assert(kKCol + 2 * (D / 2) <= 512, "tensor memory");
   static constexpr int kToken = D / 2 + 16;             // a token's K bytes as they come: an odd number of 16-byte words
   static constexpr int kConst = kLses * kRow * 4;       // -lse in bits of the tiles' rows
-  static constexpr int kBytes = kQs * kBytesTile + kConst + kOpen * kAccs * kTok * 4 + 2 * kTok * kToken + 512;
+  // the barriers, then the tensor memory's address and the abort flag, the run's ends
+  static constexpr int kBars = 512, kBarriers = 4 + 2 * kQs + 2 * kAccs + 2 * kLses + 2 * kOpen + 1;
+  static_assert(kBarriers * 8 + 8 + 2 * sizeof(ScorePlace) <= kBars, "barriers");
+  static constexpr int kBytes = kQs * kBytesTile + kConst + kOpen * kAccs * kTok * 4 + 2 * kTok * kToken + kBars;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 

@@ -188,14 +188,12 @@ template <int D>
 struct PrefixShape {
   static constexpr int kStages = D == 128 ? 2 : 4;      // of K and of V each
   static constexpr int kTileBytes = kKv * D * 2;        // a K tile, a V tile, and 128 query rows
-  // 64 tokens' bytes as they come: a group's second half begins 64 bytes late and groups lie 4 words apart modulo
-  // 32, so that the eight octets of tokens whose words a warp reads together lie on different banks
-  static constexpr int kFirst = 12 * D, kGap = 64, kGroup = 18 * D + 144;
-  static constexpr int kRaw = 4 * kGroup, kRaws = D == 128 ? 3 : 8;
-  static constexpr int kBars = 512;
+  static constexpr int kRaw = 4 * 18 * D, kRaws = D == 128 ? 3 : 6;  // 64 tokens' bytes as they come
+  // the barriers, then the tensor memory's address and the abort flag, the run's first place, its ends
+  static constexpr int kBarriers = 4 * kStages + 10 + 2 * kRaws + 1, kBars = 512;
+  static_assert(kBarriers * 8 + 8 + 40 + 16 <= kBars, "barriers");
   static constexpr int kBytes = (2 + 2 * kStages) * kTileBytes + kRaws * kRaw + kBars;
   static constexpr int kO = 2 * kKv;                    // TMEM columns: S0, S1, then O0, O1
-  static_assert((kGroup / 4) % 32 == 4 && kGroup % 16 == 0, "banks");
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
@@ -229,6 +227,7 @@ struct Place {
     group(p, at);
   }
 };
+static_assert(sizeof(Place) == 40, "what the prefix kernel's shared memory has for it");
 // The tile at cost u (an item's own cost comes before its tiles), and how many tiles
 // lie before it; past the end only the number. total: all items' cost. A whole warp.
 GDN_DEV long long find_place(const SharedKv4 &p, long long u, int lane, Place &k, long long &total) {
@@ -495,11 +494,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
     });
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    // ------------------------------------------------ 4-bit bytes into the operands: four warps for K, four for V
+    // ------------------------------------------------ 4-bit bytes into the operands: four warps for K, four for V.
+    // Both as they lie, a token's channels in a row: K is the product's B operand with the summed index (channels)
+    // along the rows, V with the summed index (tokens) across them.
     const bool values = warp >= 12;
-    const int t0 = tid & 127;
+    const int t0 = tid & 127, r0 = t0 / (D / 8), ww = t0 % (D / 8);  // eight channels of rows r0, r0 + 1024 / D, ... of 64
+    constexpr int N = D / 16, STEP = 1024 / D;
     uint64_t *full = values ? v_full : k_full, *free = values ? v_free : k_free;
-    uint32_t u = 0;  // tiles
+    uint8_t *tiles = (values ? vbuf : kbuf) + (ww / 8) * (kKv * 128);
+    uint32_t u = 0;
     segments([&](int, const Place &w, int n) {
       for (int j = 0; j < n; ++j, ++u) {
         const uint32_t s = u % NS;
@@ -510,41 +513,28 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
           const uint32_t x = 2 * u + half;
           if (!warp_wait_all(raw_full + x % NR, x / NR)) return false;
           const uint8_t *rb = raw + x % NR * S::kRaw;
-          if (!values) {
-            uint8_t *kt = kbuf + s * S::kTileBytes;
+          uint8_t *dst = tiles + s * S::kTileBytes + half * (64 * 128);
+          uint32_t code[N];
+          uint8_t sc[N];
+          // (V's rows lie in another order: the row's token)
+          auto token = [&](int row) {
+            return values ? (row & ~7) | ((row >> 1 & 1) << 2) | ((row & 1) << 1) | (row >> 2 & 1) : row;
+          };
 #pragma unroll
-            for (int i = t0; i < 64 * (D / 8); i += 128) {  // eight channels of one token
-              const int row = i / (D / 8), ww = i % (D / 8);
-              const uint8_t *g = rb + row / 16 * S::kGroup;
-              const __half2 sc = __float2half2_rn(e4m3_to_f32(g[S::kGap + kv4_k_scale<D>(row & 15, ww / 2)]));
-              uint32_t o[4];
-              decode8(*reinterpret_cast<const uint32_t *>(g + kv4_k_code<D>(row & 15, ww * 4)), sc, o);
-              *reinterpret_cast<uint4 *>(kt + (ww / 8) * (kKv * 128) + sw_off16(half * 64 + row, (ww & 7) * 8)) =
-                  make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          } else if (t0 < D) {  // V^T: eight tokens of eight channels; eight neighbouring lanes write a whole 128-byte row
-            uint8_t *vt = vbuf + s * S::kTileBytes;
-            const int oct = t0 & 7, ww = t0 >> 3, hi = oct & 1;
-            const uint8_t *g = rb + (oct >> 1) * S::kGroup;
-            const uint8_t *codes = g + hi * S::kGap;  // tokens 8 .. 15 lie in the second half
-            uint4 sw = *reinterpret_cast<const uint4 *>(g + S::kGap + 17 * D + (ww / 2) * 16);
-            if (half * 64 + oct * 8 >= valid) sw = make_uint4(0, 0, 0, 0);  // no tokens there: anything
-            const uint32_t sc[4] = {sw.x, sw.y, sw.z, sw.w};
-            uint32_t o[4][2][4];  // [pair of tokens][even / odd channels][channel pair]
+          for (int i = 0; i < N; ++i) {
+            const int t = token(r0 + i * STEP);
+            const uint8_t *g = rb + t / 16 * (18 * D);
+            code[i] = *reinterpret_cast<const uint32_t *>(g + (values ? kv4_v_code<D>(t & 15, ww * 4) : kv4_k_code<D>(t & 15, ww * 4)));
+            sc[i] = g[values ? kv4_v_scale<D>(t & 15, ww / 2) : kv4_k_scale<D>(t & 15, ww / 2)];
+          }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t a = *reinterpret_cast<const uint32_t *>(codes + kv4_v_code<D>(hi * 8 + 2 * q, ww * 4));
-              const uint32_t b = *reinterpret_cast<const uint32_t *>(codes + kv4_v_code<D>(hi * 8 + 2 * q + 1, ww * 4));
-              uint32_t h;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(hi ? sc[q] >> 16 : sc[q] & 0xFFFFu)));
-              const __half2 f = *reinterpret_cast<__half2 *>(&h);
-              decode8((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), f, o[q][0]);
-              decode8(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), f, o[q][1]);
-            }
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-              *reinterpret_cast<uint4 *>(vt + half * (D * 128) + sw_off16(ww * 8 + ch, oct * 8)) =
-                  make_uint4(o[0][ch & 1][ch >> 1], o[1][ch & 1][ch >> 1], o[2][ch & 1][ch >> 1], o[3][ch & 1][ch >> 1]);
+          for (int i = 0; i < N; ++i) {
+            const int t = token(r0 + i * STEP);
+            uint32_t h, o[4];
+            if (half * 64 + t >= valid) sc[i] = 0;  // no token there: anything, NaN scales too
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(sc[i] * 0x0101u)));
+            decode8(code[i], *reinterpret_cast<__half2 *>(&h), o);
+            *reinterpret_cast<uint4 *>(dst + sw_off16(t, (ww & 7) * 8)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(raw_free + x % NR);
@@ -558,9 +548,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 16) {
       // ------------------------------------------------ MMAs
-      constexpr uint32_t idS = idesc_f16(kKv), idO = idesc_f16(D);
+      constexpr uint32_t idS = idesc_f16(kKv), idO = idesc_f16(D) | (1u << 16);  // V: N runs along the rows
       constexpr uint64_t kStep = S::kTileBytes / 16;  // from one stage or tile to the next, in a descriptor
-      const uint64_t qd = desc_sw128(smem_u32(qs)), kd = desc_sw128(smem_u32(kbuf)), vd = desc_sw128(smem_u32(vbuf));
+      const uint64_t qd = desc_sw128(smem_u32(qs)), kd = desc_sw128(smem_u32(kbuf));
+      const uint64_t vd = desc_sw128_n(smem_u32(vbuf), kKv * 128);
       const bool me = elect_one();
       uint32_t kv = 0, uses[2] = {0, 0}, items[2] = {0, 0};  // K / V tiles taken, each row tile's, and its items
       segments([&](int, const Place &w, int n) {
@@ -581,14 +572,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
             const uint32_t d = tmem + S::kO + i * D, a = tmem + i * kKv + 64;
             if (!(ok = wait(p_ready + 2 * i + 1, uses[i]))) return;  // tokens 64..127 first
             tc_fence_after();
-            if (zero) mma_f16_ts_c<false>(d, a + 32, v + D * 128 / 16, idO);
-            else mma_f16_ts_c<true>(d, a + 32, v + D * 128 / 16, idO);
+            if (zero) mma_f16_ts_c<false>(d, a + 32, v + 4 * (2048 / 16), idO);
+            else mma_f16_ts_c<true>(d, a + 32, v + 4 * (2048 / 16), idO);
 #pragma unroll
-            for (int k = 1; k < 4; ++k) mma_f16_ts_c<true>(d, a + 32 + 8 * k, v + D * 128 / 16 + 2 * k, idO);
+            for (int k = 1; k < 4; ++k) mma_f16_ts_c<true>(d, a + 32 + 8 * k, v + (4 + k) * (2048 / 16), idO);
             if (!(ok = wait(p_ready + 2 * i, uses[i]))) return;
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ts_c<true>(d, a + 8 * k, v + 2 * k, idO);
+            for (int k = 0; k < 4; ++k) mma_f16_ts_c<true>(d, a + 8 * k, v + k * (2048 / 16), idO);
             ++uses[i];
           };
           ok = wait(q_full, items[0]++) && (two == 1 || wait(q_full + 1, items[1]++)) && wait(k_full + kv % NS, kv / NS);
@@ -624,26 +615,24 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
         mbar_wait(fin, 0u);
       }
     } else if (warp == 17) {
-      // ------------------------------------------------ the cached bytes, 64 tokens at a time: a lane per group
+      // ------------------------------------------------ the cached bytes, 64 tokens at a time: a copy for the groups of a
+      // page, which lie together (a copy's cost is near 100 cycles whatever its size)
+      const int per = min(c.page_tokens / 16, 4);  // groups of a copy
       uint32_t x = 0;
       segments([&](int, const Place &w, int n) {
         for (int j = 0; j < 2 * n; ++j, ++x) {
           const uint32_t s = x % NR;
           const int pos = (w.tile * 2 + j) * 64 + lane * 16;
           const uint8_t *src = nullptr;
-          if (lane < 4 && pos < w.S) {
+          if (lane < 4 && lane % per == 0 && pos < w.S) {
             const uint8_t *g = kv4_group<D>(c, w.lead, pos);  // a bad page id (flagged) reads page 0
             src = (g ? g : c.pages) + w.h * kv4_head_bytes<D>(c);
           }
-          const unsigned there = __ballot_sync(0xffffffffu, src != nullptr);
+          const int copies = __popc(__ballot_sync(0xffffffffu, src != nullptr));  // (whole pages are shared)
           if (x >= NR && !warp_wait_all(raw_free + s, x / NR - 1)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(raw_full + s, __popc(there) * 18 * D);
+          if (lane == 0) mbar_arrive_expect_tx(raw_full + s, copies * per * 18 * D);
           __syncwarp();
-          if (src) {
-            uint8_t *dst = raw + s * S::kRaw + lane * S::kGroup;
-            bulk_g2s(dst, src, S::kFirst, raw_full + s);
-            bulk_g2s(dst + S::kFirst + S::kGap, src + S::kFirst, 18 * D - S::kFirst, raw_full + s);
-          }
+          if (src) bulk_g2s(raw + s * S::kRaw + lane * 18 * D, src, per * 18 * D, raw_full + s);
         }
         return true;
       });

@@ -56,6 +56,12 @@ GDN_DEV uint64_t desc_sw128(uint32_t saddr) {
   d |= (uint64_t)2 << 61;              // 128-byte swizzle
   return d;
 }
+// The same for an operand whose rows (128 bytes: 64 FP16) run along M or N and
+// whose summed index runs across them: 8-row atoms of the summed index 1024 bytes
+// apart, blocks of 64 of M or N `block` bytes.
+GDN_DEV uint64_t desc_sw128_n(uint32_t saddr, uint32_t block) {
+  return (desc_sw128(saddr) & ~((uint64_t)0x3FFF << 16)) | (uint64_t)(block >> 4) << 16;
+}
 GDN_DEV void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
