@@ -9,6 +9,7 @@
 // (from about 80 rows per KV head they take longer than the token's bytes), and
 // beside them one 2^x per (row, token) and the decoding of the token's 2 d values.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "tc.cuh"
@@ -359,14 +360,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
       // ---- the row's query: FP16, scaled so that its largest lies in [2^13, 2^14)
       float cs = p.s.a.sm_scale * c.ks * kLog2e;
       {
-        uint4 x[D / 8];
         const int tok = row / p.G;
-        const uint16_t *src = p.s.a.q + (long long)tok * p.s.a.q_stride + (long long)(w.h * p.G + row - tok * p.G) * D;
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.s.a.q + (long long)tok * p.s.a.q_stride +
+                                                           (long long)(w.h * p.G + row - tok * p.G) * D);
         uint32_t mx = 0;
-#pragma unroll
+#pragma unroll 8
         for (int q = 0; q < D / 8; ++q) {
-          x[q] = have ? reinterpret_cast<const uint4 *>(src)[q] : make_uint4(0, 0, 0, 0);
-          const uint32_t y[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+          const uint4 x = have ? src[q] : make_uint4(0, 0, 0, 0);
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx = max(mx, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
         }
@@ -374,9 +375,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
         const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
         cs *= __uint_as_float((uint32_t)(127 - e) << 23);
         uint8_t *dst = qs + i * S::kTileBytes;
-#pragma unroll
+#pragma unroll 8
         for (int q = 0; q < D / 8; ++q) {
-          const uint32_t y[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+          const uint4 x = have ? src[q] : make_uint4(0, 0, 0, 0);
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -497,53 +499,58 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
     // ------------------------------------------------ 4-bit bytes into the operands: four warps for K, four for V.
     // Both as they lie, a token's channels in a row: K is the product's B operand with the summed index (channels)
     // along the rows, V with the summed index (tokens) across them.
-    const bool values = warp >= 12;
+    // Row r of a group (D = 128: r0 and r0 + 8, D = 64: r0) is K's token r, and V's kv4_v_row's token.
     const int t0 = tid & 127, r0 = t0 / (D / 8), ww = t0 % (D / 8);  // eight channels of rows r0, r0 + 1024 / D, ... of 64
-    constexpr int N = D / 16, STEP = 1024 / D;
-    uint64_t *full = values ? v_full : k_full, *free = values ? v_free : k_free;
-    uint8_t *tiles = (values ? vbuf : kbuf) + (ww / 8) * (kKv * 128);
-    uint32_t u = 0;
-    segments([&](int, const Place &w, int n) {
-      for (int j = 0; j < n; ++j, ++u) {
-        const uint32_t s = u % NS;
-        const int valid = w.S - (w.tile + j) * kKv;
-        if (u >= NS && !warp_wait_all(free + s, u / NS - 1)) return false;
+    constexpr int N = D / 16, PER = D == 128 ? 2 : 1;                 // rows of this thread: of 64, of a group
+    auto decode = [&](auto values, uint64_t *full, uint64_t *free, uint8_t *tiles) {
+      constexpr bool V = values();
+      const int t = V ? (r0 & 8) | ((r0 >> 1 & 1) << 2) | ((r0 & 1) << 1) | (r0 >> 2 & 1) : r0;
+      const int code_at = V ? kv4_v_code<D>(t, ww * 4) : kv4_k_code<D>(t, ww * 4);
+      const int scale_at = V ? kv4_v_scale<D>(t, ww / 2) : kv4_k_scale<D>(t, ww / 2);
+      constexpr int scale_step = V ? 2 : 8 * (D / 16);                // from token t's to token t + 8's
+      uint8_t *const to = tiles + (ww / 8) * (kKv * 128) + sw_off16(t, (ww & 7) * 8);
+      uint32_t u = 0;
+      segments([&](int, const Place &w, int n) {
+        for (int j = 0; j < n; ++j, ++u) {
+          const uint32_t s = u % NS;
+          if (u >= NS && !warp_wait_all(free + s, u / NS - 1)) return false;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t x = 2 * u + half;
-          if (!warp_wait_all(raw_full + x % NR, x / NR)) return false;
-          const uint8_t *rb = raw + x % NR * S::kRaw;
-          uint8_t *dst = tiles + s * S::kTileBytes + half * (64 * 128);
-          uint32_t code[N];
-          uint8_t sc[N];
-          // (V's rows lie in another order: the row's token)
-          auto token = [&](int row) {
-            return values ? (row & ~7) | ((row >> 1 & 1) << 2) | ((row & 1) << 1) | (row >> 2 & 1) : row;
-          };
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t x = 2 * u + half;
+            if (!warp_wait_all(raw_full + x % NR, x / NR)) return false;
+            const uint8_t *rb = raw + x % NR * S::kRaw;
+            uint8_t *dst = to + s * S::kTileBytes + half * (64 * 128);
+            const int valid = w.S - (w.tile + j) * kKv - half * 64;
+            uint32_t code[N];
+            uint32_t sc[N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int t = token(r0 + i * STEP);
-            const uint8_t *g = rb + t / 16 * (18 * D);
-            code[i] = *reinterpret_cast<const uint32_t *>(g + (values ? kv4_v_code<D>(t & 15, ww * 4) : kv4_k_code<D>(t & 15, ww * 4)));
-            sc[i] = g[values ? kv4_v_scale<D>(t & 15, ww / 2) : kv4_k_scale<D>(t & 15, ww / 2)];
-          }
+            for (int i = 0; i < N; ++i) {
+              code[i] = *reinterpret_cast<const uint32_t *>(rb + code_at + i / PER * (18 * D) + i % PER * (8 * (D / 2)));
+              sc[i] = rb[scale_at + i / PER * (18 * D) + i % PER * scale_step];
+            }
+            if (V && valid < 64) {  // places that hold no token hold anything, NaN scales too
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int t = token(r0 + i * STEP);
-            uint32_t h, o[4];
-            if (half * 64 + t >= valid) sc[i] = 0;  // no token there: anything, NaN scales too
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(sc[i] * 0x0101u)));
-            decode8(code[i], *reinterpret_cast<__half2 *>(&h), o);
-            *reinterpret_cast<uint4 *>(dst + sw_off16(t, (ww & 7) * 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int i = 0; i < N; ++i)
+                if (i / PER * 16 + i % PER * 8 + t >= valid) sc[i] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              uint32_t h, o[4];
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(sc[i] * 0x0101u)));
+              decode8(code[i], *reinterpret_cast<__half2 *>(&h), o);
+              *reinterpret_cast<uint4 *>(dst + (i / PER * 16 + i % PER * 8) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(raw_free + x % NR);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(raw_free + x % NR);
+          fence_async_shared();
+          mbar_arrive(full + s);
         }
-        fence_async_shared();
-        mbar_arrive(full + s);
-      }
-      return true;
-    });
+        return true;
+      });
+    };
+    if (warp < 12) decode(std::false_type{}, k_full, k_free, kbuf);
+    else decode(std::true_type{}, v_full, v_free, vbuf);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 16) {
