@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
 //   warps 12..15      decode its V
 //   warp 16           TMEM allocation; one thread issues the MMAs
 //   warp 17           streams the cached bytes by bulk copies
-// The softmax warps take over registers (152, 64 and 48 of 96 each), enough for half
+// The softmax warps take over registers (160, 56 and 48 of 96 each), enough for half
 // of a row's 128 scores at a time, which are read from tensor memory twice (with all
 // of them in registers there is room for four decoding warps only, a warp on each
 // scheduler, which then take 5000 cycles a tile: 140 us instead of 95 for 1024 rows
@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
     }
   };
 
-  // registers: 640 threads x 96 at launch = 256 x 152 + 256 x 64 + 128 x 48
+  // registers: 640 threads x 96 at launch = 256 x 160 + 256 x 56 + 128 x 48
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ------------------------------------------------ softmax: thread = row r of row tile i
     const int i = warp >> 2, r = tid & 127;
     const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
       return true;
     });
   } else if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // ------------------------------------------------ 4-bit bytes into the operands: four warps for K, four for V.
     // Both as they lie, a token's channels in a row: K is the product's B operand with the summed index (channels)
     // along the rows, V with the summed index (tokens) across them.
