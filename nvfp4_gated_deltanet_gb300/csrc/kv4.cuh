@@ -186,11 +186,22 @@ struct Kv4AttnArgs {
   uint16_t *out;
   float *lse;  // or null
 };
-// raw, raw_ml: where FP32 sums before the division go instead of out and lse: sum_j 2^(z_j - m) v_j / v_scale
-// [T][Hq][D] and (m, sum_j 2^(z_j - m)) [T][Hq][2], z in bits.
+// raw, raw_ml: instead of out and lse, FP32 sums before the division, sum_j 2^(z_j - m) v_j / v_scale [T][Hq][D] and
+// (m, sum_j 2^(z_j - m)) [T][Hq][2], z in bits -- of the (sequence, KV head, row group) items that one run holds
+// whole. The others' pieces are left where kv4_decode_pieces says. early: the call's inputs were complete before the
+// kernel in front of it let this one begin.
 cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream,
-                              float *raw = nullptr, float *raw_ml = nullptr);
-size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms);  // its workspace
+                              float *raw = nullptr, float *raw_ml = nullptr, bool early = false);
+// Pieces of rows [2 runs][rows][D] and their (m + 7, l) [2 runs][rows][2]; of item (b Hkv + h) groups + group: the first piece,
+// or -1 where it is whole, and the run of its last; the pieces between are numbers 2 run.
+struct Kv4Pieces {
+  const float *part, *ml;
+  const int32_t *ends;
+  int rows, groups;  // rows of an item, at most; items of a sequence and KV head
+};
+Kv4Pieces kv4_decode_pieces(const Kv4AttnArgs &a, const void *workspace, int num_sms);
+constexpr float kKv4PieceShift = 7.0f;  // the decode kernel's weights are 2^(z - m + 7)
+size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms, bool raw = false);  // its workspace
 cudaError_t launch_kv4_prefill(const Kv4AttnArgs &a, long long total_kv, void *workspace, int num_sms,
                                cudaStream_t stream);
 size_t kv4_prefill_bytes(const Kv4AttnArgs &a, long long total_kv);  // its workspace; 0: too large

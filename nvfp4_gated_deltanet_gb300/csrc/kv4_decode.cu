@@ -55,7 +55,7 @@ namespace {
 // A column's weights are 2^(z - m + 7); m only moves (and O is rescaled) when a
 // score passes it by 7, so that a tile whose scores do not costs no exchange
 // between lanes and no rescaling. Weights stay below 2^14 in FP16.
-constexpr float kShift = 7.0f, kSlack = 7.0f;
+constexpr float kShift = kKv4PieceShift, kSlack = 7.0f;
 
 // Warps by the registers they need: 128, 168 or 255 each. NQ: 8-row column
 // blocks of an item.
@@ -91,7 +91,9 @@ struct DecodeArgs {
   int extra;         // cost of an item beside its tiles, in tiles; kWhole: runs hold whole items, nothing to join
   int items;         // (sequence, KV head, row group)
   float *part;       // pieces [2 runs][rows][D], their (m, l) [2 runs][rows][2], the items' ends [items][2]
-  float *raw, *raw_ml;  // not null: instead of out and lse, O [T][Hq][D] and its (m, l) [T][Hq][2], FP32
+  float *raw, *raw_ml;  // not null: instead of out and lse, O [T][Hq][D] and its (m, l) [T][Hq][2], FP32, of whole items
+  int whole;            // (raw) items stay whole while no sequence has more tokens than this
+  bool early;           // (raw) what the kernel reads is there although the one before has not ended
 };
 // What the plan goes by, all measured on GB300 (d = 128, us):
 // An item's query rows, its meeting and its output take a team about as long as
@@ -193,13 +195,13 @@ struct Cuts {
   GDN_DEV long long at(int k) const { return q * k + rest * k / N; }
 };
 template <int TILE>
-GDN_DEV Cuts find_cuts(const DecodeArgs &p, int warps, int HR, int lane, int most) {
+GDN_DEV Cuts find_cuts(const DecodeArgs &p, int extra, int warps, int HR, int lane, int most) {
   const Kv4Args &c = p.a.c;
   Cuts k;
   k.n0 = lane_tiles<TILE>(c, 0, lane);
   long long tiles = warp_isum(k.n0);
   for (int b0 = 32; b0 < c.B; b0 += 32) tiles += warp_isum(lane_tiles<TILE>(c, b0, lane));
-  const long long units = (tiles + (long long)c.B * p.extra) * HR;
+  const long long units = (tiles + (long long)c.B * extra) * HR;
   k.tiles = tiles * HR;
   k.N = runs(k.tiles, warps, most);
   k.q = quot(units, k.N);
@@ -210,10 +212,10 @@ GDN_DEV Cuts find_cuts(const DecodeArgs &p, int warps, int HR, int lane, int mos
 // With whole items, runs have as many each, and a run's tiles are counted from
 // its own beginning: `from` is the run's first cut.
 template <int TILE>
-GDN_DEV long long find_cut(const DecodeArgs &p, int warps, int HR, int lane, int from, int cut, int most, Cursor &k) {
+GDN_DEV long long find_cut(const DecodeArgs &p, int extra, int warps, int HR, int lane, int from, int cut, int most, Cursor &k) {
   const Kv4Args &c = p.a.c;
   k = Cursor{0, 0, 0, 0, 0};
-  if (p.extra == kWhole) {
+  if (extra == kWhole) {
     const int items = c.B * HR;
     const int i0 = (int)quot((long long)items * from, most), i1 = (int)quot((long long)items * cut, most);
     int n = 0;
@@ -224,8 +226,8 @@ GDN_DEV long long find_cut(const DecodeArgs &p, int warps, int HR, int lane, int
     }
     return n;
   }
-  const Cuts x = find_cuts<TILE>(p, warps, HR, lane, most);
-  return cut >= x.N ? x.tiles : find_tile<TILE>(c, x.at(cut), HR, p.extra, lane, x.n0, k);
+  const Cuts x = find_cuts<TILE>(p, extra, warps, HR, lane, most);
+  return cut >= x.N ? x.tiles : find_tile<TILE>(c, x.at(cut), HR, extra, lane, x.n0, k);
 }
 
 // A group of an item's query rows, `most` at most: row x is a (token, query head).
@@ -293,7 +295,8 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     *abort_flag = 0u;
     fence_barrier_init();
   }
-  kv4_begin();
+  if (!p.early) kv4_begin();
+  else pdl_launch_dependents();
   __syncthreads();
   Cursor cur;
   int n_tiles;
@@ -304,7 +307,13 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     };
     volatile Found *found = reinterpret_cast<volatile Found *>(meet);
     if (warp < 2) {
-      const long long n = find_cut<TILE>(p, W, HR, lane, run, run + warp, gridDim.x * S::kTeams, cur);
+      int extra = p.extra;
+      if (p.raw) {  // the host knows no bound of these lengths that says much
+        int most = 0;
+        for (int b = lane; b < c.B; b += 32) most = max(most, kv4_len(c, b));
+        if (__all_sync(0xffffffffu, most <= p.whole)) extra = kWhole;
+      }
+      const long long n = find_cut<TILE>(p, extra, W, HR, lane, run, run + warp, gridDim.x * S::kTeams, cur);
       if (lane == 0) {
         found[warp].k.b = cur.b;
         found[warp].k.hr = cur.hr;
@@ -692,7 +701,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
       }
     }
     // for the join: an item's first piece (-1: it is done) and the run of its last one
-    if (tid == 0 && p.extra != kWhole) {
+    if (tid == 0 && (p.extra != kWhole || p.raw)) {
       int32_t *ends = join_ends<D>(p, gridDim.x * S::kTeams, S::kRows) + 2 * ((long long)cur.b * HR + cur.hr);
       if (cur.tile == 0) ends[0] = done ? -1 : (int)piece;
       if (cur.tile + seg == cur.nt) ends[1] = run;
@@ -707,6 +716,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     if (held > 0) mbar_wait(my_full + slot, turn);
     if (held > 1) mbar_wait(my_full + (slot ^ 1), slot == 0 ? turn : turn ^ 1u);
   }
+  if (p.early) pdl_wait();  // this grid must not end before the one it follows
 }
 
 // Join R rows, from `row`, of pieces j0, j0 + step, ... < np: U at a time are in flight.
@@ -784,13 +794,6 @@ __global__ void __launch_bounds__(256, 3) kv4_join_kernel(DecodeArgs p, int runs
     auto piece = [&](int j) { return (size_t)(j > 0 ? 2 * (first + j) : e.x) * most; };
     auto put = [&](int row, int ch, float m, float l, auto &v) {  // channels ch ... of a row
       const long long out = ((long long)b * p.r + rg.token(row)) * p.a.Hq + rg.h * p.G + rg.head(row);
-      if (p.raw) {
-#pragma unroll
-        for (int x = 0; x < (int)(sizeof(v) / sizeof(float)); x += 2)
-          *reinterpret_cast<float2 *>(p.raw + out * D + ch + x) = make_float2(v[x], v[x + 1]);
-        if (ch == 0) *reinterpret_cast<float2 *>(p.raw_ml + out * 2) = make_float2(m - kShift, l);
-        return;
-      }
       const float inv = l == 0.0f ? 0.0f : c.vs / l;
 #pragma unroll
       for (int x = 0; x < (int)(sizeof(v) / sizeof(float)); x += 2)
@@ -856,7 +859,7 @@ cudaError_t launch_decode_t(const DecodeArgs &p, int ctas, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
   e = kv4_launch(kv4_decode_kernel<D, NQ, TEAM>, ctas, S::kThreads, S::kBytes, stream, p);
   const int most = ctas * S::kTeams;  // runs, and cuts but one
-  if (e != cudaSuccess || p.extra == kWhole || most < 2) return e;
+  if (e != cudaSuccess || p.extra == kWhole || most < 2 || p.raw) return e;
   const int rows = std::min(int(S::kRows), p.r * p.G);
   const dim3 grid(TEAM ? std::min(p.items, 8 * 152) : p.items, TEAM ? (rows + 7) / 8 : rows);
   return kv4_launch(kv4_join_kernel<D, TEAM == 0>, grid, 256, 0, stream, p, most, int(S::kRows));
@@ -878,12 +881,14 @@ ShapeInfo shape_info(bool small) {
 
 struct DecodePlan {
   int NQ, RG, ctas, extra;
-  bool small;    // teams of four warps
+  int runs, whole;  // teams; items stay whole while no sequence has more tokens than this
+  bool small;       // teams of four warps
   size_t bytes;
 };
 // Everything the host knows: an upper bound of the lengths. Where it says that an
 // item takes a team few rounds of tiles, items stay whole: no piece to join.
-DecodePlan decode_plan(const Kv4AttnArgs &a, int num_sms) {
+// raw: whether they do is decided on the device.
+DecodePlan decode_plan(const Kv4AttnArgs &a, int num_sms, bool raw = false) {
   DecodePlan d{};
   const int R = a.c.T / a.c.B * (a.Hq / a.c.Hkv);
   d.NQ = blocks_of(R);
@@ -895,9 +900,12 @@ DecodePlan decode_plan(const Kv4AttnArgs &a, int num_sms) {
                                    : (d.NQ == 1 ? shape_info<64, 1>(d.small) : d.NQ == 2 ? shape_info<64, 2>(d.small)
                                                                                          : shape_info<64, 4>(d.small));
   const long long most = ((long long)a.c.cols * a.c.page_tokens + s.tile - 1) / s.tile;  // tiles of an item
-  d.extra = most <= (long long)s.team * (d.small ? kRoundsTeam : kRoundsCta) ? kWhole : d.small ? kExtraTeam : kExtraCta;
+  const int rounds = s.team * (d.small ? kRoundsTeam : kRoundsCta);
+  d.whole = rounds * s.tile;
+  d.extra = most <= rounds && !raw ? kWhole : d.small ? kExtraTeam : kExtraCta;
   const long long n = d.extra == kWhole ? items : (items * most + s.team - 1) / s.team;  // runs that could have work
   d.ctas = (int)(n < (long long)num_sms * s.teams ? (n + s.teams - 1) / s.teams : num_sms);
+  d.runs = d.ctas * s.teams;
   d.bytes = d.extra == kWhole ? 0 : 2 * (size_t)d.ctas * s.teams * 8 * d.NQ * (a.c.D + 2) * sizeof(float) + 8 * (size_t)items;
   return d;
 }
@@ -911,14 +919,21 @@ cudaError_t launch_decode(const DecodeArgs &p, const DecodePlan &d, cudaStream_t
 
 }  // namespace
 
-size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms) { return a.c.T ? decode_plan(a, num_sms).bytes : 0; }
+size_t kv4_decode_bytes(const Kv4AttnArgs &a, int num_sms, bool raw) { return a.c.T ? decode_plan(a, num_sms, raw).bytes : 0; }
+
+Kv4Pieces kv4_decode_pieces(const Kv4AttnArgs &a, const void *workspace, int num_sms) {
+  const DecodePlan d = decode_plan(a, num_sms, true);
+  const int rows = 8 * d.NQ;
+  const float *part = static_cast<const float *>(workspace), *ml = part + 2 * (size_t)d.runs * rows * a.c.D;
+  return {part, ml, reinterpret_cast<const int32_t *>(ml + 4 * (size_t)d.runs * rows), rows, d.RG};
+}
 
 cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream, float *raw,
-                              float *raw_ml) {
-  const DecodePlan d = decode_plan(a, num_sms);
+                              float *raw_ml, bool early) {
+  const DecodePlan d = decode_plan(a, num_sms, raw != nullptr);
   const int G = a.Hq / a.c.Hkv;
   const DecodeArgs p{a, a.c.T / a.c.B, G, d.RG, (uint32_t)((65536 + G - 1) / G), d.extra, (int)(a.c.B * a.c.Hkv * d.RG),
-                     static_cast<float *>(workspace), raw, raw_ml};
+                     static_cast<float *>(workspace), raw, raw_ml, d.whole, early};
   if (a.c.D == 128)
     return d.NQ == 1 ? launch_decode<128, 1>(p, d, stream) : d.NQ == 2 ? launch_decode<128, 2>(p, d, stream)
                                                                        : launch_decode<128, 4>(p, d, stream);

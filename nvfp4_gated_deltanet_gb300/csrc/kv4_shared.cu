@@ -25,9 +25,9 @@ constexpr int kPlanThreads = 256;
 struct SharedWs {
   int32_t *own_len;    // [B]: a sequence's tokens behind its shared ones
   int32_t *own_table;  // [B][cols]: their pages
-  int32_t *seq_group;  // [B]: its group, -1: none
+  int2 *seq_item;      // [B]: the first row of its group, and that row's item slot; -1: it shares nothing
   int32_t *len, *lead; // [groups]: shared tokens (0: none), the sequence through whose pages they are read
-  float *own, *own_ml;   // [T][Hq][D], [T][Hq][2]: kv4_decode's sums and their (maximum, weight)
+  float *own, *own_ml;   // [T][Hq][D], [T][Hq][2]: kv4_decode's sums and their (maximum, weight), whole items
   int32_t *ends;         // [Hkv][slots][2]: an item's first piece, or -1: it is whole; the run of its last piece
   float *pre, *pre_ml;   // whole items: [Hkv][D][rows], [Hkv][rows][2]
   float *part, *part_ml; // pieces [2 runs][D][ld], [2 runs][ld][2]
@@ -40,6 +40,7 @@ struct SharedKv4 {
   int r, G, rows;  // new tokens per sequence, query heads per KV head, T G
   int runs;        // CTAs of the prefix kernel
   int slots, ld;   // items of a KV head, at most; rows of a piece
+  Kv4Pieces own;   // of what each sequence has for itself
 };
 
 constexpr int kItemRows = 256;  // query rows of an item: two tiles of 128
@@ -71,7 +72,7 @@ size_t lay_out(const Kv4SharedArgs &s, uint8_t *base, int num_sms, SharedKv4 &p)
   const size_t rows = p.rows, all = (size_t)c.T * s.a.Hq;
   w.own_len = reinterpret_cast<int32_t *>(take(4 * (size_t)c.B));
   w.own_table = reinterpret_cast<int32_t *>(take(4 * (size_t)c.B * c.cols));
-  w.seq_group = reinterpret_cast<int32_t *>(take(4 * (size_t)c.B));
+  w.seq_item = reinterpret_cast<int2 *>(take(8 * (size_t)c.B));
   w.len = reinterpret_cast<int32_t *>(take(4 * (size_t)s.groups));
   w.lead = reinterpret_cast<int32_t *>(take(4 * (size_t)s.groups));
   w.own = reinterpret_cast<float *>(take(4 * all * c.D));
@@ -81,7 +82,8 @@ size_t lay_out(const Kv4SharedArgs &s, uint8_t *base, int num_sms, SharedKv4 &p)
   w.pre_ml = reinterpret_cast<float *>(take(8 * rows * c.Hkv));
   w.part = reinterpret_cast<float *>(take(8 * (size_t)p.runs * p.ld * c.D));
   w.part_ml = reinterpret_cast<float *>(take(16 * (size_t)p.runs * p.ld));
-  w.decode = take(kv4_decode_bytes(s.a, num_sms));
+  w.decode = take(kv4_decode_bytes(s.a, num_sms, true));
+  p.own = kv4_decode_pieces(s.a, w.decode, num_sms);
   return at;
 }
 
@@ -148,8 +150,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
   const int len = kv4_len(c, b), skip = len > 0 ? S : 0;
   if (tid == 0) {
     if (c.kv_len[b] != len) flag_status(c.status, GDN_E_RANGE);
+    const int row0 = skip > 0 ? start[g] * p.r * p.G : -1;
     p.w.own_len[b] = len - skip;
-    p.w.seq_group[b] = skip > 0 ? g : -1;
+    p.w.seq_item[b] = make_int2(row0, skip > 0 ? row0 / kItemRows + g : -1);
   }
   const int from = skip / c.page_tokens;
   for (int i = tid; i < c.cols; i += kPlanThreads)
@@ -657,89 +660,114 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
 }
 
 // ---------------------------------------------------------------- the parts joined
-// A CTA per 32 rows of a KV head and 32 channels: the prefix's pieces, lane = row,
-// then with the row's own part. Bound by latency: an item's ends, the pieces'
-// (m, l), then their sums.
+// A CTA per 32 rows of a KV head and 32 channels. First the prefix's pieces, lane =
+// row, 8 of them in flight; then, four channels a thread, what the sequence has for
+// itself. Bound by latency: the row's item, its ends, the pieces.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(SharedKv4 p) {
-  __shared__ float tile[32][33], f_own[32];
+  constexpr int U = 8;
+  __shared__ float sums[32][33], pre_m[32], pre_l[32];
   kv4_begin();
   const Kv4Args &c = p.s.a.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, ch0 = blockIdx.z * 32;
-  const int row = blockIdx.x * 32 + lane;
+  const int h = blockIdx.y, ch0 = blockIdx.z * 32;
   {
-    const bool have = row < p.rows;
-    const int tok = have ? row / p.G : 0, b = tok / p.r, g = have && p.runs ? p.w.seq_group[b] : -1;
-    const long long out = (long long)tok * p.s.a.Hq + h * p.G + row - tok * p.G;
-    // the pieces: the first, then one in each run
-    const float *src = nullptr;   // the first piece's channel 0
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
+    const int2 item = row < p.rows && p.runs ? p.w.seq_item[row / p.G / p.r] : make_int2(-1, -1);
+    const float *src = nullptr;   // the first piece's channel
     const float2 *ml = nullptr;
-    int np = 0;
-    size_t step = 0, ch_step = p.rows;
-    int second = 0;
-    if (g >= 0) {
-      const int row0 = p.s.group_start[g] * p.r * p.G, pair = (row - row0) / kItemRows;
-      const int2 e = reinterpret_cast<const int2 *>(p.w.ends)[(size_t)h * p.slots + row0 / kItemRows + g + pair];
-      const int in = row - row0 - pair * kItemRows;
+    int np = 0, second = 0;       // pieces; from the first to the second, in pieces: then one in each run
+    size_t ch_step = p.rows;
+    if (item.x >= 0) {
+      const int pair = (row - item.x) / kItemRows, in = row - item.x - pair * kItemRows;
+      const int2 e = reinterpret_cast<const int2 *>(p.w.ends)[(size_t)h * p.slots + item.y + pair];
       if (e.x < 0) {
         np = 1;
-        src = p.w.pre + (size_t)h * D * p.rows + row;
+        src = p.w.pre + ((size_t)h * D + ch0 + warp * 4) * p.rows + row;
         ml = reinterpret_cast<const float2 *>(p.w.pre_ml) + (size_t)h * p.rows + row;
       } else {
         np = e.y - e.x / 2 + 1;
-        src = p.w.part + (size_t)e.x * D * p.ld + in;
+        src = p.w.part + ((size_t)e.x * D + ch0 + warp * 4) * p.ld + in;
         ml = reinterpret_cast<const float2 *>(p.w.part_ml) + (size_t)e.x * p.ld + in;
         ch_step = p.ld;
-        second = 2 - (e.x & 1);  // from the first piece to the second, in pieces
-        step = 2;
+        second = 2 - (e.x & 1);
       }
     }
-    auto at = [&](int j) { return j == 0 ? (size_t)0 : second + (size_t)(j - 1) * step; };
-    const float2 own = have ? reinterpret_cast<const float2 *>(p.w.own_ml)[out] : make_float2(-INFINITY, 0.0f);
-    float m = own.x;
-    for (int j = 0; j < np; j += 4) {
-      float x[4];
+    float m = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < np; j += U) {
+      float2 x[U];
+      float v[U][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) x[u] = j + u < np ? ml[at(j + u) * p.ld].x : -INFINITY;
+      for (int u = 0; u < U; ++u) {
+        const int at = j + u == 0 ? 0 : second + 2 * (j + u - 1);
+        const bool in = j + u < np;
+        x[u] = in ? ml[(size_t)at * p.ld] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) m = fmaxf(m, x[u]);
-    }
-    const float safe = m == -INFINITY ? 0.0f : m, fo = ex2(own.x - safe);
-    float l = own.y * fo, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < np; j += 4) {
-      float2 x[4];
-      float v[4][4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        x[u] = j + u < np ? ml[at(j + u) * p.ld] : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[u][k] = j + u < np ? src[(at(j + u) * D + ch0 + warp * 4 + k) * ch_step] : 0.0f;
+        for (int k = 0; k < 4; ++k) v[u][k] = in ? src[(size_t)at * D * p.ld + k * ch_step] : 0.0f;
       }
+      float top = m;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float f = ex2(x[u].x - safe);
-        l = fmaf(x[u].y, f, l);
+      for (int u = 0; u < U; ++u) top = fmaxf(top, x[u].x);
+      const float safe = top == -INFINITY ? 0.0f : top, f = ex2(m - safe);
+      m = top;
+      l *= f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = fmaf(v[u][k], f, acc[k]);
+      for (int k = 0; k < 4; ++k) acc[k] *= f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float fu = ex2(x[u].x - safe);
+        l = fmaf(x[u].y, fu, l);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = fmaf(v[u][k], fu, acc[k]);
       }
     }
-    const float inv = l == 0.0f ? 0.0f : c.vs / l;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) tile[lane][warp * 4 + k] = acc[k] * inv;
+    for (int k = 0; k < 4; ++k) sums[lane][warp * 4 + k] = acc[k];
     if (warp == 0) {
-      f_own[lane] = fo * inv;
-      if (p.s.a.lse && ch0 == 0 && have) p.s.a.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
+      pre_m[lane] = m;
+      pre_l[lane] = l;
+    }
+  }
+  const int r = threadIdx.x / 8, ch = ch0 + threadIdx.x % 8 * 4, row = blockIdx.x * 32 + r;
+  const bool have = row < p.rows;
+  const int tok = have ? row / p.G : 0, b = tok / p.r, q = row - tok * p.G;
+  const long long out = (long long)tok * p.s.a.Hq + h * p.G + q;
+  // ---- the sequence's own: whole, or its pieces
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (have) {
+    const int f = row - b * p.r * p.G, rg = p.own.groups == 1 ? 0 : f / p.own.rows;
+    const int2 e = reinterpret_cast<const int2 *>(p.own.ends)[((size_t)b * c.Hkv + h) * p.own.groups + rg];
+    if (e.x < 0) {
+      const float2 x = reinterpret_cast<const float2 *>(p.w.own_ml)[out];
+      o = *reinterpret_cast<const float4 *>(p.w.own + out * D + ch);
+      m = x.x;
+      l = x.y;
+    } else {
+      const int in = f - rg * p.own.rows, np = e.y - e.x / 2 + 1;
+      for (int j = 0; j < np; ++j) {
+        const size_t at = (size_t)(j == 0 ? e.x : 2 * (e.x / 2 + j)) * p.own.rows + in;
+        float2 x = reinterpret_cast<const float2 *>(p.own.ml)[at];
+        const float4 v = *reinterpret_cast<const float4 *>(p.own.part + at * D + ch);
+        x.x -= kKv4PieceShift;
+        const float top = fmaxf(m, x.x), safe = top == -INFINITY ? 0.0f : top, fm = ex2(m - safe), fx = ex2(x.x - safe);
+        m = top;
+        l = l * fm + x.y * fx;
+        o.x = o.x * fm + v.x * fx;
+        o.y = o.y * fm + v.y * fx;
+        o.z = o.z * fm + v.z * fx;
+        o.w = o.w * fm + v.w * fx;
+      }
     }
   }
   __syncthreads();
-  const int r = threadIdx.x / 8, ch = threadIdx.x % 8 * 4, mine = blockIdx.x * 32 + r;
-  if (mine >= p.rows) return;
-  const int tok = mine / p.G;
-  const long long out = ((long long)tok * p.s.a.Hq + h * p.G + mine - tok * p.G) * D + ch0 + ch;
-  const float4 o = *reinterpret_cast<const float4 *>(p.w.own + out);
-  const float f = f_own[r];
-  *reinterpret_cast<uint2 *>(p.s.a.out + out) = make_uint2(bf16x2(fmaf(o.x, f, tile[r][ch]), fmaf(o.y, f, tile[r][ch + 1])),
-                                                           bf16x2(fmaf(o.z, f, tile[r][ch + 2]), fmaf(o.w, f, tile[r][ch + 3])));
+  if (!have) return;
+  const float mp = pre_m[r], top = fmaxf(m, mp), safe = top == -INFINITY ? 0.0f : top, fo = ex2(m - safe), fp = ex2(mp - safe);
+  l = l * fo + pre_l[r] * fp;
+  const float inv = l == 0.0f ? 0.0f : c.vs / l, go = fo * inv, gp = fp * inv;
+  const float *s = sums[r] + (ch - ch0);
+  *reinterpret_cast<uint2 *>(p.s.a.out + out * D + ch) = make_uint2(bf16x2(o.x * go + s[0] * gp, o.y * go + s[1] * gp),
+                                                                    bf16x2(o.z * go + s[2] * gp, o.w * go + s[3] * gp));
+  if (p.s.a.lse && ch == 0) p.s.a.lse[out] = (top + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int D>
@@ -757,7 +785,7 @@ cudaError_t launch_t(const SharedKv4 &p, int num_sms, cudaStream_t stream) {
   Kv4AttnArgs own = p.s.a;
   own.c.kv_len = p.w.own_len;
   own.c.table = p.w.own_table;
-  e = launch_kv4_decode(own, p.w.decode, num_sms, stream, p.w.own, p.w.own_ml);
+  e = launch_kv4_decode(own, p.w.decode, num_sms, stream, p.w.own, p.w.own_ml, p.runs > 0);
   if (e != cudaSuccess) return e;
   return kv4_launch(kv4_merge_kernel<D>, dim3((p.rows + 31) / 32, c.Hkv, D / 32), 256, 0, stream, p);
 }
