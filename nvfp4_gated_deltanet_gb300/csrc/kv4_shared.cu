@@ -232,21 +232,46 @@ struct Place {
   }
 };
 static_assert(sizeof(Place) == 40, "what the prefix kernel's shared memory has for it");
-// The tile at cost u (an item's own cost comes before its tiles), and how many tiles
-// lie before it; past the end only the number. total: all items' cost. A whole warp.
-GDN_DEV long long find_place(const SharedKv4 &p, long long u, int lane, Place &k, long long &total) {
-  long long cost = 0, tiles = 0, at = -1;
-  for (int g0 = 0; g0 < p.s.groups; g0 += 32) {
-    long long items = 0;
-    int nt = 0;
-    if (g0 + lane < p.s.groups && p.w.len[g0 + lane] > 0) {
-      Place x;
-      x.group(p, g0 + lane);
-      nt = x.nt;
-      items = (long long)x.pairs * p.s.a.c.Hkv;
-    }
-    const long long own = nt ? items * (nt + kItemCost) : 0;
-    long long incl = own, tincl = items * nt;
+// a / b, in 32 bits where they fit (64 bits take some 200 instructions)
+GDN_DEV long long quot(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+// Lane's group g0 + lane: its items' cost and tiles.
+struct GroupCost {
+  long long cost, tiles;
+  int nt;
+  GDN_DEV GroupCost(const SharedKv4 &p, int g) : cost(0), tiles(0), nt(0) {
+    if (g >= p.s.groups) return;
+    const int first = p.s.group_start[g], last = p.s.group_start[g + 1], S = p.w.len[g];
+    if (S == 0) return;
+    nt = (S + kKv - 1) / kKv;
+    const long long items = (long long)(((last - first) * p.r * p.G + kItemRows - 1) / kItemRows) * p.s.a.c.Hkv;
+    cost = items * (nt + kItemCost);
+    tiles = items * nt;
+  }
+};
+GDN_DEV long long warp_lsum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Cut `cut` of the runs' cuts: the tile there, and how many lie before it. No more
+// runs than tiles: then the pieces of an item lie in neighbouring ones. A whole warp.
+GDN_DEV long long find_cut(const SharedKv4 &p, int cut, int lane, Place &k) {
+  const GroupCost mine(p, lane);  // of the first 32 groups
+  long long total = warp_lsum(mine.cost), tiles = warp_lsum(mine.tiles);
+  for (int g0 = 32; g0 < p.s.groups; g0 += 32) {
+    const GroupCost x(p, g0 + lane);
+    total += warp_lsum(x.cost);
+    tiles += warp_lsum(x.tiles);
+  }
+  const long long n = max(1LL, min((long long)gridDim.x, tiles));
+  if (cut >= n || tiles == 0) return tiles;
+  const long long q = quot(total, n);
+  long long u = q * cut + quot((total - q * n) * cut, n), before = 0;  // the cost at the cut, the tiles of the groups before
+  for (int g0 = 0;; g0 += 32) {  // (ends: u < total)
+    const GroupCost x = g0 == 0 ? mine : GroupCost(p, g0 + lane);
+    long long incl = x.cost, tincl = x.tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, tincl, o);
@@ -255,21 +280,19 @@ GDN_DEV long long find_place(const SharedKv4 &p, long long u, int lane, Place &k
         tincl += z;
       }
     }
-    const unsigned past = __ballot_sync(0xffffffffu, cost + incl > u);
-    if (at < 0 && past) {
+    const unsigned past = __ballot_sync(0xffffffffu, incl > u);
+    if (past) {
       const int l = __ffs(past) - 1;
       k.group(p, g0 + l);
-      const long long off = u - cost - __shfl_sync(0xffffffffu, incl - own, l), item = off / (k.nt + kItemCost);
-      k.tile = max((int)(off - item * (k.nt + kItemCost)) - kItemCost, 0);
-      k.h = (int)(item / k.pairs);
+      const long long off = u - __shfl_sync(0xffffffffu, incl - x.cost, l), item = quot(off, k.nt + kItemCost);
+      k.tile = max((int)(off - item * (k.nt + kItemCost)) - kItemCost, 0);  // an item's own cost comes before its tiles
+      k.h = (int)quot(item, k.pairs);
       k.pair = (int)(item - (long long)k.h * k.pairs);
-      at = tiles + __shfl_sync(0xffffffffu, tincl - items * nt, l) + item * k.nt + k.tile;
+      return before + __shfl_sync(0xffffffffu, tincl - x.tiles, l) + item * k.nt + k.tile;
     }
-    cost += __shfl_sync(0xffffffffu, incl, 31);
-    tiles += __shfl_sync(0xffffffffu, tincl, 31);
+    u -= __shfl_sync(0xffffffffu, incl, 31);
+    before += __shfl_sync(0xffffffffu, tincl, 31);
   }
-  total = cost;
-  return at < 0 ? tiles : at;
 }
 
 template <int D>
@@ -318,11 +341,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
   kv4_begin();
   if (warp < 2) {  // the run's two ends
     Place k{};
-    long long total = 0;
-    const long long tiles = find_place(p, 0x7fffffffffffffffLL, lane, k, total);
-    // no more runs than tiles: then the pieces of an item lie in neighbouring ones
-    const long long n = max(1LL, min((long long)gridDim.x, tiles)), x = min(n, (long long)blockIdx.x + warp);
-    const long long at = find_place(p, total / n * x + total % n * x / n, lane, k, total);
+    const long long at = find_cut(p, blockIdx.x + warp, lane, k);
     if (lane == 0) {
       if (warp == 0) *first = k;
       ends[warp] = at;
@@ -366,11 +385,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
         const int tok = row / p.G;
         const uint4 *src = reinterpret_cast<const uint4 *>(p.s.a.q + (long long)tok * p.s.a.q_stride +
                                                            (long long)(w.h * p.G + row - tok * p.G) * D);
+        uint4 x[D / 8];
         uint32_t mx = 0;
-#pragma unroll 8
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q) x[q] = have ? src[q] : make_uint4(0, 0, 0, 0);
+#pragma unroll
         for (int q = 0; q < D / 8; ++q) {
-          const uint4 x = have ? src[q] : make_uint4(0, 0, 0, 0);
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t y[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx = max(mx, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
         }
@@ -378,10 +399,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
         const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
         cs *= __uint_as_float((uint32_t)(127 - e) << 23);
         uint8_t *dst = qs + i * S::kTileBytes;
-#pragma unroll 8
+#pragma unroll
         for (int q = 0; q < D / 8; ++q) {
-          const uint4 x = have ? src[q] : make_uint4(0, 0, 0, 0);
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t y[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -664,7 +684,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
 // row, 8 of them in flight; then, four channels a thread, what the sequence has for
 // itself. Bound by latency: the row's item, its ends, the pieces.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_merge_kernel(SharedKv4 p) {
+__global__ void __launch_bounds__(256, 3) kv4_merge_kernel(SharedKv4 p) {
   constexpr int U = 8;
   __shared__ float sums[32][33], pre_m[32], pre_l[32];
   kv4_begin();
