@@ -73,7 +73,8 @@ GDN_DEV uint32_t e4m3x2(uint32_t two) {
 // equal length, one per warp. A warp holds a unit's K bytes in registers: as soon
 // as a group of 16 tokens is decoded into MMA operands, the same group of the next
 // unit is on its way. No part of a token's sum leaves the warp, nothing is joined.
-constexpr int kUnit = 64;
+constexpr int kGroups = 4, kUnit = 16 * kGroups;  // (a lane of four writes a group's sums)
+constexpr int kLook = 32 / kGroups;  // units whose groups' places are worked out at once, a group per lane
 constexpr int kRowWarps = 8;
 
 struct Unit {
@@ -136,52 +137,50 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  // ---- loads: where the groups of the next eight units lie is worked out at once, a group per lane
+  // ---- loads
   Unit ahead = cur;              // the unit that is loaded next
-  int ahead_left = left, ahead_i = 8;
-  const uint8_t *where = nullptr;
+  int ahead_left = left, ahead_i = kLook;
+  const uint8_t *where = c.pages;
   auto look = [&]() {
-    if (ahead_i == 8) {
+    if (ahead_i == kLook) {
       ahead_i = 0;
-      where = nullptr;
+      where = c.pages;  // (past the run's or the sequence's end: read, and not used)
       Unit k = ahead;
-      if (lane / 4 < ahead_left) {
-        for (int i = 0; i < lane / 4; ++i) next_unit(c, k);
-        const int pos = k.pos + (lane & 3) * 16;
-        if (pos < k.len) {
-          where = kv4_group<D>(c, k.b, pos);
-          if (where) where += k.h * kv4_head_bytes<D>(c);
-        }
+      if (lane / kGroups < ahead_left) {
+        for (int i = 0; i < lane / kGroups; ++i) next_unit(c, k);
+        const int pos = k.pos + lane % kGroups * 16;
+        const uint8_t *grp = pos < k.len ? kv4_group<D>(c, k.b, pos) : nullptr;  // a bad page id is flagged
+        if (grp) where = grp + k.h * kv4_head_bytes<D>(c);
       }
     }
   };
-  uint32_t kw[4][2][W];  // [group][token g, g + 8]: 16 (d = 64: 8) code bytes, and their scales
-  uint32_t ks[4][2];
+  uint32_t kw[kGroups][2][W];  // [group][token g, g + 8]: 16 (d = 64: 8) code bytes, and their scales
+  uint32_t ks[kGroups][2];
   auto load = [&](int q) {
     const uint8_t *src = reinterpret_cast<const uint8_t *>(
-        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(where), ahead_i * 4 + q));
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(where), ahead_i * kGroups + q));
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int tok = g + 8 * x;
       if constexpr (D == 128) {
-        const uint4 v = src ? __ldg(reinterpret_cast<const uint4 *>(src + kv4_k_code<D>(tok, t * 16))) : make_uint4(0, 0, 0, 0);
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + kv4_k_code<D>(tok, t * 16)));
         kw[q][x][0] = v.x, kw[q][x][1] = v.y, kw[q][x][2 % W] = v.z, kw[q][x][3 % W] = v.w;
-        ks[q][x] = src ? __ldg(reinterpret_cast<const uint16_t *>(src + kv4_k_scale<D>(tok, 2 * t))) : 0u;
+        ks[q][x] = __ldg(reinterpret_cast<const uint16_t *>(src + kv4_k_scale<D>(tok, 2 * t)));
       } else {
-        const uint2 v = src ? __ldg(reinterpret_cast<const uint2 *>(src + kv4_k_code<D>(tok, t * 8))) : make_uint2(0, 0);
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + kv4_k_code<D>(tok, t * 8)));
         kw[q][x][0] = v.x, kw[q][x][1] = v.y;
-        ks[q][x] = src ? __ldg(src + kv4_k_scale<D>(tok, t)) : 0u;
+        ks[q][x] = __ldg(src + kv4_k_scale<D>(tok, t));
       }
     }
   };
   auto loaded = [&]() {
     ++ahead_i;
-    if (--ahead_left > 0 && ahead_i == 8)
-      for (int i = 0; i < 8; ++i) next_unit(c, ahead);  // (eight more units were looked up, so eight are behind)
+    if (--ahead_left > 0 && ahead_i == kLook)
+      for (int i = 0; i < kLook; ++i) next_unit(c, ahead);
   };
   look();
 #pragma unroll
-  for (int q = 0; q < 4; ++q) load(q);
+  for (int q = 0; q < kGroups; ++q) load(q);
   loaded();
 
   uint2 qf[NQ][KS];              // B operand: lane (g, t) = row g of the block, channels t D / 4 ...
@@ -236,7 +235,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
         const int sees = lse == -INFINITY ? -1 : s.len - n + tok;
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
-          rc[nq][e2] = c2 * __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(127 - e) << 23), (2 * t + e2) * 4);
+          // (a row that is none, or saw nothing: 0 throughout)
+          rc[nq][e2] = c2 * __shfl_sync(0xffffffffu, sees < 0 ? 0.0f : __uint_as_float((uint32_t)(127 - e) << 23), (2 * t + e2) * 4);
           hi[nq][e2] = __shfl_sync(0xffffffffu, rw.hi, (2 * t + e2) * 4);
           wt[nq][e2] = __shfl_sync(0xffffffffu, rw.w, (2 * t + e2) * 4);
           last[nq][e2] = __shfl_sync(0xffffffffu, sees, (2 * t + e2) * 4);
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
     const bool more = left > 1;
     if (more) look();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kGroups; ++q) {
       float d[NQ][4];
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq)
@@ -283,8 +283,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float z = ex2(fmaf(d[nq][2 * x + e2], rc[nq][e2], -hi[nq][e2]));
-            // a weight of 0 belongs to a row that is none (its z may be anything)
-            if (edge ? cur.pos + q * 16 + g + 8 * x <= last[nq][e2] : wt[nq][e2] != 0.0f) v[x] = fmaf(z, wt[nq][e2], v[x]);
+            if (!edge || cur.pos + q * 16 + g + 8 * x <= last[nq][e2]) v[x] = fmaf(z, wt[nq][e2], v[x]);
           }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
