@@ -197,7 +197,7 @@ cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms
 struct Kv4Pieces {
   const float *part, *ml;
   const int32_t *ends;
-  int rows, groups;  // rows of an item, at most; items of a sequence and KV head
+  int rows, groups, runs;  // rows of an item, at most; items of a sequence and KV head; runs
 };
 Kv4Pieces kv4_decode_pieces(const Kv4AttnArgs &a, const void *workspace, int num_sms);
 constexpr float kKv4PieceShift = 7.0f;  // the decode kernel's weights are 2^(z - m + 7)

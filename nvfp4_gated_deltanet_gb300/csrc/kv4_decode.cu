@@ -925,7 +925,7 @@ Kv4Pieces kv4_decode_pieces(const Kv4AttnArgs &a, const void *workspace, int num
   const DecodePlan d = decode_plan(a, num_sms, true);
   const int rows = 8 * d.NQ;
   const float *part = static_cast<const float *>(workspace), *ml = part + 2 * (size_t)d.runs * rows * a.c.D;
-  return {part, ml, reinterpret_cast<const int32_t *>(ml + 4 * (size_t)d.runs * rows), rows, d.RG};
+  return {part, ml, reinterpret_cast<const int32_t *>(ml + 4 * (size_t)d.runs * rows), rows, d.RG, d.runs};
 }
 
 cudaError_t launch_kv4_decode(const Kv4AttnArgs &a, void *workspace, int num_sms, cudaStream_t stream, float *raw,

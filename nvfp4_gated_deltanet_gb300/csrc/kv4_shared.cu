@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(256, 3) kv4_merge_kernel(SharedKv4 p) {
         np = 1;
         src = p.w.pre + ((size_t)h * D + ch0 + warp * 4) * p.rows + row;
         ml = reinterpret_cast<const float2 *>(p.w.pre_ml) + (size_t)h * p.rows + row;
-      } else {
+      } else if (e.x < 2 * p.runs && e.y >= e.x / 2 && e.y < p.runs) {  // (else a wait gave up before they were written)
         np = e.y - e.x / 2 + 1;
         src = p.w.part + ((size_t)e.x * D + ch0 + warp * 4) * p.ld + in;
         ml = reinterpret_cast<const float2 *>(p.w.part_ml) + (size_t)e.x * p.ld + in;
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(256, 3) kv4_merge_kernel(SharedKv4 p) {
       o = *reinterpret_cast<const float4 *>(p.w.own + out * D + ch);
       m = x.x;
       l = x.y;
-    } else {
+    } else if (e.x < 2 * p.own.runs && e.y >= e.x / 2 && e.y < p.own.runs) {
       const int in = f - rg * p.own.rows, np = e.y - e.x / 2 + 1;
       for (int j = 0; j < np; ++j) {
         const size_t at = (size_t)(j == 0 ? e.x : 2 * (e.x / 2 + j)) * p.own.rows + in;
