@@ -63,8 +63,8 @@ def test_samples_of_a_long_prompt(g, stream):
                 before = c.scores[l].double().sum(-1)
                 c.score(l, q, lse, batch)
                 more = c.scores[l].double().sum(-1) - before
-                used = [c._slot[s] for s in seqs]
-                assert ((more[used] / (hq // hkv) - 1).abs() < 4 * ONE).all()  # (a difference of sums) and not more[[i for i in range(6) if i not in used]].any()
+                used = [c._slot[s] for s in seqs]                # (differences of sums: four times the bound)
+                assert ((more[used] / (hq // hkv) - 1).abs() < 4 * ONE).all() and not more[[i for i in range(6) if i not in used]].any()
         # the prompt's owner and a sample are cut, the others keep theirs
         was = {(l, s): held(g, c, l, s) for l in range(L) for s in seqs}
         scores = {s: c.scores[:, c._slot[s]].clone() for s in seqs}
