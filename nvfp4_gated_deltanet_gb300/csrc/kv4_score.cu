@@ -323,7 +323,7 @@ constexpr int kWeigh = 4 * kAccs; // warps
 constexpr int kTileThreads = 32 * (kWeigh + 8);
 constexpr int kKCol = kAccs * kRow;  // TMEM column of the two items' K
 constexpr int kLses = 8;          // tiles whose rows' lse is in shared memory
-constexpr int kTileItem = 1;      // what an item costs beside its tiles, in tiles
+constexpr int kTileItem = 8;      // what an item costs beside its tiles, in tiles (masked ones among them): 1 / 4 / 8 / 12 gave 196 / 169 / 167 / 170 us
 constexpr int kOpen = 4;          // items whose sums are not all there
 
 struct ScoreInfo {  // of a run: what it leaves to be joined
@@ -580,7 +580,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
         tc_fence_after();
         // whole tiles: every row sees every token; their rows that are none have hi = infinity
         const bool mask = (w.kt + 1) * kTok - 1 > s.len - s.n + t * p.tpt || (t + 1) * p.tpt > s.n;
-        const int own = pos - (s.len - s.n) - t * p.tpt;  // the first of the tile's tokens that sees this one
+        // the tile's columns that see this token: from its first row that does, and only those that are rows
+        const int lo = max(0, pos - (s.len - s.n) - t * p.tpt) * p.G;
+        const unsigned width = (unsigned)max(0, (s.n - t * p.tpt) * p.G - lo);
         const float2 c2 = make_float2(p.c2, p.c2);
         const float4 *hi = reinterpret_cast<const float4 *>(row_hi + e8 * kRow);
         const uint32_t acc = base + i * kRow;
@@ -591,11 +593,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
             float2 z0 = fma2(make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), c2, make_float2(h.x, h.y));
             float2 z1 = fma2(make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])), c2, make_float2(h.z, h.w));
             z0.x = ex2(z0.x), z0.y = ex2(z0.y), z1.x = ex2(z1.x), z1.y = ex2(z1.y);
-            if constexpr (masked()) {  // rows that do not see the token, and those that are none
-              auto sees = [&](int col) {
-                const int tok = (int)(col * p.inv_g >> 16);
-                return tok >= own && t * p.tpt + tok < s.n;
-              };
+            if constexpr (masked()) {
+              auto sees = [&](int col) { return (unsigned)(col - lo) < width; };
               z0.x = sees(q * 16 + 4 * e) ? z0.x : 0.0f;
               z0.y = sees(q * 16 + 4 * e + 1) ? z0.y : 0.0f;
               z1.x = sees(q * 16 + 4 * e + 2) ? z1.x : 0.0f;
