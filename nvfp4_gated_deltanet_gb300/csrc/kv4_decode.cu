@@ -271,7 +271,8 @@ GDN_DEV int32_t *join_ends(const DecodeArgs &p, int runs, int rows) {
   return reinterpret_cast<int32_t *>(p.part + 2 * (size_t)runs * rows * (D + 2));
 }
 
-template <int D, int NQ, int TEAM>
+// RAW: sums instead of results (launch_kv4_decode).
+template <int D, int NQ, int TEAM, bool RAW>
 __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_decode_kernel(DecodeArgs p) {
   using S = DecodeShape<D, NQ, TEAM>;
   constexpr int TILE = S::kTile, GR = S::kGroups, W = S::kTeam;
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     *abort_flag = 0u;
     fence_barrier_init();
   }
-  if (!p.early) kv4_begin();
-  else pdl_launch_dependents();
+  if (RAW && p.early) pdl_launch_dependents();
+  else kv4_begin();
   __syncthreads();
   Cursor cur;
   int n_tiles;
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     volatile Found *found = reinterpret_cast<volatile Found *>(meet);
     if (warp < 2) {
       int extra = p.extra;
-      if (p.raw) {  // the host knows no bound of these lengths that says much
+      if (RAW) {  // the host knows no bound of these lengths that says much
         int most = 0;
         for (int b = lane; b < c.B; b += 32) most = max(most, kv4_len(c, b));
         if (__all_sync(0xffffffffu, most <= p.whole)) extra = kWhole;
@@ -684,7 +685,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
       }
       if (done) {
         const long long out = ((long long)cur.b * p.r + rg.token(row)) * p.a.Hq + rg.h * p.G + rg.head(row);
-        if (p.raw) {
+        if (RAW) {
           *reinterpret_cast<float4 *>(p.raw + out * D + d4) = o;
           if (d4 == 0) *reinterpret_cast<float2 *>(p.raw_ml + out * 2) = make_float2(top - kShift, sum);
           continue;
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
       }
     }
     // for the join: an item's first piece (-1: it is done) and the run of its last one
-    if (tid == 0 && (p.extra != kWhole || p.raw)) {
+    if (tid == 0 && (RAW || p.extra != kWhole)) {
       int32_t *ends = join_ends<D>(p, gridDim.x * S::kTeams, S::kRows) + 2 * ((long long)cur.b * HR + cur.hr);
       if (cur.tile == 0) ends[0] = done ? -1 : (int)piece;
       if (cur.tile + seg == cur.nt) ends[1] = run;
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NQ, TEAM>::kThreads, 1) kv4_dec
     if (held > 0) mbar_wait(my_full + slot, turn);
     if (held > 1) mbar_wait(my_full + (slot ^ 1), slot == 0 ? turn : turn ^ 1u);
   }
-  if (p.early) pdl_wait();  // this grid must not end before the one it follows
+  if (RAW && p.early) pdl_wait();  // this grid must not end before the one it follows
 }
 
 // Join R rows, from `row`, of pieces j0, j0 + step, ... < np: U at a time are in flight.
@@ -854,12 +855,16 @@ __global__ void __launch_bounds__(256, 3) kv4_join_kernel(DecodeArgs p, int runs
 template <int D, int NQ, int TEAM>
 cudaError_t launch_decode_t(const DecodeArgs &p, int ctas, cudaStream_t stream) {
   using S = DecodeShape<D, NQ, TEAM>;
-  static bool allowed[64];
-  cudaError_t e = kv4_allow_smem(kv4_decode_kernel<D, NQ, TEAM>, S::kBytes, allowed);
+  static bool allowed[64], allowed_raw[64];
+  if (p.raw) {
+    const cudaError_t e = kv4_allow_smem(kv4_decode_kernel<D, NQ, TEAM, true>, S::kBytes, allowed_raw);
+    return e != cudaSuccess ? e : kv4_launch(kv4_decode_kernel<D, NQ, TEAM, true>, ctas, S::kThreads, S::kBytes, stream, p);
+  }
+  cudaError_t e = kv4_allow_smem(kv4_decode_kernel<D, NQ, TEAM, false>, S::kBytes, allowed);
   if (e != cudaSuccess) return e;
-  e = kv4_launch(kv4_decode_kernel<D, NQ, TEAM>, ctas, S::kThreads, S::kBytes, stream, p);
+  e = kv4_launch(kv4_decode_kernel<D, NQ, TEAM, false>, ctas, S::kThreads, S::kBytes, stream, p);
   const int most = ctas * S::kTeams;  // runs, and cuts but one
-  if (e != cudaSuccess || p.extra == kWhole || most < 2 || p.raw) return e;
+  if (e != cudaSuccess || p.extra == kWhole || most < 2) return e;
   const int rows = std::min(int(S::kRows), p.r * p.G);
   const dim3 grid(TEAM ? std::min(p.items, 8 * 152) : p.items, TEAM ? (rows + 7) / 8 : rows);
   return kv4_launch(kv4_join_kernel<D, TEAM == 0>, grid, 256, 0, stream, p, most, int(S::kRows));
