@@ -438,10 +438,11 @@ typedef struct {
  * tokens have a score; the others' begin at 0, whatever `in` holds there. Rows
  * of slots that the batch does not name, and a row's places from kv_len on, are
  * left alone. A sequence whose slot is out of range or named twice, or whose
- * tokens a row does not hold, sets GDN_E_RANGE and is left out. q enters in FP16
- * scaled by a power of two per row, as in kv4_decode, K exactly; products,
- * exponentials and sums are FP32, in an order that depends on the sizes and the
- * table's width alone. workspace: kv4_score_workspace bytes (0: may be NULL).
+ * tokens a row does not hold, sets GDN_E_RANGE and is left out. K and
+ * q enter exactly (for up to 16 rows per sequence and KV head q in FP16 scaled by a
+ * power of two per row, as in kv4_decode); products, exponentials and sums are FP32,
+ * in an order that depends on the whole batch's lengths and rows and on the table's
+ * width, not on anything else. workspace: kv4_score_workspace bytes (0: may be NULL).
  * Errors: as kv4_append; GDN_E_SHAPE for heads as kv4_decode, for `out` that
  * overlaps `in` in part, for a workspace that is too small. v_scale is not used. */
 gdn_status kv4_score(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int n_q_heads,
@@ -458,7 +459,7 @@ size_t kv4_score_workspace(const kv4_cache *c, const kv4_batch *b, int n_q_heads
  * score_stride floats apart) choose for themselves. The rest of the last group
  * of 16 places gets zeros; the old pages are left as they are.
  *   keep: device [B]; new_table: device [B][new_pages], none of whose pages may
- *   be among the batch's own; kept: device [n_layers][B][n_kv_heads][max_keep],
+ *   be named twice or be among the batch's own; kept: device [n_layers][B][n_kv_heads][max_keep],
  *   -1 past a sequence's k; new_len: device [B], k.
  * A sequence with a bad kv_len, keep (below 0, or a k beyond max_keep or the
  * new pages) or slot (out of range, named twice) sets GDN_E_RANGE and is left

@@ -60,7 +60,7 @@ size_t lay_out(const Kv4SharedArgs &s, uint8_t *base, int num_sms, SharedKv4 &p)
   p.r = c.T / c.B;
   p.G = s.a.Hq / c.Hkv;
   p.rows = c.T * p.G;
-  p.slots = p.rows / kItemRows + s.groups + 1;  // item_slot
+  p.slots = p.rows / kItemRows + s.groups + 1;  // Place::slot
   p.ld = std::min(kItemRows, (p.rows + 31) / 32 * 32);
   p.runs = s.groups ? (int)std::min((long long)num_sms, prefix_tiles(s, p.slots)) : 0;
   size_t at = 0;
@@ -154,9 +154,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
     p.w.own_len[b] = len - skip;
     p.w.seq_item[b] = make_int2(row0, skip > 0 ? row0 / kItemRows + g : -1);
   }
-  const int from = skip / c.page_tokens;
-  for (int i = tid; i < c.cols; i += kPlanThreads)
-    p.w.own_table[(size_t)b * c.cols + i] = from + i < c.cols ? c.table[(size_t)b * c.cols + from + i] : -1;
+  const int from = skip / c.page_tokens, pages = (len - skip + c.page_tokens - 1) / c.page_tokens;
+  for (int i = tid; i < pages; i += kPlanThreads)  // (from + pages is at most cols: the length is checked)
+    p.w.own_table[(size_t)b * c.cols + i] = c.table[(size_t)b * c.cols + from + i];
 }
 
 // ---------------------------------------------------------------- the shared tokens
@@ -174,10 +174,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
 //   warp 17           streams the cached bytes by bulk copies
 // The softmax warps take over registers (160, 56 and 48 of 96 each), enough for half
 // of a row's 128 scores at a time, which are read from tensor memory twice (with all
-// of them in registers there is room for four decoding warps only, a warp on each
-// scheduler, which then take 5000 cycles a tile: 140 us instead of 95 for 1024 rows
-// of each of 4 KV heads on 65536 tokens). K and V are exact in FP16 (six significant
-// bits).
+// of them in registers there was room for four decoding warps only, one on each
+// scheduler, which then set the pace: 177 us instead of 150 for 1024 rows of each of 4
+// KV heads on 65536 tokens, the whole call). K and V are exact in FP16 (six
+// significant bits). Measured now, those rows: 108 us in this kernel, 1.27 PFLOP/s
+// (0.67 of a large BF16 product); the tensor pipe is busy half of the time, held up by
+// shared memory's bandwidth (queries and K of S = Q K^T both come from there, and the
+// decoded tiles go there) and by a row tile's chain of softmax and products.
 // The weights are 2^(z - m + 6), with a maximum m that is only moved (and O
 // rescaled in tensor memory) when the row's true maximum passes it by 8.
 // Every wait is bounded; one that gives up sets GDN_E_TIMEOUT and an abort flag

@@ -471,6 +471,8 @@ class KV4Cache:
         queries and the log-sum-exp of decode, decode_shared or prefill. q_start
         [B + 1]: q holds only these of the newest rows (a prompt's window)."""
         self._needs_scores()
+        if batch.T == 0:
+            return
         if q.dim() == 4:
             self._same_rows(q, batch)
         elif q_start is None:

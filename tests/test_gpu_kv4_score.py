@@ -197,6 +197,18 @@ def test_extreme_rows(g):
     assert (out - 1 / 333).abs().max() < 2.0 ** -15 / 333  # the lse is good to 2^-16 and a little
 
 
+def test_no_rows(g):
+    """Nothing is added; tokens without a score get one of 0."""
+    pages, table, n = cached(g, [70, 0, 33], 16, 2, 64)
+    old = torch.rand(3, 2, 80, device="cuda")
+    q, lse = torch.empty(0, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 8, device="cuda")
+    out, st = torch.full_like(old, 9.0), ints([0])
+    g.kv4_score(q, lse, pages, table, n, old, KS, q_start=ints([0] * 4), scored=ints([50, 0, 0]), out=out, dev_status=st)
+    want = torch.full_like(old, 9.0)
+    want[0, :, :50], want[0, :, 50:70], want[2, :, :33] = old[0, :, :50], 0, 0
+    assert torch.equal(out, want) and st.item() == 0
+
+
 def test_captured_and_replayed_on_a_side_stream(g):
     """In a graph, on another stream; lengths that have grown since the capture are read anew."""
     hq, hkv, d, lens = 8, 2, 128, [300, 90]

@@ -129,6 +129,9 @@ def test_cache_scores_and_evicts(g, monkeypatch):
     batch = c.batch([a, b], [2, 1])
     c.score(0, torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 4), batch)
     assert calls[-1][2]["q_start"] is batch.q_start
+    n = len(calls)
+    c.score(0, q[:0], lse[:0], c.batch([a, b], [0, 0]))               # no rows: nothing to add
+    assert len(calls) == n
     batch = c.grow([a, b], [3, 0])                                    # three that are not scored
     with pytest.raises(ValueError, match="no score"):
         c.evict([a, b], 20, recent=2)
