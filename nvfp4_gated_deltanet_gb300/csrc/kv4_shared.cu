@@ -182,12 +182,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
 // shared memory's bandwidth (queries and K of S = Q K^T both come from there, and the
 // decoded tiles go there) and by a row tile's chain of softmax and products.
 // The weights are 2^(z - m + 6), with a maximum m that is only moved (and O
-// rescaled in tensor memory) when the row's true maximum passes it by 8.
+// rescaled in tensor memory) when a tile's weights come to 2^14 or more by it.
 // Every wait is bounded; one that gives up sets GDN_E_TIMEOUT and an abort flag
 // that ends every role's loop.
 constexpr int kKv = 128;
 constexpr int kPrefixThreads = 640;
-constexpr float kShift = 6.0f, kSlack = 8.0f;
+constexpr float kShift = 6.0f, kMost = 16384.0f;
 // What an item costs beside its tiles, in tiles: its queries, its sums and their joining.
 constexpr int kItemCost = 2;
 
@@ -432,61 +432,71 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
               if (64 * half + q >= valid) s[q] = -INFINITY;
           }
         };
-        float s[64], x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // The weights by the maximum so far, and their sum over the tile: below kMost it shows that no weight passes
+        // what FP16 holds, without a look at every score before (the whole call on those 1024 rows of 4 KV heads: 128.5 -> 124.9
+        // us). Where it does not, and in an item's first tile, the maximum is found first. Decided by a row's own sum: a
+        // row's result depends on no other row.
+        float s[64];
+        uint32_t weight[2][32];
+        float2 sum[2];
+        bool up = j == 0;
+        for (bool look = j == 0;; look = true) {
+          if (look) {
+            float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              half_scores(half, s);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // the second stays in s
-          half_scores(half, s);
+              for (int q = 0; q < 64; q += 4)
 #pragma unroll
-          for (int q = 0; q < 64; q += 4)
+                for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
+            }
+            const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * cs;
+            if (j > 0) {
+              // S of this tile is complete, so the O += P V issued before it is too
+              const float f = up && top != m ? ex2(m - top) : 1.0f;
+              l *= f;
+#pragma unroll 1
+              for (int q = 0; q < D; q += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + q, o);
+                tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x4[e] = fmaxf(x4[e], s[q + e]);
-        }
-        const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * cs;
-        const bool up = top > m + kSlack;  // decided row by row: a row's result depends on no other row
-        if (j == 0) {
-          m = top;
-        } else if (__any_sync(0xffffffffu, up)) {
-          // S of this tile is complete, so the O += P V issued before it is too
-          const float f = up ? ex2(m - top) : 1.0f;
-          if (up) m = top;
-          l *= f;
-#pragma unroll
-          for (int q = 0; q < D; q += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + q, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(tO + q, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(tO + q, o);
+              }
+            }
+            if (up) m = top;
           }
-        }
-        const float off = kShift - (m == -INFINITY ? 0.0f : m);
-        const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
-        float2 sum[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
-        auto weigh = [&](const float (&s)[64], uint32_t (&x)[32]) {
+          const float off = kShift - (m == -INFINITY ? 0.0f : m);
+          const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
+          sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), cs2, off2);
-            z.x = ex2(z.x);
-            z.y = ex2(z.y);
-            sum[e & 1] = add2(sum[e & 1], z);
-            x[e] = h2u(__floats2half2_rn(z.x, z.y));
+          for (int half = 0; half < 2; ++half) {
+            half_scores(half, s);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), cs2, off2);
+              z.x = ex2(z.x);
+              z.y = ex2(z.y);
+              sum[e & 1] = add2(sum[e & 1], z);
+              weight[half][e] = h2u(__floats2half2_rn(z.x, z.y));
+            }
           }
-        };
-        auto put = [&](int half, const uint32_t (&x)[32]) {
-          tmem_st32(tS + 64 + 32 * half, x);
+          sum[0] = add2(sum[0], sum[1]);
+          if (look) break;
+          up = !(sum[0].x + sum[0].y < kMost && m > -INFINITY);
+          if (!__any_sync(0xffffffffu, up)) break;
+        }
+        l += sum[0].x + sum[0].y;
+        // P overlies S's second half; tokens 64 .. go to the products first
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+          tmem_st32(tS + 64 + 32 * half, weight[half]);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(p_ready + 2 * i + half);
-        };
-        uint32_t x[32];
-        weigh(s, x);  // tokens 64 ..: weights in columns 96 .., which only they held
-        put(1, x);
-        half_scores(0, s);
-        weigh(s, x);
-        put(0, x);
-        sum[0] = add2(sum[0], sum[1]);
-        l = sum[0].x + sum[0].y;
+        }
       }
       // ---- the row's sums, channel by channel: 32 rows are a line
       const bool whole = nkv == w.nt;
@@ -687,12 +697,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
 // row, 8 of them in flight; then, four channels a thread, what the sequence has for
 // itself. Bound by latency: the row's item, its ends, the pieces.
 template <int D>
-__global__ void __launch_bounds__(256, 3) kv4_merge_kernel(SharedKv4 p) {
-  constexpr int U = 8;
+__global__ void __launch_bounds__(256, 2) kv4_merge_kernel(SharedKv4 p) {
+  constexpr int U = 12;
   __shared__ float sums[32][33], pre_m[32], pre_l[32];
   kv4_begin();
   const Kv4Args &c = p.s.a.c;
   const int h = blockIdx.y, ch0 = blockIdx.z * 32;
+  const int r = threadIdx.x / 8, ch = ch0 + threadIdx.x % 8 * 4, row = blockIdx.x * 32 + r;
+  const bool have = row < p.rows;
+  const int tok = have ? row / p.G : 0, b = tok / p.r, q = row - tok * p.G;
+  const long long out = (long long)tok * p.s.a.Hq + h * p.G + q;
+  // where its own lies: asked for before the prefix's pieces, whose loads take as long again
+  const int own_f = row - b * p.r * p.G, own_g = p.own.groups == 1 ? 0 : own_f / p.own.rows;
+  const int2 own_e = have ? reinterpret_cast<const int2 *>(p.own.ends)[((size_t)b * c.Hkv + h) * p.own.groups + own_g] : make_int2(0, -1);
   {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
     const int2 item = row < p.rows && p.runs ? p.w.seq_item[row / p.G / p.r] : make_int2(-1, -1);
@@ -750,23 +767,18 @@ __global__ void __launch_bounds__(256, 3) kv4_merge_kernel(SharedKv4 p) {
       pre_l[lane] = l;
     }
   }
-  const int r = threadIdx.x / 8, ch = ch0 + threadIdx.x % 8 * 4, row = blockIdx.x * 32 + r;
-  const bool have = row < p.rows;
-  const int tok = have ? row / p.G : 0, b = tok / p.r, q = row - tok * p.G;
-  const long long out = (long long)tok * p.s.a.Hq + h * p.G + q;
   // ---- the sequence's own: whole, or its pieces
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (have) {
-    const int f = row - b * p.r * p.G, rg = p.own.groups == 1 ? 0 : f / p.own.rows;
-    const int2 e = reinterpret_cast<const int2 *>(p.own.ends)[((size_t)b * c.Hkv + h) * p.own.groups + rg];
+    const int2 e = own_e;
     if (e.x < 0) {
       const float2 x = reinterpret_cast<const float2 *>(p.w.own_ml)[out];
       o = *reinterpret_cast<const float4 *>(p.w.own + out * D + ch);
       m = x.x;
       l = x.y;
     } else if (e.x < 2 * p.own.runs && e.y >= e.x / 2 && e.y < p.own.runs) {
-      const int in = f - rg * p.own.rows, np = e.y - e.x / 2 + 1;
+      const int in = own_f - own_g * p.own.rows, np = e.y - e.x / 2 + 1;
       for (int j = 0; j < np; ++j) {
         const size_t at = (size_t)(j == 0 ? e.x : 2 * (e.x / 2 + j)) * p.own.rows + in;
         float2 x = reinterpret_cast<const float2 *>(p.own.ml)[at];

@@ -162,3 +162,13 @@ def test_queries_of_extreme_size(g):
     q[0, 0], q[0, 1], q[1, 3] = 0, q[0, 1] * 300, q[1, 3] * 2.0 ** -40
     out, lse = g.kv4_decode_shared(q, pages, table, n, start, shared, KS, VS, return_lse=True)
     close(out, lse, attention(pages, table, lens, [1, 1], q, 128), 128)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_maximum_that_moves(g, d):
+    """Queries up to forty times as large: their maximum rises in several tiles of the prefix, in some rows of a warp only."""
+    pages, table, n, start, shared, lens = prefixed(g, [(4000, [4100, 4001, 4200, 4030, 4007])], 32, 2, d, 8)
+    q = queries(5, 16, d, 8)
+    q *= torch.tensor([1, 4, 13, 40], device="cuda").repeat(4)[None, :, None]
+    out, lse = g.kv4_decode_shared(q, pages, table, n, start, shared, KS, VS, return_lse=True)
+    close(out, lse, attention(pages, table, lens, [1] * 5, q, d), d)
