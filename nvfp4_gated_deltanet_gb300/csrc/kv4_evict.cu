@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
   constexpr int BITS = CS > 1 ? 8 : 11, BINS = 1 << BITS, PER = BINS > THREADS ? BINS / THREADS : 1, WARPS = THREADS / 32;
   constexpr int SHARE = CS > 1 ? BINS / CS : 1;  // bins whose counts a CTA of the cluster adds up
   extern __shared__ __align__(16) float held[];  // the slice's scores
-  __shared__ unsigned hist[2][BINS], gathered[2][SHARE], sums[33], range[2][32], ext[2], mine[2], found[2];
+  __shared__ unsigned hist[2][BINS], gathered[2][SHARE], sums[33], range[2][32], ext[2], mine[2], found[3];
   kv4_begin();
   const Kv4Args &c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
       if (before < need && before + v[x] >= need) {
         found[0] = BINS - 1 - (tid * PER + x);
         found[1] = before;
+        found[2] = v[x];
       }
       before += v[x];
     }
@@ -240,6 +241,11 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
     low += found[0] << shift;
     need -= found[1];
     if (shift == 0) break;
+    if (found[2] == need && low > 0) {  // the whole bin is kept
+      --low;
+      need = 0;
+      break;
+    }
     width = shift;
     shift = max(0, shift - BITS);
     __syncthreads();  // everybody has read `found`, and (one CTA) the counts
