@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
   constexpr int BITS = CS > 1 ? 8 : 11, BINS = 1 << BITS, PER = BINS > THREADS ? BINS / THREADS : 1, WARPS = THREADS / 32;
   constexpr int SHARE = CS > 1 ? BINS / CS : 1;  // bins whose counts a CTA of the cluster adds up
   extern __shared__ __align__(16) float held[];  // the slice's scores
-  __shared__ unsigned hist[2][BINS], gathered[2][SHARE], sums[33], range[2][32], ext[2], mine[2], found[3];
+  __shared__ __align__(16) unsigned hist[2][BINS];
+  __shared__ unsigned gathered[2][SHARE], sums[33], range[2][32], ext[2], mine[2], found[3];
   kv4_begin();
   const Kv4Args &c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -148,11 +149,10 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
     for (int x = 0; x < E; ++x) {
       const int i = w0 + x * 32 + lane;
       if (i < w1) held[i] = f[x];
-      o[x] = order_of(f[x]);
-      if (i < w1 && i < rivals) {
-        lo = min(lo, o[x]);
-        hi = max(hi, o[x]);
-      }
+      const bool rival = i < min(w1, rivals);
+      o[x] = rival ? order_of(f[x]) : 0u;  // 0 is never above what is kept
+      lo = min(lo, rival ? o[x] : ~0u);
+      hi = max(hi, o[x]);
     }
   } else {
     for (int i = tid; i < len; i += THREADS) {
@@ -190,17 +190,19 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
   for (int pass = 0; some; ++pass) {
     unsigned *cnt = hist[pass & 1];
     unsigned first = 0;  // tokens in the lowest bin: many scores are equal where attention never looked
+    const uint32_t last = width >= 32 ? ~0u : (1u << width) - 1u;
     auto count = [&](uint32_t x) {
       const uint32_t t = x - low;
-      if (x >= low && (width >= 32 || (t >> width) == 0)) {
+      if (x >= low && t <= last) {
         if ((t >> shift) == 0) ++first;
         else atomicAdd(&cnt[t >> shift], 1u);
       }
     };
     if constexpr (E > 0) {
+      // (one that does not compete is an order of 0: where that is in a bin at all it is the lowest one, whose count
+      // then is too large for an early end, and for nothing else)
 #pragma unroll
-      for (int x = 0; x < E; ++x)
-        if (w0 + x * 32 + lane < min(w1, rivals)) count(o[x]);
+      for (int x = 0; x < E; ++x) count(o[x]);
     } else {
       for (int i = tid; i < rivals; i += THREADS) count(order_of(score(i)));
     }
@@ -223,8 +225,20 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
       sum = v[0];
     } else {
       __syncthreads();
+      constexpr int W = PER % 4 == 0 ? 4 : PER;  // words of a load
 #pragma unroll
-      for (int x = 0; x < PER; ++x) sum += v[x] = cnt[BINS - 1 - (tid * PER + x)];
+      for (int x = 0; x < PER; x += W) {
+        const unsigned *at = cnt + BINS - (tid * PER + x) - W;
+        if constexpr (W == 4) {
+          const uint4 y = *reinterpret_cast<const uint4 *>(at);
+          v[x] = y.w, v[x + 1] = y.z, v[x + 2] = y.y, v[x + 3] = y.x;
+        } else {
+#pragma unroll
+          for (int e = 0; e < W; ++e) v[x + e] = at[W - 1 - e];
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) sum += v[x + e];
+      }
     }
     // bin x holds the place `need` when the bins above it hold fewer than `need` and with it at least as many
     unsigned before = block_before<THREADS>(sum, sums, total);
@@ -259,11 +273,12 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
   unsigned above = 0, at = 0;
   if constexpr (E > 0) {
 #pragma unroll
-    for (int x = 0; x < E; ++x) {
-      unsigned over, same;
-      kinds(w0 + x * 32, o[x], over, same);
-      above += __popc(over);
-      at += __popc(same);
+    for (int x = 0; x < E; ++x) above += some && o[x] > low;
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (need > 0) {
+#pragma unroll
+      for (int x = 0; x < E; ++x) at += o[x] == low && w0 + x * 32 + lane < min(w1, rivals);
+      at = __reduce_add_sync(0xffffffffu, at);
     }
   } else if (HELD) {
     for (int j = w0; j < w1; j += 32) {
@@ -274,10 +289,19 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
     }
   }
   unsigned a_all, t_all;
-  const unsigned a0 = block_before<THREADS>(lane == 0 ? above : 0u, sums, a_all);
-  const unsigned t0 = block_before<THREADS>(lane == 0 ? at : 0u, sums, t_all);
-  above = __shfl_sync(0xffffffffu, a0, 0);
-  at = __shfl_sync(0xffffffffu, t0, 0);
+  if constexpr (E > 0) {  // a slice has fewer than 2^16 tokens
+    static_assert(THREADS * E < 65536);
+    const unsigned both = __shfl_sync(0xffffffffu, block_before<THREADS>(lane == 0 ? above | at << 16 : 0u, sums, a_all), 0);
+    above = both & 0xffffu;
+    at = both >> 16;
+    t_all = a_all >> 16;
+    a_all &= 0xffffu;
+  } else {
+    const unsigned a0 = block_before<THREADS>(lane == 0 ? above : 0u, sums, a_all);
+    const unsigned t0 = block_before<THREADS>(lane == 0 ? at : 0u, sums, t_all);
+    above = __shfl_sync(0xffffffffu, a0, 0);
+    at = __shfl_sync(0xffffffffu, t0, 0);
+  }
   if (CS > 1) {
     if (tid == 0) {
       mine[0] = a_all;
@@ -291,21 +315,32 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
     unsigned over, same;
     kinds(j, x, over, same);
     const unsigned before = (1u << lane) - 1u, a = above + __popc(over & before), t = at + __popc(same & before);
-    const int i = i0 + j + lane;
-    int to = -1;
-    if ((over >> lane & 1) || ((same >> lane & 1) && t < need)) to = (int)(a + min(t, need));
-    else if (j + lane < w1 && i >= m) to = k - r + (i - m);
-    if (to >= 0) {
-      kept[to] = i;
+    if ((over >> lane & 1) || ((same >> lane & 1) && t < need)) {
+      const unsigned to = a + min(t, need);
+      kept[to] = i0 + j + lane;
       out[to] = held[j + lane];
     }
     above += __popc(over);
     at += __popc(same);
   };
   if constexpr (E > 0) {
+    if (!some) {
+    } else if (need > 0) {
 #pragma unroll
-    for (int x = 0; x < E; ++x)
-      if (w0 + x * 32 < w1) write(w0 + x * 32, o[x]);
+      for (int x = 0; x < E; ++x)
+        if (w0 + x * 32 < w1) write(w0 + x * 32, o[x]);
+    } else {  // none of those at low
+#pragma unroll
+      for (int x = 0; x < E; ++x) {
+        const unsigned over = __ballot_sync(0xffffffffu, o[x] > low);
+        if (o[x] > low) {
+          const unsigned to = above + __popc(over & ((1u << lane) - 1u));
+          kept[to] = i0 + w0 + x * 32 + lane;
+          out[to] = held[w0 + x * 32 + lane];
+        }
+        above += __popc(over);
+      }
+    }
   } else if (HELD) {
     for (int j = w0; j < w1; j += 32) write(j, j + lane < w1 ? order_of(held[j + lane]) : 0u);
   } else {  // in steps of the block, each read by all before any of it is written
@@ -335,6 +370,11 @@ __global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4EvictArgs p) {
     }
     __syncthreads();
   }
+  if (HELD)  // the newest
+    for (int i = rivals + tid; i < len; i += THREADS) {
+      kept[k - r + (i0 + i - m)] = i0 + i;
+      out[k - r + (i0 + i - m)] = held[i];
+    }
   for (int i = k + rank * THREADS + tid; i < n; i += CS * THREADS) out[i] = 0.0f;
   for (int i = k + rank * THREADS + tid; i < p.max_keep; i += CS * THREADS) kept[i] = -1;
   if (CS > 1) cluster_sync();  // nobody leaves while its counts are read
