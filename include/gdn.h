@@ -547,8 +547,8 @@ size_t kv4_compact_workspace(int num_pages);
  * whenever the form allows; 3 = weight-stationary whenever the form allows
  * (else as 2). knob 12: the budget, in SM cycles, of each grid-barrier wait of
  * the persistent single-kernel step (knob 3) and of each wait of kv4_append,
- * kv4_decode and kv4_prefill: 0 = the default, 2^31 (about one second); any
- * positive value sets it. A wait that runs out records GDN_E_TIMEOUT in the
+ * kv4_decode, kv4_decode_shared, kv4_prefill and kv4_score: 0 = the default, 2^31
+ * (about one second); any positive value sets it. A wait that runs out records GDN_E_TIMEOUT in the
  * status word and the kernel finishes without it (that step's results are then
  * meaningless); the next call starts clean (the barrier words are cleared
  * before every launch). A short budget exists to test that path: the barrier
