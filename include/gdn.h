@@ -438,11 +438,11 @@ typedef struct {
  * tokens have a score; the others' begin at 0, whatever `in` holds there. Rows
  * of slots that the batch does not name, and a row's places from kv_len on, are
  * left alone. A sequence whose slot is out of range or named twice, or whose
- * tokens a row does not hold, sets GDN_E_RANGE and is left out. K and
- * q enter exactly (for up to 16 rows per sequence and KV head q in FP16 scaled by a
- * power of two per row, as in kv4_decode); products, exponentials and sums are FP32,
- * in an order that depends on the whole batch's lengths and rows and on the table's
- * width, not on anything else. workspace: kv4_score_workspace bytes (0: may be NULL).
+ * tokens a row does not hold, sets GDN_E_RANGE and is left out (with n_slots 0
+ * nothing is done). K and q enter exactly (for up to 16 rows per sequence and KV
+ * head q in FP16 scaled by a power of two per row, as in kv4_decode); products,
+ * exponentials and sums are FP32, in an order that depends on the whole batch's
+ * lengths and rows and on the table's width, not on anything else. workspace: kv4_score_workspace bytes (0: may be NULL).
  * Errors: as kv4_append; GDN_E_SHAPE for heads as kv4_decode, for `out` that
  * overlaps `in` in part, for a workspace that is too small. v_scale is not used. */
 gdn_status kv4_score(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int n_q_heads,

@@ -119,12 +119,12 @@ gdn_status check_scores(const kv4_cache *c, const kv4_scores *s, int n_layers, i
   return GDN_OK;
 }
 
-gdn_status check_shared(const kv4_shared *s, Kv4SharedArgs &a) {
+gdn_status check_shared(const kv4_shared *s, int Hq, Kv4SharedArgs &a) {
   if (!s) return GDN_E_NULL;
   if (s->groups < 0 || s->max_shared < 0) return GDN_E_SHAPE;
   if (s->groups > 0 && (!s->group_start || !s->shared_len)) return GDN_E_NULL;
   if (s->groups > 0 && !words({s->group_start, s->shared_len})) return GDN_E_ALIGN;
-  if ((long long)a.a.c.B + s->groups > 0x7fffffffLL) return GDN_E_OVERFLOW;
+  if ((long long)a.a.c.T * Hq + s->groups > 0x7ffffff0LL) return GDN_E_OVERFLOW;  // T is B or more
   a.group_start = s->group_start;
   a.shared_len = s->shared_len;
   a.groups = s->groups;
@@ -213,7 +213,7 @@ gdn_status kv4_prefill(const kv4_cache *c, const kv4_batch *b, int64_t total_kv,
 size_t kv4_decode_shared_workspace(const kv4_cache *c, const kv4_batch *b, const kv4_shared *s, int n_q_heads) {
   Kv4SharedArgs a{};
   if (check(c, b, a.a.c, nullptr) != GDN_OK || b->T == 0 || b->q_start || !heads_fit(c, n_q_heads)) return 0;
-  if (check_shared(s, a) != GDN_OK) return 0;
+  if (check_shared(s, n_q_heads, a) != GDN_OK) return 0;
   a.a.Hq = n_q_heads;
   return kv4_decode_shared_bytes(a, kMaxSms);
 }
@@ -225,7 +225,7 @@ gdn_status kv4_decode_shared(const kv4_cache *c, const kv4_batch *b, const kv4_s
   gdn_status st = check_attn(c, b, q, q_stride, n_q_heads, sm_scale, out, lse, dev_status, a.a);
   if (st != GDN_OK) return st;
   if (b->q_start) return GDN_E_SHAPE;
-  st = check_shared(s, a);
+  st = check_shared(s, n_q_heads, a);
   if (st != GDN_OK || b->T == 0) return st;
   const size_t need = kv4_decode_shared_bytes(a, kMaxSms);
   if (!workspace) return GDN_E_NULL;
@@ -297,7 +297,8 @@ gdn_status kv4_evict(const kv4_cache *c, int n_layers, int64_t layer_stride, con
   if (!keep || !new_len || (max_keep > 0 && !kept) || (new_pages > 0 && !new_table)) return GDN_E_NULL;
   if (!words({keep, new_len, kept, new_table})) return GDN_E_ALIGN;
   const long long rows = (long long)b->B * c->n_kv_heads;
-  if (rows > 0x7fffffffLL / n_layers || rows * n_layers > 0x7fffffffLL / (max_keep / 128 + 1)) return GDN_E_OVERFLOW;
+  // up to 16 CTAs choose for a row, one moves 128 of its tokens
+  if (rows > 0x7fffffffLL / 16 / n_layers || rows * n_layers > 0x7fffffffLL / (max_keep / 128 + 1)) return GDN_E_OVERFLOW;
   a.layers = n_layers;
   a.layer_stride = layer_stride;
   a.score_layer = score_stride;

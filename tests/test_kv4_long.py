@@ -240,7 +240,7 @@ def test_decode_shared_refusals(g):
     assert call(stride=4 * 64 + 4) == 2 and call(n=16) == 2 and call(T=3) == 2 and call(head_dim=96) == 2
     assert call(group_start=GOOD + 2) == 3 and call(ws=GOOD + 8) == 3 and call(q=GOOD + 2) == 3
     assert call(sm=float("nan")) == 4 and call(sm=0.0) == 5 and call(v_scale=-1.0) == 5
-    assert call(T=0, B=0) == 0
+    assert call(T=0, B=0) == 0 and call(groups=2 ** 31 - 8) == 7
     c, b, _, h = structs(g)
     need = L.kv4_decode_shared_workspace(*refs(c, b, h), 4)
     assert need > 0 and call(n=need - 1) == 2
@@ -284,7 +284,7 @@ def test_evict_refusals(g):
     assert call(layers=2, stride=8 * page, score_stride=127) == 2 and call(out=GOOD + 256) == 2
     assert call(keep=GOOD + 2) == 3 and call(pages=GOOD + 8) == 3 and call(kept=GOOD + 3) == 3
     assert call(num_pages=2 ** 31 - 1, page_tokens=256, n_kv_heads=1024) == 7
-    assert call(most=2 ** 31 - 1, B=2 ** 10) == 7
+    assert call(most=2 ** 31 - 1, B=2 ** 10) == 7 and call(most=16, B=2 ** 27) == 7
     assert call(B=0, T=0) == 0
 
 
