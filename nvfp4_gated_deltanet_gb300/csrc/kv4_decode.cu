@@ -908,7 +908,8 @@ DecodePlan decode_plan(const Kv4AttnArgs &a, int num_sms, bool raw = false) {
   const int rounds = s.team * (d.small ? kRoundsTeam : kRoundsCta);
   d.whole = rounds * s.tile;
   d.extra = most <= rounds && !raw ? kWhole : d.small ? kExtraTeam : kExtraCta;
-  const long long n = d.extra == kWhole ? items : (items * most + s.team - 1) / s.team;  // runs that could have work
+  long long n = d.extra == kWhole ? items : (items * most + s.team - 1) / s.team;  // runs that could have work
+  if (raw) n = std::max(n, items);  // (a shared decode of 8 items of 8 own tokens by one run took 40 us, now 16)
   d.ctas = (int)(n < (long long)num_sms * s.teams ? (n + s.teams - 1) / s.teams : num_sms);
   d.runs = d.ctas * s.teams;
   d.bytes = d.extra == kWhole ? 0 : 2 * (size_t)d.ctas * s.teams * 8 * d.NQ * (a.c.D + 2) * sizeof(float) + 8 * (size_t)items;
