@@ -663,19 +663,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
       const int per = min(c.page_tokens / 16, 4);  // groups of a copy
       uint32_t x = 0;
       segments([&](int, const Place &w, int n) {
+        const uint8_t *src = nullptr;
         for (int j = 0; j < 2 * n; ++j, ++x) {
           const uint32_t s = x % NR;
-          const int pos = (w.tile * 2 + j) * 64 + lane * 16;
-          const uint8_t *src = nullptr;
-          if (lane < 4 && lane % per == 0 && pos < w.S) {
-            const uint8_t *g = kv4_group<D>(c, w.lead, pos);  // a bad page id (flagged) reads page 0
-            src = (g ? g : c.pages) + w.h * kv4_head_bytes<D>(c);
+          // the places of 512 tokens at once, 16 a lane (64 at a time, tiles waited for the page table: the 1024 rows above
+          // 124 us instead of 120, six groups of ten rows on up to 38928 tokens 160 instead of 122)
+          if (j % 8 == 0) {
+            const int pos = (w.tile * 2 + j) * 64 + lane * 16;
+            src = nullptr;
+            if (lane % per == 0 && pos < w.S && j + lane / 4 < 2 * n) {
+              const uint8_t *g = kv4_group<D>(c, w.lead, pos);  // a bad page id (flagged) reads page 0
+              src = (g ? g : c.pages) + w.h * kv4_head_bytes<D>(c);
+            }
           }
-          const int copies = __popc(__ballot_sync(0xffffffffu, src != nullptr));  // (whole pages are shared)
+          const bool now = src != nullptr && lane / 4 == j % 8;
+          const int copies = __popc(__ballot_sync(0xffffffffu, now));  // (whole pages are shared)
           if (x >= NR && !warp_wait_all(raw_free + s, x / NR - 1)) return false;
           if (lane == 0) mbar_arrive_expect_tx(raw_full + s, copies * per * 18 * D);
           __syncwarp();
-          if (src) bulk_g2s(raw + s * S::kRaw + lane * 18 * D, src, per * 18 * D, raw_full + s);
+          if (now) bulk_g2s(raw + s * S::kRaw + lane % 4 * 18 * D, src, per * 18 * D, raw_full + s);
         }
         return true;
       });
