@@ -190,6 +190,10 @@ constexpr int kPrefixThreads = 640;
 constexpr float kShift = 6.0f, kMost = 16384.0f;
 // What an item costs beside its tiles, in tiles: its queries, its sums and their joining.
 constexpr int kItemCost = 2;
+// Few long items are cut into less runs than there are CTAs, sqrt(16 tiles items): joining a piece takes about a
+// sixteenth of a tile. One item of 17, 26 or 4 sequences, 274, 301 and 204 tiles: 43.9, 39.6 and 39.8 us by all CTAs,
+// now 39.4, 28.4 and 31.9; by sqrt(8 ..) 38.1, 29.0 and 33.2, by sqrt(32 ..) 40.3, 31.3 and 35.1.
+constexpr float kFewPieces = 16.0f;
 
 template <int D>
 struct PrefixShape {
@@ -268,7 +272,9 @@ GDN_DEV long long find_cut(const SharedKv4 &p, int cut, int lane, Place &k) {
     total += warp_lsum(x.cost);
     tiles += warp_lsum(x.tiles);
   }
-  const long long n = max(1LL, min((long long)gridDim.x, tiles));
+  const long long items = (total - tiles) / kItemCost;
+  const float fine = sqrtf(kFewPieces * (float)tiles * (float)items);
+  const long long n = max(1LL, min(min((long long)gridDim.x, tiles), (long long)fine));
   if (cut >= n || tiles == 0) return tiles;
   const long long q = quot(total, n);
   long long u = q * cut + quot((total - q * n) * cut, n), before = 0;  // the cost at the cut, the tiles of the groups before
