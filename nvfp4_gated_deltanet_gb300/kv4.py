@@ -314,7 +314,7 @@ class KV4Batch:
     """A batch's device tables: block_table [B][cols], kv_len [B], q_start
     [B + 1] (int32), and on the host its rows T, its cached tokens total_kv and
     the rows of each sequence, None where they differ (by default T / B). With
-    shared prefixes: group_start, shared_len and on the host max_shared; of a cache
+    shared prefixes: group_start, shared_len and on the host max_shared, or plain; of a cache
     with scores: slots and scored, and on the host the sequences and their lengths."""
 
     def __init__(self, block_table, kv_len, q_start, T, total_kv, rows="even"):
@@ -322,6 +322,7 @@ class KV4Batch:
         B = kv_len.shape[0]
         self.rows = rows if rows != "even" else T // B if B and T % B == 0 else None
         self.group_start = self.shared_len = self.max_shared = None
+        self.plain = False                               # decode_shared is decode: nothing is worth sharing
         self.slots = self.scored = self.seqs = self.lens = None
 
 
@@ -398,8 +399,9 @@ class KV4Cache:
         the copies of shared pages made, and the batch of the new rows; all on
         `stream` (default: the current one), where the batch is to be used.
         share: with the tables that decode_shared needs; sequences that share
-        pages have to be neighbours in seqs. Where one of these fails, the book
-        is as before."""
+        pages have to be neighbours in seqs. share="auto": only what is long enough
+        and shared by enough of them is read once, and where nothing is,
+        decode_shared is decode. Where one of these fails, the book is as before."""
         seqs = list(seqs)
         tokens = [tokens] * len(seqs) if isinstance(tokens, int) else list(tokens)
         pairs = self.book.extend(seqs, tokens)
@@ -428,11 +430,27 @@ class KV4Cache:
                          sum(lens), rows)
         if share:
             start, shared = self.book.groups(seqs)
+            if share == "auto":
+                shared = self._paying(start, shared)
+                batch.plain = not any(shared)
             batch.group_start, batch.shared_len, batch.max_shared = self._dev(start), self._dev(shared), max([0] + shared)
         if self.scores is not None:
             batch.slots, batch.scored = self._dev([self._slot[s] for s in seqs]), self._dev([self._scored[s] for s in seqs])
             batch.seqs, batch.lens = list(seqs), lens
         return batch
+
+    def _paying(self, start, shared):
+        """The groups' shared tokens where reading them once is the faster way, 0 elsewhere.
+
+        In us per token and KV head: read by decode 2.2e-5 a member (d = 128; 1.4e-5 at
+        64), read once for all 6.2e-5, up to 256 rows; and 13 us a call for its other
+        launches. Decode and decode_shared, 32 query heads on 8 of d = 128: 8 sequences on
+        8192 tokens 21.0 and 27.0 us, 16 33.8 and 30.2; on 32768 tokens 4 31.4 and 41.0, 8
+        54.6 and 41.7. 16 on 4 of 64, 32768 tokens: 8 21.1 and 29.8, 16 34.4 and 29.4."""
+        heads, each = self.layers.shape[2], 2.2e-5 if self.layers.shape[4] == 18 * 128 else 1.4e-5
+        gain = [S * heads * ((b - a) * each - 6.2e-5) for S, a, b in zip(shared, start, start[1:])]
+        pays = sum(max(x, 0.0) for x in gain) > 13.0
+        return [S if pays and x > 0.0 else 0 for S, x in zip(shared, gain)]
 
     def append(self, layer, k, v, batch, stream=None):
         kv4_append(k, v, self.layers[layer], batch.block_table, batch.kv_len, *self.scales[layer],
@@ -454,8 +472,10 @@ class KV4Cache:
                           dev_status=self.status, **kw)
 
     def decode_shared(self, layer, q, batch, **kw):
-        """decode, the pages that neighbours of the batch share read once (a batch of grow(..., share=True))."""
+        """decode, the pages that neighbours of the batch share read once (a batch of grow(..., share=True), or "auto")."""
         self._same_rows(q, batch)
+        if batch.plain:
+            return self.decode(layer, q, batch, **kw)
         if batch.group_start is None:
             raise ValueError("the batch was made without share=True")
         return kv4_decode_shared(q, self.layers[layer], batch.block_table, batch.kv_len, batch.group_start,

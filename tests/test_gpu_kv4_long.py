@@ -186,3 +186,20 @@ def test_order_among_streams_and_other_kernels(g, graph):
             torch.cuda.synchronize()
             assert torch.equal(out, want) and torch.equal(lse, wlse) and torch.equal(s2, score) and torch.equal(k2, kept)
             assert torch.equal(p2[-4:], more[-4:])
+
+
+@pytest.mark.parametrize("members,pays", [(3, False), (40, True)])
+def test_shared_where_that_pays(g, members, pays):
+    """share="auto" is either attention: the same results, whichever it takes."""
+    hq, hkv, d = 16, 8, 128
+    c = g.KV4Cache(600, 64, hkv, d, KS, VS)
+    root = c.new()
+    c.append(0, rows(8192, hkv, d, 1), rows(8192, hkv, d, 2), c.grow([root], 8192))
+    seqs = [c.fork(root) for _ in range(members)]
+    batch = c.grow(seqs, 1, share="auto")
+    assert batch.plain != pays
+    c.append(0, rows(members, hkv, d, 3), rows(members, hkv, d, 4), batch)
+    q = queries(members, hq, d, 5)
+    out, lse = c.decode_shared(0, q, batch, return_lse=True)
+    close(out, lse, attention(c.layers[0], batch.block_table, [8193] * members, [1] * members, q, d), d)
+    assert c.check() == 0

@@ -210,6 +210,33 @@ def test_cache_without_scores_or_groups_refuses(g, monkeypatch):
     assert calls[-1][0] == "kv4_decode_shared" and calls[-1][2]["max_shared"] == 0
 
 
+def test_shares_where_that_pays(g, monkeypatch):
+    """share="auto": long prefixes of many, none of few or of short ones; where nothing is left, decode."""
+    from nvfp4_gated_deltanet_gb300 import kv4
+    c = g.KV4Cache(6000, 16, 8, 128, 1.0, 1.0, device="cpu")
+    monkeypatch.setattr(c, "_dev", lambda rows: torch.tensor(rows, dtype=torch.int32))
+    calls = []
+    for name in ("kv4_decode", "kv4_decode_shared", "kv4_copy_pages"):
+        monkeypatch.setattr(kv4, name, lambda *a, name=name, **k: calls.append((name, k)))
+    a, b = c.new(), c.new()
+    c.grow([a, b], [32768, 8192])
+    few, many = [c.fork(a) for _ in range(4)], [c.fork(b) for _ in range(20)]
+    ask = lambda seqs, **kw: c.decode_shared(0, torch.zeros(len(seqs), 1, 8, 128, dtype=torch.bfloat16), c.batch(seqs, [1] * len(seqs), **kw))
+    ask(few, share="auto")
+    assert calls[-1][0] == "kv4_decode"
+    ask(few, share=True)
+    assert calls[-1][0] == "kv4_decode_shared" and calls[-1][1]["max_shared"] == 32768
+    ask(many[:8], share="auto")
+    assert calls[-1][0] == "kv4_decode"
+    ask(many, share="auto")
+    assert calls[-1][0] == "kv4_decode_shared" and calls[-1][1]["max_shared"] == 8192
+    batch = c.batch(few[:2] + many, [1] * 22, share="auto")           # of two that share 32768 tokens each reads its own
+    assert batch.shared_len.tolist() == [0, 8192] and batch.group_start.tolist() == [0, 2, 22] and not batch.plain
+    batch = c.batch(few + many, [1] * 24, share="auto")
+    assert batch.shared_len.tolist() == [32768, 8192]
+    assert c.batch([], [], share="auto").plain
+
+
 GOOD = 0x10000  # an address that no call reads: each of these is refused first
 
 
