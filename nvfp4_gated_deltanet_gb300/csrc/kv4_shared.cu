@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
 // of them in registers there was room for four decoding warps only, one on each
 // scheduler, which then set the pace: 177 us instead of 150 for 1024 rows of each of 4
 // KV heads on 65536 tokens, the whole call). K and V are exact in FP16 (six
-// significant bits). Measured now, those rows: 106 us in this kernel, 1.30 PFLOP/s
-// (0.68 of a large BF16 product); the tensor pipe is busy 59% of the time, held up by
+// significant bits). Measured now, those rows: 103 us in this kernel, 1.33 PFLOP/s
+// (0.70 of a large BF16 product); the tensor pipe is busy 62% of the time, held up by
 // shared memory's bandwidth (queries and K of S = Q K^T both come from there, and the
 // decoded tiles go there) and by a row tile's chain of softmax and products.
 // The weights are 2^(z - m + 6), with a maximum m that is only moved (and O
