@@ -417,6 +417,8 @@ class KV4Cache:
 
     def batch(self, seqs, tokens, share=False) -> KV4Batch:
         """The tables of the sequences as they are, their newest tokens[i] as the rows."""
+        if share not in (False, True, "auto"):
+            raise ValueError(f"share: True, False or \"auto\", not {share!r}")
         if self.scores is not None and max([0] + [self.book.length(s) for s in seqs]) > self.scores.shape[3]:
             raise MemoryError(f"a row of scores holds {self.scores.shape[3]} tokens")
         pages = [self.book.pages(s) for s in seqs]

@@ -235,6 +235,10 @@ def test_shares_where_that_pays(g, monkeypatch):
     batch = c.batch(few + many, [1] * 24, share="auto")
     assert batch.shared_len.tolist() == [32768, 8192]
     assert c.batch([], [], share="auto").plain
+    held = state(c.book)
+    with pytest.raises(ValueError, match="share"):
+        c.grow(few, 1, share="always")
+    assert state(c.book) == held
 
 
 GOOD = 0x10000  # an address that no call reads: each of these is refused first
