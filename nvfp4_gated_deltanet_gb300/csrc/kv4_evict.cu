@@ -75,7 +75,7 @@ GDN_DEV unsigned block_before(unsigned v, unsigned *sums, unsigned &total) {
 // pass. Then the kept tokens' places follow from prefix counts, in order: a warp
 // has neighbouring tokens, counts them, and after one barrier writes them.
 // Bound by instructions and by the passes' barriers (512 rows of up to
-// 8190: 23.5 us, issue 69% busy; 4 rows of 200001, sixteen CTAs each: 26.6).
+// 8190: 23.0 us, issue 67% busy; 4 rows of 200001, sixteen CTAs each: 26.3).
 constexpr int kMaxHeld = 48 * 1024;   // tokens that shared memory holds beside the counts
 constexpr int kSplit = 4096;          // where SMs are idle, a CTA's slice is halved down to this
 
