@@ -138,7 +138,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
       first = min(first, sf[i]);
     }
     lead = first < c.B ? first : -1;
-    S = lead < 0 ? 0 : least / c.page_tokens * c.page_tokens;
+    // a group of one sequence, of rows that kv4_decode takes together, reads for itself: 5 of 38016 tokens, 8 KV heads of
+    // 128, 40 us instead of 99 (2 of 512, 24 rows each, 19.3 instead of 17.6)
+    const bool alone = start[g + 1] - start[g] == 1 && p.own.groups == 1;
+    S = lead < 0 || alone ? 0 : least / c.page_tokens * c.page_tokens;
   }
   if (b < 0) {
     if (tid == 0) {
