@@ -408,10 +408,10 @@ typedef struct {
 /* kv4_decode with the tokens that a group shares read once for all of its rows.
  * The result is kv4_decode's, but for the order of the sums: a group shares, of
  * its shared_len, whole pages that every row of every member with tokens sees;
- * what is left of it each sequence reads for itself, and a group of one all. Sums, maxima and the parts
- * that are joined are FP32; roundings as kv4_decode's. group_start that does not
- * ascend within [0, B], or a shared_len below 0, sets GDN_E_RANGE and shares
- * nothing (there). workspace: kv4_decode_shared_workspace bytes.
+ * what is left of it each sequence reads for itself, and a group of one (of up to
+ * 32 rows) all. Sums, maxima and the parts that are joined are FP32; roundings as
+ * kv4_decode's. group_start that does not ascend within [0, B], or a shared_len
+ * below 0, sets GDN_E_RANGE and shares nothing (there). workspace: kv4_decode_shared_workspace bytes.
  * Errors: as kv4_decode; GDN_E_SHAPE for groups or max_shared below 0. */
 gdn_status kv4_decode_shared(const kv4_cache *c, const kv4_batch *b, const kv4_shared *s, const uint16_t *q,
                              int64_t q_stride, int n_q_heads, float sm_scale, uint16_t *out, float *lse,
