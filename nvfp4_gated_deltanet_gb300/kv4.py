@@ -315,7 +315,7 @@ class KV4Batch:
     [B + 1] (int32), and on the host its rows T, its cached tokens total_kv and
     the rows of each sequence, None where they differ (by default T / B). With
     shared prefixes: group_start, shared_len and on the host max_shared, or plain; of a cache
-    with scores: slots and scored, and on the host the sequences and their lengths."""
+    with scores: slots and scored, and on the host the sequences, their lengths and what scored holds."""
 
     def __init__(self, block_table, kv_len, q_start, T, total_kv, rows="even"):
         self.block_table, self.kv_len, self.q_start, self.T, self.total_kv = block_table, kv_len, q_start, T, total_kv
@@ -323,7 +323,7 @@ class KV4Batch:
         self.rows = rows if rows != "even" else T // B if B and T % B == 0 else None
         self.group_start = self.shared_len = self.max_shared = None
         self.plain = False                               # decode_shared is decode: nothing is worth sharing
-        self.slots = self.scored = self.seqs = self.lens = None
+        self.slots = self.scored = self.seqs = self.lens = self.counts = None
 
 
 class KV4Cache:
@@ -333,9 +333,8 @@ class KV4Cache:
 
     With score_slots and score_tokens the cache also keeps what attention weight
     each token got, for up to score_slots sequences of up to score_tokens tokens
-    (4 bytes per token, KV head and layer): per layer score after decode or
-    prefill -- in every layer that is to be evicted from, for the same batches --
-    and evict from time to time."""
+    (4 bytes per token, KV head and layer): score after decode or prefill, in
+    every layer and for the same batches, and evict from time to time."""
 
     def __init__(self, num_pages, page_tokens, n_kv_heads, head_dim, k_scale, v_scale, n_layers=1, device="cuda",
                  score_slots=0, score_tokens=0):
@@ -347,35 +346,37 @@ class KV4Cache:
         self.scores = None
         if score_slots:
             self.scores = torch.zeros(n_layers, score_slots, n_kv_heads, score_tokens, device=device)
-        self._free_slots, self._slot, self._scored = list(range(score_slots - 1, -1, -1)), {}, {}
+        # _scored: the tokens of a sequence that have a score in every layer; _ahead: {layer: tokens} of the
+        # layers that have come further
+        self._free_slots, self._slot, self._scored, self._ahead = list(range(score_slots - 1, -1, -1)), {}, {}, {}
 
     def _needs_scores(self):
         if self.scores is None:
             raise ValueError("the cache was made without score_slots")
 
-    def _slot_for(self, make, scored):
+    def _slot_for(self, make, scored, ahead):
         """The sequence that `make` adds to the book, with a slot where the cache has scores."""
         if self.scores is None:
             return make()
         if not self._free_slots:
             raise MemoryError("no score slot is free")
         seq = make()
-        self._slot[seq], self._scored[seq] = self._free_slots.pop(), scored
+        self._slot[seq], self._scored[seq], self._ahead[seq] = self._free_slots.pop(), scored, dict(ahead)
         return seq
 
     def new(self) -> int:
-        return self._slot_for(self.book.new, 0)
+        return self._slot_for(self.book.new, 0, {})
 
     def free(self, seq: int):
         self.book.free(seq)
         if self.scores is not None:
             self._free_slots.append(self._slot.pop(seq))
-            del self._scored[seq]
+            del self._scored[seq], self._ahead[seq]
 
     def fork(self, seq: int, stream=None) -> int:
         """A new sequence with the same tokens; no page is copied until one of the
         two grows (its scores are, on `stream`)."""
-        child = self._slot_for(lambda: self.book.fork(seq), self._scored.get(seq, 0))
+        child = self._slot_for(lambda: self.book.fork(seq), self._scored.get(seq, 0), self._ahead.get(seq, {}))
         if self.scores is not None:
             with self._on(stream):
                 self.scores[:, self._slot[child]].copy_(self.scores[:, self._slot[seq]])
@@ -384,7 +385,16 @@ class KV4Cache:
     def truncate(self, seq: int, tokens: int):
         self.book.truncate(seq, tokens)
         if self.scores is not None:
-            self._scored[seq] = min(self._scored[seq], tokens)
+            self._recount(seq, lambda n: min(n, tokens))
+
+    def _count(self, seq, layer):
+        """How many of a sequence's tokens have a score in the layer."""
+        return self._ahead[seq].get(layer, self._scored[seq])
+
+    def _recount(self, seq, f):
+        """f of every layer's count."""
+        self._scored[seq] = f(self._scored[seq])
+        self._ahead[seq] = {layer: f(n) for layer, n in self._ahead[seq].items()}
 
     def _dev(self, rows):
         return torch.tensor(rows, dtype=torch.int32).pin_memory().to(self.device, non_blocking=True)
@@ -437,8 +447,8 @@ class KV4Cache:
                 batch.plain = not any(shared)
             batch.group_start, batch.shared_len, batch.max_shared = self._dev(start), self._dev(shared), max([0] + shared)
         if self.scores is not None:
-            batch.slots, batch.scored = self._dev([self._slot[s] for s in seqs]), self._dev([self._scored[s] for s in seqs])
-            batch.seqs, batch.lens = list(seqs), lens
+            batch.seqs, batch.lens, batch.counts = list(seqs), lens, [self._scored[s] for s in seqs]
+            batch.slots, batch.scored = self._dev([self._slot[s] for s in seqs]), self._dev(batch.counts)
         return batch
 
     def _paying(self, start, shared):
@@ -491,7 +501,8 @@ class KV4Cache:
     def score(self, layer, q, lse, batch, q_start=None, **kw):
         """Add the weights of the batch's rows to its sequences' scores, by the
         queries and the log-sum-exp of decode, decode_shared or prefill. q_start
-        [B + 1]: q holds only these of the newest rows (a prompt's window)."""
+        [B + 1]: q holds only these of the newest rows (a prompt's window). A batch
+        is scored in every layer; again in one, it adds to what it has there."""
         self._needs_scores()
         if batch.T == 0:
             return
@@ -504,15 +515,28 @@ class KV4Cache:
                 q_start = batch.q_start
             elif batch.rows != 1:                        # as many rows each: a batch of candidates
                 q, lse = (x.unflatten(0, (-1, batch.rows)) for x in (q, lse))
+        at = range(len(self.layers))[layer]              # -1 is the last one
+        counts, scored = [self._count(s, at) for s in batch.seqs], batch.scored
+        if counts != batch.counts:                       # the layer has come further than that, or all layers have
+            if all(x >= n for x, n in zip(counts, batch.lens)):
+                scored = None
+            else:
+                with self._on(kw.get("stream")):
+                    scored = self._dev(counts)
         kv4_score(q, lse, self.layers[layer], batch.block_table, batch.kv_len, self.scores[layer], self.scales[layer][0],
-                  q_start=q_start, slots=batch.slots, scored=batch.scored, dev_status=self.status, **kw)
-        for s, n in zip(batch.seqs, batch.lens):
-            self._scored[s] = n
+                  q_start=q_start, slots=batch.slots, scored=scored, dev_status=self.status, **kw)
+        for s, n, x in zip(batch.seqs, batch.lens, counts):
+            ahead = self._ahead[s]
+            ahead[at] = max(x, min(n, self.book.length(s)))
+            if len(ahead) == len(self.layers):
+                self._scored[s] = low = min(ahead.values())
+                self._ahead[s] = {i: y for i, y in ahead.items() if y > low}
 
     def evict(self, seqs, keep, recent=0, stream=None):
         """Cut each of the sequences that is longer to keep[i] (or `keep`) tokens per
         layer and KV head: the newest `recent`, and of the others those that got the
-        most attention weight. Returns the sequences that were cut and the places
+        most attention weight; tokens that some layer has not scored have to be among
+        the newest (ValueError). Returns the sequences that were cut and the places
         their kept tokens had, int32 [layers][cut][Hkv][most], -1 past the last. From
         then on a cached token's place is not its position in the text, and differs
         between heads. The cut sequences get new pages, the old ones are free after
@@ -524,10 +548,10 @@ class KV4Cache:
         if len(keep) != len(seqs) or len(set(seqs)) != len(seqs) or recent < 0 or any(k < 0 for k in keep):
             raise ValueError("one number of tokens, zero or more, for each of distinct sequences")
         cut = [(s, k) for s, k in zip(seqs, keep) if self.book.length(s) > k]
-        news = [self.book.length(s) - self._scored[s] for s, _ in cut]  # the newest tokens, which have no score yet
+        news = [self.book.length(s) - self._scored[s] for s, _ in cut]  # the newest tokens, which some layer has not scored
         for (s, k), n in zip(cut, news):
             if n > min(recent, k):
-                raise ValueError(f"sequence {s}: {n} tokens have no score")
+                raise ValueError(f"sequence {s}: {n} tokens have no score in some layer")
         seqs, keep = [s for s, _ in cut], [k for _, k in cut]
         most = max([0] + keep)
         if not seqs:
@@ -550,8 +574,8 @@ class KV4Cache:
                 self.book.restore(seqs, old)
                 raise
         self.book.release(old)
-        for s, k, n in zip(seqs, keep, news):
-            self._scored[s] = k - n
+        for s, k, (_, n) in zip(seqs, keep, old):
+            self._recount(s, lambda x: k - (n - x))      # what had no score is among the newest still
         return seqs, kept
 
     def compact(self, stream=None) -> int:
