@@ -566,13 +566,16 @@ class KV4Cache:
         with self._on(stream):
             before, lens = table(), self._dev([self.book.length(s) for s in seqs])
             slots, keeps = self._dev([self._slot[s] for s in seqs]), self._dev(keep)
-            old = self.book.exchange(seqs, keep)
-            try:
-                kept, _ = kv4_evict(self.layers, before, lens, keeps, recent, self.scores, table(), max_keep=most,
-                                    slots=slots, dev_status=self.status)
-            except BaseException:
-                self.book.restore(seqs, old)
-                raise
+        old = self.book.exchange(seqs, keep)
+        try:
+            with self._on(stream):
+                after = table()
+            # (not within: what it returns is kept until the current stream is done with it too)
+            kept, _ = kv4_evict(self.layers, before, lens, keeps, recent, self.scores, after, max_keep=most, slots=slots,
+                                dev_status=self.status, stream=stream)
+        except BaseException:
+            self.book.restore(seqs, old)
+            raise
         self.book.release(old)
         for s, k, (_, n) in zip(seqs, keep, old):
             self._recount(s, lambda x: k - (n - x))      # what had no score is among the newest still

@@ -1,5 +1,8 @@
 """Which tokens KV4Cache takes to have a score, layer by layer, without a GPU: what it
 hands to kv4_score, and when it refuses to evict."""
+import contextlib
+from types import SimpleNamespace
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -146,3 +149,26 @@ def test_a_batch_of_a_freed_sequence_is_refused(made):
     with pytest.raises(KeyError):
         c.score(0, *rows(10), batch)
     assert len(calls) == n
+
+
+def test_evict_on_a_stream_returns_memory_of_the_current_one_too(made, monkeypatch):
+    """The call itself gets the stream, so that it records its outputs on the stream that is current for the caller;
+    the tables are made on the call's stream."""
+    from nvfp4_gated_deltanet_gb300 import kv4
+    c, calls = made(n_layers=1)
+    a = c.new()
+    c.score(0, *rows(50), c.grow([a], 50))
+    side, inside, made_on = SimpleNamespace(), [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        inside.append(stream)
+        yield
+        inside.pop()
+
+    dev, evict = c._dev, kv4.kv4_evict
+    monkeypatch.setattr(c, "_on", on)
+    monkeypatch.setattr(c, "_dev", lambda x: made_on.append(inside[-1]) or dev(x))
+    monkeypatch.setattr(kv4, "kv4_evict", lambda *x, **k: (calls.append(list(inside)), evict(*x, **k))[1])
+    c.evict([a], 20, stream=side)
+    assert calls[-2] == [] and calls[-1][2]["stream"] is side and set(map(id, made_on)) == {id(side)}
