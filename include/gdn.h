@@ -434,7 +434,7 @@ typedef struct {
  * sequence's rows (as in kv4_prefill with q_start, kv4_decode without) that see
  * token j and the query heads that read the KV head. lse: FP32 [T][n_q_heads],
  * contiguous, as the attention call returned it; a row whose lse is -infinity
- * adds nothing. scored (device [B], may be NULL: all): how many of a sequence's
+ * adds nothing, whatever its query holds. scored (device [B], may be NULL: all): how many of a sequence's
  * tokens have a score; the others' begin at 0, whatever `in` holds there. Rows
  * of slots that the batch does not name, and a row's places from kv_len on, are
  * left alone. A sequence whose slot is out of range or named twice, or whose

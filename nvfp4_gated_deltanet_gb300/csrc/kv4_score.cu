@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
   float rc[NQ][2], hi[NQ][2], wt[NQ][2];
   int last[NQ][2];
   int at_b = -1, at_h = -1, slot = -1, scored = 0, rows_b = 0;
+  bool some_out = false;         // a row's lse is -infinity: its query may be anything, NaN too
   for (; left > 0; --left) {
     if (cur.b != at_b || cur.h != at_h) {
       // ---- another sequence or head: its rows
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
       }
       at_b = cur.b;
       at_h = cur.h;
+      some_out = false;
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
         const int row = nq * 8 + g, tok = row / G;
@@ -237,6 +239,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
         // columns 2t and 2t + 1 are rows 2t and 2t + 1 of this block: held by lanes 4 (2t), 4 (2t + 1)
         const RowWeight rw = row_weight(lse, skew);
         const int sees = lse == -INFINITY ? -1 : s.len - n + tok;
+        some_out |= __any_sync(0xffffffffu, have && lse == -INFINITY) != 0;
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
           // (a row that is none, or saw nothing: 0 throughout)
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
       pos[x] = cur.pos + t * 16 + g + 8 * x;
       old[x] = slot >= 0 && pos[x] < min(scored, cur.len) ? p.s.in[row + pos[x]] : 0.0f;
     }
-    const bool edge = cur.pos + kUnit > cur.len - rows_b + 1;
+    const bool edge = some_out || cur.pos + kUnit > cur.len - rows_b + 1;
     const bool more = left > 1;
     if (more) look();
 #pragma unroll
@@ -319,7 +322,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
 //                     exactly (from shared memory it would take half of its bandwidth)
 //   warp 16           TMEM allocation; one thread issues the MMAs
 //   warp 17           streams row tiles by TMA, as they came (BF16, the B operand)
-//   warps 18, 19      the rows' lse in bits, of every other tile
+//   warps 18, 19      the rows' lse in bits, of every other tile. A row whose lse is -infinity
+//                     weighs nothing, its z being -infinity, unless its query is no number or too
+//                     large for one: it is overwritten with zeros before the MMAs
 // Measured: two chunks of 4096 and 789 tokens, 32 query heads on 8 of d = 128, over
 // 8100 and 2221 cached: 167 us, 1.29 PFLOP/s, 0.67 of a large BF16 product; the
 // exponentials' unit is busy two thirds of the time, the tensor pipe too. Four windows
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
         const uint32_t e8 = u % kLses;
         if (!warp_wait_all(row_full + e8, u / kLses) || !warp_wait_all(acc_full + i, u / kAccs)) return false;
         tc_fence_after();
-        // whole tiles: every row sees every token; their rows that are none have hi = infinity
+        // whole tiles: every row sees every token; their rows that are none have hi = -infinity
         const bool mask = (w.kt + 1) * kTok - 1 > s.len - s.n + t * p.tpt || (t + 1) * p.tpt > s.n;
         // the tile's columns that see this token: from its first row that does, and only those that are rows
         const int lo = max(0, pos - (s.len - s.n) - t * p.tpt) * p.G;
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
         ok = wait(k_full + (it & 1), it / 2);
         for (int t = t0; t < t1 && ok; ++t) {
           const uint32_t v = u + (t - t0), a = v % kAccs, q = v % NQ;
-          ok = wait(q_full + q, v / NQ) && (v < kAccs || wait(acc_free + a, v / kAccs - 1));
+          ok = wait(q_full + q, v / NQ) && wait(row_full + v % kLses, v / kLses) && (v < kAccs || wait(acc_free + a, v / kAccs - 1));
           if (!ok) break;
           tc_fence_after();
           const uint64_t qq = qd + (uint64_t)q * kStep;
@@ -796,12 +801,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
     // ------------------------------------------------ what the tiles' rows are weighed by: tiles u with u % 2 == warp % 2
     uint32_t u = 0;
     items([&](const ScorePlace &w, const ScoreSeq &s, int t0, int t1, bool) {
+      unsigned out = 0;  // of a lane's four rows of the tile looked up last: those that are left out
       auto lses = [&](int t, float (&hi)[4]) {
+        out = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int x = lane + 32 * j, over = (int)(x * p.inv_g >> 16), tok = t * p.tpt + over;
           const bool have = x < p.tpt * p.G && tok < s.n;
           hi[j] = have ? p.a.lse[(long long)(s.q0 + tok) * p.a.Hq + w.h * p.G + x - over * p.G] : -INFINITY;
+          out |= (unsigned)(have && hi[j] == -INFINITY) << j;
         }
       };
       float next[4];
@@ -813,6 +821,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv4_score_tile_kernel(const _
 #pragma unroll
         for (int j = 0; j < 4; ++j)  // a row that saw nothing, or is none, adds nothing
           hi[j] = next[j] == -INFINITY ? -INFINITY : -fmaf(next[j], kLog2e, next[j] * (1.925963e-8f - p.skew * kLog2e));
+        // (A copy of the weighing for such tiles instead: the windows 39.1 us, the chunks 182; one that found NaN in a
+        // tile's sum and weighed it again 39.5 and 183; this 38.5 and 178, before such rows were looked at 36.9 and 177.)
+        if (__any_sync(0xffffffffu, out != 0)) {
+          const uint32_t q = v % NQ;
+          if (!warp_wait_all(q_full + q, v / NQ)) return false;
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j)
+            if (out >> j & 1)
+              for (int x = 0; x < D / 64 * 8; ++x)  // a row has 128 bytes in each 64 channels' part
+                *reinterpret_cast<uint4 *>(qbuf + q * S::kBytesTile + x / 8 * (kRow * 128) + (lane + 32 * j) * 128 + x % 8 * 16) =
+                    make_uint4(0, 0, 0, 0);
+          fence_async_shared();
+        }
         if (t + 2 < t1) lses(t + 2, next);
         if (v >= kLses && !warp_wait_all(row_free + e8, v / kLses - 1)) return false;
 #pragma unroll

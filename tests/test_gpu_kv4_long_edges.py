@@ -51,3 +51,37 @@ def test_kept_places_dropped_while_the_current_stream_reads_them(g):
     assert c.check() == 0
     for x in got:
         assert (x[..., 240:] == torch.arange(584, 600, device="cuda")).all() and (x >= 0).all() and (x.diff(dim=-1) > 0).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,counts", [
+    (4, 1, 64, [1, 1, 0]),                              # up to 8 rows, up to 16, and tiles
+    (8, 2, 128, [2, 1, 1]),
+    (8, 1, 64, [1, 1, 0]),
+    (6, 1, 128, [2, 0, 0]),
+    (8, 2, 128, [300, 40, 7]),
+    (5, 1, 64, [130, 0, 90]),
+])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf"), 3e38])
+def test_a_row_left_out_of_the_scores_may_hold_anything(g, hq, hkv, d, counts, what):
+    """lse = -infinity: the row adds nothing, whatever its queries are."""
+    lens = [700, 400, 129]
+    pages, table, n, *_ = prefixed(g, [(0, lens)], 16, hkv, d, seed=hq)
+    T = sum(counts)
+    start = ints(np.concatenate([[0], np.cumsum(counts)]).tolist())
+    q = queries(T, hq, d, seed=3)
+    lse = g.kv4_prefill(q, pages, table, n, start, KS, VS, return_lse=True)[1]
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    out_of = torch.rand(T, hq, generator=gen, device="cuda") < 0.3
+    out_of[0, 0] = True
+    lse[out_of] = float("-inf")
+    bad = q.clone()
+    bad[out_of] = what
+    bad[out_of & (torch.rand(T, hq, generator=gen, device="cuda") < 0.5)] *= -1
+    q[out_of] = 0
+    a, b = torch.zeros(2, 3, hkv, 700, device="cuda")
+    g.kv4_score(q, lse, pages, table, n, a, KS, q_start=start)
+    g.kv4_score(bad, lse, pages, table, n, b, KS, q_start=start)
+    assert torch.equal(a, b) and torch.isfinite(a).all()
+    want, err = weights(pages, table, lens, counts, q, lse, hkv, d)
+    for x, m, w, e in zip(a, lens, want, err):
+        assert ((x[:, :m].double() - w).abs() <= e).all()
