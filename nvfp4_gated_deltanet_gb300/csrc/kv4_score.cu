@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
       }
     }
   };
+  // (no loads by the read-only path: pages may have been written by a kernel that had not ended when this one began)
   uint32_t kw[kGroups][2][W];  // [group][token g, g + 8]: 16 (d = 64: 8) code bytes, and their scales
   uint32_t ks[kGroups][2];
   auto load = [&](int q) {
@@ -167,13 +168,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
     for (int x = 0; x < 2; ++x) {
       const int tok = g + 8 * x;
       if constexpr (D == 128) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + kv4_k_code<D>(tok, t * 16)));
+        const uint4 v = *reinterpret_cast<const uint4 *>(src + kv4_k_code<D>(tok, t * 16));
         kw[q][x][0] = v.x, kw[q][x][1] = v.y, kw[q][x][2 % W] = v.z, kw[q][x][3 % W] = v.w;
-        ks[q][x] = __ldg(reinterpret_cast<const uint16_t *>(src + kv4_k_scale<D>(tok, 2 * t)));
+        ks[q][x] = *reinterpret_cast<const uint16_t *>(src + kv4_k_scale<D>(tok, 2 * t));
       } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + kv4_k_code<D>(tok, t * 8)));
+        const uint2 v = *reinterpret_cast<const uint2 *>(src + kv4_k_code<D>(tok, t * 8));
         kw[q][x][0] = v.x, kw[q][x][1] = v.y;
-        ks[q][x] = __ldg(src + kv4_k_scale<D>(tok, t));
+        ks[q][x] = src[kv4_k_scale<D>(tok, t)];
       }
     }
   };

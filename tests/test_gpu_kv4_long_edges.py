@@ -85,3 +85,51 @@ def test_a_row_left_out_of_the_scores_may_hold_anything(g, hq, hkv, d, counts, w
     want, err = weights(pages, table, lens, counts, q, lse, hkv, d)
     for x, m, w, e in zip(a, lens, want, err):
         assert ((x[:, :m].double() - w).abs() <= e).all()
+
+
+@pytest.mark.parametrize("hq,r", [(2, 1), (8, 2), (8, 40)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_scores_of_tokens_written_right_before(g, graph, hq, r):
+    """Scores right behind an append, and behind an eviction, whose kernels may still run when the score's begins:
+    they see the new bytes in pages that earlier scores have read."""
+    hkv, d, n, keep = 1, 128, 2000, 512
+    pages, table, kv, *_ = prefixed(g, [(0, [n])], 64, hkv, d, seed=5, spare=8)
+    used = set(table[0].tolist())
+    new = ints([[p for p in range(pages.shape[0]) if p not in used][:8]])
+    steps = 6
+    ks, vs = rows(steps * n, hkv, d, 1).view(steps, n, hkv, d), rows(steps * n, hkv, d, 2).view(steps, n, hkv, d)
+    q = queries(r, hq, d, 3)[None]
+    lse = torch.full((1, r, hq), 5.0, device="cuda")
+    rank = torch.rand(steps, 1, hkv, n, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda")
+    sums, moved = torch.zeros(steps, 1, hkv, n, device="cuda"), torch.zeros(steps, 1, hkv, n, device="cuda")
+    kept, count, limit = torch.zeros(1, hkv, keep, dtype=torch.int32, device="cuda"), ints([keep]), ints([keep])
+    aside = torch.zeros_like(rank[0])
+
+    def run(wait):
+        for i in range(steps):
+            g.kv4_append(ks[i], vs[i], pages, table, kv, KS, VS)
+            wait()
+            g.kv4_score(q, lse, pages, table, kv, sums[i], KS)
+            wait()
+            g.kv4_evict(pages, table, kv, limit, 8, rank[i], new, kept=kept, new_len=count, scores_out=aside)
+            wait()
+            g.kv4_score(q, lse, pages, new, limit, moved[i], KS)
+            wait()
+
+    run(torch.cuda.synchronize)
+    want = sums.clone(), moved.clone()
+    assert (want[0][1:] != want[0][:-1]).any(-1).all() and (want[1][1:] != want[1][:-1]).any(-1).all()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step = lambda: run(lambda: None)
+        if graph:
+            G = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(G, stream=s):
+                run(lambda: None)
+            step = G.replay
+        for _ in range(10):
+            sums.zero_(), moved.zero_()
+            step()
+            torch.cuda.synchronize()
+            assert torch.equal(sums, want[0]) and torch.equal(moved, want[1])
