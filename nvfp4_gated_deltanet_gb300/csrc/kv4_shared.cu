@@ -114,33 +114,38 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
       flag_status(c.status, GDN_E_RANGE);
       S = 0;
     }
-    int least = S, first = c.B;
+    int least = S, first = c.B, live = 0;  // live: members with tokens
     for (int i = start[g] + tid; i < start[g + 1]; i += kPlanThreads) {
       const int n = kv4_len(c, i);
       if (n > 0) {
         least = min(least, max(n - p.r + 1, 0));
         first = min(first, i);
+        ++live;
       }
     }
-    __shared__ int sl[kPlanThreads / 32], sf[kPlanThreads / 32];
+    __shared__ int sl[kPlanThreads / 32], sf[kPlanThreads / 32], sn[kPlanThreads / 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
       first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+      live += __shfl_xor_sync(0xffffffffu, live, o);
     }
     if ((tid & 31) == 0) {
       sl[tid >> 5] = least;
       sf[tid >> 5] = first;
+      sn[tid >> 5] = live;
     }
     __syncthreads();
+    live = 0;
     for (int i = 0; i < kPlanThreads / 32; ++i) {
       least = min(least, sl[i]);
       first = min(first, sf[i]);
+      live += sn[i];
     }
     lead = first < c.B ? first : -1;
-    // a group of one sequence, of rows that kv4_decode takes together, reads for itself: 5 of 38016 tokens, 8 KV heads of
-    // 128, 40 us instead of 99 (2 of 512, 24 rows each, 19.3 instead of 17.6)
-    const bool alone = start[g + 1] - start[g] == 1 && p.own.groups == 1;
+    // a group of one sequence with tokens, of rows that kv4_decode takes together, reads for itself: 5 of 38016 tokens,
+    // 8 KV heads of 128, 40 us instead of 99 (2 of 512, 24 rows each, 19.3 instead of 17.6)
+    const bool alone = live == 1 && p.own.groups == 1;
     S = lead < 0 || alone ? 0 : least / c.page_tokens * c.page_tokens;
   }
   if (b < 0) {

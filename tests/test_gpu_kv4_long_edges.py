@@ -133,3 +133,21 @@ def test_scores_of_tokens_written_right_before(g, graph, hq, r):
             step()
             torch.cuda.synchronize()
             assert torch.equal(sums, want[0]) and torch.equal(moved, want[1])
+
+
+@pytest.mark.parametrize("groups,page,hq,hkv,d,r", [
+    ([(64, [0, 80, 0])], 16, 8, 2, 64, 1),
+    ([(5000, [5100, 0, 0, 0])], 64, 16, 2, 128, 2),
+    ([(320, [0, 0, 400]), (128, [0, 130]), (64, [70])], 16, 4, 4, 64, 1),
+])
+def test_members_without_tokens_do_not_count(g, groups, page, hq, hkv, d, r):
+    """A group with one member that has tokens, as a batch padded to a fixed size has it, reads for itself: bit for bit
+    as without a group. (kv_len 0: padding.)"""
+    pages, table, n, start, shared, lens = prefixed(g, groups, page, hkv, d, seed=len(groups))
+    B = len(lens)
+    q = queries(B * r, hq, d, 5).unflatten(0, (B, r))
+    st = ints([0])
+    out, lse = g.kv4_decode_shared(q, pages, table, n, start, shared, KS, VS, return_lse=True, dev_status=st)
+    want, wlse = g.kv4_decode_shared(q, pages, table, n, ints([0]), ints([]), KS, VS, return_lse=True)
+    close(out, lse, attention(pages, table, lens, [r] * B, q.flatten(0, 1), d), d)
+    assert torch.equal(out, want) and torch.equal(lse, wlse) and st.item() == 0
