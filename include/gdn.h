@@ -412,7 +412,8 @@ typedef struct {
  * tokens (and up to 32 rows) that one reads all. Sums, maxima and the parts that are joined are FP32; roundings as
  * kv4_decode's. group_start that does not ascend within [0, B], or a shared_len
  * below 0, sets GDN_E_RANGE and shares nothing (there). workspace: kv4_decode_shared_workspace bytes.
- * Errors: as kv4_decode; GDN_E_SHAPE for groups or max_shared below 0. */
+ * Errors: as kv4_decode; GDN_E_SHAPE for groups or max_shared below 0;
+ * GDN_E_OVERFLOW for tables of more than 2^31 - 1 - 2^15 tokens. */
 gdn_status kv4_decode_shared(const kv4_cache *c, const kv4_batch *b, const kv4_shared *s, const uint16_t *q,
                              int64_t q_stride, int n_q_heads, float sm_scale, uint16_t *out, float *lse,
                              void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
@@ -444,7 +445,8 @@ typedef struct {
  * exponentials and sums are FP32, in an order that depends on the whole batch's
  * lengths and rows and on the table's width, not on anything else. workspace: kv4_score_workspace bytes (0: may be NULL).
  * Errors: as kv4_append; GDN_E_SHAPE for heads as kv4_decode, for `out` that
- * overlaps `in` in part, for a workspace that is too small. v_scale is not used. */
+ * overlaps `in` in part, for a workspace that is too small; GDN_E_OVERFLOW for
+ * tables as kv4_decode_shared. v_scale is not used. */
 gdn_status kv4_score(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, int64_t q_stride, int n_q_heads,
                      float sm_scale, const float *lse, const kv4_scores *s, const int32_t *scored, void *workspace,
                      size_t workspace_bytes, int32_t *dev_status, void *stream);
@@ -467,7 +469,8 @@ size_t kv4_score_workspace(const kv4_cache *c, const kv4_batch *b, int n_q_heads
  * new_len are -1. A bad page id sets GDN_E_RANGE: what its tokens become is
  * unspecified. Of b only kv_len, block_table, B and max_pages are used.
  * Errors: GDN_E_NULL, GDN_E_SHAPE (sizes below 0, strides, `out` that overlaps
- * `in` in part), GDN_E_ALIGN, GDN_E_OVERFLOW, GDN_E_CUDA. */
+ * `in` in part), GDN_E_ALIGN, GDN_E_OVERFLOW (also for max_keep, or tables and
+ * score rows, of more than 2^31 - 1 - 2^15 tokens), GDN_E_CUDA. */
 gdn_status kv4_evict(const kv4_cache *c, int n_layers, int64_t layer_stride, const kv4_batch *b, const int32_t *keep,
                      int recent, const kv4_scores *s, int64_t score_stride, const int32_t *new_table, int new_pages,
                      int32_t *kept, int max_keep, int32_t *new_len, int32_t *dev_status, void *stream);

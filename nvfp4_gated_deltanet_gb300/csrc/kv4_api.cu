@@ -99,6 +99,11 @@ gdn_status check_seqs(const kv4_cache *c, const kv4_batch *b, Kv4Args &a, int32_
   return check(c, &one, a, status);
 }
 
+// Shared decode, scores and eviction step past a sequence's last token, or a row's last kept place, by a block's
+// stride at most before they stop: what is longer than this their 31-bit places cannot count.
+constexpr long long kMostTokens = 0x7fffffffLL - (1 << 15);
+long long table_tokens(const Kv4Args &a) { return (long long)a.cols * a.page_tokens; }
+
 // The score rows of n_layers layers, `stride` floats apart.
 gdn_status check_scores(const kv4_cache *c, const kv4_scores *s, int n_layers, int64_t stride, Kv4ScoreRows &r) {
   if (!s) return GDN_E_NULL;
@@ -124,6 +129,7 @@ gdn_status check_shared(const kv4_shared *s, int Hq, Kv4SharedArgs &a) {
   if (s->groups < 0 || s->max_shared < 0) return GDN_E_SHAPE;
   if (s->groups > 0 && (!s->group_start || !s->shared_len)) return GDN_E_NULL;
   if (s->groups > 0 && !words({s->group_start, s->shared_len})) return GDN_E_ALIGN;
+  if (table_tokens(a.a.c) > kMostTokens) return GDN_E_OVERFLOW;
   if ((long long)a.a.c.T * Hq + s->groups > 0x7ffffff0LL) return GDN_E_OVERFLOW;  // T is B or more
   a.group_start = s->group_start;
   a.shared_len = s->shared_len;
@@ -265,6 +271,7 @@ gdn_status kv4_score(const kv4_cache *c, const kv4_batch *b, const uint16_t *q, 
   }
   if (!words({scored})) return GDN_E_ALIGN;
   if (b->B == 0 || b->max_pages == 0 || s->n_slots == 0) return GDN_OK;
+  if (table_tokens(a.c) > kMostTokens) return GDN_E_OVERFLOW;
   // a CTA per so many tokens of a sequence and head
   if (((long long)b->max_pages * c->page_tokens / 128 + 1) * b->B > 0x7fffffffLL / c->n_kv_heads) return GDN_E_OVERFLOW;
   a.q = q;
@@ -296,6 +303,7 @@ gdn_status kv4_evict(const kv4_cache *c, int n_layers, int64_t layer_stride, con
   if (st != GDN_OK || b->B == 0) return st;
   if (!keep || !new_len || (max_keep > 0 && !kept) || (new_pages > 0 && !new_table)) return GDN_E_NULL;
   if (!words({keep, new_len, kept, new_table})) return GDN_E_ALIGN;
+  if (max_keep > kMostTokens || (table_tokens(a.c) > kMostTokens && s->tokens > kMostTokens)) return GDN_E_OVERFLOW;
   const long long rows = (long long)b->B * c->n_kv_heads;
   // up to 16 CTAs choose for a row, one moves 128 of its tokens
   if (rows > 0x7fffffffLL / 16 / n_layers || rows * n_layers > 0x7fffffffLL / (max_keep / 128 + 1)) return GDN_E_OVERFLOW;
