@@ -502,7 +502,8 @@ class KV4Cache:
         """Add the weights of the batch's rows to its sequences' scores, by the
         queries and the log-sum-exp of decode, decode_shared or prefill. q_start
         [B + 1]: q holds only these of the newest rows (a prompt's window). A batch
-        is scored in every layer; again in one, it adds to what it has there."""
+        is scored in every layer; again in one, it adds to what it has there. With
+        out (a tensor as kv4_score's) the cache's own scores stay as they are."""
         self._needs_scores()
         if batch.T == 0:
             return
@@ -525,6 +526,8 @@ class KV4Cache:
                     scored = self._dev(counts)
         kv4_score(q, lse, self.layers[layer], batch.block_table, batch.kv_len, self.scores[layer], self.scales[layer][0],
                   q_start=q_start, slots=batch.slots, scored=scored, dev_status=self.status, **kw)
+        if kw.get("out") is not None:                    # the sums went elsewhere
+            return
         for s, n, x in zip(batch.seqs, batch.lens, counts):
             ahead = self._ahead[s]
             ahead[at] = max(x, min(n, self.book.length(s)))

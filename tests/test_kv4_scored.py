@@ -172,3 +172,15 @@ def test_evict_on_a_stream_returns_memory_of_the_current_one_too(made, monkeypat
     monkeypatch.setattr(kv4, "kv4_evict", lambda *x, **k: (calls.append(list(inside)), evict(*x, **k))[1])
     c.evict([a], 20, stream=side)
     assert calls[-2] == [] and calls[-1][2]["stream"] is side and set(map(id, made_on)) == {id(side)}
+
+
+def test_sums_that_go_elsewhere_are_no_scores_of_the_cache(made):
+    c, calls = made(n_layers=1)
+    a = c.new()
+    batch = c.grow([a], 50)
+    c.score(0, *rows(50), batch, out=torch.zeros(3, 2, 200))
+    with pytest.raises(ValueError, match="no score"):
+        c.evict([a], 20)
+    c.score(0, *rows(50), batch)
+    assert calls[-1][2]["scored"].tolist() == [0]
+    c.evict([a], 20)
