@@ -409,8 +409,9 @@ typedef struct {
  * The result is kv4_decode's, but for the order of the sums: a group shares, of
  * its shared_len, whole pages that every row of every member with tokens sees;
  * what is left of it each sequence reads for itself, and where one member only has
- * tokens (and up to 32 rows) that one reads all. Sums, maxima and the parts that are joined are FP32; roundings as
- * kv4_decode's. group_start that does not ascend within [0, B], or a shared_len
+ * tokens (and up to 32 rows) that one reads all. Sums, maxima and the parts that
+ * are joined are FP32; roundings as kv4_decode's, but that the softmax weights of
+ * shared tokens have one bit less below a row's maximum before FP16's end. group_start that does not ascend within [0, B], or a shared_len
  * below 0, sets GDN_E_RANGE and shares nothing (there). workspace: kv4_decode_shared_workspace bytes.
  * Errors: as kv4_decode; GDN_E_SHAPE for groups or max_shared below 0;
  * GDN_E_OVERFLOW for tables of more than 2^31 - 1 - 2^15 tokens. */

@@ -74,9 +74,11 @@ GDN_DEV uint32_t e4m3x2(uint32_t two) {
 // as a group of 16 tokens is decoded into MMA operands, the same group of the next
 // unit is on its way. No part of a token's sum leaves the warp, nothing is joined.
 // Measured: 64 sequences of up to 8190 tokens, 8 KV heads of d = 128, 4 rows each, 162
-// MB: 39 us, 4.1 TB/s (0.61 of the copy bandwidth), bound by the issue of about 700
-// instructions a unit, half of them the decoding (32 tokens a unit and a third more
-// warps: 48 to 56). The tiles below would write the decoded K down first.
+// MB: 39 us, 4.1 TB/s (0.61 of the copy bandwidth). A unit takes about 700 instructions,
+// half of them the decoding; with 16 warps an SM 52% of the issue slots are used, and
+// what is left is their latency (per issue 2.1 warps wait for loads, 1.8 for the
+// instruction before; 32 tokens a unit and a third more warps: 48 to 56). The tiles
+// below would write the decoded K down first.
 constexpr int kGroups = 4, kUnit = 16 * kGroups;  // (a lane of four writes a group's sums)
 constexpr int kLook = 32 / kGroups;  // units whose groups' places are worked out at once, a group per lane
 constexpr int kRowWarps = 8;
@@ -327,12 +329,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 ? 2 : 1) kv4_score_row
 //                     weighs nothing, its z being -infinity, unless its query is no number or too
 //                     large for one: it is overwritten with zeros before the MMAs
 // Measured: two chunks of 4096 and 789 tokens, 32 query heads on 8 of d = 128, over
-// 8100 and 2221 cached: 167 us, 1.29 PFLOP/s, 0.67 of a large BF16 product; the
-// exponentials' unit is busy two thirds of the time, the tensor pipe too. Four windows
-// of 64 rows on up to 16001 tokens: 36 us, 1.4 us an item of two tiles per CTA, of which
-// each role's own code for an item -- a few hundred instructions of one warp per
-// scheduler -- takes most. Every wait is bounded; one that gives up sets GDN_E_TIMEOUT
-// and an abort flag that ends every role's loop.
+// 8100 and 2221 cached: 168 us, 1.28 PFLOP/s, 0.67 of a large BF16 product; no unit is
+// full (exponentials and tensor pipe 57%, issue 62%): a tile's products and weights
+// wait for one another, with three of them in flight. Four windows of 64 rows on up to
+// 16001 tokens: 38 us, 1.4 us an item of two tiles per CTA, of which each role's own code
+// for an item -- a few hundred instructions of one warp per scheduler -- takes most. Every
+// wait is bounded; one that gives up sets GDN_E_TIMEOUT and an abort flag that ends every
+// role's loop.
 constexpr int kTok = 128, kRow = 128;
 constexpr int kAccs = 3;          // tiles of sums in tensor memory, 128 columns each: one for each four warps
 constexpr int kWeigh = 4 * kAccs; // warps
@@ -921,6 +924,8 @@ cudaError_t launch_kv4_score(const Kv4ScoreArgs &p, void *workspace, int num_sms
   const double exact = (double)p.sm_scale * c.ks * 1.4426950408889634074;  // a score in bits
   const float c2 = (float)exact, skew = (float)(exact / c2 - 1.0);
   const int R = most_rows(p), G = p.Hq / c.Hkv;
+  // 64 sequences of up to 8190 tokens, 8 KV heads of 128: 4 and 8 rows 38 us, 12 and 16 60, by tiles 176 whatever the rows
+  // up to 64; 8 of them, 2 heads of 64: 8 rows 5.4, 16 5.6, by tiles 13.6. (Of ragged rows the host knows the sum only.)
   if (R <= 8) return c.D == 128 ? launch_rows<128, 1>(p, c2, skew, num_sms, stream) : launch_rows<64, 1>(p, c2, skew, num_sms, stream);
   if (R <= 16) return c.D == 128 ? launch_rows<128, 2>(p, c2, skew, num_sms, stream) : launch_rows<64, 2>(p, c2, skew, num_sms, stream);
   float *pieces = static_cast<float *>(workspace);

@@ -186,9 +186,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_shared_plan_kernel(SharedKv4
 // scheduler, which then set the pace: 177 us instead of 150 for 1024 rows of each of 4
 // KV heads on 65536 tokens, the whole call). K and V are exact in FP16 (six
 // significant bits). Measured now, those rows: 103 us in this kernel, 1.33 PFLOP/s
-// (0.70 of a large BF16 product); the tensor pipe is busy 62% of the time, held up by
-// shared memory's bandwidth (queries and K of S = Q K^T both come from there, and the
-// decoded tiles go there) and by a row tile's chain of softmax and products.
+// (0.70 of a large BF16 product); the tensor pipe is busy 62% of the time. Counted for two
+// row tiles and 128 tokens, its products take 2048 cycles and shared memory about 2300
+// (queries and K of S = Q K^T both come from there, and the decoded tiles go there); the
+// rest is a row tile's chain of softmax and products, with two of them in flight.
 // The weights are 2^(z - m + 6), with a maximum m that is only moved (and O
 // rescaled in tensor memory) when a tile's weights come to 2^14 or more by it.
 // Every wait is bounded; one that gives up sets GDN_E_TIMEOUT and an abort flag
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv4_prefix_kernel(SharedKv4
 
 // ---------------------------------------------------------------- the parts joined
 // A CTA per 32 rows of a KV head and 32 channels. First the prefix's pieces, lane =
-// row, 8 of them in flight; then, four channels a thread, what the sequence has for
+// row, U of them in flight; then, four channels a thread, what the sequence has for
 // itself. Bound by latency: the row's item, its ends, the pieces.
 template <int D>
 __global__ void __launch_bounds__(256, 2) kv4_merge_kernel(SharedKv4 p) {
