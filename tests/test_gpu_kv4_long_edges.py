@@ -151,3 +151,50 @@ def test_members_without_tokens_do_not_count(g, groups, page, hq, hkv, d, r):
     want, wlse = g.kv4_decode_shared(q, pages, table, n, ints([0]), ints([]), KS, VS, return_lse=True)
     close(out, lse, attention(pages, table, lens, [r] * B, q.flatten(0, 1), d), d)
     assert torch.equal(out, want) and torch.equal(lse, wlse) and st.item() == 0
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 16, 2), (64, 8, 4)])
+def test_other_lengths_call_after_call_in_one_workspace(g, graph, d, hq, hkv):
+    """Nothing of one call's plan, sums or pieces is read by the next one, which begins while it ends: batches of other
+    lengths, tables and groups in turn, all in the same workspace and outputs."""
+    pages, table, n, start, shared, lens = prefixed(g, [(4096, [4200, 5000, 4111, 4096]), (640, [700, 9000, 2000])], 64, hkv, d)
+    q = queries(7, hq, d, 2)
+    back = torch.tensor([3, 2, 1, 0, 6, 5, 4], device="cuda")
+    batches = [(table, n, start, shared), (table[back].contiguous(), n[back].contiguous(), start, shared),
+               (table, ints([4097, 0, 4096, 0, 640, 641, 650]), start, ints([4096, 64])),
+               (table, ints([1, 5000, 70, 0, 0, 9000, 0]), ints([0, 1, 7]), ints([64, 0])),
+               (table, n, start, ints([0, 0])), (table, ints([4096, 4200, 4111, 4000, 700, 8999, 1]), start, shared)]
+    batches = [b for _ in range(4) for b in batches]
+    ws = torch.full((1 << 23,), float("nan"), device="cuda")
+    outs = [torch.zeros(7, hq, d, dtype=torch.bfloat16, device="cuda") for _ in batches]
+    lses = [torch.zeros(7, hq, device="cuda") for _ in batches]
+
+    def run(wait=lambda: None):
+        for b, o, l in zip(batches, outs, lses):
+            g.kv4_decode_shared(q, pages, *b, KS, VS, out=o, lse=l, workspace=ws)
+            wait()
+
+    def each_alone():
+        ws.fill_(float("nan"))
+        torch.cuda.synchronize()
+
+    run(each_alone)
+    want = [o.clone() for o in outs], [l.clone() for l in lses]
+    for b, o, l in zip(batches[:6], *want):
+        close(o, l, attention(pages, b[0], b[1].tolist(), [1] * 7, q, d), d)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step = run
+        if graph:
+            G = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(G, stream=s):
+                run()
+            step = G.replay
+        for _ in range(20):
+            for o in outs:
+                o.zero_()
+            step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(outs, want[0])) and all(torch.equal(x, y) for x, y in zip(lses, want[1]))
